@@ -21,6 +21,8 @@ __all__ = [
     "bskv_plan_decode", "bskv_plan_bsr", "bskv_plan_mla_sparse",
     "bskv_run_decode", "bskv_run_decode_partial", "bskv_decode_merge", "bskv_run_decode_noalloc",
     "bskv_run_bsr", "bskv_run_mla_sparse",
+    "bskv_plan_decode_fp4", "bskv_run_decode_fp4",
+    "bskv_quantize_fp4_append_paged", "bskv_dequantize_fp4_paged",
     "bskv_rope_quantize_fp8", "bskv_merge_states",
     "bskv_get_device_status", "bskv_set_debug_force_timeout",
 ]
@@ -90,6 +92,14 @@ _SIGS = {
                                              _P, _I64P, _P, _I64, _P, _I64, _P, _I64, _P, _P,
                                              _P, _P, _I32, _I32, _I64, _P,
                                              _I32, _P, _I32, _I64, _I32, _F, _F, _P], _I32),
+    "bskv_plan_decode_fp4": ([_I32P, _I32P, _I32P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                              _I32, ctypes.POINTER(_P)], _I32),
+    "bskv_run_decode_fp4": ([_P, _P, _I64P, _P, _I64P, _P, _I64P, _P, _I64P, _P, _F, _P, _SZ, _P],
+                            _I32),
+    "bskv_quantize_fp4_append_paged": ([_P, _I64P, _P, _I64P, _I32, _I64, _I32, _I32, _P, _P, _P,
+                                        _P, _I32, _I32, _I64, _P, _I64P, _P, _I64P, _P], _I32),
+    "bskv_dequantize_fp4_paged": ([_P, _I64P, _P, _I64P, _P, _P, _P, _P, _I32, _I32, _I64, _P,
+                                   _I64P, _P, _I64P, _I32, _I64, _I32, _I32, _P], _I32),
     "bskv_merge_states": ([_P, _P, _I64, _I32, _I32, _I32, _P, _I32, _P, _P], _I32),
     "bskv_get_device_status": ([_I32P, _I32], _I32),
     "bskv_set_debug_force_timeout": ([_I32], _I32),
@@ -593,6 +603,198 @@ def bskv_rope_quantize_fp8_append_paged(k_rope, k_nope, pos_k, cos_sin_cache, ba
              float(quant_scale_kv), _stream(cos_sin_cache)]
     _check("bskv_rope_quantize_fp8_append_paged", lib.bskv_rope_quantize_fp8_append_paged(*args))
     return q_rope_out, q_nope_out
+
+
+def _want(fn, name, t, shape, dtypes, device):
+    """One argument check: a tensor of this shape (None: any size) and type on this device."""
+    if not torch.is_tensor(t):
+        raise TypeError("%s: %s must be a tensor" % (fn, name))
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError("%s: %s has shape %s, not %s"
+                         % (fn, name, tuple(t.shape), tuple("*" if n is None else n for n in shape)))
+    if t.dtype not in dtypes:
+        raise ValueError("%s: %s is %s, not %s" % (fn, name, t.dtype, " or ".join(map(str, dtypes))))
+    if t.device.type != "cuda" or t.device != device:
+        raise ValueError("%s: %s is on %s; all tensors must be on one CUDA device"
+                         % (fn, name, t.device))
+
+
+def _rows_last(fn, name, t):
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s: the last dimension of %s must be contiguous" % (fn, name))
+
+
+def _dense(fn, *named):
+    for name, t in named:
+        if not t.is_contiguous():
+            raise ValueError("%s: %s must be contiguous" % (fn, name))
+
+
+def _strides_of(t, n):
+    """The first n strides; a dimension of size 1 counts as laid out densely behind it."""
+    out, dense = [], 1
+    for i in reversed(range(t.dim())):
+        out.append(dense if t.shape[i] == 1 else t.stride(i))
+        dense = max(dense, t.shape[i] * out[-1])
+    return _strides(*out[::-1][:n])
+
+
+def _check_plan(fn, plan, kind):
+    if not isinstance(plan, Plan) or plan.kind != kind:
+        raise ValueError("%s: not a %s plan" % (fn, kind))
+
+
+def _ready(fn, plan, device):
+    """The plan's workspaces on this device, uploaded at the first run."""
+    if plan.int_ws is None:
+        plan.upload(device)
+    if plan.int_ws.device != device:
+        raise ValueError("%s: the plan was uploaded to %s, the tensors are on %s"
+                         % (fn, plan.int_ws.device, device))
+
+
+def _fp4_cache(fn, kv_codes, kv_scales, device, num_pages, page_size, num_kv_heads, head_dim):
+    """Checks a 4-bit cache; its pointers and strides as the C entry points take them."""
+    _want(fn, "kv_codes", kv_codes, (num_pages, 2, num_kv_heads, page_size, head_dim // 2),
+          (torch.uint8,), device)
+    _want(fn, "kv_scales", kv_scales, (num_pages, 2, num_kv_heads, page_size, head_dim // 32),
+          (torch.uint8,), device)
+    _rows_last(fn, "kv_codes", kv_codes)
+    _rows_last(fn, "kv_scales", kv_scales)
+    if page_size > 1 and kv_scales.numel() and kv_scales.stride(3) != head_dim // 32:
+        raise ValueError("%s: the slots of kv_scales must be contiguous" % fn)
+    return kv_codes.data_ptr(), _strides_of(kv_codes, 4), kv_scales.data_ptr(), _strides_of(kv_scales, 3)
+
+
+def _fp4_rows(fn, k, v, dtypes, batch_indices, positions, kv_indptr, kv_indices):
+    """Checks K / V rows and their device page table; (nnz, heads, head_dim, batch)."""
+    nnz, heads, dim = k.shape if torch.is_tensor(k) and k.dim() == 3 else (None, None, None)
+    dev = k.device if torch.is_tensor(k) else None
+    _want(fn, "k", k, (nnz, heads, dim), dtypes, dev)
+    _want(fn, "v", v, (nnz, heads, dim), (k.dtype,), dev)
+    _rows_last(fn, "k", k)
+    _rows_last(fn, "v", v)
+    i32 = (torch.int32,)
+    _want(fn, "batch_indices", batch_indices, (nnz,), i32, dev)
+    _want(fn, "positions", positions, (nnz,), i32, dev)
+    _want(fn, "kv_indptr", kv_indptr, (None,), i32, dev)
+    _want(fn, "kv_indices", kv_indices, (None,), i32, dev)
+    if kv_indptr.numel() < 1:
+        raise ValueError("%s: kv_indptr is empty" % fn)
+    _dense(fn, ("batch_indices", batch_indices), ("positions", positions), ("kv_indptr", kv_indptr),
+           ("kv_indices", kv_indices))
+    return nnz, heads, dim, kv_indptr.numel() - 1
+
+
+def bskv_quantize_fp4_append_paged(k, v, batch_indices, positions, kv_indptr, kv_indices, kv_codes,
+                                   kv_scales):
+    """Quantise K / V rows [nnz, Hkv, D] (bf16 or fp16) to microscaled 4-bit values and write row
+    i to token positions[i] of request batch_indices[i] of the paged cache kv_codes [pages, 2,
+    Hkv, page_size, D / 2], kv_scales [pages, 2, Hkv, page_size, D / 32] (uint8), through the
+    device page table (all int32)."""
+    fn = "bskv_quantize_fp4_append_paged"
+    lib = load_library()
+    nnz, heads, dim, batch = _fp4_rows(fn, k, v, (torch.bfloat16, torch.float16), batch_indices,
+                                       positions, kv_indptr, kv_indices)
+    _want(fn, "kv_codes", kv_codes, (None, 2, heads, None, dim // 2), (torch.uint8,), k.device)
+    cache = _fp4_cache(fn, kv_codes, kv_scales, k.device, kv_codes.shape[0], kv_codes.shape[3], heads,
+                       dim)
+    with torch.cuda.device(k.device):
+        _check(fn, lib.bskv_quantize_fp4_append_paged(
+            k.data_ptr(), _strides_of(k, 2), v.data_ptr(), _strides_of(v, 2), _DT[k.dtype], nnz,
+            heads, dim, batch_indices.data_ptr(), positions.data_ptr(), kv_indptr.data_ptr(),
+            kv_indices.data_ptr(), batch, kv_codes.shape[3], kv_codes.shape[0], *cache, _stream(k)))
+
+
+def bskv_dequantize_fp4_paged(kv_codes, kv_scales, batch_indices, positions, kv_indptr, kv_indices,
+                              dtype=torch.bfloat16, k_out=None, v_out=None):
+    """Rows of a 4-bit paged cache as values: (k, v) [nnz, Hkv, D] of `dtype` (bf16, fp16 or
+    fp32), row i being token positions[i] of request batch_indices[i]. Rows whose token is out of
+    range are left as they were (outputs made here start as zeros)."""
+    fn = "bskv_dequantize_fp4_paged"
+    lib = load_library()
+    if not torch.is_tensor(kv_codes) or kv_codes.dim() != 5 or not torch.is_tensor(positions):
+        raise ValueError("%s: kv_codes must be [pages, 2, Hkv, page_size, D / 2]" % fn)
+    pages, _, heads, page_size, half = kv_codes.shape
+    shape = (positions.numel(), heads, 2 * half)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("%s: give both outputs or neither" % fn)
+    if k_out is None:
+        k_out = torch.zeros(shape, dtype=dtype, device=kv_codes.device)
+        v_out = torch.zeros(shape, dtype=dtype, device=kv_codes.device)
+    nnz, heads, dim, batch = _fp4_rows(fn, k_out, v_out,
+                                       (torch.bfloat16, torch.float16, torch.float32),
+                                       batch_indices, positions, kv_indptr, kv_indices)
+    cache = _fp4_cache(fn, kv_codes, kv_scales, k_out.device, pages, page_size, heads, dim)
+    with torch.cuda.device(k_out.device):
+        _check(fn, lib.bskv_dequantize_fp4_paged(
+            *cache, batch_indices.data_ptr(), positions.data_ptr(), kv_indptr.data_ptr(),
+            kv_indices.data_ptr(), batch, page_size, pages, k_out.data_ptr(),
+            _strides_of(k_out, 2), v_out.data_ptr(), _strides_of(v_out, 2), _DT[k_out.dtype], nnz,
+            heads, dim, _stream(k_out)))
+    return k_out, v_out
+
+
+def bskv_plan_decode_fp4(kv_indptr, kv_indices, kv_last_page_len, num_pages, page_size,
+                         num_qo_heads, num_kv_heads, head_dim, dtype=torch.bfloat16, num_sms=None,
+                         max_workers=0):
+    """Decode plan over a 4-bit paged cache, from a HOST page table (as bskv_plan_decode)."""
+    lib = load_library()
+    ip, ipp, ix, ixp, lp, lpp, batch = _page_table("bskv_plan_decode_fp4", kv_indptr, kv_indices,
+                                                   kv_last_page_len)
+    h = ctypes.c_void_p()
+    ns = _num_sms() if num_sms is None else num_sms
+    _check("bskv_plan_decode_fp4", lib.bskv_plan_decode_fp4(
+        ctypes.cast(ipp, _I32P), ctypes.cast(ixp, _I32P), ctypes.cast(lpp, _I32P), batch,
+        int(num_pages), int(page_size), int(num_qo_heads), int(num_kv_heads), int(head_dim),
+        _DT[dtype], int(ns), int(max_workers), ctypes.byref(h)))
+    return Plan(h.value, "decode_fp4", batch=batch, num_pages=int(num_pages),
+                page_size=int(page_size), num_qo_heads=int(num_qo_heads),
+                num_kv_heads=int(num_kv_heads), head_dim=int(head_dim), dtype=dtype)
+
+
+def _page_table(fn, kv_indptr, kv_indices, kv_last_page_len):
+    ip, ipp = _i32_array(kv_indptr)
+    ix, ixp = _i32_array(kv_indices)
+    lp, lpp = _i32_array(kv_last_page_len)
+    batch = ip.numel() - 1
+    if batch < 0 or lp.numel() < batch or (batch > 0 and ix.numel() < int(ip[-1])):
+        raise ValueError("%s: page table arrays of %d, %d and %d entries do not fit together"
+                         % (fn, ip.numel(), ix.numel(), lp.numel()))
+    return ip, ipp, ix, ixp, lp, lpp, batch
+
+
+def bskv_run_decode_fp4(plan, q, kv_codes, kv_scales, out=None, lse=None, return_lse=False,
+                        sm_scale=None):
+    """Decode one query token per request over a 4-bit paged cache: q [B, Hq, D]; kv_codes
+    [pages, 2, Hkv, page_size, D / 2], kv_scales [pages, 2, Hkv, page_size, D / 32] uint8."""
+    fn = "bskv_run_decode_fp4"
+    lib = load_library()
+    _check_plan(fn, plan, "decode_fp4")
+    i = plan.info
+    shape = (i["batch"], i["num_qo_heads"], i["head_dim"])
+    dev = q.device if torch.is_tensor(q) else None
+    _want(fn, "q", q, shape, (i["dtype"],), dev)
+    _rows_last(fn, "q", q)
+    cache = _fp4_cache(fn, kv_codes, kv_scales, dev, i["num_pages"], i["page_size"],
+                       i["num_kv_heads"], i["head_dim"])
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    _want(fn, "out", out, shape, (i["dtype"],), dev)
+    _rows_last(fn, "out", out)
+    if lse is None and return_lse:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    if lse is not None:
+        _want(fn, "lse", lse, shape[:2], (torch.float32,), dev)
+        _dense(fn, ("lse", lse))
+    with torch.cuda.device(dev):
+        _ready(fn, plan, dev)
+        fw = plan.float_ws
+        _check(fn, lib.bskv_run_decode_fp4(
+            plan.handle, q.data_ptr(), _strides_of(q, 2), *cache, out.data_ptr(),
+            _strides_of(out, 2), _ptr(lse), 0.0 if sm_scale is None else float(sm_scale), _ptr(fw),
+            0 if fw is None else fw.numel(), _stream(q)))
+    return (out, lse) if return_lse else out
 
 
 def bskv_merge_states(v, s, out_dtype=torch.float32, v_out=None, s_out=None):

@@ -15,7 +15,7 @@ namespace bskv {
 
 // ---- plan metadata: int32 words, header then 16-byte aligned sections ----------------
 constexpr int32_t kMetaMagic = 0x766b7362;  // "bskv"
-enum Kind : int32_t { KIND_DECODE = 1, KIND_BSR = 2, KIND_MLA = 3 };
+enum Kind : int32_t { KIND_DECODE = 1, KIND_BSR = 2, KIND_MLA = 3, KIND_DECODE_FP4 = 4 };
 enum Header : int {
   H_MAGIC = 0,
   H_KIND,
@@ -112,6 +112,17 @@ inline int32_t decode_group_heads(int32_t num_kv_heads, int32_t page_size) {
   if (page_size > kDecodeGroupMaxPage) return 0;
   if (num_kv_heads <= kDecodeGroupMax) return num_kv_heads;
   return num_kv_heads % kDecodeGroupMax == 0 ? kDecodeGroupMax : 0;
+}
+
+// 4-bit decode: one worker per warp, kFp4Warps to a CTA; the column tiles of 8 query heads per
+// kv head decide how many CTAs an SM holds (registers: 128 a thread with one tile).
+constexpr int kFp4Tile = 32;   // tokens per pipeline stage
+constexpr int kFp4Warps = 4;
+constexpr int fp4_ctas_per_sm(int column_tiles) { return column_tiles > 1 ? 2 : 4; }
+
+// Page sizes of a 4-bit paged cache: the kernels copy groups of 8 tokens that lie in one page.
+inline bool fp4_page_size(int32_t page_size) {
+  return page_size == 8 || (page_size >= 16 && page_size % 16 == 0);
 }
 
 // Byte offset in the int workspace of the merge counters (after the metadata).

@@ -398,6 +398,9 @@ void log_plan(const char* name, const bskv_plan* p) {
                : m[H_VARIANT] == BSR_PAGED_PREFILL ? "bsr_generic_kernel (paged prefill)"
                                                    : "bsr_generic_kernel";
       break;
+    case KIND_DECODE_FP4:
+      kernel = "decode_fp4_kernel (one worker per warp)";
+      break;
     case KIND_MLA:
       kernel = p->mla_variant == MLA_PAGED ? "mla_kernel (rows from the page table)"
                                            : "mla_kernel (sparse rows)";
@@ -539,6 +542,110 @@ extern "C" bskv_status bskv_plan_decode(const int32_t* kv_indptr, const int32_t*
   for (size_t i = 2; i < merges.size(); i += 3) p->max_merge_count = std::max(p->max_merge_count, merges[i]);
   *out_plan = p;
   log_plan("bskv_plan_decode", p);
+  return BSKV_OK;
+}
+
+namespace {
+
+// Validates a host page table and gives each request's length in tokens.
+bskv_status page_table_lens(const char* who, const int32_t* kv_indptr, const int32_t* kv_indices,
+                            const int32_t* kv_last_page_len, int32_t batch, int32_t num_pages,
+                            int32_t page_size, std::vector<int64_t>& lens) {
+  lens.assign(size_t(std::max(batch, 0)), 0);
+  if (batch == 0) return BSKV_OK;
+  if (!kv_indptr || !kv_last_page_len) { set_error("%s: NULL index array", who); return BSKV_ERR_INVALID_ARG; }
+  if (kv_indptr[0] != 0) { set_error("%s: kv_indptr[0] must be 0", who); return BSKV_ERR_INVALID_ARG; }
+  for (int32_t b = 0; b < batch; ++b) {
+    const int64_t n = int64_t(kv_indptr[b + 1]) - kv_indptr[b];
+    if (n < 0) { set_error("%s: kv_indptr decreases at %d", who, b); return BSKV_ERR_INVALID_ARG; }
+    if (n == 0) continue;
+    const int32_t lp = kv_last_page_len[b];
+    if (lp < 1 || lp > page_size) {
+      set_error("%s: kv_last_page_len[%d] = %d outside [1, %d]", who, b, lp, page_size);
+      return BSKV_ERR_INVALID_ARG;
+    }
+    lens[size_t(b)] = (n - 1) * page_size + lp;
+    if (lens[size_t(b)] > INT32_MAX / 2) { set_error("%s: request %d is too long", who, b); return BSKV_ERR_UNSUPPORTED; }
+  }
+  const int64_t nnz = kv_indptr[batch];
+  if (nnz > 0 && !kv_indices) { set_error("%s: kv_indices is NULL", who); return BSKV_ERR_INVALID_ARG; }
+  for (int64_t i = 0; i < nnz; ++i) {
+    if (kv_indices[i] < 0 || kv_indices[i] >= num_pages) {
+      set_error("%s: kv_indices[%lld] = %d outside [0, %d)", who, (long long)i, kv_indices[i], num_pages);
+      return BSKV_ERR_INVALID_ARG;
+    }
+  }
+  return BSKV_OK;
+}
+
+// Head counts, head_dim, page size and dtype of the cache operators.
+bskv_status check_cache_shape(const char* who, int32_t batch, int32_t num_pages, int32_t page_size,
+                              int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t num_sms) {
+  if (batch < 0 || num_pages < 0 || page_size < 1 || num_sms < 1) {
+    set_error("%s: batch=%d num_pages=%d page_size=%d num_sms=%d", who, batch, num_pages, page_size, num_sms);
+    return BSKV_ERR_INVALID_ARG;
+  }
+  if (num_qo_heads < 1 || num_kv_heads < 1 || num_qo_heads % num_kv_heads != 0) {
+    set_error("%s: num_qo_heads (%d) must be a positive multiple of num_kv_heads (%d)", who,
+              num_qo_heads, num_kv_heads);
+    return BSKV_ERR_INVALID_ARG;
+  }
+  if (head_dim != 64 && head_dim != 128) { set_error("%s: head_dim %d not in {64,128}", who, head_dim); return BSKV_ERR_UNSUPPORTED; }
+  if (!fp4_page_size(page_size)) { set_error("%s: page_size %d unsupported (8 or a multiple of 16)", who, page_size); return BSKV_ERR_UNSUPPORTED; }
+  return BSKV_OK;
+}
+
+}  // namespace
+
+extern "C" bskv_status bskv_plan_decode_fp4(const int32_t* kv_indptr, const int32_t* kv_indices,
+                                            const int32_t* kv_last_page_len, int32_t batch,
+                                            int32_t num_pages, int32_t page_size,
+                                            int32_t num_qo_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t dtype, int32_t num_sms,
+                                            int32_t max_workers, bskv_plan** out_plan) {
+  const char* who = "plan_decode_fp4";
+  if (!out_plan) { set_error("%s: out_plan is NULL", who); return BSKV_ERR_INVALID_ARG; }
+  *out_plan = nullptr;
+  if (bskv_status s = check_cache_shape(who, batch, num_pages, page_size, num_qo_heads,
+                                        num_kv_heads, head_dim, num_sms))
+    return s;
+  if (max_workers < 0) { set_error("%s: max_workers=%d", who, max_workers); return BSKV_ERR_INVALID_ARG; }
+  if (dtype != BSKV_BF16 && dtype != BSKV_FP16) { set_error("%s: dtype %s unsupported", who, dtype_name(dtype)); return BSKV_ERR_UNSUPPORTED; }
+  const int32_t group = num_qo_heads / num_kv_heads;
+  if (group > 16) { set_error("%s: %d query heads per kv head (max 16)", who, group); return BSKV_ERR_UNSUPPORTED; }
+  std::vector<int64_t> req;
+  if (bskv_status s = page_table_lens(who, kv_indptr, kv_indices, kv_last_page_len, batch,
+                                      num_pages, page_size, req))
+    return s;
+  std::vector<int64_t> len(size_t(batch) * size_t(num_kv_heads));
+  int64_t total = 0;
+  for (int32_t b = 0; b < batch; ++b) {
+    total += req[size_t(b)];
+    for (int32_t h = 0; h < num_kv_heads; ++h) len[size_t(b) * num_kv_heads + h] = req[size_t(b)];
+  }
+  if (total > INT32_MAX / num_kv_heads || len.size() > size_t(INT32_MAX / 4)) { set_error("%s: too many tokens", who); return BSKV_ERR_UNSUPPORTED; }
+  const int64_t slots_per_sm = kFp4Warps * fp4_ctas_per_sm(group > 8 ? 2 : 1);
+  std::vector<int32_t> worker_ptr, merges;
+  std::vector<Chunk> chunks;
+  int32_t slots = 0;
+  linear_partition(len, kFp4Tile, max_workers > 0 ? max_workers : num_sms * slots_per_sm,
+                   worker_ptr, chunks, slots, merges);
+  const int32_t P = int32_t(worker_ptr.size() - 1);
+  bskv_plan* p = new bskv_plan();
+  p->kind = KIND_DECODE_FP4;
+  p->batch = batch; p->num_pages = num_pages; p->page_size = page_size;
+  p->num_qo_heads = num_qo_heads; p->num_kv_heads = num_kv_heads; p->head_dim = head_dim;
+  p->dtype = dtype;
+  assemble(p, KIND_DECODE_FP4, int32_t(len.size()), worker_ptr, chunks, slots, merges, kFp4Tile,
+           kv_indptr, batch > 0 ? size_t(batch) + 1 : 0, kv_indices,
+           batch > 0 ? size_t(kv_indptr[batch]) : 0, (P + kFp4Warps - 1) / kFp4Warps, 0);
+  p->float_ws_bytes = slots == 0 ? 0
+      : align256(size_t(slots) * group * head_dim * 4) + align256(size_t(slots) * group * 4);
+  p->counter_words = merges.size() / 3;
+  for (size_t i = 2; i < merges.size(); i += 3) p->max_merge_count = std::max(p->max_merge_count, merges[i]);
+  *out_plan = p;
+  log_plan("bskv_plan_decode_fp4", p);
   return BSKV_OK;
 }
 

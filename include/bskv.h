@@ -81,6 +81,22 @@ typedef enum bskv_dtype {
   BSKV_INT64 = 5
 } bskv_dtype;
 
+/*
+ * The 4-bit paged KV cache. A row (one token's K or V of one kv head) is head_dim E2M1 values
+ * (4 bits: sign, two exponent bits, one mantissa bit; 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives) and one E8M0 scale (2^(code - 127), code 255 = NaN) per 32 consecutive values: the
+ * MXFP4 format of the OCP Microscaling Formats specification. Value d of the row is
+ * E2M1 value d times scale d / 32. It is held in two byte tensors:
+ *   kv_codes  (num_pages, 2, num_kv_heads, page_size, head_dim / 2), byte strides codes_strides
+ *             {page, K/V, kv head, slot}; byte i of a row holds value 2i in its low four bits
+ *             and value 2i + 1 in its high four;
+ *   kv_scales (num_pages, 2, num_kv_heads, page_size, head_dim / 32), byte strides
+ *             scales_strides {page, K/V, kv head}; the slots of a head and the scales of a slot
+ *             are contiguous.
+ * Strides are multiples of 16 bytes. page_size is 8 or a multiple of 16, head_dim 64 or 128. A
+ * token takes 17/64 of its 16-bit bytes.
+ */
+
 typedef struct bskv_plan bskv_plan;
 
 /* Library version (major*10000 + minor*100 + patch). */
@@ -115,6 +131,18 @@ bskv_status bskv_plan_decode(const int32_t* kv_indptr, const int32_t* kv_indices
                              int32_t page_size, int32_t num_qo_heads, int32_t num_kv_heads,
                              int32_t head_dim, int32_t dtype, int32_t num_sms,
                              int32_t max_workers, bskv_plan** out_plan);
+
+/*
+ * Batch decode plan over a 4-bit paged cache: the arguments, checks and split-KV partition of
+ * bskv_plan_decode with workers of one warp; dtype (BSKV_BF16 or BSKV_FP16) is q's and out's.
+ * Errors as bskv_plan_decode, and BSKV_ERR_UNSUPPORTED for a page_size other than 8 or a
+ * multiple of 16.
+ */
+bskv_status bskv_plan_decode_fp4(const int32_t* kv_indptr, const int32_t* kv_indices,
+                                 const int32_t* kv_last_page_len, int32_t batch,
+                                 int32_t num_pages, int32_t page_size, int32_t num_qo_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                                 int32_t num_sms, int32_t max_workers, bskv_plan** out_plan);
 
 /*
  * BSR block-sparse attention plan ([SPARSE] plan(indptr, indices, M, N, R, C,
@@ -311,6 +339,22 @@ bskv_status bskv_run_decode_noalloc(const bskv_plan* plan, const void* q,
                                     void* stream);
 
 /*
+ * Batch decode over a 4-bit paged cache, for a plan of bskv_plan_decode_fp4: what
+ * bskv_run_decode computes, with K and V the values of the cache (a scale code of 0 may read as
+ * 0 instead of 2^-127; a key's scale code 255 makes its kv head's outputs and lse NaN, a
+ * value's makes those 32 output values NaN).
+ *   q, out  [batch, num_qo_heads, head_dim] in the plan dtype, strides {batch, head} in
+ *           multiples of 8 elements; lse [batch, num_qo_heads] float32 contiguous, or NULL.
+ *   float_ws as for bskv_run_decode. Slots past a request's last token are not read.
+ * Runs of one plan share its workspaces and must not overlap on the GPU.
+ */
+bskv_status bskv_run_decode_fp4(const bskv_plan* plan, const void* q, const int64_t* q_strides,
+                                const void* kv_codes, const int64_t* codes_strides,
+                                const void* kv_scales, const int64_t* scales_strides, void* out,
+                                const int64_t* out_strides, float* lse, float sm_scale,
+                                void* float_ws, size_t float_ws_bytes, void* stream);
+
+/*
  * BSR block-sparse attention ([SPARSE] run(q, k, v, out, lse)):
  *   q [M, num_qo_heads, head_dim], k and v [N, num_kv_heads, head_dim] (strides {row,
  *   head} in elements); out like q; lse [M, num_qo_heads] float32 contiguous or NULL.
@@ -458,6 +502,39 @@ bskv_status bskv_rope_quantize_fp8_append_paged(
     int64_t num_pages, void* kv_pages,
     int32_t pos_dtype, const void* cos_sin, int32_t cos_sin_dtype, int64_t max_seq_len,
     int32_t is_neox, float quant_scale_q, float quant_scale_kv, void* stream);
+
+/*
+ * K and V rows quantised into a 4-bit paged cache.
+ *   k, v [nnz, num_kv_heads, head_dim] BSKV_BF16 or BSKV_FP16, strides {row, head} in multiples
+ *   of 16 bytes. Each 32 values of largest magnitude m get the scale 2^(floor(log2 m) - 2) (at
+ *   least 2^-127), and each value the nearest E2M1 multiple of it, ties to even, at most 6. A
+ *   block that holds an infinity or a NaN gets scale code 255: all its 32 values read as NaN.
+ *   Destination, all int32 on the device, as for bskv_rope_quantize_fp8_append_paged: row i is
+ *   token positions[i] of request batch_indices[i] and goes to its page and slot through
+ *   kv_indptr [batch + 1] and kv_indices. A row whose request, position or page is out of range
+ *   is not written and raises BSKV_ERR_DEVICE_INDEX in the device status word. Other cache bytes
+ *   are not touched. Rows that share a destination race.
+ */
+bskv_status bskv_quantize_fp4_append_paged(
+    const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides, int32_t dtype,
+    int64_t nnz, int32_t num_kv_heads, int32_t head_dim, const int32_t* batch_indices,
+    const int32_t* positions, const int32_t* kv_indptr, const int32_t* kv_indices, int32_t batch,
+    int32_t page_size, int64_t num_pages, void* kv_codes, const int64_t* codes_strides,
+    void* kv_scales, const int64_t* scales_strides, void* stream);
+
+/*
+ * Rows of a 4-bit paged cache read back as values: row i of k_out and v_out [nnz, num_kv_heads,
+ * head_dim] (BSKV_BF16: exact; BSKV_FP32: exact; BSKV_FP16: rounded to nearest even) is token
+ * positions[i] of request batch_indices[i]. Index arrays, strides and out-of-range rows (their
+ * output rows are left as they were) as for bskv_quantize_fp4_append_paged.
+ */
+bskv_status bskv_dequantize_fp4_paged(
+    const void* kv_codes, const int64_t* codes_strides, const void* kv_scales,
+    const int64_t* scales_strides, const int32_t* batch_indices, const int32_t* positions,
+    const int32_t* kv_indptr, const int32_t* kv_indices, int32_t batch, int32_t page_size,
+    int64_t num_pages, void* k_out, const int64_t* k_strides, void* v_out,
+    const int64_t* v_strides, int32_t dtype, int64_t nnz, int32_t num_kv_heads, int32_t head_dim,
+    void* stream);
 
 /*
  * Merge attention states ([CHEAT] cascade.rst merge_states; [SKILL] Cascade Inference):
