@@ -23,6 +23,8 @@ __all__ = [
     "bskv_run_bsr", "bskv_run_mla_sparse",
     "bskv_plan_decode_fp4", "bskv_run_decode_fp4",
     "bskv_quantize_fp4_append_paged", "bskv_dequantize_fp4_paged",
+    "bskv_plan_attn_weights", "bskv_run_attn_weights", "bskv_run_attn_weights_fp4",
+    "bskv_plan_evict", "bskv_run_evict", "bskv_run_evict_fp4",
     "bskv_rope_quantize_fp8", "bskv_merge_states",
     "bskv_get_device_status", "bskv_set_debug_force_timeout",
 ]
@@ -100,6 +102,15 @@ _SIGS = {
                                         _P, _I32, _I32, _I64, _P, _I64P, _P, _I64P, _P], _I32),
     "bskv_dequantize_fp4_paged": ([_P, _I64P, _P, _I64P, _P, _P, _P, _P, _I32, _I32, _I64, _P,
                                    _I64P, _P, _I64P, _I32, _I64, _I32, _I32, _P], _I32),
+    "bskv_plan_attn_weights": ([_I32P, _I32P, _I32P, _I32P, _I32, _I32, _I32, _I32, _I32, _I32,
+                                _I32, _I32, _I32, ctypes.POINTER(_P)], _I32),
+    "bskv_run_attn_weights": ([_P, _P, _I64P, _P, _I64P, _P, _P, _I64P, _F, _F, _P], _I32),
+    "bskv_run_attn_weights_fp4": ([_P, _P, _I64P, _P, _I64P, _P, _I64P, _P, _P, _I64P, _F, _F, _P],
+                                  _I32),
+    "bskv_plan_evict": ([_I32P, _I32P, _I32P, _I32P, _I32, _I32, _I32P, _I32P, _I32, _I32, _I32,
+                         _I32, _I32, _I32, ctypes.POINTER(_P)], _I32),
+    "bskv_run_evict": ([_P, _P, _I64P, _I32, _P, _I64P, _P, _P], _I32),
+    "bskv_run_evict_fp4": ([_P, _P, _I64P, _I32, _P, _I64P, _P, _I64P, _P, _P], _I32),
     "bskv_merge_states": ([_P, _P, _I64, _I32, _I32, _I32, _P, _I32, _P, _P], _I32),
     "bskv_get_device_status": ([_I32P, _I32], _I32),
     "bskv_set_debug_force_timeout": ([_I32], _I32),
@@ -795,6 +806,160 @@ def bskv_run_decode_fp4(plan, q, kv_codes, kv_scales, out=None, lse=None, return
             _strides_of(out, 2), _ptr(lse), 0.0 if sm_scale is None else float(sm_scale), _ptr(fw),
             0 if fw is None else fw.numel(), _stream(q)))
     return (out, lse) if return_lse else out
+
+
+def bskv_plan_attn_weights(qo_indptr, kv_indptr, kv_indices, kv_last_page_len, num_pages, page_size,
+                           num_qo_heads, num_kv_heads, head_dim, causal=True, dtype=torch.bfloat16,
+                           num_sms=None):
+    """Plan of the accumulated attention weights, from HOST arrays; qo_indptr None: one query per
+    request (the decode step)."""
+    fn = "bskv_plan_attn_weights"
+    lib = load_library()
+    ip, ipp, ix, ixp, lp, lpp, batch = _page_table(fn, kv_indptr, kv_indices, kv_last_page_len)
+    qi, qip = (None, None) if qo_indptr is None else _i32_array(qo_indptr)
+    if qi is not None and qi.numel() != batch + 1:
+        raise ValueError("%s: qo_indptr has %d entries, kv_indptr %d" % (fn, qi.numel(), batch + 1))
+    h = ctypes.c_void_p()
+    ns = _num_sms() if num_sms is None else num_sms
+    _check(fn, lib.bskv_plan_attn_weights(
+        None if qip is None else ctypes.cast(qip, _I32P), ctypes.cast(ipp, _I32P),
+        ctypes.cast(ixp, _I32P), ctypes.cast(lpp, _I32P), batch, int(num_pages), int(page_size),
+        int(num_qo_heads), int(num_kv_heads), int(head_dim), int(bool(causal)), _DT[dtype], int(ns),
+        ctypes.byref(h)))
+    return Plan(h.value, "attn_weights", batch=batch, total_qo=batch if qi is None else int(qi[-1]),
+                num_pages=int(num_pages), page_size=int(page_size), num_qo_heads=int(num_qo_heads),
+                num_kv_heads=int(num_kv_heads), head_dim=int(head_dim), dtype=dtype)
+
+
+def _scores(fn, plan, scores, device):
+    i = plan.info
+    _want(fn, "scores", scores, (i["num_pages"], i["num_kv_heads"], i["page_size"]), (torch.float32,),
+          device)
+    _rows_last(fn, "scores", scores)
+    return scores.data_ptr(), _strides_of(scores, 2)
+
+
+def _kv_pages(fn, plan, kv_cache, dtypes, device):
+    i = plan.info
+    _want(fn, "kv_cache", kv_cache, (i["num_pages"], 2, i["num_kv_heads"], i["page_size"],
+                                     i["head_dim"]), dtypes, device)
+    _rows_last(fn, "kv_cache", kv_cache)
+    return kv_cache.data_ptr(), _strides_of(kv_cache, 4)
+
+
+def _run_attn_weights(fn, plan, q, cache, lse, scores, decay, sm_scale):
+    i = plan.info
+    dev = q.device if torch.is_tensor(q) else None
+    _want(fn, "q", q, (i["total_qo"], i["num_qo_heads"], i["head_dim"]), (i["dtype"],), dev)
+    _rows_last(fn, "q", q)
+    _want(fn, "lse", lse, (i["total_qo"], i["num_qo_heads"]), (torch.float32,), dev)
+    _dense(fn, ("lse", lse))
+    where = _scores(fn, plan, scores, dev)
+    cache = cache(dev)
+    with torch.cuda.device(dev):
+        _ready(fn, plan, dev)
+        _check(fn, getattr(load_library(), fn)(
+            plan.handle, q.data_ptr(), _strides_of(q, 2), *cache, lse.data_ptr(), *where,
+            float(decay), 0.0 if sm_scale is None else float(sm_scale), _stream(q)))
+    return scores
+
+
+def bskv_run_attn_weights(plan, q, kv_cache, lse, scores, decay=1.0, sm_scale=None):
+    """Add the queries' attention weights over the cached tokens, summed per kv head, to scores
+    [pages, Hkv, page_size] float32 (in place): q [total_qo, Hq, D], kv_cache [pages, 2, Hkv,
+    page_size, D], lse [total_qo, Hq] as the attention run returned it. Old scores are multiplied
+    by decay first; those of the queries' own tokens (the last of each request), and all of them
+    with decay 0, start anew."""
+    fn = "bskv_run_attn_weights"
+    _check_plan(fn, plan, "attn_weights")
+    return _run_attn_weights(fn, plan, q, lambda dev: _kv_pages(fn, plan, kv_cache,
+                                                                (plan.info["dtype"],), dev),
+                             lse, scores, decay, sm_scale)
+
+
+def bskv_run_attn_weights_fp4(plan, q, kv_codes, kv_scales, lse, scores, decay=1.0, sm_scale=None):
+    """bskv_run_attn_weights over a 4-bit paged cache."""
+    fn = "bskv_run_attn_weights_fp4"
+    _check_plan(fn, plan, "attn_weights")
+    i = plan.info
+    return _run_attn_weights(fn, plan, q, lambda dev: _fp4_cache(
+        fn, kv_codes, kv_scales, dev, i["num_pages"], i["page_size"], i["num_kv_heads"],
+        i["head_dim"]), lse, scores, decay, sm_scale)
+
+
+def bskv_plan_evict(kv_indptr, kv_indices, kv_last_page_len, keep_len, sink, recent, num_pages,
+                    page_size, num_kv_heads, head_dim, dst_indptr=None, dst_indices=None,
+                    num_sms=None):
+    """Plan of an eviction to keep_len[b] tokens per request, from HOST arrays: into the pages
+    dst_indptr / dst_indices, or in place without them. plan.info["kept_indptr"] delimits each
+    request's entries in the runs' kept lists."""
+    fn = "bskv_plan_evict"
+    lib = load_library()
+    ip, ipp, ix, ixp, lp, lpp, batch = _page_table(fn, kv_indptr, kv_indices, kv_last_page_len)
+    kl, klp = _i32_array(keep_len)
+    if kl.numel() != batch:
+        raise ValueError("%s: keep_len has %d entries for %d requests" % (fn, kl.numel(), batch))
+    dip = dxp = None
+    if (dst_indptr is None) != (dst_indices is None):
+        raise ValueError("%s: give dst_indptr and dst_indices, or neither" % fn)
+    if dst_indptr is not None:
+        di, dip = _i32_array(dst_indptr)
+        dx, dxp = _i32_array(dst_indices)
+        if di.numel() != batch + 1 or dx.numel() < int(di[-1]):
+            raise ValueError("%s: dst_indptr has %d entries for %d requests, dst_indices %d"
+                             % (fn, di.numel(), batch, dx.numel()))
+    h = ctypes.c_void_p()
+    ns = _num_sms() if num_sms is None else num_sms
+    _check(fn, lib.bskv_plan_evict(
+        ctypes.cast(ipp, _I32P), ctypes.cast(ixp, _I32P), ctypes.cast(lpp, _I32P),
+        ctypes.cast(klp, _I32P), int(sink), int(recent),
+        None if dip is None else ctypes.cast(dip, _I32P),
+        None if dxp is None else ctypes.cast(dxp, _I32P), batch, int(num_pages), int(page_size),
+        int(num_kv_heads), int(head_dim), int(ns), ctypes.byref(h)))
+    pages = ip[1:batch + 1] - ip[:batch]
+    lens = torch.where(pages > 0, (pages - 1) * int(page_size) + lp[:batch], torch.zeros_like(pages))
+    kept = [0]
+    for n in torch.minimum(lens, kl).tolist():
+        kept.append(kept[-1] + n)
+    return Plan(h.value, "evict", batch=batch, num_pages=int(num_pages), page_size=int(page_size),
+                num_kv_heads=int(num_kv_heads), head_dim=int(head_dim), kept_indptr=kept)
+
+
+def _run_evict(fn, plan, scores, cache, kept, compact_scores):
+    dev = scores.device if torch.is_tensor(scores) else None
+    where = _scores(fn, plan, scores, dev)
+    cache = cache(dev)
+    shape = (plan.info["num_kv_heads"], plan.info["kept_indptr"][-1])
+    if kept is None:
+        kept = torch.empty(shape, dtype=torch.int32, device=dev)
+    _want(fn, "kept", kept, shape, (torch.int32,), dev)
+    _dense(fn, ("kept", kept))
+    with torch.cuda.device(dev):
+        _ready(fn, plan, dev)
+        _check(fn, getattr(load_library(), fn)(plan.handle, *where, int(bool(compact_scores)), *cache,
+                                               kept.data_ptr(), _stream(scores)))
+    return kept
+
+
+def bskv_run_evict(plan, scores, kv_cache, kept=None, compact_scores=True):
+    """Keep the plan's number of tokens per request, chosen per kv head by scores [pages, Hkv,
+    page_size], and move their rows of kv_cache [pages, 2, Hkv, page_size, D] (16-bit), and with
+    compact_scores their scores, to the front. Returns the old slots of the kept tokens [Hkv,
+    kept_indptr[-1]] int32."""
+    fn = "bskv_run_evict"
+    _check_plan(fn, plan, "evict")
+    return _run_evict(fn, plan, scores, lambda dev: _kv_pages(
+        fn, plan, kv_cache, (torch.bfloat16, torch.float16), dev), kept, compact_scores)
+
+
+def bskv_run_evict_fp4(plan, scores, kv_codes, kv_scales, kept=None, compact_scores=True):
+    """bskv_run_evict over a 4-bit paged cache."""
+    fn = "bskv_run_evict_fp4"
+    _check_plan(fn, plan, "evict")
+    i = plan.info
+    return _run_evict(fn, plan, scores, lambda dev: _fp4_cache(
+        fn, kv_codes, kv_scales, dev, i["num_pages"], i["page_size"], i["num_kv_heads"],
+        i["head_dim"]), kept, compact_scores)
 
 
 def bskv_merge_states(v, s, out_dtype=torch.float32, v_out=None, s_out=None):

@@ -33,6 +33,7 @@
 #include "fp4.cuh"
 #include "internal.h"
 #include "launch.h"
+#include "page_walk.cuh"
 #include "split_merge.cuh"
 
 namespace bskv {
@@ -41,6 +42,7 @@ namespace {
 using namespace dev;
 
 constexpr int kTile = kFp4Tile;  // tokens per stage
+static_assert(kTile == kWalkTile, "one walk step per stage");
 constexpr int kWarps = kFp4Warps;
 constexpr int kStages = 3;
 
@@ -84,48 +86,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// fp32 2^(code - 127) of byte b of a word of scale codes; code 0 reads as 0 (its values lie
-// below 2^-124) and code 255 is handled apart (nan_bytes).
-__device__ __forceinline__ float scale_of(uint32_t w, int b) {
-  const uint32_t s = b == 0 ? w << 23 : b == 1 ? w << 15 : b == 2 ? w << 7 : w >> 1;
-  return __uint_as_float(s & 0x7f800000u);
-}
-// Bit 7 of each byte that is 255 (other bits are noise).
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  return ((w & 0x7f7f7f7fu) + 0x01010101u) & w;
-}
-
-template <int D>
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int row) {
-  if constexpr (D == 128) return *reinterpret_cast<const uint32_t*>(s + 4 * row);
-  else return *reinterpret_cast<const uint16_t*>(s + 2 * row);
-}
-
-// 2^k for the power of two with bits `x`, inverted exactly (0 for 2^127).
-__device__ __forceinline__ float pow2_inverse(float x) {
-  return __uint_as_float((254u << 23) - __float_as_uint(x));
-}
-__device__ __forceinline__ int exponent_of(float x) {
-  return int(__float_as_uint(x) >> 23) - 127;
-}
-__device__ __forceinline__ float pow2(int k) { return __uint_as_float(uint32_t(k + 127) << 23); }
-
-__device__ __forceinline__ float max_over_rows(float x) {  // lanes of equal lane & 3
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-}
-__device__ __forceinline__ float sum_over_rows(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 4);
-  x += __shfl_xor_sync(0xffffffffu, x, 8);
-  return x + __shfl_xor_sync(0xffffffffu, x, 16);
-}
-
 // Everything a warp keeps of the unit it works on. Column j of a lane is query head
 // 8 (j / 2) + 2 t + (j & 1) of the kv head's group.
 template <int D, int NT>
@@ -145,45 +105,9 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int h = 8 * nt + g;
-    const bool live = h < p.group;
-    const T* row = static_cast<const T*>(p.q) + b * p.q_s0 + (int64_t(kvh) * p.group + h) * p.q_s1;
-    uint4 x[NB];
-#pragma unroll
-    for (int blk = 0; blk < NB; ++blk)
-      x[blk] = live ? __ldg(reinterpret_cast<const uint4*>(row + 32 * blk + 8 * t)) : make_uint4(0, 0, 0, 0);
-    float back = 1.f;
-    if constexpr (sizeof(T) == 2 && !__is_same(T, __half)) {
-      // exact power of two that puts the head's largest |q| into [2^14, 2^15)
-      uint32_t top = 0;
-#pragma unroll
-      for (int blk = 0; blk < NB; ++blk) {
-        const uint32_t w[4] = {x[blk].x, x[blk].y, x[blk].z, x[blk].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-      }
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = int(top >> 7);
-      const int k = e == 255 ? 0 : min(141 - e, 126);
-      const float f = pow2(k);
-      back = pow2(-k);
-#pragma unroll
-      for (int blk = 0; blk < NB; ++blk) {
-        const uint32_t w[4] = {x[blk].x, x[blk].y, x[blk].z, x[blk].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s.q[nt][blk][i] = pack_half2(__uint_as_float(w[i] << 16) * f,
-                                       __uint_as_float(w[i] & 0xffff0000u) * f);
-      }
-    } else {
-#pragma unroll
-      for (int blk = 0; blk < NB; ++blk) {
-        s.q[nt][blk][0] = x[blk].x;
-        s.q[nt][blk][1] = x[blk].y;
-        s.q[nt][blk][2] = x[blk].z;
-        s.q[nt][blk][3] = x[blk].w;
-      }
-    }
+    const float back = load_q_f16<T, NB>(
+        static_cast<const T*>(p.q) + b * p.q_s0 + (int64_t(kvh) * p.group + h) * p.q_s1,
+        h < p.group, lane, s.q[nt]);
     // columns 2t and 2t + 1 belong to the heads of lanes 8t and 8t + 4
     s.c[2 * nt] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t);
     s.c[2 * nt + 1] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4);
@@ -439,55 +363,21 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
   const int P = p.num_workers;
   const int w = blockIdx.x * kWarps + warp;
   if (w >= P) return;
-  const int32_t* wptr = p.meta + p.off_workers;
-  const int4* chunks = reinterpret_cast<const int4*>(p.meta + p.off_chunks);
   const int32_t* merges = p.meta + p.off_merges;
-  const int32_t* kv_indptr = p.meta + p.off_aux0;
-  const int32_t* kv_indices = p.meta + p.off_aux1;
-  const int c0 = wptr[w], c1 = wptr[w + 1], nck = c1 - c0;
-  const int Hkv = p.num_kv_heads, ps = p.page_size;
+  const int Hkv = p.num_kv_heads;
+  PageWalk walk(p.meta, p.off_workers, p.off_chunks, p.off_aux0, p.off_aux1, w, Hkv, p.page_size, lane);
+  const int nck = walk.count();
 
-  // Producer: tokens [tok, end) of chunk pk are still to be copied. Lane i holds the page and
-  // slot of the 8 tokens at win + 8 i, and of those 256 tokens later (loaded a window ahead).
-  int pk = 0, tok = 0, end = 0, pbase = 0, kvh_p = 0, win = 0;
-  int page = 0, slot = 0, page2 = 0, slot2 = 0;
-  auto lookup = [&](int first, int& pg, int& sl) {
-    const int at = first + 8 * lane;
-    if (at < end) {
-      const int i = at / ps;
-      pg = __ldg(kv_indices + pbase + i);
-      sl = at - i * ps;
-    }
-  };
-  auto open_chunk = [&]() {
-    if (pk >= nck) return;
-    const int4 ch = chunks[chunk_at(c0, c1, pk)];
-    const int b = ch.x / Hkv;
-    kvh_p = ch.x - b * Hkv;
-    tok = win = ch.y;
-    end = ch.z;
-    pbase = __ldg(kv_indptr + b);
-    lookup(win, page, slot);
-    lookup(win + 256, page2, slot2);
-  };
   auto issue = [&](int stage) {
-    if (pk < nck) {
-      if (tok - win == 256) {
-        win = tok;
-        page = page2;
-        slot = slot2;
-        lookup(win + 256, page2, slot2);
-      }
+    if (walk.live()) {
+      walk.enter();
       uint8_t* st = ring + stage * Sh::kStage;
-      const int g0 = (tok - win) >> 3;
-      const uint8_t* cb = p.codes + kvh_p * p.c_s2;
+      int pg, sl;
 #pragma unroll
       for (int i = 0; i < Sh::kParts; ++i) {
         const int r = lane / Sh::kParts + i * (32 / Sh::kParts), part = lane % Sh::kParts;
-        const int src = g0 + (r >> 3);
-        const int pg = __shfl_sync(0xffffffffu, page, src), sl = __shfl_sync(0xffffffffu, slot, src);
-        if (tok + (r & ~7) < end) {
-          const uint8_t* from = cb + pg * p.c_s0 + (sl + (r & 7)) * p.c_s3 + part * 16;
+        if (walk.row(r, pg, sl)) {
+          const uint8_t* from = p.codes + pg * p.c_s0 + walk.kvh * p.c_s2 + sl * p.c_s3 + part * 16;
           const int to = r * Sh::kRow + ((part ^ ((r >> Sh::kSwzShift) & (Sh::kParts - 1))) << 4);
           cp_async_16(st + to, from);
           cp_async_16(st + Sh::kV + to, from + p.c_s1);
@@ -495,23 +385,15 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
       }
       constexpr int kPer = 16 / Sh::kBlocks;   // tokens per 16 bytes of scales
       constexpr int kCopies = kTile / kPer;
-      const int i = lane % kCopies, r = i * kPer, which = (lane / kCopies) & 1;
-      const int src = g0 + (r >> 3);
-      const int pg = __shfl_sync(0xffffffffu, page, src), sl = __shfl_sync(0xffffffffu, slot, src);
-      if (lane < 2 * kCopies && tok + (r & ~7) < end)
+      const int i = lane % kCopies, which = (lane / kCopies) & 1;
+      if (walk.row(i * kPer, pg, sl) && lane < 2 * kCopies)
         cp_async_16(st + Sh::kKs + which * kTile * Sh::kBlocks + 16 * i,
-                    p.scales + pg * p.s_s0 + which * p.s_s1 + kvh_p * p.s_s2 +
-                        (sl + (r & 7)) * Sh::kBlocks);
-      tok += kTile;
-      if (tok >= end) {
-        ++pk;
-        open_chunk();
-      }
+                    p.scales + pg * p.s_s0 + which * p.s_s1 + walk.kvh * p.s_s2 + sl * Sh::kBlocks);
+      walk.advance();
     }
     cp_async_commit();
   };
 
-  open_chunk();
   for (int i = 0; i < kStages - 1; ++i) issue(i);
 
   // Units without tokens are zero-filled by the workers in turn.
@@ -522,7 +404,7 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
   State<D, NT> s;
   int done = 0;
   for (int k = 0; k < nck; ++k) {
-    const int4 ch = chunks[chunk_at(c0, c1, k)];
+    const int4 ch = walk.chunk(k);
     const int b = ch.x / Hkv, kvh = ch.x - b * Hkv;
     load_q<T, D, NT>(p, b, kvh, lane, s);
     for (int at = ch.y; at < ch.z; at += kTile, ++done) {

@@ -72,5 +72,92 @@ __device__ __forceinline__ bool page_slot(const int32_t* indptr, const int32_t* 
   return page >= 0 && page < num_pages;
 }
 
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// fp32 2^(code - 127) of byte b of a word of scale codes; code 0 reads as 0 (its values lie
+// below 2^-124) and code 255 is handled apart (nan_bytes).
+__device__ __forceinline__ float scale_of(uint32_t w, int b) {
+  const uint32_t s = b == 0 ? w << 23 : b == 1 ? w << 15 : b == 2 ? w << 7 : w >> 1;
+  return __uint_as_float(s & 0x7f800000u);
+}
+// Bit 7 of each byte that is 255 (other bits are noise).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & w;
+}
+
+// Scale codes of row `row` of a shared-memory tile (2 bytes for D = 64).
+template <int D>
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int row) {
+  if constexpr (D == 128) return *reinterpret_cast<const uint32_t*>(s + 4 * row);
+  else return *reinterpret_cast<const uint16_t*>(s + 2 * row);
+}
+
+// 2^k for the power of two with bits `x`, inverted exactly (0 for 2^127).
+__device__ __forceinline__ float pow2_inverse(float x) {
+  return __uint_as_float((254u << 23) - __float_as_uint(x));
+}
+__device__ __forceinline__ int exponent_of(float x) {
+  return int(__float_as_uint(x) >> 23) - 127;
+}
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float(uint32_t(k + 127) << 23); }
+
+__device__ __forceinline__ float max_over_rows(float x) {  // lanes of equal lane & 3
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float sum_over_rows(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// The B fragments of a query row of D = 32 NB values for products over NB 32-value blocks: lane
+// (g, t) holds values 32 b + 8 t .. + 7 of row g as four f16 pairs per block b. bf16 rows are
+// multiplied by the power of two that puts their largest magnitude into [2^14, 2^15) (exact:
+// values below 2^-29 of it may lose low bits to f16's subnormals); returns its inverse.
+template <typename T, int NB>
+__device__ __forceinline__ float load_q_f16(const T* row, bool live, int lane, uint32_t (&q)[NB][4]) {
+  const int t = lane & 3;
+  uint4 x[NB];
+#pragma unroll
+  for (int blk = 0; blk < NB; ++blk)
+    x[blk] = live ? __ldg(reinterpret_cast<const uint4*>(row + 32 * blk + 8 * t)) : make_uint4(0, 0, 0, 0);
+  if constexpr (__is_same(T, __half)) {
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      q[blk][0] = x[blk].x;
+      q[blk][1] = x[blk].y;
+      q[blk][2] = x[blk].z;
+      q[blk][3] = x[blk].w;
+    }
+    return 1.f;
+  } else {
+    uint32_t top = 0;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      const uint32_t w[4] = {x[blk].x, x[blk].y, x[blk].z, x[blk].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int e = int(top >> 7);
+    const int k = e == 255 ? 0 : min(141 - e, 126);
+    const float f = pow2(k);
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      const uint32_t w[4] = {x[blk].x, x[blk].y, x[blk].z, x[blk].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        q[blk][i] = pack_half2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+    }
+    return pow2(-k);
+  }
+}
+
 }  // namespace dev
 }  // namespace bskv

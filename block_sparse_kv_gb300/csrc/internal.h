@@ -15,7 +15,8 @@ namespace bskv {
 
 // ---- plan metadata: int32 words, header then 16-byte aligned sections ----------------
 constexpr int32_t kMetaMagic = 0x766b7362;  // "bskv"
-enum Kind : int32_t { KIND_DECODE = 1, KIND_BSR = 2, KIND_MLA = 3, KIND_DECODE_FP4 = 4 };
+enum Kind : int32_t { KIND_DECODE = 1, KIND_BSR = 2, KIND_MLA = 3, KIND_DECODE_FP4 = 4,
+                      KIND_WEIGHTS = 5, KIND_EVICT = 6 };
 enum Header : int {
   H_MAGIC = 0,
   H_KIND,
@@ -120,6 +121,16 @@ constexpr int kFp4Tile = 32;   // tokens per pipeline stage
 constexpr int kFp4Warps = 4;
 constexpr int fp4_ctas_per_sm(int column_tiles) { return column_tiles > 1 ? 2 : 4; }
 
+// Attention-weight plans. Stream variants (at most 8 or 16 query rows, queries times heads of a
+// group, in every request): one worker per warp over ranges of tokens of (request, kv head)
+// units. Tile variant: one CTA per 128 keys of a request (chunk {request, first, end, 0}) and kv
+// head. Per request {first query, queries, tokens} stands in the merge section.
+enum WeightsVariant : int32_t { WEIGHTS_STREAM8 = 0, WEIGHTS_STREAM16 = 1, WEIGHTS_TILE = 2 };
+constexpr int kWeightsWarps = 4;
+constexpr int kWeightsKeys = 128;
+// CTAs of the stream kernel an SM holds (its ring of 16-bit rows of 128 dims takes 98 KB).
+constexpr int weights_ctas_per_sm(int head_dim, bool fp4) { return !fp4 && head_dim == 128 ? 2 : 4; }
+
 // Page sizes of a 4-bit paged cache: the kernels copy groups of 8 tokens that lie in one page.
 inline bool fp4_page_size(int32_t page_size) {
   return page_size == 8 || (page_size >= 16 && page_size % 16 == 0);
@@ -174,6 +185,10 @@ struct bskv_plan {
   // page-major decode: word offset in the metadata of the per-worker start records
   // (kDecodeStartWords each), or -1
   int32_t decode_starts = -1;
+  // evict: tokens that stay over all requests, protected first / last tokens, the longest
+  // request, whether the kept rows stay in their pages, CTAs that share the rows of one slice
+  int64_t kept_total = 0;
+  int32_t sink = 0, recent = 0, longest = 0, in_place = 0, parts = 1;
   // set by bskv_plan_upload
   const int32_t* meta_dev = nullptr;
   int32_t* counters_dev = nullptr;  // one merge counter per merge item, zero between runs

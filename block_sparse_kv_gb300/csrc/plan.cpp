@@ -401,6 +401,13 @@ void log_plan(const char* name, const bskv_plan* p) {
     case KIND_DECODE_FP4:
       kernel = "decode_fp4_kernel (one worker per warp)";
       break;
+    case KIND_WEIGHTS:
+      kernel = m[H_VARIANT] == WEIGHTS_TILE ? "weights_tile_kernel (128 keys per CTA)"
+                                            : "weights_stream_kernel (one worker per warp)";
+      break;
+    case KIND_EVICT:
+      kernel = "evict_select_kernel, evict_move_kernel";
+      break;
     case KIND_MLA:
       kernel = p->mla_variant == MLA_PAGED ? "mla_kernel (rows from the page table)"
                                            : "mla_kernel (sparse rows)";
@@ -578,6 +585,20 @@ bskv_status page_table_lens(const char* who, const int32_t* kv_indptr, const int
   return BSKV_OK;
 }
 
+// Every page at most once: the runs of the plan write to them.
+bskv_status pages_once(const char* who, const char* name, const int32_t* indices, int64_t n,
+                       int32_t num_pages) {
+  std::vector<uint8_t> seen(size_t(num_pages), 0);
+  for (int64_t i = 0; i < n; ++i) {
+    if (seen[size_t(indices[i])]) {
+      set_error("%s: page %d is listed twice in %s; a page that is written has one owner", who, indices[i], name);
+      return BSKV_ERR_INVALID_ARG;
+    }
+    seen[size_t(indices[i])] = 1;
+  }
+  return BSKV_OK;
+}
+
 // Head counts, head_dim, page size and dtype of the cache operators.
 bskv_status check_cache_shape(const char* who, int32_t batch, int32_t num_pages, int32_t page_size,
                               int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -646,6 +667,151 @@ extern "C" bskv_status bskv_plan_decode_fp4(const int32_t* kv_indptr, const int3
   for (size_t i = 2; i < merges.size(); i += 3) p->max_merge_count = std::max(p->max_merge_count, merges[i]);
   *out_plan = p;
   log_plan("bskv_plan_decode_fp4", p);
+  return BSKV_OK;
+}
+
+extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const int32_t* kv_indptr,
+                                              const int32_t* kv_indices,
+                                              const int32_t* kv_last_page_len, int32_t batch,
+                                              int32_t num_pages, int32_t page_size,
+                                              int32_t num_qo_heads, int32_t num_kv_heads,
+                                              int32_t head_dim, int32_t causal, int32_t dtype,
+                                              int32_t num_sms, bskv_plan** out_plan) {
+  const char* who = "plan_attn_weights";
+  if (!out_plan) { set_error("%s: out_plan is NULL", who); return BSKV_ERR_INVALID_ARG; }
+  *out_plan = nullptr;
+  if (bskv_status s = check_cache_shape(who, batch, num_pages, page_size, num_qo_heads,
+                                        num_kv_heads, head_dim, num_sms))
+    return s;
+  if (dtype != BSKV_BF16 && dtype != BSKV_FP16) { set_error("%s: dtype %s unsupported", who, dtype_name(dtype)); return BSKV_ERR_UNSUPPORTED; }
+  if (num_kv_heads > 65535) { set_error("%s: %d kv heads", who, num_kv_heads); return BSKV_ERR_UNSUPPORTED; }
+  std::vector<int64_t> req;
+  if (bskv_status s = page_table_lens(who, kv_indptr, kv_indices, kv_last_page_len, batch,
+                                      num_pages, page_size, req))
+    return s;
+  if (bskv_status s = pages_once(who, "kv_indices", kv_indices, batch > 0 ? kv_indptr[batch] : 0, num_pages)) return s;
+  if (batch > 0 && qo_indptr && qo_indptr[0] != 0) { set_error("%s: qo_indptr[0] must be 0", who); return BSKV_ERR_INVALID_ARG; }
+  const int32_t group = num_qo_heads / num_kv_heads;
+  std::vector<int32_t> queries;  // 3 per request
+  int64_t most = 0, total = 0;
+  for (int32_t b = 0; b < batch; ++b) {
+    const int32_t q0 = qo_indptr ? qo_indptr[b] : b;
+    const int64_t n = qo_indptr ? int64_t(qo_indptr[b + 1]) - q0 : 1;
+    if (n < 0) { set_error("%s: qo_indptr decreases at %d", who, b); return BSKV_ERR_INVALID_ARG; }
+    if (n * group > INT32_MAX / 2) { set_error("%s: request %d has too many queries", who, b); return BSKV_ERR_UNSUPPORTED; }
+    queries.insert(queries.end(), {q0, int32_t(n), int32_t(req[size_t(b)])});
+    if (req[size_t(b)] > 0) most = std::max(most, n * group);
+    total += req[size_t(b)];
+  }
+  if (total > INT32_MAX / num_kv_heads || int64_t(batch) * num_kv_heads > INT32_MAX / 4) { set_error("%s: too many tokens", who); return BSKV_ERR_UNSUPPORTED; }
+  std::vector<int32_t> worker_ptr, no_merges;
+  std::vector<Chunk> chunks;
+  int32_t grid = 0, variant;
+  int32_t units = 0;
+  if (most <= 16) {
+    variant = most <= 8 ? WEIGHTS_STREAM8 : WEIGHTS_STREAM16;
+    std::vector<int64_t> len(size_t(batch) * size_t(num_kv_heads));
+    for (int32_t b = 0; b < batch; ++b)
+      for (int32_t h = 0; h < num_kv_heads; ++h) len[size_t(b) * num_kv_heads + h] = req[size_t(b)];
+    int32_t slots = 0;
+    linear_partition(len, kFp4Tile, int64_t(num_sms) * kWeightsWarps * 4, worker_ptr, chunks, slots, no_merges);
+    grid = (int32_t(worker_ptr.size()) - 1 + kWeightsWarps - 1) / kWeightsWarps;
+    units = int32_t(len.size());
+  } else {
+    variant = WEIGHTS_TILE;
+    for (int32_t b = 0; b < batch; ++b)
+      for (int64_t t = 0; t < req[size_t(b)]; t += kWeightsKeys)
+        chunks.push_back(Chunk{b, int32_t(t), int32_t(std::min<int64_t>(t + kWeightsKeys, req[size_t(b)])), 0});
+    grid = int32_t(chunks.size());
+    units = grid;
+  }
+  bskv_plan* p = new bskv_plan();
+  p->kind = KIND_WEIGHTS;
+  p->batch = batch; p->num_pages = num_pages; p->page_size = page_size;
+  p->num_qo_heads = num_qo_heads; p->num_kv_heads = num_kv_heads; p->head_dim = head_dim;
+  p->dtype = dtype; p->causal = causal ? 1 : 0;
+  assemble(p, KIND_WEIGHTS, units, worker_ptr, chunks, 0, queries, kFp4Tile, kv_indptr,
+           batch > 0 ? size_t(batch) + 1 : 0, kv_indices, batch > 0 ? size_t(kv_indptr[batch]) : 0,
+           grid, variant);
+  *out_plan = p;
+  log_plan("bskv_plan_attn_weights", p);
+  return BSKV_OK;
+}
+
+extern "C" bskv_status bskv_plan_evict(const int32_t* kv_indptr, const int32_t* kv_indices,
+                                       const int32_t* kv_last_page_len, const int32_t* keep_len,
+                                       int32_t sink, int32_t recent, const int32_t* dst_indptr,
+                                       const int32_t* dst_indices, int32_t batch,
+                                       int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t num_sms, bskv_plan** out_plan) {
+  const char* who = "plan_evict";
+  if (!out_plan) { set_error("%s: out_plan is NULL", who); return BSKV_ERR_INVALID_ARG; }
+  *out_plan = nullptr;
+  if (bskv_status s = check_cache_shape(who, batch, num_pages, page_size, num_kv_heads,
+                                        num_kv_heads, head_dim, num_sms))
+    return s;
+  if (batch > 65535 || num_kv_heads > 65535) { set_error("%s: batch %d, %d kv heads (max 65535)", who, batch, num_kv_heads); return BSKV_ERR_UNSUPPORTED; }
+  if (sink < 0 || recent < 0) { set_error("%s: sink=%d recent=%d", who, sink, recent); return BSKV_ERR_INVALID_ARG; }
+  std::vector<int64_t> req;
+  if (bskv_status s = page_table_lens(who, kv_indptr, kv_indices, kv_last_page_len, batch,
+                                      num_pages, page_size, req))
+    return s;
+  const bool in_place = !dst_indptr;
+  const int64_t nnz = batch > 0 ? kv_indptr[batch] : 0;
+  if (batch > 0 && !keep_len) { set_error("%s: keep_len is NULL", who); return BSKV_ERR_INVALID_ARG; }
+  std::vector<int32_t> dst;
+  if (in_place) {
+    if (bskv_status s = pages_once(who, "kv_indices", kv_indices, nnz, num_pages)) return s;
+  } else if (batch > 0) {
+    if (dst_indptr[0] != 0) { set_error("%s: dst_indptr[0] must be 0", who); return BSKV_ERR_INVALID_ARG; }
+    for (int32_t b = 0; b < batch; ++b)
+      if (dst_indptr[b + 1] < dst_indptr[b]) { set_error("%s: dst_indptr decreases at %d", who, b); return BSKV_ERR_INVALID_ARG; }
+    const int64_t n = dst_indptr[batch];
+    if (n > 0 && !dst_indices) { set_error("%s: dst_indices is NULL", who); return BSKV_ERR_INVALID_ARG; }
+    for (int64_t i = 0; i < n; ++i)
+      if (dst_indices[i] < 0 || dst_indices[i] >= num_pages) { set_error("%s: dst_indices[%lld] = %d outside [0, %d)", who, (long long)i, dst_indices[i], num_pages); return BSKV_ERR_INVALID_ARG; }
+    if (bskv_status s = pages_once(who, "dst_indices", dst_indices, n, num_pages)) return s;
+    std::vector<uint8_t> source(size_t(num_pages), 0);
+    for (int64_t i = 0; i < nnz; ++i) source[size_t(kv_indices[i])] = 1;
+    for (int64_t i = 0; i < n; ++i)
+      if (source[size_t(dst_indices[i])]) { set_error("%s: destination page %d is a source page too", who, dst_indices[i]); return BSKV_ERR_INVALID_ARG; }
+    dst.assign(dst_indices, dst_indices + n);
+  }
+  std::vector<Chunk> reqs;
+  int64_t total = 0, longest = 0, most = 0;
+  for (int32_t b = 0; b < batch; ++b) {
+    const int64_t L = req[size_t(b)];
+    if (keep_len[b] < 0) { set_error("%s: keep_len[%d] = %d", who, b, keep_len[b]); return BSKV_ERR_INVALID_ARG; }
+    const int64_t K = std::min<int64_t>(L, keep_len[b]);
+    if (K < L && int64_t(sink) + recent > K) {
+      set_error("%s: sink %d and recent %d exceed keep_len[%d] = %d", who, sink, recent, b, keep_len[b]);
+      return BSKV_ERR_INVALID_ARG;
+    }
+    if (!in_place && (int64_t(dst_indptr[b + 1]) - dst_indptr[b]) * page_size < K) {
+      set_error("%s: request %d keeps %lld tokens, its destination has %d pages", who, b, (long long)K, dst_indptr[b + 1] - dst_indptr[b]);
+      return BSKV_ERR_INVALID_ARG;
+    }
+    reqs.push_back(Chunk{int32_t(L), int32_t(K), int32_t(total), in_place ? kv_indptr[b] : dst_indptr[b]});
+    total += K;
+    longest = std::max(longest, L);
+    most = std::max(most, K);
+    if (total > INT32_MAX / num_kv_heads) { set_error("%s: too many tokens", who); return BSKV_ERR_UNSUPPORTED; }
+  }
+  bskv_plan* p = new bskv_plan();
+  p->kind = KIND_EVICT;
+  p->batch = batch; p->num_pages = num_pages; p->page_size = page_size;
+  p->num_qo_heads = num_kv_heads; p->num_kv_heads = num_kv_heads; p->head_dim = head_dim;
+  p->kept_total = total; p->sink = sink; p->recent = recent; p->longest = int32_t(longest);
+  p->in_place = in_place ? 1 : 0;
+  // enough CTAs per slice to fill the GPU's eight 256-thread CTAs per SM, a wave of 512 rows each
+  const int64_t slices = std::max<int64_t>(1, int64_t(batch) * num_kv_heads * (head_dim / 16));
+  p->parts = int32_t(std::max<int64_t>(1, std::min<int64_t>((most + 511) / 512, int64_t(num_sms) * 8 / slices)));
+  std::vector<int32_t> none;
+  assemble(p, KIND_EVICT, batch, dst, reqs, 0, none, 0, kv_indptr,
+           batch > 0 ? size_t(batch) + 1 : 0, kv_indices, size_t(nnz), batch, 0);
+  p->meta[H_WORKERS] = 0;  // the first section holds the destination pages
+  *out_plan = p;
+  log_plan("bskv_plan_evict", p);
   return BSKV_OK;
 }
 

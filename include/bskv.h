@@ -242,6 +242,40 @@ bskv_status bskv_plan_mla_paged(const int32_t* kv_indptr, const int32_t* kv_indi
                                 int32_t num_pages, int32_t page_size, int32_t num_heads,
                                 int32_t num_sms, bskv_plan** out_plan);
 
+/*
+ * Plan of the accumulated attention weights over a paged cache (16-bit or 4-bit).
+ *   qo_indptr[batch+1] HOST int32: request b owns query tokens [qo_indptr[b], qo_indptr[b+1]),
+ *   the last ones of its sequence; NULL: one query per request (the decode step). Page table,
+ *   head counts, head_dim and page_size as for bskv_plan_decode_fp4 (any group size), dtype
+ *   (BSKV_BF16 or BSKV_FP16) is q's and a 16-bit cache's. causal: query t of request b (0-based)
+ *   sees key j iff j <= t + L_b - qo_len_b. Pages listed twice are refused: their scores would
+ *   have two writers.
+ */
+bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const int32_t* kv_indptr,
+                                   const int32_t* kv_indices, const int32_t* kv_last_page_len,
+                                   int32_t batch, int32_t num_pages, int32_t page_size,
+                                   int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t causal, int32_t dtype, int32_t num_sms,
+                                   bskv_plan** out_plan);
+
+/*
+ * Plan of an eviction: request b keeps n_b = min(L_b, keep_len[b]) of its L_b tokens. Page table,
+ * head_dim and page_size as for bskv_plan_decode_fp4; all arrays HOST int32.
+ *   keep_len[batch] >= 0. The first `sink` and the last `recent` tokens always stay (a request
+ *   that loses tokens needs sink + recent <= keep_len[b]).
+ *   dst_indptr[batch+1], dst_indices: pages that take the kept tokens, request b's first
+ *   ceil(n_b / page_size) of dst_indices[dst_indptr[b] .. dst_indptr[b+1]); each page once, and
+ *   none of them a source page (sources may be shared between requests). Both NULL: in place,
+ *   into the first ceil(n_b / page_size) pages of the request's own list; then no page may be
+ *   listed twice.
+ */
+bskv_status bskv_plan_evict(const int32_t* kv_indptr, const int32_t* kv_indices,
+                            const int32_t* kv_last_page_len, const int32_t* keep_len, int32_t sink,
+                            int32_t recent, const int32_t* dst_indptr, const int32_t* dst_indices,
+                            int32_t batch, int32_t num_pages, int32_t page_size,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t num_sms,
+                            bskv_plan** out_plan);
+
 /* Free a plan (NULL is accepted). */
 bskv_status bskv_plan_destroy(bskv_plan* plan);
 
@@ -353,6 +387,55 @@ bskv_status bskv_run_decode_fp4(const bskv_plan* plan, const void* q, const int6
                                 const void* kv_scales, const int64_t* scales_strides, void* out,
                                 const int64_t* out_strides, float* lse, float sm_scale,
                                 void* float_ws, size_t float_ws_bytes, void* stream);
+
+/*
+ * Accumulated attention weights: how much the plan's queries attend to each cached token, added
+ * to the token's score (what bskv_run_evict chooses by). For token j of request b and kv head h
+ *   w = sum over the queries t of b that see j and the query heads r of h's group of
+ *       exp(sm_scale q[t, r] . k_j - lse[t, r]);
+ *   score = w                  for the last qo_len_b tokens (new: their history begins here), and
+ *                              for all tokens when decay is 0 (old scores are not read then);
+ *   score = decay score + w    for the others. 0 <= decay <= 1.
+ *   q [total queries, num_qo_heads, head_dim], strides {token, head} in multiples of 8 elements;
+ *   lse [total queries, num_qo_heads] float32 contiguous, the log-sum-exp that the decode or
+ *   prefill run of the same queries returned (-inf: the query adds nothing);
+ *   kv_cache and kv_strides as for bskv_run_decode (only K is read);
+ *   scores float32 (num_pages, num_kv_heads, page_size), strides {page, kv head} in multiples of
+ *   4 elements, slots contiguous, 16-byte aligned. Slots past a request's last token are left as
+ *   they were. Deterministic: the same inputs give the same bits.
+ */
+bskv_status bskv_run_attn_weights(const bskv_plan* plan, const void* q, const int64_t* q_strides,
+                                  const void* kv_cache, const int64_t* kv_strides,
+                                  const float* lse, float* scores, const int64_t* scores_strides,
+                                  float decay, float sm_scale, void* stream);
+/* The same over a 4-bit paged cache (a key with scale code 255 gets a NaN score). */
+bskv_status bskv_run_attn_weights_fp4(const bskv_plan* plan, const void* q,
+                                      const int64_t* q_strides, const void* kv_codes,
+                                      const int64_t* codes_strides, const void* kv_scales,
+                                      const int64_t* scales_strides, const float* lse,
+                                      float* scores, const int64_t* scores_strides, float decay,
+                                      float sm_scale, void* stream);
+
+/*
+ * Eviction from a paged cache by score, for a plan of bskv_plan_evict, per (request, kv head):
+ * besides the protected first and last tokens the tokens of highest score stay (NaN counts as the
+ * highest, -0 as +0, the lowest slot among equal ones first) until n_b are kept. They move to
+ * slots 0 .. n_b - 1 of the destination pages in their old order; the heads of a request may keep
+ * different tokens. Slots from n_b on are left as they were, in their bytes.
+ *   scores float32 (num_pages, num_kv_heads, page_size) as for bskv_run_attn_weights; moved with
+ *   their tokens when compact_scores is nonzero, else only read.
+ *   kv_cache, kv_strides as for bskv_run_decode, 16-bit elements.
+ *   kept [num_kv_heads, sum n_b] int32 device memory: for head h, request b's entries (from the
+ *   sum of the n of the requests before it) are the old slots of its kept tokens, ascending.
+ */
+bskv_status bskv_run_evict(const bskv_plan* plan, float* scores, const int64_t* scores_strides,
+                           int32_t compact_scores, void* kv_cache, const int64_t* kv_strides,
+                           int32_t* kept, void* stream);
+/* The same over a 4-bit paged cache. */
+bskv_status bskv_run_evict_fp4(const bskv_plan* plan, float* scores, const int64_t* scores_strides,
+                               int32_t compact_scores, void* kv_codes,
+                               const int64_t* codes_strides, void* kv_scales,
+                               const int64_t* scales_strides, int32_t* kept, void* stream);
 
 /*
  * BSR block-sparse attention ([SPARSE] run(q, k, v, out, lse)):

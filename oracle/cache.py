@@ -83,21 +83,23 @@ def attn_weights(q, keys, lse, scores, qo_indptr, kv_indptr, kv_indices, kv_last
         L = int(L)
         nq = int(qo_indptr[b + 1] - qo_indptr[b])
         k = request_rows(keys, kv_indptr, kv_indices, b, L)
-        for j in range(L):
-            page = int(kv_indices[kv_indptr[b] + j // page_size])
-            for h in range(Hkv):
-                w = 0.0
-                for t in range(nq):
-                    if causal and j > t + L - nq:
-                        continue
-                    i = int(qo_indptr[b]) + t
-                    for r in range(h * g, (h + 1) * g):
-                        if lse[i, r] == -np.inf:
-                            continue
-                        w += np.exp(sm_scale * (k[h, j] @ q[i, r]) - lse[i, r])
-                old = out[page, h, j % page_size]
-                fresh = decay == 0 or j >= L - nq
-                out[page, h, j % page_size] = w if fresh else decay * old + w
+        see = np.ones((L, nq), dtype=bool)
+        if causal:
+            see = np.arange(L)[:, None] <= np.arange(nq)[None, :] + L - nq
+        rows = slice(int(qo_indptr[b]), int(qo_indptr[b]) + nq)
+        fresh = (decay == 0) | (np.arange(L) >= L - nq)
+        pages = np.asarray(kv_indices)[kv_indptr[b] + np.arange(L) // page_size]
+        for h in range(Hkv):
+            w = np.zeros(L)
+            for r in range(h * g, (h + 1) * g):
+                z = lse[rows, r][None, :]
+                live = see & ~np.isneginf(z)
+                with np.errstate(invalid="ignore", over="ignore"):
+                    e = np.exp(sm_scale * (k[h] @ q[rows, r].T) - z)
+                w += np.where(live, e, 0.0).sum(1)
+            slots = (pages, h, np.arange(L) % page_size)
+            with np.errstate(invalid="ignore"):
+                out[slots] = np.where(fresh, w, decay * out[slots] + w)
     return out
 
 
