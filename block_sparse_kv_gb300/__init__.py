@@ -618,21 +618,36 @@ def bskv_rope_quantize_fp8_append_paged(k_rope, k_nope, pos_k, cos_sin_cache, ba
 
 def _want(fn, name, t, shape, dtypes, device):
     """One argument check: a tensor of this shape (None: any size) and type on this device."""
-    if not torch.is_tensor(t):
+    if not isinstance(t, torch.Tensor):
         raise TypeError("%s: %s must be a tensor" % (fn, name))
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    if t.shape != shape and (t.dim() != len(shape) or
+                             any(n is not None and n != m for n, m in zip(shape, t.shape))):
         raise ValueError("%s: %s has shape %s, not %s"
                          % (fn, name, tuple(t.shape), tuple("*" if n is None else n for n in shape)))
     if t.dtype not in dtypes:
         raise ValueError("%s: %s is %s, not %s" % (fn, name, t.dtype, " or ".join(map(str, dtypes))))
-    if t.device.type != "cuda" or t.device != device:
+    if t.device != device:
         raise ValueError("%s: %s is on %s; all tensors must be on one CUDA device"
                          % (fn, name, t.device))
 
 
-def _rows_last(fn, name, t):
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+def _cuda_of(fn, name, t):
+    """The CUDA device of a call's first tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: %s must be a tensor" % (fn, name))
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("%s: %s is on %s; all tensors must be on one CUDA device" % (fn, name, dev))
+    return dev
+
+
+def _rows_last(fn, name, t, written=False):
+    """The last dimension contiguous; a tensor that is written has no expanded dimension."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError("%s: the last dimension of %s must be contiguous" % (fn, name))
+    if written and 0 in st and any(s == 0 and n > 1 for s, n in zip(st, t.shape)):
+        raise ValueError("%s: %s is written and must not be an expanded view" % (fn, name))
 
 
 def _dense(fn, *named):
@@ -641,13 +656,42 @@ def _dense(fn, *named):
             raise ValueError("%s: %s must be contiguous" % (fn, name))
 
 
+_stride_arrays = {}
+
+
 def _strides_of(t, n):
-    """The first n strides; a dimension of size 1 counts as laid out densely behind it."""
-    out, dense = [], 1
-    for i in reversed(range(t.dim())):
-        out.append(dense if t.shape[i] == 1 else t.stride(i))
-        dense = max(dense, t.shape[i] * out[-1])
-    return _strides(*out[::-1][:n])
+    """The first n strides as the C entry points take them; a dimension of size 1 counts as laid
+    out densely behind the next."""
+    st = t.stride()
+    if 1 in t.shape:
+        out, dense = [], 1
+        for s, m in zip(reversed(st), reversed(t.shape)):
+            out.append(dense if m == 1 else s)
+            dense = max(dense, m * out[-1])
+        st = tuple(out[::-1])
+    st = st[:n]
+    arr = _stride_arrays.get(st)
+    if arr is None:
+        if len(_stride_arrays) > 4096:
+            _stride_arrays.clear()
+        arr = _stride_arrays[st] = _strides(*st)
+    return arr
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(fn, dev, *args):
+    """The C entry point `fn` on the current stream of the tensors' device."""
+    entry = getattr(load_library(), fn)
+    if torch.cuda.current_device() == dev.index:
+        code = entry(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            code = entry(*args, _raw_stream(dev.index))
+    if code:
+        _check(fn, code)
 
 
 def _check_plan(fn, plan, kind):
@@ -658,43 +702,49 @@ def _check_plan(fn, plan, kind):
 def _ready(fn, plan, device):
     """The plan's workspaces on this device, uploaded at the first run."""
     if plan.int_ws is None:
-        plan.upload(device)
+        with torch.cuda.device(device):
+            plan.upload(device)
     if plan.int_ws.device != device:
         raise ValueError("%s: the plan was uploaded to %s, the tensors are on %s"
                          % (fn, plan.int_ws.device, device))
 
 
-def _fp4_cache(fn, kv_codes, kv_scales, device, num_pages, page_size, num_kv_heads, head_dim):
+_U8, _I32T, _F32T = (torch.uint8,), (torch.int32,), (torch.float32,)
+_HALVES = (torch.bfloat16, torch.float16)
+
+
+def _fp4_cache(fn, kv_codes, kv_scales, device, num_pages, page_size, num_kv_heads, head_dim,
+               written=False):
     """Checks a 4-bit cache; its pointers and strides as the C entry points take them."""
-    _want(fn, "kv_codes", kv_codes, (num_pages, 2, num_kv_heads, page_size, head_dim // 2),
-          (torch.uint8,), device)
-    _want(fn, "kv_scales", kv_scales, (num_pages, 2, num_kv_heads, page_size, head_dim // 32),
-          (torch.uint8,), device)
-    _rows_last(fn, "kv_codes", kv_codes)
-    _rows_last(fn, "kv_scales", kv_scales)
-    if page_size > 1 and kv_scales.numel() and kv_scales.stride(3) != head_dim // 32:
+    _want(fn, "kv_codes", kv_codes, (num_pages, 2, num_kv_heads, page_size, head_dim // 2), _U8, device)
+    _want(fn, "kv_scales", kv_scales, (num_pages, 2, num_kv_heads, page_size, head_dim // 32), _U8,
+          device)
+    _rows_last(fn, "kv_codes", kv_codes, written)
+    _rows_last(fn, "kv_scales", kv_scales, written)
+    if page_size > 1 and kv_scales.stride(3) != head_dim // 32 and kv_scales.numel():
         raise ValueError("%s: the slots of kv_scales must be contiguous" % fn)
     return kv_codes.data_ptr(), _strides_of(kv_codes, 4), kv_scales.data_ptr(), _strides_of(kv_scales, 3)
 
 
-def _fp4_rows(fn, k, v, dtypes, batch_indices, positions, kv_indptr, kv_indices):
-    """Checks K / V rows and their device page table; (nnz, heads, head_dim, batch)."""
-    nnz, heads, dim = k.shape if torch.is_tensor(k) and k.dim() == 3 else (None, None, None)
-    dev = k.device if torch.is_tensor(k) else None
-    _want(fn, "k", k, (nnz, heads, dim), dtypes, dev)
-    _want(fn, "v", v, (nnz, heads, dim), (k.dtype,), dev)
-    _rows_last(fn, "k", k)
-    _rows_last(fn, "v", v)
-    i32 = (torch.int32,)
-    _want(fn, "batch_indices", batch_indices, (nnz,), i32, dev)
-    _want(fn, "positions", positions, (nnz,), i32, dev)
-    _want(fn, "kv_indptr", kv_indptr, (None,), i32, dev)
-    _want(fn, "kv_indices", kv_indices, (None,), i32, dev)
+def _fp4_rows(fn, k, v, dtypes, batch_indices, positions, kv_indptr, kv_indices, written=False):
+    """Checks K / V rows and their device page table; (device, nnz, heads, head_dim, batch)."""
+    dev = _cuda_of(fn, "k", k)
+    if k.dim() != 3:
+        raise ValueError("%s: k has shape %s, not (rows, heads, head_dim)" % (fn, tuple(k.shape)))
+    shape = k.shape
+    _want(fn, "k", k, shape, dtypes, dev)
+    _want(fn, "v", v, shape, (k.dtype,), dev)
+    _rows_last(fn, "k", k, written)
+    _rows_last(fn, "v", v, written)
+    for name, x in (("batch_indices", batch_indices), ("positions", positions)):
+        _want(fn, name, x, (shape[0],), _I32T, dev)
+    for name, x in (("kv_indptr", kv_indptr), ("kv_indices", kv_indices)):
+        _want(fn, name, x, (None,), _I32T, dev)
     if kv_indptr.numel() < 1:
         raise ValueError("%s: kv_indptr is empty" % fn)
     _dense(fn, ("batch_indices", batch_indices), ("positions", positions), ("kv_indptr", kv_indptr),
            ("kv_indices", kv_indices))
-    return nnz, heads, dim, kv_indptr.numel() - 1
+    return dev, shape[0], shape[1], shape[2], kv_indptr.numel() - 1
 
 
 def bskv_quantize_fp4_append_paged(k, v, batch_indices, positions, kv_indptr, kv_indices, kv_codes,
@@ -704,45 +754,38 @@ def bskv_quantize_fp4_append_paged(k, v, batch_indices, positions, kv_indptr, kv
     Hkv, page_size, D / 2], kv_scales [pages, 2, Hkv, page_size, D / 32] (uint8), through the
     device page table (all int32)."""
     fn = "bskv_quantize_fp4_append_paged"
-    lib = load_library()
-    nnz, heads, dim, batch = _fp4_rows(fn, k, v, (torch.bfloat16, torch.float16), batch_indices,
-                                       positions, kv_indptr, kv_indices)
-    _want(fn, "kv_codes", kv_codes, (None, 2, heads, None, dim // 2), (torch.uint8,), k.device)
-    cache = _fp4_cache(fn, kv_codes, kv_scales, k.device, kv_codes.shape[0], kv_codes.shape[3], heads,
-                       dim)
-    with torch.cuda.device(k.device):
-        _check(fn, lib.bskv_quantize_fp4_append_paged(
-            k.data_ptr(), _strides_of(k, 2), v.data_ptr(), _strides_of(v, 2), _DT[k.dtype], nnz,
-            heads, dim, batch_indices.data_ptr(), positions.data_ptr(), kv_indptr.data_ptr(),
-            kv_indices.data_ptr(), batch, kv_codes.shape[3], kv_codes.shape[0], *cache, _stream(k)))
+    dev, nnz, heads, dim, batch = _fp4_rows(fn, k, v, _HALVES, batch_indices, positions, kv_indptr,
+                                            kv_indices)
+    _want(fn, "kv_codes", kv_codes, (None, 2, heads, None, dim // 2), _U8, dev)
+    pages, _, _, page_size, _ = kv_codes.shape
+    cache = _fp4_cache(fn, kv_codes, kv_scales, dev, pages, page_size, heads, dim, written=True)
+    _call(fn, dev, k.data_ptr(), _strides_of(k, 2), v.data_ptr(), _strides_of(v, 2), _DT[k.dtype],
+          nnz, heads, dim, batch_indices.data_ptr(), positions.data_ptr(), kv_indptr.data_ptr(),
+          kv_indices.data_ptr(), batch, page_size, pages, *cache)
 
 
 def bskv_dequantize_fp4_paged(kv_codes, kv_scales, batch_indices, positions, kv_indptr, kv_indices,
                               dtype=torch.bfloat16, k_out=None, v_out=None):
     """Rows of a 4-bit paged cache as values: (k, v) [nnz, Hkv, D] of `dtype` (bf16, fp16 or
     fp32), row i being token positions[i] of request batch_indices[i]. Rows whose token is out of
-    range are left as they were (outputs made here start as zeros)."""
+    range are left as they were (unspecified in outputs that are made here)."""
     fn = "bskv_dequantize_fp4_paged"
-    lib = load_library()
-    if not torch.is_tensor(kv_codes) or kv_codes.dim() != 5 or not torch.is_tensor(positions):
+    dev = _cuda_of(fn, "kv_codes", kv_codes)
+    if kv_codes.dim() != 5 or not isinstance(positions, torch.Tensor):
         raise ValueError("%s: kv_codes must be [pages, 2, Hkv, page_size, D / 2]" % fn)
     pages, _, heads, page_size, half = kv_codes.shape
-    shape = (positions.numel(), heads, 2 * half)
     if (k_out is None) != (v_out is None):
         raise ValueError("%s: give both outputs or neither" % fn)
     if k_out is None:
-        k_out = torch.zeros(shape, dtype=dtype, device=kv_codes.device)
-        v_out = torch.zeros(shape, dtype=dtype, device=kv_codes.device)
-    nnz, heads, dim, batch = _fp4_rows(fn, k_out, v_out,
-                                       (torch.bfloat16, torch.float16, torch.float32),
-                                       batch_indices, positions, kv_indptr, kv_indices)
+        shape = (positions.numel(), heads, 2 * half)
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+        v_out = torch.empty(shape, dtype=dtype, device=dev)
+    _, nnz, heads, dim, batch = _fp4_rows(fn, k_out, v_out, _HALVES + _F32T, batch_indices, positions,
+                                          kv_indptr, kv_indices, written=True)
     cache = _fp4_cache(fn, kv_codes, kv_scales, k_out.device, pages, page_size, heads, dim)
-    with torch.cuda.device(k_out.device):
-        _check(fn, lib.bskv_dequantize_fp4_paged(
-            *cache, batch_indices.data_ptr(), positions.data_ptr(), kv_indptr.data_ptr(),
-            kv_indices.data_ptr(), batch, page_size, pages, k_out.data_ptr(),
-            _strides_of(k_out, 2), v_out.data_ptr(), _strides_of(v_out, 2), _DT[k_out.dtype], nnz,
-            heads, dim, _stream(k_out)))
+    _call(fn, dev, *cache, batch_indices.data_ptr(), positions.data_ptr(), kv_indptr.data_ptr(),
+          kv_indices.data_ptr(), batch, page_size, pages, k_out.data_ptr(), _strides_of(k_out, 2),
+          v_out.data_ptr(), _strides_of(v_out, 2), _DT[k_out.dtype], nnz, heads, dim)
     return k_out, v_out
 
 
@@ -761,7 +804,8 @@ def bskv_plan_decode_fp4(kv_indptr, kv_indices, kv_last_page_len, num_pages, pag
         _DT[dtype], int(ns), int(max_workers), ctypes.byref(h)))
     return Plan(h.value, "decode_fp4", batch=batch, num_pages=int(num_pages),
                 page_size=int(page_size), num_qo_heads=int(num_qo_heads),
-                num_kv_heads=int(num_kv_heads), head_dim=int(head_dim), dtype=dtype)
+                num_kv_heads=int(num_kv_heads), head_dim=int(head_dim), dtype=dtype,
+                q_shape=(batch, int(num_qo_heads), int(head_dim)))
 
 
 def _page_table(fn, kv_indptr, kv_indices, kv_last_page_len):
@@ -780,31 +824,29 @@ def bskv_run_decode_fp4(plan, q, kv_codes, kv_scales, out=None, lse=None, return
     """Decode one query token per request over a 4-bit paged cache: q [B, Hq, D]; kv_codes
     [pages, 2, Hkv, page_size, D / 2], kv_scales [pages, 2, Hkv, page_size, D / 32] uint8."""
     fn = "bskv_run_decode_fp4"
-    lib = load_library()
     _check_plan(fn, plan, "decode_fp4")
     i = plan.info
-    shape = (i["batch"], i["num_qo_heads"], i["head_dim"])
-    dev = q.device if torch.is_tensor(q) else None
-    _want(fn, "q", q, shape, (i["dtype"],), dev)
+    shape, dtypes = i["q_shape"], (i["dtype"],)
+    dev = _cuda_of(fn, "q", q)
+    _want(fn, "q", q, shape, dtypes, dev)
     _rows_last(fn, "q", q)
     cache = _fp4_cache(fn, kv_codes, kv_scales, dev, i["num_pages"], i["page_size"],
                        i["num_kv_heads"], i["head_dim"])
     if out is None:
         out = torch.empty(shape, dtype=q.dtype, device=dev)
-    _want(fn, "out", out, shape, (i["dtype"],), dev)
-    _rows_last(fn, "out", out)
-    if lse is None and return_lse:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    else:
+        _want(fn, "out", out, shape, dtypes, dev)
+        _rows_last(fn, "out", out, written=True)
     if lse is not None:
-        _want(fn, "lse", lse, shape[:2], (torch.float32,), dev)
+        _want(fn, "lse", lse, shape[:2], _F32T, dev)
         _dense(fn, ("lse", lse))
-    with torch.cuda.device(dev):
-        _ready(fn, plan, dev)
-        fw = plan.float_ws
-        _check(fn, lib.bskv_run_decode_fp4(
-            plan.handle, q.data_ptr(), _strides_of(q, 2), *cache, out.data_ptr(),
-            _strides_of(out, 2), _ptr(lse), 0.0 if sm_scale is None else float(sm_scale), _ptr(fw),
-            0 if fw is None else fw.numel(), _stream(q)))
+    elif return_lse:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    _ready(fn, plan, dev)
+    fw = plan.float_ws
+    _call(fn, dev, plan.handle, q.data_ptr(), _strides_of(q, 2), *cache, out.data_ptr(),
+          _strides_of(out, 2), _ptr(lse), 0.0 if sm_scale is None else float(sm_scale), _ptr(fw),
+          0 if fw is None else fw.numel())
     return (out, lse) if return_lse else out
 
 
@@ -826,41 +868,45 @@ def bskv_plan_attn_weights(qo_indptr, kv_indptr, kv_indices, kv_last_page_len, n
         ctypes.cast(ixp, _I32P), ctypes.cast(lpp, _I32P), batch, int(num_pages), int(page_size),
         int(num_qo_heads), int(num_kv_heads), int(head_dim), int(bool(causal)), _DT[dtype], int(ns),
         ctypes.byref(h)))
-    return Plan(h.value, "attn_weights", batch=batch, total_qo=batch if qi is None else int(qi[-1]),
-                num_pages=int(num_pages), page_size=int(page_size), num_qo_heads=int(num_qo_heads),
-                num_kv_heads=int(num_kv_heads), head_dim=int(head_dim), dtype=dtype)
+    total_qo = batch if qi is None else int(qi[-1])
+    return Plan(h.value, "attn_weights", batch=batch, num_pages=int(num_pages), page_size=int(page_size),
+                num_qo_heads=int(num_qo_heads), num_kv_heads=int(num_kv_heads),
+                head_dim=int(head_dim), dtype=dtype,
+                q_shape=(total_qo, int(num_qo_heads), int(head_dim)))
 
 
 def _scores(fn, plan, scores, device):
     i = plan.info
-    _want(fn, "scores", scores, (i["num_pages"], i["num_kv_heads"], i["page_size"]), (torch.float32,),
-          device)
-    _rows_last(fn, "scores", scores)
+    _want(fn, "scores", scores, (i["num_pages"], i["num_kv_heads"], i["page_size"]), _F32T, device)
+    _rows_last(fn, "scores", scores, written=True)
     return scores.data_ptr(), _strides_of(scores, 2)
 
 
-def _kv_pages(fn, plan, kv_cache, dtypes, device):
+def _kv_pages(fn, plan, kv_cache, dtypes, device, written=False):
     i = plan.info
     _want(fn, "kv_cache", kv_cache, (i["num_pages"], 2, i["num_kv_heads"], i["page_size"],
                                      i["head_dim"]), dtypes, device)
-    _rows_last(fn, "kv_cache", kv_cache)
+    _rows_last(fn, "kv_cache", kv_cache, written)
     return kv_cache.data_ptr(), _strides_of(kv_cache, 4)
 
 
-def _run_attn_weights(fn, plan, q, cache, lse, scores, decay, sm_scale):
+def _fp4_pages(fn, plan, kv_codes, kv_scales, device, written=False):
     i = plan.info
-    dev = q.device if torch.is_tensor(q) else None
-    _want(fn, "q", q, (i["total_qo"], i["num_qo_heads"], i["head_dim"]), (i["dtype"],), dev)
+    return _fp4_cache(fn, kv_codes, kv_scales, device, i["num_pages"], i["page_size"],
+                      i["num_kv_heads"], i["head_dim"], written)
+
+
+def _run_attn_weights(fn, plan, q, dev, cache, lse, scores, decay, sm_scale):
+    i = plan.info
+    shape = i["q_shape"]
+    _want(fn, "q", q, shape, (i["dtype"],), dev)
     _rows_last(fn, "q", q)
-    _want(fn, "lse", lse, (i["total_qo"], i["num_qo_heads"]), (torch.float32,), dev)
+    _want(fn, "lse", lse, shape[:2], _F32T, dev)
     _dense(fn, ("lse", lse))
     where = _scores(fn, plan, scores, dev)
-    cache = cache(dev)
-    with torch.cuda.device(dev):
-        _ready(fn, plan, dev)
-        _check(fn, getattr(load_library(), fn)(
-            plan.handle, q.data_ptr(), _strides_of(q, 2), *cache, lse.data_ptr(), *where,
-            float(decay), 0.0 if sm_scale is None else float(sm_scale), _stream(q)))
+    _ready(fn, plan, dev)
+    _call(fn, dev, plan.handle, q.data_ptr(), _strides_of(q, 2), *cache, lse.data_ptr(), *where,
+          float(decay), 0.0 if sm_scale is None else float(sm_scale))
     return scores
 
 
@@ -872,19 +918,18 @@ def bskv_run_attn_weights(plan, q, kv_cache, lse, scores, decay=1.0, sm_scale=No
     with decay 0, start anew."""
     fn = "bskv_run_attn_weights"
     _check_plan(fn, plan, "attn_weights")
-    return _run_attn_weights(fn, plan, q, lambda dev: _kv_pages(fn, plan, kv_cache,
-                                                                (plan.info["dtype"],), dev),
-                             lse, scores, decay, sm_scale)
+    dev = _cuda_of(fn, "q", q)
+    cache = _kv_pages(fn, plan, kv_cache, (plan.info["dtype"],), dev)
+    return _run_attn_weights(fn, plan, q, dev, cache, lse, scores, decay, sm_scale)
 
 
 def bskv_run_attn_weights_fp4(plan, q, kv_codes, kv_scales, lse, scores, decay=1.0, sm_scale=None):
     """bskv_run_attn_weights over a 4-bit paged cache."""
     fn = "bskv_run_attn_weights_fp4"
     _check_plan(fn, plan, "attn_weights")
-    i = plan.info
-    return _run_attn_weights(fn, plan, q, lambda dev: _fp4_cache(
-        fn, kv_codes, kv_scales, dev, i["num_pages"], i["page_size"], i["num_kv_heads"],
-        i["head_dim"]), lse, scores, decay, sm_scale)
+    dev = _cuda_of(fn, "q", q)
+    cache = _fp4_pages(fn, plan, kv_codes, kv_scales, dev)
+    return _run_attn_weights(fn, plan, q, dev, cache, lse, scores, decay, sm_scale)
 
 
 def bskv_plan_evict(kv_indptr, kv_indices, kv_last_page_len, keep_len, sink, recent, num_pages,
@@ -925,19 +970,16 @@ def bskv_plan_evict(kv_indptr, kv_indices, kv_last_page_len, keep_len, sink, rec
                 num_kv_heads=int(num_kv_heads), head_dim=int(head_dim), kept_indptr=kept)
 
 
-def _run_evict(fn, plan, scores, cache, kept, compact_scores):
-    dev = scores.device if torch.is_tensor(scores) else None
+def _run_evict(fn, plan, dev, scores, cache, kept, compact_scores):
     where = _scores(fn, plan, scores, dev)
-    cache = cache(dev)
     shape = (plan.info["num_kv_heads"], plan.info["kept_indptr"][-1])
     if kept is None:
         kept = torch.empty(shape, dtype=torch.int32, device=dev)
-    _want(fn, "kept", kept, shape, (torch.int32,), dev)
-    _dense(fn, ("kept", kept))
-    with torch.cuda.device(dev):
-        _ready(fn, plan, dev)
-        _check(fn, getattr(load_library(), fn)(plan.handle, *where, int(bool(compact_scores)), *cache,
-                                               kept.data_ptr(), _stream(scores)))
+    else:
+        _want(fn, "kept", kept, shape, _I32T, dev)
+        _dense(fn, ("kept", kept))
+    _ready(fn, plan, dev)
+    _call(fn, dev, plan.handle, *where, int(bool(compact_scores)), *cache, kept.data_ptr())
     return kept
 
 
@@ -948,18 +990,18 @@ def bskv_run_evict(plan, scores, kv_cache, kept=None, compact_scores=True):
     kept_indptr[-1]] int32."""
     fn = "bskv_run_evict"
     _check_plan(fn, plan, "evict")
-    return _run_evict(fn, plan, scores, lambda dev: _kv_pages(
-        fn, plan, kv_cache, (torch.bfloat16, torch.float16), dev), kept, compact_scores)
+    dev = _cuda_of(fn, "scores", scores)
+    cache = _kv_pages(fn, plan, kv_cache, _HALVES, dev, written=True)
+    return _run_evict(fn, plan, dev, scores, cache, kept, compact_scores)
 
 
 def bskv_run_evict_fp4(plan, scores, kv_codes, kv_scales, kept=None, compact_scores=True):
     """bskv_run_evict over a 4-bit paged cache."""
     fn = "bskv_run_evict_fp4"
     _check_plan(fn, plan, "evict")
-    i = plan.info
-    return _run_evict(fn, plan, scores, lambda dev: _fp4_cache(
-        fn, kv_codes, kv_scales, dev, i["num_pages"], i["page_size"], i["num_kv_heads"],
-        i["head_dim"]), kept, compact_scores)
+    dev = _cuda_of(fn, "scores", scores)
+    cache = _fp4_pages(fn, plan, kv_codes, kv_scales, dev, written=True)
+    return _run_evict(fn, plan, dev, scores, cache, kept, compact_scores)
 
 
 def bskv_merge_states(v, s, out_dtype=torch.float32, v_out=None, s_out=None):

@@ -23,6 +23,8 @@
 // query's type, relative to its largest scale, and multiplies that back after the product.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "fp4.cuh"
 #include "internal.h"
@@ -135,7 +137,7 @@ __device__ __forceinline__ void load_rows(const WeightsParams& p, const Request&
                    (int64_t(kvh) * p.group + (row - tok * p.group)) * p.q_s1;
     float back = 1.f;
     if constexpr (FP4) {
-      back = load_q_f16<T, D / 32>(src, live, lane, s.q[nt]);
+      back = load_q_f16<T, D / 32>(src, live, false, lane, s.q[nt]);
     } else {
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
@@ -163,30 +165,24 @@ __device__ __forceinline__ void dot_tile(const uint8_t* st, int h, int lane, con
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
   if constexpr (FP4) {
-    constexpr uint32_t kHigh = D == 128 ? 0x80808080u : 0x8080u;
-    const uint32_t w0 = scale_word<D>(st + Sh::kScales, r0), w1 = scale_word<D>(st + Sh::kScales, r1);
-    const float n0 = nan_bytes(w0) & kHigh ? NAN : 0.f, n1 = nan_bytes(w1) & kHigh ? NAN : 0.f;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      x[nt][0] = x[nt][1] = n0;
-      x[nt][2] = x[nt][3] = n1;
-    }
+    float s0[D / 32], s1[D / 32];
+    scales_of<D / 32>(scale_word<D>(st + Sh::kScales, r0), s0);
+    scales_of<D / 32>(scale_word<D>(st + Sh::kScales, r1), s1);
 #pragma unroll
     for (int blk = 0; blk < D / 32; ++blk) {
       uint32_t a0[4], a1[4];
       cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(st + r0 * Sh::kRow + (Sh::part(r0, blk) << 4) + 4 * t), a0);
       cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(st + r1 * Sh::kRow + (Sh::part(r1, blk) << 4) + 4 * t), a1);
       const uint32_t f0[4] = {a0[0], a1[0], a0[1], a1[1]}, f1[4] = {a0[2], a1[2], a0[3], a1[3]};
-      const float s0 = scale_of(w0, blk), s1 = scale_of(w1, blk);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
         MmaOp<__half>::run(acc, f0, s.q[nt][blk][0], s.q[nt][blk][1]);
         MmaOp<__half>::run(acc, f1, s.q[nt][blk][2], s.q[nt][blk][3]);
-        x[nt][0] = fmaf(acc[0], s0, x[nt][0]);
-        x[nt][1] = fmaf(acc[1], s0, x[nt][1]);
-        x[nt][2] = fmaf(acc[2], s1, x[nt][2]);
-        x[nt][3] = fmaf(acc[3], s1, x[nt][3]);
+        x[nt][0] = fmaf(acc[0], s0[blk], x[nt][0]);
+        x[nt][1] = fmaf(acc[1], s0[blk], x[nt][1]);
+        x[nt][2] = fmaf(acc[2], s1[blk], x[nt][2]);
+        x[nt][3] = fmaf(acc[3], s1[blk], x[nt][3]);
       }
     }
   } else {
@@ -219,30 +215,40 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm(D, FP4))
   const int nck = walk.count();
   const bool old = p.decay != 0.f;
 
+  constexpr int kStep = 32 / Sh::kParts;  // rows one copy instruction of the warp covers
+  const int row_in = lane / Sh::kParts, part = lane % Sh::kParts;
+  constexpr int kPer = FP4 ? 16 / Sh::kBlocks : 8, kCopies = kTile / kPer;  // tokens per 16 bytes of scales
+  const int s_row = lane % kCopies * kPer, w_row = (lane & 7) * 4;
+  int64_t k_off = 0, s_off = 0, w_off = 0;
   auto issue = [&](int stage) {
     if (walk.live()) {
-      walk.enter();
+      if (walk.enter()) {
+        k_off = walk.page * p.k_s0 + walk.kvh * p.k_s2 + walk.slot * p.k_s3;
+        if constexpr (FP4) s_off = walk.page * p.s_s0 + walk.kvh * p.s_s2 + walk.slot * Sh::kBlocks;
+        w_off = walk.page * p.w_s0 + walk.kvh * p.w_s1 + walk.slot;
+      }
       uint8_t* st = ring + stage * kStride;
-      int pg, sl;
+      auto copy = [&](auto whole) {
 #pragma unroll
-      for (int i = 0; i < Sh::kParts; ++i) {
-        const int c = lane + 32 * i, r = c / Sh::kParts, part = c % Sh::kParts;
-        if (walk.row(r, pg, sl))
-          cp_async_16(st + r * Sh::kRow + (Sh::part(r, part) << 4),
-                      p.keys + pg * p.k_s0 + walk.kvh * p.k_s2 + sl * p.k_s3 + part * 16);
-      }
-      if constexpr (FP4) {
-        constexpr int kPer = 16 / Sh::kBlocks, kCopies = kTile / kPer;
-        const int i = lane % kCopies;
-        if (walk.row(i * kPer, pg, sl) && lane < kCopies)
-          cp_async_16(st + Sh::kScales + 16 * i, p.scales + pg * p.s_s0 + walk.kvh * p.s_s2 + sl * Sh::kBlocks);
-      }
-      const int i = lane & 7;  // four scores
-      if (walk.row(4 * i, pg, sl) && lane < 8) {
-        const int64_t at = pg * p.w_s0 + walk.kvh * p.w_s1 + sl;
-        if (old) cp_async_16(st + Sh::kOld + 16 * i, p.scores + at);
-        if ((i & 1) == 0) *reinterpret_cast<int64_t*>(st + Sh::kPlace + 4 * i) = at;
-      }
+        for (int i = 0; i < kTile / kStep; ++i) {
+          const int r = row_in + i * kStep;
+          const int64_t off = walk.of_group(k_off, r);
+          if (whole || walk.has(r))
+            cp_async_16(st + r * Sh::kRow + (Sh::part(r, part) << 4), p.keys + off + (r & 7) * p.k_s3 + part * 16);
+        }
+        if constexpr (FP4) {
+          const int64_t off = walk.of_group(s_off, s_row);
+          if ((whole || walk.has(s_row)) && lane < kCopies)
+            cp_async_16(st + Sh::kScales + 16 * lane, p.scales + off + (s_row & 7) * Sh::kBlocks);
+        }
+        const int64_t off = walk.of_group(w_off, w_row);  // four scores
+        if ((whole || walk.has(w_row)) && lane < 8) {
+          if (old) cp_async_16(st + Sh::kOld + 16 * lane, p.scores + off + (w_row & 7));
+          if ((lane & 1) == 0) *reinterpret_cast<int64_t*>(st + Sh::kPlace + 4 * lane) = off;
+        }
+      };
+      if (walk.tok + kTile <= walk.end) copy(std::true_type{});
+      else copy(std::false_type{});
       walk.advance();
     }
     cp_async_commit();

@@ -29,6 +29,8 @@
 // workers is merged in the same launch as in the 16-bit decode, by the same code.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "fp4.cuh"
 #include "internal.h"
@@ -92,9 +94,8 @@ template <int D, int NT>
 struct State {
   uint32_t q[NT][Shape<D>::kBlocks][4];     // query fragments (B operand), f16
   float o[NT][Shape<D>::kBlocks][2][4];     // O^T accumulators, in units of 1 / rr
-  float m[2 * NT], l[2 * NT], c[2 * NT];    // running maximum and sum, logit scale (base 2)
+  float m[2 * NT], l[2 * NT], c[2 * NT];    // maximum of q.k, sum, logit scale (base 2, > 0)
   float rr[2 * NT][Shape<D>::kBlocks];      // power of two that p * scale is multiplied by
-  uint32_t k_nan, v_nan;                    // nan_bytes of every scale word seen
 };
 
 template <typename T, int D, int NT>
@@ -107,10 +108,10 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
     const int h = 8 * nt + g;
     const float back = load_q_f16<T, NB>(
         static_cast<const T*>(p.q) + b * p.q_s0 + (int64_t(kvh) * p.group + h) * p.q_s1,
-        h < p.group, lane, s.q[nt]);
+        h < p.group, p.scale_log2 < 0.f, lane, s.q[nt]);
     // columns 2t and 2t + 1 belong to the heads of lanes 8t and 8t + 4
-    s.c[2 * nt] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t);
-    s.c[2 * nt + 1] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4);
+    s.c[2 * nt] = fabsf(p.scale_log2) * __shfl_sync(0xffffffffu, back, 8 * t);
+    s.c[2 * nt + 1] = fabsf(p.scale_log2) * __shfl_sync(0xffffffffu, back, 8 * t + 4);
   }
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
@@ -125,7 +126,6 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
     for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s.o[nt][blk][i >> 2][i & 3] = 0.f;
-  s.k_nan = s.v_nan = 0;
 }
 
 // Multiply the accumulators of column j, block blk by f (column j is elements j & 1 and
@@ -139,8 +139,8 @@ __device__ __forceinline__ void scale_o(State<D, NT>& s, int j, int blk, float f
   }
 }
 
-// One 32-token tile in shared memory; tokens >= valid lie past the chunk.
-template <int D, int NT>
+// One 32-token tile in shared memory; with WHOLE false, tokens >= valid lie past the chunk.
+template <int D, int NT, bool WHOLE>
 __device__ __forceinline__ void tile(const uint8_t* st, int valid, int lane, State<D, NT>& s) {
   using Sh = Shape<D>;
   using Mma = MmaOp<__half>;
@@ -148,18 +148,13 @@ __device__ __forceinline__ void tile(const uint8_t* st, int valid, int lane, Sta
   const int g = lane >> 2, t = lane & 3;
   const int kx = (g >> Sh::kSwzShift) & (Sh::kParts - 1);
   const int vx = ((2 * t) >> Sh::kSwzShift) & (Sh::kParts - 1);
-  float x[2][NT][4];  // logits, then weights: [16-token half][column tile][fragment]
+  float x[2][NT][4];  // q.k, then weights: [16-token half][column tile][fragment]
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r0 = 16 * h + g, r1 = r0 + 8;
-    uint32_t w0 = scale_word<D>(st + Sh::kKs, r0), w1 = scale_word<D>(st + Sh::kKs, r1);
-    if (valid < kTile) {
-      w0 = r0 < valid ? w0 : 0u;
-      w1 = r1 < valid ? w1 : 0u;
-    }
-    s.k_nan |= nan_bytes(w0) | nan_bytes(w1);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) x[h][nt][0] = x[h][nt][1] = x[h][nt][2] = x[h][nt][3] = 0.f;
+    float s0[NB], s1[NB];
+    scales_of<NB>(scale_word<D>(st + Sh::kKs, r0), s0);
+    scales_of<NB>(scale_word<D>(st + Sh::kKs, r1), s1);
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) {
       const uint8_t* at = st + ((blk ^ kx) << 4) + 4 * t;
@@ -167,17 +162,23 @@ __device__ __forceinline__ void tile(const uint8_t* st, int valid, int lane, Sta
       cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(at + r0 * Sh::kRow), a0);
       cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(at + r1 * Sh::kRow), a1);
       const uint32_t f0[4] = {a0[0], a1[0], a0[1], a1[1]}, f1[4] = {a0[2], a1[2], a0[3], a1[3]};
-      const float s0 = scale_of(w0, blk), s1 = scale_of(w1, blk);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
         Mma::run(acc, f0, s.q[nt][blk][0], s.q[nt][blk][1]);
         Mma::run(acc, f1, s.q[nt][blk][2], s.q[nt][blk][3]);
-        x[h][nt][0] = fmaf(acc[0], s0, x[h][nt][0]);
-        x[h][nt][1] = fmaf(acc[1], s0, x[h][nt][1]);
-        x[h][nt][2] = fmaf(acc[2], s1, x[h][nt][2]);
-        x[h][nt][3] = fmaf(acc[3], s1, x[h][nt][3]);
+        x[h][nt][0] = blk ? fmaf(acc[0], s0[blk], x[h][nt][0]) : acc[0] * s0[blk];
+        x[h][nt][1] = blk ? fmaf(acc[1], s0[blk], x[h][nt][1]) : acc[1] * s0[blk];
+        x[h][nt][2] = blk ? fmaf(acc[2], s1[blk], x[h][nt][2]) : acc[2] * s1[blk];
+        x[h][nt][3] = blk ? fmaf(acc[3], s1[blk], x[h][nt][3]) : acc[3] * s1[blk];
       }
+    }
+    if constexpr (!WHOLE) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (16 * h + 8 * (i >> 1) + g >= valid) x[h][nt][i] = -INFINITY;
     }
   }
   // online softmax, column by column
@@ -185,14 +186,6 @@ __device__ __forceinline__ void tile(const uint8_t* st, int valid, int lane, Sta
   bool up = false;
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float& v = x[h][j >> 1][(j & 1) + 2 * i];
-        v *= s.c[j];
-        if (valid < kTile && 16 * h + 8 * i + g >= valid) v = -INFINITY;
-      }
     const int e = j & 1;
     mn[j] = fmaxf(fmaxf(x[0][j >> 1][e], x[0][j >> 1][e + 2]), fmaxf(x[1][j >> 1][e], x[1][j >> 1][e + 2]));
     mn[j] = fmaxf(s.m[j], max_over_rows(mn[j]));
@@ -203,7 +196,7 @@ __device__ __forceinline__ void tile(const uint8_t* st, int valid, int lane, Sta
     // power of two, so that p * scale * rr of a given product never becomes smaller.
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {
-      const float delta = mn[j] - s.m[j];
+      const float delta = (mn[j] - s.m[j]) * s.c[j];
       const float alpha = fast_exp2(-delta);
       s.l[j] *= alpha;
       const int grow = int(fminf(ceilf(delta), 254.f));
@@ -218,70 +211,62 @@ __device__ __forceinline__ void tile(const uint8_t* st, int valid, int lane, Sta
     }
   }
 #pragma unroll
-  for (int j = 0; j < 2 * NT; ++j)
+  for (int j = 0; j < 2 * NT; ++j) {
+    const float mc = s.m[j] * s.c[j];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float& v = x[h][j >> 1][(j & 1) + 2 * i];
-        v = fast_exp2(v - s.m[j]);
+        v = fast_exp2(fmaf(v, s.c[j], -mc));
         s.l[j] += v;
       }
-  // weights times value scales, as f16 pairs of two heads
-  uint32_t vw[2][2];
+  }
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h) {
+    // weights times value scales, as f16 pairs of two heads
+    float f[2][NB];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = 16 * h + 8 * i + g;
       uint32_t w = scale_word<D>(st + Sh::kVs, r);
-      if (valid < kTile && r >= valid) w = 0u;
-      s.v_nan |= nan_bytes(w);
-      vw[h][i] = w;
+      if constexpr (!WHOLE) w = r < valid ? w : 0u;
+      scales_of<NB>(w, f[i]);
     }
-  uint32_t pp[2][NT][NB][2];
-  for (int round = 0; round < 2; ++round) {
-    __half2 top = __float2half2_rn(0.f);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
+    uint32_t pp[NT][NB][2];
+    for (int round = 0; round < 2; ++round) {
+      __half2 top = __float2half2_rn(0.f);
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float f = scale_of(vw[h][i], blk);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t w = pack_half2(x[h][nt][2 * i] * s.rr[2 * nt][blk] * f,
-                                          x[h][nt][2 * i + 1] * s.rr[2 * nt + 1][blk] * f);
-            pp[h][nt][blk][i] = w;
+            const uint32_t w = pack_half2(x[h][nt][2 * i] * s.rr[2 * nt][blk] * f[i][blk],
+                                          x[h][nt][2 * i + 1] * s.rr[2 * nt + 1][blk] * f[i][blk]);
+            pp[nt][blk][i] = w;
             top = __hmax2(top, *reinterpret_cast<const __half2*>(&w));
           }
         }
-    // up to 2^15 the products are safe in f16; above, lower rr so that the largest becomes
-    // [2^10, 2^11): products 2^-24 of it still keep 11 bits, and smaller ones are off by at
-    // most 2^-35 of it
-    const bool over = __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f));
-    if (round == 1 || !__any_sync(0xffffffffu, over)) break;
+      // up to 2^15 the products are safe in f16; above, lower rr so that the largest becomes
+      // [2^10, 2^11): products 2^-24 of it still keep 11 bits, and smaller ones are off by at
+      // most 2^-35 of it
+      const bool over = __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f));
+      if (round == 1 || !__any_sync(0xffffffffu, over)) break;
 #pragma unroll
-    for (int j = 0; j < 2 * NT; ++j)
+      for (int j = 0; j < 2 * NT; ++j)
 #pragma unroll
-      for (int blk = 0; blk < NB; ++blk) {
-        float big = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            big = fmaxf(big, x[h][j >> 1][(j & 1) + 2 * i] * scale_of(vw[h][i], blk));
-        big = max_over_rows(big);
-        const int k = exponent_of(s.rr[j][blk]);
-        const int kn = min(k, max(-126, 10 - exponent_of(big)));
-        scale_o(s, j, blk, fast_exp2(float(kn - k)));
-        s.rr[j][blk] = pow2(kn);
-      }
-  }
-  // O^T += V^T P^T
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
+        for (int blk = 0; blk < NB; ++blk) {
+          float big = fmaxf(x[h][j >> 1][j & 1] * f[0][blk],
+                            x[h][j >> 1][(j & 1) + 2] * f[1][blk]);
+          big = max_over_rows(big);
+          const int k = exponent_of(s.rr[j][blk]);
+          const int kn = min(k, max(-126, 10 - exponent_of(big)));
+          scale_o(s, j, blk, fast_exp2(float(kn - k)));
+          s.rr[j][blk] = pow2(kn);
+        }
+    }
+    // O^T += V^T P^T
     const uint8_t* row = st + Sh::kV + (16 * h + 2 * t) * Sh::kRow + 2 * g;
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) {
@@ -297,7 +282,7 @@ __device__ __forceinline__ void tile(const uint8_t* st, int valid, int lane, Sta
       cvt_e2m1x4(((h2 >> 4) & 0x0f0fu) | (h3 & 0xf0f0u), a[0][3], a[1][3]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const uint32_t b0 = movmatrix(pp[h][nt][blk][0]), b1 = movmatrix(pp[h][nt][blk][1]);
+        const uint32_t b0 = movmatrix(pp[nt][blk][0]), b1 = movmatrix(pp[nt][blk][1]);
         Mma::run(s.o[nt][blk][0], a[0], b0, b1);
         Mma::run(s.o[nt][blk][1], a[1], b0, b1);
       }
@@ -312,15 +297,11 @@ __device__ __forceinline__ void finish(const Fp4DecodeParams& p, int b, int kvh,
   using Mma = MmaOp<T>;
   constexpr int NB = Shape<D>::kBlocks;
   const int g = lane >> 2, t = lane & 3;
-  constexpr uint32_t kHigh = D == 128 ? 0x80808080u : 0x8080u;
-  const bool k_bad = __any_sync(0xffffffffu, (s.k_nan & kHigh) != 0u);
-  const uint32_t v_bad = __reduce_or_sync(0xffffffffu, s.v_nan & kHigh);
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
     const int h = 8 * (j >> 1) + 2 * t + (j & 1);
     const float l = sum_over_rows(s.l[j]);
-    float inv = 1.f / l, lse = (s.m[j] + __log2f(l)) * kLn2;
-    if (k_bad) inv = lse = NAN;
+    const float inv = 1.f / l, lse = fmaf(s.m[j], s.c[j], __log2f(l)) * kLn2;
     if (h >= p.group) continue;
     if (g == 0) {
       if (slot >= 0) p.ws_lse[int64_t(slot) * p.group + h] = lse;
@@ -328,8 +309,7 @@ __device__ __forceinline__ void finish(const Fp4DecodeParams& p, int b, int kvh,
     }
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) {
-      float f = pow2_inverse(s.rr[j][blk]) * inv;
-      if (v_bad >> (8 * blk + 7) & 1u) f = NAN;
+      const float f = pow2_inverse(s.rr[j][blk]) * inv;
       const auto& o = s.o[j >> 1][blk];
       const int e = j & 1;
       const float4 v = make_float4(o[0][e] * f, o[0][e + 2] * f, o[1][e] * f, o[1][e + 2] * f);
@@ -368,27 +348,41 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
   PageWalk walk(p.meta, p.off_workers, p.off_chunks, p.off_aux0, p.off_aux1, w, Hkv, p.page_size, lane);
   const int nck = walk.count();
 
+  // Part of a row that this lane copies, and the 16 bytes of scales: their place relative to the
+  // row's group of 8 tokens, whose own offsets the group's lane keeps.
+  const int row_in = lane / Sh::kParts, part = lane % Sh::kParts;
+  const uint8_t* k_lane = p.codes + (row_in & 7) * p.c_s3 + part * 16;
+  const uint8_t* v_lane = k_lane + p.c_s1;
+  constexpr int kPer = 16 / Sh::kBlocks;  // tokens per 16 bytes of scales
+  constexpr int kCopies = kTile / kPer;
+  const int s_row = lane % kCopies * kPer, which = (lane / kCopies) & 1;
+  const uint8_t* s_lane = p.scales + which * p.s_s1 + (s_row & 7) * Sh::kBlocks;
+  uint8_t* to_lane = ring + row_in * Sh::kRow + ((part ^ ((row_in >> Sh::kSwzShift) & (Sh::kParts - 1))) << 4);
+  uint8_t* s_to_lane = ring + Sh::kKs + which * kTile * Sh::kBlocks + lane % kCopies * 16;
+  int64_t c_off = 0, s_off = 0;
   auto issue = [&](int stage) {
     if (walk.live()) {
-      walk.enter();
-      uint8_t* st = ring + stage * Sh::kStage;
-      int pg, sl;
-#pragma unroll
-      for (int i = 0; i < Sh::kParts; ++i) {
-        const int r = lane / Sh::kParts + i * (32 / Sh::kParts), part = lane % Sh::kParts;
-        if (walk.row(r, pg, sl)) {
-          const uint8_t* from = p.codes + pg * p.c_s0 + walk.kvh * p.c_s2 + sl * p.c_s3 + part * 16;
-          const int to = r * Sh::kRow + ((part ^ ((r >> Sh::kSwzShift) & (Sh::kParts - 1))) << 4);
-          cp_async_16(st + to, from);
-          cp_async_16(st + Sh::kV + to, from + p.c_s1);
-        }
+      if (walk.enter()) {
+        c_off = walk.page * p.c_s0 + walk.kvh * p.c_s2 + walk.slot * p.c_s3;
+        s_off = walk.page * p.s_s0 + walk.kvh * p.s_s2 + walk.slot * Sh::kBlocks;
       }
-      constexpr int kPer = 16 / Sh::kBlocks;   // tokens per 16 bytes of scales
-      constexpr int kCopies = kTile / kPer;
-      const int i = lane % kCopies, which = (lane / kCopies) & 1;
-      if (walk.row(i * kPer, pg, sl) && lane < 2 * kCopies)
-        cp_async_16(st + Sh::kKs + which * kTile * Sh::kBlocks + 16 * i,
-                    p.scales + pg * p.s_s0 + which * p.s_s1 + walk.kvh * p.s_s2 + sl * Sh::kBlocks);
+      auto copy = [&](auto whole) {
+        uint8_t* to = to_lane + stage * Sh::kStage;
+#pragma unroll
+        for (int i = 0; i < Sh::kParts; ++i) {
+          const int r = row_in + i * (32 / Sh::kParts);
+          const int64_t off = walk.of_group(c_off, r);
+          if (whole || walk.has(r)) {
+            cp_async_16(to + i * (32 / Sh::kParts) * Sh::kRow, k_lane + off);
+            cp_async_16(to + i * (32 / Sh::kParts) * Sh::kRow + Sh::kV, v_lane + off);
+          }
+        }
+        const int64_t off = walk.of_group(s_off, s_row);
+        if ((whole || walk.has(s_row)) && lane < 2 * kCopies)
+          cp_async_16(s_to_lane + stage * Sh::kStage, s_lane + off);
+      };
+      if (walk.tok + kTile <= walk.end) copy(std::true_type{});
+      else copy(std::false_type{});
       walk.advance();
     }
     cp_async_commit();
@@ -411,7 +405,9 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
       cp_async_wait<kStages - 2>();
       __syncwarp();  // the tile is there for every lane, and the stage refilled next is free
       issue((done + kStages - 1) % kStages);
-      tile<D, NT>(ring + (done % kStages) * Sh::kStage, min(kTile, ch.z - at), lane, s);
+      const uint8_t* st = ring + (done % kStages) * Sh::kStage;
+      if (ch.z - at >= kTile) tile<D, NT, true>(st, kTile, lane, s);
+      else tile<D, NT, false>(st, ch.z - at, lane, s);
     }
     finish<T, D, NT>(p, b, kvh, ch.w, lane, s);
     if (ch.w >= 0 && p.counters) {

@@ -77,15 +77,17 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// fp32 2^(code - 127) of byte b of a word of scale codes; code 0 reads as 0 (its values lie
-// below 2^-124) and code 255 is handled apart (nan_bytes).
-__device__ __forceinline__ float scale_of(uint32_t w, int b) {
-  const uint32_t s = b == 0 ? w << 23 : b == 1 ? w << 15 : b == 2 ? w << 7 : w >> 1;
-  return __uint_as_float(s & 0x7f800000u);
-}
-// Bit 7 of each byte that is 255 (other bits are noise).
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  return ((w & 0x7f7f7f7fu) + 0x01010101u) & w;
+// The scales 2^(code - 127) of the codes in a word's bytes as fp32, exactly; NaN for 255.
+template <int NB>
+__device__ __forceinline__ void scales_of(uint32_t w, float (&f)[NB]) {
+#pragma unroll
+  for (int i = 0; i < NB; i += 2) {
+    uint32_t pair;  // bf16 has fp32's exponents
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %0, lo;\n\t}" : "=r"(pair) : "r"(i ? w >> 16 : w));
+    f[i] = __uint_as_float(pair << 16);
+    f[i + 1] = __uint_as_float(pair & 0xffff0000u);
+  }
 }
 
 // Scale codes of row `row` of a shared-memory tile (2 bytes for D = 64).
@@ -118,9 +120,11 @@ __device__ __forceinline__ float sum_over_rows(float x) {
 // The B fragments of a query row of D = 32 NB values for products over NB 32-value blocks: lane
 // (g, t) holds values 32 b + 8 t .. + 7 of row g as four f16 pairs per block b. bf16 rows are
 // multiplied by the power of two that puts their largest magnitude into [2^14, 2^15) (exact:
-// values below 2^-29 of it may lose low bits to f16's subnormals); returns its inverse.
+// values below 2^-29 of it may lose low bits to f16's subnormals); returns its inverse. `negate`
+// flips the row's signs.
 template <typename T, int NB>
-__device__ __forceinline__ float load_q_f16(const T* row, bool live, int lane, uint32_t (&q)[NB][4]) {
+__device__ __forceinline__ float load_q_f16(const T* row, bool live, bool negate, int lane,
+                                            uint32_t (&q)[NB][4]) {
   const int t = lane & 3;
   uint4 x[NB];
 #pragma unroll
@@ -129,10 +133,11 @@ __device__ __forceinline__ float load_q_f16(const T* row, bool live, int lane, u
   if constexpr (__is_same(T, __half)) {
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) {
-      q[blk][0] = x[blk].x;
-      q[blk][1] = x[blk].y;
-      q[blk][2] = x[blk].z;
-      q[blk][3] = x[blk].w;
+      const uint32_t sign = negate ? 0x80008000u : 0u;
+      q[blk][0] = x[blk].x ^ sign;
+      q[blk][1] = x[blk].y ^ sign;
+      q[blk][2] = x[blk].z ^ sign;
+      q[blk][3] = x[blk].w ^ sign;
     }
     return 1.f;
   } else {
@@ -147,7 +152,7 @@ __device__ __forceinline__ float load_q_f16(const T* row, bool live, int lane, u
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int e = int(top >> 7);
     const int k = e == 255 ? 0 : min(141 - e, 126);
-    const float f = pow2(k);
+    const float f = negate ? -pow2(k) : pow2(k);
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) {
       const uint32_t w[4] = {x[blk].x, x[blk].y, x[blk].z, x[blk].w};

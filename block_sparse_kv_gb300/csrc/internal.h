@@ -119,7 +119,7 @@ inline int32_t decode_group_heads(int32_t num_kv_heads, int32_t page_size) {
 // kv head decide how many CTAs an SM holds (registers: 128 a thread with one tile).
 constexpr int kFp4Tile = 32;   // tokens per pipeline stage
 constexpr int kFp4Warps = 4;
-constexpr int fp4_ctas_per_sm(int column_tiles) { return column_tiles > 1 ? 2 : 4; }
+constexpr int fp4_ctas_per_sm(int column_tiles) { return column_tiles > 1 ? 2 : 3; }
 
 // Attention-weight plans. Stream variants (at most 8 or 16 query rows, queries times heads of a
 // group, in every request): one worker per warp over ranges of tokens of (request, kv head)

@@ -22,6 +22,7 @@ struct PageWalk {
   // Lane i holds the page and slot of the 8 tokens at win + 8 i, and of those 256 tokens later,
   // read a window ahead so that no copy waits for a page id.
   int page = 0, slot = 0, page2 = 0, slot2 = 0;
+  bool fresh = false;
 
   __device__ __forceinline__ PageWalk(const int32_t* meta, int off_workers, int off_chunks,
                                       int off_aux0, int off_aux1, int worker, int heads, int ps,
@@ -51,26 +52,29 @@ struct PageWalk {
     tok = win = ch.y;
     end = ch.z;
     pbase = __ldg(kv_indptr + b);
+    fresh = true;
     lookup(win, page, slot);
     lookup(win + 256, page2, slot2);
   }
-  // Before the tile at `tok` is copied: move on to the next window where it begins one.
-  __device__ __forceinline__ void enter() {
-    if (tok - win == 256) {
-      win = tok;
-      page = page2;
-      slot = slot2;
-      lookup(win + 256, page2, slot2);
-    }
+  // Before the tile at `tok` is copied: move on to the next window where it begins one. True when
+  // this lane's group is another one than at the last tile.
+  __device__ __forceinline__ bool enter() {
+    const bool was = fresh;
+    fresh = false;
+    if (tok - win != 256) return was;
+    win = tok;
+    page = page2;
+    slot = slot2;
+    lookup(win + 256, page2, slot2);
+    return true;
   }
-  // Page and slot of row r (0..31) of the tile, the whole warp calling; false past the chunk's
-  // last group of 8 tokens (rows of the last group past `end` lie in its page).
-  __device__ __forceinline__ bool row(int r, int& pg, int& sl) const {
-    const int src = ((tok - win) >> 3) + (r >> 3);
-    pg = __shfl_sync(0xffffffffu, page, src);
-    sl = __shfl_sync(0xffffffffu, slot, src) + (r & 7);
-    return tok + (r & ~7) < end;
+  // The offset that the lane of row r's group (r in 0..31 of the tile) computed for its group.
+  __device__ __forceinline__ int64_t of_group(int64_t offset, int r) const {
+    return __shfl_sync(0xffffffffu, static_cast<long long>(offset), ((tok - win) >> 3) + (r >> 3));
   }
+  // Whether row r's group of 8 tokens begins before the chunk's end (its last group's rows past
+  // `end` lie in the same page).
+  __device__ __forceinline__ bool has(int r) const { return tok + (r & ~7) < end; }
   __device__ __forceinline__ void advance() {
     tok += kWalkTile;
     if (tok >= end) {
