@@ -7,9 +7,11 @@
 // The codes are exact in f16, so both inner sums are f16 tensor-core products of the codes
 // themselves: a key's scale multiplies the fp32 partial sum of its block, a value's scale is
 // folded into the softmax weight. Queries in bf16 are made f16 by an exact power of two per
-// head. The weight times scale is rounded to f16 (half a step, 2^-11 relative) relative to a
-// power of two per (head, block) that follows the largest product so far, so the scales may
-// have any magnitude: rr below.
+// head. Weight times scale, p_j X_V[j, b], is rounded to f16. The reference that weights are
+// taken relative to (any reference gives the same softmax) is therefore not the largest logit but
+// 2^10 below the largest product so far of the head, up to a factor 2^5: products down to 2^-24 of
+// it keep f16's 11 bits, smaller ones are off by at most 2^-35 of it. It changes on the first tile
+// and rarely after, so a tile has no reduction over its tokens, only a vote.
 //
 // Tokens are the M = 16 rows of mma.sync m16n8k16 and the query heads of a kv head its N = 8
 // columns (two column tiles above 8 heads): with heads as rows a group of 4 would leave three
@@ -28,8 +30,6 @@
 // (any page size and stride, no swizzle constraint on the page layout). A unit cut between
 // workers is merged in the same launch as in the 16-bit decode, by the same code.
 #include <math.h>
-
-#include <type_traits>
 
 #include "common.cuh"
 #include "fp4.cuh"
@@ -93,9 +93,20 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
 template <int D, int NT>
 struct State {
   uint32_t q[NT][Shape<D>::kBlocks][4];     // query fragments (B operand), f16
-  float o[NT][Shape<D>::kBlocks][2][4];     // O^T accumulators, in units of 1 / rr
-  float m[2 * NT], l[2 * NT], c[2 * NT];    // maximum of q.k, sum, logit scale (base 2, > 0)
-  float rr[2 * NT][Shape<D>::kBlocks];      // power of two that p * scale is multiplied by
+  float o[NT][Shape<D>::kBlocks][2][4];     // O^T accumulators
+  float ref[2 * NT], l[2 * NT], c[2 * NT];  // exponent reference, sum, logit scale (base 2, > 0)
+};
+
+// Up to 4 query heads per kv head (NT = 0): column n of the products is head n / 2, so that a lane
+// has one head, t. In O^T = V^T P^T the two columns of a head take the even and the odd values: the
+// k-pair of the A operand is (value 2i, value 2i + 1) of one token, as the codes lie in a byte, and
+// the B operand holds the weight in the half of its column's parity and zero in the other. That
+// needs no pairing of two tokens' nibbles and wastes no column.
+template <int D>
+struct State<D, 0> {
+  uint32_t q[Shape<D>::kBlocks][4];
+  float o[Shape<D>::kBlocks][4];  // values 32 b + 4 g .. + 3 of head t
+  float ref, l, c;
 };
 
 template <typename T, int D, int NT>
@@ -103,6 +114,17 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
                                        State<D, NT>& s) {
   constexpr int NB = Shape<D>::kBlocks;
   const int g = lane >> 2, t = lane & 3;
+  if constexpr (NT == 0) {
+    const float back = load_q_f16<T, NB>(
+        static_cast<const T*>(p.q) + b * p.q_s0 + (int64_t(kvh) * p.group + (g >> 1)) * p.q_s1,
+        (g >> 1) < p.group, p.scale_log2 < 0.f, lane, s.q);
+    s.c = fabsf(p.scale_log2) * __shfl_sync(0xffffffffu, back, 8 * t);
+    s.ref = -INFINITY;
+    s.l = 0.f;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) s.o[blk][0] = s.o[blk][1] = s.o[blk][2] = s.o[blk][3] = 0.f;
+    return;
+  } else {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int h = 8 * nt + g;
@@ -115,10 +137,8 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
   }
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
-    s.m[j] = -INFINITY;
+    s.ref[j] = -INFINITY;
     s.l[j] = 0.f;
-#pragma unroll
-    for (int blk = 0; blk < NB; ++blk) s.rr[j][blk] = pow2(127);
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -126,32 +146,49 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
     for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s.o[nt][blk][i >> 2][i & 3] = 0.f;
-}
-
-// Multiply the accumulators of column j, block blk by f (column j is elements j & 1 and
-// (j & 1) + 2 of its tile's fragments).
-template <int D, int NT>
-__device__ __forceinline__ void scale_o(State<D, NT>& s, int j, int blk, float f) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    s.o[j >> 1][blk][i][j & 1] *= f;
-    s.o[j >> 1][blk][i][(j & 1) + 2] *= f;
   }
 }
 
-// One 32-token tile in shared memory; with WHOLE false, tokens >= valid lie past the chunk.
+// Raise a head's reference to 2^10 below the largest product of weight and scale among 16 tokens:
+// a lane's two logits (base 2) plus the exponents f of the tokens' largest scales. The weights
+// themselves stay within [2^-80, 2^100], whatever the scales. Returns what sums so far shrink by.
+__device__ __forceinline__ float raise_ref(float& ref, float v0, float v1, const float (&f)[2]) {
+  const float top = max_over_rows(fmaxf(v0, v1));
+  float need = max_over_rows(fmaxf(v0 + f[0], v1 + f[1]));
+  need = fmaxf(ref, fminf(fmaxf(need - 10.f, top - 100.f), top + 80.f));
+  const float shrink = fast_exp2(ref - need);
+  ref = need;
+  return shrink;
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void raise_refs(State<D, NT>& s, const float (&x)[NT][4], const float (&f)[2]) {
+#pragma unroll
+  for (int j = 0; j < 2 * NT; ++j) {
+    const float shrink = raise_ref(s.ref[j], x[j >> 1][j & 1] * s.c[j], x[j >> 1][(j & 1) + 2] * s.c[j], f);
+    s.l[j] *= shrink;
+#pragma unroll
+    for (int blk = 0; blk < Shape<D>::kBlocks; ++blk)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        s.o[j >> 1][blk][i][j & 1] *= shrink;
+        s.o[j >> 1][blk][i][(j & 1) + 2] *= shrink;
+      }
+  }
+}
+
+// Tokens 16 h .. 16 h + 15 of a tile in shared memory; with WHOLE false, tokens >= valid lie past
+// the chunk (valid > 16 h).
 template <int D, int NT, bool WHOLE>
-__device__ __forceinline__ void tile(const uint8_t* st, int valid, int lane, State<D, NT>& s) {
+__device__ __forceinline__ void half_tile(const uint8_t* st, int h, int valid, int lane, State<D, NT>& s) {
   using Sh = Shape<D>;
   using Mma = MmaOp<__half>;
   constexpr int NB = Sh::kBlocks;
-  const int g = lane >> 2, t = lane & 3;
+  const int g = lane >> 2, t = lane & 3, r0 = 16 * h + g, r1 = r0 + 8;
   const int kx = (g >> Sh::kSwzShift) & (Sh::kParts - 1);
   const int vx = ((2 * t) >> Sh::kSwzShift) & (Sh::kParts - 1);
-  float x[2][NT][4];  // q.k, then weights: [16-token half][column tile][fragment]
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r0 = 16 * h + g, r1 = r0 + 8;
+  float x[NT][4];  // q.k: rows r0 (first two) and r1, columns 2t and 2t + 1
+  {
     float s0[NB], s1[NB];
     scales_of<NB>(scale_word<D>(st + Sh::kKs, r0), s0);
     scales_of<NB>(scale_word<D>(st + Sh::kKs, r1), s1);
@@ -167,10 +204,10 @@ __device__ __forceinline__ void tile(const uint8_t* st, int valid, int lane, Sta
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
         Mma::run(acc, f0, s.q[nt][blk][0], s.q[nt][blk][1]);
         Mma::run(acc, f1, s.q[nt][blk][2], s.q[nt][blk][3]);
-        x[h][nt][0] = blk ? fmaf(acc[0], s0[blk], x[h][nt][0]) : acc[0] * s0[blk];
-        x[h][nt][1] = blk ? fmaf(acc[1], s0[blk], x[h][nt][1]) : acc[1] * s0[blk];
-        x[h][nt][2] = blk ? fmaf(acc[2], s1[blk], x[h][nt][2]) : acc[2] * s1[blk];
-        x[h][nt][3] = blk ? fmaf(acc[3], s1[blk], x[h][nt][3]) : acc[3] * s1[blk];
+        x[nt][0] = blk ? fmaf(acc[0], s0[blk], x[nt][0]) : acc[0] * s0[blk];
+        x[nt][1] = blk ? fmaf(acc[1], s0[blk], x[nt][1]) : acc[1] * s0[blk];
+        x[nt][2] = blk ? fmaf(acc[2], s1[blk], x[nt][2]) : acc[2] * s1[blk];
+        x[nt][3] = blk ? fmaf(acc[3], s1[blk], x[nt][3]) : acc[3] * s1[blk];
       }
     }
     if constexpr (!WHOLE) {
@@ -178,147 +215,223 @@ __device__ __forceinline__ void tile(const uint8_t* st, int valid, int lane, Sta
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (16 * h + 8 * (i >> 1) + g >= valid) x[h][nt][i] = -INFINITY;
+          if ((i < 2 ? r0 : r1) >= valid) x[nt][i] = -INFINITY;
     }
   }
-  // online softmax, column by column
-  float mn[2 * NT];
-  bool up = false;
+  // Weights relative to the reference, times the value scales, as f16 pairs of two heads. Products
+  // up to 2^15 are safe in f16; the first tokens, and later ones with a larger product, set it.
+  float sv[2][NB];
 #pragma unroll
-  for (int j = 0; j < 2 * NT; ++j) {
-    const int e = j & 1;
-    mn[j] = fmaxf(fmaxf(x[0][j >> 1][e], x[0][j >> 1][e + 2]), fmaxf(x[1][j >> 1][e], x[1][j >> 1][e + 2]));
-    mn[j] = fmaxf(s.m[j], max_over_rows(mn[j]));
-    up = up || mn[j] > s.m[j];
+  for (int i = 0; i < 2; ++i) {
+    const int r = i ? r1 : r0;
+    uint32_t w = scale_word<D>(st + Sh::kVs, r);
+    if constexpr (!WHOLE) w = r < valid ? w : 0u;
+    scales_of<NB>(w, sv[i]);
   }
-  if (__any_sync(0xffffffffu, up)) {
-    // A higher maximum: weights so far shrink by 2^-(mn - m). rr grows by the next whole
-    // power of two, so that p * scale * rr of a given product never becomes smaller.
+  uint32_t pp[NT][NB][2];
+  auto weigh = [&](float (&add)[2 * NT]) {
+    __half2 top = __float2half2_rn(0.f);
 #pragma unroll
-    for (int j = 0; j < 2 * NT; ++j) {
-      const float delta = (mn[j] - s.m[j]) * s.c[j];
-      const float alpha = fast_exp2(-delta);
-      s.l[j] *= alpha;
-      const int grow = int(fminf(ceilf(delta), 254.f));
+    for (int nt = 0; nt < NT; ++nt) {
+      float e[4];
 #pragma unroll
-      for (int blk = 0; blk < NB; ++blk) {
-        const int k = exponent_of(s.rr[j][blk]);
-        const int kn = min(k + grow, 127);
-        scale_o(s, j, blk, fast_exp2(float(kn - k) - delta));
-        s.rr[j][blk] = pow2(kn);
-      }
-      s.m[j] = mn[j];
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 2 * NT; ++j) {
-    const float mc = s.m[j] * s.c[j];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float& v = x[h][j >> 1][(j & 1) + 2 * i];
-        v = fast_exp2(fmaf(v, s.c[j], -mc));
-        s.l[j] += v;
-      }
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    // weights times value scales, as f16 pairs of two heads
-    float f[2][NB];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 16 * h + 8 * i + g;
-      uint32_t w = scale_word<D>(st + Sh::kVs, r);
-      if constexpr (!WHOLE) w = r < valid ? w : 0u;
-      scales_of<NB>(w, f[i]);
-    }
-    uint32_t pp[NT][NB][2];
-    for (int round = 0; round < 2; ++round) {
-      __half2 top = __float2half2_rn(0.f);
+      for (int i = 0; i < 4; ++i) e[i] = fast_exp2(fmaf(x[nt][i], s.c[2 * nt + (i & 1)], -s.ref[2 * nt + (i & 1)]));
+      add[2 * nt] = e[0] + e[2];
+      add[2 * nt + 1] = e[1] + e[3];
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t w = pack_half2(x[h][nt][2 * i] * s.rr[2 * nt][blk] * f[i][blk],
-                                          x[h][nt][2 * i + 1] * s.rr[2 * nt + 1][blk] * f[i][blk]);
-            pp[nt][blk][i] = w;
-            top = __hmax2(top, *reinterpret_cast<const __half2*>(&w));
-          }
-        }
-      // up to 2^15 the products are safe in f16; above, lower rr so that the largest becomes
-      // [2^10, 2^11): products 2^-24 of it still keep 11 bits, and smaller ones are off by at
-      // most 2^-35 of it
-      const bool over = __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f));
-      if (round == 1 || !__any_sync(0xffffffffu, over)) break;
-#pragma unroll
-      for (int j = 0; j < 2 * NT; ++j)
-#pragma unroll
-        for (int blk = 0; blk < NB; ++blk) {
-          float big = fmaxf(x[h][j >> 1][j & 1] * f[0][blk],
-                            x[h][j >> 1][(j & 1) + 2] * f[1][blk]);
-          big = max_over_rows(big);
-          const int k = exponent_of(s.rr[j][blk]);
-          const int kn = min(k, max(-126, 10 - exponent_of(big)));
-          scale_o(s, j, blk, fast_exp2(float(kn - k)));
-          s.rr[j][blk] = pow2(kn);
+          const uint32_t w = pack_half2(e[2 * i] * sv[i][blk], e[2 * i + 1] * sv[i][blk]);
+          pp[nt][blk][i] = w;
+          top = __hmax2(top, *reinterpret_cast<const __half2*>(&w));
         }
     }
-    // O^T += V^T P^T
-    const uint8_t* row = st + Sh::kV + (16 * h + 2 * t) * Sh::kRow + 2 * g;
+    return __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f));
+  };
+  float add[2 * NT];
+  const bool over = weigh(add);
+  if (__any_sync(0xffffffffu, over || s.ref[0] == -INFINITY)) {
+    float f[2];  // exponent of each token's largest scale
 #pragma unroll
-    for (int blk = 0; blk < NB; ++blk) {
-      const uint8_t* at = row + ((blk ^ vx) << 4);
-      const uint32_t h0 = *reinterpret_cast<const uint16_t*>(at);
-      const uint32_t h1 = *reinterpret_cast<const uint16_t*>(at + Sh::kRow);
-      const uint32_t h2 = *reinterpret_cast<const uint16_t*>(at + 8 * Sh::kRow);
-      const uint32_t h3 = *reinterpret_cast<const uint16_t*>(at + 9 * Sh::kRow);
-      uint32_t a[2][4];  // rows g / g + 8 of the two products: values 4g + {0, 1} and {2, 3}
-      cvt_e2m1x4((h0 & 0x0f0fu) | ((h1 << 4) & 0xf0f0u), a[0][0], a[1][0]);
-      cvt_e2m1x4(((h0 >> 4) & 0x0f0fu) | (h1 & 0xf0f0u), a[0][1], a[1][1]);
-      cvt_e2m1x4((h2 & 0x0f0fu) | ((h3 << 4) & 0xf0f0u), a[0][2], a[1][2]);
-      cvt_e2m1x4(((h2 >> 4) & 0x0f0fu) | (h3 & 0xf0f0u), a[0][3], a[1][3]);
+    for (int i = 0; i < 2; ++i) {
+      float big = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint32_t b0 = movmatrix(pp[nt][blk][0]), b1 = movmatrix(pp[nt][blk][1]);
-        Mma::run(s.o[nt][blk][0], a[0], b0, b1);
-        Mma::run(s.o[nt][blk][1], a[1], b0, b1);
-      }
+      for (int blk = 0; blk < NB; ++blk) big = fmaxf(big, sv[i][blk]);
+      f[i] = float(exponent_of(big));
+    }
+    raise_refs<D, NT>(s, x, f);
+    weigh(add);
+  }
+#pragma unroll
+  for (int j = 0; j < 2 * NT; ++j) s.l[j] += add[j];
+  // O^T += V^T P^T
+  const uint8_t* row = st + Sh::kV + (16 * h + 2 * t) * Sh::kRow + 2 * g;
+#pragma unroll
+  for (int blk = 0; blk < NB; ++blk) {
+    const uint8_t* at = row + ((blk ^ vx) << 4);
+    const uint32_t h0 = *reinterpret_cast<const uint16_t*>(at);
+    const uint32_t h1 = *reinterpret_cast<const uint16_t*>(at + Sh::kRow);
+    const uint32_t h2 = *reinterpret_cast<const uint16_t*>(at + 8 * Sh::kRow);
+    const uint32_t h3 = *reinterpret_cast<const uint16_t*>(at + 9 * Sh::kRow);
+    uint32_t a[2][4];  // rows g / g + 8 of the two products: values 4g + {0, 1} and {2, 3}
+    cvt_e2m1x4((h0 & 0x0f0f0f0fu) | ((h1 << 4) & 0xf0f0f0f0u), a[0][0], a[1][0]);
+    cvt_e2m1x4(((h0 >> 4) & 0x0f0f0f0fu) | (h1 & 0xf0f0f0f0u), a[0][1], a[1][1]);
+    cvt_e2m1x4((h2 & 0x0f0f0f0fu) | ((h3 << 4) & 0xf0f0f0f0u), a[0][2], a[1][2]);
+    cvt_e2m1x4(((h2 >> 4) & 0x0f0f0f0fu) | (h3 & 0xf0f0f0f0u), a[0][3], a[1][3]);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint32_t b0 = movmatrix(pp[nt][blk][0]), b1 = movmatrix(pp[nt][blk][1]);
+      Mma::run(s.o[nt][blk][0], a[0], b0, b1);
+      Mma::run(s.o[nt][blk][1], a[1], b0, b1);
     }
   }
 }
 
+// A pair of weights' halves into the half of the lane's column parity, zero elsewhere: byte
+// selectors for the low (e = 0) and the high weight.
+__device__ __forceinline__ uint32_t half_select(int e, int parity) {
+  return parity ? (e ? 0x3244u : 0x1044u) : (e ? 0x4432u : 0x4410u);
+}
+
+// half_tile for up to 4 query heads per kv head.
+template <int D, bool WHOLE>
+__device__ __forceinline__ void half_tile4(const uint8_t* st, int h, int valid, int lane, State<D, 0>& s) {
+  using Sh = Shape<D>;
+  using Mma = MmaOp<__half>;
+  constexpr int NB = Sh::kBlocks;
+  const int g = lane >> 2, t = lane & 3, r0 = 16 * h + g, r1 = r0 + 8;
+  const int kx = (g >> Sh::kSwzShift) & (Sh::kParts - 1);
+  float x[2];  // q.k of tokens r0 and r1 with head t
+  {
+    float s0[NB], s1[NB];
+    scales_of<NB>(scale_word<D>(st + Sh::kKs, r0), s0);
+    scales_of<NB>(scale_word<D>(st + Sh::kKs, r1), s1);
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      const uint8_t* at = st + ((blk ^ kx) << 4) + 4 * t;
+      uint32_t a0[4], a1[4];
+      cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(at + r0 * Sh::kRow), a0);
+      cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(at + r1 * Sh::kRow), a1);
+      const uint32_t f0[4] = {a0[0], a1[0], a0[1], a1[1]}, f1[4] = {a0[2], a1[2], a0[3], a1[3]};
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      Mma::run(acc, f0, s.q[blk][0], s.q[blk][1]);
+      Mma::run(acc, f1, s.q[blk][2], s.q[blk][3]);
+      x[0] = blk ? fmaf(acc[0], s0[blk], x[0]) : acc[0] * s0[blk];
+      x[1] = blk ? fmaf(acc[2], s1[blk], x[1]) : acc[2] * s1[blk];
+    }
+    if constexpr (!WHOLE) {
+      if (r0 >= valid) x[0] = -INFINITY;
+      if (r1 >= valid) x[1] = -INFINITY;
+    }
+  }
+  float sv[2][NB];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = i ? r1 : r0;
+    uint32_t w = scale_word<D>(st + Sh::kVs, r);
+    if constexpr (!WHOLE) w = r < valid ? w : 0u;
+    scales_of<NB>(w, sv[i]);
+  }
+  uint32_t pw[2][NB / 2];  // weight times scale of blocks 2 n and 2 n + 1
+  float add;
+  auto weigh = [&]() {
+    __half2 top = __float2half2_rn(0.f);
+    add = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float e = fast_exp2(fmaf(x[i], s.c, -s.ref));
+      add += e;
+#pragma unroll
+      for (int n = 0; n < NB / 2; ++n) {
+        pw[i][n] = pack_half2(e * sv[i][2 * n], e * sv[i][2 * n + 1]);
+        top = __hmax2(top, *reinterpret_cast<const __half2*>(&pw[i][n]));
+      }
+    }
+    return __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f));
+  };
+  const bool over = weigh();
+  if (__any_sync(0xffffffffu, over || s.ref == -INFINITY)) {
+    float f[2];  // exponent of each token's largest scale
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float big = 0.f;
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) big = fmaxf(big, sv[i][blk]);
+      f[i] = float(exponent_of(big));
+    }
+    const float shrink = raise_ref(s.ref, x[0] * s.c, x[1] * s.c, f);
+    s.l *= shrink;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s.o[blk][i] *= shrink;
+    weigh();
+  }
+  s.l += add;
+  // O^T += V^T P^T, 8 tokens a product: lane (g, t) gives tokens t and t + 4 of head g / 2
+  const uint32_t sel0 = half_select(0, g & 1), sel1 = half_select(1, g & 1);
+  const int vx = (t >> Sh::kSwzShift) & (Sh::kParts - 1), vx4 = ((t + 4) >> Sh::kSwzShift) & (Sh::kParts - 1);
+  const uint8_t* row = st + Sh::kV + (16 * h + t) * Sh::kRow + 2 * g;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int n = 0; n < NB / 2; ++n) {
+      const uint32_t p0 = __shfl_sync(0xffffffffu, pw[i][n], 4 * t + (g >> 1));
+      const uint32_t p4 = __shfl_sync(0xffffffffu, pw[i][n], 4 * (t + 4) + (g >> 1));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int blk = 2 * n + e;
+        const uint8_t* at = row + 8 * i * Sh::kRow;
+        uint32_t a[4];
+        cvt_e2m1x4(*reinterpret_cast<const uint16_t*>(at + ((blk ^ vx) << 4)), a[0], a[1]);
+        cvt_e2m1x4(*reinterpret_cast<const uint16_t*>(at + 4 * Sh::kRow + ((blk ^ vx4) << 4)), a[2], a[3]);
+        Mma::run(s.o[blk], a, __byte_perm(p0, 0u, e ? sel1 : sel0), __byte_perm(p4, 0u, e ? sel1 : sel0));
+      }
+    }
+}
+
 // Normalise a finished chunk and write it to out / lse (slot < 0) or as a partial state.
+template <typename T, int D>
+__device__ __forceinline__ void put_head(const Fp4DecodeParams& p, int b, int kvh, int slot, int h, int d, float4 v) {
+  using Mma = MmaOp<T>;
+  if (slot >= 0) {
+    *reinterpret_cast<float4*>(p.ws_o + (int64_t(slot) * p.group + h) * D + d) = v;
+  } else {
+    T* dst = static_cast<T*>(p.out) + b * p.o_s0 + (int64_t(kvh) * p.group + h) * p.o_s1 + d;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(Mma::pack(v.x, v.y), Mma::pack(v.z, v.w));
+  }
+}
+__device__ __forceinline__ void put_lse(const Fp4DecodeParams& p, int b, int kvh, int slot, int h, float lse) {
+  if (slot >= 0) p.ws_lse[int64_t(slot) * p.group + h] = lse;
+  else if (p.lse) p.lse[int64_t(b) * p.num_qo_heads + kvh * p.group + h] = lse;
+}
+
 template <typename T, int D, int NT>
 __device__ __forceinline__ void finish(const Fp4DecodeParams& p, int b, int kvh, int slot, int lane,
                                        State<D, NT>& s) {
-  using Mma = MmaOp<T>;
   constexpr int NB = Shape<D>::kBlocks;
   const int g = lane >> 2, t = lane & 3;
+  if constexpr (NT == 0) {
+    const float l = sum_over_rows(s.l), inv = 1.f / l;
+    if (t >= p.group) return;
+    if (g == 0) put_lse(p, b, kvh, slot, t, (s.ref + __log2f(l)) * kLn2);
 #pragma unroll
-  for (int j = 0; j < 2 * NT; ++j) {
-    const int h = 8 * (j >> 1) + 2 * t + (j & 1);
-    const float l = sum_over_rows(s.l[j]);
-    const float inv = 1.f / l, lse = fmaf(s.m[j], s.c[j], __log2f(l)) * kLn2;
-    if (h >= p.group) continue;
-    if (g == 0) {
-      if (slot >= 0) p.ws_lse[int64_t(slot) * p.group + h] = lse;
-      else if (p.lse) p.lse[int64_t(b) * p.num_qo_heads + kvh * p.group + h] = lse;
-    }
+    for (int blk = 0; blk < NB; ++blk)
+      put_head<T, D>(p, b, kvh, slot, t, 32 * blk + 4 * g,
+                     make_float4(s.o[blk][0] * inv, s.o[blk][1] * inv, s.o[blk][2] * inv, s.o[blk][3] * inv));
+  } else {
 #pragma unroll
-    for (int blk = 0; blk < NB; ++blk) {
-      const float f = pow2_inverse(s.rr[j][blk]) * inv;
-      const auto& o = s.o[j >> 1][blk];
-      const int e = j & 1;
-      const float4 v = make_float4(o[0][e] * f, o[0][e + 2] * f, o[1][e] * f, o[1][e + 2] * f);
-      const int d = 32 * blk + 4 * g;
-      if (slot >= 0) {
-        *reinterpret_cast<float4*>(p.ws_o + (int64_t(slot) * p.group + h) * D + d) = v;
-      } else {
-        T* dst = static_cast<T*>(p.out) + b * p.o_s0 + (int64_t(kvh) * p.group + h) * p.o_s1 + d;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(Mma::pack(v.x, v.y), Mma::pack(v.z, v.w));
+    for (int j = 0; j < 2 * NT; ++j) {
+      const int h = 8 * (j >> 1) + 2 * t + (j & 1), e = j & 1;
+      const float l = sum_over_rows(s.l[j]), inv = 1.f / l;
+      if (h >= p.group) continue;
+      if (g == 0) put_lse(p, b, kvh, slot, h, (s.ref[j] + __log2f(l)) * kLn2);
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) {
+        const auto& o = s.o[j >> 1][blk];
+        put_head<T, D>(p, b, kvh, slot, h, 32 * blk + 4 * g,
+                       make_float4(o[0][e] * inv, o[0][e + 2] * inv, o[1][e] * inv, o[1][e + 2] * inv));
       }
     }
   }
@@ -348,17 +461,18 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
   PageWalk walk(p.meta, p.off_workers, p.off_chunks, p.off_aux0, p.off_aux1, w, Hkv, p.page_size, lane);
   const int nck = walk.count();
 
-  // Part of a row that this lane copies, and the 16 bytes of scales: their place relative to the
-  // row's group of 8 tokens, whose own offsets the group's lane keeps.
-  const int row_in = lane / Sh::kParts, part = lane % Sh::kParts;
-  const uint8_t* k_lane = p.codes + (row_in & 7) * p.c_s3 + part * 16;
-  const uint8_t* v_lane = k_lane + p.c_s1;
-  constexpr int kPer = 16 / Sh::kBlocks;  // tokens per 16 bytes of scales
-  constexpr int kCopies = kTile / kPer;
-  const int s_row = lane % kCopies * kPer, which = (lane / kCopies) & 1;
-  const uint8_t* s_lane = p.scales + which * p.s_s1 + (s_row & 7) * Sh::kBlocks;
-  uint8_t* to_lane = ring + row_in * Sh::kRow + ((part ^ ((row_in >> Sh::kSwzShift) & (Sh::kParts - 1))) << 4);
-  uint8_t* s_to_lane = ring + Sh::kKs + which * kTile * Sh::kBlocks + lane % kCopies * 16;
+  // Eight lanes copy a group of 8 tokens: row `sub / kParts` and every kRows-th after it, part
+  // `sub % kParts` of each (XORed as swizzled), and the first of them its 16-byte pieces of scales.
+  // What the addresses add to the group's own offset, kept by lane (tok - win) / 8 + j, is fixed.
+  constexpr int kRows = 8 / Sh::kParts;
+  constexpr int kPieces = 8 * Sh::kBlocks / 16;  // of a group's K scales
+  const int j = lane >> 3, sub = lane & 7, which = (sub / kPieces) & 1, chunk = sub % kPieces;
+  const uint8_t* k_lane = p.codes + sub / Sh::kParts * p.c_s3 + sub % Sh::kParts * 16;
+  const uint8_t* s_lane = p.scales + which * p.s_s1 + chunk * 16;
+  const int64_t step = kRows * p.c_s3;
+  const uint32_t to_lane = smem_u32(ring + (8 * j + sub / Sh::kParts) * Sh::kRow + sub % Sh::kParts * 16);
+  const uint32_t s_to_lane =
+      smem_u32(ring + Sh::kKs + which * kTile * Sh::kBlocks + 8 * j * Sh::kBlocks + chunk * 16);
   int64_t c_off = 0, s_off = 0;
   auto issue = [&](int stage) {
     if (walk.live()) {
@@ -366,23 +480,18 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
         c_off = walk.page * p.c_s0 + walk.kvh * p.c_s2 + walk.slot * p.c_s3;
         s_off = walk.page * p.s_s0 + walk.kvh * p.s_s2 + walk.slot * Sh::kBlocks;
       }
-      auto copy = [&](auto whole) {
-        uint8_t* to = to_lane + stage * Sh::kStage;
+      const uint8_t* from = k_lane + walk.of_group(c_off, 8 * j);
+      const uint8_t* s_from = s_lane + walk.of_group(s_off, 8 * j);
+      if (walk.has(8 * j)) {
+        const uint32_t to = to_lane + stage * Sh::kStage;
 #pragma unroll
         for (int i = 0; i < Sh::kParts; ++i) {
-          const int r = row_in + i * (32 / Sh::kParts);
-          const int64_t off = walk.of_group(c_off, r);
-          if (whole || walk.has(r)) {
-            cp_async_16(to + i * (32 / Sh::kParts) * Sh::kRow, k_lane + off);
-            cp_async_16(to + i * (32 / Sh::kParts) * Sh::kRow + Sh::kV, v_lane + off);
-          }
+          cp_async_16_at((to ^ (i << 4)) + i * kRows * Sh::kRow, from);
+          cp_async_16_at((to ^ (i << 4)) + i * kRows * Sh::kRow + Sh::kV, from + p.c_s1);
+          from += step;
         }
-        const int64_t off = walk.of_group(s_off, s_row);
-        if ((whole || walk.has(s_row)) && lane < 2 * kCopies)
-          cp_async_16(s_to_lane + stage * Sh::kStage, s_lane + off);
-      };
-      if (walk.tok + kTile <= walk.end) copy(std::true_type{});
-      else copy(std::false_type{});
+        if (sub < 2 * kPieces) cp_async_16_at(s_to_lane + stage * Sh::kStage, s_from);
+      }
       walk.advance();
     }
     cp_async_commit();
@@ -406,8 +515,19 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
       __syncwarp();  // the tile is there for every lane, and the stage refilled next is free
       issue((done + kStages - 1) % kStages);
       const uint8_t* st = ring + (done % kStages) * Sh::kStage;
-      if (ch.z - at >= kTile) tile<D, NT, true>(st, kTile, lane, s);
-      else tile<D, NT, false>(st, ch.z - at, lane, s);
+      if (ch.z - at >= kTile) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (NT == 0) half_tile4<D, true>(st, h, kTile, lane, s);
+          else half_tile<D, NT, true>(st, h, kTile, lane, s);
+        }
+      } else {
+#pragma unroll 1
+        for (int h = 0; 16 * h < ch.z - at; ++h) {
+          if constexpr (NT == 0) half_tile4<D, false>(st, h, ch.z - at, lane, s);
+          else half_tile<D, NT, false>(st, h, ch.z - at, lane, s);
+        }
+      }
     }
     finish<T, D, NT>(p, b, kvh, ch.w, lane, s);
     if (ch.w >= 0 && p.counters) {
@@ -443,9 +563,10 @@ bskv_status launch(const bskv_plan* plan, const Fp4DecodeParams& dp, cudaStream_
 
 template <typename T>
 bskv_status launch_t(const bskv_plan* plan, const Fp4DecodeParams& dp, cudaStream_t st) {
-  const bool wide = dp.group > 8;
-  if (plan->head_dim == 128) return wide ? launch<T, 128, 2>(plan, dp, st) : launch<T, 128, 1>(plan, dp, st);
-  return wide ? launch<T, 64, 2>(plan, dp, st) : launch<T, 64, 1>(plan, dp, st);
+  const int tiles = fp4_column_tiles(dp.group);
+  if (plan->head_dim == 128)
+    return tiles == 0 ? launch<T, 128, 0>(plan, dp, st) : tiles == 1 ? launch<T, 128, 1>(plan, dp, st) : launch<T, 128, 2>(plan, dp, st);
+  return tiles == 0 ? launch<T, 64, 0>(plan, dp, st) : tiles == 1 ? launch<T, 64, 1>(plan, dp, st) : launch<T, 64, 2>(plan, dp, st);
 }
 
 }  // namespace

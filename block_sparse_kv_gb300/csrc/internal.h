@@ -115,11 +115,13 @@ inline int32_t decode_group_heads(int32_t num_kv_heads, int32_t page_size) {
   return num_kv_heads % kDecodeGroupMax == 0 ? kDecodeGroupMax : 0;
 }
 
-// 4-bit decode: one worker per warp, kFp4Warps to a CTA; the column tiles of 8 query heads per
-// kv head decide how many CTAs an SM holds (registers: 128 a thread with one tile).
+// 4-bit decode: one worker per warp, kFp4Warps to a CTA. The variant by query heads per kv head (0:
+// up to 4, 1: up to 8, 2: up to 16) decides how many CTAs an SM holds (registers: 128, 168 and 255 a
+// thread).
 constexpr int kFp4Tile = 32;   // tokens per pipeline stage
 constexpr int kFp4Warps = 4;
-constexpr int fp4_ctas_per_sm(int column_tiles) { return column_tiles > 1 ? 2 : 3; }
+constexpr int fp4_column_tiles(int group) { return group <= 4 ? 0 : group <= 8 ? 1 : 2; }
+constexpr int fp4_ctas_per_sm(int column_tiles) { return column_tiles == 0 ? 3 : column_tiles == 1 ? 3 : 2; }
 
 // Attention-weight plans. Stream variants (at most 8 or 16 query rows, queries times heads of a
 // group, in every request): one worker per warp over ranges of tokens of (request, kv head)

@@ -646,7 +646,7 @@ extern "C" bskv_status bskv_plan_decode_fp4(const int32_t* kv_indptr, const int3
     for (int32_t h = 0; h < num_kv_heads; ++h) len[size_t(b) * num_kv_heads + h] = req[size_t(b)];
   }
   if (total > INT32_MAX / num_kv_heads || len.size() > size_t(INT32_MAX / 4)) { set_error("%s: too many tokens", who); return BSKV_ERR_UNSUPPORTED; }
-  const int64_t slots_per_sm = kFp4Warps * fp4_ctas_per_sm(group > 8 ? 2 : 1);
+  const int64_t slots_per_sm = kFp4Warps * fp4_ctas_per_sm(fp4_column_tiles(group));
   std::vector<int32_t> worker_ptr, merges;
   std::vector<Chunk> chunks;
   int32_t slots = 0;

@@ -6,7 +6,7 @@ fp32; each softmax weight times scale is rounded once to f16 (half a step, 2^-11
 output once to its type (half a step: 2^-8 of the value in bf16, 2^-11 in fp16). With
 A = sum_j w_j |v_j| that is |error| <= 2^-11 A + half |o|, plus fp32 sums and ex2 of a few 2^-22
 (covered by 2^-12 A). A product of weight and scale below 2^-14 is an f16 subnormal, off by up to
-2^-25; the kernel keeps the largest one M of a (head, block) at 2^10 or more, so each of the L
+2^-25; the kernel keeps the largest one M of a head at 2^10 or more, so each of the L
 products is off by 2^-35 M at most and its value's code is at most 6: + 6 L 2^-35 M (it matters
 where the tokens of large weight hold the code 0). The lse carries the fp32 rounding of logits of its size: 2^-18 (1 + |lse|).
 """
@@ -53,11 +53,11 @@ def _reference(d, codes, scales):
          d["sm_scale"])
     ref, ref_lse = oc.paged_decode(q, cache, *a)
     size, _ = oc.paged_decode(q, np.concatenate([cache[:, :1], np.abs(cache[:, 1:])], 1), *a)
-    # values of code 6 everywhere: their weighted sum is at least 6 M
+    # values of code 6 everywhere: the largest weighted sum of a head is at least 6 M
     six, _ = oc.paged_decode(q, np.concatenate(
         [cache[:, :1], oc.fp4_decode(np.full_like(codes[:, 1:], 0x77), scales[:, 1:])], 1), *a)
     n = d["kv_lens"].numpy()[:, None, None].astype(np.float64)
-    return ref, ref_lse, (2.0 ** -11 + 2.0 ** -12) * size + n * 2.0 ** -35 * six
+    return ref, ref_lse, (2.0 ** -11 + 2.0 ** -12) * size + n * 2.0 ** -35 * six.max(-1, keepdims=True)
 
 
 def _check_decode(d, dtype, codes, scales, out, lse):
@@ -197,7 +197,11 @@ CASES = [
     (6, 4, 4, 128, 8, 1, 90, torch.bfloat16, 4),       # 1
     (2, 12, 4, 64, 32, 33, 97, torch.float16, 3),      # 3
     (3, 36, 4, 128, 48, 20, 300, torch.float16, 6),    # 9, pages of 48
-    (2, 16, 2, 128, 16, 900, 1000, torch.bfloat16, 20),  # more than 8 pieces: the merge kernel
+    (2, 16, 2, 128, 16, 900, 1000, torch.bfloat16, 20),  # many pieces
+    (1, 8, 2, 128, 64, 5000, 5000, torch.bfloat16, 150),  # more than 64: merged by a kernel of their own
+    (3, 10, 5, 128, 8, 1, 300, torch.float16, 0),      # 5 kv heads: 15 of 16 warps
+    (2, 24, 12, 64, 32, 40, 200, torch.bfloat16, 5),   # 12 kv heads: two groups of 6
+    (2, 22, 2, 128, 8, 30, 700, torch.bfloat16, 9),    # 11 query heads per kv head, pages of 8
     (1, 8, 8, 64, 8, 1, 1, torch.bfloat16, 0),         # one token
     (2, 13, 1, 64, 8, 600, 900, torch.bfloat16, 2),    # windows of 256 tokens turn over
 ]
@@ -234,8 +238,8 @@ def test_decode_empty_requests(cuda):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_decode_scales_of_any_magnitude(cuda, dtype):
     """Blocks of very different scale, growing and shrinking along the sequence and between the
-    blocks of a row: every output value keeps the precision of its own block. The few tokens whose
-    keys align with a query make the largest products of weight and scale small ones of the scales."""
+    blocks of a row. The few tokens whose keys align with a query make the largest products of
+    weight and scale small ones of the scales."""
     D, L = 128, 500
     d = synth.paged_decode_inputs(721, 2, 16, 2, D, 16, 0, 0, lengths=[L, 77], dtype=dtype)
     codes, scales = _cache(722, d, cuda, 121, 123)
