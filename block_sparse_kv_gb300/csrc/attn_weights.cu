@@ -54,7 +54,7 @@ struct WeightsParams {
   float* scores;
   int64_t w_s0, w_s1;               // floats: page, kv head
   int num_kv_heads, group, page_size, num_qo_heads, causal;
-  int off_workers, off_chunks, off_aux0, off_aux1, off_req, num_workers, num_chunks;
+  int off_workers, off_chunks, off_records, off_aux0, off_aux1, off_req, num_workers;
   float decay, scale_log2;
 };
 
@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm(D, FP4))
   uint8_t* ring = smem + warp * Sh::kRing;
   const int w = blockIdx.x * kWarps + warp;
   if (w >= p.num_workers) return;
-  PageWalk walk(p.meta, p.off_workers, p.off_chunks, p.off_aux0, p.off_aux1, w, p.num_kv_heads,
-                p.page_size, lane);
-  const int nck = walk.count();
+  const int c0 = __ldg(p.meta + p.off_workers + w), nck = __ldg(p.meta + p.off_workers + w + 1) - c0;
+  const int32_t* records = p.meta + p.off_records + c0 * kWalkWords;
+  PageWalk walk(records, nck, p.meta + p.off_aux1, p.num_kv_heads, p.page_size, lane);
   const bool old = p.decay != 0.f;
 
   constexpr int kStep = 32 / Sh::kParts;  // rows one copy instruction of the warp covers
@@ -259,11 +259,11 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm(D, FP4))
   Rows<D, NT> s;
   int done = 0;
   for (int k = 0; k < nck; ++k) {
-    const int4 ch = walk.chunk(k);
-    const int b = ch.x / p.num_kv_heads, kvh = ch.x - b * p.num_kv_heads;
+    const WalkChunk ch = walk_chunk(records, k);
+    const int b = ch.unit / p.num_kv_heads, kvh = ch.unit - b * p.num_kv_heads;
     const Request rq = request_of(p, b);
     load_rows<T, D, NT, FP4>(p, rq, kvh, lane, s);
-    for (int at = ch.y; at < ch.z; at += kTile, ++done) {
+    for (int at = ch.begin; at < ch.end; at += kTile, ++done) {
       cp_async_wait<kStages - 2>();
       __syncwarp();  // the tile is there for every lane, and the stage refilled next is free
       issue((done + kStages - 1) % kStages);
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm(D, FP4))
       // lane (g, t) writes key at + 8 t + g
       const float mine = t == 0 ? sum[0] : t == 1 ? sum[1] : t == 2 ? sum[2] : sum[3];
       const int r = 8 * t + g;
-      if (at + r < ch.z) {
+      if (at + r < ch.end) {
         float* dst = p.scores + *reinterpret_cast<const int64_t*>(st + Sh::kPlace + 8 * t) + g;
         const bool fresh = !old || at + r >= rq.len - rq.nq;
         *dst = fresh ? mine : fmaf(p.decay, *reinterpret_cast<const float*>(st + Sh::kOld + 4 * r), mine);
@@ -440,10 +440,8 @@ template <typename T, int D, int NT, bool FP4>
 bskv_status launch_stream(const bskv_plan* plan, const WeightsParams& wp, cudaStream_t st) {
   const size_t smem = size_t(kWarps) * Shape<D, FP4>::kRing;
   auto kern = weights_stream_kernel<T, D, NT, FP4>;
-  if (bskv_status s = cuda_check(
-          cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)),
-          "attn_weights: cudaFuncSetAttribute"))
-    return s;
+  static std::atomic<int> allowed[64];
+  if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "attn_weights: cudaFuncSetAttribute")) return s;
   kern<<<meta_word(plan, H_GRID), kWarps * 32, smem, st>>>(wp);
   return cuda_check(cudaGetLastError(), "attn_weights launch");
 }
@@ -486,7 +484,7 @@ bskv_status run(const char* who, const bskv_plan* plan, const void* q, const int
   wp.off_aux1 = meta_word(plan, H_OFF_AUX1);
   wp.off_req = meta_word(plan, H_OFF_MERGES);
   wp.num_workers = meta_word(plan, H_WORKERS);
-  wp.num_chunks = meta_word(plan, H_CHUNKS);
+  wp.off_records = plan->walk_records;
   wp.decay = decay;
   wp.scale_log2 = sm_scale_log2(sm_scale, plan->head_dim);
   const bool bf = plan->dtype == BSKV_BF16;

@@ -63,7 +63,7 @@ struct Fp4DecodeParams {
   float* ws_lse;
   int* counters;  // non-null: the last worker to finish a split unit merges it
   int num_kv_heads, group, page_size, num_qo_heads;
-  int off_workers, off_chunks, off_merges, off_aux0, off_aux1, num_merges, num_workers;
+  int off_workers, off_records, off_merges, off_aux1, num_merges, num_workers;
   float scale_log2;
 };
 
@@ -275,10 +275,10 @@ __device__ __forceinline__ void half_tile(const uint8_t* st, int h, int valid, i
     const uint32_t h2 = *reinterpret_cast<const uint16_t*>(at + 8 * Sh::kRow);
     const uint32_t h3 = *reinterpret_cast<const uint16_t*>(at + 9 * Sh::kRow);
     uint32_t a[2][4];  // rows g / g + 8 of the two products: values 4g + {0, 1} and {2, 3}
-    cvt_e2m1x4((h0 & 0x0f0f0f0fu) | ((h1 << 4) & 0xf0f0f0f0u), a[0][0], a[1][0]);
-    cvt_e2m1x4(((h0 >> 4) & 0x0f0f0f0fu) | (h1 & 0xf0f0f0f0u), a[0][1], a[1][1]);
-    cvt_e2m1x4((h2 & 0x0f0f0f0fu) | ((h3 << 4) & 0xf0f0f0f0u), a[0][2], a[1][2]);
-    cvt_e2m1x4(((h2 >> 4) & 0x0f0f0f0fu) | (h3 & 0xf0f0f0f0u), a[0][3], a[1][3]);
+    cvt_e2m1x4(nibbles(h0, h1 << 4), a[0][0], a[1][0]);
+    cvt_e2m1x4(nibbles(h0 >> 4, h1), a[0][1], a[1][1]);
+    cvt_e2m1x4(nibbles(h2, h3 << 4), a[0][2], a[1][2]);
+    cvt_e2m1x4(nibbles(h2 >> 4, h3), a[0][3], a[1][3]);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const uint32_t b0 = movmatrix(pp[nt][blk][0]), b1 = movmatrix(pp[nt][blk][1]);
@@ -458,8 +458,9 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
   if (w >= P) return;
   const int32_t* merges = p.meta + p.off_merges;
   const int Hkv = p.num_kv_heads;
-  PageWalk walk(p.meta, p.off_workers, p.off_chunks, p.off_aux0, p.off_aux1, w, Hkv, p.page_size, lane);
-  const int nck = walk.count();
+  const int c0 = __ldg(p.meta + p.off_workers + w), nck = __ldg(p.meta + p.off_workers + w + 1) - c0;
+  const int32_t* records = p.meta + p.off_records + c0 * kWalkWords;
+  PageWalk walk(records, nck, p.meta + p.off_aux1, Hkv, p.page_size, lane);
 
   // Eight lanes copy a group of 8 tokens: row `sub / kParts` and every kRows-th after it, part
   // `sub % kParts` of each (XORed as swizzled), and the first of them its 16-byte pieces of scales.
@@ -507,15 +508,15 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
   State<D, NT> s;
   int done = 0;
   for (int k = 0; k < nck; ++k) {
-    const int4 ch = walk.chunk(k);
-    const int b = ch.x / Hkv, kvh = ch.x - b * Hkv;
+    const WalkChunk ch = walk_chunk(records, k);
+    const int b = ch.unit / Hkv, kvh = ch.unit - b * Hkv;
     load_q<T, D, NT>(p, b, kvh, lane, s);
-    for (int at = ch.y; at < ch.z; at += kTile, ++done) {
+    for (int at = ch.begin; at < ch.end; at += kTile, ++done) {
       cp_async_wait<kStages - 2>();
       __syncwarp();  // the tile is there for every lane, and the stage refilled next is free
       issue((done + kStages - 1) % kStages);
       const uint8_t* st = ring + (done % kStages) * Sh::kStage;
-      if (ch.z - at >= kTile) {
+      if (ch.end - at >= kTile) {
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           if constexpr (NT == 0) half_tile4<D, true>(st, h, kTile, lane, s);
@@ -523,26 +524,22 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
         }
       } else {
 #pragma unroll 1
-        for (int h = 0; 16 * h < ch.z - at; ++h) {
-          if constexpr (NT == 0) half_tile4<D, false>(st, h, ch.z - at, lane, s);
-          else half_tile<D, NT, false>(st, h, ch.z - at, lane, s);
+        for (int h = 0; 16 * h < ch.end - at; ++h) {
+          if constexpr (NT == 0) half_tile4<D, false>(st, h, ch.end - at, lane, s);
+          else half_tile<D, NT, false>(st, h, ch.end - at, lane, s);
         }
       }
     }
-    finish<T, D, NT>(p, b, kvh, ch.w, lane, s);
-    if (ch.w >= 0 && p.counters) {
+    finish<T, D, NT>(p, b, kvh, ch.slot, lane, s);
+    if (ch.slot >= 0 && p.counters) {
       // The last of the unit's chunks to finish merges all of them (release / acquire through
       // lane 0's atomic, the other lanes' writes ordered before it by the __syncwarp).
       __syncwarp();
       int last = 0;
-      if (lane == 0) {
-        const int item = find_merge_item(merges, p.num_merges, ch.x);
-        last = atomic_add_acq_rel(p.counters + item, 1) == merges[3 * item + 2] - 1 ? item + 1 : 0;
-      }
-      last = __shfl_sync(0xffffffffu, last, 0);
-      if (last) {
-        merge_unit<T, D>(p, lane, ch.x, merges[3 * (last - 1) + 1], merges[3 * (last - 1) + 2]);
-        if (lane == 0) p.counters[last - 1] = 0;  // ready for the next run
+      if (lane == 0) last = atomic_add_acq_rel(p.counters + ch.item, 1) == ch.pieces - 1;
+      if (__shfl_sync(0xffffffffu, last, 0)) {
+        merge_unit<T, D>(p, lane, ch.unit, ch.first_slot, ch.pieces);
+        if (lane == 0) p.counters[ch.item] = 0;  // ready for the next run
       }
     }
   }
@@ -553,10 +550,8 @@ template <typename T, int D, int NT>
 bskv_status launch(const bskv_plan* plan, const Fp4DecodeParams& dp, cudaStream_t st) {
   const size_t smem = size_t(kWarps) * kStages * Shape<D>::kStage;
   auto kern = decode_fp4_kernel<T, D, NT>;
-  if (bskv_status s = cuda_check(
-          cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)),
-          "decode_fp4: cudaFuncSetAttribute"))
-    return s;
+  static std::atomic<int> allowed[64];
+  if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "decode_fp4: cudaFuncSetAttribute")) return s;
   kern<<<meta_word(plan, H_GRID), kWarps * 32, smem, st>>>(dp);
   return cuda_check(cudaGetLastError(), "decode_fp4 kernel launch");
 }
@@ -620,15 +615,14 @@ extern "C" bskv_status bskv_run_decode_fp4(const bskv_plan* plan, const void* q,
                                                ((size_t(slots) * dp.group * plan->head_dim * 4 + 255) & ~size_t(255)))
                     : nullptr;
   dp.off_workers = meta_word(plan, H_OFF_WORKERS);
-  dp.off_chunks = meta_word(plan, H_OFF_CHUNKS);
+  dp.off_records = plan->walk_records;
   dp.off_merges = meta_word(plan, H_OFF_MERGES);
-  dp.off_aux0 = meta_word(plan, H_OFF_AUX0);
   dp.off_aux1 = meta_word(plan, H_OFF_AUX1);
   dp.num_merges = meta_word(plan, H_MERGES);
   dp.num_workers = meta_word(plan, H_WORKERS);
   dp.scale_log2 = sm_scale_log2(sm_scale, plan->head_dim);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool fused = grid && dp.num_merges > 0 && plan->max_merge_count <= kFusedMergeMaxPieces;
+  const bool fused = grid && dp.num_merges > 0 && plan->max_merge_count <= kFp4FusedPieces;
   if (fused) dp.counters = plan->counters_dev;
   if (grid) {
     const bskv_status s = plan->dtype == BSKV_BF16 ? launch_t<__nv_bfloat16>(plan, dp, st)

@@ -254,8 +254,8 @@ bskv_status run(const char* who, const bskv_plan* plan, float* scores, const int
   if (compact_scores)
     mp.plane[planes++] = Plane{reinterpret_cast<uint8_t*>(scores), 4 * e.w_s0, 4 * e.w_s1, 4, 4, 1};
   const int smem = int(sizeof(uint32_t)) * std::min(kSelectKeys, plan->longest);
-  if (bskv_status s = cuda_check(cudaFuncSetAttribute(evict_select_kernel,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+  static std::atomic<int> allowed[64];
+  if (bskv_status s = allow_smem(reinterpret_cast<const void*>(evict_select_kernel), size_t(smem), allowed,
                                  "evict: cudaFuncSetAttribute"))
     return s;
   evict_select_kernel<<<dim3(unsigned(plan->num_kv_heads), unsigned(plan->batch)), kSelectThreads, smem, st>>>(e);

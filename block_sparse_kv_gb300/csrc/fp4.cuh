@@ -43,6 +43,14 @@ __device__ __forceinline__ void cvt_e2m1x4(uint32_t w, uint32_t& lo, uint32_t& h
       : "r"(w));
 }
 
+// (a & 0x0f0f0f0f) | (b & 0xf0f0f0f0) in one instruction (written out, the compiler narrows the
+// masks to the bits it knows and needs two).
+__device__ __forceinline__ uint32_t nibbles(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, 0x0f0f0f0f, 0xE4;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Scale code of a block whose largest magnitude has the fp32 bits `top` (sign cleared):
 // 2^(floor(log2 max) - 2), so that the largest value lands in [4, 8) and rounds to 4 or 6;
 // 0 (2^-127) below 2^-125; 255 (NaN) when the block holds an infinity or a NaN.

@@ -120,6 +120,9 @@ inline int32_t decode_group_heads(int32_t num_kv_heads, int32_t page_size) {
 // thread).
 constexpr int kFp4Tile = 32;   // tokens per pipeline stage
 constexpr int kFp4Warps = 4;
+constexpr int kFp4PublishTiles = 1, kFp4MergeTiles = 1, kFp4BoundaryTiles = 0;
+constexpr int kFp4MinTiles = 2;      // a worker has at least this many (unless there are fewer)
+constexpr int kFp4FusedPieces = 16;  // a unit of more pieces is merged by a kernel of its own
 constexpr int fp4_column_tiles(int group) { return group <= 4 ? 0 : group <= 8 ? 1 : 2; }
 constexpr int fp4_ctas_per_sm(int column_tiles) { return column_tiles == 0 ? 3 : column_tiles == 1 ? 3 : 2; }
 
@@ -132,6 +135,11 @@ constexpr int kWeightsWarps = 4;
 constexpr int kWeightsKeys = 128;
 // CTAs of the stream kernel an SM holds (its ring of 16-bit rows of 128 dims takes 98 KB).
 constexpr int weights_ctas_per_sm(int head_dim, bool fp4) { return !fp4 && head_dim == 128 ? 2 : 4; }
+
+// Walk records: 4-bit decode plans and the stream variants of attention-weight plans end with one
+// per chunk, worker by worker in the order in which the worker walks its chunks: {unit, first token,
+// end token, slot, kv_indptr of the request, merge item of the unit, its first slot, its pieces}.
+constexpr int kWalkWords = 8;
 
 // Page sizes of a 4-bit paged cache: the kernels copy groups of 8 tokens that lie in one page.
 inline bool fp4_page_size(int32_t page_size) {
@@ -187,6 +195,7 @@ struct bskv_plan {
   // page-major decode: word offset in the metadata of the per-worker start records
   // (kDecodeStartWords each), or -1
   int32_t decode_starts = -1;
+  int32_t walk_records = -1;  // word offset of the walk records, or -1
   // evict: tokens that stay over all requests, protected first / last tokens, the longest
   // request, whether the kept rows stay in their pages, CTAs that share the rows of one slice
   int64_t kept_total = 0;

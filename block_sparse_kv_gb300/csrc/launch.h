@@ -4,6 +4,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -28,6 +30,10 @@ bskv_status check_fp4_cache(const char* who, const void* kv_codes, const int64_t
 bskv_status launch_state_merge(const bskv_plan* plan, const int32_t* meta, float* ws_o,
                                float* ws_lse, void* out, const int64_t* out_strides, float* lse,
                                int units_per_request, int slot_rows, cudaStream_t stream);
+
+// Allow a kernel `bytes` of dynamic shared memory on the current device, asking the runtime only
+// when it has not been allowed as much there before.
+bskv_status allow_smem(const void* kernel, size_t bytes, std::atomic<int> (&allowed)[64], const char* what);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

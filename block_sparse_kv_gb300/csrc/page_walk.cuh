@@ -4,19 +4,27 @@
 #pragma once
 
 #include "common.cuh"
-#include "split_merge.cuh"
 
 namespace bskv {
 namespace dev {
 
 constexpr int kWalkTile = 32;
 
+// One walk record of the plan (kWalkWords).
+struct WalkChunk {
+  int unit, begin, end, slot, pbase, item, first_slot, pieces;
+};
+__device__ __forceinline__ WalkChunk walk_chunk(const int32_t* records, int i) {
+  const int4 a = __ldg(reinterpret_cast<const int4*>(records) + 2 * i);
+  const int4 b = __ldg(reinterpret_cast<const int4*>(records) + 2 * i + 1);
+  return WalkChunk{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
 struct PageWalk {
-  const int4* chunks;         // {unit, first token, end token, slot}; unit = request * heads + head
-  const int32_t* kv_indptr;
+  const int32_t* records;     // of this worker
   const int32_t* kv_indices;
-  int c0, c1, num_kv_heads, page_size, lane;
-  int k = 0;                  // chunk being walked, in chunk_at order
+  int left, num_kv_heads, page_size, lane;  // chunks to open yet
+  int k = -1;                 // chunk being walked
   int tok = 0, end = 0;       // its tokens [tok, end) are still to come
   int kvh = 0, pbase = 0, win = 0;
   // Lane i holds the page and slot of the 8 tokens at win + 8 i, and of those 256 tokens later,
@@ -24,17 +32,12 @@ struct PageWalk {
   int page = 0, slot = 0, page2 = 0, slot2 = 0;
   bool fresh = false;
 
-  __device__ __forceinline__ PageWalk(const int32_t* meta, int off_workers, int off_chunks,
-                                      int off_aux0, int off_aux1, int worker, int heads, int ps,
-                                      int lane_)
-      : chunks(reinterpret_cast<const int4*>(meta + off_chunks)), kv_indptr(meta + off_aux0),
-        kv_indices(meta + off_aux1), c0(__ldg(meta + off_workers + worker)),
-        c1(__ldg(meta + off_workers + worker + 1)), num_kv_heads(heads), page_size(ps), lane(lane_) {
+  __device__ __forceinline__ PageWalk(const int32_t* records_, int chunks, const int32_t* indices, int heads,
+                                      int ps, int lane_)
+      : records(records_), kv_indices(indices), left(chunks), num_kv_heads(heads), page_size(ps), lane(lane_) {
     open();
   }
-  __device__ __forceinline__ int count() const { return c1 - c0; }
-  __device__ __forceinline__ int4 chunk(int i) const { return __ldg(chunks + chunk_at(c0, c1, i)); }
-  __device__ __forceinline__ bool live() const { return k < c1 - c0; }
+  __device__ __forceinline__ bool live() const { return left >= 0; }
 
   __device__ __forceinline__ void lookup(int first, int& pg, int& sl) const {
     const int at = first + 8 * lane;
@@ -45,13 +48,13 @@ struct PageWalk {
     }
   }
   __device__ __forceinline__ void open() {
-    if (!live()) return;
-    const int4 ch = chunk(k);
-    const int b = ch.x / num_kv_heads;
-    kvh = ch.x - b * num_kv_heads;
-    tok = win = ch.y;
-    end = ch.z;
-    pbase = __ldg(kv_indptr + b);
+    ++k;
+    if (--left < 0) return;
+    const WalkChunk c = walk_chunk(records, k);
+    kvh = c.unit % num_kv_heads;
+    tok = win = c.begin;
+    end = c.end;
+    pbase = c.pbase;
     fresh = true;
     lookup(win, page, slot);
     lookup(win + 256, page2, slot2);
@@ -77,10 +80,7 @@ struct PageWalk {
   __device__ __forceinline__ bool has(int r) const { return tok + (r & ~7) < end; }
   __device__ __forceinline__ void advance() {
     tok += kWalkTile;
-    if (tok >= end) {
-      ++k;
-      open();
-    }
+    if (tok >= end) open();
   }
 };
 

@@ -599,6 +599,34 @@ bskv_status pages_once(const char* who, const char* name, const int32_t* indices
   return BSKV_OK;
 }
 
+// Appends the walk records (kWalkWords) to an assembled plan whose units are (request, kv head).
+void add_walk_records(bskv_plan* p, const std::vector<int32_t>& worker_ptr, const std::vector<Chunk>& chunks,
+                      const std::vector<int32_t>& merges, const int32_t* kv_indptr, int32_t units_per_request) {
+  std::vector<int32_t>& m = p->meta;
+  p->walk_records = int32_t(m.size());
+  for (size_t w = 0; w + 1 < worker_ptr.size(); ++w) {
+    const int32_t w0 = worker_ptr[w], n = worker_ptr[w + 1] - w0;
+    for (int32_t k = 0; k < n; ++k) {
+      // the last chunk first: a unit cut between two workers is then finished early by both
+      const Chunk& c = chunks[size_t(n >= 2 ? (k == 0 ? w0 + n - 1 : w0 + k - 1) : w0 + k)];
+      int32_t rec[kWalkWords] = {c.unit, c.a, c.b, c.c, kv_indptr[c.unit / units_per_request], -1, -1, 0};
+      if (c.c >= 0) {  // merge items are sorted by unit
+        size_t lo = 0, hi = merges.size() / 3;
+        while (hi - lo > 1) {
+          const size_t mid = (lo + hi) / 2;
+          if (merges[3 * mid] <= c.unit) lo = mid;
+          else hi = mid;
+        }
+        rec[5] = int32_t(lo);
+        rec[6] = merges[3 * lo + 1];
+        rec[7] = merges[3 * lo + 2];
+      }
+      m.insert(m.end(), rec, rec + kWalkWords);
+    }
+  }
+  m[H_TOTAL] = int32_t(m.size());
+}
+
 // Head counts, head_dim, page size and dtype of the cache operators.
 bskv_status check_cache_shape(const char* who, int32_t batch, int32_t num_pages, int32_t page_size,
                               int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -646,12 +674,16 @@ extern "C" bskv_status bskv_plan_decode_fp4(const int32_t* kv_indptr, const int3
     for (int32_t h = 0; h < num_kv_heads; ++h) len[size_t(b) * num_kv_heads + h] = req[size_t(b)];
   }
   if (total > INT32_MAX / num_kv_heads || len.size() > size_t(INT32_MAX / 4)) { set_error("%s: too many tokens", who); return BSKV_ERR_UNSUPPORTED; }
-  const int64_t slots_per_sm = kFp4Warps * fp4_ctas_per_sm(fp4_column_tiles(group));
+  int64_t tiles = 0;
+  for (int64_t L : len) tiles += (L + kFp4Tile - 1) / kFp4Tile;
+  const int64_t cap = std::min<int64_t>(int64_t(num_sms) * kFp4Warps * fp4_ctas_per_sm(fp4_column_tiles(group)),
+                                        (tiles + kFp4MinTiles - 1) / kFp4MinTiles);
   std::vector<int32_t> worker_ptr, merges;
   std::vector<Chunk> chunks;
   int32_t slots = 0;
-  linear_partition(len, kFp4Tile, max_workers > 0 ? max_workers : num_sms * slots_per_sm,
-                   worker_ptr, chunks, slots, merges);
+  linear_partition_cost(len, kFp4Tile, max_workers > 0 ? max_workers : cap,
+                        FillCosts{kFp4PublishTiles, kFp4MergeTiles, kFp4BoundaryTiles}, worker_ptr,
+                        chunks, slots, merges);
   const int32_t P = int32_t(worker_ptr.size() - 1);
   bskv_plan* p = new bskv_plan();
   p->kind = KIND_DECODE_FP4;
@@ -661,6 +693,7 @@ extern "C" bskv_status bskv_plan_decode_fp4(const int32_t* kv_indptr, const int3
   assemble(p, KIND_DECODE_FP4, int32_t(len.size()), worker_ptr, chunks, slots, merges, kFp4Tile,
            kv_indptr, batch > 0 ? size_t(batch) + 1 : 0, kv_indices,
            batch > 0 ? size_t(kv_indptr[batch]) : 0, (P + kFp4Warps - 1) / kFp4Warps, 0);
+  add_walk_records(p, worker_ptr, chunks, merges, kv_indptr, num_kv_heads);
   p->float_ws_bytes = slots == 0 ? 0
       : align256(size_t(slots) * group * head_dim * 4) + align256(size_t(slots) * group * 4);
   p->counter_words = merges.size() / 3;
@@ -715,6 +748,7 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
       for (int32_t h = 0; h < num_kv_heads; ++h) len[size_t(b) * num_kv_heads + h] = req[size_t(b)];
     int32_t slots = 0;
     linear_partition(len, kFp4Tile, int64_t(num_sms) * kWeightsWarps * 4, worker_ptr, chunks, slots, no_merges);
+    for (Chunk& c : chunks) c.c = -1;  // every token's sum is complete where it is computed
     grid = (int32_t(worker_ptr.size()) - 1 + kWeightsWarps - 1) / kWeightsWarps;
     units = int32_t(len.size());
   } else {
@@ -733,6 +767,7 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
   assemble(p, KIND_WEIGHTS, units, worker_ptr, chunks, 0, queries, kFp4Tile, kv_indptr,
            batch > 0 ? size_t(batch) + 1 : 0, kv_indices, batch > 0 ? size_t(kv_indptr[batch]) : 0,
            grid, variant);
+  if (variant != WEIGHTS_TILE) add_walk_records(p, worker_ptr, chunks, no_merges, kv_indptr, num_kv_heads);
   *out_plan = p;
   log_plan("bskv_plan_attn_weights", p);
   return BSKV_OK;

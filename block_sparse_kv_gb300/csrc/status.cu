@@ -63,6 +63,17 @@ bskv_status status_args(dev::StatusArgs* out) {
   return BSKV_OK;
 }
 
+bskv_status allow_smem(const void* kernel, size_t bytes, std::atomic<int> (&allowed)[64], const char* what) {
+  int d = 0;
+  if (bskv_status s = cuda_check(cudaGetDevice(&d), "cudaGetDevice")) return s;
+  if (d >= 0 && d < 64 && allowed[d].load(std::memory_order_relaxed) >= int(bytes)) return BSKV_OK;
+  if (bskv_status s = cuda_check(
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)), what))
+    return s;
+  if (d >= 0 && d < 64) allowed[d].store(int(bytes), std::memory_order_relaxed);
+  return BSKV_OK;
+}
+
 }  // namespace bskv
 
 using namespace bskv;
