@@ -5,10 +5,15 @@
 // to v / X (ties to even, at most 6): the OCP Microscaling conversion. X is a power of two, so
 // v / X is exact in fp32 and one rounding, cvt.rn.satfinite.e2m1x2, is made per value.
 //
-// Both directions are HBM streams (2 bytes and 17/32 bytes a value). A lane owns 8 values: one
-// 16-byte load or store on the 16-bit side, 4 bytes of codes on the other; the four lanes of a
-// block find its maximum with two shuffles. A lane issues the loads of kUnroll chunks, and the
-// index chains of their rows (request, position -> page table -> page), before it converts any.
+// Both directions are HBM streams (2 bytes and 17/32 bytes a value), and what it takes to find a
+// row's addresses costs more instructions than the conversion if every thread does it. A thread owns
+// half a block of 32 (a chunk): the values 8 e .. 8 e + 7 and 16 + 8 e .. of it for lane parity e, so
+// that a pair of lanes reads or writes whole 32-byte sectors; one shuffle finds the block's maximum.
+// A CTA of a few thousand chunks makes two tables in shared memory, one entry per thread: the places
+// of its tokens (three dependent loads: request and position, page table, page) and of the 2 x heads
+// rows of a token.
+#include <algorithm>
+
 #include "common.cuh"
 #include "fp4.cuh"
 #include "internal.h"
@@ -19,8 +24,12 @@ namespace {
 
 using namespace dev;
 
-constexpr int kUnroll = 4;     // 8-value chunks per lane
 constexpr int kThreads = 256;
+constexpr int kUnroll = 4;                   // chunks of 16 values per thread and pass
+constexpr int kPass = kThreads * kUnroll;
+constexpr int kMaxTokens = kPass / 8 + 2;    // of a CTA: a pass touches at most these (8 chunks a token)
+constexpr int kCtas = 4 * 152;               // four per SM: enough CTAs to share long inputs
+constexpr int kMaxHeads = 128;
 
 struct Fp4CacheParams {
   void* rows[2];  // K, V: 16-bit (or fp32) rows, [nnz, heads, D]
@@ -35,28 +44,75 @@ struct Fp4CacheParams {
   const int32_t* indices;
   int32_t batch, page_size;
   int64_t num_pages;
-  int64_t chunks;     // nnz * 2 * heads * D / 8
-  int32_t per_token;  // 2 * heads * D / 8
-  int32_t heads;
+  int64_t chunks;     // nnz * 2 * heads * D / 16
+  int32_t span;       // chunks of a CTA, a multiple of kPass
+  int32_t per_token;  // 2 * heads * D / 16
+  uint32_t magic;     // ceil(2^32 / (2 heads)): r / (2 heads) = hi(r * magic) while r * 2 heads < 2^32
+  int32_t heads, esz;  // bytes per value of the rows
   StatusArgs st;
 };
 
-// Where a chunk's row lies: token, K or V, head, first value.
-struct ChunkAt {
-  int64_t token;
-  int32_t which, head, d;
+// Byte offsets of a token in the cache (codes = -1 when it has no place there), and of row r of a
+// token (K of every head, then V); `rows` is the row of the CTA's first token on the 16-bit side.
+struct TokenAt {
+  int64_t codes, scales;
+};
+struct RowAt {
+  const uint8_t* rows;
+  int64_t codes, scales;
+};
+struct Tables {
+  TokenAt token[kMaxTokens];
+  RowAt row[2 * kMaxHeads];
 };
 
+// The CTA's chunks. Chunk j of a thread (j * kThreads + its index) has the same values of its row for
+// every j: d .. d + 7 and d + 16 .. d + 23.
 template <int D>
-__device__ __forceinline__ ChunkAt chunk_place(const Fp4CacheParams& p, int64_t id) {
-  ChunkAt a;
-  a.token = id / p.per_token;
-  const int32_t r = int32_t(id - a.token * p.per_token);
-  const int32_t row = r / (D / 8);
-  a.d = (r % (D / 8)) * 8;
-  a.which = row >= p.heads ? 1 : 0;
-  a.head = row - a.which * p.heads;
-  return a;
+struct Chunks {
+  int64_t t0;  // first token
+  int32_t row0, d, left;
+  __device__ __forceinline__ explicit Chunks(const Fp4CacheParams& p) {
+    const int64_t base = int64_t(blockIdx.x) * p.span;
+    t0 = base / p.per_token;
+    const int32_t r = int32_t(base - t0 * p.per_token) + threadIdx.x, c = r % (D / 16);
+    row0 = r / (D / 16);
+    d = (c >> 1) * 32 + (c & 1) * 8;
+    left = int32_t(min(int64_t(p.span), p.chunks - base));
+  }
+  // The CTA's token of chunk j and the row within it.
+  __device__ __forceinline__ void at(const Fp4CacheParams& p, int j, int& token, int& row) const {
+    const uint32_t r = uint32_t(row0 + j * (kThreads / (D / 16)));
+    token = int(__umulhi(r, p.magic));
+    row = int(r) - token * 2 * p.heads;
+  }
+  __device__ __forceinline__ bool live(int j) const { return j * kThreads + int(threadIdx.x) < left; }
+  __device__ __forceinline__ int tokens(const Fp4CacheParams& p) const {
+    return int((int64_t(blockIdx.x) * p.span + left - 1) / p.per_token - t0) + 1;
+  }
+};
+
+__device__ __forceinline__ void make_rows(const Fp4CacheParams& p, int64_t t0, Tables& tab) {
+  if (int(threadIdx.x) >= 2 * p.heads) return;
+  const int which = int(threadIdx.x) >= p.heads, head = threadIdx.x - which * p.heads;
+  tab.row[threadIdx.x] = RowAt{static_cast<const uint8_t*>(p.rows[which]) + (t0 * p.r_s0[which] + head * p.r_s1[which]) * p.esz,
+                               which * p.c_s1 + head * p.c_s2, which * p.s_s1 + head * p.s_s2};
+}
+
+template <int D>
+__device__ __forceinline__ void make_tokens(const Fp4CacheParams& p, const Chunks<D>& c, Tables& tab) {
+  if (int(threadIdx.x) >= c.tokens(p)) return;
+  const int64_t t = c.t0 + threadIdx.x;
+  int32_t page, slot;
+  TokenAt at{-1, -1};
+  if (page_slot(p.indptr, p.indices, p.batch, p.page_size, p.num_pages, __ldg(p.batch_indices + t),
+                __ldg(p.positions + t), page, slot)) {
+    at.codes = page * p.c_s0 + slot * p.c_s3;
+    at.scales = page * p.s_s0 + slot * (D / kFp4Block);
+  } else {
+    record_error(p.st, BSKV_ERR_DEVICE_INDEX);
+  }
+  tab.token[threadIdx.x] = at;
 }
 
 template <typename T>
@@ -70,56 +126,66 @@ __device__ __forceinline__ float2 to_float2<__half>(uint32_t w) {
   return __half22float2(*reinterpret_cast<__half2*>(&w));
 }
 
+// Largest magnitude of the two lanes' 32 values as fp32 bits; the sign-less 16-bit patterns of both
+// types order as integers, a NaN above infinity.
+template <typename T>
+__device__ __forceinline__ uint32_t block_max(const uint4 (&x)[2]) {
+  constexpr uint32_t k = 0x7fff7fffu;
+  uint32_t m = __vmaxu2(__vmaxu2(x[0].x & k, x[0].y & k), __vmaxu2(x[0].z & k, x[0].w & k));
+  m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[1].x & k, x[1].y & k), __vmaxu2(x[1].z & k, x[1].w & k)));
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m & 0xffffu, m >> 16);
+  return __float_as_uint(to_float2<T>(m).x);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t quantise8(const uint4& x, float inv) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t packed = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = to_float2<T>(w[i]);
+    packed |= cvt_e2m1x2(v.x * inv, v.y * inv) << (8 * i);
+  }
+  return packed;
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) fp4_append_kernel(const Fp4CacheParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t base = (int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (32 * kUnroll);
-  uint4 x[kUnroll];
-  ChunkAt at[kUnroll];
-  int32_t page[kUnroll], slot[kUnroll];
-  bool live[kUnroll], ok[kUnroll];
+__global__ void __launch_bounds__(kThreads, 4) fp4_append_kernel(const Fp4CacheParams p) {
+  __shared__ Tables tab;
+  const Chunks<D> c(p);
+  make_rows(p, c.t0, tab);
+  make_tokens<D>(p, c, tab);
+  __syncthreads();
+  for (int j0 = 0; j0 * kThreads < c.left; j0 += kUnroll) {
+    uint4 x[kUnroll][2];
 #pragma unroll
-  for (int j = 0; j < kUnroll; ++j) {
-    const int64_t id = base + j * 32 + lane;
-    live[j] = id < p.chunks;
-    x[j] = make_uint4(0, 0, 0, 0);
-    if (!live[j]) continue;
-    at[j] = chunk_place<D>(p, id);
-    const T* row = static_cast<const T*>(p.rows[at[j].which]) + at[j].token * p.r_s0[at[j].which] +
-                   at[j].head * p.r_s1[at[j].which] + at[j].d;
-    x[j] = __ldcs(reinterpret_cast<const uint4*>(row));
-  }
-#pragma unroll
-  for (int j = 0; j < kUnroll; ++j) {
-    ok[j] = live[j] && page_slot(p.indptr, p.indices, p.batch, p.page_size, p.num_pages,
-                                 __ldg(p.batch_indices + at[j].token),
-                                 __ldg(p.positions + at[j].token), page[j], slot[j]);
-    if (live[j] && !ok[j]) record_error(p.st, BSKV_ERR_DEVICE_INDEX);
-  }
-#pragma unroll
-  for (int j = 0; j < kUnroll; ++j) {
-    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-    float2 v[4];
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = to_float2<T>(w[i]);
-      top = max(top, max(__float_as_uint(v[i].x) & 0x7fffffffu, __float_as_uint(v[i].y) & 0x7fffffffu));
+    for (int j = 0; j < kUnroll; ++j) {
+      int token, row;
+      c.at(p, j0 + j, token, row);
+      x[j][0] = x[j][1] = make_uint4(0, 0, 0, 0);
+      if (!c.live(j0 + j)) continue;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          tab.row[row].rows + token * (p.r_s0[row >= p.heads] * int64_t(sizeof(T))) + c.d * sizeof(T));
+      x[j][0] = __ldcs(src);
+      x[j][1] = __ldcs(src + 2);
     }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const uint32_t code = e8m0_of_max(top);
-    const float inv = e8m0_inverse(code == 255u ? 127u : code);
-    uint32_t packed = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) packed |= cvt_e2m1x2(v[i].x * inv, v[i].y * inv) << (8 * i);
-    if (!ok[j]) continue;
-    uint8_t* c = p.codes + page[j] * p.c_s0 + at[j].which * p.c_s1 + at[j].head * p.c_s2 +
-                 slot[j] * p.c_s3 + at[j].d / 2;
-    *reinterpret_cast<uint32_t*>(c) = packed;
-    if ((lane & 3) == 0)
-      p.scales[page[j] * p.s_s0 + at[j].which * p.s_s1 + at[j].head * p.s_s2 +
-               slot[j] * (D / kFp4Block) + at[j].d / kFp4Block] = uint8_t(code);
+    for (int j = 0; j < kUnroll; ++j) {
+      const uint32_t code = e8m0_of_max(block_max<T>(x[j]));
+      const float inv = e8m0_inverse(code == 255u ? 127u : code);
+      const uint32_t lo = quantise8<T>(x[j][0], inv), hi = quantise8<T>(x[j][1], inv);
+      if (!c.live(j0 + j)) continue;
+      int token, row;
+      c.at(p, j0 + j, token, row);
+      const TokenAt at = tab.token[token];
+      if (at.codes < 0) continue;
+      const RowAt r = tab.row[row];
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.codes + at.codes + r.codes + c.d / 2);
+      dst[0] = lo;
+      dst[2] = hi;
+      if ((threadIdx.x & 1) == 0) p.scales[at.scales + r.scales + c.d / kFp4Block] = uint8_t(code);
+    }
   }
 }
 
@@ -144,43 +210,48 @@ __device__ __forceinline__ void store8<__half>(__half* dst, const float (&v)[8])
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) fp4_read_kernel(const Fp4CacheParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t base = (int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (32 * kUnroll);
-  ChunkAt at[kUnroll];
-  uint32_t w[kUnroll], code[kUnroll];
-  bool ok[kUnroll];
+__global__ void __launch_bounds__(kThreads, 4) fp4_read_kernel(const Fp4CacheParams p) {
+  __shared__ Tables tab;
+  const Chunks<D> c(p);
+  make_rows(p, c.t0, tab);
+  make_tokens<D>(p, c, tab);
+  __syncthreads();
+  for (int j0 = 0; j0 * kThreads < c.left; j0 += kUnroll) {
+    uint32_t w[kUnroll][2], code[kUnroll];
+    T* dst[kUnroll];
 #pragma unroll
-  for (int j = 0; j < kUnroll; ++j) {
-    const int64_t id = base + j * 32 + lane;
-    const bool live = id < p.chunks;
-    int32_t page = 0, slot = 0;
-    if (live) at[j] = chunk_place<D>(p, id);
-    ok[j] = live && page_slot(p.indptr, p.indices, p.batch, p.page_size, p.num_pages,
-                              __ldg(p.batch_indices + at[j].token),
-                              __ldg(p.positions + at[j].token), page, slot);
-    if (live && !ok[j]) record_error(p.st, BSKV_ERR_DEVICE_INDEX);
-    if (!ok[j]) continue;
-    w[j] = *reinterpret_cast<const uint32_t*>(p.codes + page * p.c_s0 + at[j].which * p.c_s1 +
-                                              at[j].head * p.c_s2 + slot * p.c_s3 + at[j].d / 2);
-    code[j] = p.scales[page * p.s_s0 + at[j].which * p.s_s1 + at[j].head * p.s_s2 +
-                       slot * (D / kFp4Block) + at[j].d / kFp4Block];
-  }
-#pragma unroll
-  for (int j = 0; j < kUnroll; ++j) {
-    if (!ok[j]) continue;
-    uint32_t h[4];
-    cvt_e2m1x8(w[j], h);
-    const float f = e8m0_value(code[j]);
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 a = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
-      v[2 * i] = a.x * f;
-      v[2 * i + 1] = a.y * f;
+    for (int j = 0; j < kUnroll; ++j) {
+      int token, row;
+      c.at(p, j0 + j, token, row);
+      dst[j] = nullptr;
+      if (!c.live(j0 + j)) continue;
+      const TokenAt at = tab.token[token];
+      if (at.codes < 0) continue;
+      const RowAt r = tab.row[row];
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.codes + at.codes + r.codes + c.d / 2);
+      w[j][0] = __ldg(src);
+      w[j][1] = __ldg(src + 2);
+      code[j] = __ldg(p.scales + at.scales + r.scales + c.d / kFp4Block);
+      dst[j] = reinterpret_cast<T*>(const_cast<uint8_t*>(r.rows) + token * (p.r_s0[row >= p.heads] * int64_t(sizeof(T)))) + c.d;
     }
-    store8<T>(static_cast<T*>(p.rows[at[j].which]) + at[j].token * p.r_s0[at[j].which] +
-                  at[j].head * p.r_s1[at[j].which] + at[j].d, v);
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      if (!dst[j]) continue;
+      const float f = e8m0_value(code[j]);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t h[4];
+        cvt_e2m1x8(w[j][half], h);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 e = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
+          v[2 * i] = e.x * f;
+          v[2 * i + 1] = e.y * f;
+        }
+        store8<T>(dst[j] + 16 * half, v);
+      }
+    }
   }
 }
 
@@ -200,8 +271,8 @@ bskv_status prepare(const char* who, const void* k, const int64_t* k_strides, co
   if (head_dim != 64 && head_dim != 128) { set_error("%s: head_dim %d not in {64,128}", who, head_dim); return BSKV_ERR_UNSUPPORTED; }
   if (page_size < 1) { set_error("%s: page_size %d", who, page_size); return BSKV_ERR_INVALID_ARG; }
   if (!fp4_page_size(page_size)) { set_error("%s: page_size %d unsupported (8 or a multiple of 16)", who, page_size); return BSKV_ERR_UNSUPPORTED; }
-  if (num_pages > INT32_MAX || int64_t(num_kv_heads) * head_dim / 4 > INT32_MAX) {
-    set_error("%s: too large", who);
+  if (num_pages > INT32_MAX || num_kv_heads > kMaxHeads) {
+    set_error("%s: num_pages=%lld num_kv_heads=%d (max %d)", who, (long long)num_pages, num_kv_heads, kMaxHeads);
     return BSKV_ERR_UNSUPPORTED;
   }
   if (nnz == 0) return BSKV_OK;
@@ -230,18 +301,22 @@ bskv_status prepare(const char* who, const void* k, const int64_t* k_strides, co
   p->indptr = kv_indptr; p->indices = kv_indices;
   p->batch = batch; p->page_size = page_size; p->num_pages = num_pages;
   p->heads = num_kv_heads;
-  p->per_token = 2 * num_kv_heads * (head_dim / 8);
+  p->per_token = 2 * num_kv_heads * (head_dim / 16);
   p->chunks = nnz * p->per_token;
-  if ((p->chunks + kThreads * kUnroll - 1) / (kThreads * kUnroll) > INT32_MAX) {
+  p->esz = esz;
+  p->magic = uint32_t(((uint64_t(1) << 32) + uint32_t(2 * num_kv_heads) - 1) / uint32_t(2 * num_kv_heads));
+  // passes per CTA: as many as let kCtas CTAs share the input, within the token table
+  const int64_t passes = (p->chunks + kPass - 1) / kPass;
+  const int64_t most = std::max<int64_t>(1, int64_t(kMaxTokens - 2) * p->per_token / kPass);
+  p->span = int32_t(kPass * std::min(most, (passes + kCtas - 1) / kCtas));
+  if ((p->chunks + p->span - 1) / p->span > INT32_MAX) {
     set_error("%s: too many rows", who);
     return BSKV_ERR_UNSUPPORTED;
   }
   return status_args(&p->st);
 }
 
-unsigned grid_of(const Fp4CacheParams& p) {
-  return unsigned((p.chunks + kThreads * kUnroll - 1) / (kThreads * kUnroll));
-}
+unsigned grid_of(const Fp4CacheParams& p) { return unsigned((p.chunks + p.span - 1) / p.span); }
 
 }  // namespace
 
