@@ -8,21 +8,23 @@
 // only, each key's sum is independent of every other's, and one warp makes it: no atomics, and
 // the same bits on every run.
 //
-// Keys are the M = 16 rows of mma.sync m16n8k16, query rows (token, head) its N = 8 columns, so a
-// key's sum stays in its lanes until one reduction over the four lanes of its row. A row's lane
-// reads 16-byte chunks t, t + 4, ...: products of chunk c with the same chunk of the query are
-// two k-steps, whatever the order of the dims. Two kernels:
-//   * stream (up to 16 query rows a request, the decode step): query fragments stay in
-//     registers, each warp streams a range of tokens through a private ring of 32-token tiles
+// Two kernels, by the query rows (queries times heads of the group) of the longest request:
+//   * stream (up to 16 rows, the decode step): keys are the M = 16 rows of mma.sync m16n8k16, query
+//     rows its N = 8 columns, so a key's sum stays in its lanes until one reduction over the four
+//     lanes of its row. A row's lane reads 16-byte chunks t, t + 4, ...: products of chunk c with the
+//     same chunk of the query are two k-steps, whatever the order of the dims. Query fragments stay
+//     in registers, each warp streams a range of tokens through a private ring of 32-token tiles
 //     filled by 16-byte asynchronous copies; bound by reading K (HBM).
-//   * tile (more rows, a prefill window): a CTA keeps the fragments of 128 keys in registers and
-//     passes the query rows, staged in shared memory 64 at a time, over them; a warp's 32 keys
-//     halve the shared-memory reads per product against 16. Bound by the tensor pipe and exp.
+//   * tile (more rows, a prefill window): S = K Q^T by tcgen05, 128 keys against up to 128 query rows
+//     a product. A key is a TMEM lane and so a thread, which reads its row of S and adds up its
+//     weights: no reduction between threads, and two packed FMAs per two weights next to their two
+//     exponentials, which bound it (16 a clock on an SM) together with reading K.
 // 4-bit keys (E2M1 codes times 2^x per 32 values): the stream kernel multiplies codes and f16
 // queries and scales each block's fp32 partial sum; the tile kernel turns a key once into the
 // query's type, relative to its largest scale, and multiplies that back after the product.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -39,23 +41,25 @@ using namespace dev;
 constexpr int kStages = 3;
 constexpr int kTile = kWalkTile;     // tokens per stage of the stream kernel
 constexpr int kWarps = kWeightsWarps;
-constexpr int kKeys = kWeightsKeys;  // keys per CTA of the tile kernel
-constexpr int kRows = 64;            // query rows staged at a time
+constexpr int kKeys = kWeightsKeys;  // keys per CTA of the tile kernel, one per computing thread
+constexpr int kPanel = kKeys * 128;  // 128 rows of 64 16-bit values, swizzled
 
 struct WeightsParams {
   const int32_t* meta;
   const void* q;
   int64_t q_s0, q_s1;
   const uint8_t* keys;              // 16-bit keys or codes
-  int64_t k_s0, k_s2, k_s3;         // bytes: page, kv head, slot
+  int64_t k_s0, k_s1, k_s2, k_s3;   // bytes: page, K/V, kv head, slot
   const uint8_t* scales;            // 4-bit keys
   int64_t s_s0, s_s2;               // bytes
   const float* lse;
   float* scores;
   int64_t w_s0, w_s1;               // floats: page, kv head
   int num_kv_heads, group, page_size, num_qo_heads, causal;
+  int box, tile_queries, buffers;   // tile kernel: keys per TMA box, queries per product, S buffers
   int off_workers, off_chunks, off_records, off_aux0, off_aux1, off_req, num_workers;
   float decay, scale_log2;
+  StatusArgs st;
 };
 
 // The request's queries, in the metadata: first row of q, number of queries, tokens.
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm(D, FP4))
 // tile kernel
 // ---------------------------------------------------------------------------------------
 
-// 16 bytes (8 values) of a 4-bit key as a fragment chunk of T, in units of the row's largest scale.
+// 16 bytes (8 values) of a 4-bit key as a chunk of T, in units of the row's largest scale.
 template <typename T>
 __device__ __forceinline__ uint4 widen(uint32_t w, float f) {
   uint32_t h[4], o[4];
@@ -315,125 +319,228 @@ __device__ __forceinline__ uint4 widen(uint32_t w, float f) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+struct TileShared {
+  float4 pair[2][64];  // of query rows 2 i and 2 i + 1: {-hi, -hi, r, r}
+  int last[2][128];
+  uint64_t k_full, q_full[2], q_empty[2], s_full[2], s_empty[2];
+  uint32_t tmem;
+  int abort;
+};
+
+constexpr int kTileThreads = kKeys + 32;  // a thread per key, and the warp that copies and multiplies
+
 template <typename T, int D, bool FP4>
-__global__ void __launch_bounds__(kKeys) weights_tile_kernel(const WeightsParams p) {
-  constexpr int kRowBytes = 2 * D, kParts = kRowBytes / 16, kThreads = kKeys;
-  __shared__ __align__(128) uint8_t qs[2][kRows * kRowBytes];
-  __shared__ float2 row_hi_r[2][kRows];
-  __shared__ int row_last[2][kRows];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+__global__ void __launch_bounds__(kTileThreads)
+    weights_tile_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ WeightsParams p) {
+  constexpr int kPanels = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ks = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* qs = ks + kPanels * kPanel;
+  TileShared& sh = *reinterpret_cast<TileShared*>(qs + p.buffers * kPanels * kPanel);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kvh = blockIdx.y;
   const int4 ch = __ldg(reinterpret_cast<const int4*>(p.meta + p.off_chunks) + blockIdx.x);
   const int b = ch.x;  // {request, first key, end key, 0}
   const Request rq = request_of(p, b);
-  const int pbase = __ldg(p.meta + p.off_aux0 + b);
-  const int32_t* pages = p.meta + p.off_aux1 + pbase;
-  const int nrows = rq.nq * p.group;
+  const int32_t* pages = p.meta + p.off_aux1 + __ldg(p.meta + p.off_aux0 + b);
   // causal: the first query that sees the tile's first key
-  const int row0 = p.causal ? max(0, ch.y - (rq.len - rq.nq)) * p.group : 0;
+  const int tok0 = p.causal ? max(0, ch.y - (rq.len - rq.nq)) : 0;
+  const int tiles = tok0 < rq.nq ? (rq.nq - tok0 + p.tile_queries - 1) / p.tile_queries : 0;
+  const int nb = p.buffers;
+  const uint32_t cols = nb > 1 ? 256 : 128;
+  if (threadIdx.x == 0) {
+    mbar_init(&sh.k_full, FP4 ? kKeys : 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_empty[i], kKeys);
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(&sh.tmem, cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const bool forced = forced_timeout(p.st);
+  volatile int* abort_flag = &sh.abort;
 
-  auto stage = [&](int buf, int first) {
-    for (int c = threadIdx.x; c < kRows * kParts; c += kThreads) {
-      const int r = c / kParts, part = c % kParts, row = first + r;
-      uint8_t* dst = qs[buf] + r * kRowBytes + ((part ^ ((r & 1) << 2)) << 4);
-      if (row < nrows) {
-        const int tok = row / p.group;
-        cp_async_16(dst, static_cast<const T*>(p.q) + int64_t(rq.qo + tok) * p.q_s0 +
-                             (int64_t(kvh) * p.group + (row - tok * p.group)) * p.q_s1 + part * 8);
-      } else {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+  if (warp == 4) {
+    // The warp stays converged; one lane's copies and products are executed.
+    const uint32_t leader = elect_leader();
+    bool ok = true;
+    if (!FP4 && tiles > 0) {
+      const uint64_t once = l2_evict_first_policy();
+      const int boxes = (ch.z - ch.y + p.box - 1) / p.box;  // at most 16
+      int page = 0, slot = 0;
+      if (lane < boxes) {
+        const int t = ch.y + lane * p.box, n = t / p.page_size;
+        page = __ldg(pages + n);
+        slot = t - n * p.page_size;
+      }
+      mbar_arrive_expect_tx_w(leader, &sh.k_full, uint32_t(boxes) * kPanels * p.box * 128);
+      for (int i = 0; i < boxes; ++i) {
+        const int pg = __shfl_sync(0xffffffffu, page, i), sl = __shfl_sync(0xffffffffu, slot, i);
+#pragma unroll
+        for (int pn = 0; pn < kPanels; ++pn)
+          tma_load_5d_hint_w(leader, ks + pn * kPanel + i * p.box * 128, &kmap, pn * 64, sl, kvh, 0, pg, &sh.k_full, once);
       }
     }
-    cp_async_commit();
-    if (threadIdx.x < kRows) {
-      const RowInfo o = row_info(p, rq, kvh, first + threadIdx.x);
-      row_hi_r[buf][threadIdx.x] = make_float2(o.hi, o.r);
-      row_last[buf][threadIdx.x] = o.last;
+    const uint64_t again = l2_evict_last_policy();  // every tile of the request reads its queries
+    auto load_q = [&](int n) {
+      const int buf = n % nb;
+      mbar_arrive_expect_tx_w(leader, &sh.q_full[buf], uint32_t(kPanels) * p.tile_queries * p.group * 128);
+#pragma unroll
+      for (int pn = 0; pn < kPanels; ++pn)
+        tma_load_3d_hint_w(leader, qs + (buf * kPanels + pn) * kPanel, &qmap, pn * 64, kvh * p.group,
+                           rq.qo + tok0 + n * p.tile_queries, &sh.q_full[buf], again);
+    };
+    int loaded = 0, done = 0;  // query tiles copied, products issued
+    for (; loaded < nb && loaded < tiles; ++loaded) load_q(loaded);
+    const uint32_t fmt = __is_same(T, __half) ? 0u : 1u;
+    const uint32_t idesc = umma_idesc(128, uint32_t((p.tile_queries * p.group + 15) & ~15), fmt, fmt, 0, 0);
+    const uint64_t dk = umma_desc(smem_u32(ks), 16, 1024, kSwz128), dq = umma_desc(smem_u32(qs), 16, 1024, kSwz128);
+    for (int n = 0; n < tiles && ok; ++n) {
+      const int buf = n % nb;
+      const uint32_t use = uint32_t(n / nb);
+      ok = (n > 0 || issuer_wait(&sh.k_full, 0, p.st, forced, abort_flag)) &&
+           issuer_wait(&sh.q_full[buf], use & 1u, p.st, forced, abort_flag) &&
+           (n < nb || issuer_wait(&sh.s_empty[buf], (use - 1) & 1u, p.st, forced, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t at = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+        umma_f16_w(leader, tmem + buf * 128, dk + at, dq + ((buf * kPanels * kPanel) >> 4) + at, idesc, kk > 0 ? 1u : 0u);
+      }
+      umma_commit_w(leader, &sh.s_full[buf]);
+      umma_commit_w(leader, &sh.q_empty[buf]);
+      done = n + 1;
+      if (loaded < tiles) {
+        ok = issuer_wait(&sh.q_empty[buf], use & 1u, p.st, forced, abort_flag);
+        if (ok) load_q(loaded++);
+      }
     }
-  };
-  if (row0 < nrows) stage(0, row0);
-
-  // this warp's 32 keys as A fragments, straight from the cache; row i of a lane is key
-  // ch.y + 32 warp + 8 i + g
-  uint4 a[D / 32][4];
-  float unit[4];
-  const int key0 = ch.y + 32 * warp;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int key = key0 + 8 * i + g;
-    unit[i] = p.scale_log2;
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) a[j][i] = make_uint4(0, 0, 0, 0);
-    if (key < ch.z) {
+    if (!ok) {
+      // copies and products in flight land before the CTA leaves (bounded, not forcible)
+      *abort_flag = 1;
+      if (done > 0) mbar_wait(&sh.s_full[(done - 1) % nb], uint32_t((done - 1) / nb) & 1u, p.st, false);
+      if (!FP4) mbar_wait(&sh.k_full, 0, p.st, false);
+      for (int n = max(0, loaded - nb); n < loaded; ++n) mbar_wait(&sh.q_full[n % nb], (n / nb) & 1u, p.st, false);
+    }
+  } else {
+    const int key = ch.y + int(threadIdx.x);
+    const bool there = key < ch.z;
+    float unit = p.scale_log2;
+    float* score = nullptr;
+    float old = 0.f;
+    const bool fresh = p.decay == 0.f || key >= rq.len - rq.nq;
+    if (there) {
       const int n = key / p.page_size, sl = key - n * p.page_size;
       const int64_t pg = __ldg(pages + n);
-      const uint8_t* src = p.keys + pg * p.k_s0 + kvh * p.k_s2 + sl * p.k_s3;
+      score = p.scores + pg * p.w_s0 + kvh * p.w_s1 + sl;
       if constexpr (FP4) {
-        const uint8_t* sc = p.scales + pg * p.s_s0 + kvh * p.s_s2;
-        uint32_t code[D / 32], top = 0;
-        bool bad = false;
+        if (tiles > 0) {
+          const uint8_t* src = p.keys + pg * p.k_s0 + kvh * p.k_s2 + sl * p.k_s3;
+          const uint8_t* sc = p.scales + pg * p.s_s0 + kvh * p.s_s2 + sl * (D / 32);
+          uint4 w[D / 32];
+          uint32_t code[D / 32], top = 0;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          code[j] = __ldg(sc + sl * (D / 32) + j);
-          bad = bad || code[j] == 255u;
-          top = max(top, code[j]);
+          for (int j = 0; j < D / 32; ++j) {
+            w[j] = __ldg(reinterpret_cast<const uint4*>(src) + j);
+            code[j] = __ldg(sc + j);
+          }
+          bool bad = false;
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            bad = bad || code[j] == 255u;
+            top = max(top, code[j]);
+          }
+          unit = bad ? NAN : p.scale_log2 * e8m0_value(top);
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            const float f = top - code[j] > 126u ? 0.f : pow2(int(code[j]) - int(top));
+            const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sts128(smem_u32(ks) + (j >> 1) * kPanel + swz(threadIdx.x, (j & 1) * 4 + i, 128), widen<T>(v[i], f));
+          }
         }
-        unit[i] = bad ? NAN : p.scale_log2 * e8m0_value(top);
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j)
-          a[j][i] = widen<T>(__ldg(reinterpret_cast<const uint32_t*>(src + 16 * j + 4 * t)),
-                             top - code[j] > 126u ? 0.f : pow2(int(code[j]) - int(top)));
-      } else {
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) a[j][i] = __ldg(reinterpret_cast<const uint4*>(src + 64 * j + 16 * t));
       }
+      if (!fresh) old = __ldg(score);
     }
-  }
-
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  int buf = 0;
-  for (int first = row0; first < nrows; first += kRows, buf ^= 1) {
-    cp_async_wait<0>();
-    __syncthreads();  // this block of rows is there, and everyone is done with the other buffer
-    if (first + kRows < nrows) stage(buf ^ 1, first + kRows);
-    const int tiles = (min(kRows, nrows - first) + 7) / 8;
+    if constexpr (FP4) {
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.k_full);
+    }
+    const uint32_t row = tmem + (uint32_t(warp) << 21);  // TMEM lane 32 * warp
+    float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+    const float2 unit2 = make_float2(unit, unit);
+    bool ok = true;
+    // a warp whose wait failed goes on to every barrier, so that none is left behind
     for (int n = 0; n < tiles; ++n) {
-      float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      const uint8_t* qr = qs[buf] + (8 * n + g) * kRowBytes;
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        const uint4 x = *reinterpret_cast<const uint4*>(qr + (((t + 4 * j) ^ ((g & 1) << 2)) << 4));
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const uint4 &u = a[j][2 * m], &v = a[j][2 * m + 1];
-          const uint32_t f0[4] = {u.x, v.x, u.y, v.y}, f1[4] = {u.z, v.z, u.w, v.w};
-          MmaOp<T>::run(acc[m], f0, x.x, x.y);
-          MmaOp<T>::run(acc[m], f1, x.z, x.w);
+      const int buf = n % nb, info = n & 1;
+      const int count = min(p.tile_queries, rq.nq - tok0 - n * p.tile_queries) * p.group;
+      {
+        const int c = threadIdx.x;
+        RowInfo o{0.f, 0.f, INT32_MAX};
+        if (c < count) {
+          o = row_info(p, rq, kvh, (tok0 + n * p.tile_queries) * p.group + c);
+          sh.last[info][c] = o.last;
         }
-      }
-      const float4 hr = *reinterpret_cast<const float4*>(&row_hi_r[buf][8 * n + 2 * t]);
-      const int2 last = *reinterpret_cast<const int2*>(&row_last[buf][8 * n + 2 * t]);
-      const bool all = __all_sync(0xffffffffu, min(last.x, last.y) >= key0 + 31);
+        float* pair = reinterpret_cast<float*>(&sh.pair[info][c >> 1]) + (c & 1);
+        pair[0] = c < count ? -o.hi : -INFINITY;  // past the last row a weight of 0
+        pair[2] = o.r;
+        // all rows see all keys of the tile: no comparisons below
+        const bool all = bar_and(1, kKeys, o.last >= ch.z - 1);
+        if (ok) {
+          ok = warp_wait(&sh.s_full[buf], uint32_t(n / nb) & 1u, p.st, forced, abort_flag);
+          if (!ok && lane == 0) *abort_flag = 1;
+        }
+        if (!ok) continue;
+        tc_fence_after();
+        for (int c0 = 0; c0 < count; c0 += 32) {
+          uint32_t s[32];
+          tmem_ld32(row + buf * 128 + c0, s);
+          tmem_ld_wait();
+          if (all && c0 + 32 <= count) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e0 = fast_exp2(fmaf(acc[i >> 1][2 * (i & 1)], unit[i], -hr.x));
-        const float e1 = fast_exp2(fmaf(acc[i >> 1][2 * (i & 1) + 1], unit[i], -hr.z));
-        const int key = key0 + 8 * i + g;
-        if (all || key <= last.x) sum[i] = fmaf(e0, hr.y, sum[i]);
-        if (all || key <= last.y) sum[i] = fmaf(e1, hr.w, sum[i]);
+            for (int i = 0; i < 16; ++i) {
+              const float4 hr = sh.pair[info][c0 / 2 + i];
+              const float2 x = ffma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), unit2,
+                                     make_float2(hr.x, hr.y));
+              sum[i & 1] = ffma2(make_float2(fast_exp2(x.x), fast_exp2(x.y)), make_float2(hr.z, hr.w), sum[i & 1]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int c1 = c0 + i;
+              if (c1 >= count) continue;
+              const float* hr = reinterpret_cast<const float*>(&sh.pair[info][c1 >> 1]) + (c1 & 1);
+              if (key <= sh.last[info][c1])
+                sum[0].x = fmaf(fast_exp2(fmaf(__uint_as_float(s[i]), unit, hr[0])), hr[2], sum[0].x);
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&sh.s_empty[buf]);
       }
     }
+    if (there && ok) {
+      const float w = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      *score = fresh ? w : fmaf(p.decay, old, w);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) sum[i] = quad_sum(sum[i]);
-  const float mine = t == 0 ? sum[0] : t == 1 ? sum[1] : t == 2 ? sum[2] : sum[3];
-  const int key = key0 + 8 * t + g;
-  if (key < ch.z) {
-    const int n = key / p.page_size, sl = key - n * p.page_size;
-    float* dst = p.scores + __ldg(pages + n) * p.w_s0 + kvh * p.w_s1 + sl;
-    const bool fresh = p.decay == 0.f || key >= rq.len - rq.nq;
-    *dst = fresh ? mine : fmaf(p.decay, *dst, mine);
-  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 4) tmem_dealloc(tmem, cols);
 }
 
 template <typename T, int D, int NT, bool FP4>
@@ -447,14 +554,38 @@ bskv_status launch_stream(const bskv_plan* plan, const WeightsParams& wp, cudaSt
 }
 
 template <typename T, int D, bool FP4>
-bskv_status launch(const bskv_plan* plan, const WeightsParams& wp, cudaStream_t st) {
+bskv_status launch_tile(const bskv_plan* plan, WeightsParams& wp, cudaStream_t st) {
+  const int ps = plan->page_size;
+  wp.box = ps % 128 == 0 ? 128 : ps % 64 == 0 ? 64 : ps % 32 == 0 ? 32 : ps % 16 == 0 ? 16 : 8;
+  wp.tile_queries = std::min(kKeys / wp.group, plan->q_len);
+  wp.buffers = plan->q_len > wp.tile_queries ? 2 : 1;
+  const CUtensorMapDataType dt = __is_same(T, __half) ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap qmap, kmap{};
+  const uint64_t qd[3] = {D, uint64_t(plan->num_qo_heads), uint64_t(plan->M)};
+  const uint64_t qst[2] = {uint64_t(wp.q_s1) * 2, uint64_t(wp.q_s0) * 2};
+  const uint32_t qb[3] = {64, uint32_t(wp.group), uint32_t(wp.tile_queries)};
+  if (bskv_status s = encode_tiled(&qmap, dt, 3, wp.q, qd, qst, qb, CU_TENSOR_MAP_SWIZZLE_128B)) return s;
+  if (!FP4) {
+    const uint64_t kd[5] = {D, uint64_t(ps), uint64_t(plan->num_kv_heads), 2, uint64_t(plan->num_pages)};
+    const uint64_t kst[4] = {uint64_t(wp.k_s3), uint64_t(wp.k_s2), uint64_t(wp.k_s1), uint64_t(wp.k_s0)};
+    const uint32_t kb[5] = {64, uint32_t(wp.box), 1, 1, 1};
+    if (bskv_status s = encode_tiled(&kmap, dt, 5, wp.keys, kd, kst, kb, CU_TENSOR_MAP_SWIZZLE_128B)) return s;
+  }
+  const size_t smem = 1024 + size_t(1 + wp.buffers) * (D / 64) * kPanel + sizeof(TileShared);
+  auto kern = weights_tile_kernel<T, D, FP4>;
+  static std::atomic<int> allowed[64];
+  if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "attn_weights: cudaFuncSetAttribute")) return s;
+  kern<<<dim3(unsigned(meta_word(plan, H_GRID)), unsigned(wp.num_kv_heads)), kTileThreads, smem, st>>>(qmap, kmap, wp);
+  return cuda_check(cudaGetLastError(), "attn_weights launch");
+}
+
+template <typename T, int D, bool FP4>
+bskv_status launch(const bskv_plan* plan, WeightsParams& wp, cudaStream_t st) {
   switch (meta_word(plan, H_VARIANT)) {
     case WEIGHTS_STREAM8: return launch_stream<T, D, 1, FP4>(plan, wp, st);
     case WEIGHTS_STREAM16: return launch_stream<T, D, 2, FP4>(plan, wp, st);
-    default: break;
+    default: return launch_tile<T, D, FP4>(plan, wp, st);
   }
-  weights_tile_kernel<T, D, FP4><<<dim3(unsigned(meta_word(plan, H_GRID)), unsigned(wp.num_kv_heads)), kKeys, 0, st>>>(wp);
-  return cuda_check(cudaGetLastError(), "attn_weights launch");
 }
 
 template <bool FP4>
@@ -463,7 +594,9 @@ bskv_status run(const char* who, const bskv_plan* plan, const void* q, const int
                 float sm_scale, WeightsParams& wp, cudaStream_t st) {
   if (!q || !q_strides || !lse || !scores || !scores_strides) { set_error("%s: NULL tensor", who); return BSKV_ERR_INVALID_ARG; }
   if (!aligned16(q) || !aligned16(scores)) { set_error("%s: tensors must be 16-byte aligned", who); return BSKV_ERR_INVALID_ARG; }
-  if (q_strides[0] % 8 || q_strides[1] % 8) { set_error("%s: q strides must be multiples of 8 elements", who); return BSKV_ERR_INVALID_ARG; }
+  for (int i = 0; i < 2; ++i) {
+    if (q_strides[i] <= 0 || q_strides[i] % 8) { set_error("%s: q strides must be positive multiples of 8 elements", who); return BSKV_ERR_INVALID_ARG; }
+  }
   for (int i = 0; i < 2; ++i) {
     if (scores_strides[i] <= 0 || scores_strides[i] % 4) {
       set_error("%s: scores stride %d (%lld) must be a positive multiple of 4 elements", who, i, (long long)scores_strides[i]);
@@ -487,6 +620,7 @@ bskv_status run(const char* who, const bskv_plan* plan, const void* q, const int
   wp.off_records = plan->walk_records;
   wp.decay = decay;
   wp.scale_log2 = sm_scale_log2(sm_scale, plan->head_dim);
+  if (bskv_status s = status_args(&wp.st)) return s;
   const bool bf = plan->dtype == BSKV_BF16;
   if (plan->head_dim == 128)
     return bf ? launch<__nv_bfloat16, 128, FP4>(plan, wp, st) : launch<__half, 128, FP4>(plan, wp, st);
@@ -522,7 +656,7 @@ extern "C" bskv_status bskv_run_attn_weights(const bskv_plan* plan, const void* 
   }
   WeightsParams wp{};
   wp.keys = static_cast<const uint8_t*>(kv_cache);
-  wp.k_s0 = 2 * kv_strides[0]; wp.k_s2 = 2 * kv_strides[2]; wp.k_s3 = 2 * kv_strides[3];
+  wp.k_s0 = 2 * kv_strides[0]; wp.k_s1 = 2 * kv_strides[1]; wp.k_s2 = 2 * kv_strides[2]; wp.k_s3 = 2 * kv_strides[3];
   return run<false>(who, plan, q, q_strides, lse, scores, scores_strides, decay, sm_scale, wp,
                     static_cast<cudaStream_t>(stream));
 }
@@ -541,7 +675,7 @@ extern "C" bskv_status bskv_run_attn_weights_fp4(const bskv_plan* plan, const vo
   if (bskv_status s = check_fp4_cache(who, kv_codes, codes_strides, kv_scales, scales_strides)) return s;
   WeightsParams wp{};
   wp.keys = static_cast<const uint8_t*>(kv_codes);
-  wp.k_s0 = codes_strides[0]; wp.k_s2 = codes_strides[2]; wp.k_s3 = codes_strides[3];
+  wp.k_s0 = codes_strides[0]; wp.k_s1 = codes_strides[1]; wp.k_s2 = codes_strides[2]; wp.k_s3 = codes_strides[3];
   wp.scales = static_cast<const uint8_t*>(kv_scales);
   wp.s_s0 = scales_strides[0]; wp.s_s2 = scales_strides[2];
   return run<true>(who, plan, q, q_strides, lse, scores, scores_strides, decay, sm_scale, wp,

@@ -725,8 +725,9 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
   if (bskv_status s = pages_once(who, "kv_indices", kv_indices, batch > 0 ? kv_indptr[batch] : 0, num_pages)) return s;
   if (batch > 0 && qo_indptr && qo_indptr[0] != 0) { set_error("%s: qo_indptr[0] must be 0", who); return BSKV_ERR_INVALID_ARG; }
   const int32_t group = num_qo_heads / num_kv_heads;
+  if (group > 128) { set_error("%s: %d query heads per kv head (max 128)", who, group); return BSKV_ERR_UNSUPPORTED; }
   std::vector<int32_t> queries;  // 3 per request
-  int64_t most = 0, total = 0;
+  int64_t most = 0, total = 0, longest = 0;
   for (int32_t b = 0; b < batch; ++b) {
     const int32_t q0 = qo_indptr ? qo_indptr[b] : b;
     const int64_t n = qo_indptr ? int64_t(qo_indptr[b + 1]) - q0 : 1;
@@ -734,6 +735,7 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
     if (n * group > INT32_MAX / 2) { set_error("%s: request %d has too many queries", who, b); return BSKV_ERR_UNSUPPORTED; }
     queries.insert(queries.end(), {q0, int32_t(n), int32_t(req[size_t(b)])});
     if (req[size_t(b)] > 0) most = std::max(most, n * group);
+    longest = std::max(longest, n);
     total += req[size_t(b)];
   }
   if (total > INT32_MAX / num_kv_heads || int64_t(batch) * num_kv_heads > INT32_MAX / 4) { set_error("%s: too many tokens", who); return BSKV_ERR_UNSUPPORTED; }
@@ -764,6 +766,8 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
   p->batch = batch; p->num_pages = num_pages; p->page_size = page_size;
   p->num_qo_heads = num_qo_heads; p->num_kv_heads = num_kv_heads; p->head_dim = head_dim;
   p->dtype = dtype; p->causal = causal ? 1 : 0;
+  p->M = batch == 0 ? 0 : qo_indptr ? qo_indptr[batch] : batch;
+  p->q_len = int32_t(longest);
   assemble(p, KIND_WEIGHTS, units, worker_ptr, chunks, 0, queries, kFp4Tile, kv_indptr,
            batch > 0 ? size_t(batch) + 1 : 0, kv_indices, batch > 0 ? size_t(kv_indptr[batch]) : 0,
            grid, variant);

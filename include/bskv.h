@@ -246,7 +246,8 @@ bskv_status bskv_plan_mla_paged(const int32_t* kv_indptr, const int32_t* kv_indi
  * Plan of the accumulated attention weights over a paged cache (16-bit or 4-bit).
  *   qo_indptr[batch+1] HOST int32: request b owns query tokens [qo_indptr[b], qo_indptr[b+1]),
  *   the last ones of its sequence; NULL: one query per request (the decode step). Page table,
- *   head counts, head_dim and page_size as for bskv_plan_decode_fp4 (any group size), dtype
+ *   head counts, head_dim and page_size as for bskv_plan_decode_fp4 (up to 128 query heads per
+ *   kv head), dtype
  *   (BSKV_BF16 or BSKV_FP16) is q's and a 16-bit cache's. causal: query t of request b (0-based)
  *   sees key j iff j <= t + L_b - qo_len_b. Pages listed twice are refused: their scores would
  *   have two writers.
