@@ -56,7 +56,7 @@ struct WeightsParams {
   float* scores;
   int64_t w_s0, w_s1;               // floats: page, kv head
   int num_kv_heads, group, page_size, num_qo_heads, causal;
-  int box, tile_queries, buffers;   // tile kernel: keys per TMA box, queries per product, S buffers
+  int box, tile_queries, buffers, num_items;  // tile kernel: keys per TMA box, queries per product, S buffers
   int off_workers, off_chunks, off_records, off_aux0, off_aux1, off_req, num_workers;
   float decay, scale_log2;
   StatusArgs st;
@@ -79,18 +79,21 @@ struct RowInfo {
   float hi, r;
   int last;
 };
-__device__ __forceinline__ RowInfo row_info(const WeightsParams& p, const Request& rq, int kvh, int row) {
+__device__ __forceinline__ RowInfo row_info(const WeightsParams& p, const Request& rq, float lse, int tok) {
   RowInfo o{0.f, 0.f, -1};
-  const int t = row / p.group;
-  if (t >= rq.nq) return o;
-  const float lse = __ldg(p.lse + int64_t(rq.qo + t) * p.num_qo_heads + kvh * p.group + (row - t * p.group));
   if (lse == -INFINITY) return o;
   constexpr float kLog2eLow = 1.925963033500011e-8f;  // log2 e - fp32(log2 e)
   o.hi = lse * kLog2e;
   const float lo = isinf(o.hi) ? 0.f : fmaf(lse, kLog2e, -o.hi) + lse * kLog2eLow;
   o.r = exp2f(-lo);
-  o.last = p.causal ? t + rq.len - rq.nq : INT32_MAX;
+  o.last = p.causal ? tok + rq.len - rq.nq : INT32_MAX;
   return o;
+}
+// Log-sum-exp of query row `row` (token, head of the group); -inf past the request's queries.
+__device__ __forceinline__ float row_lse(const WeightsParams& p, const Request& rq, int kvh, int row) {
+  const int t = row / p.group;
+  if (t >= rq.nq) return -INFINITY;
+  return __ldg(p.lse + int64_t(rq.qo + t) * p.num_qo_heads + kvh * p.group + (row - t * p.group));
 }
 
 __device__ __forceinline__ float quad_sum(float x) {
@@ -155,7 +158,8 @@ __device__ __forceinline__ void load_rows(const WeightsParams& p, const Request&
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       s.c[2 * nt + e] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4 * e);
-      s.info[2 * nt + e] = row_info(p, rq, kvh, 8 * nt + 2 * t + e);
+      const int r = 8 * nt + 2 * t + e;
+      s.info[2 * nt + e] = row_info(p, rq, row_lse(p, rq, kvh, r), r / p.group);
     }
   }
 }
@@ -322,15 +326,43 @@ __device__ __forceinline__ uint4 widen(uint32_t w, float f) {
 struct TileShared {
   float4 pair[2][64];  // of query rows 2 i and 2 i + 1: {-hi, -hi, r, r}
   int last[2][128];
-  uint64_t k_full, q_full[2], q_empty[2], s_full[2], s_empty[2];
+  uint64_t k_full, k_empty, q_full[2], q_empty[2], s_full[2], s_empty[2];
   uint32_t tmem;
   int abort;
 };
 
+// An item of the tile kernel: 128 keys of a request (a record of the plan) for one kv head.
+struct TileItem {
+  int begin, end, pbase, kvh, tok0, tiles;
+  Request rq;
+};
+__device__ __forceinline__ TileItem tile_item(const WeightsParams& p, int i) {
+  TileItem t;
+  const int c = i / p.num_kv_heads;
+  const int4 a = __ldg(reinterpret_cast<const int4*>(p.meta + p.off_records) + 2 * c);
+  const int4 r = __ldg(reinterpret_cast<const int4*>(p.meta + p.off_records) + 2 * c + 1);
+  t.kvh = i - c * p.num_kv_heads;
+  t.begin = a.y;
+  t.end = a.z;
+  t.pbase = a.w;
+  t.rq = Request{r.x, r.y, r.z};
+  // causal: the first query that sees the first key
+  t.tok0 = p.causal ? max(0, t.begin - (t.rq.len - t.rq.nq)) : 0;
+  t.tiles = t.tok0 < t.rq.nq ? (t.rq.nq - t.tok0 + p.tile_queries - 1) / p.tile_queries : 0;
+  return t;
+}
+
 constexpr int kTileThreads = kKeys + 32;  // a thread per key, and the warp that copies and multiplies
 
+// A 4-bit key's row and scales on their way to shared memory.
+template <int D>
+struct Row4 {
+  uint4 w[D / 32];
+  uint32_t code[D / 32];
+};
+
 template <typename T, int D, bool FP4>
-__global__ void __launch_bounds__(kTileThreads)
+__global__ void __launch_bounds__(kTileThreads, D == 128 ? 3 : 4)
     weights_tile_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ WeightsParams p) {
   constexpr int kPanels = D / 64;
@@ -339,18 +371,11 @@ __global__ void __launch_bounds__(kTileThreads)
   uint8_t* qs = ks + kPanels * kPanel;
   TileShared& sh = *reinterpret_cast<TileShared*>(qs + p.buffers * kPanels * kPanel);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = blockIdx.y;
-  const int4 ch = __ldg(reinterpret_cast<const int4*>(p.meta + p.off_chunks) + blockIdx.x);
-  const int b = ch.x;  // {request, first key, end key, 0}
-  const Request rq = request_of(p, b);
-  const int32_t* pages = p.meta + p.off_aux1 + __ldg(p.meta + p.off_aux0 + b);
-  // causal: the first query that sees the tile's first key
-  const int tok0 = p.causal ? max(0, ch.y - (rq.len - rq.nq)) : 0;
-  const int tiles = tok0 < rq.nq ? (rq.nq - tok0 + p.tile_queries - 1) / p.tile_queries : 0;
   const int nb = p.buffers;
   const uint32_t cols = nb > 1 ? 256 : 128;
   if (threadIdx.x == 0) {
     mbar_init(&sh.k_full, FP4 ? kKeys : 1);
+    mbar_init(&sh.k_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
@@ -372,169 +397,239 @@ __global__ void __launch_bounds__(kTileThreads)
   volatile int* abort_flag = &sh.abort;
 
   if (warp == 4) {
-    // The warp stays converged; one lane's copies and products are executed.
+    // The warp stays converged; one lane's copies and products are executed. K and the queries of
+    // an item are copied as soon as the product before has read theirs, under its exponentials.
     const uint32_t leader = elect_leader();
     bool ok = true;
-    if (!FP4 && tiles > 0) {
-      const uint64_t once = l2_evict_first_policy();
-      const int boxes = (ch.z - ch.y + p.box - 1) / p.box;  // at most 16
-      int page = 0, slot = 0;
-      if (lane < boxes) {
-        const int t = ch.y + lane * p.box, n = t / p.page_size;
-        page = __ldg(pages + n);
-        slot = t - n * p.page_size;
-      }
-      mbar_arrive_expect_tx_w(leader, &sh.k_full, uint32_t(boxes) * kPanels * p.box * 128);
-      for (int i = 0; i < boxes; ++i) {
-        const int pg = __shfl_sync(0xffffffffu, page, i), sl = __shfl_sync(0xffffffffu, slot, i);
-#pragma unroll
-        for (int pn = 0; pn < kPanels; ++pn)
-          tma_load_5d_hint_w(leader, ks + pn * kPanel + i * p.box * 128, &kmap, pn * 64, sl, kvh, 0, pg, &sh.k_full, once);
-      }
-    }
-    const uint64_t again = l2_evict_last_policy();  // every tile of the request reads its queries
-    auto load_q = [&](int n) {
-      const int buf = n % nb;
-      mbar_arrive_expect_tx_w(leader, &sh.q_full[buf], uint32_t(kPanels) * p.tile_queries * p.group * 128);
-#pragma unroll
-      for (int pn = 0; pn < kPanels; ++pn)
-        tma_load_3d_hint_w(leader, qs + (buf * kPanels + pn) * kPanel, &qmap, pn * 64, kvh * p.group,
-                           rq.qo + tok0 + n * p.tile_queries, &sh.q_full[buf], again);
-    };
-    int loaded = 0, done = 0;  // query tiles copied, products issued
-    for (; loaded < nb && loaded < tiles; ++loaded) load_q(loaded);
+    const uint64_t once = l2_evict_first_policy(), again = l2_evict_last_policy();
     const uint32_t fmt = __is_same(T, __half) ? 0u : 1u;
     const uint32_t idesc = umma_idesc(128, uint32_t((p.tile_queries * p.group + 15) & ~15), fmt, fmt, 0, 0);
     const uint64_t dk = umma_desc(smem_u32(ks), 16, 1024, kSwz128), dq = umma_desc(smem_u32(qs), 16, 1024, kSwz128);
-    for (int n = 0; n < tiles && ok; ++n) {
-      const int buf = n % nb;
-      const uint32_t use = uint32_t(n / nb);
-      ok = (n > 0 || issuer_wait(&sh.k_full, 0, p.st, forced, abort_flag)) &&
-           issuer_wait(&sh.q_full[buf], use & 1u, p.st, forced, abort_flag) &&
-           (n < nb || issuer_wait(&sh.s_empty[buf], (use - 1) & 1u, p.st, forced, abort_flag));
-      if (!ok) break;
-      tc_fence_after();
+    int page = 0, slot = 0;  // of the lane's box of the item
+    auto lookup = [&](const TileItem& t) {
+      const int key = t.begin + lane * p.box;  // at most 16 boxes
+      if (!FP4 && t.tiles > 0 && lane * p.box < kKeys && key < t.end) {
+        const int n = key / p.page_size;
+        page = __ldg(p.meta + p.off_aux1 + t.pbase + n);
+        slot = key - n * p.page_size;
+      }
+    };
+    int kc = 0, loaded = 0, done = 0;  // K tiles, query tiles copied, products issued
+    TileItem t = tile_item(p, blockIdx.x);
+    lookup(t);
+    for (int i = blockIdx.x; i < p.num_items && ok; i += gridDim.x) {
+      TileItem next = t;
+      if (i + int(gridDim.x) < p.num_items) next = tile_item(p, i + gridDim.x);
+      if (t.tiles > 0) {
+        ok = kc == 0 || issuer_wait(&sh.k_empty, uint32_t(kc - 1) & 1u, p.st, forced, abort_flag);
+        if (!ok) break;
+        if constexpr (!FP4) {
+          const int boxes = (t.end - t.begin + p.box - 1) / p.box;
+          mbar_arrive_expect_tx_w(leader, &sh.k_full, uint32_t(boxes) * kPanels * p.box * 128);
+          for (int x = 0; x < boxes; ++x) {
+            const int pg = __shfl_sync(0xffffffffu, page, x), sl = __shfl_sync(0xffffffffu, slot, x);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t at = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
-        umma_f16_w(leader, tmem + buf * 128, dk + at, dq + ((buf * kPanels * kPanel) >> 4) + at, idesc, kk > 0 ? 1u : 0u);
+            for (int pn = 0; pn < kPanels; ++pn)
+              tma_load_5d_hint_w(leader, ks + pn * kPanel + x * p.box * 128, &kmap, pn * 64, sl, t.kvh, 0, pg,
+                                 &sh.k_full, once);
+          }
+        }
+        ++kc;
+        auto load_q = [&](int n) {  // query tile n of the item
+          const int buf = loaded % nb;
+          if (loaded >= nb && !issuer_wait(&sh.q_empty[buf], uint32_t(loaded / nb - 1) & 1u, p.st, forced, abort_flag))
+            return false;
+          mbar_arrive_expect_tx_w(leader, &sh.q_full[buf], uint32_t(kPanels) * p.tile_queries * p.group * 128);
+#pragma unroll
+          for (int pn = 0; pn < kPanels; ++pn)
+            tma_load_3d_hint_w(leader, qs + (buf * kPanels + pn) * kPanel, &qmap, pn * 64, t.kvh * p.group,
+                               t.rq.qo + t.tok0 + n * p.tile_queries, &sh.q_full[buf], again);
+          ++loaded;
+          return true;
+        };
+        int nq = 0;  // query tiles of the item copied
+        for (; nq < nb && nq < t.tiles && ok; ++nq) ok = load_q(nq);
+        for (int n = 0; n < t.tiles && ok; ++n) {
+          const int buf = done % nb;
+          const uint32_t use = uint32_t(done / nb);
+          ok = (n > 0 || issuer_wait(&sh.k_full, uint32_t(kc - 1) & 1u, p.st, forced, abort_flag)) &&
+               issuer_wait(&sh.q_full[buf], use & 1u, p.st, forced, abort_flag) &&
+               (done < nb || issuer_wait(&sh.s_empty[buf], (use - 1) & 1u, p.st, forced, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t at = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+            umma_f16_w(leader, tmem + buf * 128, dk + at, dq + ((buf * kPanels * kPanel) >> 4) + at, idesc, kk > 0 ? 1u : 0u);
+          }
+          umma_commit_w(leader, &sh.s_full[buf]);
+          umma_commit_w(leader, &sh.q_empty[buf]);
+          if (n == t.tiles - 1) umma_commit_w(leader, &sh.k_empty);
+          ++done;
+          if (nq < t.tiles) {
+            ok = load_q(nq);
+            ++nq;
+          }
+        }
       }
-      umma_commit_w(leader, &sh.s_full[buf]);
-      umma_commit_w(leader, &sh.q_empty[buf]);
-      done = n + 1;
-      if (loaded < tiles) {
-        ok = issuer_wait(&sh.q_empty[buf], use & 1u, p.st, forced, abort_flag);
-        if (ok) load_q(loaded++);
-      }
+      t = next;
+      lookup(t);
     }
     if (!ok) {
       // copies and products in flight land before the CTA leaves (bounded, not forcible)
       *abort_flag = 1;
       if (done > 0) mbar_wait(&sh.s_full[(done - 1) % nb], uint32_t((done - 1) / nb) & 1u, p.st, false);
-      if (!FP4) mbar_wait(&sh.k_full, 0, p.st, false);
+      if (!FP4 && kc > 0) mbar_wait(&sh.k_full, uint32_t(kc - 1) & 1u, p.st, false);
       for (int n = max(0, loaded - nb); n < loaded; ++n) mbar_wait(&sh.q_full[n % nb], (n / nb) & 1u, p.st, false);
     }
   } else {
-    const int key = ch.y + int(threadIdx.x);
-    const bool there = key < ch.z;
-    float unit = p.scale_log2;
-    float* score = nullptr;
-    float old = 0.f;
-    const bool fresh = p.decay == 0.f || key >= rq.len - rq.nq;
-    if (there) {
-      const int n = key / p.page_size, sl = key - n * p.page_size;
-      const int64_t pg = __ldg(pages + n);
-      score = p.scores + pg * p.w_s0 + kvh * p.w_s1 + sl;
-      if constexpr (FP4) {
-        if (tiles > 0) {
-          const uint8_t* src = p.keys + pg * p.k_s0 + kvh * p.k_s2 + sl * p.k_s3;
-          const uint8_t* sc = p.scales + pg * p.s_s0 + kvh * p.s_s2 + sl * (D / 32);
-          uint4 w[D / 32];
-          uint32_t code[D / 32], top = 0;
+    // What an item needs from memory is read an item ahead: its record two ahead, then the page of
+    // the thread's key, the key's score, and a 4-bit key's row.
+    const uint32_t row = tmem + (uint32_t(warp) << 21);  // TMEM lane 32 * warp
+    auto page_of = [&](const TileItem& t) {
+      const int key = t.begin + int(threadIdx.x);
+      return key < t.end ? __ldg(p.meta + p.off_aux1 + t.pbase + key / p.page_size) : 0;
+    };
+    auto score_at = [&](const TileItem& t, int page) {
+      const int key = t.begin + int(threadIdx.x);
+      return p.scores + page * p.w_s0 + t.kvh * p.w_s1 + key % p.page_size;
+    };
+    auto is_fresh = [&](const TileItem& t) { return p.decay == 0.f || t.begin + int(threadIdx.x) >= t.rq.len - t.rq.nq; };
+    auto old_score = [&](const TileItem& t, const float* at) {
+      return t.begin + int(threadIdx.x) < t.end && !is_fresh(t) ? __ldg(at) : 0.f;
+    };
+    auto lse_of = [&](const TileItem& t, int n) {  // of row threadIdx.x of query tile n
+      const int r = (t.tok0 + n * p.tile_queries) * p.group + int(threadIdx.x), tok = r / p.group;
+      if (n >= t.tiles || int(threadIdx.x) >= p.tile_queries * p.group || tok >= t.rq.nq) return -INFINITY;
+      return __ldg(p.lse + int64_t(t.rq.qo + tok) * p.num_qo_heads + t.kvh * p.group + (r - tok * p.group));
+    };
+    auto read_row = [&](const TileItem& t, int page) {
+      Row4<D> x{};
+      const int key = t.begin + int(threadIdx.x), sl = key % p.page_size;
+      if (t.tiles > 0 && key < t.end) {
+        const uint8_t* src = p.keys + page * p.k_s0 + t.kvh * p.k_s2 + sl * p.k_s3;
+        const uint8_t* sc = p.scales + page * p.s_s0 + t.kvh * p.s_s2 + sl * (D / 32);
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            w[j] = __ldg(reinterpret_cast<const uint4*>(src) + j);
-            code[j] = __ldg(sc + j);
-          }
-          bool bad = false;
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            bad = bad || code[j] == 255u;
-            top = max(top, code[j]);
-          }
-          unit = bad ? NAN : p.scale_log2 * e8m0_value(top);
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            const float f = top - code[j] > 126u ? 0.f : pow2(int(code[j]) - int(top));
-            const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              sts128(smem_u32(ks) + (j >> 1) * kPanel + swz(threadIdx.x, (j & 1) * 4 + i, 128), widen<T>(v[i], f));
-          }
+        for (int j = 0; j < D / 32; ++j) {
+          x.w[j] = __ldg(reinterpret_cast<const uint4*>(src) + j);
+          x.code[j] = __ldg(sc + j);
         }
       }
-      if (!fresh) old = __ldg(score);
-    }
-    if constexpr (FP4) {
+      return x;
+    };
+    // The row as T relative to its largest scale into shared memory; what multiplies its products.
+    auto put_row = [&](const Row4<D>& x) {
+      uint32_t top = 0;
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        bad = bad || x.code[j] == 255u;
+        top = max(top, x.code[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const float f = top - x.code[j] > 126u ? 0.f : pow2(int(x.code[j]) - int(top));
+        const uint32_t v[4] = {x.w[j].x, x.w[j].y, x.w[j].z, x.w[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sts128(smem_u32(ks) + (j >> 1) * kPanel + swz(threadIdx.x, (j & 1) * 4 + i, 128), widen<T>(v[i], f));
+      }
       fence_proxy_async_smem();
       mbar_arrive(&sh.k_full);
-    }
-    const uint32_t row = tmem + (uint32_t(warp) << 21);  // TMEM lane 32 * warp
-    float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-    const float2 unit2 = make_float2(unit, unit);
+      return bad ? NAN : p.scale_log2 * e8m0_value(top);
+    };
+
     bool ok = true;
-    // a warp whose wait failed goes on to every barrier, so that none is left behind
-    for (int n = 0; n < tiles; ++n) {
-      const int buf = n % nb, info = n & 1;
-      const int count = min(p.tile_queries, rq.nq - tok0 - n * p.tile_queries) * p.group;
-      {
+    int done = 0;
+    TileItem t = tile_item(p, blockIdx.x), next = t;
+    const bool two = int(blockIdx.x) + int(gridDim.x) < p.num_items;
+    if (two) next = tile_item(p, blockIdx.x + gridDim.x);
+    int page = page_of(t);
+    float* score = score_at(t, page);
+    float old = old_score(t, score), lse = lse_of(t, 0), unit = p.scale_log2, next_unit = unit;
+    if constexpr (FP4) {
+      if (t.tiles > 0) unit = put_row(read_row(t, page));
+    }
+    for (int i = blockIdx.x; i < p.num_items; i += gridDim.x) {
+      const int key = t.begin + int(threadIdx.x);
+      const bool more = i + int(gridDim.x) < p.num_items;
+      TileItem after = next;
+      if (i + 2 * int(gridDim.x) < p.num_items) after = tile_item(p, i + 2 * gridDim.x);
+      const int next_page = more ? page_of(next) : 0;
+      float* next_score = score_at(next, next_page);
+      float next_old = 0.f;
+      Row4<D> ahead;
+      if constexpr (FP4) {
+        if (more) ahead = read_row(next, next_page);
+      }
+      float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+      const float2 unit2 = make_float2(unit, unit);
+      // a warp whose wait failed goes on to every barrier, so that none is left behind
+      for (int n = 0; n < t.tiles; ++n, ++done) {
+        const int buf = done % nb, info = done & 1;
+        const int count = min(p.tile_queries, t.rq.nq - t.tok0 - n * p.tile_queries) * p.group;
         const int c = threadIdx.x;
-        RowInfo o{0.f, 0.f, INT32_MAX};
-        if (c < count) {
-          o = row_info(p, rq, kvh, (tok0 + n * p.tile_queries) * p.group + c);
-          sh.last[info][c] = o.last;
-        }
+        const RowInfo o = row_info(p, t.rq, lse, (t.tok0 + n * p.tile_queries) + c / p.group);
+        sh.last[info][c] = o.last;
         float* pair = reinterpret_cast<float*>(&sh.pair[info][c >> 1]) + (c & 1);
-        pair[0] = c < count ? -o.hi : -INFINITY;  // past the last row a weight of 0
+        pair[0] = -o.hi;
         pair[2] = o.r;
+        lse = n + 1 < t.tiles ? lse_of(t, n + 1) : more ? lse_of(next, 0) : 0.f;
         // all rows see all keys of the tile: no comparisons below
-        const bool all = bar_and(1, kKeys, o.last >= ch.z - 1);
+        const bool all = bar_and(1, kKeys, c >= count || o.last >= t.end - 1);
         if (ok) {
-          ok = warp_wait(&sh.s_full[buf], uint32_t(n / nb) & 1u, p.st, forced, abort_flag);
+          ok = warp_wait(&sh.s_full[buf], uint32_t(done / nb) & 1u, p.st, forced, abort_flag);
           if (!ok && lane == 0) *abort_flag = 1;
         }
         if (!ok) continue;
         tc_fence_after();
+        if (n == t.tiles - 1) {
+          if constexpr (FP4) {
+            if (more && next.tiles > 0) next_unit = put_row(ahead);  // the product has read this item's keys
+          }
+        }
         for (int c0 = 0; c0 < count; c0 += 32) {
           uint32_t s[32];
           tmem_ld32(row + buf * 128 + c0, s);
           tmem_ld_wait();
           if (all && c0 + 32 <= count) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float4 hr = sh.pair[info][c0 / 2 + i];
-              const float2 x = ffma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), unit2,
+            for (int j = 0; j < 16; ++j) {
+              const float4 hr = sh.pair[info][c0 / 2 + j];
+              const float2 x = ffma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), unit2,
                                      make_float2(hr.x, hr.y));
-              sum[i & 1] = ffma2(make_float2(fast_exp2(x.x), fast_exp2(x.y)), make_float2(hr.z, hr.w), sum[i & 1]);
+              sum[j & 1] = ffma2(make_float2(fast_exp2(x.x), fast_exp2(x.y)), make_float2(hr.z, hr.w), sum[j & 1]);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int c1 = c0 + i;
+            for (int j = 0; j < 32; ++j) {
+              const int c1 = c0 + j;
               if (c1 >= count) continue;
               const float* hr = reinterpret_cast<const float*>(&sh.pair[info][c1 >> 1]) + (c1 & 1);
               if (key <= sh.last[info][c1])
-                sum[0].x = fmaf(fast_exp2(fmaf(__uint_as_float(s[i]), unit, hr[0])), hr[2], sum[0].x);
+                sum[0].x = fmaf(fast_exp2(fmaf(__uint_as_float(s[j]), unit, hr[0])), hr[2], sum[0].x);
             }
           }
         }
         tc_fence_before();
         mbar_arrive(&sh.s_empty[buf]);
       }
-    }
-    if (there && ok) {
-      const float w = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      *score = fresh ? w : fmaf(p.decay, old, w);
+      if (t.tiles == 0) {  // no query sees these keys: the scores only fade
+        lse = more ? lse_of(next, 0) : 0.f;
+        if constexpr (FP4) {
+          if (more && next.tiles > 0 && ok) next_unit = put_row(ahead);
+        }
+      }
+      if (more) next_old = old_score(next, next_score);
+      if (key < t.end && ok) {
+        const float w = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        *score = is_fresh(t) ? w : fmaf(p.decay, old, w);
+      }
+      t = next;
+      next = after;
+      score = next_score;
+      old = next_old;
+      unit = next_unit;
     }
   }
   tc_fence_before();
@@ -575,7 +670,11 @@ bskv_status launch_tile(const bskv_plan* plan, WeightsParams& wp, cudaStream_t s
   auto kern = weights_tile_kernel<T, D, FP4>;
   static std::atomic<int> allowed[64];
   if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "attn_weights: cudaFuncSetAttribute")) return s;
-  kern<<<dim3(unsigned(meta_word(plan, H_GRID)), unsigned(wp.num_kv_heads)), kTileThreads, smem, st>>>(qmap, kmap, wp);
+  // as many CTAs as the GPU holds: by shared memory and by TMEM (128 columns a buffer)
+  const int per_sm = wp.buffers > 1 ? 2 : D == 128 ? 3 : 4;
+  wp.num_items = meta_word(plan, H_UNITS);
+  const int grid = std::min(wp.num_items, plan->num_sms * per_sm);
+  kern<<<grid, kTileThreads, smem, st>>>(qmap, kmap, wp);
   return cuda_check(cudaGetLastError(), "attn_weights launch");
 }
 

@@ -196,7 +196,8 @@ struct bskv_plan {
   // page-major decode: word offset in the metadata of the per-worker start records
   // (kDecodeStartWords each), or -1
   int32_t decode_starts = -1;
-  int32_t walk_records = -1;  // word offset of the walk records, or -1
+  int32_t walk_records = -1;  // word offset of the walk records (tile records), or -1
+  int32_t num_sms = 0;        // attn_weights: SM count of the target GPU
   // evict: tokens that stay over all requests, protected first / last tokens, the longest
   // request, whether the kept rows stay in their pages, CTAs that share the rows of one slice
   int64_t kept_total = 0;

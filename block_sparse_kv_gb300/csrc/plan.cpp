@@ -758,11 +758,13 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
     for (int32_t b = 0; b < batch; ++b)
       for (int64_t t = 0; t < req[size_t(b)]; t += kWeightsKeys)
         chunks.push_back(Chunk{b, int32_t(t), int32_t(std::min<int64_t>(t + kWeightsKeys, req[size_t(b)])), 0});
+    if (int64_t(chunks.size()) * num_kv_heads > INT32_MAX / 2) { set_error("%s: too many tokens", who); return BSKV_ERR_UNSUPPORTED; }
     grid = int32_t(chunks.size());
-    units = grid;
+    units = grid * num_kv_heads;
   }
   bskv_plan* p = new bskv_plan();
   p->kind = KIND_WEIGHTS;
+  p->num_sms = num_sms;
   p->batch = batch; p->num_pages = num_pages; p->page_size = page_size;
   p->num_qo_heads = num_qo_heads; p->num_kv_heads = num_kv_heads; p->head_dim = head_dim;
   p->dtype = dtype; p->causal = causal ? 1 : 0;
@@ -771,7 +773,15 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
   assemble(p, KIND_WEIGHTS, units, worker_ptr, chunks, 0, queries, kFp4Tile, kv_indptr,
            batch > 0 ? size_t(batch) + 1 : 0, kv_indices, batch > 0 ? size_t(kv_indptr[batch]) : 0,
            grid, variant);
-  if (variant != WEIGHTS_TILE) add_walk_records(p, worker_ptr, chunks, no_merges, kv_indptr, num_kv_heads);
+  if (variant != WEIGHTS_TILE) {
+    add_walk_records(p, worker_ptr, chunks, no_merges, kv_indptr, num_kv_heads);
+  } else {  // {request, first, end, its kv_indptr, its first query, queries, tokens, 0} per tile
+    p->walk_records = int32_t(p->meta.size());
+    for (const Chunk& c : chunks)
+      p->meta.insert(p->meta.end(), {c.unit, c.a, c.b, kv_indptr[c.unit], queries[size_t(3 * c.unit)],
+                                     queries[size_t(3 * c.unit + 1)], queries[size_t(3 * c.unit + 2)], 0});
+    p->meta[H_TOTAL] = int32_t(p->meta.size());
+  }
   *out_plan = p;
   log_plan("bskv_plan_attn_weights", p);
   return BSKV_OK;
