@@ -55,8 +55,9 @@ struct WeightsParams {
   const float* lse;
   float* scores;
   int64_t w_s0, w_s1;               // floats: page, kv head
-  int num_kv_heads, group, page_size, num_qo_heads, causal;
-  int box, tile_queries, buffers, num_items;  // tile kernel: keys per TMA box, queries per product, S buffers
+  int num_kv_heads, group, num_qo_heads, causal;
+  FastDiv heads, groups, page_size, queries;
+  int box, tile_queries, buffers, num_items, num_requests;  // tile kernel: keys per TMA box, queries per product, S buffers
   int off_workers, off_chunks, off_records, off_aux0, off_aux1, off_req, num_workers;
   float decay, scale_log2;
   StatusArgs st;
@@ -91,9 +92,10 @@ __device__ __forceinline__ RowInfo row_info(const WeightsParams& p, const Reques
 }
 // Log-sum-exp of query row `row` (token, head of the group); -inf past the request's queries.
 __device__ __forceinline__ float row_lse(const WeightsParams& p, const Request& rq, int kvh, int row) {
-  const int t = row / p.group;
+  int head;
+  const int t = p.groups.divmod(row, head);
   if (t >= rq.nq) return -INFINITY;
-  return __ldg(p.lse + int64_t(rq.qo + t) * p.num_qo_heads + kvh * p.group + (row - t * p.group));
+  return __ldg(p.lse + int64_t(rq.qo + t) * p.num_qo_heads + kvh * p.group + head);
 }
 
 __device__ __forceinline__ float quad_sum(float x) {
@@ -138,7 +140,7 @@ __device__ __forceinline__ void load_rows(const WeightsParams& p, const Request&
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int row = 8 * nt + g, tok = row / p.group;
+    const int row = 8 * nt + g, tok = p.groups.div(row);
     const bool live = tok < rq.nq;
     const T* src = static_cast<const T*>(p.q) + int64_t(rq.qo + tok) * p.q_s0 +
                    (int64_t(kvh) * p.group + (row - tok * p.group)) * p.q_s1;
@@ -159,7 +161,7 @@ __device__ __forceinline__ void load_rows(const WeightsParams& p, const Request&
     for (int e = 0; e < 2; ++e) {
       s.c[2 * nt + e] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4 * e);
       const int r = 8 * nt + 2 * t + e;
-      s.info[2 * nt + e] = row_info(p, rq, row_lse(p, rq, kvh, r), r / p.group);
+      s.info[2 * nt + e] = row_info(p, rq, row_lse(p, rq, kvh, r), p.groups.div(r));
     }
   }
 }
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm(D, FP4))
   if (w >= p.num_workers) return;
   const int c0 = __ldg(p.meta + p.off_workers + w), nck = __ldg(p.meta + p.off_workers + w + 1) - c0;
   const int32_t* records = p.meta + p.off_records + c0 * kWalkWords;
-  PageWalk walk(records, nck, p.meta + p.off_aux1, p.num_kv_heads, p.page_size, lane);
+  PageWalk walk(records, nck, p.meta + p.off_aux1, p.heads, p.page_size, lane);
   const bool old = p.decay != 0.f;
 
   constexpr int kStep = 32 / Sh::kParts;  // rows one copy instruction of the warp covers
@@ -268,7 +270,8 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm(D, FP4))
   int done = 0;
   for (int k = 0; k < nck; ++k) {
     const WalkChunk ch = walk_chunk(records, k);
-    const int b = ch.unit / p.num_kv_heads, kvh = ch.unit - b * p.num_kv_heads;
+    int kvh;
+    const int b = p.heads.divmod(ch.unit, kvh);
     const Request rq = request_of(p, b);
     load_rows<T, D, NT, FP4>(p, rq, kvh, lane, s);
     for (int at = ch.begin; at < ch.end; at += kTile, ++done) {
@@ -326,29 +329,61 @@ __device__ __forceinline__ uint4 widen(uint32_t w, float f) {
 struct TileShared {
   float4 pair[2][64];  // of query rows 2 i and 2 i + 1: {-hi, -hi, r, r}
   int last[2][128];
-  uint64_t k_full, k_empty, q_full[2], q_empty[2], s_full[2], s_empty[2];
+  uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], s_full[2], s_empty[2];
   uint32_t tmem;
   int abort;
 };
 
-// An item of the tile kernel: 128 keys of a request (a record of the plan) for one kv head.
+// An item of the tile kernel: 128 keys of a request for one kv head. Items are numbered by request,
+// head, then keys, and a CTA takes a contiguous range: its queries mostly stay the same.
 struct TileItem {
-  int begin, end, pbase, kvh, tok0, tiles;
+  int r, kvh, c;              // request record, kv head, which 128 keys
+  int begin, end, pbase, tok0, tiles;
   Request rq;
+  int tiles_of_keys;          // of the request
 };
-__device__ __forceinline__ TileItem tile_item(const WeightsParams& p, int i) {
-  TileItem t;
-  const int c = i / p.num_kv_heads;
-  const int4 a = __ldg(reinterpret_cast<const int4*>(p.meta + p.off_records) + 2 * c);
-  const int4 r = __ldg(reinterpret_cast<const int4*>(p.meta + p.off_records) + 2 * c + 1);
-  t.kvh = i - c * p.num_kv_heads;
-  t.begin = a.y;
-  t.end = a.z;
-  t.pbase = a.w;
-  t.rq = Request{r.x, r.y, r.z};
+// Record of request r of the plan: {first item, 128-key tiles, tokens, kv_indptr, first query, queries}.
+__device__ __forceinline__ void place_item(const WeightsParams& p, TileItem& t) {
+  t.begin = t.c * kKeys;
+  t.end = min(t.begin + kKeys, t.rq.len);
   // causal: the first query that sees the first key
   t.tok0 = p.causal ? max(0, t.begin - (t.rq.len - t.rq.nq)) : 0;
-  t.tiles = t.tok0 < t.rq.nq ? (t.rq.nq - t.tok0 + p.tile_queries - 1) / p.tile_queries : 0;
+  t.tiles = t.tok0 < t.rq.nq ? p.queries.div(t.rq.nq - t.tok0 + p.tile_queries - 1) : 0;
+}
+__device__ __forceinline__ void open_request(const WeightsParams& p, TileItem& t) {
+  const int4 a = __ldg(reinterpret_cast<const int4*>(p.meta + p.off_records) + 2 * t.r);
+  const int4 q = __ldg(reinterpret_cast<const int4*>(p.meta + p.off_records) + 2 * t.r + 1);
+  t.tiles_of_keys = a.y;
+  t.pbase = a.w;
+  t.rq = Request{q.x, q.y, a.z};
+}
+__device__ __forceinline__ TileItem find_item(const WeightsParams& p, int i) {
+  int lo = 0, hi = p.num_requests;  // the last record whose first item is at most i
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.meta + p.off_records + kWalkWords * mid) <= i) lo = mid;
+    else hi = mid;
+  }
+  TileItem t;
+  t.r = lo;
+  open_request(p, t);
+  const int rest = i - __ldg(p.meta + p.off_records + kWalkWords * lo);
+  t.kvh = rest / t.tiles_of_keys;
+  t.c = rest - t.kvh * t.tiles_of_keys;
+  place_item(p, t);
+  return t;
+}
+// The item after t, which exists.
+__device__ __forceinline__ TileItem next_item(const WeightsParams& p, TileItem t) {
+  if (++t.c == t.tiles_of_keys) {
+    t.c = 0;
+    if (++t.kvh == p.num_kv_heads) {
+      t.kvh = 0;
+      ++t.r;
+      open_request(p, t);
+    }
+  }
+  place_item(p, t);
   return t;
 }
 
@@ -362,21 +397,21 @@ struct Row4 {
 };
 
 template <typename T, int D, bool FP4>
-__global__ void __launch_bounds__(kTileThreads, D == 128 ? 3 : 4)
+__global__ void __launch_bounds__(kTileThreads, D == 128 ? 2 : 3)
     weights_tile_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ WeightsParams p) {
   constexpr int kPanels = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ks = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* qs = ks + kPanels * kPanel;
-  TileShared& sh = *reinterpret_cast<TileShared*>(qs + p.buffers * kPanels * kPanel);
+  const int nb = p.buffers, nk = 3 - nb;  // buffers of queries and products; of keys
+  uint8_t* qs = ks + nk * kPanels * kPanel;
+  TileShared& sh = *reinterpret_cast<TileShared*>(qs + nb * kPanels * kPanel);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nb = p.buffers;
   const uint32_t cols = nb > 1 ? 256 : 128;
   if (threadIdx.x == 0) {
-    mbar_init(&sh.k_full, FP4 ? kKeys : 1);
-    mbar_init(&sh.k_empty, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_full[i], FP4 ? kKeys : 1);
+      mbar_init(&sh.k_empty[i], 1);
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
@@ -395,117 +430,155 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 3 : 4)
   const uint32_t tmem = sh.tmem;
   const bool forced = forced_timeout(p.st);
   volatile int* abort_flag = &sh.abort;
+  const int i0 = int(int64_t(blockIdx.x) * p.num_items / gridDim.x);
+  const int i1 = int(int64_t(blockIdx.x + 1) * p.num_items / gridDim.x);
+  TileItem t = find_item(p, i0), next = i0 + 1 < i1 ? next_item(p, t) : t;
 
   if (warp == 4) {
-    // The warp stays converged; one lane's copies and products are executed. K and the queries of
-    // an item are copied as soon as the product before has read theirs, under its exponentials.
+    // The warp stays converged; one lane's copies and products are executed. With one query tile per
+    // item (nb = 1) the next item's keys are copied before this item's product, and the queries
+    // only when they change; with several, queries and products alternate between two buffers.
     const uint32_t leader = elect_leader();
     bool ok = true;
     const uint64_t once = l2_evict_first_policy(), again = l2_evict_last_policy();
     const uint32_t fmt = __is_same(T, __half) ? 0u : 1u;
     const uint32_t idesc = umma_idesc(128, uint32_t((p.tile_queries * p.group + 15) & ~15), fmt, fmt, 0, 0);
     const uint64_t dk = umma_desc(smem_u32(ks), 16, 1024, kSwz128), dq = umma_desc(smem_u32(qs), 16, 1024, kSwz128);
-    int page = 0, slot = 0;  // of the lane's box of the item
-    auto lookup = [&](const TileItem& t) {
-      const int key = t.begin + lane * p.box;  // at most 16 boxes
-      if (!FP4 && t.tiles > 0 && lane * p.box < kKeys && key < t.end) {
-        const int n = key / p.page_size;
-        page = __ldg(p.meta + p.off_aux1 + t.pbase + n);
-        slot = key - n * p.page_size;
-      }
+    constexpr uint32_t kBuffer = uint32_t(kPanels * kPanel);
+    int page = 0, slot = 0;  // of the lane's box of the item whose keys are copied next
+    auto lookup = [&](const TileItem& u) {
+      const int key = u.begin + lane * p.box;  // at most 16 boxes
+      if (!FP4 && u.tiles > 0 && lane * p.box < kKeys && key < u.end)
+        page = __ldg(p.meta + p.off_aux1 + u.pbase + p.page_size.divmod(key, slot));
     };
-    int kc = 0, loaded = 0, done = 0;  // K tiles, query tiles copied, products issued
-    TileItem t = tile_item(p, blockIdx.x);
-    lookup(t);
-    for (int i = blockIdx.x; i < p.num_items && ok; i += gridDim.x) {
-      TileItem next = t;
-      if (i + int(gridDim.x) < p.num_items) next = tile_item(p, i + gridDim.x);
-      if (t.tiles > 0) {
-        ok = kc == 0 || issuer_wait(&sh.k_empty, uint32_t(kc - 1) & 1u, p.st, forced, abort_flag);
-        if (!ok) break;
-        if constexpr (!FP4) {
-          const int boxes = (t.end - t.begin + p.box - 1) / p.box;
-          mbar_arrive_expect_tx_w(leader, &sh.k_full, uint32_t(boxes) * kPanels * p.box * 128);
-          for (int x = 0; x < boxes; ++x) {
-            const int pg = __shfl_sync(0xffffffffu, page, x), sl = __shfl_sync(0xffffffffu, slot, x);
-#pragma unroll
-            for (int pn = 0; pn < kPanels; ++pn)
-              tma_load_5d_hint_w(leader, ks + pn * kPanel + x * p.box * 128, &kmap, pn * 64, sl, t.kvh, 0, pg,
-                                 &sh.k_full, once);
-          }
-        }
-        ++kc;
-        auto load_q = [&](int n) {  // query tile n of the item
-          const int buf = loaded % nb;
-          if (loaded >= nb && !issuer_wait(&sh.q_empty[buf], uint32_t(loaded / nb - 1) & 1u, p.st, forced, abort_flag))
-            return false;
-          mbar_arrive_expect_tx_w(leader, &sh.q_full[buf], uint32_t(kPanels) * p.tile_queries * p.group * 128);
+    int kc = 0, ku = 0, loaded = 0, done = 0;  // key tiles copied, used; query tiles copied; products issued
+    auto load_k = [&](const TileItem& u) {
+      if (u.tiles == 0) return true;
+      const int buf = kc % nk;
+      if (kc >= nk && !issuer_wait(&sh.k_empty[buf], uint32_t(kc / nk - 1) & 1u, p.st, forced, abort_flag)) return false;
+      if constexpr (!FP4) {
+        const int boxes = (u.end - u.begin + p.box - 1) / p.box;
+        mbar_arrive_expect_tx_w(leader, &sh.k_full[buf], uint32_t(boxes) * kPanels * p.box * 128);
+        for (int x = 0; x < boxes; ++x) {
+          const int pg = __shfl_sync(0xffffffffu, page, x), sl = __shfl_sync(0xffffffffu, slot, x);
 #pragma unroll
           for (int pn = 0; pn < kPanels; ++pn)
-            tma_load_3d_hint_w(leader, qs + (buf * kPanels + pn) * kPanel, &qmap, pn * 64, t.kvh * p.group,
-                               t.rq.qo + t.tok0 + n * p.tile_queries, &sh.q_full[buf], again);
-          ++loaded;
-          return true;
-        };
+            tma_load_5d_hint_w(leader, ks + buf * kBuffer + pn * kPanel + x * p.box * 128, &kmap, pn * 64, sl, u.kvh,
+                               0, pg, &sh.k_full[buf], once);
+        }
+      }
+      ++kc;
+      return true;
+    };
+    int q_r = -1, q_h = -1, q_n = -1;  // nb = 1: whose queries are in the buffer
+    auto load_q = [&](int n) {         // query tile n of the item
+      const int buf = loaded % nb;
+      if (loaded >= nb && !issuer_wait(&sh.q_empty[buf], uint32_t(loaded / nb - 1) & 1u, p.st, forced, abort_flag))
+        return false;
+      mbar_arrive_expect_tx_w(leader, &sh.q_full[buf], uint32_t(kPanels) * p.tile_queries * p.group * 128);
+#pragma unroll
+      for (int pn = 0; pn < kPanels; ++pn)
+        tma_load_3d_hint_w(leader, qs + buf * kBuffer + pn * kPanel, &qmap, pn * 64, t.kvh * p.group,
+                           t.rq.qo + t.tok0 + n * p.tile_queries, &sh.q_full[buf], again);
+      ++loaded;
+      return true;
+    };
+    lookup(t);
+    ok = load_k(t);
+    for (int i = i0; i < i1 && ok; ++i) {
+      const TileItem after = i + 2 < i1 ? next_item(p, next) : next;
+      if (nk > 1 && i + 1 < i1) lookup(next);
+      if (t.tiles > 0) {
         int nq = 0;  // query tiles of the item copied
-        for (; nq < nb && nq < t.tiles && ok; ++nq) ok = load_q(nq);
+        if (nb > 1) {
+          for (; nq < nb && nq < t.tiles && ok; ++nq) ok = load_q(nq);
+        } else if (t.r != q_r || t.kvh != q_h || t.tok0 != q_n) {
+          // the one buffer: every product that reads the old queries is done first
+          ok = done == 0 || issuer_wait(&sh.s_full[0], uint32_t(done - 1) & 1u, p.st, forced, abort_flag);
+          if (ok) {
+            mbar_arrive_expect_tx_w(leader, &sh.q_full[0], uint32_t(kPanels) * p.tile_queries * p.group * 128);
+#pragma unroll
+            for (int pn = 0; pn < kPanels; ++pn)
+              tma_load_3d_hint_w(leader, qs + pn * kPanel, &qmap, pn * 64, t.kvh * p.group, t.rq.qo + t.tok0,
+                                 &sh.q_full[0], again);
+            ++loaded;
+            q_r = t.r;
+            q_h = t.kvh;
+            q_n = t.tok0;
+          }
+        }
+        if (nk > 1 && i + 1 < i1 && ok) ok = load_k(next);
         for (int n = 0; n < t.tiles && ok; ++n) {
-          const int buf = done % nb;
+          const int buf = done % nb, kb = ku % nk;
           const uint32_t use = uint32_t(done / nb);
-          ok = (n > 0 || issuer_wait(&sh.k_full, uint32_t(kc - 1) & 1u, p.st, forced, abort_flag)) &&
-               issuer_wait(&sh.q_full[buf], use & 1u, p.st, forced, abort_flag) &&
+          ok = (n > 0 || issuer_wait(&sh.k_full[kb], uint32_t(ku / nk) & 1u, p.st, forced, abort_flag)) &&
+               issuer_wait(&sh.q_full[buf], (nb > 1 ? use : uint32_t(loaded - 1)) & 1u, p.st, forced, abort_flag) &&
                (done < nb || issuer_wait(&sh.s_empty[buf], (use - 1) & 1u, p.st, forced, abort_flag));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t at = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
-            umma_f16_w(leader, tmem + buf * 128, dk + at, dq + ((buf * kPanels * kPanel) >> 4) + at, idesc, kk > 0 ? 1u : 0u);
+            umma_f16_w(leader, tmem + buf * 128, dk + ((kb * kBuffer) >> 4) + at, dq + ((buf * kBuffer) >> 4) + at,
+                       idesc, kk > 0 ? 1u : 0u);
           }
           umma_commit_w(leader, &sh.s_full[buf]);
-          umma_commit_w(leader, &sh.q_empty[buf]);
-          if (n == t.tiles - 1) umma_commit_w(leader, &sh.k_empty);
+          if (nb > 1) umma_commit_w(leader, &sh.q_empty[buf]);
+          if (n == t.tiles - 1) umma_commit_w(leader, &sh.k_empty[kb]);
           ++done;
-          if (nq < t.tiles) {
+          if (nb > 1 && nq < t.tiles) {
             ok = load_q(nq);
             ++nq;
           }
         }
+        ++ku;
+      } else if (nk > 1 && i + 1 < i1) {
+        ok = load_k(next);
+      }
+      if (nk == 1 && i + 1 < i1 && ok) {
+        lookup(next);
+        ok = load_k(next);
       }
       t = next;
-      lookup(t);
+      next = after;
     }
     if (!ok) {
       // copies and products in flight land before the CTA leaves (bounded, not forcible)
       *abort_flag = 1;
       if (done > 0) mbar_wait(&sh.s_full[(done - 1) % nb], uint32_t((done - 1) / nb) & 1u, p.st, false);
-      if (!FP4 && kc > 0) mbar_wait(&sh.k_full, uint32_t(kc - 1) & 1u, p.st, false);
-      for (int n = max(0, loaded - nb); n < loaded; ++n) mbar_wait(&sh.q_full[n % nb], (n / nb) & 1u, p.st, false);
+      if (!FP4)
+        for (int n = max(0, kc - nk); n < kc; ++n) mbar_wait(&sh.k_full[n % nk], uint32_t(n / nk) & 1u, p.st, false);
+      for (int n = max(0, loaded - nb); n < loaded; ++n) mbar_wait(&sh.q_full[n % nb], uint32_t(n / nb) & 1u, p.st, false);
     }
   } else {
     // What an item needs from memory is read an item ahead: its record two ahead, then the page of
     // the thread's key, the key's score, and a 4-bit key's row.
     const uint32_t row = tmem + (uint32_t(warp) << 21);  // TMEM lane 32 * warp
+    int my_head;
+    const int my_tok = p.groups.divmod(int(threadIdx.x), my_head);  // of query row threadIdx.x of a tile
     auto page_of = [&](const TileItem& t) {
       const int key = t.begin + int(threadIdx.x);
-      return key < t.end ? __ldg(p.meta + p.off_aux1 + t.pbase + key / p.page_size) : 0;
+      return key < t.end ? __ldg(p.meta + p.off_aux1 + t.pbase + p.page_size.div(key)) : 0;
     };
     auto score_at = [&](const TileItem& t, int page) {
-      const int key = t.begin + int(threadIdx.x);
-      return p.scores + page * p.w_s0 + t.kvh * p.w_s1 + key % p.page_size;
+      int slot;
+      p.page_size.divmod(t.begin + int(threadIdx.x), slot);
+      return p.scores + page * p.w_s0 + t.kvh * p.w_s1 + slot;
     };
     auto is_fresh = [&](const TileItem& t) { return p.decay == 0.f || t.begin + int(threadIdx.x) >= t.rq.len - t.rq.nq; };
     auto old_score = [&](const TileItem& t, const float* at) {
       return t.begin + int(threadIdx.x) < t.end && !is_fresh(t) ? __ldg(at) : 0.f;
     };
     auto lse_of = [&](const TileItem& t, int n) {  // of row threadIdx.x of query tile n
-      const int r = (t.tok0 + n * p.tile_queries) * p.group + int(threadIdx.x), tok = r / p.group;
-      if (n >= t.tiles || int(threadIdx.x) >= p.tile_queries * p.group || tok >= t.rq.nq) return -INFINITY;
-      return __ldg(p.lse + int64_t(t.rq.qo + tok) * p.num_qo_heads + t.kvh * p.group + (r - tok * p.group));
+      const int tok = t.tok0 + n * p.tile_queries + my_tok;
+      if (n >= t.tiles || my_tok >= p.tile_queries || tok >= t.rq.nq) return -INFINITY;
+      return __ldg(p.lse + int64_t(t.rq.qo + tok) * p.num_qo_heads + t.kvh * p.group + my_head);
     };
     auto read_row = [&](const TileItem& t, int page) {
       Row4<D> x{};
-      const int key = t.begin + int(threadIdx.x), sl = key % p.page_size;
+      const int key = t.begin + int(threadIdx.x);
+      int sl;
+      p.page_size.divmod(key, sl);
       if (t.tiles > 0 && key < t.end) {
         const uint8_t* src = p.keys + page * p.k_s0 + t.kvh * p.k_s2 + sl * p.k_s3;
         const uint8_t* sc = p.scales + page * p.s_s0 + t.kvh * p.s_s2 + sl * (D / 32);
@@ -518,7 +591,9 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 3 : 4)
       return x;
     };
     // The row as T relative to its largest scale into shared memory; what multiplies its products.
+    int kc = 0;  // key tiles written
     auto put_row = [&](const Row4<D>& x) {
+      const int kb = kc++ % nk;
       uint32_t top = 0;
       bool bad = false;
 #pragma unroll
@@ -532,35 +607,33 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 3 : 4)
         const uint32_t v[4] = {x.w[j].x, x.w[j].y, x.w[j].z, x.w[j].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          sts128(smem_u32(ks) + (j >> 1) * kPanel + swz(threadIdx.x, (j & 1) * 4 + i, 128), widen<T>(v[i], f));
+          sts128(smem_u32(ks) + (kb * kPanels + (j >> 1)) * kPanel + swz(threadIdx.x, (j & 1) * 4 + i, 128), widen<T>(v[i], f));
       }
       fence_proxy_async_smem();
-      mbar_arrive(&sh.k_full);
+      mbar_arrive(&sh.k_full[kb]);
       return bad ? NAN : p.scale_log2 * e8m0_value(top);
     };
 
     bool ok = true;
     int done = 0;
-    TileItem t = tile_item(p, blockIdx.x), next = t;
-    const bool two = int(blockIdx.x) + int(gridDim.x) < p.num_items;
-    if (two) next = tile_item(p, blockIdx.x + gridDim.x);
     int page = page_of(t);
     float* score = score_at(t, page);
     float old = old_score(t, score), lse = lse_of(t, 0), unit = p.scale_log2, next_unit = unit;
     if constexpr (FP4) {
       if (t.tiles > 0) unit = put_row(read_row(t, page));
     }
-    for (int i = blockIdx.x; i < p.num_items; i += gridDim.x) {
+    for (int i = i0; i < i1; ++i) {
       const int key = t.begin + int(threadIdx.x);
-      const bool more = i + int(gridDim.x) < p.num_items;
-      TileItem after = next;
-      if (i + 2 * int(gridDim.x) < p.num_items) after = tile_item(p, i + 2 * gridDim.x);
+      const bool more = i + 1 < i1;
+      const TileItem after = i + 2 < i1 ? next_item(p, next) : next;
       const int next_page = more ? page_of(next) : 0;
       float* next_score = score_at(next, next_page);
       float next_old = 0.f;
       Row4<D> ahead;
       if constexpr (FP4) {
         if (more) ahead = read_row(next, next_page);
+        // the other key buffer: the product that read it is done, this thread has its sums
+        if (nk > 1 && more && next.tiles > 0 && ok) next_unit = put_row(ahead);
       }
       float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
       const float2 unit2 = make_float2(unit, unit);
@@ -569,7 +642,7 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 3 : 4)
         const int buf = done % nb, info = done & 1;
         const int count = min(p.tile_queries, t.rq.nq - t.tok0 - n * p.tile_queries) * p.group;
         const int c = threadIdx.x;
-        const RowInfo o = row_info(p, t.rq, lse, (t.tok0 + n * p.tile_queries) + c / p.group);
+        const RowInfo o = row_info(p, t.rq, lse, t.tok0 + n * p.tile_queries + my_tok);
         sh.last[info][c] = o.last;
         float* pair = reinterpret_cast<float*>(&sh.pair[info][c >> 1]) + (c & 1);
         pair[0] = -o.hi;
@@ -585,16 +658,17 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 3 : 4)
         tc_fence_after();
         if (n == t.tiles - 1) {
           if constexpr (FP4) {
-            if (more && next.tiles > 0) next_unit = put_row(ahead);  // the product has read this item's keys
+            if (nk == 1 && more && next.tiles > 0) next_unit = put_row(ahead);  // the product has read the keys
           }
         }
-        for (int c0 = 0; c0 < count; c0 += 32) {
-          uint32_t s[32];
+        for (int c0 = 0; c0 < count; c0 += 64) {
+          uint32_t s[64];
           tmem_ld32(row + buf * 128 + c0, s);
+          tmem_ld32(row + buf * 128 + c0 + 32, s + 32);
           tmem_ld_wait();
-          if (all && c0 + 32 <= count) {
+          if (all && c0 + 64 <= count) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < 32; ++j) {
               const float4 hr = sh.pair[info][c0 / 2 + j];
               const float2 x = ffma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), unit2,
                                      make_float2(hr.x, hr.y));
@@ -602,7 +676,7 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 3 : 4)
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < 64; ++j) {
               const int c1 = c0 + j;
               if (c1 >= count) continue;
               const float* hr = reinterpret_cast<const float*>(&sh.pair[info][c1 >> 1]) + (c1 & 1);
@@ -617,7 +691,7 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 3 : 4)
       if (t.tiles == 0) {  // no query sees these keys: the scores only fade
         lse = more ? lse_of(next, 0) : 0.f;
         if constexpr (FP4) {
-          if (more && next.tiles > 0 && ok) next_unit = put_row(ahead);
+          if (nk == 1 && more && next.tiles > 0 && ok) next_unit = put_row(ahead);
         }
       }
       if (more) next_old = old_score(next, next_score);
@@ -666,13 +740,15 @@ bskv_status launch_tile(const bskv_plan* plan, WeightsParams& wp, cudaStream_t s
     const uint32_t kb[5] = {64, uint32_t(wp.box), 1, 1, 1};
     if (bskv_status s = encode_tiled(&kmap, dt, 5, wp.keys, kd, kst, kb, CU_TENSOR_MAP_SWIZZLE_128B)) return s;
   }
-  const size_t smem = 1024 + size_t(1 + wp.buffers) * (D / 64) * kPanel + sizeof(TileShared);
+  const size_t smem = 1024 + size_t(3) * (D / 64) * kPanel + sizeof(TileShared);
   auto kern = weights_tile_kernel<T, D, FP4>;
   static std::atomic<int> allowed[64];
   if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "attn_weights: cudaFuncSetAttribute")) return s;
   // as many CTAs as the GPU holds: by shared memory and by TMEM (128 columns a buffer)
-  const int per_sm = wp.buffers > 1 ? 2 : D == 128 ? 3 : 4;
+  const int per_sm = wp.buffers > 1 || D == 128 ? 2 : 3;
+  wp.num_requests = meta_word(plan, H_MERGES);
   wp.num_items = meta_word(plan, H_UNITS);
+  wp.queries = FastDiv(wp.tile_queries);
   const int grid = std::min(wp.num_items, plan->num_sms * per_sm);
   kern<<<grid, kTileThreads, smem, st>>>(qmap, kmap, wp);
   return cuda_check(cudaGetLastError(), "attn_weights launch");
@@ -709,7 +785,10 @@ bskv_status run(const char* who, const bskv_plan* plan, const void* q, const int
   wp.scores = scores; wp.w_s0 = scores_strides[0]; wp.w_s1 = scores_strides[1];
   wp.num_kv_heads = plan->num_kv_heads;
   wp.group = plan->num_qo_heads / plan->num_kv_heads;
-  wp.page_size = plan->page_size; wp.num_qo_heads = plan->num_qo_heads; wp.causal = plan->causal;
+  wp.heads = FastDiv(plan->num_kv_heads);
+  wp.groups = FastDiv(wp.group);
+  wp.page_size = FastDiv(plan->page_size);
+  wp.num_qo_heads = plan->num_qo_heads; wp.causal = plan->causal;
   wp.off_workers = meta_word(plan, H_OFF_WORKERS);
   wp.off_chunks = meta_word(plan, H_OFF_CHUNKS);
   wp.off_aux0 = meta_word(plan, H_OFF_AUX0);

@@ -13,6 +13,26 @@
 namespace bskv {
 namespace dev {
 
+// n / d for 0 <= n < 2^31 by one multiplication: with 2^(s-1) < d <= 2^s and m = ceil(2^(31+s) / d),
+// n m / 2^(31+s) is n / d plus less than 2^31 2^s / 2^(31+s) / d, so it has the same integer part.
+struct FastDiv {
+  uint32_t d, m, shift;  // m = 0: d = 1
+  FastDiv() = default;
+  explicit FastDiv(int32_t divisor) : d(uint32_t(divisor)), m(0), shift(0) {
+    if (d <= 1) return;
+    uint32_t s = 1;
+    while ((uint64_t(1) << s) < d) ++s;
+    m = uint32_t(((uint64_t(1) << (31 + s)) + d - 1) / d);
+    shift = s - 1;
+  }
+  __device__ __forceinline__ int div(int n) const { return m ? int(__umulhi(uint32_t(n), m) >> shift) : n; }
+  __device__ __forceinline__ int divmod(int n, int& rest) const {
+    const int q = div(n);
+    rest = n - q * int(d);
+    return q;
+  }
+};
+
 // ---------------------------------------------------------------------------------------
 // device status word and bounded waits
 // ---------------------------------------------------------------------------------------

@@ -62,7 +62,8 @@ struct Fp4DecodeParams {
   float* ws_o;
   float* ws_lse;
   int* counters;  // non-null: the last worker to finish a split unit merges it
-  int num_kv_heads, group, page_size, num_qo_heads;
+  int num_kv_heads, group, num_qo_heads;
+  FastDiv heads, page_size;
   int off_workers, off_records, off_merges, off_aux1, num_merges, num_workers;
   float scale_log2;
 };
@@ -457,10 +458,9 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
   const int w = blockIdx.x * kWarps + warp;
   if (w >= P) return;
   const int32_t* merges = p.meta + p.off_merges;
-  const int Hkv = p.num_kv_heads;
   const int c0 = __ldg(p.meta + p.off_workers + w), nck = __ldg(p.meta + p.off_workers + w + 1) - c0;
   const int32_t* records = p.meta + p.off_records + c0 * kWalkWords;
-  PageWalk walk(records, nck, p.meta + p.off_aux1, Hkv, p.page_size, lane);
+  PageWalk walk(records, nck, p.meta + p.off_aux1, p.heads, p.page_size, lane);
 
   // Eight lanes copy a group of 8 tokens: row `sub / kParts` and every kRows-th after it, part
   // `sub % kParts` of each (XORed as swizzled), and the first of them its 16-byte pieces of scales.
@@ -509,7 +509,8 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
   int done = 0;
   for (int k = 0; k < nck; ++k) {
     const WalkChunk ch = walk_chunk(records, k);
-    const int b = ch.unit / Hkv, kvh = ch.unit - b * Hkv;
+    int kvh;
+    const int b = p.heads.divmod(ch.unit, kvh);
     load_q<T, D, NT>(p, b, kvh, lane, s);
     for (int at = ch.begin; at < ch.end; at += kTile, ++done) {
       cp_async_wait<kStages - 2>();
@@ -607,7 +608,8 @@ extern "C" bskv_status bskv_run_decode_fp4(const bskv_plan* plan, const void* q,
   dp.lse = lse;
   dp.num_kv_heads = plan->num_kv_heads;
   dp.group = plan->num_qo_heads / plan->num_kv_heads;
-  dp.page_size = plan->page_size;
+  dp.heads = FastDiv(plan->num_kv_heads);
+  dp.page_size = FastDiv(plan->page_size);
   dp.num_qo_heads = plan->num_qo_heads;
   const int slots = meta_word(plan, H_SLOTS);
   dp.ws_o = static_cast<float*>(float_ws);

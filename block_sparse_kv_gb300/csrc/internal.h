@@ -128,8 +128,8 @@ constexpr int fp4_ctas_per_sm(int column_tiles) { return column_tiles == 0 ? 3 :
 
 // Attention-weight plans. Stream variants (at most 8 or 16 query rows, queries times heads of a
 // group, in every request): one worker per warp over ranges of tokens of (request, kv head)
-// units. Tile variant: one CTA per 128 keys of a request (chunk {request, first, end, 0}) and kv
-// head. Per request {first query, queries, tokens} stands in the merge section.
+// units; {first query, queries, tokens} of each request stands in the merge section. Tile variant:
+// items of 128 keys of a request for one kv head, by a record of kWalkWords per request with tokens.
 enum WeightsVariant : int32_t { WEIGHTS_STREAM8 = 0, WEIGHTS_STREAM16 = 1, WEIGHTS_TILE = 2 };
 constexpr int kWeightsWarps = 4;
 constexpr int kWeightsKeys = 128;

@@ -23,7 +23,8 @@ __device__ __forceinline__ WalkChunk walk_chunk(const int32_t* records, int i) {
 struct PageWalk {
   const int32_t* records;     // of this worker
   const int32_t* kv_indices;
-  int left, num_kv_heads, page_size, lane;  // chunks to open yet
+  int left, lane;             // chunks to open yet
+  FastDiv heads, page_size;
   int k = -1;                 // chunk being walked
   int tok = 0, end = 0;       // its tokens [tok, end) are still to come
   int kvh = 0, pbase = 0, win = 0;
@@ -32,9 +33,9 @@ struct PageWalk {
   int page = 0, slot = 0, page2 = 0, slot2 = 0;
   bool fresh = false;
 
-  __device__ __forceinline__ PageWalk(const int32_t* records_, int chunks, const int32_t* indices, int heads,
-                                      int ps, int lane_)
-      : records(records_), kv_indices(indices), left(chunks), num_kv_heads(heads), page_size(ps), lane(lane_) {
+  __device__ __forceinline__ PageWalk(const int32_t* records_, int chunks, const int32_t* indices,
+                                      const FastDiv& heads_, const FastDiv& ps, int lane_)
+      : records(records_), kv_indices(indices), left(chunks), lane(lane_), heads(heads_), page_size(ps) {
     open();
   }
   __device__ __forceinline__ bool live() const { return left >= 0; }
@@ -42,16 +43,14 @@ struct PageWalk {
   __device__ __forceinline__ void lookup(int first, int& pg, int& sl) const {
     const int at = first + 8 * lane;
     if (at < end) {
-      const int i = at / page_size;
-      pg = __ldg(kv_indices + pbase + i);
-      sl = at - i * page_size;
+      pg = __ldg(kv_indices + pbase + page_size.divmod(at, sl));
     }
   }
   __device__ __forceinline__ void open() {
     ++k;
     if (--left < 0) return;
     const WalkChunk c = walk_chunk(records, k);
-    kvh = c.unit % num_kv_heads;
+    heads.divmod(c.unit, kvh);
     tok = win = c.begin;
     end = c.end;
     pbase = c.pbase;

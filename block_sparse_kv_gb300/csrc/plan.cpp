@@ -755,12 +755,9 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
     units = int32_t(len.size());
   } else {
     variant = WEIGHTS_TILE;
-    for (int32_t b = 0; b < batch; ++b)
-      for (int64_t t = 0; t < req[size_t(b)]; t += kWeightsKeys)
-        chunks.push_back(Chunk{b, int32_t(t), int32_t(std::min<int64_t>(t + kWeightsKeys, req[size_t(b)])), 0});
-    if (int64_t(chunks.size()) * num_kv_heads > INT32_MAX / 2) { set_error("%s: too many tokens", who); return BSKV_ERR_UNSUPPORTED; }
-    grid = int32_t(chunks.size());
-    units = grid * num_kv_heads;
+    int64_t items = 0;
+    for (int32_t b = 0; b < batch; ++b) items += (req[size_t(b)] + kWeightsKeys - 1) / kWeightsKeys * num_kv_heads;
+    grid = units = int32_t(items);  // at most the tokens times the heads
   }
   bskv_plan* p = new bskv_plan();
   p->kind = KIND_WEIGHTS;
@@ -775,11 +772,18 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
            grid, variant);
   if (variant != WEIGHTS_TILE) {
     add_walk_records(p, worker_ptr, chunks, no_merges, kv_indptr, num_kv_heads);
-  } else {  // {request, first, end, its kv_indptr, its first query, queries, tokens, 0} per tile
+  } else {  // a record per request with tokens: {first item, key tiles, tokens, kv_indptr, first query, queries, 0, 0}
     p->walk_records = int32_t(p->meta.size());
-    for (const Chunk& c : chunks)
-      p->meta.insert(p->meta.end(), {c.unit, c.a, c.b, kv_indptr[c.unit], queries[size_t(3 * c.unit)],
-                                     queries[size_t(3 * c.unit + 1)], queries[size_t(3 * c.unit + 2)], 0});
+    int32_t items = 0, records = 0;
+    for (int32_t b = 0; b < batch; ++b) {
+      if (req[size_t(b)] == 0) continue;
+      const int32_t n = int32_t((req[size_t(b)] + kWeightsKeys - 1) / kWeightsKeys);
+      p->meta.insert(p->meta.end(), {items, n, int32_t(req[size_t(b)]), kv_indptr[b], queries[size_t(3 * b)],
+                                     queries[size_t(3 * b + 1)], 0, 0});
+      items += n * num_kv_heads;
+      ++records;
+    }
+    p->meta[H_MERGES] = records;
     p->meta[H_TOTAL] = int32_t(p->meta.size());
   }
   *out_plan = p;
