@@ -57,7 +57,8 @@ struct WeightsParams {
   int64_t w_s0, w_s1;               // floats: page, kv head
   int num_kv_heads, group, num_qo_heads, causal;
   FastDiv heads, groups, page_size, queries;
-  int box, tile_queries, buffers, num_items, num_requests;  // tile kernel: keys per TMA box, queries per product, S buffers
+  int box, tile_queries, num_items, num_requests;  // tile kernel: keys per TMA box, queries per product
+  int single;                                      // no item has more than one product
   int off_workers, off_chunks, off_records, off_aux0, off_aux1, off_req, num_workers;
   float decay, scale_log2;
   StatusArgs st;
@@ -327,8 +328,10 @@ __device__ __forceinline__ uint4 widen(uint32_t w, float f) {
 }
 
 struct TileShared {
-  float4 pair[2][64];  // of query rows 2 i and 2 i + 1: {-hi, -hi, r, r}
-  int last[2][128];
+  float4 pair[2][2][64];  // [group of threads][parity] of query rows 2 i and 2 i + 1: {-hi, -hi, r, r}
+  int last[2][2][128];
+  float part[2][kKeys];   // the second group's sums of an item
+  float unit[2][kKeys];   // what the keys' products are multiplied by
   uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], s_full[2], s_empty[2];
   uint32_t tmem;
   int abort;
@@ -387,7 +390,7 @@ __device__ __forceinline__ TileItem next_item(const WeightsParams& p, TileItem t
   return t;
 }
 
-constexpr int kTileThreads = kKeys + 32;  // a thread per key, and the warp that copies and multiplies
+constexpr int kTileThreads = 2 * kKeys + 32;  // two groups of a thread per key, and a warp that copies and multiplies
 
 // A 4-bit key's row and scales on their way to shared memory.
 template <int D>
@@ -396,18 +399,24 @@ struct Row4 {
   uint32_t code[D / 32];
 };
 
+// Products alternate between two TMEM buffers, each with a group of 128 threads that adds up its
+// weights, so that one group's exponentials run under the other's waits. Two modes:
+//   * single: no request has more query rows than one product takes. Item n of the CTA goes to group
+//     n mod 2; keys have two buffers too, queries stay while they are the same.
+//   * several products per item: they alternate between the groups, whose sums are added at its end;
+//     queries have two buffers, keys one.
 template <typename T, int D, bool FP4>
-__global__ void __launch_bounds__(kTileThreads, D == 128 ? 2 : 3)
+__global__ void __launch_bounds__(kTileThreads, 2)
     weights_tile_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ WeightsParams p) {
   constexpr int kPanels = D / 64;
+  constexpr uint32_t kBuffer = uint32_t(kPanels * kPanel), kCols = 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ks = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int nb = p.buffers, nk = 3 - nb;  // buffers of queries and products; of keys
-  uint8_t* qs = ks + nk * kPanels * kPanel;
-  TileShared& sh = *reinterpret_cast<TileShared*>(qs + nb * kPanels * kPanel);
+  const bool single = p.single;
+  uint8_t* qs = ks + (single ? 2 : 1) * kBuffer;
+  TileShared& sh = *reinterpret_cast<TileShared*>(ks + 3 * kBuffer);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t cols = nb > 1 ? 256 : 128;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.k_full[i], FP4 ? kKeys : 1);
@@ -420,8 +429,8 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 2 : 3)
     sh.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 4) {
-    tmem_alloc(&sh.tmem, cols);
+  if (warp == 8) {
+    tmem_alloc(&sh.tmem, kCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -432,112 +441,115 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 2 : 3)
   volatile int* abort_flag = &sh.abort;
   const int i0 = int(int64_t(blockIdx.x) * p.num_items / gridDim.x);
   const int i1 = int(int64_t(blockIdx.x + 1) * p.num_items / gridDim.x);
-  TileItem t = find_item(p, i0), next = i0 + 1 < i1 ? next_item(p, t) : t;
+  TileItem t = find_item(p, i0);
 
-  if (warp == 4) {
-    // The warp stays converged; one lane's copies and products are executed. With one query tile per
-    // item (nb = 1) the next item's keys are copied before this item's product, and the queries
-    // only when they change; with several, queries and products alternate between two buffers.
+  if (warp == 8) {
+    // The warp stays converged; one lane's copies and products are executed. The next item's keys
+    // are copied before this item's product where they have a buffer of their own.
     const uint32_t leader = elect_leader();
     bool ok = true;
     const uint64_t once = l2_evict_first_policy(), again = l2_evict_last_policy();
     const uint32_t fmt = __is_same(T, __half) ? 0u : 1u;
     const uint32_t idesc = umma_idesc(128, uint32_t((p.tile_queries * p.group + 15) & ~15), fmt, fmt, 0, 0);
     const uint64_t dk = umma_desc(smem_u32(ks), 16, 1024, kSwz128), dq = umma_desc(smem_u32(qs), 16, 1024, kSwz128);
-    constexpr uint32_t kBuffer = uint32_t(kPanels * kPanel);
+    TileItem next = i0 + 1 < i1 ? next_item(p, t) : t;
     int page = 0, slot = 0;  // of the lane's box of the item whose keys are copied next
     auto lookup = [&](const TileItem& u) {
       const int key = u.begin + lane * p.box;  // at most 16 boxes
       if (!FP4 && u.tiles > 0 && lane * p.box < kKeys && key < u.end)
         page = __ldg(p.meta + p.off_aux1 + u.pbase + p.page_size.divmod(key, slot));
     };
-    int kc = 0, ku = 0, loaded = 0, done = 0;  // key tiles copied, used; query tiles copied; products issued
-    auto load_k = [&](const TileItem& u) {
+    // Times each buffer was filled (keys, queries) or multiplied into (products).
+    int kn0 = 0, kn1 = 0, qn = 0, sn0 = 0, sn1 = 0;
+    auto wait = [&](uint64_t* bar, int phase) { return issuer_wait(bar, uint32_t(phase) & 1u, p.st, forced, abort_flag); };
+    auto load_k = [&](const TileItem& u, int kb) {
       if (u.tiles == 0) return true;
-      const int buf = kc % nk;
-      if (kc >= nk && !issuer_wait(&sh.k_empty[buf], uint32_t(kc / nk - 1) & 1u, p.st, forced, abort_flag)) return false;
+      int& n = kb ? kn1 : kn0;
+      if (n > 0 && !wait(&sh.k_empty[kb], n - 1)) return false;
       if constexpr (!FP4) {
         const int boxes = (u.end - u.begin + p.box - 1) / p.box;
-        mbar_arrive_expect_tx_w(leader, &sh.k_full[buf], uint32_t(boxes) * kPanels * p.box * 128);
+        mbar_arrive_expect_tx_w(leader, &sh.k_full[kb], uint32_t(boxes) * kPanels * p.box * 128);
         for (int x = 0; x < boxes; ++x) {
           const int pg = __shfl_sync(0xffffffffu, page, x), sl = __shfl_sync(0xffffffffu, slot, x);
 #pragma unroll
           for (int pn = 0; pn < kPanels; ++pn)
-            tma_load_5d_hint_w(leader, ks + buf * kBuffer + pn * kPanel + x * p.box * 128, &kmap, pn * 64, sl, u.kvh,
-                               0, pg, &sh.k_full[buf], once);
+            tma_load_5d_hint_w(leader, ks + kb * kBuffer + pn * kPanel + x * p.box * 128, &kmap, pn * 64, sl, u.kvh, 0,
+                               pg, &sh.k_full[kb], once);
         }
       }
-      ++kc;
+      ++n;
       return true;
     };
-    int q_r = -1, q_h = -1, q_n = -1;  // nb = 1: whose queries are in the buffer
-    auto load_q = [&](int n) {         // query tile n of the item
-      const int buf = loaded % nb;
-      if (loaded >= nb && !issuer_wait(&sh.q_empty[buf], uint32_t(loaded / nb - 1) & 1u, p.st, forced, abort_flag))
-        return false;
-      mbar_arrive_expect_tx_w(leader, &sh.q_full[buf], uint32_t(kPanels) * p.tile_queries * p.group * 128);
+    auto load_q = [&](int tok, int qb) {
+      mbar_arrive_expect_tx_w(leader, &sh.q_full[qb], uint32_t(kPanels) * p.tile_queries * p.group * 128);
 #pragma unroll
       for (int pn = 0; pn < kPanels; ++pn)
-        tma_load_3d_hint_w(leader, qs + buf * kBuffer + pn * kPanel, &qmap, pn * 64, t.kvh * p.group,
-                           t.rq.qo + t.tok0 + n * p.tile_queries, &sh.q_full[buf], again);
-      ++loaded;
+        tma_load_3d_hint_w(leader, qs + qb * kBuffer + pn * kPanel, &qmap, pn * 64, t.kvh * p.group, t.rq.qo + tok,
+                           &sh.q_full[qb], again);
+      ++qn;
+    };
+    auto multiply = [&](int kb, int qb, int sb, bool last) {
+      int& n = sb ? sn1 : sn0;
+      if (n > 0 && !wait(&sh.s_empty[sb], n - 1)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t at = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+        umma_f16_w(leader, tmem + sb * 128, dk + ((kb * kBuffer) >> 4) + at, dq + ((qb * kBuffer) >> 4) + at, idesc,
+                   kk > 0 ? 1u : 0u);
+      }
+      umma_commit_w(leader, &sh.s_full[sb]);
+      if (!single) umma_commit_w(leader, &sh.q_empty[qb]);
+      if (last) umma_commit_w(leader, &sh.k_empty[kb]);
+      ++n;
       return true;
     };
+    int q_r = -1, q_h = -1, q_tok = -1;  // single: whose queries are in the buffer
+    int prev = 0;                        // and the buffer of the last product
     lookup(t);
-    ok = load_k(t);
+    ok = load_k(t, 0);
     for (int i = i0; i < i1 && ok; ++i) {
       const TileItem after = i + 2 < i1 ? next_item(p, next) : next;
-      if (nk > 1 && i + 1 < i1) lookup(next);
-      if (t.tiles > 0) {
-        int nq = 0;  // query tiles of the item copied
-        if (nb > 1) {
-          for (; nq < nb && nq < t.tiles && ok; ++nq) ok = load_q(nq);
-        } else if (t.r != q_r || t.kvh != q_h || t.tok0 != q_n) {
-          // the one buffer: every product that reads the old queries is done first
-          ok = done == 0 || issuer_wait(&sh.s_full[0], uint32_t(done - 1) & 1u, p.st, forced, abort_flag);
-          if (ok) {
-            mbar_arrive_expect_tx_w(leader, &sh.q_full[0], uint32_t(kPanels) * p.tile_queries * p.group * 128);
-#pragma unroll
-            for (int pn = 0; pn < kPanels; ++pn)
-              tma_load_3d_hint_w(leader, qs + pn * kPanel, &qmap, pn * 64, t.kvh * p.group, t.rq.qo + t.tok0,
-                                 &sh.q_full[0], again);
-            ++loaded;
-            q_r = t.r;
-            q_h = t.kvh;
-            q_n = t.tok0;
-          }
-        }
-        if (nk > 1 && i + 1 < i1 && ok) ok = load_k(next);
-        for (int n = 0; n < t.tiles && ok; ++n) {
-          const int buf = done % nb, kb = ku % nk;
-          const uint32_t use = uint32_t(done / nb);
-          ok = (n > 0 || issuer_wait(&sh.k_full[kb], uint32_t(ku / nk) & 1u, p.st, forced, abort_flag)) &&
-               issuer_wait(&sh.q_full[buf], (nb > 1 ? use : uint32_t(loaded - 1)) & 1u, p.st, forced, abort_flag) &&
-               (done < nb || issuer_wait(&sh.s_empty[buf], (use - 1) & 1u, p.st, forced, abort_flag));
+      const bool more = i + 1 < i1;
+      const int par = (i - i0) & 1;
+      if (single) {
+        if (more) lookup(next);
+        if (t.tiles > 0 && (t.r != q_r || t.kvh != q_h || t.tok0 != q_tok)) {
+          // the one buffer: the products that read the old queries are done first
+          const int n = prev ? sn1 : sn0;
+          ok = n == 0 || wait(&sh.s_full[prev], n - 1);
           if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t at = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
-            umma_f16_w(leader, tmem + buf * 128, dk + ((kb * kBuffer) >> 4) + at, dq + ((buf * kBuffer) >> 4) + at,
-                       idesc, kk > 0 ? 1u : 0u);
-          }
-          umma_commit_w(leader, &sh.s_full[buf]);
-          if (nb > 1) umma_commit_w(leader, &sh.q_empty[buf]);
-          if (n == t.tiles - 1) umma_commit_w(leader, &sh.k_empty[kb]);
-          ++done;
-          if (nb > 1 && nq < t.tiles) {
-            ok = load_q(nq);
-            ++nq;
-          }
+          load_q(t.tok0, 0);
+          q_r = t.r;
+          q_h = t.kvh;
+          q_tok = t.tok0;
         }
-        ++ku;
-      } else if (nk > 1 && i + 1 < i1) {
-        ok = load_k(next);
-      }
-      if (nk == 1 && i + 1 < i1 && ok) {
-        lookup(next);
-        ok = load_k(next);
+        if (more) ok = load_k(next, par ^ 1);
+        if (ok && t.tiles > 0) {
+          ok = wait(&sh.k_full[par], (par ? kn1 : kn0) - 1) && wait(&sh.q_full[0], qn - 1) && multiply(par, 0, par, true);
+          prev = par;
+        }
+      } else {
+        int q = 0;  // query tiles of the item copied
+        const int q0 = qn;
+        auto fill = [&]() {
+          const int qb = qn & 1;
+          if (qn >= 2 && !wait(&sh.q_empty[qb], (qn >> 1) - 1)) return false;
+          load_q(t.tok0 + q * p.tile_queries, qb);
+          ++q;
+          return true;
+        };
+        while (ok && q < 2 && q < t.tiles) ok = fill();
+        if (ok && t.tiles > 0) ok = wait(&sh.k_full[0], kn0 - 1);
+        for (int n = 0; n < t.tiles && ok; ++n) {
+          const int u = q0 + n;  // query tiles and products are numbered alike
+          ok = wait(&sh.q_full[u & 1], u >> 1) && multiply(0, u & 1, u & 1, n == t.tiles - 1);
+          if (ok && q < t.tiles) ok = fill();
+        }
+        if (more && ok) {
+          lookup(next);
+          ok = load_k(next, 0);
+        }
       }
       t = next;
       next = after;
@@ -545,43 +557,46 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 2 : 3)
     if (!ok) {
       // copies and products in flight land before the CTA leaves (bounded, not forcible)
       *abort_flag = 1;
-      if (done > 0) mbar_wait(&sh.s_full[(done - 1) % nb], uint32_t((done - 1) / nb) & 1u, p.st, false);
-      if (!FP4)
-        for (int n = max(0, kc - nk); n < kc; ++n) mbar_wait(&sh.k_full[n % nk], uint32_t(n / nk) & 1u, p.st, false);
-      for (int n = max(0, loaded - nb); n < loaded; ++n) mbar_wait(&sh.q_full[n % nb], uint32_t(n / nb) & 1u, p.st, false);
+      if (sn0 > 0) mbar_wait(&sh.s_full[0], uint32_t(sn0 - 1) & 1u, p.st, false);
+      if (sn1 > 0) mbar_wait(&sh.s_full[1], uint32_t(sn1 - 1) & 1u, p.st, false);
+      if (!FP4 && kn0 > 0) mbar_wait(&sh.k_full[0], uint32_t(kn0 - 1) & 1u, p.st, false);
+      if (!FP4 && kn1 > 0) mbar_wait(&sh.k_full[1], uint32_t(kn1 - 1) & 1u, p.st, false);
+      for (int n = max(0, qn - (single ? 1 : 2)); n < qn; ++n)
+        mbar_wait(&sh.q_full[single ? 0 : n & 1], uint32_t(single ? n : n >> 1) & 1u, p.st, false);
     }
   } else {
-    // What an item needs from memory is read an item ahead: its record two ahead, then the page of
-    // the thread's key, the key's score, and a 4-bit key's row.
-    const uint32_t row = tmem + (uint32_t(warp) << 21);  // TMEM lane 32 * warp
+    // What an item needs from memory is read an item ahead: the page of the thread's key, the key's
+    // score, the log-sum-exps, and a 4-bit key's row.
+    const int grp = warp >> 2, tid = threadIdx.x & (kKeys - 1), bar = 1 + grp;
+    const uint32_t row = tmem + (uint32_t(warp & 3) << 21) + grp * 128;  // TMEM lane 32 * (warp mod 4)
     int my_head;
-    const int my_tok = p.groups.divmod(int(threadIdx.x), my_head);  // of query row threadIdx.x of a tile
-    auto page_of = [&](const TileItem& t) {
-      const int key = t.begin + int(threadIdx.x);
-      return key < t.end ? __ldg(p.meta + p.off_aux1 + t.pbase + p.page_size.div(key)) : 0;
+    const int my_tok = p.groups.divmod(tid, my_head);  // of query row tid of a product
+    auto page_of = [&](const TileItem& u) {
+      const int key = u.begin + tid;
+      return key < u.end ? __ldg(p.meta + p.off_aux1 + u.pbase + p.page_size.div(key)) : 0;
     };
-    auto score_at = [&](const TileItem& t, int page) {
+    auto score_at = [&](const TileItem& u, int page) {
       int slot;
-      p.page_size.divmod(t.begin + int(threadIdx.x), slot);
-      return p.scores + page * p.w_s0 + t.kvh * p.w_s1 + slot;
+      p.page_size.divmod(u.begin + tid, slot);
+      return p.scores + page * p.w_s0 + u.kvh * p.w_s1 + slot;
     };
-    auto is_fresh = [&](const TileItem& t) { return p.decay == 0.f || t.begin + int(threadIdx.x) >= t.rq.len - t.rq.nq; };
-    auto old_score = [&](const TileItem& t, const float* at) {
-      return t.begin + int(threadIdx.x) < t.end && !is_fresh(t) ? __ldg(at) : 0.f;
+    auto is_fresh = [&](const TileItem& u) { return p.decay == 0.f || u.begin + tid >= u.rq.len - u.rq.nq; };
+    auto old_score = [&](const TileItem& u, const float* at) {
+      return u.begin + tid < u.end && !is_fresh(u) ? __ldg(at) : 0.f;
     };
-    auto lse_of = [&](const TileItem& t, int n) {  // of row threadIdx.x of query tile n
-      const int tok = t.tok0 + n * p.tile_queries + my_tok;
-      if (n >= t.tiles || my_tok >= p.tile_queries || tok >= t.rq.nq) return -INFINITY;
-      return __ldg(p.lse + int64_t(t.rq.qo + tok) * p.num_qo_heads + t.kvh * p.group + my_head);
+    auto lse_of = [&](const TileItem& u, int n) {  // of row tid of product n
+      const int tok = u.tok0 + n * p.tile_queries + my_tok;
+      if (n >= u.tiles || my_tok >= p.tile_queries || tok >= u.rq.nq) return -INFINITY;
+      return __ldg(p.lse + int64_t(u.rq.qo + tok) * p.num_qo_heads + u.kvh * p.group + my_head);
     };
-    auto read_row = [&](const TileItem& t, int page) {
+    auto read_row = [&](const TileItem& u, int page) {
       Row4<D> x{};
-      const int key = t.begin + int(threadIdx.x);
+      const int key = u.begin + tid;
       int sl;
       p.page_size.divmod(key, sl);
-      if (t.tiles > 0 && key < t.end) {
-        const uint8_t* src = p.keys + page * p.k_s0 + t.kvh * p.k_s2 + sl * p.k_s3;
-        const uint8_t* sc = p.scales + page * p.s_s0 + t.kvh * p.s_s2 + sl * (D / 32);
+      if (u.tiles > 0 && key < u.end) {
+        const uint8_t* src = p.keys + page * p.k_s0 + u.kvh * p.k_s2 + sl * p.k_s3;
+        const uint8_t* sc = p.scales + page * p.s_s0 + u.kvh * p.s_s2 + sl * (D / 32);
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
           x.w[j] = __ldg(reinterpret_cast<const uint4*>(src) + j);
@@ -590,10 +605,8 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 2 : 3)
       }
       return x;
     };
-    // The row as T relative to its largest scale into shared memory; what multiplies its products.
-    int kc = 0;  // key tiles written
-    auto put_row = [&](const Row4<D>& x) {
-      const int kb = kc++ % nk;
+    // The row as T relative to its largest scale into key buffer kb; what multiplies its products.
+    auto put_row = [&](const Row4<D>& x, int kb) {
       uint32_t top = 0;
       bool bad = false;
 #pragma unroll
@@ -607,7 +620,7 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 2 : 3)
         const uint32_t v[4] = {x.w[j].x, x.w[j].y, x.w[j].z, x.w[j].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          sts128(smem_u32(ks) + (kb * kPanels + (j >> 1)) * kPanel + swz(threadIdx.x, (j & 1) * 4 + i, 128), widen<T>(v[i], f));
+          sts128(smem_u32(ks) + (kb * kPanels + (j >> 1)) * kPanel + swz(tid, (j & 1) * 4 + i, 128), widen<T>(v[i], f));
       }
       fence_proxy_async_smem();
       mbar_arrive(&sh.k_full[kb]);
@@ -615,92 +628,119 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 2 : 3)
     };
 
     bool ok = true;
-    int done = 0;
-    int page = page_of(t);
+    int sn = 0;        // products of this group so far
+    int products = 0;  // several: of the CTA
+    float2 sum[2];
+    // The group's weights of one product of item u (query tokens from tok on), lse its row's.
+    auto add_weights = [&](const TileItem& u, int tok, float lse, float unit) {
+      const int info = sn & 1, key = u.begin + tid;
+      const int count = min(p.tile_queries, u.rq.nq - tok) * p.group;
+      const RowInfo o = row_info(p, u.rq, lse, tok + my_tok);
+      sh.last[grp][info][tid] = o.last;
+      float* pair = reinterpret_cast<float*>(&sh.pair[grp][info][tid >> 1]) + (tid & 1);
+      pair[0] = -o.hi;
+      pair[2] = o.r;
+      // all rows see all keys of the item: no comparisons below
+      const bool all = bar_and(bar, kKeys, tid >= count || o.last >= u.end - 1);
+      // a warp whose wait failed goes on to every barrier, so that none is left behind
+      if (ok) {
+        ok = warp_wait(&sh.s_full[grp], uint32_t(sn) & 1u, p.st, forced, abort_flag);
+        if (!ok && lane == 0) *abort_flag = 1;
+      }
+      ++sn;
+      if (!ok) return;
+      tc_fence_after();
+      const float2 unit2 = make_float2(unit, unit);
+      for (int c0 = 0; c0 < count; c0 += 32) {
+        uint32_t s[32];
+        tmem_ld32(row + c0, s);
+        tmem_ld_wait();
+        if (all && c0 + 32 <= count) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float4 hr = sh.pair[grp][info][c0 / 2 + j];
+            const float2 x = ffma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), unit2,
+                                   make_float2(hr.x, hr.y));
+            sum[j & 1] = ffma2(make_float2(fast_exp2(x.x), fast_exp2(x.y)), make_float2(hr.z, hr.w), sum[j & 1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int c1 = c0 + j;
+            if (c1 >= count) continue;
+            const float* hr = reinterpret_cast<const float*>(&sh.pair[grp][info][c1 >> 1]) + (c1 & 1);
+            if (key <= sh.last[grp][info][c1])
+              sum[0].x = fmaf(fast_exp2(fmaf(__uint_as_float(s[j]), unit, hr[0])), hr[2], sum[0].x);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&sh.s_empty[grp]);
+    };
+    auto total = [&]() { return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y); };
+    const int step = single ? 2 : 1;
+    int i = i0 + (single ? grp : 0);
+    if (single && grp == 1 && i < i1) t = next_item(p, t);
+    int page = i < i1 ? page_of(t) : 0;
     float* score = score_at(t, page);
-    float old = old_score(t, score), lse = lse_of(t, 0), unit = p.scale_log2, next_unit = unit;
+    float old = i < i1 ? old_score(t, score) : 0.f;
+    float lse = single ? lse_of(t, 0) : 0.f, unit = p.scale_log2;
     if constexpr (FP4) {
-      if (t.tiles > 0) unit = put_row(read_row(t, page));
+      if (i < i1 && t.tiles > 0 && (single || grp == 0)) {
+        unit = put_row(read_row(t, page), single ? grp : 0);
+        sh.unit[0][tid] = unit;
+      }
+      if (!single) {
+        bar_and(3, 2 * kKeys, true);
+        unit = sh.unit[0][tid];
+      }
     }
-    for (int i = i0; i < i1; ++i) {
-      const int key = t.begin + int(threadIdx.x);
-      const bool more = i + 1 < i1;
-      const TileItem after = i + 2 < i1 ? next_item(p, next) : next;
+    for (; i < i1; i += step) {
+      const bool more = i + step < i1;
+      TileItem next = t;
+      if (more) next = next_item(p, t);
+      if (more && single) next = next_item(p, next);
       const int next_page = more ? page_of(next) : 0;
       float* next_score = score_at(next, next_page);
-      float next_old = 0.f;
+      const float next_old = more ? old_score(next, next_score) : 0.f;
+      float next_unit = unit;
       Row4<D> ahead;
       if constexpr (FP4) {
-        if (more) ahead = read_row(next, next_page);
-        // the other key buffer: the product that read it is done, this thread has its sums
-        if (nk > 1 && more && next.tiles > 0 && ok) next_unit = put_row(ahead);
+        if (more && (single || grp == 0)) ahead = read_row(next, next_page);
       }
-      float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-      const float2 unit2 = make_float2(unit, unit);
-      // a warp whose wait failed goes on to every barrier, so that none is left behind
-      for (int n = 0; n < t.tiles; ++n, ++done) {
-        const int buf = done % nb, info = done & 1;
-        const int count = min(p.tile_queries, t.rq.nq - t.tok0 - n * p.tile_queries) * p.group;
-        const int c = threadIdx.x;
-        const RowInfo o = row_info(p, t.rq, lse, t.tok0 + n * p.tile_queries + my_tok);
-        sh.last[info][c] = o.last;
-        float* pair = reinterpret_cast<float*>(&sh.pair[info][c >> 1]) + (c & 1);
-        pair[0] = -o.hi;
-        pair[2] = o.r;
-        lse = n + 1 < t.tiles ? lse_of(t, n + 1) : more ? lse_of(next, 0) : 0.f;
-        // all rows see all keys of the tile: no comparisons below
-        const bool all = bar_and(1, kKeys, c >= count || o.last >= t.end - 1);
-        if (ok) {
-          ok = warp_wait(&sh.s_full[buf], uint32_t(done / nb) & 1u, p.st, forced, abort_flag);
-          if (!ok && lane == 0) *abort_flag = 1;
+      sum[0] = sum[1] = make_float2(0.f, 0.f);
+      float w = 0.f;
+      if (single) {
+        const float next_lse = more ? lse_of(next, 0) : 0.f;
+        if (t.tiles > 0) add_weights(t, t.tok0, lse, unit);
+        w = total();
+        if constexpr (FP4) {  // the group's product has read its key buffer
+          if (more && next.tiles > 0 && ok) next_unit = put_row(ahead, grp);
         }
-        if (!ok) continue;
-        tc_fence_after();
-        if (n == t.tiles - 1) {
-          if constexpr (FP4) {
-            if (nk == 1 && more && next.tiles > 0) next_unit = put_row(ahead);  // the product has read the keys
-          }
-        }
-        for (int c0 = 0; c0 < count; c0 += 64) {
-          uint32_t s[64];
-          tmem_ld32(row + buf * 128 + c0, s);
-          tmem_ld32(row + buf * 128 + c0 + 32, s + 32);
-          tmem_ld_wait();
-          if (all && c0 + 64 <= count) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float4 hr = sh.pair[info][c0 / 2 + j];
-              const float2 x = ffma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), unit2,
-                                     make_float2(hr.x, hr.y));
-              sum[j & 1] = ffma2(make_float2(fast_exp2(x.x), fast_exp2(x.y)), make_float2(hr.z, hr.w), sum[j & 1]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 64; ++j) {
-              const int c1 = c0 + j;
-              if (c1 >= count) continue;
-              const float* hr = reinterpret_cast<const float*>(&sh.pair[info][c1 >> 1]) + (c1 & 1);
-              if (key <= sh.last[info][c1])
-                sum[0].x = fmaf(fast_exp2(fmaf(__uint_as_float(s[j]), unit, hr[0])), hr[2], sum[0].x);
-            }
-          }
-        }
-        tc_fence_before();
-        mbar_arrive(&sh.s_empty[buf]);
-      }
-      if (t.tiles == 0) {  // no query sees these keys: the scores only fade
-        lse = more ? lse_of(next, 0) : 0.f;
+        lse = next_lse;
+      } else {
+        for (int n = 0; n < t.tiles; ++n)
+          if (((products + n) & 1) == grp) add_weights(t, t.tok0 + n * p.tile_queries, lse_of(t, n), unit);
+        products += t.tiles;
+        w = total();
+        const int par = (i - i0) & 1;
+        if (grp == 1) sh.part[par][tid] = w;
         if constexpr (FP4) {
-          if (nk == 1 && more && next.tiles > 0 && ok) next_unit = put_row(ahead);
+          if (grp == 0 && more && next.tiles > 0 && ok) {
+            // the item's last product, of either group, has read the key buffer
+            const int last = products - 1;
+            if (t.tiles > 0) ok = warp_wait(&sh.s_full[last & 1], uint32_t(last >> 1) & 1u, p.st, forced, abort_flag);
+            if (ok) sh.unit[par ^ 1][tid] = put_row(ahead, 0);
+          }
+        }
+        bar_and(3, 2 * kKeys, true);
+        if (grp == 0) w += sh.part[par][tid];
+        if constexpr (FP4) {
+          if (more && next.tiles > 0) next_unit = sh.unit[par ^ 1][tid];
         }
       }
-      if (more) next_old = old_score(next, next_score);
-      if (key < t.end && ok) {
-        const float w = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        *score = is_fresh(t) ? w : fmaf(p.decay, old, w);
-      }
+      if (t.begin + tid < t.end && ok && (single || grp == 0)) *score = is_fresh(t) ? w : fmaf(p.decay, old, w);
       t = next;
-      next = after;
       score = next_score;
       old = next_old;
       unit = next_unit;
@@ -709,7 +749,7 @@ __global__ void __launch_bounds__(kTileThreads, D == 128 ? 2 : 3)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 4) tmem_dealloc(tmem, cols);
+  if (warp == 8) tmem_dealloc(tmem, kCols);
 }
 
 template <typename T, int D, int NT, bool FP4>
@@ -727,7 +767,7 @@ bskv_status launch_tile(const bskv_plan* plan, WeightsParams& wp, cudaStream_t s
   const int ps = plan->page_size;
   wp.box = ps % 128 == 0 ? 128 : ps % 64 == 0 ? 64 : ps % 32 == 0 ? 32 : ps % 16 == 0 ? 16 : 8;
   wp.tile_queries = std::min(kKeys / wp.group, plan->q_len);
-  wp.buffers = plan->q_len > wp.tile_queries ? 2 : 1;
+  wp.single = plan->q_len <= wp.tile_queries;
   const CUtensorMapDataType dt = __is_same(T, __half) ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap qmap, kmap{};
   const uint64_t qd[3] = {D, uint64_t(plan->num_qo_heads), uint64_t(plan->M)};
@@ -744,8 +784,7 @@ bskv_status launch_tile(const bskv_plan* plan, WeightsParams& wp, cudaStream_t s
   auto kern = weights_tile_kernel<T, D, FP4>;
   static std::atomic<int> allowed[64];
   if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "attn_weights: cudaFuncSetAttribute")) return s;
-  // as many CTAs as the GPU holds: by shared memory and by TMEM (128 columns a buffer)
-  const int per_sm = wp.buffers > 1 || D == 128 ? 2 : 3;
+  const int per_sm = 2;  // by shared memory (96 KB for 128 dims) and TMEM (256 columns)
   wp.num_requests = meta_word(plan, H_MERGES);
   wp.num_items = meta_word(plan, H_UNITS);
   wp.queries = FastDiv(wp.tile_queries);
