@@ -197,11 +197,11 @@ struct bskv_plan {
   // (kDecodeStartWords each), or -1
   int32_t decode_starts = -1;
   int32_t walk_records = -1;  // word offset of the walk records (tile records), or -1
-  int32_t num_sms = 0;        // attn_weights: SM count of the target GPU
+  int32_t num_sms = 0;        // attn_weights, evict: SM count of the target GPU
   // evict: tokens that stay over all requests, protected first / last tokens, the longest
   // request, whether the kept rows stay in their pages, CTAs that share the rows of one slice
   int64_t kept_total = 0;
-  int32_t sink = 0, recent = 0, longest = 0, in_place = 0, parts = 1;
+  int32_t sink = 0, recent = 0, longest = 0, most = 0, in_place = 0;
   // set by bskv_plan_upload
   const int32_t* meta_dev = nullptr;
   int32_t* counters_dev = nullptr;  // one merge counter per merge item, zero between runs

@@ -856,9 +856,8 @@ extern "C" bskv_status bskv_plan_evict(const int32_t* kv_indptr, const int32_t* 
   p->num_qo_heads = num_kv_heads; p->num_kv_heads = num_kv_heads; p->head_dim = head_dim;
   p->kept_total = total; p->sink = sink; p->recent = recent; p->longest = int32_t(longest);
   p->in_place = in_place ? 1 : 0;
-  // enough CTAs per slice to fill the GPU's eight 256-thread CTAs per SM, a wave of 512 rows each
-  const int64_t slices = std::max<int64_t>(1, int64_t(batch) * num_kv_heads * (head_dim / 16));
-  p->parts = int32_t(std::max<int64_t>(1, std::min<int64_t>((most + 511) / 512, int64_t(num_sms) * 8 / slices)));
+  p->most = int32_t(most);
+  p->num_sms = num_sms;
   std::vector<int32_t> none;
   assemble(p, KIND_EVICT, batch, dst, reqs, 0, none, 0, kv_indptr,
            batch > 0 ? size_t(batch) + 1 : 0, kv_indices, size_t(nnz), batch, 0);
