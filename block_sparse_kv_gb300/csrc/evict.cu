@@ -97,94 +97,6 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
   __shared__ __align__(8) int counts[2];
   __shared__ uint32_t found_digit;
   __shared__ int found_rest;
-// compaction of their rows.
-//
-// Selection. Per (request, kv head): the first `sink` and the last `recent` tokens stay, and of
-// the others the k of highest score (NaN above everything, -0 = +0, the lowest slot among equals).
-// Scores become 32-bit keys of the same order; three histogram passes (11, 11 and 10 bits) find
-// the k-th largest key T, and one pass in slot order keeps the keys above T and the first ones
-// equal to it. Counts are integers, so the result does not depend on the order of the atomics.
-//
-// Compaction. Kept tokens move to the front in their order: row j comes from slot kept[j] >= j.
-// Within one cache it is done in place: rows are taken in waves of ascending j, every read of a
-// wave before its first write (one barrier), and a later wave only reads slots above every slot
-// written so far. A wave's rows therefore never meet, so column slices of the rows (64 bytes of
-// K or of V of a head), the scores and the 4-bit scales each go through their waves on their own
-// CTA. Into other pages there is nothing to order and the rows are split over CTAs too.
-#include <algorithm>
-
-#include "common.cuh"
-#include "fp4.cuh"
-#include "internal.h"
-#include "launch.h"
-
-namespace bskv {
-namespace {
-
-using namespace dev;
-
-struct EvictParams {
-  const int32_t* meta;
-  float* scores;
-  int64_t w_s0, w_s1;  // floats: page, kv head
-  int32_t* kept;
-  int64_t total;       // kept tokens over all requests
-  FastDiv page_size;
-  int off_req, off_src, off_src_ptr, off_dst;
-  int sink, recent, in_place;
-  int held;            // selection: groups of four keys of a CTA that shared memory holds
-  int block, planes;   // compaction: rows per CTA when copying, column slices
-};
-
-// {tokens, kept tokens, first of them in `kept`, first destination page entry}
-__device__ __forceinline__ int4 request_of(const EvictParams& p, int b) {
-  return __ldg(reinterpret_cast<const int4*>(p.meta + p.off_req) + b);
-}
-
-// ---------------------------------------------------------------------------------------
-// selection
-// ---------------------------------------------------------------------------------------
-
-constexpr int kBins = 2048;
-constexpr int kSelectFours = 8192;  // most groups of four keys that a CTA's shared memory holds; more are read again
-constexpr int kMaxCluster = 8;      // the portable size
-constexpr int kClusterTokens = 2048;  // least tokens of a CTA of a cluster
-
-__device__ __forceinline__ uint32_t order_key(float x) {
-  const uint32_t u = __float_as_uint(x + 0.f);  // -0 becomes +0
-  if (x != x) return 0xffffffffu;
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-// Sum over the threads below of one value per thread; the sums go through warp_sums[32].
-template <int THREADS>
-__device__ __forceinline__ int block_scan(int v, int* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  const int s = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0);
-  return s + x - v;
-}
-
-// One (request, kv head) per cluster of `ctas` CTAs, each with a contiguous part of the tokens, four
-// of a page to a thread at a time. Protected tokens among them get the key 0, below every score's.
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_constant__ EvictParams p, int ctas) {
-  constexpr int kWarps = THREADS / 32, kPer = kBins / THREADS;  // bins per thread
-  extern __shared__ uint4 keys[];
-  const bool cluster = THREADS >= kBins / 2 && ctas > 1;  // a bin of a cluster CTA's share per thread
-  __shared__ __align__(16) int hist[2][kBins];
-  __shared__ int sums[kBins / 2], totals[kMaxCluster];  // a cluster's bins: this CTA's share, each share's total
-  __shared__ int warp_sums[32], warp_eq[32];
-  __shared__ __align__(8) int counts[2];
-  __shared__ uint32_t found_digit;
-  __shared__ int found_rest;
   const int b = blockIdx.z, h = blockIdx.y, rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t* pages = p.meta + p.off_src + __ldg(p.meta + p.off_src_ptr + b);
   const int4 rq = request_of(p, b);
@@ -219,7 +131,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
   auto key = [&](int i) { return held ? keys[i] : load(i); };
   auto all_sync = [&]() {
     __syncwarp();
-    if (ctas > 1) cluster_sync();
+    if (cluster) cluster_sync();
     else __syncthreads();
   };
 
@@ -246,7 +158,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
     }
     all_sync();
     // thread i's bins are below those of the threads before it: sums over these are of larger keys
-    if (ctas > 1) {
+    if (cluster) {
       // each CTA adds up its share of the bins over the cluster; the total says whose share has T's digit
       const int bins = kBins / ctas;
       int sum = 0;
@@ -320,7 +232,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
   const int wa = lane < kWarps ? warp_sums[lane] : 0, we = lane < kWarps ? warp_eq[lane] : 0;
   int at = __reduce_add_sync(0xffffffffu, lane < warp ? wa : 0);
   int eq = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0);
-  if (ctas > 1) {
+  if (cluster) {
     if (warp == 0) {
       const int a = __reduce_add_sync(0xffffffffu, wa), e = __reduce_add_sync(0xffffffffu, we);
       if (lane == 0) {
@@ -365,7 +277,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
     for (int u = 0; u < 4; ++u)
       if (stay[u]) kept[to++] = base + 4 * i + u;
   }
-  if (ctas > 1) {
+  if (cluster) {
     __syncwarp();
     cluster_wait();
   }
