@@ -18,11 +18,15 @@
 // Within one cache it is done in place: rows are taken in waves of ascending j, every read of a
 // wave before its first write (one barrier), and a later wave only reads slots above every slot
 // written so far, which is why it may be read before that. A wave's rows therefore never meet, so
-// K, V, the scores and the 4-bit scales each go through their waves on their own CTA. Into other
-// pages there is nothing to order and blocks of rows have CTAs too. Bound by memory: of the widths
-// 64, 128 and 256 bytes per row and CTA, whole rows were fastest in place (138, 115 and 104 us), and
-// eight CTAs per SM with two rows a thread ahead of four with four (104 and 113 us), for all that
-// 32 registers a thread spill some. 537 MB in place in 90 us: 5.9 TB/s.
+// K, V, the scores and the 4-bit scales each go through their waves on their own CTA, or, where
+// there are few requests, on a cluster of up to 8 that shares the waves (131072 tokens of 8 heads
+// halved: 151 us; 8 requests of 8192 tokens halved: 150 us on one CTA each, 64 us on 4). The cluster's barrier need not release anything: a read has returned its value
+// before its thread arrives, and nobody reads what another CTA wrote (a releasing arrival waits
+// for the last writes: 272 and 93 us). Into other pages there is nothing to order and blocks of
+// rows have CTAs too.
+// Bound by memory: of the widths 64, 128 and 256 bytes per row and CTA, whole rows were fastest in
+// place (138, 115 and 104 us), and eight CTAs per SM with two rows a thread ahead of four with
+// four (104 and 113 us). 537 MB in place in 83 us: 6.4 TB/s.
 #include <algorithm>
 
 #include "common.cuh"
@@ -45,7 +49,7 @@ struct EvictParams {
   int off_req, off_src, off_src_ptr, off_dst;
   int sink, recent, in_place;
   int held;            // selection: groups of four keys of a CTA that shared memory holds
-  int block, planes;   // compaction: rows per CTA when copying, column slices
+  int planes;          // compaction: column slices
 };
 
 // {tokens, kept tokens, first of them in `kept`, first destination page entry}
@@ -288,8 +292,9 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
 // ---------------------------------------------------------------------------------------
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 2;      // rows a thread holds between a wave's reads and its writes
 constexpr int kMoveTable = 1024;  // rows whose places a CTA looks up at a time
+constexpr int kMoveBlock = 256;   // rows per CTA when copying
+constexpr int kMoveShare = 1024;  // least rows of a CTA of a cluster
 
 // One column slice of a paged tensor's rows: 2^shift units per row (16, 4 or 2 bytes each).
 struct Plane {
@@ -303,47 +308,58 @@ struct MoveParams {
   Plane plane[kMaxPlanes];
 };
 
-constexpr int kMoveBlock = 256;   // rows per CTA when copying
 struct Places {
   int64_t from[kMoveTable], to[kMoveTable];  // bytes from the plane's base; to < 0: stays
 };
 
-// Rows [0, n) of the table. The next wave is read before the barrier and writes of this one.
-template <typename U>
-__device__ __forceinline__ void move_rows(const Places& at, uint8_t* base, int shift, int n, bool in_place) {
-  const int row = threadIdx.x >> shift, per = kMoveThreads >> shift, wave = per * kMoveRows;
+// The table's rows [0, n) in waves of ROWS per thread. The next wave is read before the barrier and
+// the writes of this one.
+template <typename U, int ROWS, typename Arrive, typename Wait>
+__device__ __forceinline__ void move_rows(const Places& at, uint8_t* base, int shift, int n, Arrive arrive, Wait wait) {
+  const int row = threadIdx.x >> shift, per = kMoveThreads >> shift, wave = per * ROWS;
   base += (threadIdx.x & ((1 << shift) - 1)) * sizeof(U);
-  auto read = [&](U (&x)[kMoveRows], int w) {
+  auto read = [&](U (&x)[ROWS], int w) {
 #pragma unroll
-    for (int i = 0; i < kMoveRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       const int j = w + i * per + row;
       if (j < n && at.to[j] >= 0) x[i] = *reinterpret_cast<const U*>(base + at.from[j]);
     }
   };
-  auto write = [&](const U (&x)[kMoveRows], int w) {
+  auto write = [&](const U (&x)[ROWS], int w) {
 #pragma unroll
-    for (int i = 0; i < kMoveRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       const int j = w + i * per + row;
       if (j < n && at.to[j] >= 0) *reinterpret_cast<U*>(base + at.to[j]) = x[i];
     }
   };
-  U x0[kMoveRows], x1[kMoveRows];
+  U x0[ROWS] = {}, x1[ROWS] = {};
   read(x0, 0);
   for (int w = 0; w < n; w += 2 * wave) {
+    arrive(x0);
     read(x1, w + wave);
-    if (in_place) __syncthreads();  // every read of the wave before its first write
+    wait();  // every read of the wave before its first write
     write(x0, w);
     if (w + wave >= n) break;
+    arrive(x1);
     read(x0, w + 2 * wave);
-    if (in_place) __syncthreads();
+    wait();
     write(x1, w + wave);
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads, 8) evict_move_kernel(const __grid_constant__ MoveParams mp) {
+__device__ __forceinline__ uint32_t first_word(uint4 x) { return x.x; }
+__device__ __forceinline__ uint32_t first_word(uint32_t x) { return x; }
+
+// SHARED: a slice's waves are spread over a cluster of `ctas` CTAs, in place.
+template <bool SHARED>
+__global__ void __launch_bounds__(kMoveThreads, SHARED ? 2 : 8)
+    evict_move_kernel(const __grid_constant__ MoveParams mp, int ctas) {
+  constexpr int kRows = SHARED ? 8 : 2;
   __shared__ Places at;
+  __shared__ volatile uint32_t seen[SHARED ? kMoveThreads : 1];
   const EvictParams& p = mp.e;
-  const Plane& pl = mp.plane[blockIdx.x % p.planes];
+  const int rank = SHARED ? blockIdx.x % ctas : 0;
+  const Plane& pl = mp.plane[SHARED ? blockIdx.x / ctas : blockIdx.x % p.planes];
   const int h = blockIdx.y, b = blockIdx.z;
   const int4 rq = request_of(p, b);
   const int K = rq.y;
@@ -352,24 +368,68 @@ __global__ void __launch_bounds__(kMoveThreads, 8) evict_move_kernel(const __gri
   const int32_t* src_pages = p.meta + p.off_src + __ldg(p.meta + p.off_src_ptr + b);
   const int32_t* dst_pages = p.meta + p.off_dst + rq.w;
   uint8_t* base = pl.base + h * pl.s_head;
-  const int j0 = blockIdx.x / p.planes * p.block;
-  const int j1 = p.in_place ? K : min(K, j0 + p.block);
-  for (int j = j0; j < j1; j += kMoveTable) {
-    const int n = min(kMoveTable, j1 - j);
-    if (j > j0) __syncthreads();
+  // CTA `rank` of a cluster has the rows [wave * rank, wave * (rank + 1)) of every wave * ctas
+  const int wave = min(kMoveTable, (kMoveThreads >> pl.shift) * kRows), turn = __ffs(wave) - 1;
+  const int j0 = SHARED || p.in_place ? 0 : blockIdx.x / p.planes * kMoveBlock;
+  const int j1 = SHARED || p.in_place ? K : min(K, j0 + kMoveBlock);
+  const int total = SHARED ? (K + wave * ctas - 1) / (wave * ctas) * wave : j1 - j0;  // rows of this CTA
+  for (int r0 = 0; r0 < total; r0 += kMoveTable) {
+    const int n = min(kMoveTable, total - r0);
+    if (r0 > 0) __syncthreads();
 #pragma unroll 4
     for (int i = threadIdx.x; i < n; i += kMoveThreads) {
-      const int s = __ldcg(kept + j + i);
-      int ss, ds;
-      const int sn = p.page_size.divmod(s, ss), dn = p.page_size.divmod(j + i, ds);
-      at.from[i] = __ldg(src_pages + sn) * pl.s0 + ss * pl.s_slot;
-      at.to[i] = p.in_place && s == j + i ? -1 : __ldg(dst_pages + dn) * pl.s0 + ds * pl.s_slot;
+      const int r = r0 + i, j = SHARED ? ((((r >> turn) * ctas + rank) << turn) | (r & (wave - 1))) : j0 + r;
+      const int s = j < j1 ? __ldcg(kept + j) : j;
+      int64_t from = 0, to = -1;
+      if (j < j1 && !(p.in_place && s == j)) {
+        int ss, ds;
+        const int sn = p.page_size.divmod(s, ss), dn = p.page_size.divmod(j, ds);
+        from = __ldg(src_pages + sn) * pl.s0 + ss * pl.s_slot;
+        to = __ldg(dst_pages + dn) * pl.s0 + ds * pl.s_slot;
+      }
+      at.from[i] = from;
+      at.to[i] = to;
     }
     __syncthreads();
-    if (pl.unit == 16) move_rows<uint4>(at, base, pl.shift, n, p.in_place);
-    else if (pl.unit == 4) move_rows<uint32_t>(at, base, pl.shift, n, p.in_place);
-    else move_rows<uint16_t>(at, base, pl.shift, n, p.in_place);
+    auto arrive = [&](const auto& x) {
+      if constexpr (SHARED) {  // with the values in hand: shared memory gets a word made of each
+        uint32_t all = 0;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) all ^= first_word(x[i]);
+        seen[threadIdx.x] = all;
+        __syncwarp();
+        cluster_arrive_relaxed();
+      }
+    };
+    auto wait = [&]() {
+      if constexpr (SHARED) {
+        __syncwarp();
+        cluster_wait();
+      } else if (p.in_place) {
+        __syncthreads();
+      }
+    };
+    if (pl.unit == 16) move_rows<uint4, kRows>(at, base, pl.shift, n, arrive, wait);
+    else if (pl.unit == 4) move_rows<uint32_t, kRows>(at, base, pl.shift, n, arrive, wait);
+    else move_rows<uint16_t, kRows>(at, base, pl.shift, n, arrive, wait);
   }
+}
+
+// Launches kern(params, ctas) with clusters of `ctas` CTAs along x.
+template <typename P>
+cudaError_t launch_clusters(void (*kern)(P, int), dim3 grid, int threads, size_t smem, int ctas, const P& params,
+                            cudaStream_t st) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {unsigned(ctas), 1, 1};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, params, ctas);
 }
 
 template <int THREADS>
@@ -378,17 +438,8 @@ bskv_status select(const EvictParams& e, const bskv_plan* plan, int ctas, size_t
   static std::atomic<int> allowed[64];
   if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "evict: cudaFuncSetAttribute"))
     return s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {unsigned(ctas), 1, 1};
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(ctas), unsigned(plan->num_kv_heads), unsigned(plan->batch));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, kern, e, ctas), "evict select launch");
+  const dim3 grid(unsigned(ctas), unsigned(plan->num_kv_heads), unsigned(plan->batch));
+  return cuda_check(launch_clusters<EvictParams>(kern, grid, THREADS, smem, ctas, e, st), "evict select launch");
 }
 
 bskv_status run(const char* who, const bskv_plan* plan, float* scores, const int64_t* scores_strides,
@@ -421,10 +472,14 @@ bskv_status run(const char* who, const bskv_plan* plan, float* scores, const int
   const bool big = ctas > 1 || share > 512;
   if (bskv_status s = big ? select<1024>(e, plan, ctas, smem, st) : select<256>(e, plan, ctas, smem, st)) return s;
   e.planes = planes;
-  e.block = kMoveBlock;
-  const int parts = plan->in_place ? 1 : (plan->most + kMoveBlock - 1) / kMoveBlock;
-  evict_move_kernel<<<dim3(unsigned(planes * parts), unsigned(plan->num_kv_heads), unsigned(plan->batch)),
-                      kMoveThreads, 0, st>>>(mp);
+  ctas = 1;
+  while (plan->in_place && ctas < kMaxCluster && plan->most / (2 * ctas) >= kMoveShare && rows * planes * ctas <= 4 * plan->num_sms)
+    ctas *= 2;
+  const int parts = plan->in_place ? ctas : (plan->most + kMoveBlock - 1) / kMoveBlock;
+  const dim3 grid(unsigned(planes * parts), unsigned(plan->num_kv_heads), unsigned(plan->batch));
+  if (ctas > 1)
+    return cuda_check(launch_clusters<MoveParams>(evict_move_kernel<true>, grid, kMoveThreads, 0, ctas, mp, st), "evict move launch");
+  evict_move_kernel<false><<<grid, kMoveThreads, 0, st>>>(mp, 1);
   return cuda_check(cudaGetLastError(), "evict move launch");
 }
 
@@ -456,9 +511,14 @@ extern "C" bskv_status bskv_run_evict(const bskv_plan* plan, float* scores,
   }
   MoveParams mp{};
   int planes = 0;
+  // whole rows, or 64 bytes of them where few long requests would leave SMs idle
+  const bool narrow = plan->in_place && plan->most >= 2 * kMoveShare &&
+                      int64_t(plan->batch) * plan->num_kv_heads * plan->head_dim / 16 <= plan->num_sms / kMaxCluster;
+  const int cols = narrow ? 64 : 2 * plan->head_dim;
   for (int which = 0; which < 2; ++which)
-    mp.plane[planes++] = Plane{static_cast<uint8_t*>(kv_cache) + 2 * which * kv_strides[1], 2 * kv_strides[0],
-                               2 * kv_strides[2], 2 * kv_strides[3], 16, plan->head_dim == 128 ? 4 : 3};
+    for (int col = 0; col < 2 * plan->head_dim; col += cols)
+      mp.plane[planes++] = Plane{static_cast<uint8_t*>(kv_cache) + 2 * which * kv_strides[1] + col, 2 * kv_strides[0],
+                                 2 * kv_strides[2], 2 * kv_strides[3], 16, narrow ? 2 : plan->head_dim == 128 ? 4 : 3};
   return run(who, plan, scores, scores_strides, kept, compact_scores != 0, mp, planes,
              static_cast<cudaStream_t>(stream));
 }

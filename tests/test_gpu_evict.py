@@ -93,6 +93,30 @@ def test_evict(cuda, case, place, four):
     _same(cuda, s, lens, ps, Hkv, D, keep, sink, recent, compact=not four or place == "copy")
 
 
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("lens, keep, Hkv, D", [
+    ([20011], [17001], 1, 128),            # a cluster of eight CTAs, slices of 64 bytes
+    ([9000, 9, 6007], [7000, 9, 6000], 4, 128),
+    ([5000, 4999], [4990, 2100], 2, 64),   # two CTAs
+    ([4097], [1], 1, 64),
+])
+def test_evict_long_in_place(cuda, lens, keep, Hkv, D, four):
+    """Waves of rows and shares of scores that several CTAs take."""
+    s = _setup(lens, 16, Hkv, D, 941, four)
+    _same(cuda, s, lens, 16, Hkv, D, keep, 1, 0, True)
+
+
+def test_evict_more_scores_than_shared_memory(cuda):
+    """Scores that a cluster's shared memory cannot hold are read in every pass."""
+    L, keep, ps = 270007, 3, 64
+    s = _setup([L], ps, 1, 64, 951, True, [keep])
+    rows = s["scores"][s["indices"].long(), 0].reshape(-1)[:L]
+    p = bskv.bskv_plan_evict(s["indptr"], s["indices"], s["last"], [keep], 0, 0, s["pages"], ps, 1, 64,
+                             s["dst_indptr"], s["dst_indices"])
+    kept = bskv.bskv_run_evict_fp4(p, s["scores"].to(cuda), *[x.to(cuda) for x in s["pools"]])
+    assert kept.cpu().tolist() == [sorted(torch.sort(rows, descending=True, stable=True).indices[:keep].tolist())]
+
+
 def test_evict_order_of_scores(cuda):
     """Equal scores, both zeros, NaN, infinities and subnormals: NaN first, then by value, the
     lowest slot among equals, at every cut."""
