@@ -188,6 +188,7 @@ class Plan:
         self._h = ctypes.c_void_p(handle)
         self.kind = kind
         self.info = info
+        self.layouts = {}  # of tensors that passed a run's checks
         self.int_ws = None
         self.float_ws = None
 
@@ -684,7 +685,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
 
 def _call(fn, dev, *args):
     """The C entry point `fn` on the current stream of the tensors' device."""
-    entry = getattr(load_library(), fn)
+    entry = getattr(_lib or load_library(), fn)
     if torch.cuda.current_device() == dev.index:
         code = entry(*args, _raw_stream(dev.index))
     else:
@@ -713,9 +714,29 @@ _U8, _I32T, _F32T = (torch.uint8,), (torch.int32,), (torch.float32,)
 _HALVES = (torch.bfloat16, torch.float16)
 
 
+_call_layouts = {}
+
+
+def _once(memo, check, fn, owner, *tensors):
+    """check(fn, owner, *tensors), which depends on nothing but the memo's owner and the tensors'
+    shapes, strides, types and devices: the answer is kept for calls with the same ones."""
+    try:
+        key = (fn,) + tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+                             for t in tensors])
+    except AttributeError:  # not tensors; the check says which
+        return check(fn, owner, *tensors)
+    found = memo.get(key)
+    if found is None:
+        found = check(fn, owner, *tensors)
+        if len(memo) >= 1024:
+            memo.clear()
+        memo[key] = found
+    return found
+
+
 def _fp4_cache(fn, kv_codes, kv_scales, device, num_pages, page_size, num_kv_heads, head_dim,
                written=False):
-    """Checks a 4-bit cache; its pointers and strides as the C entry points take them."""
+    """Checks a 4-bit cache; its strides as the C entry points take them."""
     _want(fn, "kv_codes", kv_codes, (num_pages, 2, num_kv_heads, page_size, head_dim // 2), _U8, device)
     _want(fn, "kv_scales", kv_scales, (num_pages, 2, num_kv_heads, page_size, head_dim // 32), _U8,
           device)
@@ -723,7 +744,7 @@ def _fp4_cache(fn, kv_codes, kv_scales, device, num_pages, page_size, num_kv_hea
     _rows_last(fn, "kv_scales", kv_scales, written)
     if page_size > 1 and kv_scales.stride(3) != head_dim // 32 and kv_scales.numel():
         raise ValueError("%s: the slots of kv_scales must be contiguous" % fn)
-    return kv_codes.data_ptr(), _strides_of(kv_codes, 4), kv_scales.data_ptr(), _strides_of(kv_scales, 3)
+    return _strides_of(kv_codes, 4), _strides_of(kv_scales, 3)
 
 
 def _fp4_rows(fn, k, v, dtypes, batch_indices, positions, kv_indptr, kv_indices, written=False):
@@ -754,14 +775,23 @@ def bskv_quantize_fp4_append_paged(k, v, batch_indices, positions, kv_indptr, kv
     Hkv, page_size, D / 2], kv_scales [pages, 2, Hkv, page_size, D / 32] (uint8), through the
     device page table (all int32)."""
     fn = "bskv_quantize_fp4_append_paged"
+    dev, ks, vs, dtype, rows, cache, batch = _once(
+        _call_layouts, _check_append, fn, None, k, v, batch_indices, positions, kv_indptr, kv_indices,
+        kv_codes, kv_scales)
+    _call(fn, dev, k.data_ptr(), ks, v.data_ptr(), vs, dtype, *rows, batch_indices.data_ptr(),
+          positions.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(), *batch,
+          kv_codes.data_ptr(), cache[0], kv_scales.data_ptr(), cache[1])
+
+
+def _check_append(fn, _, k, v, batch_indices, positions, kv_indptr, kv_indices, kv_codes,
+                  kv_scales):
     dev, nnz, heads, dim, batch = _fp4_rows(fn, k, v, _HALVES, batch_indices, positions, kv_indptr,
                                             kv_indices)
     _want(fn, "kv_codes", kv_codes, (None, 2, heads, None, dim // 2), _U8, dev)
     pages, _, _, page_size, _ = kv_codes.shape
     cache = _fp4_cache(fn, kv_codes, kv_scales, dev, pages, page_size, heads, dim, written=True)
-    _call(fn, dev, k.data_ptr(), _strides_of(k, 2), v.data_ptr(), _strides_of(v, 2), _DT[k.dtype],
-          nnz, heads, dim, batch_indices.data_ptr(), positions.data_ptr(), kv_indptr.data_ptr(),
-          kv_indices.data_ptr(), batch, page_size, pages, *cache)
+    return (dev, _strides_of(k, 2), _strides_of(v, 2), _DT[k.dtype], (nnz, heads, dim), cache,
+            (batch, page_size, pages))
 
 
 def bskv_dequantize_fp4_paged(kv_codes, kv_scales, batch_indices, positions, kv_indptr, kv_indices,
@@ -770,23 +800,35 @@ def bskv_dequantize_fp4_paged(kv_codes, kv_scales, batch_indices, positions, kv_
     fp32), row i being token positions[i] of request batch_indices[i]. Rows whose token is out of
     range are left as they were (unspecified in outputs that are made here)."""
     fn = "bskv_dequantize_fp4_paged"
-    dev = _cuda_of(fn, "kv_codes", kv_codes)
-    if kv_codes.dim() != 5 or not isinstance(positions, torch.Tensor):
-        raise ValueError("%s: kv_codes must be [pages, 2, Hkv, page_size, D / 2]" % fn)
-    pages, _, heads, page_size, half = kv_codes.shape
     if (k_out is None) != (v_out is None):
         raise ValueError("%s: give both outputs or neither" % fn)
     if k_out is None:
-        shape = (positions.numel(), heads, 2 * half)
+        dev = _cuda_of(fn, "kv_codes", kv_codes)
+        if kv_codes.dim() != 5 or not isinstance(positions, torch.Tensor):
+            raise ValueError("%s: kv_codes must be [pages, 2, Hkv, page_size, D / 2]" % fn)
+        shape = (positions.numel(), kv_codes.shape[2], 2 * kv_codes.shape[4])
         k_out = torch.empty(shape, dtype=dtype, device=dev)
         v_out = torch.empty(shape, dtype=dtype, device=dev)
-    _, nnz, heads, dim, batch = _fp4_rows(fn, k_out, v_out, _HALVES + _F32T, batch_indices, positions,
-                                          kv_indptr, kv_indices, written=True)
-    cache = _fp4_cache(fn, kv_codes, kv_scales, k_out.device, pages, page_size, heads, dim)
-    _call(fn, dev, *cache, batch_indices.data_ptr(), positions.data_ptr(), kv_indptr.data_ptr(),
-          kv_indices.data_ptr(), batch, page_size, pages, k_out.data_ptr(), _strides_of(k_out, 2),
-          v_out.data_ptr(), _strides_of(v_out, 2), _DT[k_out.dtype], nnz, heads, dim)
+    dev, ks, vs, out_dtype, rows, cache, batch = _once(
+        _call_layouts, _check_dequantize, fn, None, k_out, v_out, batch_indices, positions, kv_indptr, kv_indices,
+        kv_codes, kv_scales)
+    _call(fn, dev, kv_codes.data_ptr(), cache[0], kv_scales.data_ptr(), cache[1],
+          batch_indices.data_ptr(), positions.data_ptr(), kv_indptr.data_ptr(),
+          kv_indices.data_ptr(), *batch, k_out.data_ptr(), ks, v_out.data_ptr(), vs, out_dtype, *rows)
     return k_out, v_out
+
+
+def _check_dequantize(fn, _, k, v, batch_indices, positions, kv_indptr, kv_indices, kv_codes,
+                      kv_scales):
+    dev = _cuda_of(fn, "kv_codes", kv_codes)
+    if kv_codes.dim() != 5:
+        raise ValueError("%s: kv_codes must be [pages, 2, Hkv, page_size, D / 2]" % fn)
+    pages, _, _, page_size, _ = kv_codes.shape
+    rows_dev, nnz, heads, dim, batch = _fp4_rows(fn, k, v, _HALVES + _F32T, batch_indices, positions,
+                                                 kv_indptr, kv_indices, written=True)
+    cache = _fp4_cache(fn, kv_codes, kv_scales, rows_dev, pages, page_size, heads, dim)
+    return (dev, _strides_of(k, 2), _strides_of(v, 2), _DT[k.dtype], (nnz, heads, dim), cache,
+            (batch, page_size, pages))
 
 
 def bskv_plan_decode_fp4(kv_indptr, kv_indices, kv_last_page_len, num_pages, page_size,
@@ -825,29 +867,35 @@ def bskv_run_decode_fp4(plan, q, kv_codes, kv_scales, out=None, lse=None, return
     [pages, 2, Hkv, page_size, D / 2], kv_scales [pages, 2, Hkv, page_size, D / 32] uint8."""
     fn = "bskv_run_decode_fp4"
     _check_plan(fn, plan, "decode_fp4")
+    dev, qs, cache, outs, shape = _once(plan.layouts, _check_decode_fp4, fn, plan, q, kv_codes,
+                                        kv_scales, out, lse)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    if lse is None and return_lse:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    _ready(fn, plan, dev)
+    fw = plan.float_ws
+    _call(fn, dev, plan.handle, q.data_ptr(), qs, kv_codes.data_ptr(), cache[0], kv_scales.data_ptr(),
+          cache[1], out.data_ptr(), outs, _ptr(lse), 0.0 if sm_scale is None else float(sm_scale),
+          _ptr(fw), 0 if fw is None else fw.numel())
+    return (out, lse) if return_lse else out
+
+
+def _check_decode_fp4(fn, plan, q, kv_codes, kv_scales, out, lse):
     i = plan.info
     shape, dtypes = i["q_shape"], (i["dtype"],)
     dev = _cuda_of(fn, "q", q)
     _want(fn, "q", q, shape, dtypes, dev)
     _rows_last(fn, "q", q)
-    cache = _fp4_cache(fn, kv_codes, kv_scales, dev, i["num_pages"], i["page_size"],
-                       i["num_kv_heads"], i["head_dim"])
-    if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=dev)
-    else:
+    cache = _fp4_pages(fn, plan, kv_codes, kv_scales, dev)
+    if out is not None:
         _want(fn, "out", out, shape, dtypes, dev)
         _rows_last(fn, "out", out, written=True)
     if lse is not None:
         _want(fn, "lse", lse, shape[:2], _F32T, dev)
         _dense(fn, ("lse", lse))
-    elif return_lse:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
-    _ready(fn, plan, dev)
-    fw = plan.float_ws
-    _call(fn, dev, plan.handle, q.data_ptr(), _strides_of(q, 2), *cache, out.data_ptr(),
-          _strides_of(out, 2), _ptr(lse), 0.0 if sm_scale is None else float(sm_scale), _ptr(fw),
-          0 if fw is None else fw.numel())
-    return (out, lse) if return_lse else out
+    outs = _strides(shape[1] * shape[2], shape[2]) if out is None else _strides_of(out, 2)
+    return dev, _strides_of(q, 2), cache, outs, shape
 
 
 def bskv_plan_attn_weights(qo_indptr, kv_indptr, kv_indices, kv_last_page_len, num_pages, page_size,
@@ -879,7 +927,7 @@ def _scores(fn, plan, scores, device):
     i = plan.info
     _want(fn, "scores", scores, (i["num_pages"], i["num_kv_heads"], i["page_size"]), _F32T, device)
     _rows_last(fn, "scores", scores, written=True)
-    return scores.data_ptr(), _strides_of(scores, 2)
+    return _strides_of(scores, 2)
 
 
 def _kv_pages(fn, plan, kv_cache, dtypes, device, written=False):
@@ -887,7 +935,7 @@ def _kv_pages(fn, plan, kv_cache, dtypes, device, written=False):
     _want(fn, "kv_cache", kv_cache, (i["num_pages"], 2, i["num_kv_heads"], i["page_size"],
                                      i["head_dim"]), dtypes, device)
     _rows_last(fn, "kv_cache", kv_cache, written)
-    return kv_cache.data_ptr(), _strides_of(kv_cache, 4)
+    return (_strides_of(kv_cache, 4),)
 
 
 def _fp4_pages(fn, plan, kv_codes, kv_scales, device, written=False):
@@ -896,18 +944,17 @@ def _fp4_pages(fn, plan, kv_codes, kv_scales, device, written=False):
                       i["num_kv_heads"], i["head_dim"], written)
 
 
-def _run_attn_weights(fn, plan, q, dev, cache, lse, scores, decay, sm_scale):
+def _check_attn_weights(fn, plan, q, lse, scores, *cache):
     i = plan.info
     shape = i["q_shape"]
+    dev = _cuda_of(fn, "q", q)
     _want(fn, "q", q, shape, (i["dtype"],), dev)
     _rows_last(fn, "q", q)
     _want(fn, "lse", lse, shape[:2], _F32T, dev)
     _dense(fn, ("lse", lse))
-    where = _scores(fn, plan, scores, dev)
-    _ready(fn, plan, dev)
-    _call(fn, dev, plan.handle, q.data_ptr(), _strides_of(q, 2), *cache, lse.data_ptr(), *where,
-          float(decay), 0.0 if sm_scale is None else float(sm_scale))
-    return scores
+    strides = _fp4_pages(fn, plan, *cache, dev) if len(cache) == 2 else _kv_pages(
+        fn, plan, *cache, (i["dtype"],), dev)
+    return dev, _strides_of(q, 2), strides, _scores(fn, plan, scores, dev)
 
 
 def bskv_run_attn_weights(plan, q, kv_cache, lse, scores, decay=1.0, sm_scale=None):
@@ -918,18 +965,24 @@ def bskv_run_attn_weights(plan, q, kv_cache, lse, scores, decay=1.0, sm_scale=No
     with decay 0, start anew."""
     fn = "bskv_run_attn_weights"
     _check_plan(fn, plan, "attn_weights")
-    dev = _cuda_of(fn, "q", q)
-    cache = _kv_pages(fn, plan, kv_cache, (plan.info["dtype"],), dev)
-    return _run_attn_weights(fn, plan, q, dev, cache, lse, scores, decay, sm_scale)
+    dev, qs, cache, where = _once(plan.layouts, _check_attn_weights, fn, plan, q, lse, scores, kv_cache)
+    _ready(fn, plan, dev)
+    _call(fn, dev, plan.handle, q.data_ptr(), qs, kv_cache.data_ptr(), cache[0], lse.data_ptr(),
+          scores.data_ptr(), where, float(decay), 0.0 if sm_scale is None else float(sm_scale))
+    return scores
 
 
 def bskv_run_attn_weights_fp4(plan, q, kv_codes, kv_scales, lse, scores, decay=1.0, sm_scale=None):
     """bskv_run_attn_weights over a 4-bit paged cache."""
     fn = "bskv_run_attn_weights_fp4"
     _check_plan(fn, plan, "attn_weights")
-    dev = _cuda_of(fn, "q", q)
-    cache = _fp4_pages(fn, plan, kv_codes, kv_scales, dev)
-    return _run_attn_weights(fn, plan, q, dev, cache, lse, scores, decay, sm_scale)
+    dev, qs, cache, where = _once(plan.layouts, _check_attn_weights, fn, plan, q, lse, scores, kv_codes,
+                                  kv_scales)
+    _ready(fn, plan, dev)
+    _call(fn, dev, plan.handle, q.data_ptr(), qs, kv_codes.data_ptr(), cache[0], kv_scales.data_ptr(),
+          cache[1], lse.data_ptr(), scores.data_ptr(), where, float(decay),
+          0.0 if sm_scale is None else float(sm_scale))
+    return scores
 
 
 def bskv_plan_evict(kv_indptr, kv_indices, kv_last_page_len, keep_len, sink, recent, num_pages,
@@ -970,17 +1023,15 @@ def bskv_plan_evict(kv_indptr, kv_indices, kv_last_page_len, keep_len, sink, rec
                 num_kv_heads=int(num_kv_heads), head_dim=int(head_dim), kept_indptr=kept)
 
 
-def _run_evict(fn, plan, dev, scores, cache, kept, compact_scores):
-    where = _scores(fn, plan, scores, dev)
+def _check_evict(fn, plan, scores, kept, *cache):
+    dev = _cuda_of(fn, "scores", scores)
     shape = (plan.info["num_kv_heads"], plan.info["kept_indptr"][-1])
-    if kept is None:
-        kept = torch.empty(shape, dtype=torch.int32, device=dev)
-    else:
+    if kept is not None:
         _want(fn, "kept", kept, shape, _I32T, dev)
         _dense(fn, ("kept", kept))
-    _ready(fn, plan, dev)
-    _call(fn, dev, plan.handle, *where, int(bool(compact_scores)), *cache, kept.data_ptr())
-    return kept
+    strides = _fp4_pages(fn, plan, *cache, dev, written=True) if len(cache) == 2 else _kv_pages(
+        fn, plan, *cache, _HALVES, dev, written=True)
+    return dev, shape, strides, _scores(fn, plan, scores, dev)
 
 
 def bskv_run_evict(plan, scores, kv_cache, kept=None, compact_scores=True):
@@ -990,18 +1041,27 @@ def bskv_run_evict(plan, scores, kv_cache, kept=None, compact_scores=True):
     kept_indptr[-1]] int32."""
     fn = "bskv_run_evict"
     _check_plan(fn, plan, "evict")
-    dev = _cuda_of(fn, "scores", scores)
-    cache = _kv_pages(fn, plan, kv_cache, _HALVES, dev, written=True)
-    return _run_evict(fn, plan, dev, scores, cache, kept, compact_scores)
+    dev, shape, cache, where = _once(plan.layouts, _check_evict, fn, plan, scores, kept, kv_cache)
+    if kept is None:
+        kept = torch.empty(shape, dtype=torch.int32, device=dev)
+    _ready(fn, plan, dev)
+    _call(fn, dev, plan.handle, scores.data_ptr(), where, int(bool(compact_scores)),
+          kv_cache.data_ptr(), cache[0], kept.data_ptr())
+    return kept
 
 
 def bskv_run_evict_fp4(plan, scores, kv_codes, kv_scales, kept=None, compact_scores=True):
     """bskv_run_evict over a 4-bit paged cache."""
     fn = "bskv_run_evict_fp4"
     _check_plan(fn, plan, "evict")
-    dev = _cuda_of(fn, "scores", scores)
-    cache = _fp4_pages(fn, plan, kv_codes, kv_scales, dev, written=True)
-    return _run_evict(fn, plan, dev, scores, cache, kept, compact_scores)
+    dev, shape, cache, where = _once(plan.layouts, _check_evict, fn, plan, scores, kept, kv_codes,
+                                     kv_scales)
+    if kept is None:
+        kept = torch.empty(shape, dtype=torch.int32, device=dev)
+    _ready(fn, plan, dev)
+    _call(fn, dev, plan.handle, scores.data_ptr(), where, int(bool(compact_scores)),
+          kv_codes.data_ptr(), cache[0], kv_scales.data_ptr(), cache[1], kept.data_ptr())
+    return kept
 
 
 def bskv_merge_states(v, s, out_dtype=torch.float32, v_out=None, s_out=None):
