@@ -117,7 +117,9 @@ struct Shape {
   static constexpr int kOld = kScales + (FP4 ? kTile * kBlocks : 0);    // scores read
   static constexpr int kPlace = kOld + 4 * kTile;                       // where they belong
   static constexpr int kStage = kPlace + 8 * (kTile / 8);
-  static constexpr int kRing = kStages * ((kStage + 15) / 16 * 16);
+  static constexpr int kRing = kStages * ((kStage + 127) / 128 * 128);
+  // What the copy of rows kRows i .. of a group adds to addresses by XOR, as part() stores them.
+  static __device__ __forceinline__ constexpr int turn(int i) { return FP4 ? i << 4 : (i & 1) << 6; }
   // Stored part of part c of row r: word and 16-byte reads of the compute loop then fall into
   // distinct banks.
   static __device__ __forceinline__ int part(int r, int c) {
@@ -226,10 +228,20 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm(D, FP4))
   PageWalk walk(records, nck, p.meta + p.off_aux1, p.heads, p.page_size, lane);
   const bool old = p.decay != 0.f;
 
-  constexpr int kStep = 32 / Sh::kParts;  // rows one copy instruction of the warp covers
-  const int row_in = lane / Sh::kParts, part = lane % Sh::kParts;
-  constexpr int kPer = FP4 ? 16 / Sh::kBlocks : 8, kCopies = kTile / kPer;  // tokens per 16 bytes of scales
-  const int s_row = lane % kCopies * kPer, w_row = (lane & 7) * 4;
+  // Eight lanes copy a group of 8 tokens: 16-byte parts of rows, then one or two pieces of the
+  // scales, two of the scores, and where these belong. What the addresses add to the group's own
+  // offset, kept by lane (tok - win) / 8 + j, is fixed.
+  const int j = lane >> 3, sub = lane & 7;
+  constexpr int kLanes = Sh::kParts < 8 ? Sh::kParts : 8;  // side by side in a row
+  constexpr int kRows = 8 / kLanes;                        // rows a copy instruction covers
+  constexpr int kPieces = 8 * Sh::kBlocks / 16;
+  const int row = sub / kLanes;
+  const uint8_t* k_lane = p.keys + row * p.k_s3 + sub % kLanes * 16;
+  const int64_t step = kRows * p.k_s3;
+  const uint32_t to_lane = smem_u32(ring + (8 * j + row) * Sh::kRow + sub % kLanes * 16);
+  const bool takes_scales = FP4 && sub < kPieces, takes_scores = old && (sub & 6) == 4;
+  const uint32_t scales_to = smem_u32(ring + Sh::kScales + 8 * j * Sh::kBlocks + sub * 16);
+  const uint32_t scores_to = smem_u32(ring + Sh::kOld + 32 * j + (sub & 1) * 16);
   int64_t k_off = 0, s_off = 0, w_off = 0;
   auto issue = [&](int stage) {
     if (walk.live()) {
@@ -238,28 +250,22 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm(D, FP4))
         if constexpr (FP4) s_off = walk.page * p.s_s0 + walk.kvh * p.s_s2 + walk.slot * Sh::kBlocks;
         w_off = walk.page * p.w_s0 + walk.kvh * p.w_s1 + walk.slot;
       }
-      uint8_t* st = ring + stage * kStride;
-      auto copy = [&](auto whole) {
+      const uint8_t* from = k_lane + walk.of_group(k_off, 8 * j);
+      const uint8_t* s_from = FP4 ? p.scales + walk.of_group(s_off, 8 * j) + sub * 16 : nullptr;
+      const int64_t place = walk.of_group(w_off, 8 * j);
+      if (walk.has(8 * j)) {
+        const uint32_t at = stage * kStride;
 #pragma unroll
-        for (int i = 0; i < kTile / kStep; ++i) {
-          const int r = row_in + i * kStep;
-          const int64_t off = walk.of_group(k_off, r);
-          if (whole || walk.has(r))
-            cp_async_16(st + r * Sh::kRow + (Sh::part(r, part) << 4), p.keys + off + (r & 7) * p.k_s3 + part * 16);
+        for (int i = 0; i < 8 / kRows; ++i) {
+#pragma unroll
+          for (int c = 0; c < Sh::kParts; c += kLanes)
+            cp_async_16_at(((to_lane + at) ^ Sh::turn(i)) + i * kRows * Sh::kRow + 16 * c, from + 16 * c);
+          from += step;
         }
-        if constexpr (FP4) {
-          const int64_t off = walk.of_group(s_off, s_row);
-          if ((whole || walk.has(s_row)) && lane < kCopies)
-            cp_async_16(st + Sh::kScales + 16 * lane, p.scales + off + (s_row & 7) * Sh::kBlocks);
-        }
-        const int64_t off = walk.of_group(w_off, w_row);  // four scores
-        if ((whole || walk.has(w_row)) && lane < 8) {
-          if (old) cp_async_16(st + Sh::kOld + 16 * lane, p.scores + off + (w_row & 7));
-          if ((lane & 1) == 0) *reinterpret_cast<int64_t*>(st + Sh::kPlace + 4 * lane) = off;
-        }
-      };
-      if (walk.tok + kTile <= walk.end) copy(std::true_type{});
-      else copy(std::false_type{});
+        if (takes_scales) cp_async_16_at(scales_to + at, s_from);
+        if (takes_scores) cp_async_16_at(scores_to + at, p.scores + place + 4 * (sub & 1));
+        if (sub == 0) *reinterpret_cast<int64_t*>(ring + at + Sh::kPlace + 8 * j) = place;
+      }
       walk.advance();
     }
     cp_async_commit();
