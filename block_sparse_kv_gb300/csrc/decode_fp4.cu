@@ -46,7 +46,7 @@ using namespace dev;
 constexpr int kTile = kFp4Tile;  // tokens per stage
 static_assert(kTile == kWalkTile, "one walk step per stage");
 constexpr int kWarps = kFp4Warps;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 
 struct Fp4DecodeParams {
   const int32_t* meta;
@@ -150,23 +150,33 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
   }
 }
 
-// Raise a head's reference to 2^10 below the largest product of weight and scale among 16 tokens:
-// a lane's two logits (base 2) plus the exponents f of the tokens' largest scales. The weights
+// Raise a head's reference to 2^10 below the largest product of weight and scale among 16 H tokens:
+// a lane's 2 H logits (base 2) plus the exponents f of the tokens' largest scales. The weights
 // themselves stay within [2^-80, 2^100], whatever the scales. Returns what sums so far shrink by.
-__device__ __forceinline__ float raise_ref(float& ref, float v0, float v1, const float (&f)[2]) {
-  const float top = max_over_rows(fmaxf(v0, v1));
-  float need = max_over_rows(fmaxf(v0 + f[0], v1 + f[1]));
+template <int N>
+__device__ __forceinline__ float raise_ref(float& ref, const float (&v)[N], const float (&f)[N]) {
+  float top = v[0], need = v[0] + f[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) {
+    top = fmaxf(top, v[i]);
+    need = fmaxf(need, v[i] + f[i]);
+  }
+  top = max_over_rows(top);
+  need = max_over_rows(need);
   need = fmaxf(ref, fminf(fmaxf(need - 10.f, top - 100.f), top + 80.f));
   const float shrink = fast_exp2(ref - need);
   ref = need;
   return shrink;
 }
 
-template <int D, int NT>
-__device__ __forceinline__ void raise_refs(State<D, NT>& s, const float (&x)[NT][4], const float (&f)[2]) {
+template <int D, int NT, int N>
+__device__ __forceinline__ void raise_refs(State<D, NT>& s, const float (&x)[NT][2][N], const float (&f)[N]) {
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
-    const float shrink = raise_ref(s.ref[j], x[j >> 1][j & 1] * s.c[j], x[j >> 1][(j & 1) + 2] * s.c[j], f);
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = x[j >> 1][j & 1][i] * s.c[j];
+    const float shrink = raise_ref(s.ref[j], v, f);
     s.l[j] *= shrink;
 #pragma unroll
     for (int blk = 0; blk < Shape<D>::kBlocks; ++blk)
@@ -178,115 +188,129 @@ __device__ __forceinline__ void raise_refs(State<D, NT>& s, const float (&x)[NT]
   }
 }
 
-// Tokens 16 h .. 16 h + 15 of a tile in shared memory; with WHOLE false, tokens >= valid lie past
-// the chunk (valid > 16 h).
-template <int D, int NT, bool WHOLE>
-__device__ __forceinline__ void half_tile(const uint8_t* st, int h, int valid, int lane, State<D, NT>& s) {
+// Largest exponent of each token's value scales.
+template <int NB, int N>
+__device__ __forceinline__ void scale_exponents(const float (&sv)[N][NB], float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float big = 0.f;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) big = fmaxf(big, sv[i][blk]);
+    f[i] = float(exponent_of(big));
+  }
+}
+
+// 16 H tokens from row `first` of a tile in shared memory on; with WHOLE false, rows >= valid lie
+// past the chunk (valid > first). Row i of a lane is first + g + 8 i.
+template <int D, int NT, bool WHOLE, int H>
+__device__ __forceinline__ void some_tokens(const uint8_t* st, int first, int valid, int lane, State<D, NT>& s) {
   using Sh = Shape<D>;
   using Mma = MmaOp<__half>;
-  constexpr int NB = Sh::kBlocks;
-  const int g = lane >> 2, t = lane & 3, r0 = 16 * h + g, r1 = r0 + 8;
+  constexpr int NB = Sh::kBlocks, N = 2 * H;
+  const int g = lane >> 2, t = lane & 3, r0 = first + g;
   const int kx = (g >> Sh::kSwzShift) & (Sh::kParts - 1);
   const int vx = ((2 * t) >> Sh::kSwzShift) & (Sh::kParts - 1);
-  float x[NT][4];  // q.k: rows r0 (first two) and r1, columns 2t and 2t + 1
-  {
+  float x[NT][2][N];  // q.k of columns 2t and 2t + 1
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
     float s0[NB], s1[NB];
-    scales_of<NB>(scale_word<D>(st + Sh::kKs, r0), s0);
-    scales_of<NB>(scale_word<D>(st + Sh::kKs, r1), s1);
+    scales_of<NB>(scale_word<D>(st + Sh::kKs, r0 + 8 * i), s0);
+    scales_of<NB>(scale_word<D>(st + Sh::kKs, r0 + 8 * i + 8), s1);
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) {
-      const uint8_t* at = st + ((blk ^ kx) << 4) + 4 * t;
+      const uint8_t* at = st + ((blk ^ kx) << 4) + 4 * t + (r0 + 8 * i) * Sh::kRow;
       uint32_t a0[4], a1[4];
-      cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(at + r0 * Sh::kRow), a0);
-      cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(at + r1 * Sh::kRow), a1);
+      cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(at), a0);
+      cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(at + 8 * Sh::kRow), a1);
       const uint32_t f0[4] = {a0[0], a1[0], a0[1], a1[1]}, f1[4] = {a0[2], a1[2], a0[3], a1[3]};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
         Mma::run(acc, f0, s.q[nt][blk][0], s.q[nt][blk][1]);
         Mma::run(acc, f1, s.q[nt][blk][2], s.q[nt][blk][3]);
-        x[nt][0] = blk ? fmaf(acc[0], s0[blk], x[nt][0]) : acc[0] * s0[blk];
-        x[nt][1] = blk ? fmaf(acc[1], s0[blk], x[nt][1]) : acc[1] * s0[blk];
-        x[nt][2] = blk ? fmaf(acc[2], s1[blk], x[nt][2]) : acc[2] * s1[blk];
-        x[nt][3] = blk ? fmaf(acc[3], s1[blk], x[nt][3]) : acc[3] * s1[blk];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[nt][e][i] = blk ? fmaf(acc[e], s0[blk], x[nt][e][i]) : acc[e] * s0[blk];
+          x[nt][e][i + 1] = blk ? fmaf(acc[e + 2], s1[blk], x[nt][e][i + 1]) : acc[e + 2] * s1[blk];
+        }
       }
     }
     if constexpr (!WHOLE) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if ((i < 2 ? r0 : r1) >= valid) x[nt][i] = -INFINITY;
+        for (int e = 0; e < 2; ++e) {
+          if (r0 + 8 * i >= valid) x[nt][e][i] = -INFINITY;
+          if (r0 + 8 * i + 8 >= valid) x[nt][e][i + 1] = -INFINITY;
+        }
     }
   }
   // Weights relative to the reference, times the value scales, as f16 pairs of two heads. Products
   // up to 2^15 are safe in f16; the first tokens, and later ones with a larger product, set it.
-  float sv[2][NB];
+  float sv[N][NB];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = i ? r1 : r0;
-    uint32_t w = scale_word<D>(st + Sh::kVs, r);
-    if constexpr (!WHOLE) w = r < valid ? w : 0u;
+  for (int i = 0; i < N; ++i) {
+    uint32_t w = scale_word<D>(st + Sh::kVs, r0 + 8 * i);
+    if constexpr (!WHOLE) w = r0 + 8 * i < valid ? w : 0u;
     scales_of<NB>(w, sv[i]);
   }
-  uint32_t pp[NT][NB][2];
-  auto weigh = [&](float (&add)[2 * NT]) {
+  uint32_t pp[NT][NB][N];
+  float add[2 * NT];
+  auto weigh = [&]() {
     __half2 top = __float2half2_rn(0.f);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float e[4];
+      add[2 * nt] = add[2 * nt + 1] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = fast_exp2(fmaf(x[nt][i], s.c[2 * nt + (i & 1)], -s.ref[2 * nt + (i & 1)]));
-      add[2 * nt] = e[0] + e[2];
-      add[2 * nt + 1] = e[1] + e[3];
+      for (int i = 0; i < N; ++i) {
+        float e[2];
 #pragma unroll
-      for (int blk = 0; blk < NB; ++blk)
+        for (int k = 0; k < 2; ++k) {
+          e[k] = fast_exp2(fmaf(x[nt][k][i], s.c[2 * nt + k], -s.ref[2 * nt + k]));
+          add[2 * nt + k] += e[k];
+        }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t w = pack_half2(e[2 * i] * sv[i][blk], e[2 * i + 1] * sv[i][blk]);
+        for (int blk = 0; blk < NB; ++blk) {
+          const uint32_t w = pack_half2(e[0] * sv[i][blk], e[1] * sv[i][blk]);
           pp[nt][blk][i] = w;
           top = __hmax2(top, *reinterpret_cast<const __half2*>(&w));
         }
+      }
     }
     return __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f));
   };
-  float add[2 * NT];
-  const bool over = weigh(add);
+  const bool over = weigh();
   if (__any_sync(0xffffffffu, over || s.ref[0] == -INFINITY)) {
-    float f[2];  // exponent of each token's largest scale
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float big = 0.f;
-#pragma unroll
-      for (int blk = 0; blk < NB; ++blk) big = fmaxf(big, sv[i][blk]);
-      f[i] = float(exponent_of(big));
-    }
+    float f[N];
+    scale_exponents(sv, f);
     raise_refs<D, NT>(s, x, f);
-    weigh(add);
+    weigh();
   }
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) s.l[j] += add[j];
-  // O^T += V^T P^T
-  const uint8_t* row = st + Sh::kV + (16 * h + 2 * t) * Sh::kRow + 2 * g;
+  // O^T += V^T P^T, 16 tokens a product
+  const uint8_t* row = st + Sh::kV + (first + 2 * t) * Sh::kRow + 2 * g;
 #pragma unroll
-  for (int blk = 0; blk < NB; ++blk) {
-    const uint8_t* at = row + ((blk ^ vx) << 4);
-    const uint32_t h0 = *reinterpret_cast<const uint16_t*>(at);
-    const uint32_t h1 = *reinterpret_cast<const uint16_t*>(at + Sh::kRow);
-    const uint32_t h2 = *reinterpret_cast<const uint16_t*>(at + 8 * Sh::kRow);
-    const uint32_t h3 = *reinterpret_cast<const uint16_t*>(at + 9 * Sh::kRow);
-    uint32_t a[2][4];  // rows g / g + 8 of the two products: values 4g + {0, 1} and {2, 3}
-    cvt_e2m1x4(nibbles(h0, h1 << 4), a[0][0], a[1][0]);
-    cvt_e2m1x4(nibbles(h0 >> 4, h1), a[0][1], a[1][1]);
-    cvt_e2m1x4(nibbles(h2, h3 << 4), a[0][2], a[1][2]);
-    cvt_e2m1x4(nibbles(h2 >> 4, h3), a[0][3], a[1][3]);
+  for (int h = 0; h < H; ++h)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const uint32_t b0 = movmatrix(pp[nt][blk][0]), b1 = movmatrix(pp[nt][blk][1]);
-      Mma::run(s.o[nt][blk][0], a[0], b0, b1);
-      Mma::run(s.o[nt][blk][1], a[1], b0, b1);
+    for (int blk = 0; blk < NB; ++blk) {
+      const uint8_t* at = row + ((blk ^ vx) << 4) + 16 * h * Sh::kRow;
+      const uint32_t h0 = *reinterpret_cast<const uint16_t*>(at);
+      const uint32_t h1 = *reinterpret_cast<const uint16_t*>(at + Sh::kRow);
+      const uint32_t h2 = *reinterpret_cast<const uint16_t*>(at + 8 * Sh::kRow);
+      const uint32_t h3 = *reinterpret_cast<const uint16_t*>(at + 9 * Sh::kRow);
+      uint32_t a[2][4];  // rows g / g + 8 of the two products: values 4g + {0, 1} and {2, 3}
+      cvt_e2m1x4(nibbles(h0, h1 << 4), a[0][0], a[1][0]);
+      cvt_e2m1x4(nibbles(h0 >> 4, h1), a[0][1], a[1][1]);
+      cvt_e2m1x4(nibbles(h2, h3 << 4), a[0][2], a[1][2]);
+      cvt_e2m1x4(nibbles(h2 >> 4, h3), a[0][3], a[1][3]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint32_t b0 = movmatrix(pp[nt][blk][2 * h]), b1 = movmatrix(pp[nt][blk][2 * h + 1]);
+        Mma::run(s.o[nt][blk][0], a[0], b0, b1);
+        Mma::run(s.o[nt][blk][1], a[1], b0, b1);
+      }
     }
-  }
 }
 
 // A pair of weights' halves into the half of the lane's column parity, zero elsewhere: byte
@@ -295,52 +319,52 @@ __device__ __forceinline__ uint32_t half_select(int e, int parity) {
   return parity ? (e ? 0x3244u : 0x1044u) : (e ? 0x4432u : 0x4410u);
 }
 
-// half_tile for up to 4 query heads per kv head.
-template <int D, bool WHOLE>
-__device__ __forceinline__ void half_tile4(const uint8_t* st, int h, int valid, int lane, State<D, 0>& s) {
+// some_tokens for up to 4 query heads per kv head.
+template <int D, bool WHOLE, int H>
+__device__ __forceinline__ void some_tokens4(const uint8_t* st, int first, int valid, int lane, State<D, 0>& s) {
   using Sh = Shape<D>;
   using Mma = MmaOp<__half>;
-  constexpr int NB = Sh::kBlocks;
-  const int g = lane >> 2, t = lane & 3, r0 = 16 * h + g, r1 = r0 + 8;
+  constexpr int NB = Sh::kBlocks, N = 2 * H;
+  const int g = lane >> 2, t = lane & 3, r0 = first + g;
   const int kx = (g >> Sh::kSwzShift) & (Sh::kParts - 1);
-  float x[2];  // q.k of tokens r0 and r1 with head t
-  {
+  float x[N];  // q.k of the lane's tokens with head t
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
     float s0[NB], s1[NB];
-    scales_of<NB>(scale_word<D>(st + Sh::kKs, r0), s0);
-    scales_of<NB>(scale_word<D>(st + Sh::kKs, r1), s1);
+    scales_of<NB>(scale_word<D>(st + Sh::kKs, r0 + 8 * i), s0);
+    scales_of<NB>(scale_word<D>(st + Sh::kKs, r0 + 8 * i + 8), s1);
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) {
-      const uint8_t* at = st + ((blk ^ kx) << 4) + 4 * t;
+      const uint8_t* at = st + ((blk ^ kx) << 4) + 4 * t + (r0 + 8 * i) * Sh::kRow;
       uint32_t a0[4], a1[4];
-      cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(at + r0 * Sh::kRow), a0);
-      cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(at + r1 * Sh::kRow), a1);
+      cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(at), a0);
+      cvt_e2m1x8(*reinterpret_cast<const uint32_t*>(at + 8 * Sh::kRow), a1);
       const uint32_t f0[4] = {a0[0], a1[0], a0[1], a1[1]}, f1[4] = {a0[2], a1[2], a0[3], a1[3]};
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       Mma::run(acc, f0, s.q[blk][0], s.q[blk][1]);
       Mma::run(acc, f1, s.q[blk][2], s.q[blk][3]);
-      x[0] = blk ? fmaf(acc[0], s0[blk], x[0]) : acc[0] * s0[blk];
-      x[1] = blk ? fmaf(acc[2], s1[blk], x[1]) : acc[2] * s1[blk];
+      x[i] = blk ? fmaf(acc[0], s0[blk], x[i]) : acc[0] * s0[blk];
+      x[i + 1] = blk ? fmaf(acc[2], s1[blk], x[i + 1]) : acc[2] * s1[blk];
     }
     if constexpr (!WHOLE) {
-      if (r0 >= valid) x[0] = -INFINITY;
-      if (r1 >= valid) x[1] = -INFINITY;
+      if (r0 + 8 * i >= valid) x[i] = -INFINITY;
+      if (r0 + 8 * i + 8 >= valid) x[i + 1] = -INFINITY;
     }
   }
-  float sv[2][NB];
+  float sv[N][NB];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = i ? r1 : r0;
-    uint32_t w = scale_word<D>(st + Sh::kVs, r);
-    if constexpr (!WHOLE) w = r < valid ? w : 0u;
+  for (int i = 0; i < N; ++i) {
+    uint32_t w = scale_word<D>(st + Sh::kVs, r0 + 8 * i);
+    if constexpr (!WHOLE) w = r0 + 8 * i < valid ? w : 0u;
     scales_of<NB>(w, sv[i]);
   }
-  uint32_t pw[2][NB / 2];  // weight times scale of blocks 2 n and 2 n + 1
+  uint32_t pw[N][NB / 2];  // weight times scale of blocks 2 n and 2 n + 1
   float add;
   auto weigh = [&]() {
     __half2 top = __float2half2_rn(0.f);
     add = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float e = fast_exp2(fmaf(x[i], s.c, -s.ref));
       add += e;
 #pragma unroll
@@ -353,15 +377,11 @@ __device__ __forceinline__ void half_tile4(const uint8_t* st, int h, int valid, 
   };
   const bool over = weigh();
   if (__any_sync(0xffffffffu, over || s.ref == -INFINITY)) {
-    float f[2];  // exponent of each token's largest scale
+    float f[N], v[N];
+    scale_exponents(sv, f);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float big = 0.f;
-#pragma unroll
-      for (int blk = 0; blk < NB; ++blk) big = fmaxf(big, sv[i][blk]);
-      f[i] = float(exponent_of(big));
-    }
-    const float shrink = raise_ref(s.ref, x[0] * s.c, x[1] * s.c, f);
+    for (int i = 0; i < N; ++i) v[i] = x[i] * s.c;
+    const float shrink = raise_ref(s.ref, v, f);
     s.l *= shrink;
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk)
@@ -373,9 +393,9 @@ __device__ __forceinline__ void half_tile4(const uint8_t* st, int h, int valid, 
   // O^T += V^T P^T, 8 tokens a product: lane (g, t) gives tokens t and t + 4 of head g / 2
   const uint32_t sel0 = half_select(0, g & 1), sel1 = half_select(1, g & 1);
   const int vx = (t >> Sh::kSwzShift) & (Sh::kParts - 1), vx4 = ((t + 4) >> Sh::kSwzShift) & (Sh::kParts - 1);
-  const uint8_t* row = st + Sh::kV + (16 * h + t) * Sh::kRow + 2 * g;
+  const uint8_t* row = st + Sh::kV + (first + t) * Sh::kRow + 2 * g;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int n = 0; n < NB / 2; ++n) {
       const uint32_t p0 = __shfl_sync(0xffffffffu, pw[i][n], 4 * t + (g >> 1));
@@ -500,13 +520,8 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
 
   for (int i = 0; i < kStages - 1; ++i) issue(i);
 
-  // Units without tokens are zero-filled by the workers in turn.
-  if (p.counters)
-    for (int i = w; i < p.num_merges; i += P)
-      if (merges[3 * i + 2] == 0) merge_unit<T, D>(p, lane, merges[3 * i], 0, 0);
-
   State<D, NT> s;
-  int done = 0;
+  int done = 0, first_merge = -1, last_merge = -1;  // chunks whose units this worker merges
   for (int k = 0; k < nck; ++k) {
     const WalkChunk ch = walk_chunk(records, k);
     int kvh;
@@ -517,34 +532,49 @@ __global__ void __launch_bounds__(kWarps * 32, fp4_ctas_per_sm(NT))
       __syncwarp();  // the tile is there for every lane, and the stage refilled next is free
       issue((done + kStages - 1) % kStages);
       const uint8_t* st = ring + (done % kStages) * Sh::kStage;
-      if (ch.end - at >= kTile) {
+      constexpr int H = NT == 2 ? 1 : 2;
+      const int valid = ch.end - at;
+      if (valid >= kTile) {
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          if constexpr (NT == 0) half_tile4<D, true>(st, h, kTile, lane, s);
-          else half_tile<D, NT, true>(st, h, kTile, lane, s);
+        for (int r = 0; r < kTile; r += 16 * H) {
+          if constexpr (NT == 0) some_tokens4<D, true, H>(st, r, kTile, lane, s);
+          else some_tokens<D, NT, true, H>(st, r, kTile, lane, s);
         }
       } else {
 #pragma unroll 1
-        for (int h = 0; 16 * h < ch.end - at; ++h) {
-          if constexpr (NT == 0) half_tile4<D, false>(st, h, ch.end - at, lane, s);
-          else half_tile<D, NT, false>(st, h, ch.end - at, lane, s);
+        for (int r = 0; r < valid; r += 16) {
+          if constexpr (NT == 0) some_tokens4<D, false, 1>(st, r, valid, lane, s);
+          else some_tokens<D, NT, false, 1>(st, r, valid, lane, s);
         }
       }
     }
     finish<T, D, NT>(p, b, kvh, ch.slot, lane, s);
     if (ch.slot >= 0 && p.counters) {
       // The last of the unit's chunks to finish merges all of them (release / acquire through
-      // lane 0's atomic, the other lanes' writes ordered before it by the __syncwarp).
+      // lane 0's atomic, the other lanes' writes ordered before it by the __syncwarp). Only the
+      // first and the last chunk of a worker are pieces of a unit. The merges come after the loop:
+      // a call inside it costs the loop its registers.
       __syncwarp();
       int last = 0;
       if (lane == 0) last = atomic_add_acq_rel(p.counters + ch.item, 1) == ch.pieces - 1;
-      if (__shfl_sync(0xffffffffu, last, 0)) {
-        merge_unit<T, D>(p, lane, ch.unit, ch.first_slot, ch.pieces);
-        if (lane == 0) p.counters[ch.item] = 0;  // ready for the next run
-      }
+      if (__shfl_sync(0xffffffffu, last, 0)) (k == 0 ? first_merge : last_merge) = k;
     }
   }
   cp_async_wait<0>();
+  if (p.counters) {
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const int k = i ? last_merge : first_merge;
+      if (k < 0) continue;
+      const WalkChunk ch = walk_chunk(records, k);
+      merge_unit<T, D>(p, lane, ch.unit, ch.first_slot, ch.pieces);
+      if (lane == 0) p.counters[ch.item] = 0;  // ready for the next run
+    }
+    // Units without tokens are zero-filled by the workers in turn.
+#pragma unroll 1
+    for (int i = w; i < p.num_merges; i += P)
+      if (merges[3 * i + 2] == 0) merge_unit<T, D>(p, lane, merges[3 * i], 0, 0);
+  }
 }
 
 template <typename T, int D, int NT>
