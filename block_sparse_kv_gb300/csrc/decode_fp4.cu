@@ -299,11 +299,11 @@ __device__ __forceinline__ void some_tokens(const uint8_t* st, int first, int va
       const uint32_t h1 = *reinterpret_cast<const uint16_t*>(at + Sh::kRow);
       const uint32_t h2 = *reinterpret_cast<const uint16_t*>(at + 8 * Sh::kRow);
       const uint32_t h3 = *reinterpret_cast<const uint16_t*>(at + 9 * Sh::kRow);
-      uint32_t a[2][4];  // rows g / g + 8 of the two products: values 4g + {0, 1} and {2, 3}
-      cvt_e2m1x4(nibbles(h0, h1 << 4), a[0][0], a[1][0]);
-      cvt_e2m1x4(nibbles(h0 >> 4, h1), a[0][1], a[1][1]);
-      cvt_e2m1x4(nibbles(h2, h3 << 4), a[0][2], a[1][2]);
-      cvt_e2m1x4(nibbles(h2 >> 4, h3), a[0][3], a[1][3]);
+      const uint32_t even = __byte_perm(h0, h2, 0x5410), odd = __byte_perm(h1, h3, 0x5410);
+      uint32_t lo[4], hi[4];  // rows g / g + 8 of the two products: values 4g + {0, 1} and {2, 3}
+      cvt_e2m1x8(nibbles(even, odd << 4), lo);
+      cvt_e2m1x8(nibbles(even >> 4, odd), hi);
+      const uint32_t a[2][4] = {{lo[0], hi[0], lo[2], hi[2]}, {lo[1], hi[1], lo[3], hi[3]}};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint32_t b0 = movmatrix(pp[nt][blk][2 * h]), b1 = movmatrix(pp[nt][blk][2 * h + 1]);
