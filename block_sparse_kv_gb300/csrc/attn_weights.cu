@@ -320,15 +320,22 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm(D, FP4))
 // tile kernel
 // ---------------------------------------------------------------------------------------
 
-// 16 bytes (8 values) of a 4-bit key as a chunk of T, in units of the row's largest scale.
+// 16 bytes (8 values) of a 4-bit key as a chunk of T, in units of the row's largest scale; f a power of
+// two, at most 1.
 template <typename T>
 __device__ __forceinline__ uint4 widen(uint32_t w, float f) {
   uint32_t h[4], o[4];
   cvt_e2m1x8(w, h);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 a = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
-    o[i] = MmaOp<T>::pack(a.x * f, a.y * f);
+    __half2 x = *reinterpret_cast<__half2*>(&h[i]);
+    if constexpr (__is_same(T, __half)) {  // below 2^-24 of the largest block a value may round
+      x = __hmul2(x, __float2half2_rn(f));
+      o[i] = *reinterpret_cast<uint32_t*>(&x);
+    } else {
+      const float2 a = __half22float2(x);
+      o[i] = MmaOp<T>::pack(a.x * f, a.y * f);
+    }
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -337,7 +344,7 @@ struct TileShared {
   float4 pair[2][2][64];  // [group of threads][parity] of query rows 2 i and 2 i + 1: {-hi, -hi, r, r}
   int last[2][2][128];
   float part[2][kKeys];   // the second group's sums of an item
-  float unit[2][kKeys];   // what the keys' products are multiplied by
+  float unit[4][kKeys];   // 4-bit keys: what a key's products are multiplied by
   uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], s_full[2], s_empty[2];
   uint32_t tmem;
   int abort;
@@ -396,7 +403,9 @@ __device__ __forceinline__ TileItem next_item(const WeightsParams& p, TileItem t
   return t;
 }
 
-constexpr int kTileThreads = 2 * kKeys + 32;  // two groups of a thread per key, and a warp that copies and multiplies
+// Two groups of a thread per key, a warp that copies and multiplies, and for 4-bit keys a group that
+// turns them into 16 bits.
+constexpr int tile_threads(bool fp4) { return (fp4 ? 3 : 2) * kKeys + 32; }
 
 // A 4-bit key's row and scales on their way to shared memory.
 template <int D>
@@ -412,11 +421,11 @@ struct Row4 {
 //   * several products per item: they alternate between the groups, whose sums are added at its end;
 //     queries have two buffers, keys one.
 template <typename T, int D, bool FP4>
-__global__ void __launch_bounds__(kTileThreads, 2)
+__global__ void __launch_bounds__(tile_threads(FP4), 2)
     weights_tile_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ WeightsParams p) {
   constexpr int kPanels = D / 64;
-  constexpr uint32_t kBuffer = uint32_t(kPanels * kPanel), kCols = 256;
+  constexpr uint32_t kBuffer = uint32_t(kPanels * kPanel), kTmem = 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ks = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const bool single = p.single;
@@ -436,7 +445,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     fence_mbar_init();
   }
   if (warp == 8) {
-    tmem_alloc(&sh.tmem, kCols);
+    tmem_alloc(&sh.tmem, kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -471,8 +480,8 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     auto load_k = [&](const TileItem& u, int kb) {
       if (u.tiles == 0) return true;
       int& n = kb ? kn1 : kn0;
-      if (n > 0 && !wait(&sh.k_empty[kb], n - 1)) return false;
       if constexpr (!FP4) {
+        if (n > 0 && !wait(&sh.k_empty[kb], n - 1)) return false;
         const int boxes = (u.end - u.begin + p.box - 1) / p.box;
         mbar_arrive_expect_tx_w(leader, &sh.k_full[kb], uint32_t(boxes) * kPanels * p.box * 128);
         for (int x = 0; x < boxes; ++x) {
@@ -570,9 +579,79 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       for (int n = max(0, qn - (single ? 1 : 2)); n < qn; ++n)
         mbar_wait(&sh.q_full[single ? 0 : n & 1], uint32_t(single ? n : n >> 1) & 1u, p.st, false);
     }
+  } else if (FP4 && warp > 8) {
+    // A thread per key turns 4-bit rows into 16 bits; the next item's row is read ahead.
+    const int tid = threadIdx.x - (2 * kKeys + 32);
+    auto read_row = [&](const TileItem& u, int page) {
+      Row4<D> x{};
+      const int key = u.begin + tid;
+      int sl;
+      p.page_size.divmod(key, sl);
+      if (u.tiles > 0 && key < u.end) {
+        const uint8_t* src = p.keys + page * p.k_s0 + u.kvh * p.k_s2 + sl * p.k_s3;
+        const uint8_t* sc = p.scales + page * p.s_s0 + u.kvh * p.s_s2 + sl * (D / 32);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          x.w[j] = __ldg(reinterpret_cast<const uint4*>(src) + j);
+          x.code[j] = __ldg(sc + j);
+        }
+      }
+      return x;
+    };
+    // The row as T relative to its largest scale into key buffer kb; its products' unit. A slot of
+    // units is written again when the products that use it have been read: two fills of a buffer on
+    // (single: a buffer's products belong to one group), or four (several: they alternate, and a fill
+    // has one product at least).
+    auto put_row = [&](const Row4<D>& x, int kb, int slot) {
+      uint32_t top = 0;
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        bad = bad || x.code[j] == 255u;
+        top = max(top, x.code[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const float f = top - x.code[j] > 126u ? 0.f : pow2(int(x.code[j]) - int(top));
+        const uint32_t v[4] = {x.w[j].x, x.w[j].y, x.w[j].z, x.w[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sts128(smem_u32(ks) + (kb * kPanels + (j >> 1)) * kPanel + swz(tid, (j & 1) * 4 + i, 128), widen<T>(v[i], f));
+      }
+      sh.unit[slot][tid] = bad ? NAN : p.scale_log2 * e8m0_value(top);
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.k_full[kb]);
+    };
+
+    auto page_of = [&](const TileItem& u) {
+      const int key = u.begin + tid;
+      return key < u.end ? __ldg(p.meta + p.off_aux1 + u.pbase + p.page_size.div(key)) : 0;
+    };
+    int kn0 = 0, kn1 = 0;  // fills of the buffers
+    TileItem next = i0 + 1 < i1 ? next_item(p, t) : t;
+    Row4<D> row = read_row(t, page_of(t));
+    int page = page_of(next);
+    for (int i = i0; i < i1; ++i) {
+      const Row4<D> ahead = read_row(next, page);
+      const TileItem after = i + 2 < i1 ? next_item(p, next) : next;
+      page = page_of(after);
+      if (t.tiles > 0) {
+        const int kb = single ? (i - i0) & 1 : 0;
+        int& n = kb ? kn1 : kn0;
+        if (n > 0 && !warp_wait(&sh.k_empty[kb], uint32_t(n - 1) & 1u, p.st, forced, abort_flag)) {
+          if (lane == 0) *abort_flag = 1;
+          break;
+        }
+        put_row(row, kb, single ? 2 * kb + (n & 1) : n & 3);
+        ++n;
+      }
+      row = ahead;
+      t = next;
+      next = after;
+    }
   } else {
     // What an item needs from memory is read an item ahead: the page of the thread's key, the key's
-    // score, the log-sum-exps, and a 4-bit key's row.
+    // score and the log-sum-exps.
     const int grp = warp >> 2, tid = threadIdx.x & (kKeys - 1), bar = 1 + grp;
     const uint32_t row = tmem + (uint32_t(warp & 3) << 21) + grp * 128;  // TMEM lane 32 * (warp mod 4)
     int my_head;
@@ -595,50 +674,12 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       if (n >= u.tiles || my_tok >= p.tile_queries || tok >= u.rq.nq) return -INFINITY;
       return __ldg(p.lse + int64_t(u.rq.qo + tok) * p.num_qo_heads + u.kvh * p.group + my_head);
     };
-    auto read_row = [&](const TileItem& u, int page) {
-      Row4<D> x{};
-      const int key = u.begin + tid;
-      int sl;
-      p.page_size.divmod(key, sl);
-      if (u.tiles > 0 && key < u.end) {
-        const uint8_t* src = p.keys + page * p.k_s0 + u.kvh * p.k_s2 + sl * p.k_s3;
-        const uint8_t* sc = p.scales + page * p.s_s0 + u.kvh * p.s_s2 + sl * (D / 32);
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          x.w[j] = __ldg(reinterpret_cast<const uint4*>(src) + j);
-          x.code[j] = __ldg(sc + j);
-        }
-      }
-      return x;
-    };
-    // The row as T relative to its largest scale into key buffer kb; what multiplies its products.
-    auto put_row = [&](const Row4<D>& x, int kb) {
-      uint32_t top = 0;
-      bool bad = false;
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        bad = bad || x.code[j] == 255u;
-        top = max(top, x.code[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        const float f = top - x.code[j] > 126u ? 0.f : pow2(int(x.code[j]) - int(top));
-        const uint32_t v[4] = {x.w[j].x, x.w[j].y, x.w[j].z, x.w[j].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sts128(smem_u32(ks) + (kb * kPanels + (j >> 1)) * kPanel + swz(tid, (j & 1) * 4 + i, 128), widen<T>(v[i], f));
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&sh.k_full[kb]);
-      return bad ? NAN : p.scale_log2 * e8m0_value(top);
-    };
-
     bool ok = true;
     int sn = 0;        // products of this group so far
-    int products = 0;  // several: of the CTA
+    int products = 0, fills = 0;  // several: of the CTA, and key tiles
     float2 sum[2];
     // The group's weights of one product of item u (query tokens from tok on), lse its row's.
-    auto add_weights = [&](const TileItem& u, int tok, float lse, float unit) {
+    auto add_weights = [&](const TileItem& u, int tok, float lse) {
       const int info = sn & 1, key = u.begin + tid;
       const int count = min(p.tile_queries, u.rq.nq - tok) * p.group;
       const RowInfo o = row_info(p, u.rq, lse, tok + my_tok);
@@ -656,28 +697,37 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       ++sn;
       if (!ok) return;
       tc_fence_after();
+      const float unit = FP4 ? sh.unit[single ? 2 * grp + info : fills & 3][tid] : p.scale_log2;
       const float2 unit2 = make_float2(unit, unit);
-      for (int c0 = 0; c0 < count; c0 += 32) {
-        uint32_t s[32];
-        tmem_ld32(row + c0, s);
+      constexpr int kCols = FP4 ? 16 : 32;  // at a time; 32 would spill next to a third group's registers
+      for (int c0 = 0; c0 < count; c0 += kCols) {
+        uint32_t s[kCols];
+        if constexpr (FP4) tmem_ld16(row + c0, s);
+        else tmem_ld32(row + c0, s);
         tmem_ld_wait();
-        if (all && c0 + 32 <= count) {
+        auto pair_of_rows = [&](int j) {
+          const float4 hr = sh.pair[grp][info][c0 / 2 + j];
+          const float2 x = ffma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), unit2,
+                                 make_float2(hr.x, hr.y));
+          sum[j & 1] = ffma2(make_float2(fast_exp2(x.x), fast_exp2(x.y)), make_float2(hr.z, hr.w), sum[j & 1]);
+        };
+        auto one_row = [&](int j) {
+          const float* hr = reinterpret_cast<const float*>(&sh.pair[grp][info][(c0 + j) >> 1]) + (j & 1);
+          sum[0].x = fmaf(fast_exp2(fmaf(__uint_as_float(s[j]), unit, hr[0])), hr[2], sum[0].x);
+        };
+        if (all && c0 + kCols <= count) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float4 hr = sh.pair[grp][info][c0 / 2 + j];
-            const float2 x = ffma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), unit2,
-                                   make_float2(hr.x, hr.y));
-            sum[j & 1] = ffma2(make_float2(fast_exp2(x.x), fast_exp2(x.y)), make_float2(hr.z, hr.w), sum[j & 1]);
+          for (int j = 0; j < kCols / 2; ++j) pair_of_rows(j);
+        } else if (all) {
+#pragma unroll
+          for (int j = 0; j < kCols / 2; ++j) {
+            if (c0 + 2 * j + 1 < count) pair_of_rows(j);
+            else if (c0 + 2 * j < count) one_row(2 * j);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int c1 = c0 + j;
-            if (c1 >= count) continue;
-            const float* hr = reinterpret_cast<const float*>(&sh.pair[grp][info][c1 >> 1]) + (c1 & 1);
-            if (key <= sh.last[grp][info][c1])
-              sum[0].x = fmaf(fast_exp2(fmaf(__uint_as_float(s[j]), unit, hr[0])), hr[2], sum[0].x);
-          }
+          for (int j = 0; j < kCols; ++j)
+            if (c0 + j < count && key <= sh.last[grp][info][c0 + j]) one_row(j);
         }
       }
       tc_fence_before();
@@ -690,17 +740,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     int page = i < i1 ? page_of(t) : 0;
     float* score = score_at(t, page);
     float old = i < i1 ? old_score(t, score) : 0.f;
-    float lse = single ? lse_of(t, 0) : 0.f, unit = p.scale_log2;
-    if constexpr (FP4) {
-      if (i < i1 && t.tiles > 0 && (single || grp == 0)) {
-        unit = put_row(read_row(t, page), single ? grp : 0);
-        sh.unit[0][tid] = unit;
-      }
-      if (!single) {
-        bar_and(3, 2 * kKeys, true);
-        unit = sh.unit[0][tid];
-      }
-    }
+    float lse = single ? lse_of(t, 0) : 0.f;
     for (; i < i1; i += step) {
       const bool more = i + step < i1;
       TileItem next = t;
@@ -709,53 +749,34 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       const int next_page = more ? page_of(next) : 0;
       float* next_score = score_at(next, next_page);
       const float next_old = more ? old_score(next, next_score) : 0.f;
-      float next_unit = unit;
-      Row4<D> ahead;
-      if constexpr (FP4) {
-        if (more && (single || grp == 0)) ahead = read_row(next, next_page);
-      }
       sum[0] = sum[1] = make_float2(0.f, 0.f);
       float w = 0.f;
       if (single) {
         const float next_lse = more ? lse_of(next, 0) : 0.f;
-        if (t.tiles > 0) add_weights(t, t.tok0, lse, unit);
+        if (t.tiles > 0) add_weights(t, t.tok0, lse);
         w = total();
-        if constexpr (FP4) {  // the group's product has read its key buffer
-          if (more && next.tiles > 0 && ok) next_unit = put_row(ahead, grp);
-        }
         lse = next_lse;
       } else {
         for (int n = 0; n < t.tiles; ++n)
-          if (((products + n) & 1) == grp) add_weights(t, t.tok0 + n * p.tile_queries, lse_of(t, n), unit);
+          if (((products + n) & 1) == grp) add_weights(t, t.tok0 + n * p.tile_queries, lse_of(t, n));
         products += t.tiles;
+        fills += t.tiles > 0;
         w = total();
         const int par = (i - i0) & 1;
         if (grp == 1) sh.part[par][tid] = w;
-        if constexpr (FP4) {
-          if (grp == 0 && more && next.tiles > 0 && ok) {
-            // the item's last product, of either group, has read the key buffer
-            const int last = products - 1;
-            if (t.tiles > 0) ok = warp_wait(&sh.s_full[last & 1], uint32_t(last >> 1) & 1u, p.st, forced, abort_flag);
-            if (ok) sh.unit[par ^ 1][tid] = put_row(ahead, 0);
-          }
-        }
         bar_and(3, 2 * kKeys, true);
         if (grp == 0) w += sh.part[par][tid];
-        if constexpr (FP4) {
-          if (more && next.tiles > 0) next_unit = sh.unit[par ^ 1][tid];
-        }
       }
       if (t.begin + tid < t.end && ok && (single || grp == 0)) *score = is_fresh(t) ? w : fmaf(p.decay, old, w);
       t = next;
       score = next_score;
       old = next_old;
-      unit = next_unit;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, kCols);
+  if (warp == 8) tmem_dealloc(tmem, kTmem);
 }
 
 template <typename T, int D, int NT, bool FP4>
@@ -795,7 +816,7 @@ bskv_status launch_tile(const bskv_plan* plan, WeightsParams& wp, cudaStream_t s
   wp.num_items = meta_word(plan, H_UNITS);
   wp.queries = FastDiv(wp.tile_queries);
   const int grid = std::min(wp.num_items, plan->num_sms * per_sm);
-  kern<<<grid, kTileThreads, smem, st>>>(qmap, kmap, wp);
+  kern<<<grid, tile_threads(FP4), smem, st>>>(qmap, kmap, wp);
   return cuda_check(cudaGetLastError(), "attn_weights launch");
 }
 

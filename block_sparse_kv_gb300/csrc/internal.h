@@ -116,20 +116,35 @@ inline int32_t decode_group_heads(int32_t num_kv_heads, int32_t page_size) {
 }
 
 // 4-bit decode: one worker per warp, kFp4Warps to a CTA. The variant by query heads per kv head (0:
-// up to 4, 1: up to 8, 2: up to 16) decides how many CTAs an SM holds (registers: 128, 168 and 255 a
-// thread).
+// up to 4, 1: up to 8, 2: up to 16) decides how many CTAs an SM holds: by registers 3, 3 and 2.
+// Measured on 64 requests of 512 to 4096 tokens with 4 query heads on each of 8 kv heads ("batch"),
+// 8 of 131072 with 8 ("long"), one request of 700 tokens, and 37 of up to 999 ("ragged"):
+//   * variant 0 for 4 heads 39.4 us, variant 1 44.1 (batch); variant 1 for 8 heads 233 us, variant 2
+//     315 (long);
+//   * 16 warps per SM at 128 registers a thread leave the loops less to overlap than 12: 44.4
+//     against 41.9 us (batch), 261 against 243 (long);
+//   * workers of at least 1, 2, 4, 6, 8 tiles: one request 16.2, 12.9, 12.4, 12.7, 13.7 us, ragged
+//     14.8, 13.0, 12.4, 13.2, 15.9;
+//   * publishing a piece and merging it are counted as a tile each, or as nothing: 39.4 against
+//     41.9 us (batch), 13.0 against 16.4 (ragged);
+//   * merging up to 16 pieces in the same launch, or all of them by a kernel of their own: the
+//     device takes as long (one request 12.9 against 12.1 us, batch 39.4 against 39.0), the host
+//     15.5 us a call against 18.7.
 constexpr int kFp4Tile = 32;   // tokens per pipeline stage
 constexpr int kFp4Warps = 4;
 constexpr int kFp4PublishTiles = 1, kFp4MergeTiles = 1, kFp4BoundaryTiles = 0;
-constexpr int kFp4MinTiles = 2;      // a worker has at least this many (unless there are fewer)
+constexpr int kFp4MinTiles = 4;      // a worker has at least this many (unless there are fewer)
 constexpr int kFp4FusedPieces = 16;  // a unit of more pieces is merged by a kernel of its own
 constexpr int fp4_column_tiles(int group) { return group <= 4 ? 0 : group <= 8 ? 1 : 2; }
-constexpr int fp4_ctas_per_sm(int column_tiles) { return column_tiles == 0 ? 3 : column_tiles == 1 ? 3 : 2; }
+constexpr int fp4_ctas_per_sm(int column_tiles) { return column_tiles < 2 ? 3 : 2; }
 
 // Attention-weight plans. Stream variants (at most 8 or 16 query rows, queries times heads of a
 // group, in every request): one worker per warp over ranges of tokens of (request, kv head)
 // units; {first query, queries, tokens} of each request stands in the merge section. Tile variant:
 // items of 128 keys of a request for one kv head, by a record of kWalkWords per request with tokens.
+// 64 requests of 2048 tokens, 8 kv heads of 128 dims, 4 to 8 rows: stream (8) 48.9 us, stream (16)
+// 50.5, tile 48.3; 16 rows: stream 52.1, tile 49.4; of 64 dims 31.0 and 42.5. In 4 bits 4 to 8 rows
+// take 21.8, 28.0 and 72 us, 16 rows stream 29.0, tile above 60.
 enum WeightsVariant : int32_t { WEIGHTS_STREAM8 = 0, WEIGHTS_STREAM16 = 1, WEIGHTS_TILE = 2 };
 constexpr int kWeightsWarps = 4;
 constexpr int kWeightsKeys = 128;
