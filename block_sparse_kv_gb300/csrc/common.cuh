@@ -177,6 +177,13 @@ __device__ __forceinline__ bool bar_and(uint32_t id, uint32_t nthreads, bool pre
   return out != 0;
 }
 
+// ---- overlapping launches --------------------------------------------------------------
+
+// Lets a kernel launched to start early begin once every CTA of this one got here or ended.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Waits until the kernel before this one has ended and its writes are visible.
+__device__ __forceinline__ void wait_for_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- thread-block clusters ------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {

@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
   __shared__ uint32_t found_digit;
   __shared__ int found_rest;
   const int b = blockIdx.z, h = blockIdx.y, rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  launch_dependents();
   const int32_t* pages = p.meta + p.off_src + __ldg(p.meta + p.off_src_ptr + b);
   const int4 rq = request_of(p, b);
   const int L = rq.x, K = rq.y;
@@ -363,6 +364,9 @@ __global__ void __launch_bounds__(kMoveThreads, SHARED ? 2 : 8)
   const int h = blockIdx.y, b = blockIdx.z;
   const int4 rq = request_of(p, b);
   const int K = rq.y;
+  // `kept` is read below and pages are written that the selection reads; and what follows this kernel
+  // on the stream follows the selection only if every CTA waits for it
+  wait_for_prior_grid();
   if (p.in_place && K == rq.x) return;
   const int32_t* kept = p.kept + h * p.total + rq.z;
   const int32_t* src_pages = p.meta + p.off_src + __ldg(p.meta + p.off_src_ptr + b);
@@ -415,11 +419,14 @@ __global__ void __launch_bounds__(kMoveThreads, SHARED ? 2 : 8)
   }
 }
 
-// Launches kern(params, ctas) with clusters of `ctas` CTAs along x.
+// Launches kern(params, ctas) with clusters of `ctas` CTAs along x; early: once every CTA of the
+// kernel before it on the stream runs.
 template <typename P>
 cudaError_t launch_clusters(void (*kern)(P, int), dim3 grid, int threads, size_t smem, int ctas, const P& params,
-                            cudaStream_t st) {
-  cudaLaunchAttribute attr[1];
+                            bool early, cudaStream_t st) {
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {unsigned(ctas), 1, 1};
   cudaLaunchConfig_t cfg{};
@@ -428,7 +435,7 @@ cudaError_t launch_clusters(void (*kern)(P, int), dim3 grid, int threads, size_t
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = early ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, params, ctas);
 }
 
@@ -439,7 +446,7 @@ bskv_status select(const EvictParams& e, const bskv_plan* plan, int ctas, size_t
   if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "evict: cudaFuncSetAttribute"))
     return s;
   const dim3 grid(unsigned(ctas), unsigned(plan->num_kv_heads), unsigned(plan->batch));
-  return cuda_check(launch_clusters<EvictParams>(kern, grid, THREADS, smem, ctas, e, st), "evict select launch");
+  return cuda_check(launch_clusters<EvictParams>(kern, grid, THREADS, smem, ctas, e, false, st), "evict select launch");
 }
 
 bskv_status run(const char* who, const bskv_plan* plan, float* scores, const int64_t* scores_strides,
@@ -477,10 +484,8 @@ bskv_status run(const char* who, const bskv_plan* plan, float* scores, const int
     ctas *= 2;
   const int parts = plan->in_place ? ctas : (plan->most + kMoveBlock - 1) / kMoveBlock;
   const dim3 grid(unsigned(planes * parts), unsigned(plan->num_kv_heads), unsigned(plan->batch));
-  if (ctas > 1)
-    return cuda_check(launch_clusters<MoveParams>(evict_move_kernel<true>, grid, kMoveThreads, 0, ctas, mp, st), "evict move launch");
-  evict_move_kernel<false><<<grid, kMoveThreads, 0, st>>>(mp, 1);
-  return cuda_check(cudaGetLastError(), "evict move launch");
+  auto kern = ctas > 1 ? evict_move_kernel<true> : evict_move_kernel<false>;
+  return cuda_check(launch_clusters<MoveParams>(kern, grid, kMoveThreads, 0, ctas, mp, true, st), "evict move launch");
 }
 
 bskv_status check_plan(const char* who, const bskv_plan* plan) {
