@@ -14,11 +14,13 @@
 //     lanes of its row. A row's lane reads 16-byte chunks t, t + 4, ...: products of chunk c with the
 //     same chunk of the query are two k-steps, whatever the order of the dims. Query fragments stay
 //     in registers, each warp streams a range of tokens through a private ring of 32-token tiles
-//     filled by 16-byte asynchronous copies; bound by reading K (HBM).
+//     filled by 16-byte asynchronous copies. Bound by reading K: 64 requests of 512 to 4096 tokens
+//     in 16 bits 53.0 us (5.9 TB/s); in 4 bits by instructions: 8 of 32000 to 40000 39.0 us (4.5 TB/s).
 //   * tile (more rows, a prefill window): S = K Q^T by tcgen05, 128 keys against up to 128 query rows
 //     a product. A key is a TMEM lane and so a thread, which reads its row of S and adds up its
-//     weights: no reduction between threads, and two packed FMAs per two weights next to their two
-//     exponentials, which bound it (16 a clock on an SM) together with reading K.
+//     weights: no reduction between threads, and two packed FMAs and two exponentials per two
+//     weights. The last 32 queries of 16 prompts, 128 rows, take 42.2 us (4.2 TB/s): no pipe is full,
+//     each item waits for its keys, its product and its columns of tensor memory.
 // 4-bit keys (E2M1 codes times 2^x per 32 values): the stream kernel multiplies codes and f16
 // queries and scales each block's fp32 partial sum; the tile kernel turns a key once into the
 // query's type, relative to its largest scale, and multiplies that back after the product.
@@ -27,7 +29,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "common.cuh"
+#include "cache_common.cuh"
 #include "fp4.cuh"
 #include "internal.h"
 #include "launch.h"

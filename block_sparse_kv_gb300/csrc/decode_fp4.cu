@@ -24,14 +24,18 @@
 //     cvt.rn.f16x2.e2m1x2 then yields the (token, token + 1) pairs of the A operand.
 //
 // What bounds it: the cache is read once, 136 bytes per token and kv head of 128 dims against
-// 512 in 16 bits, so instructions issued per byte are what to save; see the measured figures at
-// kFp4WarpsPerSm. Each warp is a worker of its own over a range of one or more (request, kv
+// 512 in 16 bits, so instructions issued per byte are what to save: converting and pairing 4-bit
+// values keeps the ALU pipe busy for half to two thirds of the time. 64 requests of 512 to 4096
+// tokens with 4 query heads per kv head take 39.5 us (4.1 TB/s), 8 of 131072 with 8 heads 233 us (4.9
+// TB/s). A warp works on 32 tokens at a time: the second 16's products fill the first's waits (41.2
+// and 239 us with 16). Two stages are enough of a ring (three: 41.9 and 243 us).
+// Each warp is a worker of its own over a range of one or more (request, kv
 // head) units, with a private ring of 32-token tiles filled by 16-byte asynchronous copies
 // (any page size and stride, no swizzle constraint on the page layout). A unit cut between
 // workers is merged in the same launch as in the 16-bit decode, by the same code.
 #include <math.h>
 
-#include "common.cuh"
+#include "cache_common.cuh"
 #include "fp4.cuh"
 #include "internal.h"
 #include "launch.h"
@@ -127,26 +131,26 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
     return;
   } else {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int h = 8 * nt + g;
-    const float back = load_q_f16<T, NB>(
-        static_cast<const T*>(p.q) + b * p.q_s0 + (int64_t(kvh) * p.group + h) * p.q_s1,
-        h < p.group, p.scale_log2 < 0.f, lane, s.q[nt]);
-    // columns 2t and 2t + 1 belong to the heads of lanes 8t and 8t + 4
-    s.c[2 * nt] = fabsf(p.scale_log2) * __shfl_sync(0xffffffffu, back, 8 * t);
-    s.c[2 * nt + 1] = fabsf(p.scale_log2) * __shfl_sync(0xffffffffu, back, 8 * t + 4);
-  }
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = 8 * nt + g;
+      const float back = load_q_f16<T, NB>(
+          static_cast<const T*>(p.q) + b * p.q_s0 + (int64_t(kvh) * p.group + h) * p.q_s1,
+          h < p.group, p.scale_log2 < 0.f, lane, s.q[nt]);
+      // columns 2t and 2t + 1 belong to the heads of lanes 8t and 8t + 4
+      s.c[2 * nt] = fabsf(p.scale_log2) * __shfl_sync(0xffffffffu, back, 8 * t);
+      s.c[2 * nt + 1] = fabsf(p.scale_log2) * __shfl_sync(0xffffffffu, back, 8 * t + 4);
+    }
 #pragma unroll
-  for (int j = 0; j < 2 * NT; ++j) {
-    s.ref[j] = -INFINITY;
-    s.l[j] = 0.f;
-  }
+    for (int j = 0; j < 2 * NT; ++j) {
+      s.ref[j] = -INFINITY;
+      s.l[j] = 0.f;
+    }
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int blk = 0; blk < NB; ++blk)
+      for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s.o[nt][blk][i >> 2][i & 3] = 0.f;
+        for (int i = 0; i < 8; ++i) s.o[nt][blk][i >> 2][i & 3] = 0.f;
   }
 }
 

@@ -29,7 +29,7 @@
 // four (104 and 113 us). 537 MB in place in 83 us: 6.4 TB/s.
 #include <algorithm>
 
-#include "common.cuh"
+#include "cache_common.cuh"
 #include "fp4.cuh"
 #include "internal.h"
 #include "launch.h"

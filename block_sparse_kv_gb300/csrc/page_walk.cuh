@@ -3,7 +3,7 @@
 // of 16 and chunks start at multiples of 32, so a group never crosses a page).
 #pragma once
 
-#include "common.cuh"
+#include "cache_common.cuh"
 
 namespace bskv {
 namespace dev {

@@ -375,9 +375,10 @@ bskv_status bskv_run_decode_noalloc(const bskv_plan* plan, const void* q,
 
 /*
  * Batch decode over a 4-bit paged cache, for a plan of bskv_plan_decode_fp4: what
- * bskv_run_decode computes, with K and V the values of the cache (a scale code of 0 may read as
- * 0 instead of 2^-127; a key's scale code 255 makes its kv head's outputs and lse NaN, a
- * value's makes those 32 output values NaN).
+ * bskv_run_decode computes, with K and V the values of the cache. A softmax weight times a value's
+ * scale is rounded to 16 bits: half a step of 2^-11, or 2^-35 of the largest such product of its head
+ * where that is more. A key's scale code 255 makes its kv head's outputs and lse NaN, a value's
+ * makes those 32 output values NaN. Values up to about 2^90 in size are safe.
  *   q, out  [batch, num_qo_heads, head_dim] in the plan dtype, strides {batch, head} in
  *           multiples of 8 elements; lse [batch, num_qo_heads] float32 contiguous, or NULL.
  *   float_ws as for bskv_run_decode. Slots past a request's last token are not read.
@@ -598,6 +599,7 @@ bskv_status bskv_rope_quantize_fp8_append_paged(
  *   kv_indptr [batch + 1] and kv_indices. A row whose request, position or page is out of range
  *   is not written and raises BSKV_ERR_DEVICE_INDEX in the device status word. Other cache bytes
  *   are not touched. Rows that share a destination race.
+ * Errors: BSKV_ERR_UNSUPPORTED also for more than 128 kv heads.
  */
 bskv_status bskv_quantize_fp4_append_paged(
     const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides, int32_t dtype,
@@ -608,7 +610,8 @@ bskv_status bskv_quantize_fp4_append_paged(
 
 /*
  * Rows of a 4-bit paged cache read back as values: row i of k_out and v_out [nnz, num_kv_heads,
- * head_dim] (BSKV_BF16: exact; BSKV_FP32: exact; BSKV_FP16: rounded to nearest even) is token
+ * head_dim] (BSKV_BF16: exact; BSKV_FP32: exact; BSKV_FP16: rounded to nearest even; infinite past
+ * the type's largest value) is token
  * positions[i] of request batch_indices[i]. Index arrays, strides and out-of-range rows (their
  * output rows are left as they were) as for bskv_quantize_fp4_append_paged.
  */
