@@ -704,6 +704,9 @@ def _ready(fn, plan, device):
     """The plan's workspaces on this device, uploaded at the first run."""
     if plan.int_ws is None:
         with torch.cuda.device(device):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("%s: upload the plan before the capture: a graph would copy its "
+                                   "host memory at every replay" % fn)
             plan.upload(device)
     if plan.int_ws.device != device:
         raise ValueError("%s: the plan was uploaded to %s, the tensors are on %s"

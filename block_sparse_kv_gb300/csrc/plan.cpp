@@ -586,17 +586,13 @@ bskv_status page_table_lens(const char* who, const int32_t* kv_indptr, const int
 }
 
 // Every page at most once: the runs of the plan write to them.
-bskv_status pages_once(const char* who, const char* name, const int32_t* indices, int64_t n,
-                       int32_t num_pages) {
-  std::vector<uint8_t> seen(size_t(num_pages), 0);
-  for (int64_t i = 0; i < n; ++i) {
-    if (seen[size_t(indices[i])]) {
-      set_error("%s: page %d is listed twice in %s; a page that is written has one owner", who, indices[i], name);
-      return BSKV_ERR_INVALID_ARG;
-    }
-    seen[size_t(indices[i])] = 1;
-  }
-  return BSKV_OK;
+bskv_status pages_once(const char* who, const char* name, const int32_t* indices, int64_t n) {
+  std::vector<int32_t> sorted(indices, indices + n);
+  std::sort(sorted.begin(), sorted.end());
+  const auto twice = std::adjacent_find(sorted.begin(), sorted.end());
+  if (twice == sorted.end()) return BSKV_OK;
+  set_error("%s: page %d is listed twice in %s; a page that is written has one owner", who, *twice, name);
+  return BSKV_ERR_INVALID_ARG;
 }
 
 // Appends the walk records (kWalkWords) to an assembled plan whose units are (request, kv head).
@@ -722,7 +718,7 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
   if (bskv_status s = page_table_lens(who, kv_indptr, kv_indices, kv_last_page_len, batch,
                                       num_pages, page_size, req))
     return s;
-  if (bskv_status s = pages_once(who, "kv_indices", kv_indices, batch > 0 ? kv_indptr[batch] : 0, num_pages)) return s;
+  if (bskv_status s = pages_once(who, "kv_indices", kv_indices, batch > 0 ? kv_indptr[batch] : 0)) return s;
   if (batch > 0 && qo_indptr && qo_indptr[0] != 0) { set_error("%s: qo_indptr[0] must be 0", who); return BSKV_ERR_INVALID_ARG; }
   const int32_t group = num_qo_heads / num_kv_heads;
   if (group > 128) { set_error("%s: %d query heads per kv head (max 128)", who, group); return BSKV_ERR_UNSUPPORTED; }
@@ -814,7 +810,7 @@ extern "C" bskv_status bskv_plan_evict(const int32_t* kv_indptr, const int32_t* 
   if (batch > 0 && !keep_len) { set_error("%s: keep_len is NULL", who); return BSKV_ERR_INVALID_ARG; }
   std::vector<int32_t> dst;
   if (in_place) {
-    if (bskv_status s = pages_once(who, "kv_indices", kv_indices, nnz, num_pages)) return s;
+    if (bskv_status s = pages_once(who, "kv_indices", kv_indices, nnz)) return s;
   } else if (batch > 0) {
     if (dst_indptr[0] != 0) { set_error("%s: dst_indptr[0] must be 0", who); return BSKV_ERR_INVALID_ARG; }
     for (int32_t b = 0; b < batch; ++b)
@@ -823,11 +819,11 @@ extern "C" bskv_status bskv_plan_evict(const int32_t* kv_indptr, const int32_t* 
     if (n > 0 && !dst_indices) { set_error("%s: dst_indices is NULL", who); return BSKV_ERR_INVALID_ARG; }
     for (int64_t i = 0; i < n; ++i)
       if (dst_indices[i] < 0 || dst_indices[i] >= num_pages) { set_error("%s: dst_indices[%lld] = %d outside [0, %d)", who, (long long)i, dst_indices[i], num_pages); return BSKV_ERR_INVALID_ARG; }
-    if (bskv_status s = pages_once(who, "dst_indices", dst_indices, n, num_pages)) return s;
-    std::vector<uint8_t> source(size_t(num_pages), 0);
-    for (int64_t i = 0; i < nnz; ++i) source[size_t(kv_indices[i])] = 1;
+    if (bskv_status s = pages_once(who, "dst_indices", dst_indices, n)) return s;
+    std::vector<int32_t> source(kv_indices, kv_indices + nnz);
+    std::sort(source.begin(), source.end());
     for (int64_t i = 0; i < n; ++i)
-      if (source[size_t(dst_indices[i])]) { set_error("%s: destination page %d is a source page too", who, dst_indices[i]); return BSKV_ERR_INVALID_ARG; }
+      if (std::binary_search(source.begin(), source.end(), dst_indices[i])) { set_error("%s: destination page %d is a source page too", who, dst_indices[i]); return BSKV_ERR_INVALID_ARG; }
     dst.assign(dst_indices, dst_indices + n);
   }
   std::vector<Chunk> reqs;

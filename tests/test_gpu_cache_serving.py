@@ -173,6 +173,80 @@ def test_graph_of_windows_and_halves(cuda):
     _graph_equal(run, [got, pool, kept])
 
 
+def test_plans_are_not_uploaded_by_a_capture(cuda):
+    """A graph must not copy the plan's host memory at every replay."""
+    s = _case(cuda)
+    p = bskv.bskv_plan_decode_fp4(*s["table"], s["pages"], PS, 16, H, D)
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="upload"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            bskv.bskv_run_decode_fp4(p, s["q"], s["codes"], s["scales"])
+    torch.cuda.synchronize()
+    out = bskv.bskv_run_decode_fp4(p, s["q"], s["codes"], s["scales"])
+    torch.cuda.synchronize()
+    assert torch.isfinite(out.float()).all()
+
+
+def test_a_query_that_is_not_finite_stays_in_its_head(cuda):
+    s = _case(cuda)
+    p = bskv.bskv_plan_decode_fp4(*s["table"], s["pages"], PS, 16, H, D)
+    w = bskv.bskv_plan_attn_weights(None, *s["table"], s["pages"], PS, 16, H, D)
+    out, lse = bskv.bskv_run_decode_fp4(p, s["q"], s["codes"], s["scales"], return_lse=True)
+    want = bskv.bskv_run_attn_weights_fp4(w, s["q"], s["codes"], s["scales"], lse, s["scores"].clone())
+    for bad in (float("nan"), float("inf")):
+        q = s["q"].clone()
+        q[1, 3, 5] = bad  # of kv head 0
+        got, z = bskv.bskv_run_decode_fp4(p, q, s["codes"], s["scales"], return_lse=True)
+        assert torch.isnan(got[1, 3].float()).all()
+        keep = torch.ones(4, 16, dtype=torch.bool, device=cuda)
+        keep[1, 3] = False
+        assert torch.equal(got[keep], out[keep]) and torch.equal(z[keep], lse[keep])
+        sc = bskv.bskv_run_attn_weights_fp4(w, q, s["codes"], s["scales"], z, s["scores"].clone())
+        assert torch.equal(sc[:, 1], want[:, 1])
+        pages = s["table"][1][s["table"][0][1]:s["table"][0][2]].to(cuda).long()
+        other = torch.ones(s["pages"], dtype=torch.bool, device=cuda)
+        other[pages] = False
+        assert torch.equal(sc[other], want[other])
+
+
+def test_offsets_past_32_bits(cuda):
+    """Pages 2 GiB apart, in bytes, in every pool that takes strides."""
+    step, pages, lens = 2 ** 31 + 4096, 4, [30, 25]
+    s = _case(cuda, lens=(30, 25))
+    assert s["pages"] == pages
+
+    def spread(x):
+        n = step // x.element_size()
+        far = torch.empty(n * (pages - 1) + x[0].numel(), dtype=x.dtype, device=cuda).as_strided(
+            x.shape, (n,) + x[0].contiguous().stride())
+        return far.copy_(x)
+
+    far = {n: spread(s[n]) for n in ("codes", "scales", "kv", "scores")}
+    t = (*s["table"], pages, PS, 16, H, D)
+    p, w = bskv.bskv_plan_decode_fp4(*t), bskv.bskv_plan_attn_weights(None, *t)
+    qo = torch.tensor([0, 20, 40], dtype=torch.int32)
+    tile = bskv.bskv_plan_attn_weights(qo, *t)
+    e = bskv.bskv_plan_evict(*s["table"], [17, 9], 1, 2, pages, PS, H, D)
+    rows = torch.randn(2, 2, H, D, device=cuda).bfloat16()
+    at = [torch.tensor(x, dtype=torch.int32, device=cuda) for x in ([0, 1], [29, 24])] + [x.to(cuda) for x in s["table"][:2]]
+    qs = torch.randn(40, 16, D, device=cuda).bfloat16()
+    zs = torch.full((40, 16), 5.0, device=cuda)
+    got = []
+    for x in (s, far):
+        bskv.bskv_quantize_fp4_append_paged(rows[0], rows[1], *at, x["codes"], x["scales"])
+        k, v = bskv.bskv_dequantize_fp4_paged(x["codes"], x["scales"], *at)
+        out, lse = bskv.bskv_run_decode_fp4(p, s["q"], x["codes"], x["scales"], return_lse=True)
+        bskv.bskv_run_attn_weights_fp4(w, s["q"], x["codes"], x["scales"], lse, x["scores"])
+        bskv.bskv_run_attn_weights(w, s["q"], x["kv"], lse, x["scores"])
+        bskv.bskv_run_attn_weights_fp4(tile, qs, x["codes"], x["scales"], zs, x["scores"])
+        bskv.bskv_run_attn_weights(tile, qs, x["kv"], zs, x["scores"])
+        a = bskv.bskv_run_evict_fp4(e, x["scores"], x["codes"], x["scales"], compact_scores=False)
+        b = bskv.bskv_run_evict(e, x["scores"], x["kv"])
+        got.append([k, v, out, lse, a, b] + [x[n].contiguous() for n in ("codes", "scales", "kv", "scores")])
+    for u, v in zip(*got):
+        assert torch.equal(u.view(torch.uint8), v.view(torch.uint8))
+
+
 def test_calls_run_on_the_current_stream(cuda):
     """Two plans' runs on two streams at once give what each gives alone."""
     a, b = _case(cuda, seed=1), _case(cuda, lens=(1500, 2), seed=2)

@@ -116,6 +116,16 @@ def test_evict_plan(lib):
     assert p.info["kept_indptr"] == [0, 20, 20, 52]
 
 
+def test_plans_of_a_pool_far_larger_than_the_table(lib):
+    """What a plan takes depends on the pages listed, not on the pool."""
+    big = 2 ** 31 - 1
+    assert _weights(pages=big).info["num_pages"] == big
+    assert _evict(pages=big).info["num_pages"] == big
+    _evict(pages=big, dst_indptr=[0, 2, 2, 3], dst_indices=[7, big - 1, 8])
+    with pytest.raises(bskv.BskvError):
+        _evict(pages=big, dst_indptr=[0, 2, 2, 3], dst_indices=[7, big, 8])
+
+
 def test_plans_of_nothing(lib):
     for p in (_decode([0], [], [], 0), _weights(None, [0], [], [], 0), _evict((), 0, 0, [0], [], [], 0)):
         assert p.info["batch"] == 0
