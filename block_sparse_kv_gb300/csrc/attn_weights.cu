@@ -61,7 +61,7 @@ struct WeightsParams {
   FastDiv heads, groups, page_size, queries;
   int box, tile_queries, num_items, num_requests;  // tile kernel: keys per TMA box, queries per product
   int single;                                      // no item has more than one product
-  int off_workers, off_chunks, off_records, off_aux0, off_aux1, off_req, num_workers;
+  int off_workers, off_records, off_aux1, off_req, num_workers;
   int take;                                        // stream kernel: workers per warp
   float decay, scale_log2;
   StatusArgs st;
@@ -612,11 +612,13 @@ __global__ void __launch_bounds__(tile_threads(FP4), 2)
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         bad = bad || x.code[j] == 255u;
-        top = max(top, x.code[j]);
+        // a block of zeros does not count, whatever its scale
+        if ((x.w[j].x | x.w[j].y | x.w[j].z | x.w[j].w) & 0x77777777u) top = max(top, x.code[j]);
       }
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
-        const float f = top - x.code[j] > 126u ? 0.f : pow2(int(x.code[j]) - int(top));
+        const int d = min(0, int(x.code[j]) - int(top));  // above 0 only for zeros
+        const float f = d < -126 ? 0.f : pow2(d);
         const uint32_t v[4] = {x.w[j].x, x.w[j].y, x.w[j].z, x.w[j].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -864,8 +866,6 @@ bskv_status run(const char* who, const bskv_plan* plan, const void* q, const int
   wp.page_size = FastDiv(plan->page_size);
   wp.num_qo_heads = plan->num_qo_heads; wp.causal = plan->causal;
   wp.off_workers = meta_word(plan, H_OFF_WORKERS);
-  wp.off_chunks = meta_word(plan, H_OFF_CHUNKS);
-  wp.off_aux0 = meta_word(plan, H_OFF_AUX0);
   wp.off_aux1 = meta_word(plan, H_OFF_AUX1);
   wp.off_req = meta_word(plan, H_OFF_MERGES);
   wp.num_workers = meta_word(plan, H_WORKERS);

@@ -105,10 +105,6 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int row) {
   else return *reinterpret_cast<const uint16_t*>(s + 2 * row);
 }
 
-// 2^k for the power of two with bits `x`, inverted exactly (0 for 2^127).
-__device__ __forceinline__ float pow2_inverse(float x) {
-  return __uint_as_float((254u << 23) - __float_as_uint(x));
-}
 __device__ __forceinline__ int exponent_of(float x) {
   return int(__float_as_uint(x) >> 23) - 127;
 }

@@ -410,7 +410,11 @@ bskv_status bskv_run_attn_weights(const bskv_plan* plan, const void* q, const in
                                   const void* kv_cache, const int64_t* kv_strides,
                                   const float* lse, float* scores, const int64_t* scores_strides,
                                   float decay, float sm_scale, void* stream);
-/* The same over a 4-bit paged cache (a key with scale code 255 gets a NaN score). */
+/*
+ * The same over a 4-bit paged cache. A key with scale code 255 gets a NaN score. With FP16 queries and
+ * more than 16 query rows (queries times heads of a group) of a request, a key's values below 2^-24 of
+ * its largest scale with values other than zero may round.
+ */
 bskv_status bskv_run_attn_weights_fp4(const bskv_plan* plan, const void* q,
                                       const int64_t* q_strides, const void* kv_codes,
                                       const int64_t* codes_strides, const void* kv_scales,

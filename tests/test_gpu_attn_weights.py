@@ -99,6 +99,28 @@ def test_weights(cuda, case, four):
     _check(d, keys, lse, scores, after, causal, decay)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("nq", [1, 20, 70])
+def test_weights_scales_of_any_size(cuda, dtype, nq):
+    """Scales that differ by 2^18 within a key, and blocks of zeros with scales far above them."""
+    lens, Hq, Hkv, D, ps = [150, 33], 4, 2, 128, 16
+    d = synth.paged_decode_inputs(871, 2, Hq, Hkv, D, ps, 0, 0, lengths=lens, dtype=dtype)
+    d["qo_indptr"] = torch.tensor([0, nq, 2 * nq], dtype=torch.int32)
+    g = torch.Generator().manual_seed(872)
+    d["q"] = torch.randn(2 * nq, Hq, D, generator=g).to(dtype)
+    lse, scores = torch.randn(2 * nq, Hq, generator=g) + 4.0, torch.rand(d["num_pages"], Hkv, ps, generator=g)
+    codes, scales = _cache(873, d, "cpu", 108, 127)
+    zero = (torch.rand(scales.shape, generator=g) < 0.3) & (scales != 255)
+    scales[zero] = 250
+    codes.view(*scales.shape, 16)[zero] &= 0x88  # zeros of either sign
+    p = bskv.bskv_plan_attn_weights(d["qo_indptr"], d["kv_indptr"], d["kv_indices"], d["kv_last_page_len"],
+                                    d["num_pages"], ps, Hq, Hkv, D, causal=False, dtype=dtype)
+    after = scores.clone().to(cuda)
+    bskv.bskv_run_attn_weights_fp4(p, d["q"].to(cuda), codes.to(cuda), scales.to(cuda), lse.to(cuda), after)
+    keys = oc.fp4_decode(codes[:, 0].numpy(), scales[:, 0].numpy())
+    _check(d, keys, lse, scores, after, False, 1.0)
+
+
 def test_weights_of_a_decode_sum_to_the_heads(cuda):
     """With the log-sum-exp of the decode itself, the weights of a request sum to its query heads."""
     d = synth.paged_decode_inputs(811, 6, 32, 8, 128, 16, 1, 900)
