@@ -805,29 +805,32 @@ def bskv_dequantize_fp4_paged(kv_codes, kv_scales, batch_indices, positions, kv_
     fn = "bskv_dequantize_fp4_paged"
     if (k_out is None) != (v_out is None):
         raise ValueError("%s: give both outputs or neither" % fn)
+    if dtype not in _read_layouts:
+        raise ValueError("%s: dtype is %s, not %s" % (fn, dtype, " or ".join(map(str, _read_layouts))))
+    dev, ks, vs, out_dtype, shape, cache, batch = _once(
+        _read_layouts[dtype], _check_dequantize, fn, dtype, k_out, v_out, batch_indices, positions,
+        kv_indptr, kv_indices, kv_codes, kv_scales)
     if k_out is None:
-        dev = _cuda_of(fn, "kv_codes", kv_codes)
-        if kv_codes.dim() != 5 or not isinstance(positions, torch.Tensor):
-            raise ValueError("%s: kv_codes must be [pages, 2, Hkv, page_size, D / 2]" % fn)
-        shape = (positions.numel(), kv_codes.shape[2], 2 * kv_codes.shape[4])
         k_out = torch.empty(shape, dtype=dtype, device=dev)
         v_out = torch.empty(shape, dtype=dtype, device=dev)
-    dev, ks, vs, out_dtype, rows, cache, batch = _once(
-        _call_layouts, _check_dequantize, fn, None, k_out, v_out, batch_indices, positions, kv_indptr, kv_indices,
-        kv_codes, kv_scales)
     _call(fn, dev, kv_codes.data_ptr(), cache[0], kv_scales.data_ptr(), cache[1],
           batch_indices.data_ptr(), positions.data_ptr(), kv_indptr.data_ptr(),
-          kv_indices.data_ptr(), *batch, k_out.data_ptr(), ks, v_out.data_ptr(), vs, out_dtype, *rows)
+          kv_indices.data_ptr(), *batch, k_out.data_ptr(), ks, v_out.data_ptr(), vs, out_dtype, *shape)
     return k_out, v_out
 
 
-def _check_dequantize(fn, _, k, v, batch_indices, positions, kv_indptr, kv_indices, kv_codes,
+_read_layouts = {torch.bfloat16: {}, torch.float16: {}, torch.float32: {}}
+
+
+def _check_dequantize(fn, dtype, k, v, batch_indices, positions, kv_indptr, kv_indices, kv_codes,
                       kv_scales):
     dev = _cuda_of(fn, "kv_codes", kv_codes)
-    if kv_codes.dim() != 5:
+    if kv_codes.dim() != 5 or not isinstance(positions, torch.Tensor):
         raise ValueError("%s: kv_codes must be [pages, 2, Hkv, page_size, D / 2]" % fn)
-    pages, _, _, page_size, _ = kv_codes.shape
-    rows_dev, nnz, heads, dim, batch = _fp4_rows(fn, k, v, _HALVES + _F32T, batch_indices, positions,
+    pages, _, heads, page_size, half = kv_codes.shape
+    if k is None:  # what the caller gets
+        k = v = torch.empty((positions.numel(), heads, 2 * half), dtype=dtype, device=dev)
+    rows_dev, nnz, heads, dim, batch = _fp4_rows(fn, k, v, tuple(_read_layouts), batch_indices, positions,
                                                  kv_indptr, kv_indices, written=True)
     cache = _fp4_cache(fn, kv_codes, kv_scales, rows_dev, pages, page_size, heads, dim)
     return (dev, _strides_of(k, 2), _strides_of(v, 2), _DT[k.dtype], (nnz, heads, dim), cache,
