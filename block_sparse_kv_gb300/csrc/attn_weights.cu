@@ -102,9 +102,11 @@ __device__ __forceinline__ float row_lse(const WeightsParams& p, const Request& 
   return __ldg(p.lse + int64_t(rq.qo + t) * p.num_qo_heads + kvh * p.group + head);
 }
 
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+// Sums over the four lanes of a quad: lane t gets that of x[t].
+__device__ __forceinline__ float quad_sums(const float (&x)[4], int t) {
+  const float a = (t & 2 ? x[2] : x[0]) + __shfl_xor_sync(0xffffffffu, t & 2 ? x[0] : x[2], 2);
+  const float b = (t & 2 ? x[3] : x[1]) + __shfl_xor_sync(0xffffffffu, t & 2 ? x[1] : x[3], 2);
+  return (t & 1 ? b : a) + __shfl_xor_sync(0xffffffffu, t & 1 ? a : b, 1);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -285,36 +287,46 @@ __global__ void __launch_bounds__(kWarps * 32, weights_ctas_per_sm(D, FP4))
     const int b = p.heads.divmod(ch.unit, kvh);
     const Request rq = request_of(p, b);
     load_rows<T, D, NT, FP4>(p, rq, kvh, lane, s);
+    // tiles up to here are seen by all rows, are whole and of older tokens
+    int plain = min(ch.end, rq.len - rq.nq);
+#pragma unroll
+    for (int j = 0; j < 2 * NT; ++j)
+      if (s.info[j].last >= 0) plain = min(plain, s.info[j].last + 1);
+    plain = __reduce_min_sync(0xffffffffu, plain);
     for (int at = ch.begin; at < ch.end; at += kTile, ++done) {
       cp_async_wait<kStages - 2>();
       __syncwarp();  // the tile is there for every lane, and the stage refilled next is free
       issue((done + kStages - 1) % kStages);
       const uint8_t* st = ring + (done % kStages) * kStride;
-      float sum[4];  // keys at + 8 i + g
+      auto tile = [&](auto is_plain) {
+        float sum[4];  // keys at + 8 i + g
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float x[NT][4];
-        dot_tile<T, D, NT, FP4>(st, h, lane, s, x);
+        for (int h = 0; h < 2; ++h) {
+          float x[NT][4];
+          dot_tile<T, D, NT, FP4>(st, h, lane, s, x);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int key = at + 16 * h + 8 * i + g;
-          float a = 0.f;
+          for (int i = 0; i < 2; ++i) {
+            const int key = at + 16 * h + 8 * i + g;
+            float a = 0.f;
 #pragma unroll
-          for (int j = 0; j < 2 * NT; ++j) {
-            const float e = fast_exp2(fmaf(x[j >> 1][2 * i + (j & 1)], s.c[j], -s.info[j].hi));
-            if (key <= s.info[j].last) a = fmaf(e, s.info[j].r, a);
+            for (int j = 0; j < 2 * NT; ++j) {
+              const float e = fast_exp2(fmaf(x[j >> 1][2 * i + (j & 1)], s.c[j], -s.info[j].hi));
+              if (is_plain ? s.info[j].last >= 0 : key <= s.info[j].last) a = fmaf(e, s.info[j].r, a);
+            }
+            sum[2 * h + i] = a;
           }
-          sum[2 * h + i] = quad_sum(a);
         }
-      }
-      // lane (g, t) writes key at + 8 t + g
-      const float mine = t == 0 ? sum[0] : t == 1 ? sum[1] : t == 2 ? sum[2] : sum[3];
-      const int r = 8 * t + g;
-      if (at + r < ch.end) {
-        float* dst = p.scores + *reinterpret_cast<const int64_t*>(st + Sh::kPlace + 8 * t) + g;
-        const bool fresh = !old || at + r >= rq.len - rq.nq;
-        *dst = fresh ? mine : fmaf(p.decay, *reinterpret_cast<const float*>(st + Sh::kOld + 4 * r), mine);
-      }
+        // lane (g, t) writes key at + 8 t + g
+        const float mine = quad_sums(sum, t);
+        const int r = 8 * t + g;
+        if (is_plain || at + r < ch.end) {
+          float* dst = p.scores + *reinterpret_cast<const int64_t*>(st + Sh::kPlace + 8 * t) + g;
+          const bool fresh = !old || (!is_plain && at + r >= rq.len - rq.nq);
+          *dst = fresh ? mine : fmaf(p.decay, *reinterpret_cast<const float*>(st + Sh::kOld + 4 * r), mine);
+        }
+      };
+      if (at + kTile <= plain) tile(std::true_type{});
+      else tile(std::false_type{});
     }
   }
   cp_async_wait<0>();
