@@ -15,7 +15,7 @@
 //     same chunk of the query are two k-steps, whatever the order of the dims. Query fragments stay
 //     in registers, each warp streams a range of tokens through a private ring of 32-token tiles
 //     filled by 16-byte asynchronous copies. Bound by reading K: 64 requests of 512 to 4096 tokens
-//     in 16 bits 53.0 us (5.9 TB/s); in 4 bits by instructions: 8 of 32000 to 40000 39.0 us (4.5 TB/s).
+//     in 16 bits 52.0 us (6.0 TB/s); in 4 bits by instructions: 8 of 32000 to 40000 36.6 us (4.8 TB/s).
 //   * tile (more rows, a prefill window): S = K Q^T by tcgen05, 128 keys against up to 128 query rows
 //     a product. A key is a TMEM lane and so a thread, which reads its row of S and adds up its
 //     weights: no reduction between threads, and two packed FMAs and two exponentials per two
@@ -808,7 +808,7 @@ bskv_status launch_stream(const bskv_plan* plan, WeightsParams& wp, cudaStream_t
   static std::atomic<int> allowed[64];
   if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "attn_weights: cudaFuncSetAttribute")) return s;
   // Plans have up to 16 workers per SM. Where fewer warps fit, a warp takes two workers' chunks in a row
-  // (64 requests of 512 to 4096 tokens at 8 warps per SM: 53.0 us, in two waves of CTAs 54.1).
+  // (64 requests of 512 to 4096 tokens at 8 warps per SM: 53.0 us where two waves of CTAs took 54.1).
   wp.take = wp.num_workers > plan->num_sms * kWarps * weights_ctas_per_sm(D, FP4) ? 2 : 1;
   const int warps = (wp.num_workers + wp.take - 1) / wp.take;
   kern<<<(warps + kWarps - 1) / kWarps, kWarps * 32, smem, st>>>(wp);

@@ -142,9 +142,9 @@ constexpr int fp4_ctas_per_sm(int column_tiles) { return column_tiles < 2 ? 3 : 
 // group, in every request): one worker per warp over ranges of tokens of (request, kv head)
 // units; {first query, queries, tokens} of each request stands in the merge section. Tile variant:
 // items of 128 keys of a request for one kv head, by a record of kWalkWords per request with tokens.
-// 64 requests of 2048 tokens, 8 kv heads of 128 dims, 4 to 8 rows: stream (8) 48.9 us, stream (16)
-// 50.5, tile 48.3; 16 rows: stream 52.1, tile 49.4; of 64 dims 31.0 and 42.5. In 4 bits 4 to 8 rows
-// take 21.8, 28.0 and 72 us, 16 rows stream 29.0, tile above 60.
+// 64 requests of 2048 tokens, 8 kv heads of 128 dims, 4 to 8 rows: stream (8) 46.7 us, stream (16)
+// about 49, tile 48; 16 rows: stream 49.3, tile 49; of 64 dims 30.8 and 42.5. In 4 bits 4 to 8 rows
+// take 20.9, 28 and above 60 us, 16 rows stream 28.5, tile above 60.
 enum WeightsVariant : int32_t { WEIGHTS_STREAM8 = 0, WEIGHTS_STREAM16 = 1, WEIGHTS_TILE = 2 };
 constexpr int kWeightsWarps = 4;
 constexpr int kWeightsKeys = 128;
