@@ -859,7 +859,8 @@ template <bool FP4>
 bskv_status run(const char* who, const bskv_plan* plan, const void* q, const int64_t* q_strides,
                 const float* lse, float* scores, const int64_t* scores_strides, float decay,
                 float sm_scale, WeightsParams& wp, cudaStream_t st) {
-  if (!q || !q_strides || !lse || !scores || !scores_strides) { set_error("%s: NULL tensor", who); return BSKV_ERR_INVALID_ARG; }
+  // without queries the scores fade only
+  if ((plan->M > 0 && (!q || !lse)) || !q_strides || !scores || !scores_strides) { set_error("%s: NULL tensor", who); return BSKV_ERR_INVALID_ARG; }
   if (!aligned16(q) || !aligned16(scores)) { set_error("%s: tensors must be 16-byte aligned", who); return BSKV_ERR_INVALID_ARG; }
   for (int i = 0; i < 2; ++i) {
     if (q_strides[i] <= 0 || q_strides[i] % 8) { set_error("%s: q strides must be positive multiples of 8 elements", who); return BSKV_ERR_INVALID_ARG; }

@@ -332,6 +332,23 @@ def test_layouts_are_checked_again_when_they_change(cuda):
     assert bskv.bskv_get_device_status() == 0
 
 
+def test_weights_without_queries_fade(cuda):
+    s = _case(cuda, lens=(40, 17))
+    w = bskv.bskv_plan_attn_weights(torch.zeros(3, dtype=torch.int32), *s["table"], s["pages"], PS, 16, H, D)
+    q, lse = torch.zeros(0, 16, D, dtype=torch.bfloat16, device=cuda), torch.zeros(0, 16, device=cuda)
+    want = s["scores"].clone()
+    for b, n in enumerate((40, 17)):
+        for j in range(n):
+            want[int(s["table"][1][int(s["table"][0][b]) + j // PS]), :, j % PS] *= 0.5
+    for four in (True, False):
+        got = s["scores"].clone()
+        if four:
+            bskv.bskv_run_attn_weights_fp4(w, q, s["codes"], s["scales"], lse, got, decay=0.5)
+        else:
+            bskv.bskv_run_attn_weights(w, q, s["kv"], lse, got, decay=0.5)
+        assert torch.equal(got, want)
+
+
 def test_runs_of_nothing(cuda):
     """Requests without tokens: outputs of zeros and -inf, nothing else touched."""
     lens = [0, 0]
