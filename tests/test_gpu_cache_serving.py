@@ -173,6 +173,7 @@ def test_graph_of_windows_and_halves(cuda):
     _graph_equal(run, [got, pool, kept])
 
 
+@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
 def test_plans_are_not_uploaded_by_a_capture(cuda):
     """A graph must not copy the plan's host memory at every replay."""
     s = _case(cuda)
