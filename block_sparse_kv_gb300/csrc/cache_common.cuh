@@ -36,10 +36,8 @@ __device__ __forceinline__ void wait_for_prior_grid() { asm volatile("griddepcon
 
 // ---- thread-block clusters ------------------------------------------------------------
 
-// The halves of a cluster barrier: what was written before a (releasing) arrival is visible after the
-// wait; after a relaxed arrival only the threads have met.
+// The halves of a cluster barrier: what was written before the arrival is visible after the wait.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {

@@ -20,10 +20,11 @@
 // written so far, which is why it may be read before that. A wave's rows therefore never meet, so
 // K, V, the scores and the 4-bit scales each go through their waves on their own CTA, or, where
 // there are few requests, on a cluster of up to 8 that shares the waves (131072 tokens of 8 heads
-// halved: 151 us; 8 requests of 8192 tokens halved: 150 us on one CTA each, 64 us on 4). The cluster's barrier need not release anything: a read has returned its value
-// before its thread arrives, and nobody reads what another CTA wrote (a releasing arrival waits
-// for the last writes: 272 and 93 us). Into other pages there is nothing to order and blocks of
-// rows have CTAs too.
+// halved: 178 us; 8 requests of 8192 tokens
+// halved: 150 us on one CTA each, 67 us on 4). The cluster's barrier waits for what its threads wrote
+// and read before, so it pays to hold many rows between two: 16 a thread, where 8 with the next 8
+// under way took 244 and 83 us. Into other pages there is nothing to order and blocks of rows have
+// CTAs too.
 // Bound by memory: of the widths 64, 128 and 256 bytes per row and CTA, whole rows were fastest in
 // place (138, 115 and 104 us), and eight CTAs per SM with two rows a thread ahead of four with
 // four (104 and 113 us). 537 MB in place in 83 us: 6.4 TB/s.
@@ -313,10 +314,10 @@ struct Places {
   int64_t from[kMoveTable], to[kMoveTable];  // bytes from the plane's base; to < 0: stays
 };
 
-// The table's rows [0, n) in waves of ROWS per thread. The next wave is read before the barrier and
-// the writes of this one.
-template <typename U, int ROWS, typename Arrive, typename Wait>
-__device__ __forceinline__ void move_rows(const Places& at, uint8_t* base, int shift, int n, Arrive arrive, Wait wait) {
+// The table's rows [0, n) in waves of ROWS per thread. Where a wave's barrier is the CTA's (SHARED
+// false), the next wave is read before it.
+template <typename U, int ROWS, bool SHARED, typename Sync>
+__device__ __forceinline__ void move_rows(const Places& at, uint8_t* base, int shift, int n, Sync sync) {
   const int row = threadIdx.x >> shift, per = kMoveThreads >> shift, wave = per * ROWS;
   base += (threadIdx.x & ((1 << shift) - 1)) * sizeof(U);
   auto read = [&](U (&x)[ROWS], int w) {
@@ -333,31 +334,34 @@ __device__ __forceinline__ void move_rows(const Places& at, uint8_t* base, int s
       if (j < n && at.to[j] >= 0) *reinterpret_cast<U*>(base + at.to[j]) = x[i];
     }
   };
-  U x0[ROWS] = {}, x1[ROWS] = {};
-  read(x0, 0);
-  for (int w = 0; w < n; w += 2 * wave) {
-    arrive(x0);
-    read(x1, w + wave);
-    wait();  // every read of the wave before its first write
-    write(x0, w);
-    if (w + wave >= n) break;
-    arrive(x1);
-    read(x0, w + 2 * wave);
-    wait();
-    write(x1, w + wave);
+  U x0[ROWS] = {};
+  if constexpr (SHARED) {
+    for (int w = 0; w < n; w += wave) {
+      read(x0, w);
+      sync();  // every read of the wave before its first write
+      write(x0, w);
+    }
+  } else {
+    U x1[ROWS] = {};
+    read(x0, 0);
+    for (int w = 0; w < n; w += 2 * wave) {
+      read(x1, w + wave);
+      sync();
+      write(x0, w);
+      if (w + wave >= n) break;
+      read(x0, w + 2 * wave);
+      sync();
+      write(x1, w + wave);
+    }
   }
 }
-
-__device__ __forceinline__ uint32_t first_word(uint4 x) { return x.x; }
-__device__ __forceinline__ uint32_t first_word(uint32_t x) { return x; }
 
 // SHARED: a slice's waves are spread over a cluster of `ctas` CTAs, in place.
 template <bool SHARED>
 __global__ void __launch_bounds__(kMoveThreads, SHARED ? 2 : 8)
     evict_move_kernel(const __grid_constant__ MoveParams mp, int ctas) {
-  constexpr int kRows = SHARED ? 8 : 2;
+  constexpr int kRows = SHARED ? 16 : 2;
   __shared__ Places at;
-  __shared__ volatile uint32_t seen[SHARED ? kMoveThreads : 1];
   const EvictParams& p = mp.e;
   const int rank = SHARED ? blockIdx.x % ctas : 0;
   const Plane& pl = mp.plane[SHARED ? blockIdx.x / ctas : blockIdx.x % p.planes];
@@ -395,27 +399,17 @@ __global__ void __launch_bounds__(kMoveThreads, SHARED ? 2 : 8)
       at.to[i] = to;
     }
     __syncthreads();
-    auto arrive = [&](const auto& x) {
-      if constexpr (SHARED) {  // with the values in hand: shared memory gets a word made of each
-        uint32_t all = 0;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) all ^= first_word(x[i]);
-        seen[threadIdx.x] = all;
-        __syncwarp();
-        cluster_arrive_relaxed();
-      }
-    };
-    auto wait = [&]() {
+    auto sync = [&]() {
       if constexpr (SHARED) {
         __syncwarp();
-        cluster_wait();
+        cluster_sync();
       } else if (p.in_place) {
         __syncthreads();
       }
     };
-    if (pl.unit == 16) move_rows<uint4, kRows>(at, base, pl.shift, n, arrive, wait);
-    else if (pl.unit == 4) move_rows<uint32_t, kRows>(at, base, pl.shift, n, arrive, wait);
-    else move_rows<uint16_t, kRows>(at, base, pl.shift, n, arrive, wait);
+    if (pl.unit == 16) move_rows<uint4, kRows, SHARED>(at, base, pl.shift, n, sync);
+    else if (pl.unit == 4) move_rows<uint32_t, kRows, SHARED>(at, base, pl.shift, n, sync);
+    else move_rows<uint16_t, kRows, SHARED>(at, base, pl.shift, n, sync);
   }
 }
 
@@ -517,7 +511,7 @@ extern "C" bskv_status bskv_run_evict(const bskv_plan* plan, float* scores,
   MoveParams mp{};
   int planes = 0;
   // whole rows, or 64 bytes of them where few long requests would leave SMs idle (131072 tokens of one
-  // head halved: 57 us, by whole rows 160)
+  // head halved: 61 us, by whole rows 160)
   const bool narrow = plan->in_place && plan->most >= 2 * kMoveShare &&
                       int64_t(plan->batch) * plan->num_kv_heads * plan->head_dim / 16 <= plan->num_sms / kMaxCluster;
   const int cols = narrow ? 64 : 2 * plan->head_dim;
