@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(tile_threads(FP4), 2)
       mbar_init(&sh.k_empty[i], 1);
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
-      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_full[i], FP4 ? 2 : 1);
       mbar_init(&sh.s_empty[i], kKeys);
     }
     sh.abort = 0;
@@ -534,6 +534,10 @@ __global__ void __launch_bounds__(tile_threads(FP4), 2)
                    kk > 0 ? 1u : 0u);
       }
       umma_commit_w(leader, &sh.s_full[sb]);
+      if constexpr (FP4) {  // with an arrival of its own the warp hands on the units that k_full gave it
+        if (leader) mbar_arrive(&sh.s_full[sb]);
+        __syncwarp();
+      }
       if (!single) umma_commit_w(leader, &sh.q_empty[qb]);
       if (last) umma_commit_w(leader, &sh.k_empty[kb]);
       ++n;

@@ -20,11 +20,10 @@
 // written so far, which is why it may be read before that. A wave's rows therefore never meet, so
 // K, V, the scores and the 4-bit scales each go through their waves on their own CTA, or, where
 // there are few requests, on a cluster of up to 8 that shares the waves (131072 tokens of 8 heads
-// halved: 178 us; 8 requests of 8192 tokens
-// halved: 150 us on one CTA each, 67 us on 4). The cluster's barrier waits for what its threads wrote
-// and read before, so it pays to hold many rows between two: 16 a thread, where 8 with the next 8
-// under way took 244 and 83 us. Into other pages there is nothing to order and blocks of rows have
-// CTAs too.
+// halved: 178 us; 8 requests of 8192 tokens halved: 150 us on one CTA each, 67 us on 4). The
+// cluster's barrier waits for what its threads wrote and read before, so it pays to hold many rows
+// between two: 16 a thread, where 8 with the next 8 under way took 244 and 83 us. Into other pages
+// there is nothing to order and blocks of rows have CTAs too.
 // Bound by memory: of the widths 64, 128 and 256 bytes per row and CTA, whole rows were fastest in
 // place (138, 115 and 104 us), and eight CTAs per SM with two rows a thread ahead of four with
 // four (104 and 113 us). 537 MB in place in 83 us: 6.4 TB/s.
