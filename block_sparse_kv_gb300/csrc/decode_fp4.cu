@@ -11,7 +11,8 @@
 // taken relative to (any reference gives the same softmax) is therefore not the largest logit but
 // 2^10 below the largest product so far of the head, up to a factor 2^5: products down to 2^-24 of
 // it keep f16's 11 bits, smaller ones are off by at most 2^-35 of it. It changes on the first tile
-// and rarely after, so a tile has no reduction over its tokens, only a vote.
+// and rarely after, so a tile has no reduction over its tokens, only a vote: a product past 2^15
+// moves it, and so do weights that sum to 2^97, which tokens whose values are zero reach without one.
 //
 // Tokens are the M = 16 rows of mma.sync m16n8k16 and the query heads of a kv head its N = 8
 // columns (two column tiles above 8 heads): with heads as rows a group of 4 would leave three
@@ -154,9 +155,14 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
   }
 }
 
+// A lane's sum of weights of one step (at most 4 tokens) past this calls for a new reference. A request
+// has at most 2^30 tokens, 16 or more of them a step, so the sum over the steps and the 8 lanes of a
+// head stays below 2^127.
+constexpr float kMaxAdd = 0x1p97f;
+
 // Raise a head's reference to 2^10 below the largest product of weight and scale among 16 H tokens:
-// a lane's 2 H logits (base 2) plus the exponents f of the tokens' largest scales. The weights
-// themselves stay within [2^-80, 2^100], whatever the scales. Returns what sums so far shrink by.
+// a lane's 2 H logits (base 2) plus the exponents f of the tokens' largest scales. The largest weight
+// of these tokens is then within [2^-80, 2^94], whatever the scales. Returns what sums so far shrink by.
 template <int N>
 __device__ __forceinline__ float raise_ref(float& ref, const float (&v)[N], const float (&f)[N]) {
   float top = v[0], need = v[0] + f[0];
@@ -167,7 +173,7 @@ __device__ __forceinline__ float raise_ref(float& ref, const float (&v)[N], cons
   }
   top = max_over_rows(top);
   need = max_over_rows(need);
-  need = fmaxf(ref, fminf(fmaxf(need - 10.f, top - 100.f), top + 80.f));
+  need = fmaxf(ref, fminf(fmaxf(need - 10.f, top - 94.f), top + 80.f));
   const float shrink = fast_exp2(ref - need);
   ref = need;
   return shrink;
@@ -281,7 +287,10 @@ __device__ __forceinline__ void some_tokens(const uint8_t* st, int first, int va
         }
       }
     }
-    return __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f));
+    float most = add[0];
+#pragma unroll
+    for (int j = 1; j < 2 * NT; ++j) most = fmaxf(most, add[j]);
+    return most > kMaxAdd || __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f));
   };
   const bool over = weigh();
   if (__any_sync(0xffffffffu, over || s.ref[0] == -INFINITY)) {
@@ -377,7 +386,7 @@ __device__ __forceinline__ void some_tokens4(const uint8_t* st, int first, int v
         top = __hmax2(top, *reinterpret_cast<const __half2*>(&pw[i][n]));
       }
     }
-    return __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f));
+    return add > kMaxAdd || __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f));
   };
   const bool over = weigh();
   if (__any_sync(0xffffffffu, over || s.ref == -INFINITY)) {
