@@ -161,7 +161,7 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
 constexpr float kMaxAdd = 0x1p97f;
 
 // Raise a head's reference to 2^10 below the largest product of weight and scale among 16 H tokens:
-// a lane's 2 H logits (base 2) plus the exponents f of the tokens' largest scales. The largest weight
+// a lane's 2 H logits (base 2) plus the exponents f of the tokens' largest scales (-inf without one). The largest weight
 // of these tokens is then within [2^-80, 2^94], whatever the scales. Returns what sums so far shrink by.
 template <int N>
 __device__ __forceinline__ float raise_ref(float& ref, const float (&v)[N], const float (&f)[N]) {
@@ -198,15 +198,26 @@ __device__ __forceinline__ void raise_refs(State<D, NT>& s, const float (&x)[NT]
   }
 }
 
-// Largest exponent of each token's value scales.
-template <int NB, int N>
-__device__ __forceinline__ void scale_exponents(const float (&sv)[N][NB], float (&f)[N]) {
+// Largest exponent of the scales of each token's value blocks, -inf where all values are zero or NaN. A
+// block of zeros gives nothing whatever its scale, which may stand far above the others': it becomes 0.
+// Row i of the lane is r0 + 8 i, its block blk at part blk ^ kx; the four lanes of a row look at a block
+// each.
+template <int D, int N>
+__device__ __forceinline__ void scale_exponents(const uint8_t* st, int r0, int kx, float (&sv)[N][Shape<D>::kBlocks],
+                                                float (&f)[N]) {
+  using Sh = Shape<D>;
+  const int quad = threadIdx.x & 28, mine = threadIdx.x & (Sh::kBlocks - 1);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
+    const uint4 c = *reinterpret_cast<const uint4*>(st + Sh::kV + (r0 + 8 * i) * Sh::kRow + ((mine ^ kx) << 4));
+    const uint32_t zeros = __ballot_sync(0xffffffffu, ((c.x | c.y | c.z | c.w) & 0x77777777u) == 0) >> quad;
     float big = 0.f;
 #pragma unroll
-    for (int blk = 0; blk < NB; ++blk) big = fmaxf(big, sv[i][blk]);
-    f[i] = float(exponent_of(big));
+    for (int blk = 0; blk < Sh::kBlocks; ++blk) {
+      if ((zeros >> blk & 1u) && sv[i][blk] == sv[i][blk]) sv[i][blk] = 0.f;
+      big = fmaxf(big, sv[i][blk]);
+    }
+    f[i] = big > 0.f ? float(exponent_of(big)) : -INFINITY;
   }
 }
 
@@ -295,7 +306,7 @@ __device__ __forceinline__ void some_tokens(const uint8_t* st, int first, int va
   const bool over = weigh();
   if (__any_sync(0xffffffffu, over || s.ref[0] == -INFINITY)) {
     float f[N];
-    scale_exponents(sv, f);
+    scale_exponents<D>(st, r0, kx, sv, f);
     raise_refs<D, NT>(s, x, f);
     weigh();
   }
@@ -391,7 +402,7 @@ __device__ __forceinline__ void some_tokens4(const uint8_t* st, int first, int v
   const bool over = weigh();
   if (__any_sync(0xffffffffu, over || s.ref == -INFINITY)) {
     float f[N], v[N];
-    scale_exponents(sv, f);
+    scale_exponents<D>(st, r0, kx, sv, f);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = x[i] * s.c;
     const float shrink = raise_ref(s.ref, v, f);

@@ -133,3 +133,23 @@ def test_values_of_zero_behind_ordinary_ones(cuda, rise, Hq, workers):
     for end in (600, L):  # without and with the last ordinary ones
         _check(cuda, [end], [np.stack([kc, vc])[:, :, :end]], [np.stack([ks, vs])[:, :, :end]],
                _ones(1, Hq, 1, D, torch.bfloat16), 1.0, workers)
+
+
+@pytest.mark.parametrize("workers", [1, 4])
+@pytest.mark.parametrize("Hq", [4, 8, 16])
+@pytest.mark.parametrize("scale", [160, 250])
+def test_blocks_of_zeros_under_large_scales(cuda, scale, Hq, workers):
+    """Blocks of zeros, of either sign, whose scale is far above that of the values beside them."""
+    L, D = 500, 128
+    g = np.random.default_rng(13)
+    kc, ks = _values(14, 1, L, D, 120, 123)
+    vc, vs = _values(15, 1, L, D)
+    zero = g.random(vs.shape) < 0.3
+    zero[:, :40] = False
+    zero[0, 20, 1] = zero[0, 470, 3] = True
+    vs[zero] = scale
+    vc.reshape(vs.shape + (16,))[zero] &= 0x88
+    q = torch.from_numpy(g.standard_normal((1, Hq, D))).to(torch.bfloat16)
+    _check(cuda, [L], [np.stack([kc, vc])], [np.stack([ks, vs])], q, D ** -0.5, workers)
+    first = np.roll(vs, -20, 1), np.roll(vc, -20, 1)  # and on the first token
+    _check(cuda, [L], [np.stack([kc, first[1]])], [np.stack([ks, first[0]])], q, D ** -0.5, workers)
