@@ -13,6 +13,8 @@
 // it keep f16's 11 bits, smaller ones are off by at most 2^-35 of it. It changes on the first tile
 // and rarely after, so a tile has no reduction over its tokens, only a vote: a product past 2^15
 // moves it, and so do weights that sum to 2^97, which tokens whose values are zero reach without one.
+// Value scales so large that the weights would leave fp32's range at its lower end are taken relative to
+// a power of two of the (request, kv head).
 //
 // Tokens are the M = 16 rows of mma.sync m16n8k16 and the query heads of a kv head its N = 8
 // columns (two column tiles above 8 heads): with heads as rows a group of 4 would leave three
@@ -27,7 +29,7 @@
 // What bounds it: the cache is read once, 136 bytes per token and kv head of 128 dims against
 // 512 in 16 bits, so instructions issued per byte are what to save: converting and pairing 4-bit
 // values keeps the ALU pipe busy for half to two thirds of the time. 64 requests of 512 to 4096
-// tokens with 4 query heads per kv head take 39.5 us (4.1 TB/s), 8 of 131072 with 8 heads 233 us (4.9
+// tokens with 4 query heads per kv head take 39.9 us (4.0 TB/s), 8 of 131072 with 8 heads 239 us (4.8
 // TB/s). A warp works on 32 tokens at a time: the second 16's products fill the first's waits (41.2
 // and 239 us with 16). Two stages are enough of a ring (three: 41.9 and 243 us).
 // Each warp is a worker of its own over a range of one or more (request, kv
@@ -101,6 +103,7 @@ struct State {
   uint32_t q[NT][Shape<D>::kBlocks][4];     // query fragments (B operand), f16
   float o[NT][Shape<D>::kBlocks][2][4];     // O^T accumulators
   float ref[2 * NT], l[2 * NT], c[2 * NT];  // exponent reference, sum, logit scale (base 2, > 0)
+  int unit;                                 // value scales count relative to 2^unit >= 1; -1: no tokens yet
 };
 
 // Up to 4 query heads per kv head (NT = 0): column n of the products is head n / 2, so that a lane
@@ -113,6 +116,7 @@ struct State<D, 0> {
   uint32_t q[Shape<D>::kBlocks][4];
   float o[Shape<D>::kBlocks][4];  // values 32 b + 4 g .. + 3 of head t
   float ref, l, c;
+  int unit;
 };
 
 template <typename T, int D, int NT>
@@ -120,12 +124,14 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
                                        State<D, NT>& s) {
   constexpr int NB = Shape<D>::kBlocks;
   const int g = lane >> 2, t = lane & 3;
+  s.unit = -1;
+  // a column without a head keeps the reference +inf: its weights are 0 and it asks for nothing
   if constexpr (NT == 0) {
     const float back = load_q_f16<T, NB>(
         static_cast<const T*>(p.q) + b * p.q_s0 + (int64_t(kvh) * p.group + (g >> 1)) * p.q_s1,
         (g >> 1) < p.group, p.scale_log2 < 0.f, lane, s.q);
     s.c = fabsf(p.scale_log2) * __shfl_sync(0xffffffffu, back, 8 * t);
-    s.ref = -INFINITY;
+    s.ref = t < p.group ? -INFINITY : INFINITY;
     s.l = 0.f;
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) s.o[blk][0] = s.o[blk][1] = s.o[blk][2] = s.o[blk][3] = 0.f;
@@ -143,7 +149,7 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
     }
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {
-      s.ref[j] = -INFINITY;
+      s.ref[j] = 8 * (j >> 1) + 2 * t + (j & 1) < p.group ? -INFINITY : INFINITY;
       s.l[j] = 0.f;
     }
 #pragma unroll
@@ -160,42 +166,78 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
 // head stays below 2^127.
 constexpr float kMaxAdd = 0x1p97f;
 
-// Raise a head's reference to 2^10 below the largest product of weight and scale among 16 H tokens:
-// a lane's 2 H logits (base 2) plus the exponents f of the tokens' largest scales (-inf without one). The largest weight
-// of these tokens is then within [2^-80, 2^94], whatever the scales. Returns what sums so far shrink by.
+// What 16 H tokens ask of a head's reference, a lane giving 2 H logits (base 2) and the exponents f of
+// the tokens' largest scales (-inf without one): the largest logit, and of weight times scale.
+struct Need {
+  float top, product;
+};
 template <int N>
-__device__ __forceinline__ float raise_ref(float& ref, const float (&v)[N], const float (&f)[N]) {
-  float top = v[0], need = v[0] + f[0];
+__device__ __forceinline__ Need need_of(const float (&v)[N], const float (&f)[N]) {
+  Need n{v[0], v[0] + f[0]};
 #pragma unroll
   for (int i = 1; i < N; ++i) {
-    top = fmaxf(top, v[i]);
-    need = fmaxf(need, v[i] + f[i]);
+    n.top = fmaxf(n.top, v[i]);
+    n.product = fmaxf(n.product, v[i] + f[i]);
   }
-  top = max_over_rows(top);
-  need = max_over_rows(need);
-  need = fmaxf(ref, fminf(fmaxf(need - 10.f, top - 94.f), top + 80.f));
-  const float shrink = fast_exp2(ref - need);
-  ref = need;
+  return Need{max_over_rows(n.top), max_over_rows(n.product)};
+}
+// By how many powers of two the unit has to grow so that a reference 2^10 below the head's largest
+// product stands at most 2^40 above its largest weight so far, which is 2^-40 of the old reference or
+// more.
+__device__ __forceinline__ float unit_growth(float ref, const Need& n, int unit) {
+  const float x = n.product - 10.f - max(unit, 0) - fmaxf(n.top, ref - 40.f);
+  return x > 40.f ? ceilf(x) : 0.f;
+}
+// The reference 2^10 below the largest product, relative to the unit, and at most 2^94 below the largest
+// weight; it never falls. Returns what sums so far shrink by.
+__device__ __forceinline__ float raise_ref(float& ref, const Need& n, int unit) {
+  const float to = fmaxf(ref, fmaxf(n.product - 10.f - unit, n.top - 94.f));
+  const float shrink = fast_exp2(ref - to);
+  ref = to;
   return shrink;
+}
+// The warp's unit grows by the most that a lane asks for; returns the factor for values summed so far.
+__device__ __forceinline__ float grow_unit(int& unit, float growth) {
+  const int by = __reduce_max_sync(0xffffffffu, int(growth));
+  unit = max(unit, 0) + by;
+  return pow2(-by);
 }
 
 template <int D, int NT, int N>
 __device__ __forceinline__ void raise_refs(State<D, NT>& s, const float (&x)[NT][2][N], const float (&f)[N]) {
+  Need need[2 * NT];
+  float growth = 0.f;
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
     float v[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = x[j >> 1][j & 1][i] * s.c[j];
-    const float shrink = raise_ref(s.ref[j], v, f);
+    need[j] = need_of(v, f);
+    growth = fmaxf(growth, unit_growth(s.ref[j], need[j], s.unit));
+  }
+  const float less = grow_unit(s.unit, growth);
+#pragma unroll
+  for (int j = 0; j < 2 * NT; ++j) {
+    const float shrink = raise_ref(s.ref[j], need[j], s.unit);
     s.l[j] *= shrink;
 #pragma unroll
     for (int blk = 0; blk < Shape<D>::kBlocks; ++blk)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        s.o[j >> 1][blk][i][j & 1] *= shrink;
-        s.o[j >> 1][blk][i][(j & 1) + 2] *= shrink;
+        s.o[j >> 1][blk][i][j & 1] *= shrink * less;
+        s.o[j >> 1][blk][i][(j & 1) + 2] *= shrink * less;
       }
   }
+}
+
+// The lane's value scales relative to the unit.
+template <int NB, int N>
+__device__ __forceinline__ void to_unit(int unit, float (&sv)[N][NB]) {
+  const float u = pow2(-unit);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) sv[i][blk] *= u;
 }
 
 // Largest exponent of the scales of each token's value blocks, -inf where all values are zero or NaN. A
@@ -267,7 +309,9 @@ __device__ __forceinline__ void some_tokens(const uint8_t* st, int first, int va
     }
   }
   // Weights relative to the reference, times the value scales, as f16 pairs of two heads. Products
-  // up to 2^15 are safe in f16; the first tokens, and later ones with a larger product, set it.
+  // up to 2^15 are safe in f16; the first tokens, and later ones with a larger product, set it. Where the
+  // unit is above 1 all tokens take the second way: a branch around the factor in the first costs ordinary
+  // caches 5 to 7 % (64 requests of 512 to 4096 tokens 41.7 us, 8 of 131072 with 8 heads 249).
   float sv[N][NB];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -304,10 +348,11 @@ __device__ __forceinline__ void some_tokens(const uint8_t* st, int first, int va
     return most > kMaxAdd || __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f));
   };
   const bool over = weigh();
-  if (__any_sync(0xffffffffu, over || s.ref[0] == -INFINITY)) {
+  if (__any_sync(0xffffffffu, over || s.unit != 0)) {
     float f[N];
     scale_exponents<D>(st, r0, kx, sv, f);
     raise_refs<D, NT>(s, x, f);
+    to_unit(s.unit, sv);
     weigh();
   }
 #pragma unroll
@@ -400,17 +445,20 @@ __device__ __forceinline__ void some_tokens4(const uint8_t* st, int first, int v
     return add > kMaxAdd || __hgt(__hmax(__low2half(top), __high2half(top)), __float2half(32768.f));
   };
   const bool over = weigh();
-  if (__any_sync(0xffffffffu, over || s.ref == -INFINITY)) {
+  if (__any_sync(0xffffffffu, over || s.unit != 0)) {
     float f[N], v[N];
     scale_exponents<D>(st, r0, kx, sv, f);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = x[i] * s.c;
-    const float shrink = raise_ref(s.ref, v, f);
+    const Need need = need_of(v, f);
+    const float less = grow_unit(s.unit, unit_growth(s.ref, need, s.unit));
+    const float shrink = raise_ref(s.ref, need, s.unit);
     s.l *= shrink;
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s.o[blk][i] *= shrink;
+      for (int i = 0; i < 4; ++i) s.o[blk][i] *= shrink * less;
+    to_unit(s.unit, sv);
     weigh();
   }
   s.l += add;
@@ -457,6 +505,7 @@ __device__ __forceinline__ void finish(const Fp4DecodeParams& p, int b, int kvh,
                                        State<D, NT>& s) {
   constexpr int NB = Shape<D>::kBlocks;
   const int g = lane >> 2, t = lane & 3;
+  const float u = pow2(s.unit);
   if constexpr (NT == 0) {
     const float l = sum_over_rows(s.l), inv = 1.f / l;
     if (t >= p.group) return;
@@ -464,7 +513,7 @@ __device__ __forceinline__ void finish(const Fp4DecodeParams& p, int b, int kvh,
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk)
       put_head<T, D>(p, b, kvh, slot, t, 32 * blk + 4 * g,
-                     make_float4(s.o[blk][0] * inv, s.o[blk][1] * inv, s.o[blk][2] * inv, s.o[blk][3] * inv));
+                     make_float4(s.o[blk][0] * inv * u, s.o[blk][1] * inv * u, s.o[blk][2] * inv * u, s.o[blk][3] * inv * u));
   } else {
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {
@@ -476,7 +525,7 @@ __device__ __forceinline__ void finish(const Fp4DecodeParams& p, int b, int kvh,
       for (int blk = 0; blk < NB; ++blk) {
         const auto& o = s.o[j >> 1][blk];
         put_head<T, D>(p, b, kvh, slot, h, 32 * blk + 4 * g,
-                       make_float4(o[0][e] * inv, o[0][e + 2] * inv, o[1][e] * inv, o[1][e + 2] * inv));
+                       make_float4(o[0][e] * inv * u, o[0][e + 2] * inv * u, o[1][e] * inv * u, o[1][e + 2] * inv * u));
       }
     }
   }

@@ -153,3 +153,25 @@ def test_blocks_of_zeros_under_large_scales(cuda, scale, Hq, workers):
     _check(cuda, [L], [np.stack([kc, vc])], [np.stack([ks, vs])], q, D ** -0.5, workers)
     first = np.roll(vs, -20, 1), np.roll(vc, -20, 1)  # and on the first token
     _check(cuda, [L], [np.stack([kc, first[1]])], [np.stack([ks, first[0]])], q, D ** -0.5, workers)
+
+
+@pytest.mark.parametrize("workers", [1, 4])
+@pytest.mark.parametrize("Hq, D", [(4, 128), (3, 64), (8, 128), (16, 64)])
+@pytest.mark.parametrize("lo, hi", [(223, 249), (100, 249), (1, 30)])
+def test_values_to_the_ends_of_the_range(cuda, lo, hi, Hq, D, workers):
+    """Values of 2^96 to 2^124, alone and beside ordinary ones that follow or precede them, and of
+    less than 2^-96."""
+    L = 500
+    kc, ks = _values(16, 1, L, D, 120, 123)
+    vc, vs = _values(17, 1, L, D, lo, hi)
+    rows = [(vc, vs)]
+    if hi > 127:
+        late, early = vs.copy(), vs.copy()
+        late[:, :300] = 124
+        early[:, 100:] = 124
+        rows += [(vc, late), (vc, early)]
+    q = torch.from_numpy(np.random.default_rng(18).standard_normal((3, Hq, D))).to(torch.bfloat16)
+    q[1] = 0
+    q[2] *= 16
+    _check(cuda, [L] * len(rows), [np.stack([kc, c]) for c, _ in rows], [np.stack([ks, s]) for _, s in rows],
+           q[:len(rows)], D ** -0.5, workers)
