@@ -119,6 +119,12 @@ struct State<D, 0> {
   int unit;
 };
 
+// Scale (base 2, > 0) of a head's logits; `back` is the power of two its query was divided by. Above 0
+// even where the product is not: a masked token's -inf times 0 would be NaN.
+__device__ __forceinline__ float logit_scale(float scale_log2, float back) {
+  return fmaxf(fabsf(scale_log2) * back, 0x1p-149f);
+}
+
 template <typename T, int D, int NT>
 __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh, int lane,
                                        State<D, NT>& s) {
@@ -130,7 +136,7 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
     const float back = load_q_f16<T, NB>(
         static_cast<const T*>(p.q) + b * p.q_s0 + (int64_t(kvh) * p.group + (g >> 1)) * p.q_s1,
         (g >> 1) < p.group, p.scale_log2 < 0.f, lane, s.q);
-    s.c = fabsf(p.scale_log2) * __shfl_sync(0xffffffffu, back, 8 * t);
+    s.c = logit_scale(p.scale_log2, __shfl_sync(0xffffffffu, back, 8 * t));
     s.ref = t < p.group ? -INFINITY : INFINITY;
     s.l = 0.f;
 #pragma unroll
@@ -144,8 +150,8 @@ __device__ __forceinline__ void load_q(const Fp4DecodeParams& p, int b, int kvh,
           static_cast<const T*>(p.q) + b * p.q_s0 + (int64_t(kvh) * p.group + h) * p.q_s1,
           h < p.group, p.scale_log2 < 0.f, lane, s.q[nt]);
       // columns 2t and 2t + 1 belong to the heads of lanes 8t and 8t + 4
-      s.c[2 * nt] = fabsf(p.scale_log2) * __shfl_sync(0xffffffffu, back, 8 * t);
-      s.c[2 * nt + 1] = fabsf(p.scale_log2) * __shfl_sync(0xffffffffu, back, 8 * t + 4);
+      s.c[2 * nt] = logit_scale(p.scale_log2, __shfl_sync(0xffffffffu, back, 8 * t));
+      s.c[2 * nt + 1] = logit_scale(p.scale_log2, __shfl_sync(0xffffffffu, back, 8 * t + 4));
     }
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {

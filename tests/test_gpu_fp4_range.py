@@ -175,3 +175,15 @@ def test_values_to_the_ends_of_the_range(cuda, lo, hi, Hq, D, workers):
     q[2] *= 16
     _check(cuda, [L] * len(rows), [np.stack([kc, c]) for c, _ in rows], [np.stack([ks, s]) for _, s in rows],
            q[:len(rows)], D ** -0.5, workers)
+
+
+@pytest.mark.parametrize("Hq", [4, 8])
+def test_a_scale_that_leaves_no_logits(cuda, Hq):
+    """bf16 queries of zeros or near the type's smallest under a tiny sm_scale: every token weighs the
+    same, and those past the end nothing."""
+    L, D = 37, 128
+    kc, ks = _values(19, 1, L, D)
+    vc, vs = _values(20, 1, L, D)
+    for size in (0.0, 1e-38):
+        q = torch.full((1, Hq, D), size, dtype=torch.bfloat16)
+        _check(cuda, [L], [np.stack([kc, vc])], [np.stack([ks, vs])], q, 1e-9, 1)
