@@ -91,7 +91,7 @@ __device__ __forceinline__ RowInfo row_info(const WeightsParams& p, const Reques
   o.hi = lse * kLog2e;
   const float lo = isinf(o.hi) ? 0.f : fmaf(lse, kLog2e, -o.hi) + lse * kLog2eLow;
   o.r = exp2f(-lo);
-  o.last = p.causal ? tok + rq.len - rq.nq : INT32_MAX;
+  o.last = p.causal ? tok + rq.len - rq.nq : rq.len - 1;
   return o;
 }
 // Log-sum-exp of query row `row` (token, head of the group); -inf past the request's queries.

@@ -176,3 +176,45 @@ def test_weights_strides(cuda):
     bskv.bskv_run_attn_weights(p, big[:, 1::2], kv, lse.to(cuda), scores, sm_scale=0.04)
     _check(d, _f64(d["kv_cache"][:, 0]), lse, before, scores, True, 1.0)
     assert torch.equal(pool[:, 0::2], rest[:, 0::2]) and torch.equal(pool[:, 5], rest[:, 5])
+
+
+def _many(cuda, lens, Hq, Hkv, D, ps, nq, dtype, causal, decay, four, plans):
+    """Scores of the same call by plans for several numbers of SMs: within the tolerance of the oracle,
+    and, as a key's sum does not depend on who makes it, the same bits."""
+    d = synth.paged_decode_inputs(840 + Hq, len(lens), Hq, Hkv, D, ps, 0, 0, lengths=lens, dtype=dtype)
+    d["qo_indptr"] = torch.tensor([0] + list(np.cumsum(nq)), dtype=torch.int32)
+    g = torch.Generator().manual_seed(841)
+    n = int(d["qo_indptr"][-1])
+    d["q"] = torch.randn(n, Hq, D, generator=g).to(dtype)
+    lse = torch.randn(n, Hq, generator=g) + 5.0
+    lse[n // 2, 0] = -float("inf")
+    scores = torch.rand(d["num_pages"], Hkv, ps, generator=g) * 3
+    q, z = d["q"].to(cuda), lse.to(cuda)
+    if four:
+        codes, scales = _cache(842, d, cuda, 120, 126)
+        keys = oc.fp4_decode(codes[:, 0].cpu().numpy(), scales[:, 0].cpu().numpy())
+    else:
+        keys, kv = _f64(d["kv_cache"][:, 0]), d["kv_cache"].to(cuda)
+    first = None
+    for sms in plans:
+        p = bskv.bskv_plan_attn_weights(d["qo_indptr"], d["kv_indptr"], d["kv_indices"], d["kv_last_page_len"],
+                                        d["num_pages"], ps, Hq, Hkv, D, causal=causal, dtype=dtype, num_sms=sms)
+        after = scores.clone().to(cuda)
+        if four:
+            bskv.bskv_run_attn_weights_fp4(p, q, codes, scales, z, after, decay=decay)
+        else:
+            bskv.bskv_run_attn_weights(p, q, kv, z, after, decay=decay)
+        torch.cuda.synchronize()
+        if first is None:
+            first = after
+            _check(d, keys, lse, scores, after, causal, decay)
+        assert torch.equal(after.view(torch.int32), first.view(torch.int32)), sms
+    assert bskv.bskv_get_device_status() == 0
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_weights_of_long_requests_without_a_mask(cuda, four):
+    """Every row sees every key, over many whole tiles: one query and its last-query mask are the same."""
+    for causal in (False, True):
+        _many(cuda, [900, 40, 3001], 8, 2, 128, 16, [1, 1, 1], torch.bfloat16, causal, 0.5, four, (1, None))
+    _many(cuda, [900, 40, 3001], 8, 2, 64, 16, [3, 1, 2], torch.float16, False, 1.0, four, (1, None))
