@@ -218,3 +218,29 @@ def test_weights_of_long_requests_without_a_mask(cuda, four):
     for causal in (False, True):
         _many(cuda, [900, 40, 3001], 8, 2, 128, 16, [1, 1, 1], torch.bfloat16, causal, 0.5, four, (1, None))
     _many(cuda, [900, 40, 3001], 8, 2, 64, 16, [3, 1, 2], torch.float16, False, 1.0, four, (1, None))
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("Hq, Hkv, D, ps, nq, dtype, causal, decay", [
+    (12, 3, 128, 16, [1] * 5, torch.bfloat16, True, 0.75),         # two workers per warp in 16 bits
+    (12, 3, 64, 8, [1] * 5, torch.float16, True, 1.0),
+    (6, 2, 128, 48, [4, 1, 0, 5, 2], torch.bfloat16, True, 0.0),   # 9 to 16 rows
+    (16, 1, 128, 64, [1] * 5, torch.float16, False, 0.5),
+])
+def test_weights_stream_of_many_tiles(cuda, four, Hq, Hkv, D, ps, nq, dtype, causal, decay):
+    """16 workers for everything: rings that turn over, chunks of several units, windows of page ids."""
+    _many(cuda, [2100, 33, 0, 1207, 5], Hq, Hkv, D, ps, nq, dtype, causal, decay, four, (1, 2, None))
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("Hq, Hkv, D, ps, nq, dtype, causal, decay", [
+    (8, 2, 128, 16, [20, 0, 7, 32, 1], torch.bfloat16, True, 0.75),    # one product an item, items without one
+    (8, 2, 64, 8, [9, 30, 2, 31, 5], torch.float16, False, 0.0),
+    (40, 2, 128, 64, [6, 3, 0, 1, 2], torch.bfloat16, True, 1.0),      # 20 heads per kv head
+    (8, 2, 128, 16, [70, 0, 1, 333, 40], torch.bfloat16, True, 0.75),  # several products
+    (6, 3, 64, 32, [200, 65, 0, 64, 129], torch.float16, False, 0.5),
+    (4, 4, 128, 48, [500, 900, 1, 129, 2], torch.float16, True, 1.0),  # more queries than tokens
+])
+def test_weights_tile_of_many_items(cuda, four, Hq, Hkv, D, ps, nq, dtype, causal, decay):
+    """Two CTAs, or four, for everything: both key buffers, queries that change, every parity."""
+    _many(cuda, [1000, 150, 1, 2049, 260], Hq, Hkv, D, ps, nq, dtype, causal, decay, four, (1, 2, None))

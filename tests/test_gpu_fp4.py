@@ -307,3 +307,32 @@ def test_decode_strides_and_scale(cuda):
     bskv.bskv_run_decode_fp4(p, big[:, ::2], tok, scales, out=out[:, 1::3], lse=lse, sm_scale=0.05)
     _check_decode(d, torch.bfloat16, codes, scales, out[:, 1::3], lse)
     assert bool((out[:, 0::3] == -7).all()) and bool((out[:, 2::3] == -7).all())
+
+
+@pytest.mark.parametrize("n, H, D", [(6001, 8, 128), (40003, 8, 128), (30011, 3, 64)])
+def test_append_and_read_of_many_rows(cuda, n, H, D):
+    """Spans of several passes per CTA give the bytes and values that short calls give."""
+    ps, pages = 16, -(-n // 16)
+    g = torch.Generator(device=cuda).manual_seed(61)
+    indptr = torch.tensor([0, pages], dtype=torch.int32, device=cuda)
+    indices = torch.randperm(pages, generator=g, device=cuda).to(torch.int32)
+    k, v = (torch.randn(n, H, D, generator=g, device=cuda).to(torch.bfloat16) for _ in range(2))
+    bi = torch.zeros(n, dtype=torch.int32, device=cuda)
+    pos = torch.randperm(n, generator=g, device=cuda).to(torch.int32)
+    got = []
+    for step in (n, 777):
+        codes = torch.zeros((pages, 2, H, ps, D // 2), dtype=torch.uint8, device=cuda)
+        scales = torch.zeros((pages, 2, H, ps, D // 32), dtype=torch.uint8, device=cuda)
+        rows = []
+        for i in range(0, n, step):
+            at = slice(i, i + step)
+            bskv.bskv_quantize_fp4_append_paged(k[at], v[at], bi[at].clone(), pos[at].clone(), indptr, indices, codes,
+                                                scales)
+        for i in range(0, n, step):
+            at = slice(i, i + step)
+            rows.append(bskv.bskv_dequantize_fp4_paged(codes, scales, bi[at].clone(), pos[at].clone(), indptr, indices))
+        got.append((codes, scales, torch.cat([r[0] for r in rows]), torch.cat([r[1] for r in rows])))
+    torch.cuda.synchronize()
+    assert bskv.bskv_get_device_status() == 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
