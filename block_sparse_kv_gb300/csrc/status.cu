@@ -7,6 +7,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "launch.h"
+#include "smem_limit.h"
 
 namespace bskv {
 
@@ -66,12 +67,11 @@ bskv_status status_args(dev::StatusArgs* out) {
 bskv_status allow_smem(const void* kernel, size_t bytes, std::atomic<int> (&allowed)[64], const char* what) {
   int d = 0;
   if (bskv_status s = cuda_check(cudaGetDevice(&d), "cudaGetDevice")) return s;
-  if (d >= 0 && d < 64 && allowed[d].load(std::memory_order_relaxed) >= int(bytes)) return BSKV_OK;
-  if (bskv_status s = cuda_check(
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)), what))
-    return s;
-  if (d >= 0 && d < 64) allowed[d].store(int(bytes), std::memory_order_relaxed);
-  return BSKV_OK;
+  if (d < 0 || d >= 64) { set_error("device ordinal %d too large", d); return BSKV_ERR_UNSUPPORTED; }
+  static std::mutex mu;  // not the status words': their look-up may wait for the device's context
+  return raise_smem_limit(allowed[d], mu, int(bytes), [&](int n) {
+    return cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, n), what);
+  });
 }
 
 }  // namespace bskv
