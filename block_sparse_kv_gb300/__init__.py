@@ -166,6 +166,10 @@ def _stream(t=None):
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _num_sms(device=None):
     if torch.cuda.is_available():
         d = torch.cuda.current_device() if device is None else torch.device(device).index or 0
@@ -182,7 +186,13 @@ def bskv_last_error_message():
 
 
 class Plan:
-    """Host plan handle plus (after upload) its device int workspace."""
+    """Host plan handle plus (after upload) its device workspaces.
+
+    A run on another stream than the upload's waits for the upload, and the workspaces' memory is
+    not given to anyone else before the runs are done, also where the plan is dropped after a run.
+    Runs of one plan share its workspaces: on several streams they have to be ordered by events.
+    Captured runs are not ordered behind the upload (wait for it before the capture begins, as
+    torch.cuda.graph does), and their graph needs the plan for as long as it is replayed."""
 
     def __init__(self, handle, kind, **info):
         self._h = ctypes.c_void_p(handle)
@@ -191,6 +201,8 @@ class Plan:
         self.layouts = {}  # of tensors that passed a run's checks
         self.int_ws = None
         self.float_ws = None
+        self._uploaded = None    # event on the upload's stream
+        self._streams = set()    # streams whose runs are ordered behind the upload
 
     def __del__(self):
         if getattr(self, "_h", None) and self._h.value and _lib is not None:
@@ -228,7 +240,29 @@ class Plan:
                                                         int_ws.numel(), _stream(int_ws)))
         self.int_ws = int_ws
         self.float_ws = float_ws
+        self._streams = set()
+        self._uploaded = None
+        with torch.cuda.device(int_ws.device):
+            if not torch.cuda.is_current_stream_capturing():
+                self._uploaded = torch.cuda.current_stream().record_event()
+                self._streams.add(_raw_stream(int_ws.device.index))
         return self
+
+    def on_stream(self, device):
+        """Before a run on the current stream of the device: uploads at the first run, and lets a
+        stream that is new to the plan wait for the upload."""
+        if self.int_ws is None:
+            self.upload(device)
+        elif _raw_stream(device.index) not in self._streams:
+            with torch.cuda.device(device):
+                if self._uploaded is None or torch.cuda.is_current_stream_capturing():
+                    return
+                stream = torch.cuda.current_stream()
+                stream.wait_event(self._uploaded)
+                for ws in (self.int_ws, self.float_ws):
+                    if ws is not None:
+                        ws.record_stream(stream)
+                self._streams.add(stream.cuda_stream)
 
 
 def bskv_plan_decode(kv_indptr, kv_indices, kv_last_page_len, num_pages, page_size,
@@ -254,8 +288,7 @@ def bskv_run_decode(plan, q, kv_cache, out=None, lse=None, return_lse=False, sm_
     """Decode one query token per request; kv_cache [pages, 2, Hkv, page_size, D] (any
     strides with a contiguous last dim)."""
     lib = load_library()
-    if plan.int_ws is None:
-        plan.upload(q.device)
+    plan.on_stream(q.device)
     B, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
@@ -283,6 +316,8 @@ def bskv_decode_merge(plan, out, lse=None):
     """Merge the split-KV partial states a bskv_run_decode_partial left in the plan's
     float workspace into out (and lse)."""
     lib = load_library()
+    if plan.int_ws is not None:
+        plan.on_stream(out.device)
     fw = plan.float_ws
     _check("bskv_decode_merge", lib.bskv_decode_merge(
         plan.handle, out.data_ptr(), _strides(out.stride(0), out.stride(1)), _ptr(lse), _ptr(fw),
@@ -335,8 +370,7 @@ def bskv_plan_bsr(indptr, indices, M, N, R, C, num_qo_heads, num_kv_heads, head_
 
 def bskv_run_bsr(plan, q, k, v, out=None, lse=None, return_lse=False, sm_scale=None):
     lib = load_library()
-    if plan.int_ws is None:
-        plan.upload(q.device)
+    plan.on_stream(q.device)
     M, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
@@ -373,8 +407,7 @@ def bskv_run_bsr_masked(plan, q, k, v, packed_mask, out=None, lse=None, return_l
                         sm_scale=None):
     """packed_mask: uint8 device tensor, the (nnz, R, C) mask packed little-endian per byte."""
     lib = load_library()
-    if plan.int_ws is None:
-        plan.upload(q.device)
+    plan.on_stream(q.device)
     M, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
@@ -413,8 +446,7 @@ def bskv_plan_bsr_variable(block_mask_map, block_row_sz, block_col_sz, num_qo_he
 def bskv_run_bsr_variable(plan, q, k, v, out=None, lse=None, return_lse=False, sm_scale=None):
     """q [Hq, qo_len, D], k/v [Hkv, kv_len, D] -> out [Hq, qo_len, D] (and lse [Hq, qo_len])."""
     lib = load_library()
-    if plan.int_ws is None:
-        plan.upload(q.device)
+    plan.on_stream(q.device)
     Hq, L, D = q.shape
     if out is None:
         out = torch.empty_like(q)
@@ -455,8 +487,7 @@ def bskv_run_prefill_paged(plan, q, kv_cache, out=None, lse=None, return_lse=Fal
                            sm_scale=None):
     """q [total_qo, Hq, D]; kv_cache [pages, 2, Hkv, page_size, D] (any strides)."""
     lib = load_library()
-    if plan.int_ws is None:
-        plan.upload(q.device)
+    plan.on_stream(q.device)
     T, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
@@ -486,8 +517,7 @@ def bskv_run_mla_sparse(plan, query, kv_rows, indices, bmm1_scale, bmm2_scale=1.
                         lse=None, return_lse=False):
     """query [B, T, H, 576] uint8/e4m3; kv_rows [rows, 576] (or [pages, page_size, 576])."""
     lib = load_library()
-    if plan.int_ws is None:
-        plan.upload(query.device)
+    plan.on_stream(query.device)
     B, T, H, _ = query.shape
     rows = kv_rows.numel() // 576
     if out is None:
@@ -522,8 +552,7 @@ def bskv_run_mla_paged(plan, query, kv_pages, bmm1_scale, bmm2_scale=1.0, out=No
                        return_lse=False):
     """query [B, H, 576] uint8/e4m3; kv_pages [num_pages, page_size, 576] uint8/e4m3."""
     lib = load_library()
-    if plan.int_ws is None:
-        plan.upload(query.device)
+    plan.on_stream(query.device)
     B, H, _ = query.shape
     if out is None:
         out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=query.device)
@@ -679,10 +708,6 @@ def _strides_of(t, n):
     return arr
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
 def _call(fn, dev, *args):
     """The C entry point `fn` on the current stream of the tensors' device."""
     entry = getattr(_lib or load_library(), fn)
@@ -708,9 +733,11 @@ def _ready(fn, plan, device):
                 raise RuntimeError("%s: upload the plan before the capture: a graph would copy its "
                                    "host memory at every replay" % fn)
             plan.upload(device)
-    if plan.int_ws.device != device:
+    elif plan.int_ws.device != device:
         raise ValueError("%s: the plan was uploaded to %s, the tensors are on %s"
                          % (fn, plan.int_ws.device, device))
+    else:
+        plan.on_stream(device)
 
 
 _U8, _I32T, _F32T = (torch.uint8,), (torch.int32,), (torch.float32,)
