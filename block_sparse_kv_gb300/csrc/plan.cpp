@@ -16,6 +16,9 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
+#include <memory>
+#include <new>
 #include <queue>
 #include <utility>
 
@@ -595,6 +598,12 @@ bskv_status pages_once(const char* who, const char* name, const int32_t* indices
   return BSKV_ERR_INVALID_ARG;
 }
 
+// What a plan's own memory raised, as a status: no exception leaves a C entry point.
+bskv_status host_error(const char* who, const std::exception& e) {
+  set_error("%s: %s", who, dynamic_cast<const std::bad_alloc*>(&e) ? "out of host memory" : e.what());
+  return BSKV_ERR_UNSUPPORTED;
+}
+
 // Appends the walk records (kWalkWords) to an assembled plan whose units are (request, kv head).
 void add_walk_records(bskv_plan* p, const std::vector<int32_t>& worker_ptr, const std::vector<Chunk>& chunks,
                       const std::vector<int32_t>& merges, const int32_t* kv_indptr, int32_t units_per_request) {
@@ -648,7 +657,7 @@ extern "C" bskv_status bskv_plan_decode_fp4(const int32_t* kv_indptr, const int3
                                             int32_t num_pages, int32_t page_size,
                                             int32_t num_qo_heads, int32_t num_kv_heads,
                                             int32_t head_dim, int32_t dtype, int32_t num_sms,
-                                            int32_t max_workers, bskv_plan** out_plan) {
+                                            int32_t max_workers, bskv_plan** out_plan) try {
   const char* who = "plan_decode_fp4";
   if (!out_plan) { set_error("%s: out_plan is NULL", who); return BSKV_ERR_INVALID_ARG; }
   *out_plan = nullptr;
@@ -663,13 +672,12 @@ extern "C" bskv_status bskv_plan_decode_fp4(const int32_t* kv_indptr, const int3
   if (bskv_status s = page_table_lens(who, kv_indptr, kv_indices, kv_last_page_len, batch,
                                       num_pages, page_size, req))
     return s;
-  std::vector<int64_t> len(size_t(batch) * size_t(num_kv_heads));
   int64_t total = 0;
-  for (int32_t b = 0; b < batch; ++b) {
-    total += req[size_t(b)];
+  for (int64_t L : req) total += L;
+  if (total > INT32_MAX / num_kv_heads || int64_t(batch) * num_kv_heads > INT32_MAX / 4) { set_error("%s: too many tokens", who); return BSKV_ERR_UNSUPPORTED; }
+  std::vector<int64_t> len(size_t(batch) * size_t(num_kv_heads));
+  for (int32_t b = 0; b < batch; ++b)
     for (int32_t h = 0; h < num_kv_heads; ++h) len[size_t(b) * num_kv_heads + h] = req[size_t(b)];
-  }
-  if (total > INT32_MAX / num_kv_heads || len.size() > size_t(INT32_MAX / 4)) { set_error("%s: too many tokens", who); return BSKV_ERR_UNSUPPORTED; }
   int64_t tiles = 0;
   for (int64_t L : len) tiles += (L + kFp4Tile - 1) / kFp4Tile;
   const int64_t cap = std::min<int64_t>(int64_t(num_sms) * kFp4Warps * fp4_ctas_per_sm(fp4_column_tiles(group)),
@@ -681,7 +689,8 @@ extern "C" bskv_status bskv_plan_decode_fp4(const int32_t* kv_indptr, const int3
                         FillCosts{kFp4PublishTiles, kFp4MergeTiles, kFp4BoundaryTiles}, worker_ptr,
                         chunks, slots, merges);
   const int32_t P = int32_t(worker_ptr.size() - 1);
-  bskv_plan* p = new bskv_plan();
+  std::unique_ptr<bskv_plan> owner(new bskv_plan());
+  bskv_plan* p = owner.get();
   p->kind = KIND_DECODE_FP4;
   p->batch = batch; p->num_pages = num_pages; p->page_size = page_size;
   p->num_qo_heads = num_qo_heads; p->num_kv_heads = num_kv_heads; p->head_dim = head_dim;
@@ -694,9 +703,11 @@ extern "C" bskv_status bskv_plan_decode_fp4(const int32_t* kv_indptr, const int3
       : align256(size_t(slots) * group * head_dim * 4) + align256(size_t(slots) * group * 4);
   p->counter_words = merges.size() / 3;
   for (size_t i = 2; i < merges.size(); i += 3) p->max_merge_count = std::max(p->max_merge_count, merges[i]);
-  *out_plan = p;
+  *out_plan = owner.release();
   log_plan("bskv_plan_decode_fp4", p);
   return BSKV_OK;
+} catch (const std::exception& e) {
+  return host_error("plan_decode_fp4", e);
 }
 
 extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const int32_t* kv_indptr,
@@ -705,7 +716,7 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
                                               int32_t num_pages, int32_t page_size,
                                               int32_t num_qo_heads, int32_t num_kv_heads,
                                               int32_t head_dim, int32_t causal, int32_t dtype,
-                                              int32_t num_sms, bskv_plan** out_plan) {
+                                              int32_t num_sms, bskv_plan** out_plan) try {
   const char* who = "plan_attn_weights";
   if (!out_plan) { set_error("%s: out_plan is NULL", who); return BSKV_ERR_INVALID_ARG; }
   *out_plan = nullptr;
@@ -755,7 +766,8 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
     for (int32_t b = 0; b < batch; ++b) items += (req[size_t(b)] + kWeightsKeys - 1) / kWeightsKeys * num_kv_heads;
     grid = units = int32_t(items);  // at most the tokens times the heads
   }
-  bskv_plan* p = new bskv_plan();
+  std::unique_ptr<bskv_plan> owner(new bskv_plan());
+  bskv_plan* p = owner.get();
   p->kind = KIND_WEIGHTS;
   p->num_sms = num_sms;
   p->batch = batch; p->num_pages = num_pages; p->page_size = page_size;
@@ -782,9 +794,11 @@ extern "C" bskv_status bskv_plan_attn_weights(const int32_t* qo_indptr, const in
     p->meta[H_MERGES] = records;
     p->meta[H_TOTAL] = int32_t(p->meta.size());
   }
-  *out_plan = p;
+  *out_plan = owner.release();
   log_plan("bskv_plan_attn_weights", p);
   return BSKV_OK;
+} catch (const std::exception& e) {
+  return host_error("plan_attn_weights", e);
 }
 
 extern "C" bskv_status bskv_plan_evict(const int32_t* kv_indptr, const int32_t* kv_indices,
@@ -792,7 +806,7 @@ extern "C" bskv_status bskv_plan_evict(const int32_t* kv_indptr, const int32_t* 
                                        int32_t sink, int32_t recent, const int32_t* dst_indptr,
                                        const int32_t* dst_indices, int32_t batch,
                                        int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
-                                       int32_t head_dim, int32_t num_sms, bskv_plan** out_plan) {
+                                       int32_t head_dim, int32_t num_sms, bskv_plan** out_plan) try {
   const char* who = "plan_evict";
   if (!out_plan) { set_error("%s: out_plan is NULL", who); return BSKV_ERR_INVALID_ARG; }
   *out_plan = nullptr;
@@ -846,7 +860,8 @@ extern "C" bskv_status bskv_plan_evict(const int32_t* kv_indptr, const int32_t* 
     most = std::max(most, K);
     if (total > INT32_MAX / num_kv_heads) { set_error("%s: too many tokens", who); return BSKV_ERR_UNSUPPORTED; }
   }
-  bskv_plan* p = new bskv_plan();
+  std::unique_ptr<bskv_plan> owner(new bskv_plan());
+  bskv_plan* p = owner.get();
   p->kind = KIND_EVICT;
   p->batch = batch; p->num_pages = num_pages; p->page_size = page_size;
   p->num_qo_heads = num_kv_heads; p->num_kv_heads = num_kv_heads; p->head_dim = head_dim;
@@ -858,9 +873,11 @@ extern "C" bskv_status bskv_plan_evict(const int32_t* kv_indptr, const int32_t* 
   assemble(p, KIND_EVICT, batch, dst, reqs, 0, none, 0, kv_indptr,
            batch > 0 ? size_t(batch) + 1 : 0, kv_indices, size_t(nnz), batch, 0);
   p->meta[H_WORKERS] = 0;  // the first section holds the destination pages
-  *out_plan = p;
+  *out_plan = owner.release();
   log_plan("bskv_plan_evict", p);
   return BSKV_OK;
+} catch (const std::exception& e) {
+  return host_error("plan_evict", e);
 }
 
 namespace {

@@ -241,3 +241,40 @@ def test_entry_points_refuse_null_and_unaligned(lib):
     for bad in (dict(k=None), dict(k=24), dict(codes=8), dict(scales=None), dict(dim=96), dict(ps=12), dict(nnz=-1),
                 dict(heads=0), dict(heads=129), dict(dt=77), dict(pages=-1), dict(batch=-1)):
         assert append(**bad) in (1, 2), bad
+
+
+_HUGE = """
+import resource, sys
+import torch
+import block_sparse_kv_gb300 as bskv
+bskv.load_library()
+pages = int(open("/proc/self/statm").read().split()[0])
+limit = pages * resource.getpagesize() + (1 << 30)
+resource.setrlimit(resource.RLIMIT_AS, (limit, limit))
+z = torch.zeros(65, dtype=torch.int32)
+for heads, message in ((1 << 30, "too many tokens"), (1 << 22, "out of host memory")):
+    try:
+        bskv.bskv_plan_decode_fp4(z, [], z, 0, 16, heads, heads, 128, num_sms=152)
+    except bskv.BskvError as e:
+        assert e.status == "ERR_UNSUPPORTED" and message in str(e), e
+    else:
+        raise AssertionError(heads)
+t = torch.zeros(5001, dtype=torch.int32)
+try:
+    bskv.bskv_plan_attn_weights(None, t, [], t, 0, 16, 65535, 65535, 128, num_sms=152)
+except bskv.BskvError as e:
+    assert e.status == "ERR_UNSUPPORTED" and "out of host memory" in str(e), e
+else:
+    raise AssertionError("made")
+assert bskv.bskv_plan_decode_fp4(z[:2], [], z[:1], 0, 16, 8, 8, 128, num_sms=152) is not None
+"""
+
+
+def test_plans_past_the_host_memory_are_refused(lib):
+    """A child process with a gigabyte to spare: statuses, no exception out of a C entry point."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _HUGE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
