@@ -813,7 +813,7 @@ bskv_status launch_stream(const bskv_plan* plan, WeightsParams& wp, cudaStream_t
   if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "attn_weights: cudaFuncSetAttribute")) return s;
   // Plans have up to 16 workers per SM. Where fewer warps fit, a warp takes two workers' chunks in a row
   // (64 requests of 512 to 4096 tokens at 8 warps per SM: 53.0 us where two waves of CTAs took 54.1).
-  wp.take = wp.num_workers > plan->num_sms * kWarps * weights_ctas_per_sm(D, FP4) ? 2 : 1;
+  wp.take = wp.num_workers > int64_t(plan->num_sms) * kWarps * weights_ctas_per_sm(D, FP4) ? 2 : 1;
   const int warps = (wp.num_workers + wp.take - 1) / wp.take;
   kern<<<(warps + kWarps - 1) / kWarps, kWarps * 32, smem, st>>>(wp);
   return cuda_check(cudaGetLastError(), "attn_weights launch");
@@ -845,7 +845,7 @@ bskv_status launch_tile(const bskv_plan* plan, WeightsParams& wp, cudaStream_t s
   wp.num_requests = meta_word(plan, H_MERGES);
   wp.num_items = meta_word(plan, H_UNITS);
   wp.queries = FastDiv(wp.tile_queries);
-  const int grid = std::min(wp.num_items, plan->num_sms * per_sm);
+  const int grid = int(std::min<int64_t>(wp.num_items, int64_t(plan->num_sms) * per_sm));
   kern<<<grid, tile_threads(FP4), smem, st>>>(qmap, kmap, wp);
   return cuda_check(cudaGetLastError(), "attn_weights launch");
 }

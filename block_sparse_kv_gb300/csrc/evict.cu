@@ -473,7 +473,7 @@ bskv_status run(const char* who, const bskv_plan* plan, float* scores, const int
   if (bskv_status s = big ? select<1024>(e, plan, ctas, smem, st) : select<256>(e, plan, ctas, smem, st)) return s;
   e.planes = planes;
   ctas = 1;
-  while (plan->in_place && ctas < kMaxCluster && plan->most / (2 * ctas) >= kMoveShare && rows * planes * ctas <= 4 * plan->num_sms)
+  while (plan->in_place && ctas < kMaxCluster && plan->most / (2 * ctas) >= kMoveShare && rows * planes * ctas <= int64_t(4) * plan->num_sms)
     ctas *= 2;
   const int parts = plan->in_place ? ctas : (plan->most + kMoveBlock - 1) / kMoveBlock;
   const dim3 grid(unsigned(planes * parts), unsigned(plan->num_kv_heads), unsigned(plan->batch));

@@ -244,3 +244,8 @@ def test_weights_stream_of_many_tiles(cuda, four, Hq, Hkv, D, ps, nq, dtype, cau
 def test_weights_tile_of_many_items(cuda, four, Hq, Hkv, D, ps, nq, dtype, causal, decay):
     """Two CTAs, or four, for everything: both key buffers, queries that change, every parity."""
     _many(cuda, [1000, 150, 1, 2049, 260], Hq, Hkv, D, ps, nq, dtype, causal, decay, four, (1, 2, None))
+
+
+@pytest.mark.parametrize("nq", [1, 30])
+def test_weights_of_any_number_of_sms(cuda, nq):
+    _many(cuda, [300, 41], 8, 2, 128, 16, [nq, nq], torch.bfloat16, True, 0.5, False, (None, 2 ** 30, 2 ** 31 - 1))
