@@ -170,6 +170,14 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _capturing(device):
+    """Whether the device's current stream is being captured."""
+    if torch.cuda.current_device() == device.index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _num_sms(device=None):
     if torch.cuda.is_available():
         d = torch.cuda.current_device() if device is None else torch.device(device).index or 0
@@ -236,16 +244,16 @@ class Plan:
             int_ws = torch.empty(max(ib, 16), dtype=torch.uint8, device=device)
         if float_ws is None and fb > 0:
             float_ws = torch.empty(fb, dtype=torch.uint8, device=device)
-        _check("bskv_plan_upload", lib.bskv_plan_upload(self._h, int_ws.data_ptr(),
-                                                        int_ws.numel(), _stream(int_ws)))
+        stream = torch.cuda.current_stream(int_ws.device)
+        _check("bskv_plan_upload", lib.bskv_plan_upload(self._h, int_ws.data_ptr(), int_ws.numel(),
+                                                        ctypes.c_void_p(stream.cuda_stream)))
         self.int_ws = int_ws
         self.float_ws = float_ws
-        self._streams = set()
-        self._uploaded = None
-        with torch.cuda.device(int_ws.device):
-            if not torch.cuda.is_current_stream_capturing():
-                self._uploaded = torch.cuda.current_stream().record_event()
-                self._streams.add(_raw_stream(int_ws.device.index))
+        self._streams, self._uploaded = set(), None
+        if not _capturing(int_ws.device):
+            self._uploaded = torch.cuda.Event()
+            self._uploaded.record(stream)
+            self._streams.add(stream.cuda_stream)
         return self
 
     def on_stream(self, device):
@@ -254,15 +262,14 @@ class Plan:
         if self.int_ws is None:
             self.upload(device)
         elif _raw_stream(device.index) not in self._streams:
-            with torch.cuda.device(device):
-                if self._uploaded is None or torch.cuda.is_current_stream_capturing():
-                    return
-                stream = torch.cuda.current_stream()
-                stream.wait_event(self._uploaded)
-                for ws in (self.int_ws, self.float_ws):
-                    if ws is not None:
-                        ws.record_stream(stream)
-                self._streams.add(stream.cuda_stream)
+            if self._uploaded is None or _capturing(device):
+                return
+            stream = torch.cuda.current_stream(device)
+            stream.wait_event(self._uploaded)
+            for ws in (self.int_ws, self.float_ws):
+                if ws is not None:
+                    ws.record_stream(stream)
+            self._streams.add(stream.cuda_stream)
 
 
 def bskv_plan_decode(kv_indptr, kv_indices, kv_last_page_len, num_pages, page_size,
@@ -728,10 +735,10 @@ def _check_plan(fn, plan, kind):
 def _ready(fn, plan, device):
     """The plan's workspaces on this device, uploaded at the first run."""
     if plan.int_ws is None:
+        if _capturing(device):
+            raise RuntimeError("%s: upload the plan before the capture: a graph would copy its "
+                               "host memory at every replay" % fn)
         with torch.cuda.device(device):
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("%s: upload the plan before the capture: a graph would copy its "
-                                   "host memory at every replay" % fn)
             plan.upload(device)
     elif plan.int_ws.device != device:
         raise ValueError("%s: the plan was uploaded to %s, the tensors are on %s"
