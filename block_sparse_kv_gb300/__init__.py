@@ -834,7 +834,7 @@ def _check_append(fn, _, k, v, batch_indices, positions, kv_indptr, kv_indices, 
 def bskv_dequantize_fp4_paged(kv_codes, kv_scales, batch_indices, positions, kv_indptr, kv_indices,
                               dtype=torch.bfloat16, k_out=None, v_out=None):
     """Rows of a 4-bit paged cache as values: (k, v) [nnz, Hkv, D] of `dtype` (bf16, fp16 or
-    fp32), row i being token positions[i] of request batch_indices[i]. Rows whose token is out of
+    fp32; that of k_out and v_out where they are given), row i being token positions[i] of request batch_indices[i]. Rows whose token is out of
     range are left as they were (unspecified in outputs that are made here)."""
     fn = "bskv_dequantize_fp4_paged"
     if (k_out is None) != (v_out is None):

@@ -117,7 +117,8 @@ inline int32_t decode_group_heads(int32_t num_kv_heads, int32_t page_size) {
 
 // 4-bit decode: one worker per warp, kFp4Warps to a CTA. The variant by query heads per kv head (0:
 // up to 4, 1: up to 8, 2: up to 16) decides how many CTAs an SM holds: by registers 3, 3 and 2.
-// Measured on 64 requests of 512 to 4096 tokens with 4 query heads on each of 8 kv heads ("batch"),
+// Measured, each pair side by side (the loop has become 1 to 3 % longer since: decode_fp4.cu), on 64
+// requests of 512 to 4096 tokens with 4 query heads on each of 8 kv heads ("batch"),
 // 8 of 131072 with 8 ("long"), one request of 700 tokens, and 37 of up to 999 ("ragged"):
 //   * variant 0 for 4 heads 39.4 us, variant 1 44.1 (batch); variant 1 for 8 heads 233 us, variant 2
 //     315 (long);
@@ -214,7 +215,7 @@ struct bskv_plan {
   int32_t walk_records = -1;  // word offset of the walk records (tile records), or -1
   int32_t num_sms = 0;        // attn_weights, evict: SM count of the target GPU
   // evict: tokens that stay over all requests, protected first / last tokens, the longest
-  // request, whether the kept rows stay in their pages, CTAs that share the rows of one slice
+  // request, the most tokens that one keeps, whether the kept rows stay in their pages
   int64_t kept_total = 0;
   int32_t sink = 0, recent = 0, longest = 0, most = 0, in_place = 0;
   // set by bskv_plan_upload

@@ -383,7 +383,8 @@ bskv_status bskv_run_decode_noalloc(const bskv_plan* plan, const void* q,
  * up to about 2^90 in size are safe), and values within 2^120.
  *   q, out  [batch, num_qo_heads, head_dim] in the plan dtype, strides {batch, head} in
  *           multiples of 8 elements; lse [batch, num_qo_heads] float32 contiguous, or NULL.
- *   float_ws as for bskv_run_decode. Slots past a request's last token are not read.
+ *   float_ws as for bskv_run_decode. What slots past a request's last token hold does not matter
+ *   (copies of whole groups of 8 slots may read them).
  * Runs of one plan share its workspaces and must not overlap on the GPU.
  */
 bskv_status bskv_run_decode_fp4(const bskv_plan* plan, const void* q, const int64_t* q_strides,
