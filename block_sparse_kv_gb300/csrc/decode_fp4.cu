@@ -197,22 +197,26 @@ __device__ __forceinline__ float unit_growth(float ref, const Need& n, int unit)
   return x > 40.f ? ceilf(x) : 0.f;
 }
 // The reference 2^10 below the largest product, relative to the unit, and at most 2^94 below the largest
-// weight; it never falls. Returns what sums so far shrink by.
-__device__ __forceinline__ float raise_ref(float& ref, const Need& n, int unit) {
-  const float to = fmaxf(ref, fmaxf(n.product - 10.f - unit, n.top - 94.f));
+// weight. It falls only with the unit, by which all heads' products have become smaller, and no further
+// than leaves the weights so far, whose sum in the lane is l, below 2^94. Returns what that sum shrinks by
+// (or grows).
+__device__ __forceinline__ float move_ref(float& ref, const Need& n, int unit, int grown, float l) {
+  float least = ref;
+  if (grown > 0) least = fminf(ref, fmaxf(ref - grown, ref + float(exponent_of(max_over_rows(l)) + 1 - 94)));
+  const float to = fmaxf(least, fmaxf(n.product - 10.f - unit, n.top - 94.f));
   const float shrink = fast_exp2(ref - to);
   ref = to;
   return shrink;
 }
-// The warp's unit grows by the most that a lane asks for; returns the factor for values summed so far.
-__device__ __forceinline__ float grow_unit(int& unit, float growth) {
+// The warp's unit grows by the most that a lane asks for; returns by how much.
+__device__ __forceinline__ int grow_unit(int& unit, float growth) {
   const int by = __reduce_max_sync(0xffffffffu, int(growth));
   unit = max(unit, 0) + by;
-  return pow2(-by);
+  return by;
 }
 
 template <int D, int NT, int N>
-__device__ __forceinline__ void raise_refs(State<D, NT>& s, const float (&x)[NT][2][N], const float (&f)[N]) {
+__device__ __forceinline__ void move_refs(State<D, NT>& s, const float (&x)[NT][2][N], const float (&f)[N]) {
   Need need[2 * NT];
   float growth = 0.f;
 #pragma unroll
@@ -223,17 +227,17 @@ __device__ __forceinline__ void raise_refs(State<D, NT>& s, const float (&x)[NT]
     need[j] = need_of(v, f);
     growth = fmaxf(growth, unit_growth(s.ref[j], need[j], s.unit));
   }
-  const float less = grow_unit(s.unit, growth);
+  const int grown = grow_unit(s.unit, growth);
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
-    const float shrink = raise_ref(s.ref[j], need[j], s.unit);
+    const float shrink = move_ref(s.ref[j], need[j], s.unit, grown, s.l[j]), shrink_o = shrink * pow2(-grown);
     s.l[j] *= shrink;
 #pragma unroll
     for (int blk = 0; blk < Shape<D>::kBlocks; ++blk)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        s.o[j >> 1][blk][i][j & 1] *= shrink * less;
-        s.o[j >> 1][blk][i][(j & 1) + 2] *= shrink * less;
+        s.o[j >> 1][blk][i][j & 1] *= shrink_o;
+        s.o[j >> 1][blk][i][(j & 1) + 2] *= shrink_o;
       }
   }
 }
@@ -359,7 +363,7 @@ __device__ __forceinline__ void some_tokens(const uint8_t* st, int first, int va
   if (__any_sync(0xffffffffu, over || s.unit != 0)) {
     float f[N];
     scale_exponents<D>(st, r0, kx, sv, f);
-    raise_refs<D, NT>(s, x, f);
+    move_refs<D, NT>(s, x, f);
     to_unit(s.unit, sv);
     weigh();
   }
@@ -459,13 +463,13 @@ __device__ __forceinline__ void some_tokens4(const uint8_t* st, int first, int v
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = x[i] * s.c;
     const Need need = need_of(v, f);
-    const float less = grow_unit(s.unit, unit_growth(s.ref, need, s.unit));
-    const float shrink = raise_ref(s.ref, need, s.unit);
+    const int grown = grow_unit(s.unit, unit_growth(s.ref, need, s.unit));
+    const float shrink = move_ref(s.ref, need, s.unit, grown, s.l), shrink_o = shrink * pow2(-grown);
     s.l *= shrink;
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s.o[blk][i] *= shrink * less;
+      for (int i = 0; i < 4; ++i) s.o[blk][i] *= shrink_o;
     to_unit(s.unit, sv);
     weigh();
   }

@@ -377,8 +377,8 @@ bskv_status bskv_run_decode_noalloc(const bskv_plan* plan, const void* q,
  * Batch decode over a 4-bit paged cache, for a plan of bskv_plan_decode_fp4: what
  * bskv_run_decode computes, with K and V the values of the cache. A softmax weight times a value's
  * scale is rounded to 16 bits: half a step of 2^-11, or 2^-35 of the largest such product of its head,
- * or 2^-119 of the head's largest weight where one of these is more (the last times 2^-50 of the kv
- * head's largest scale, if that is above 1). A key's scale code 255 makes its kv head's outputs and
+ * or 2^-119 of the head's largest weight where one of these is more (the last times 2^-10 of the kv
+ * head's largest scale, if that is above 2^50). A key's scale code 255 makes its kv head's outputs and
  * lse NaN, a value's makes those 32 output values NaN. Logits have to stay within fp32's range (keys
  * up to about 2^90 in size are safe), and values within 2^120.
  *   q, out  [batch, num_qo_heads, head_dim] in the plan dtype, strides {batch, head} in

@@ -177,6 +177,18 @@ def test_values_to_the_ends_of_the_range(cuda, lo, hi, Hq, D, workers):
            q[:len(rows)], D ** -0.5, workers)
 
 
+@pytest.mark.parametrize("workers", [1, 3])
+@pytest.mark.parametrize("Hq, D", [(4, 128), (8, 64), (16, 128)])
+def test_large_values_that_only_some_heads_see(cuda, Hq, D, workers):
+    """Tokens of values around 2^110 that weigh 2^-184 for most heads, 2^-369 and 2^-92 for one each: only
+    the last one's result is theirs, the others' tokens before and after keep their 16 bits."""
+    L = 700
+    kc, ks = _keys([128.0] * 32 + [0.0] * 32 + [128.0] * (L - 64), 1, D)
+    vc, vs = _values(24, 1, L, D)
+    vs[:, 32:64] = 237
+    _check(cuda, [L], [np.stack([kc, vc])], [np.stack([ks, vs])], _ones(1, Hq, 1, D, torch.bfloat16), 1.0, workers)
+
+
 @pytest.mark.parametrize("Hq", [4, 8])
 def test_a_scale_that_leaves_no_logits(cuda, Hq):
     """bf16 queries of zeros or near the type's smallest under a tiny sm_scale: every token weighs the
