@@ -198,15 +198,15 @@ __device__ __forceinline__ float unit_growth(float ref, const Need& n, int unit)
 }
 // The reference 2^10 below the largest product, relative to the unit, and at most 2^94 below the largest
 // weight. It falls only with the unit, by which all heads' products have become smaller, and no further
-// than leaves the weights so far, whose sum in the lane is l, below 2^94. Returns what that sum shrinks by
-// (or grows).
+// than leaves the weights so far, whose sum in the lane is l, below 2^94. Returns the square root of what
+// that sum shrinks by, or grows: a factor of up to 2^-134 matters, to weights of 2^94.
 __device__ __forceinline__ float move_ref(float& ref, const Need& n, int unit, int grown, float l) {
   float least = ref;
   if (grown > 0) least = fminf(ref, fmaxf(ref - grown, ref + float(exponent_of(max_over_rows(l)) + 1 - 94)));
   const float to = fmaxf(least, fmaxf(n.product - 10.f - unit, n.top - 94.f));
-  const float shrink = fast_exp2(ref - to);
+  const float root = fast_exp2(0.5f * (ref - to));
   ref = to;
-  return shrink;
+  return root;
 }
 // The warp's unit grows by the most that a lane asks for; returns by how much.
 __device__ __forceinline__ int grow_unit(int& unit, float growth) {
@@ -230,14 +230,16 @@ __device__ __forceinline__ void move_refs(State<D, NT>& s, const float (&x)[NT][
   const int grown = grow_unit(s.unit, growth);
 #pragma unroll
   for (int j = 0; j < 2 * NT; ++j) {
-    const float shrink = move_ref(s.ref[j], need[j], s.unit, grown, s.l[j]), shrink_o = shrink * pow2(-grown);
-    s.l[j] *= shrink;
+    const float root = move_ref(s.ref[j], need[j], s.unit, grown, s.l[j]), root_o = root * pow2(-grown);
+    s.l[j] = s.l[j] * root * root;
 #pragma unroll
     for (int blk = 0; blk < Shape<D>::kBlocks; ++blk)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        s.o[j >> 1][blk][i][j & 1] *= shrink_o;
-        s.o[j >> 1][blk][i][(j & 1) + 2] *= shrink_o;
+        float& a = s.o[j >> 1][blk][i][j & 1];
+        float& b = s.o[j >> 1][blk][i][(j & 1) + 2];
+        a = a * root * root_o;
+        b = b * root * root_o;
       }
   }
 }
@@ -464,12 +466,12 @@ __device__ __forceinline__ void some_tokens4(const uint8_t* st, int first, int v
     for (int i = 0; i < N; ++i) v[i] = x[i] * s.c;
     const Need need = need_of(v, f);
     const int grown = grow_unit(s.unit, unit_growth(s.ref, need, s.unit));
-    const float shrink = move_ref(s.ref, need, s.unit, grown, s.l), shrink_o = shrink * pow2(-grown);
-    s.l *= shrink;
+    const float root = move_ref(s.ref, need, s.unit, grown, s.l), root_o = root * pow2(-grown);
+    s.l = s.l * root * root;
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s.o[blk][i] *= shrink_o;
+      for (int i = 0; i < 4; ++i) s.o[blk][i] = s.o[blk][i] * root * root_o;
     to_unit(s.unit, sv);
     weigh();
   }

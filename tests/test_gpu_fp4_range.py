@@ -177,6 +177,21 @@ def test_values_to_the_ends_of_the_range(cuda, lo, hi, Hq, D, workers):
            q[:len(rows)], D ** -0.5, workers)
 
 
+@pytest.mark.parametrize("workers", [1, 4])
+@pytest.mark.parametrize("Hq, D", [(4, 128), (8, 64), (16, 128)])
+@pytest.mark.parametrize("scale", [160, 170, 200])
+def test_large_values_behind_zeros(cuda, scale, Hq, D, workers):
+    """Tokens of zeros, then as many of large values with the same logits: both count in the sum."""
+    L = 320
+    kc, ks = _keys([4.0] * L, 1, D)
+    vc, vs = _values(25, 1, L, D)
+    vs[:] = scale
+    for zeros in (slice(0, 160), slice(32, 200), slice(100, 320)):
+        c, s = vc.copy(), vs.copy()
+        c[:, zeros], s[:, zeros] = 0, 0
+        _check(cuda, [L], [np.stack([kc, c])], [np.stack([ks, s])], _ones(1, Hq, 1, D, torch.bfloat16), 1.0, workers)
+
+
 @pytest.mark.parametrize("workers", [1, 3])
 @pytest.mark.parametrize("Hq, D", [(4, 128), (8, 64), (16, 128)])
 def test_large_values_that_only_some_heads_see(cuda, Hq, D, workers):
