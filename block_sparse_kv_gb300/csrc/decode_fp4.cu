@@ -29,9 +29,9 @@
 // What bounds it: the cache is read once, 136 bytes per token and kv head of 128 dims against
 // 512 in 16 bits, so instructions issued per byte are what to save: converting and pairing 4-bit
 // values keeps the ALU pipe busy for half to two thirds of the time. 64 requests of 512 to 4096
-// tokens with 4 query heads per kv head take 39.9 us (4.0 TB/s), 8 of 131072 with 8 heads 239 us (4.8
-// TB/s; with 16 heads 76 and 323 us). Blocks of zeros and the unit in the way of setting a reference cost
-// 0.6 and 6 us of these. Without them 39.4 and 233 us were measured for what the loop is made of: a warp
+// tokens with 4 query heads per kv head take 40.6 us (4.0 TB/s), 8 of 131072 with 8 heads 238 us (4.8
+// TB/s; with 16 heads 78 and 330 us). Blocks of zeros and the unit in the way of setting a reference cost
+// 1.2 and 5 us of these. Without them 39.4 and 233 us were measured for what the loop is made of: a warp
 // works on 32 tokens at a time, the second 16's products fill the first's waits (41.2 and 239 us with
 // 16), and two stages are enough of a ring (three: 41.9 and 243 us).
 // Each warp is a worker of its own over a range of one or more (request, kv

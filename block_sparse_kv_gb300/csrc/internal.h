@@ -117,7 +117,7 @@ inline int32_t decode_group_heads(int32_t num_kv_heads, int32_t page_size) {
 
 // 4-bit decode: one worker per warp, kFp4Warps to a CTA. The variant by query heads per kv head (0:
 // up to 4, 1: up to 8, 2: up to 16) decides how many CTAs an SM holds: by registers 3, 3 and 2.
-// Measured, each pair side by side (the loop has become 1 to 3 % longer since: decode_fp4.cu), on 64
+// Measured, each pair side by side (the loop has become 2 to 4 % longer since: decode_fp4.cu), on 64
 // requests of 512 to 4096 tokens with 4 query heads on each of 8 kv heads ("batch"),
 // 8 of 131072 with 8 ("long"), one request of 700 tokens, and 37 of up to 999 ("ragged"):
 //   * variant 0 for 4 heads 39.4 us, variant 1 44.1 (batch); variant 1 for 8 heads 233 us, variant 2
