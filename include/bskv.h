@@ -382,7 +382,9 @@ bskv_status bskv_run_decode_noalloc(const bskv_plan* plan, const void* q,
  * lse NaN, a value's makes those 32 output values NaN. Logits have to stay within fp32's range (keys
  * up to about 2^90 in size are safe), and values within 2^120.
  *   q, out  [batch, num_qo_heads, head_dim] in the plan dtype, strides {batch, head} in
- *           multiples of 8 elements; lse [batch, num_qo_heads] float32 contiguous, or NULL.
+ *           multiples of 8 elements; lse [batch, num_qo_heads] float32 contiguous, or NULL; sums are
+ *           kept relative to the products, so value scales of 2^64 or 2^-64 and beyond leave it an
+ *           error of up to 1e-5.
  *   float_ws as for bskv_run_decode. What slots past a request's last token hold does not matter
  *   (copies of whole groups of 8 slots may read them).
  * Runs of one plan share its workspaces and must not overlap on the GPU.
