@@ -340,7 +340,7 @@ def _own_select(s, t):
 def _own_attend(s, t):
     import block_sparse_kv_gb300 as bskv
     out, lse = bskv.bskv_run_decode_blocks(s["plan"], s["q"], s["kv"], s["blocks"], t["batch_indices"], t["positions"],
-                                           t["kv_indptr"], t["kv_indices"], out=s["out"], lse=s["lse"])
+                                           t["kv_indptr"], t["kv_indices"], out=s["out"], lse=s["lse"], return_lse=True)
     return {"out": out, "lse": lse}
 
 
