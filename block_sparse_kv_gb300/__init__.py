@@ -25,6 +25,8 @@ __all__ = [
     "bskv_quantize_fp4_append_paged", "bskv_dequantize_fp4_paged",
     "bskv_plan_attn_weights", "bskv_run_attn_weights", "bskv_run_attn_weights_fp4",
     "bskv_plan_evict", "bskv_run_evict", "bskv_run_evict_fp4",
+    "PageTable", "bskv_build_page_table", "bskv_norm_rope_append_paged", "bskv_block_bounds_paged",
+    "bskv_plan_decode_blocks", "bskv_run_select_blocks", "bskv_run_decode_blocks",
     "bskv_rope_quantize_fp8", "bskv_merge_states",
     "bskv_get_device_status", "bskv_set_debug_force_timeout",
 ]
@@ -111,6 +113,18 @@ _SIGS = {
                          _I32, _I32, _I32, ctypes.POINTER(_P)], _I32),
     "bskv_run_evict": ([_P, _P, _I64P, _I32, _P, _I64P, _P, _P], _I32),
     "bskv_run_evict_fp4": ([_P, _P, _I64P, _I32, _P, _I64P, _P, _I64P, _P, _P], _I32),
+    "bskv_build_page_table": ([_P, _P, _I32, _I32, _P, _I64, _I32, _I32, _P, _I32, _P, _P, _P, _P, _I64,
+                               _P, _P, _P, _P, _P, _I64, _P], _I32),
+    "bskv_norm_rope_append_paged": ([_P, _I64P, _P, _I64P, _P, _I64P, _I32, _I64, _I32, _I32, _I32, _P,
+                                     _P, _F, _P, _I32, _I64, _I32, _I32, _P, _P, _P, _P, _P, _I32, _I32,
+                                     _I64, _P, _I64P, _P, _I64P, _P], _I32),
+    "bskv_block_bounds_paged": ([_P, _I64P, _I32, _I32, _I32, _I32, _I64, _P, _P, _I64, _P, _P, _P,
+                                 _I32, _P, _I64P, _P], _I32),
+    "bskv_plan_decode_blocks": ([_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                 ctypes.POINTER(_P)], _I32),
+    "bskv_run_select_blocks": ([_P, _P, _I64P, _P, _I64P, _P, _P, _P, _P, _I32, _P, _P, _SZ, _P], _I32),
+    "bskv_run_decode_blocks": ([_P, _P, _I64P, _P, _I64P, _P, _P, _P, _P, _P, _I32, _P, _I64P, _P, _F,
+                                _P, _SZ, _P], _I32),
     "bskv_merge_states": ([_P, _P, _I64, _I32, _I32, _I32, _P, _I32, _P, _P], _I32),
     "bskv_get_device_status": ([_I32P, _I32], _I32),
     "bskv_set_debug_force_timeout": ([_I32], _I32),
@@ -1102,6 +1116,318 @@ def bskv_run_evict_fp4(plan, scores, kv_codes, kv_scales, kept=None, compact_sco
     _call(fn, dev, plan.handle, scores.data_ptr(), where, int(bool(compact_scores)),
           kv_codes.data_ptr(), cache[0], kv_scales.data_ptr(), cache[1], kept.data_ptr())
     return kept
+
+
+class PageTable:
+    """The index arrays of a batch as bskv_build_page_table writes them: kv_indptr and qo_indptr [B + 1],
+    kv_indices, kv_last_page_len [B] and, per new token, batch_indices, positions (int32) and slots
+    (int64); free_left [1] where pages were handed out of a free list, else None."""
+
+    __slots__ = ("kv_indptr", "kv_indices", "kv_last_page_len", "qo_indptr", "batch_indices", "positions",
+                 "slots", "free_left")
+
+    def __init__(self, kv_indptr, kv_indices, kv_last_page_len, qo_indptr, batch_indices, positions, slots,
+                 free_left=None):
+        self.kv_indptr, self.kv_indices, self.kv_last_page_len = kv_indptr, kv_indices, kv_last_page_len
+        self.qo_indptr, self.batch_indices, self.positions = qo_indptr, batch_indices, positions
+        self.slots, self.free_left = slots, free_left
+
+
+_I64T = (torch.int64,)
+
+
+def _list_of(fn, name, t, n, device, dtypes=_I32T):
+    _want(fn, name, t, (n,), dtypes, device)
+    _dense(fn, (name, t))
+
+
+def _check_page_table(fn, _, seq_lens, block_table, new_lens, free_pages, free_count, kv_indptr,
+                      kv_indices, kv_last_page_len, qo_indptr, batch_indices, positions, slots, free_left):
+    dev = _cuda_of(fn, "seq_lens", seq_lens)
+    _list_of(fn, "seq_lens", seq_lens, None, dev)
+    batch = seq_lens.numel()
+    _want(fn, "block_table", block_table, (batch, None), _I32T, dev)
+    _rows_last(fn, "block_table", block_table, written=free_pages is not None)
+    if new_lens is not None:
+        _list_of(fn, "new_lens", new_lens, batch, dev)
+    if (free_pages is None) != (free_count is None):
+        raise ValueError("%s: give free_pages and free_count, or neither" % fn)
+    if free_pages is not None:
+        _list_of(fn, "free_pages", free_pages, None, dev)
+        _list_of(fn, "free_count", free_count, 1, dev)
+        if kv_indptr is not None:
+            _list_of(fn, "out.free_left", free_left, 1, dev)
+    if kv_indptr is not None:
+        most = batch * block_table.shape[1]
+        for name, t, n in (("kv_indptr", kv_indptr, batch + 1), ("kv_indices", kv_indices, None),
+                           ("kv_last_page_len", kv_last_page_len, batch), ("qo_indptr", qo_indptr, batch + 1),
+                           ("batch_indices", batch_indices, None)):
+            _list_of(fn, "out." + name, t, n, dev)
+        if kv_indices.numel() < most:
+            raise ValueError("%s: out.kv_indices has %d entries, %d requests may have %d pages"
+                             % (fn, kv_indices.numel(), batch, most))
+        _list_of(fn, "out.positions", positions, batch_indices.numel(), dev)
+        if slots is not None:
+            _list_of(fn, "out.slots", slots, batch_indices.numel(), dev, _I64T)
+    return dev, batch, block_table.shape[1], _strides_of(block_table, 1)[0]
+
+
+def bskv_build_page_table(seq_lens, block_table, page_size, num_pages, new_lens=None, free_pages=None,
+                          free_count=None, max_tokens=None, out=None):
+    """Page table and token map of a batch from its requests' lengths, all int32 on the GPU: seq_lens [B] with
+    the new tokens included, new_lens [B] (None: one each), block_table [B, max_pages]. With free_pages and
+    free_count [1], pages that new tokens need come from the end of the free list and are written into
+    block_table. The PageTable has room for max_tokens new tokens (None: B, and new_lens must be None);
+    rows without one are -1. `out` is an earlier PageTable to write into (its room is what counts then)."""
+    fn = "bskv_build_page_table"
+    o = out
+    if o is not None and not isinstance(o, PageTable):
+        raise TypeError("%s: out must be a PageTable" % fn)
+    arrays = (None,) * 8 if o is None else (o.kv_indptr, o.kv_indices, o.kv_last_page_len, o.qo_indptr,
+                                            o.batch_indices, o.positions, o.slots, o.free_left)
+    dev, batch, max_pages, stride = _once(_call_layouts, _check_page_table, fn, None, seq_lens, block_table,
+                                          new_lens, free_pages, free_count, *arrays)
+    if o is None:
+        if max_tokens is None:
+            if new_lens is not None:
+                raise ValueError("%s: new_lens need max_tokens (or out)" % fn)
+            max_tokens = batch
+        if int(max_tokens) < 0:
+            raise ValueError("%s: max_tokens is %d" % (fn, max_tokens))
+
+        def ints(n, dtype=torch.int32):
+            return torch.empty(n, dtype=dtype, device=dev)
+
+        o = PageTable(ints(batch + 1), ints(batch * max_pages), ints(batch), ints(batch + 1), ints(int(max_tokens)),
+                      ints(int(max_tokens)), ints(int(max_tokens), torch.int64),
+                      None if free_pages is None else ints(1))
+    _call(fn, dev, seq_lens.data_ptr(), _ptr(new_lens), batch, int(page_size), block_table.data_ptr(), stride,
+          max_pages, int(num_pages), _ptr(free_pages), 0 if free_pages is None else free_pages.numel(),
+          _ptr(free_count), None if free_pages is None else o.free_left.data_ptr(), o.kv_indptr.data_ptr(),
+          o.kv_indices.data_ptr(), o.kv_indices.numel(), o.kv_last_page_len.data_ptr(), o.qo_indptr.data_ptr(),
+          o.batch_indices.data_ptr(), o.positions.data_ptr(), _ptr(o.slots), o.batch_indices.numel())
+    return o
+
+
+def _check_norm_rope(fn, _, q, k, v, cos_sin_cache, batch_indices, positions, kv_indptr, kv_indices, kv_cache,
+                     q_weight, k_weight, pos_ids, q_out):
+    if q is None and k is None:
+        raise ValueError("%s: give q, or k, v and kv_cache, or all" % fn)
+    if (k is None) != (v is None) or (k is None) != (kv_cache is None):
+        raise ValueError("%s: give k, v and kv_cache, or none of them" % fn)
+    first = q if q is not None else k
+    dev = _cuda_of(fn, "q" if q is not None else "k", first)
+    if first.dim() != 3:
+        raise ValueError("%s: %s has shape %s, not (rows, heads, head_dim)"
+                         % (fn, "q" if q is not None else "k", tuple(first.shape)))
+    nnz, _, dim = first.shape
+    dtypes = (first.dtype,) if first.dtype in _HALVES else _HALVES
+    qs = qos = ks = vs = cs = None
+    hq = hkv = pages = 0
+    page_size = 1
+    if q is not None:
+        _want(fn, "q", q, (nnz, None, dim), dtypes, dev)
+        _rows_last(fn, "q", q)
+        hq, qs = q.shape[1], _strides_of(q, 2)
+        qos = _strides(hq * dim, dim)
+        if q_out is not None:
+            _want(fn, "q_out", q_out, q.shape, dtypes, dev)
+            _rows_last(fn, "q_out", q_out, written=True)
+            qos = _strides_of(q_out, 2)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("%s: q_out and q_weight need q" % fn)
+    if k is not None:
+        _want(fn, "k", k, (nnz, None, dim), dtypes, dev)
+        hkv = k.shape[1]
+        _want(fn, "v", v, (nnz, hkv, dim), dtypes, dev)
+        _want(fn, "kv_cache", kv_cache, (None, 2, hkv, None, dim), dtypes, dev)
+        _rows_last(fn, "k", k)
+        _rows_last(fn, "v", v)
+        _rows_last(fn, "kv_cache", kv_cache, written=True)
+        ks, vs, cs = _strides_of(k, 2), _strides_of(v, 2), _strides_of(kv_cache, 4)
+        pages, page_size = kv_cache.shape[0], kv_cache.shape[3]
+    elif k_weight is not None:
+        raise ValueError("%s: k_weight needs k" % fn)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _list_of(fn, name, w, dim, dev, dtypes)
+    rot = limit = 0
+    table = FP32
+    if cos_sin_cache is not None:
+        _want(fn, "cos_sin_cache", cos_sin_cache, (None, None), (torch.float32, torch.bfloat16), dev)
+        _dense(fn, ("cos_sin_cache", cos_sin_cache))
+        limit, rot = cos_sin_cache.shape
+        table = _DT[cos_sin_cache.dtype]
+    for name, x in (("batch_indices", batch_indices), ("positions", positions), ("pos_ids", pos_ids)):
+        if x is not None or name != "pos_ids":
+            _list_of(fn, name, x, nnz, dev)
+    batch = 0
+    if k is not None:
+        _list_of(fn, "kv_indptr", kv_indptr, None, dev)
+        _list_of(fn, "kv_indices", kv_indices, None, dev)
+        batch = kv_indptr.numel() - 1
+        if batch < 0:
+            raise ValueError("%s: kv_indptr is empty" % fn)
+    return (dev, qs, qos, ks, vs, cs, (_DT[first.dtype], nnz, hq, hkv, dim), (table, limit, rot),
+            (batch, page_size, pages))
+
+
+def bskv_norm_rope_append_paged(q, k, v, cos_sin_cache, batch_indices, positions, kv_indptr, kv_indices,
+                                kv_cache, q_weight=None, k_weight=None, eps=1e-6, is_neox=True, pos_ids=None,
+                                q_out=None):
+    """RMS norms per head (q_weight, k_weight [D]; None: none) and rotation by cos_sin_cache [max_seq_len,
+    rotary_dim] (fp32 or bf16; None: none) at pos_ids (None: positions) of q [nnz, Hq, D] and k [nnz, Hkv, D];
+    k and v are written to token positions[i] of request batch_indices[i] of kv_cache [pages, 2, Hkv, page_size, D]
+    through the device page table (int32); rows with batch_indices -1 are passed over. q, or k, v and kv_cache, may be None.
+    Returns q's result (q_out, which may be q; unspecified in rows that are passed over if it is made here), or None."""
+    fn = "bskv_norm_rope_append_paged"
+    dev, qs, qos, ks, vs, cs, shape, table, where = _once(
+        _call_layouts, _check_norm_rope, fn, None, q, k, v, cos_sin_cache, batch_indices, positions, kv_indptr,
+        kv_indices, kv_cache, q_weight, k_weight, pos_ids, q_out)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    _call(fn, dev, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, *shape, _ptr(q_weight), _ptr(k_weight), float(eps),
+          _ptr(cos_sin_cache), *table, int(bool(is_neox)), _ptr(pos_ids), batch_indices.data_ptr(),
+          positions.data_ptr(), _ptr(kv_indptr), _ptr(kv_indices), *where, _ptr(q_out), qos, _ptr(kv_cache), cs)
+    return q_out
+
+
+def _bounds_strides(fn, bounds, shape, dtypes, device, written=False):
+    _want(fn, "bounds", bounds, shape, dtypes, device)
+    _rows_last(fn, "bounds", bounds, written)
+    if bounds.stride(2) != shape[3] and bounds.numel():
+        raise ValueError("%s: the last two dimensions of bounds must be contiguous" % fn)
+    return _strides_of(bounds, 2)
+
+
+def _check_block_bounds(fn, _, kv_cache, bounds, batch_indices, positions, kv_indptr, kv_indices, kv_last_page_len):
+    dev = _cuda_of(fn, "kv_cache", kv_cache)
+    _want(fn, "kv_cache", kv_cache, (None, 2, None, None, None), _HALVES, dev)
+    _rows_last(fn, "kv_cache", kv_cache)
+    pages, _, heads, page_size, dim = kv_cache.shape
+    bs = _bounds_strides(fn, bounds, (pages, heads, 2, dim), (kv_cache.dtype,), dev, written=True)
+    _list_of(fn, "batch_indices", batch_indices, None, dev)
+    nnz = batch_indices.numel()
+    _list_of(fn, "positions", positions, nnz, dev)
+    _list_of(fn, "kv_indptr", kv_indptr, None, dev)
+    _list_of(fn, "kv_indices", kv_indices, None, dev)
+    batch = kv_indptr.numel() - 1
+    if batch < 0:
+        raise ValueError("%s: kv_indptr is empty" % fn)
+    _list_of(fn, "kv_last_page_len", kv_last_page_len, batch, dev)
+    return dev, _strides_of(kv_cache, 4), bs, (_DT[kv_cache.dtype], heads, dim, page_size, pages), nnz, batch
+
+
+def bskv_block_bounds_paged(kv_cache, bounds, batch_indices, positions, kv_indptr, kv_indices, kv_last_page_len):
+    """Bring bounds [pages, Hkv, 2, D] (least and greatest key values per channel, in the cache's type) up to
+    date for the pages of kv_cache [pages, 2, Hkv, page_size, D] that hold the rows (batch_indices,
+    positions), through the device page table (all int32). Returns bounds."""
+    fn = "bskv_block_bounds_paged"
+    dev, cs, bs, shape, nnz, batch = _once(_call_layouts, _check_block_bounds, fn, None, kv_cache, bounds,
+                                           batch_indices, positions, kv_indptr, kv_indices, kv_last_page_len)
+    _call(fn, dev, kv_cache.data_ptr(), cs, *shape, batch_indices.data_ptr(), positions.data_ptr(), nnz,
+          kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_last_page_len.data_ptr(), batch, bounds.data_ptr(), bs)
+    return bounds
+
+
+def bskv_plan_decode_blocks(num_tokens, max_blocks, num_pages, page_size, num_qo_heads, num_kv_heads,
+                            head_dim, top_k, sink=0, recent=1, dtype=torch.bfloat16, num_sms=None):
+    """Plan of a block-sparse decode of num_tokens query rows over requests of up to max_blocks pages: each
+    query and kv head attends to top_k pages, the first `sink` and the last `recent` among them."""
+    fn = "bskv_plan_decode_blocks"
+    lib = load_library()
+    h = ctypes.c_void_p()
+    ns = _num_sms() if num_sms is None else num_sms
+    if dtype not in _DT:
+        raise ValueError("%s: dtype is %s, not %s" % (fn, dtype, " or ".join(map(str, _HALVES))))
+    _check(fn, lib.bskv_plan_decode_blocks(
+        int(num_tokens), int(max_blocks), int(num_pages), int(page_size), int(num_qo_heads), int(num_kv_heads),
+        int(head_dim), int(top_k), int(sink), int(recent), _DT[dtype], int(ns), ctypes.byref(h)))
+    return Plan(h.value, "decode_blocks", num_pages=int(num_pages), page_size=int(page_size),
+                num_qo_heads=int(num_qo_heads), num_kv_heads=int(num_kv_heads), head_dim=int(head_dim), dtype=dtype,
+                max_blocks=int(max_blocks), blocks_shape=(int(num_tokens), int(num_kv_heads), int(top_k)),
+                q_shape=(int(num_tokens), int(num_qo_heads), int(head_dim)))
+
+
+def _check_blocks(fn, plan, q, blocks, batch_indices, positions, kv_indptr, kv_indices):
+    i = plan.info
+    dev = _cuda_of(fn, "q", q)
+    _want(fn, "q", q, i["q_shape"], (i["dtype"],), dev)
+    _rows_last(fn, "q", q)
+    if blocks is not None:
+        _want(fn, "blocks", blocks, i["blocks_shape"], _I32T, dev)
+        _dense(fn, ("blocks", blocks))
+    _list_of(fn, "batch_indices", batch_indices, i["q_shape"][0], dev)
+    _list_of(fn, "positions", positions, i["q_shape"][0], dev)
+    _list_of(fn, "kv_indptr", kv_indptr, None, dev)
+    _list_of(fn, "kv_indices", kv_indices, None, dev)
+    if kv_indptr.numel() < 1:
+        raise ValueError("%s: kv_indptr is empty" % fn)
+    return dev, _strides_of(q, 2), kv_indptr.numel() - 1
+
+
+def _check_select_blocks(fn, plan, q, bounds, *lists):
+    i = plan.info
+    dev, qs, batch = _check_blocks(fn, plan, q, *lists)
+    bs = _bounds_strides(fn, bounds, (i["num_pages"], i["num_kv_heads"], 2, i["head_dim"]), (i["dtype"],), dev)
+    return dev, qs, bs, batch, i["blocks_shape"]
+
+
+def bskv_run_select_blocks(plan, q, bounds, batch_indices, positions, kv_indptr, kv_indices, blocks=None):
+    """The pages that each query row (token positions[t] of request batch_indices[t]) and kv head attends to, chosen
+    by bounds [pages, Hkv, 2, D]: blocks [T, Hkv, top_k] int32, page numbers within the request, ascending, -1 where
+    there are fewer; rows with batch_indices -1 are left as they were (unspecified in an output made here)."""
+    fn = "bskv_run_select_blocks"
+    _check_plan(fn, plan, "decode_blocks")
+    dev, qs, bs, batch, shape = _once(plan.layouts, _check_select_blocks, fn, plan, q, bounds, blocks, batch_indices,
+                                      positions, kv_indptr, kv_indices)
+    if blocks is None:
+        blocks = torch.empty(shape, dtype=torch.int32, device=dev)
+    _ready(fn, plan, dev)
+    fw = plan.float_ws
+    _call(fn, dev, plan.handle, q.data_ptr(), qs, bounds.data_ptr(), bs, batch_indices.data_ptr(),
+          positions.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(), batch, blocks.data_ptr(), _ptr(fw),
+          0 if fw is None else fw.numel())
+    return blocks
+
+
+def _check_decode_blocks(fn, plan, q, kv_cache, out, lse, *lists):
+    i = plan.info
+    if lists[0] is None:
+        raise TypeError("%s: blocks must be a tensor" % fn)
+    dev, qs, batch = _check_blocks(fn, plan, q, *lists)
+    shape = i["q_shape"]
+    cache = _kv_pages(fn, plan, kv_cache, (i["dtype"],), dev)
+    if out is not None:
+        _want(fn, "out", out, shape, (i["dtype"],), dev)
+        _rows_last(fn, "out", out, written=True)
+    if lse is not None:
+        _want(fn, "lse", lse, shape[:2], _F32T, dev)
+        _dense(fn, ("lse", lse))
+    outs = _strides(shape[1] * shape[2], shape[2]) if out is None else _strides_of(out, 2)
+    return dev, qs, cache[0], outs, batch, shape
+
+
+def bskv_run_decode_blocks(plan, q, kv_cache, blocks, batch_indices, positions, kv_indptr, kv_indices,
+                           out=None, lse=None, return_lse=False, sm_scale=None):
+    """Attention of query rows q [T, Hq, D] (token positions[t] of request batch_indices[t]) over the listed blocks
+    [T, Hkv, top_k] of kv_cache [pages, 2, Hkv, page_size, D], each up to the query's own token. Rows with
+    batch_indices -1 are left as they were (unspecified in outputs made here)."""
+    fn = "bskv_run_decode_blocks"
+    _check_plan(fn, plan, "decode_blocks")
+    dev, qs, cs, outs, batch, shape = _once(plan.layouts, _check_decode_blocks, fn, plan, q, kv_cache, out, lse,
+                                            blocks, batch_indices, positions, kv_indptr, kv_indices)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    if lse is None and return_lse:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    _ready(fn, plan, dev)
+    fw = plan.float_ws
+    _call(fn, dev, plan.handle, q.data_ptr(), qs, kv_cache.data_ptr(), cs, blocks.data_ptr(),
+          batch_indices.data_ptr(), positions.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(), batch,
+          out.data_ptr(), outs, _ptr(lse), 0.0 if sm_scale is None else float(sm_scale), _ptr(fw),
+          0 if fw is None else fw.numel())
+    return (out, lse) if return_lse else out
 
 
 def bskv_merge_states(v, s, out_dtype=torch.float32, v_out=None, s_out=None):

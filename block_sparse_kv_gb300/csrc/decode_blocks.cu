@@ -1,0 +1,570 @@
+// Decode over chosen blocks of a paged cache: each (query, kv head) row attends to its own list.
+//
+// Mathematics. For query t, kv head h and the group's query heads, over the tokens j <= position of t that
+// lie in a listed block (a page): out = sum_j softmax_j(scale q.k_j) v_j, lse = log sum_j exp(scale q.k_j),
+// in one pass with a running maximum and sum.
+//
+// Bound by reading K and V of the listed blocks: a block of one head is a piece of page_size * D 16-bit
+// values, wherever its page lies. One worker is one warp; eight to a CTA and one CTA per SM keep up to
+// 192 KB of copies in flight, each warp in a ring of its own, so that no warp waits for another. The up to 16
+// query heads of a group are the M = 16 rows of mma.sync m16n8k16 against 16 tokens at a time.
+//
+// Split. The lists' lengths are known on the GPU only, so the cut is made in list places: the rows'
+// lists of top_k places follow one another and each worker takes an equal run of them; a worker's run
+// covers the same fraction of a row's actual list (place f of top_k stands for entry f n / top_k of n),
+// so that short lists are cut as evenly as full ones. A row in several pieces leaves partial states in the float
+// workspace, and the warp that finishes its last piece joins them in the same launch, in piece order.
+#include <algorithm>
+
+#include "cache_common.cuh"
+#include "internal.h"
+#include "launch.h"
+
+namespace bskv {
+namespace {
+
+using namespace dev;
+
+constexpr int kTile = 16;  // tokens per stage
+constexpr int kWarps = kBlocksWarps;
+constexpr int kPanel = kTile * 128;  // 16 rows of 64 16-bit values, swizzled
+
+struct BlocksParams {
+  const void* q;
+  int64_t q_s0, q_s1;
+  void* out;
+  int64_t o_s0, o_s1;
+  float* lse;
+  const int32_t *blocks, *batch_indices, *positions, *kv_indptr, *kv_indices;
+  float *ws_o, *ws_lse;
+  int* counters;
+  int num_rows, top_k, per_worker, workers, places;  // places = num_rows * top_k
+  int group, num_qo_heads, batch, num_pages;
+  FastDiv heads, page_size, by_top, by_worker;
+  float scale_log2;
+  StatusArgs st;
+};
+
+template <int D>
+struct Ring {
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kTileBytes = (D / 64) * kPanel;
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kBytes = kStages * kStageBytes;
+};
+
+// What the copying side tells the computing side about a stage.
+struct StageInfo {
+  int row;      // (query, kv head)
+  int valid;    // tokens of its two groups of eight that are attended to: low and high half word
+  int flags;    // 1: first tile of a piece, 2: last
+  int piece;    // of the row
+};
+constexpr int kFirst = 1, kLast = 2;
+
+// Pieces of a row: those of the workers from `first` to `last`.
+struct Pieces {
+  int first, last;
+};
+__device__ __forceinline__ Pieces pieces_of(const BlocksParams& p, int row) {
+  return Pieces{p.by_worker.div(row * p.top_k), p.by_worker.div(row * p.top_k + p.top_k - 1)};
+}
+
+// A worker's way through its places: piece by piece, 32 list entries at a time, one lane each.
+struct Walk {
+  const BlocksParams& p;
+  int place, end;       // places that are to come
+  int lane;
+  // the piece
+  int row, at, stop;    // entries [at, stop) of the row's list are to come
+  int start, pos;       // of the row's request
+  int piece;
+  bool fresh;           // no tile of the piece has been given out
+  bool skip;            // a row without a token
+  // the window of up to 32 entries: lane i holds entry i's page and its attended tokens
+  int page, count;
+  uint32_t todo;        // entries that are not given out yet
+  int entry, slot;      // the one being given out, and its next slot
+
+  __device__ __forceinline__ Walk(const BlocksParams& p_, int w, int lane_)
+      : p(p_), place(w * p_.per_worker), end(min(p_.places, place + p_.per_worker)), lane(lane_), todo(0), entry(-1) {
+    open();
+  }
+  __device__ __forceinline__ bool live() const { return row >= 0; }
+  // The next piece, if there is one.
+  __device__ __forceinline__ void open() {
+    row = -1;
+    while (place < end) {
+      int f0;
+      const int r = p.by_top.divmod(place, f0);
+      const int f1 = min(p.top_k, f0 + end - place);
+      const int first = place - f0;  // the row's first place
+      piece = p.by_worker.div(place) - p.by_worker.div(first);
+      place += f1 - f0;
+      int h;
+      const int t = p.heads.divmod(r, h);
+      const int b = __ldg(p.batch_indices + t);
+      if (b < 0) continue;  // a row without a token: nothing is written
+      pos = __ldg(p.positions + t);
+      int n = 0;
+      bool bad = b >= p.batch || pos < 0;
+      if (!bad) {
+        start = __ldg(p.kv_indptr + b);
+        n = p.page_size.div(pos) + 1;
+        bad = n > __ldg(p.kv_indptr + b + 1) - start;
+      }
+      if (bad) {
+        if (lane == 0) record_error(p.st, BSKV_ERR_DEVICE_INDEX);
+        n = 0;
+      }
+      n = min(n, p.top_k);
+      at = int(int64_t(f0) * n / p.top_k);
+      stop = int(int64_t(f1) * n / p.top_k);
+      row = r;
+      fresh = true;
+      window();
+      return;
+    }
+  }
+  __device__ __forceinline__ void window() {
+    page = -1;
+    count = 0;
+    if (at + lane < stop) {
+      const int block = __ldg(p.blocks + int64_t(row) * p.top_k + at + lane);
+      if (block >= 0) {
+        const int seen = p.page_size.div(pos) + 1;
+        if (block < seen) {
+          page = __ldg(p.kv_indices + start + block);
+          count = block < seen - 1 ? int(p.page_size.d) : pos - block * int(p.page_size.d) + 1;
+        }
+        if (page < 0 || page >= p.num_pages) {
+          record_error(p.st, BSKV_ERR_DEVICE_INDEX);
+          count = 0;
+        }
+      }
+    }
+    at = min(stop, at + 32);
+    todo = __ballot_sync(0xffffffffu, count > 0);
+  }
+  // Moves to an entry that has tokens left; false: the piece has none.
+  __device__ __forceinline__ bool seek() {
+    if (entry >= 0) return true;
+    while (!todo && at < stop) window();
+    if (!todo) return false;
+    entry = __ffs(todo) - 1;
+    todo &= todo - 1;
+    slot = 0;
+    return true;
+  }
+};
+
+// Row r of 64-column half hf of a stage's K or V: rows of 128 bytes, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_row(uint32_t base, int r, int hf) { return base + hf * kPanel + r * 128; }
+
+// One tile of 16 tokens for the (up to 16) query heads of a row. v0 and v1 of the two groups of eight
+// tokens are attended to.
+template <typename T, int D>
+__device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, int v0, int v1, float scale_log2, int lane,
+                                            const uint32_t (&qa)[D / 16][4], float (&o)[D / 8][4], float& m0,
+                                            float& m1, float& l0, float& l1) {
+  using Mma = MmaOp<T>;
+  const int cq = lane & 3;
+  if (v0 + v1 < kTile) {
+    // slots that are not attended to may hold anything: 0 * NaN must not reach the output
+    for (int i = lane; i < kTile * (D / 8); i += 32) {
+      const int r = i / (D / 8), c = i % (D / 8);
+      if ((r & 7) >= (r < 8 ? v0 : v1)) sts128(tile_row(v_at, r, c >> 3) + (c & 7) * 16, make_uint4(0, 0, 0, 0));
+    }
+    __syncwarp();
+  }
+  float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  {
+    const int mi = lane >> 3, r = (mi >> 1) * 8 + (lane & 7);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const int dim = kk * 16 + (mi & 1) * 8;
+      uint32_t b0, b1, b2, b3;
+      ldsm_x4(tile_row(k_at, r, dim / 64) + ((((dim % 64) / 8) ^ (r & 7)) << 4), b0, b1, b2, b3);
+      Mma::run(s[0], qa[kk], b0, b1);
+      Mma::run(s[1], qa[kk], b2, b3);
+    }
+  }
+  float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt) {
+    const int valid = nt ? v1 : v0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[nt][e] = 2 * cq + (e & 1) < valid ? s[nt][e] * scale_log2 : -INFINITY;
+    mx0 = fmaxf(mx0, fmaxf(s[nt][0], s[nt][1]));
+    mx1 = fmaxf(mx1, fmaxf(s[nt][2], s[nt][3]));
+  }
+  mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+  mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+  mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+  mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+  const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+  const float a0 = fast_exp2(m0 - mn0), a1 = fast_exp2(m1 - mn1);
+  m0 = mn0;
+  m1 = mn1;
+  float ps0 = 0.f, ps1 = 0.f;
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt) {
+    s[nt][0] = fast_exp2(s[nt][0] - mn0);
+    s[nt][1] = fast_exp2(s[nt][1] - mn0);
+    s[nt][2] = fast_exp2(s[nt][2] - mn1);
+    s[nt][3] = fast_exp2(s[nt][3] - mn1);
+    ps0 += s[nt][0] + s[nt][1];
+    ps1 += s[nt][2] + s[nt][3];
+  }
+  l0 = l0 * a0 + ps0;
+  l1 = l1 * a1 + ps1;
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n) {
+    o[n][0] *= a0;
+    o[n][1] *= a0;
+    o[n][2] *= a1;
+    o[n][3] *= a1;
+  }
+  // weights at most 1 round to 16 bits for the product with V
+  const uint32_t pa[4] = {Mma::pack(s[0][0], s[0][1]), Mma::pack(s[0][2], s[0][3]), Mma::pack(s[1][0], s[1][1]),
+                          Mma::pack(s[1][2], s[1][3])};
+  {
+    const int mi = lane >> 3, r = (mi & 1) * 8 + (lane & 7);
+#pragma unroll
+    for (int dd = 0; dd < D / 16; ++dd) {
+      const int dim = dd * 16 + (mi >> 1) * 8;
+      uint32_t b0, b1, b2, b3;
+      ldsm_x4_t(tile_row(v_at, r, dim / 64) + ((((dim % 64) / 8) ^ (r & 7)) << 4), b0, b1, b2, b3);
+      Mma::run(o[2 * dd], pa, b0, b1);
+      Mma::run(o[2 * dd + 1], pa, b2, b3);
+    }
+  }
+}
+
+// Joins the `count` states of a row from slot `first` on and writes them: a lane covers four values
+// of every (128 / D)-th query head. States without a token (lse -inf) are passed over.
+template <typename T, int D>
+__device__ __forceinline__ void join(const BlocksParams& p, int lane, int first, int count, T* out, float* lse) {
+  constexpr int kHeads = 128 / D, kAhead = 4;
+  const int dl = (lane * 4) % D;
+  for (int g = (lane * 4) / D; g - (lane * 4) / D < p.group; g += kHeads) {
+    float m = -INFINITY, total = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = 0; c0 < count; c0 += kAhead) {
+      float z[kAhead];
+      float4 x[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        z[j] = -INFINITY;
+        if (c0 + j < count && g < p.group) {
+          const int64_t at = int64_t(first + c0 + j) * p.group + g;
+          z[j] = __ldcg(p.ws_lse + at);
+          x[j] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * D + dl));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (z[j] == -INFINITY) continue;
+        const float mn = fmaxf(m, z[j]);
+        const float sc = m == -INFINITY ? 0.f : expf(m - mn), w = expf(z[j] - mn);
+        total = total * sc + w;
+        acc.x = acc.x * sc + w * x[j].x;
+        acc.y = acc.y * sc + w * x[j].y;
+        acc.z = acc.z * sc + w * x[j].z;
+        acc.w = acc.w * sc + w * x[j].w;
+        // a NaN state makes the sums NaN; the maximum passes over it
+        m = mn;
+      }
+    }
+    if (g < p.group) {
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      uint32_t* to = reinterpret_cast<uint32_t*>(out + g * p.o_s1 + dl);
+      to[0] = MmaOp<T>::pack(acc.x * inv, acc.y * inv);
+      to[1] = MmaOp<T>::pack(acc.z * inv, acc.w * inv);
+      if (lse && dl == 0) lse[g] = total == 0.f ? -INFINITY : m + logf(total);
+    }
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    decode_blocks_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ BlocksParams p) {
+  using R = Ring<D>;
+  using Mma = MmaOp<T>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = smem + warp * R::kBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * R::kBytes) + warp * R::kStages;
+  StageInfo* infos = reinterpret_cast<StageInfo*>(smem + kWarps * R::kBytes + kWarps * R::kStages * 8) + warp * R::kStages;
+  const int w = warp * gridDim.x + blockIdx.x;  // every SM has one worker before any has two
+  if (w >= p.workers) return;
+  if (lane == 0) {
+    for (int s = 0; s < R::kStages; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+    prefetch_tensormap(&kv_map);
+  }
+  __syncwarp();
+  const bool forced = forced_timeout(p.st);
+  const uint64_t policy = l2_evict_first_policy();
+  const int ps = int(p.page_size.d);
+
+  // Copies the next tile of the walk into a stage; a piece without tokens is a tile of none.
+  Walk walk(p, w, lane);
+  uint32_t issued = 0;
+  auto issue = [&]() {
+    if (!walk.live()) return;
+    const int stage = issued % R::kStages;
+    uint8_t* k_to = ring + stage * R::kStageBytes;
+    uint8_t* v_to = k_to + R::kTileBytes;
+    StageInfo info{walk.row, 0, walk.fresh ? kFirst : 0, walk.piece};
+    walk.fresh = false;
+    int h;
+    p.heads.divmod(walk.row, h);
+    if (!walk.seek()) {
+      if (lane == 0) mbar_arrive(&bars[stage]);
+    } else if (ps >= kTile) {
+      const int page = __shfl_sync(0xffffffffu, walk.page, walk.entry), count = __shfl_sync(0xffffffffu, walk.count, walk.entry);
+      const int slot = walk.slot, left = count - slot;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars[stage], uint32_t(R::kStageBytes));
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf) {
+          tma_load_5d_hint(k_to + hf * kPanel, &kv_map, hf * 64, slot, h, 0, page, &bars[stage], policy);
+          tma_load_5d_hint(v_to + hf * kPanel, &kv_map, hf * 64, slot, h, 1, page, &bars[stage], policy);
+        }
+      }
+      info.valid = min(left, 8) | max(0, min(left - 8, 8)) << 16;
+      walk.slot += kTile;
+      if (walk.slot >= count) walk.entry = -1;
+    } else {  // two pages of eight
+      const int page0 = __shfl_sync(0xffffffffu, walk.page, walk.entry), c0 = __shfl_sync(0xffffffffu, walk.count, walk.entry);
+      walk.entry = -1;
+      int page1 = -1, c1 = 0;
+      if (walk.seek()) {
+        page1 = __shfl_sync(0xffffffffu, walk.page, walk.entry);
+        c1 = __shfl_sync(0xffffffffu, walk.count, walk.entry);
+        walk.entry = -1;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars[stage], uint32_t(c1 ? R::kStageBytes : R::kStageBytes / 2));
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf) {
+          tma_load_5d_hint(k_to + hf * kPanel, &kv_map, hf * 64, 0, h, 0, page0, &bars[stage], policy);
+          tma_load_5d_hint(v_to + hf * kPanel, &kv_map, hf * 64, 0, h, 1, page0, &bars[stage], policy);
+          if (c1) {
+            tma_load_5d_hint(k_to + hf * kPanel + 1024, &kv_map, hf * 64, 0, h, 0, page1, &bars[stage], policy);
+            tma_load_5d_hint(v_to + hf * kPanel + 1024, &kv_map, hf * 64, 0, h, 1, page1, &bars[stage], policy);
+          }
+        }
+      }
+      info.valid = c0 | c1 << 16;
+    }
+    if (!walk.seek()) {
+      info.flags |= kLast;
+      walk.open();
+    }
+    if (lane == 0) infos[stage] = info;
+    ++issued;
+  };
+  for (int s = 0; s < R::kStages; ++s) issue();
+  __syncwarp();
+
+  uint32_t qa[D / 16][4];
+  float o[D / 8][4];
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  const int r0 = lane >> 2, r1 = r0 + 8, cq = lane & 3;
+  uint32_t consumed = 0;
+  bool ok = true;
+  while (consumed < issued) {
+    const int stage = consumed % R::kStages;
+    const StageInfo info = infos[stage];
+    int h;
+    const int t = p.heads.divmod(info.row, h);
+    if (info.flags & kFirst) {
+      const T* q = static_cast<const T*>(p.q) + t * p.q_s0 + int64_t(h) * p.group * p.q_s1;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const int d = kk * 16 + 2 * cq;
+        qa[kk][0] = r0 < p.group ? __ldg(reinterpret_cast<const uint32_t*>(q + r0 * p.q_s1 + d)) : 0u;
+        qa[kk][1] = r1 < p.group ? __ldg(reinterpret_cast<const uint32_t*>(q + r1 * p.q_s1 + d)) : 0u;
+        qa[kk][2] = r0 < p.group ? __ldg(reinterpret_cast<const uint32_t*>(q + r0 * p.q_s1 + d + 8)) : 0u;
+        qa[kk][3] = r1 < p.group ? __ldg(reinterpret_cast<const uint32_t*>(q + r1 * p.q_s1 + d + 8)) : 0u;
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      m0 = m1 = -INFINITY;
+      l0 = l1 = 0.f;
+    }
+    if (!warp_wait(&bars[stage], (consumed / R::kStages) & 1u, p.st, forced)) {
+      ok = false;
+      break;
+    }
+    const uint32_t at = smem_u32(ring + stage * R::kStageBytes);
+    if (info.valid) attend_tile<T, D>(at, at + R::kTileBytes, info.valid & 0xffff, info.valid >> 16, p.scale_log2, lane, qa, o, m0, m1, l0, l1);
+    ++consumed;
+    __syncwarp();
+    if (lane == 0) fence_proxy_async_smem();
+    issue();
+    __syncwarp();
+    if (!(info.flags & kLast)) continue;
+
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
+    const float z0 = l0 == 0.f ? -INFINITY : (m0 + __log2f(l0)) * kLn2, z1 = l1 == 0.f ? -INFINITY : (m1 + __log2f(l1)) * kLn2;
+    T* out = static_cast<T*>(p.out) + t * p.o_s0 + int64_t(h) * p.group * p.o_s1;
+    float* lse = p.lse ? p.lse + int64_t(t) * p.num_qo_heads + h * p.group : nullptr;
+    const Pieces pieces = pieces_of(p, info.row);
+    if (pieces.first == pieces.last) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        const int d = n * 8 + 2 * cq;
+        if (r0 < p.group) *reinterpret_cast<uint32_t*>(out + r0 * p.o_s1 + d) = Mma::pack(o[n][0] * inv0, o[n][1] * inv0);
+        if (r1 < p.group) *reinterpret_cast<uint32_t*>(out + r1 * p.o_s1 + d) = Mma::pack(o[n][2] * inv1, o[n][3] * inv1);
+      }
+      if (lse && cq == 0) {
+        if (r0 < p.group) lse[r0] = z0;
+        if (r1 < p.group) lse[r1] = z1;
+      }
+      continue;
+    }
+    // a row's slots follow one another: workers before it and rows before it have had one each
+    const int slot0 = pieces.first + info.row;
+    const int64_t base = int64_t(slot0 + info.piece) * p.group;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+      const int d = n * 8 + 2 * cq;
+      if (r0 < p.group) *reinterpret_cast<float2*>(p.ws_o + (base + r0) * D + d) = make_float2(o[n][0] * inv0, o[n][1] * inv0);
+      if (r1 < p.group) *reinterpret_cast<float2*>(p.ws_o + (base + r1) * D + d) = make_float2(o[n][2] * inv1, o[n][3] * inv1);
+    }
+    if (cq == 0) {
+      if (r0 < p.group) p.ws_lse[base + r0] = z0;
+      if (r1 < p.group) p.ws_lse[base + r1] = z1;
+    }
+    __syncwarp();
+    const int count = pieces.last - pieces.first + 1;
+    int old = 0;
+    if (lane == 0) old = atomic_add_acq_rel(p.counters + info.row, 1);
+    if (__shfl_sync(0xffffffffu, old, 0) == count - 1) {
+      join<T, D>(p, lane, slot0, count, out, lse);
+      if (lane == 0) p.counters[info.row] = 0;  // ready for the next run
+    }
+    __syncwarp();
+  }
+  if (!ok) {
+    // the copies in flight land before the warp leaves (bounded, not forcible)
+    for (uint32_t s = consumed; s < issued; ++s) mbar_wait(&bars[s % R::kStages], (s / R::kStages) & 1u, p.st, false);
+  }
+}
+
+template <typename T, int D>
+bskv_status launch(const CUtensorMap& map, const BlocksParams& p, int num_sms, cudaStream_t st) {
+  using R = Ring<D>;
+  auto kern = decode_blocks_kernel<T, D>;
+  constexpr size_t smem = 1024 + kWarps * (R::kBytes + R::kStages * (8 + sizeof(StageInfo)));
+  static std::atomic<int> allowed[64];
+  if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "run_decode_blocks: cudaFuncSetAttribute")) return s;
+  kern<<<unsigned(std::min(num_sms, p.workers)), kWarps * 32, smem, st>>>(map, p);
+  return cuda_check(cudaGetLastError(), "run_decode_blocks launch");
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+BlocksWorkspace blocks_workspace(const bskv_plan* plan) {
+  BlocksWorkspace w{};
+  const size_t rows = size_t(plan->M) * size_t(plan->num_kv_heads), blocks = size_t(plan->max_blocks);
+  const size_t group = size_t(plan->num_qo_heads / std::max(1, plan->num_kv_heads));
+  const size_t slots = rows + size_t(plan->workers);
+  w.parts = plan->parts;
+  size_t at = 0;
+  w.exact = at; at += align256(rows * blocks * 8);
+  w.scores = at; at += align256(rows * blocks * 4);
+  w.sums = at; at += align256(rows * size_t(plan->parts) * 4);
+  w.states = at; at += align256(slots * group * size_t(plan->head_dim) * 4);
+  w.lse = at; at += align256(slots * group * 4);
+  w.total = at;
+  return w;
+}
+
+bskv_status check_blocks_run(const char* who, const bskv_plan* plan, const int32_t* batch_indices,
+                             const int32_t* positions, const int32_t* kv_indptr, const int32_t* kv_indices,
+                             int32_t batch, const int32_t* blocks, const void* float_ws, size_t float_ws_bytes) {
+  if (!plan || plan->kind != KIND_BLOCKS) { set_error("%s: not a block-sparse decode plan", who); return BSKV_ERR_INVALID_ARG; }
+  if (!plan->meta_dev) { set_error("%s: plan not uploaded (bskv_plan_upload)", who); return BSKV_ERR_INVALID_ARG; }
+  if (batch < 0) { set_error("%s: batch=%d", who, batch); return BSKV_ERR_INVALID_ARG; }
+  if (plan->M == 0) return BSKV_OK;
+  if (!batch_indices || !positions || !kv_indptr || !kv_indices || !blocks) { set_error("%s: NULL argument", who); return BSKV_ERR_INVALID_ARG; }
+  if ((reinterpret_cast<uintptr_t>(batch_indices) | reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(kv_indptr) |
+       reinterpret_cast<uintptr_t>(kv_indices) | reinterpret_cast<uintptr_t>(blocks)) & 3) {
+    set_error("%s: index arrays must be 4-byte aligned", who);
+    return BSKV_ERR_INVALID_ARG;
+  }
+  if (!float_ws || float_ws_bytes < plan->float_ws_bytes) {
+    set_error("%s: float workspace of %zu bytes, %zu needed", who, float_ws_bytes, plan->float_ws_bytes);
+    return BSKV_ERR_WORKSPACE_TOO_SMALL;
+  }
+  if (!aligned16(float_ws)) { set_error("%s: the float workspace must be 16-byte aligned", who); return BSKV_ERR_INVALID_ARG; }
+  return BSKV_OK;
+}
+
+}  // namespace bskv
+
+using namespace bskv;
+
+extern "C" bskv_status bskv_run_decode_blocks(
+    const bskv_plan* plan, const void* q, const int64_t* q_strides, const void* kv_cache,
+    const int64_t* kv_strides, const int32_t* blocks, const int32_t* batch_indices,
+    const int32_t* positions, const int32_t* kv_indptr, const int32_t* kv_indices, int32_t batch,
+    void* out, const int64_t* out_strides, float* lse, float sm_scale, void* float_ws,
+    size_t float_ws_bytes, void* stream) {
+  BSKV_NVTX_RANGE("bskv_run_decode_blocks");
+  const char* who = "run_decode_blocks";
+  if (bskv_status s = check_blocks_run(who, plan, batch_indices, positions, kv_indptr, kv_indices, batch, blocks, float_ws, float_ws_bytes)) return s;
+  if (plan->M == 0) return BSKV_OK;
+  if (!q || !q_strides || !out || !out_strides || !kv_cache || !kv_strides) { set_error("%s: NULL argument", who); return BSKV_ERR_INVALID_ARG; }
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out)) { set_error("%s: tensors must be 16-byte aligned", who); return BSKV_ERR_INVALID_ARG; }
+  for (int i = 0; i < 4; ++i)
+    if (kv_strides[i] <= 0 || kv_strides[i] % 8) {
+      set_error("%s: kv stride %d (%lld elements) must be positive and 16-byte aligned", who, i, (long long)kv_strides[i]);
+      return BSKV_ERR_INVALID_ARG;
+    }
+  for (int i = 0; i < 2; ++i)
+    if (q_strides[i] < 0 || q_strides[i] % 8 || out_strides[i] < 0 || out_strides[i] % 8) {
+      set_error("%s: q and out strides must be multiples of 16 bytes", who);
+      return BSKV_ERR_INVALID_ARG;
+    }
+  if (plan->num_pages == 0) { set_error("%s: a cache without pages", who); return BSKV_ERR_INVALID_ARG; }
+  const BlocksWorkspace ws = blocks_workspace(plan);
+  uint8_t* base = static_cast<uint8_t*>(float_ws);
+  BlocksParams p{};
+  p.q = q; p.q_s0 = q_strides[0]; p.q_s1 = q_strides[1];
+  p.out = out; p.o_s0 = out_strides[0]; p.o_s1 = out_strides[1];
+  p.lse = lse;
+  p.blocks = blocks; p.batch_indices = batch_indices; p.positions = positions; p.kv_indptr = kv_indptr; p.kv_indices = kv_indices;
+  p.ws_o = reinterpret_cast<float*>(base + ws.states); p.ws_lse = reinterpret_cast<float*>(base + ws.lse);
+  p.num_rows = plan->M * plan->num_kv_heads;
+  p.counters = plan->counters_dev + p.num_rows;  // the selection's come first
+  p.top_k = plan->top_k; p.per_worker = plan->per_worker; p.workers = plan->workers; p.places = p.num_rows * plan->top_k;
+  p.group = plan->num_qo_heads / plan->num_kv_heads; p.num_qo_heads = plan->num_qo_heads;
+  p.batch = batch; p.num_pages = plan->num_pages;
+  p.heads = FastDiv(plan->num_kv_heads); p.page_size = FastDiv(plan->page_size);
+  p.by_top = FastDiv(plan->top_k); p.by_worker = FastDiv(plan->per_worker);
+  p.scale_log2 = sm_scale_log2(sm_scale, plan->head_dim);
+  if (bskv_status s = status_args(&p.st)) return s;
+  const int ps = plan->page_size, D = plan->head_dim;
+  const uint64_t dims[5] = {uint64_t(D), uint64_t(ps), uint64_t(plan->num_kv_heads), 2, uint64_t(plan->num_pages)};
+  const uint64_t strides[4] = {uint64_t(kv_strides[3]) * 2, uint64_t(kv_strides[2]) * 2, uint64_t(kv_strides[1]) * 2, uint64_t(kv_strides[0]) * 2};
+  const uint32_t box[5] = {64, uint32_t(std::min(ps, kTile)), 1, 1, 1};
+  CUtensorMap map;
+  if (bskv_status s = encode_tiled(&map, plan->dtype == BSKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                                   5, kv_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (D == 128) return plan->dtype == BSKV_BF16 ? launch<__nv_bfloat16, 128>(map, p, plan->num_sms, st) : launch<__half, 128>(map, p, plan->num_sms, st);
+  return plan->dtype == BSKV_BF16 ? launch<__nv_bfloat16, 64>(map, p, plan->num_sms, st) : launch<__half, 64>(map, p, plan->num_sms, st);
+}

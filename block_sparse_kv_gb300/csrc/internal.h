@@ -16,7 +16,7 @@ namespace bskv {
 // ---- plan metadata: int32 words, header then 16-byte aligned sections ----------------
 constexpr int32_t kMetaMagic = 0x766b7362;  // "bskv"
 enum Kind : int32_t { KIND_DECODE = 1, KIND_BSR = 2, KIND_MLA = 3, KIND_DECODE_FP4 = 4,
-                      KIND_WEIGHTS = 5, KIND_EVICT = 6 };
+                      KIND_WEIGHTS = 5, KIND_EVICT = 6, KIND_BLOCKS = 7 };
 enum Header : int {
   H_MAGIC = 0,
   H_KIND,
@@ -162,6 +162,17 @@ inline bool fp4_page_size(int32_t page_size) {
   return page_size == 8 || (page_size >= 16 && page_size % 16 == 0);
 }
 
+// Block-sparse decode plans. A (query, kv head) row's blocks are scored by up to kSelectParts-many CTAs
+// (a part has at least kSelectMin blocks), all candidates of a row fit the shared memory of the CTA that
+// selects. The attention's workers are warps: the rows' lists of top_k blocks one after another, cut into
+// equal pieces of at least kBlocksMinTokens tokens.
+constexpr int kSelectThreads = 256;
+constexpr int kSelectMaxBlocks = 49152;
+constexpr int kSelectMin = 64;
+constexpr int kSelectCtasPerSm = 4;
+constexpr int kBlocksWarps = 8;
+constexpr int kBlocksMinTokens = 64;
+
 // Byte offset in the int workspace of the merge counters (after the metadata).
 inline size_t merge_counter_offset(size_t meta_words) { return ((meta_words * 4 + 255) / 256) * 256; }
 
@@ -218,7 +229,22 @@ struct bskv_plan {
   // request, the most tokens that one keeps, whether the kept rows stay in their pages
   int64_t kept_total = 0;
   int32_t sink = 0, recent = 0, longest = 0, most = 0, in_place = 0;
+  // blocks: M query tokens, top_k blocks of at most max_blocks, sink and recent of them by place; parts
+  // of a row when blocks are scored, list entries of a worker, workers of the attention
+  int32_t max_blocks = 0, parts = 0, per_worker = 0, workers = 0;
   // set by bskv_plan_upload
   const int32_t* meta_dev = nullptr;
   int32_t* counters_dev = nullptr;  // one merge counter per merge item, zero between runs
 };
+
+namespace bskv {
+
+// Where a block-sparse plan's parts of the float workspace begin (bytes): fp64 keys, fp32 scores and sums
+// of the selection, partial states of the attention.
+struct BlocksWorkspace {
+  size_t exact, scores, sums, states, lse, total;
+  int parts;
+};
+BlocksWorkspace blocks_workspace(const bskv_plan* plan);
+
+}  // namespace bskv

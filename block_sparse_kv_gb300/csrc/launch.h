@@ -35,6 +35,11 @@ bskv_status launch_state_merge(const bskv_plan* plan, const int32_t* meta, float
 // when it has not been allowed as much there before.
 bskv_status allow_smem(const void* kernel, size_t bytes, std::atomic<int> (&allowed)[64], const char* what);
 
+// Checks that the two runs of a block-sparse plan share.
+bskv_status check_blocks_run(const char* who, const bskv_plan* plan, const int32_t* batch_indices,
+                             const int32_t* positions, const int32_t* kv_indptr, const int32_t* kv_indices,
+                             int32_t batch, const int32_t* blocks, const void* float_ws, size_t float_ws_bytes);
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline int32_t meta_word(const bskv_plan* p, int h) { return p->meta[size_t(h)]; }

@@ -411,6 +411,9 @@ void log_plan(const char* name, const bskv_plan* p) {
     case KIND_EVICT:
       kernel = "evict_select_kernel, evict_move_kernel";
       break;
+    case KIND_BLOCKS:
+      kernel = "select_kernel, decode_blocks_kernel (one worker per warp)";
+      break;
     case KIND_MLA:
       kernel = p->mla_variant == MLA_PAGED ? "mla_kernel (rows from the page table)"
                                            : "mla_kernel (sparse rows)";
@@ -878,6 +881,61 @@ extern "C" bskv_status bskv_plan_evict(const int32_t* kv_indptr, const int32_t* 
   return BSKV_OK;
 } catch (const std::exception& e) {
   return host_error("plan_evict", e);
+}
+
+extern "C" bskv_status bskv_plan_decode_blocks(int32_t num_tokens, int32_t max_blocks,
+                                               int32_t num_pages, int32_t page_size,
+                                               int32_t num_qo_heads, int32_t num_kv_heads,
+                                               int32_t head_dim, int32_t top_k, int32_t sink,
+                                               int32_t recent, int32_t dtype, int32_t num_sms,
+                                               bskv_plan** out_plan) try {
+  const char* who = "plan_decode_blocks";
+  if (!out_plan) { set_error("%s: out_plan is NULL", who); return BSKV_ERR_INVALID_ARG; }
+  *out_plan = nullptr;
+  if (bskv_status s = check_cache_shape(who, num_tokens, num_pages, page_size, num_qo_heads,
+                                        num_kv_heads, head_dim, num_sms))
+    return s;
+  if (dtype != BSKV_BF16 && dtype != BSKV_FP16) { set_error("%s: dtype %s unsupported", who, dtype_name(dtype)); return BSKV_ERR_UNSUPPORTED; }
+  const int32_t group = num_qo_heads / num_kv_heads;
+  if (group > 16) { set_error("%s: %d query heads per kv head (max 16)", who, group); return BSKV_ERR_UNSUPPORTED; }
+  if (max_blocks < 1 || top_k < 1 || sink < 0 || recent < 1 || int64_t(sink) + recent > top_k) {
+    set_error("%s: max_blocks=%d top_k=%d sink=%d recent=%d (recent at least 1, sink + recent at most top_k)", who,
+              max_blocks, top_k, sink, recent);
+    return BSKV_ERR_INVALID_ARG;
+  }
+  if (max_blocks > kSelectMaxBlocks) { set_error("%s: %d blocks of a request (max %d)", who, max_blocks, kSelectMaxBlocks); return BSKV_ERR_UNSUPPORTED; }
+  const int64_t rows = int64_t(num_tokens) * num_kv_heads;
+  if (rows > INT32_MAX / 256 || rows * top_k > INT32_MAX / 2 || rows * max_blocks > (int64_t(1) << 36)) {
+    set_error("%s: %d queries of %d kv heads with %d of %d blocks each are too many", who, num_tokens, num_kv_heads, top_k, max_blocks);
+    return BSKV_ERR_UNSUPPORTED;
+  }
+  std::unique_ptr<bskv_plan> owner(new bskv_plan());
+  bskv_plan* p = owner.get();
+  p->kind = KIND_BLOCKS;
+  p->M = num_tokens; p->num_pages = num_pages; p->page_size = page_size;
+  p->num_qo_heads = num_qo_heads; p->num_kv_heads = num_kv_heads; p->head_dim = head_dim;
+  p->dtype = dtype; p->num_sms = num_sms;
+  p->max_blocks = max_blocks; p->top_k = top_k; p->sink = sink; p->recent = recent;
+  // rows are scored in parts while they alone do not fill the GPU
+  const int64_t want = (int64_t(num_sms) * kSelectCtasPerSm + rows - 1) / std::max<int64_t>(rows, 1);
+  p->parts = int32_t(std::max<int64_t>(1, std::min<int64_t>(want, (max_blocks + kSelectMin - 1) / kSelectMin)));
+  // workers of the attention: a warp slot of the GPU each, unless their pieces would be too short
+  const int64_t places = rows * top_k;
+  const int64_t least = std::max<int64_t>(1, kBlocksMinTokens / page_size);
+  const int64_t slots = int64_t(num_sms) * kBlocksWarps;
+  p->per_worker = int32_t(std::max(least, (places + slots - 1) / slots));
+  p->workers = int32_t((places + p->per_worker - 1) / p->per_worker);
+  std::vector<int32_t> none;
+  std::vector<Chunk> no_chunks;
+  assemble(p, KIND_BLOCKS, int32_t(rows), none, no_chunks, 0, none, page_size, nullptr, 0, nullptr, 0,
+           std::min(num_sms, p->workers), 0);
+  p->counter_words = size_t(2 * rows);
+  p->float_ws_bytes = rows > 0 ? blocks_workspace(p).total : 0;
+  *out_plan = owner.release();
+  log_plan("bskv_plan_decode_blocks", p);
+  return BSKV_OK;
+} catch (const std::exception& e) {
+  return host_error("plan_decode_blocks", e);
 }
 
 namespace {

@@ -277,6 +277,24 @@ bskv_status bskv_plan_evict(const int32_t* kv_indptr, const int32_t* kv_indices,
                             int32_t num_kv_heads, int32_t head_dim, int32_t num_sms,
                             bskv_plan** out_plan);
 
+/*
+ * Plan of a block-sparse decode over a paged cache (a block is a page): bskv_run_select_blocks and
+ * bskv_run_decode_blocks. It depends on sizes alone: the requests' lengths, page table and query
+ * positions are device arrays of the runs, so one plan (and one captured graph of its runs) serves a
+ * batch whose requests grow.
+ *   num_tokens: query rows of every run (rows without a token are marked, see the runs);
+ *   max_blocks: most blocks that a query sees, at most 49152; num_pages: pages of the pool.
+ *   Each query and kv head attends to top_k blocks, or all that it sees if these are fewer: the first
+ *   `sink` and the last `recent` that it sees (recent >= 1, sink + recent <= top_k), and the others by
+ *   score.
+ *   Head counts, head_dim, page_size and dtype as for bskv_plan_decode_fp4 (up to 16 query heads per
+ *   kv head).
+ */
+bskv_status bskv_plan_decode_blocks(int32_t num_tokens, int32_t max_blocks, int32_t num_pages,
+                                    int32_t page_size, int32_t num_qo_heads, int32_t num_kv_heads,
+                                    int32_t head_dim, int32_t top_k, int32_t sink, int32_t recent,
+                                    int32_t dtype, int32_t num_sms, bskv_plan** out_plan);
+
 /* Free a plan (NULL is accepted). */
 bskv_status bskv_plan_destroy(bskv_plan* plan);
 
@@ -447,6 +465,49 @@ bskv_status bskv_run_evict_fp4(const bskv_plan* plan, float* scores, const int64
                                int32_t compact_scores, void* kv_codes,
                                const int64_t* codes_strides, void* kv_scales,
                                const int64_t* scales_strides, int32_t* kept, void* stream);
+
+/*
+ * The blocks that each query and kv head attends to, for a plan of bskv_plan_decode_blocks. Query row t is
+ * token positions[t] of request batch_indices[t] and sees the request's blocks 0 .. positions[t] /
+ * page_size. Of a block, with bounds lo and hi, the score is the sum over the query heads r of the kv head's group of
+ *   sum_d max(q[t, r, d] lo_d, q[t, r, d] hi_d),
+ * which no sum of the group's logits with one of the block's keys exceeds (for lo <= hi). Besides the first `sink` and the last
+ * `recent` blocks those of highest score are chosen, as 64-bit arithmetic orders them (NaN as the highest, the lowest
+ * block among equals). Scores have to stay within fp32's range; infinite ones are equal.
+ *   q [num_tokens, num_qo_heads, head_dim], strides {row, head} in multiples of 8 elements; bounds as
+ *     bskv_block_bounds_paged writes them; kv_indptr [batch + 1] and kv_indices on the device.
+ *   blocks [num_tokens, num_kv_heads, top_k] int32 contiguous: the chosen blocks ascending, -1 behind
+ *     the last where the query sees fewer.
+ *   Rows with a negative batch_indices have no token: their part of blocks is left as it was. A row that is out of range,
+ *   or sees more than max_blocks, gets -1 everywhere, a block whose page id is out of range the lowest score; both raise
+ *   BSKV_ERR_DEVICE_INDEX in the device status word.
+ *   float_ws as for bskv_run_decode. Runs of one plan share its workspaces and must not overlap on the GPU.
+ */
+bskv_status bskv_run_select_blocks(
+    const bskv_plan* plan, const void* q, const int64_t* q_strides, const void* bounds,
+    const int64_t* bounds_strides, const int32_t* batch_indices, const int32_t* positions,
+    const int32_t* kv_indptr, const int32_t* kv_indices, int32_t batch, int32_t* blocks,
+    void* float_ws, size_t float_ws_bytes, void* stream);
+
+/*
+ * Decode over chosen blocks, for a plan of bskv_plan_decode_blocks: what bskv_run_decode computes, over
+ * the tokens up to positions[t] that lie in the listed blocks of the row and kv head.
+ *   blocks as bskv_run_select_blocks writes them, or the caller's: the first min(top_k, positions[t] /
+ *     page_size + 1) entries are read, in any order, each block at most once; -1 (any negative) stands
+ *     for no block. A block that the query does not see, or whose page id is out of range, is passed over and
+ *     raises BSKV_ERR_DEVICE_INDEX in the device status word.
+ *   q, out [num_tokens, num_qo_heads, head_dim], strides {row, head} in multiples of 8 elements; kv_cache and kv_strides as
+ *     for bskv_run_decode; lse [num_tokens, num_qo_heads] float32 contiguous, or NULL.
+ *   Rows with a negative batch_indices have no token: their out and lse are left as they were. A row that is out of range
+ *   (raised as above), or that lists no block, gets out = 0 and lse = -inf.
+ *   Deterministic: the same inputs give the same bits.
+ */
+bskv_status bskv_run_decode_blocks(
+    const bskv_plan* plan, const void* q, const int64_t* q_strides, const void* kv_cache,
+    const int64_t* kv_strides, const int32_t* blocks, const int32_t* batch_indices,
+    const int32_t* positions, const int32_t* kv_indptr, const int32_t* kv_indices, int32_t batch,
+    void* out, const int64_t* out_strides, float* lse, float sm_scale, void* float_ws,
+    size_t float_ws_bytes, void* stream);
 
 /*
  * BSR block-sparse attention ([SPARSE] run(q, k, v, out, lse)):
@@ -630,6 +691,80 @@ bskv_status bskv_dequantize_fp4_paged(
     const int32_t* kv_indptr, const int32_t* kv_indices, int32_t batch, int32_t page_size,
     int64_t num_pages, void* k_out, const int64_t* k_strides, void* v_out,
     const int64_t* v_strides, int32_t dtype, int64_t nnz, int32_t num_kv_heads, int32_t head_dim,
+    void* stream);
+
+/*
+ * Page table and token map of a batch, made on the device from the requests' lengths: the index
+ * arrays that the paged appends and the block-sparse runs take.
+ *   seq_lens [batch] int32: tokens of each request, the new ones included; new_lens [batch] int32: how
+ *     many of them are new (the last ones); NULL: one of every request that has any.
+ *   block_table [batch, max_pages] int32, row stride table_stride (elements): each request's page ids.
+ *   free_pages [max_free] int32, free_count [1]: pages to hand out, the last of the first *free_count
+ *     entries first, to the requests in order: page j of a request gets one if no older token lies in it,
+ *     and its entry of block_table is written. *free_left (other memory) takes the number that remains.
+ *     All three NULL: block_table holds every page already.
+ *   Written: kv_indptr and qo_indptr [batch + 1], kv_indices [max_entries >= batch * max_pages] and
+ *     kv_last_page_len [batch], as host plans take them (qo_indptr delimits the new tokens); and for new token i in
+ *     order of request and position batch_indices[i], positions[i] and, unless NULL, slots[i] (int64: page *
+ *     page_size + slot in the page). Rows from the last new token to max_tokens get -1 in all three; kv_indices
+ *     past the last page is left as it was.
+ *   BSKV_ERR_DEVICE_INDEX is raised in the device status word for a request whose lengths are negative, exceed
+ *   max_pages pages or contradict each other (it counts as empty), for a page id outside [0, num_pages) or
+ *   a free list that runs out (the entry, and slots of its tokens, become -1), and for more new tokens
+ *   than max_tokens (those behind are left out).
+ * batch at most 8192; batch * max_pages * page_size below 2^31.
+ */
+bskv_status bskv_build_page_table(
+    const int32_t* seq_lens, const int32_t* new_lens, int32_t batch, int32_t page_size,
+    int32_t* block_table, int64_t table_stride, int32_t max_pages, int32_t num_pages,
+    const int32_t* free_pages, int32_t max_free, const int32_t* free_count, int32_t* free_left,
+    int32_t* kv_indptr, int32_t* kv_indices, int64_t max_entries, int32_t* kv_last_page_len,
+    int32_t* qo_indptr, int32_t* batch_indices, int32_t* positions, int64_t* slots,
+    int64_t max_tokens, void* stream);
+
+/*
+ * Queries and keys normalised per head and rotated, keys and values appended to the paged cache that
+ * bskv_run_decode reads. In fp32, rounded once:
+ *   y = x * w / sqrt(mean(x^2) + eps) over head_dim, with q_weight for q, k_weight for k ([head_dim] of
+ *     dtype, NULL: x itself);
+ *   the first rotary_dim values (a multiple of 16, 0: none) rotate as in bskv_rope_quantize_fp8: is_neox != 0
+ *     pairs i with i + rotary_dim / 2, 0 pairs 2i with 2i + 1; pair i uses cos = cos_sin[at, i] and
+ *     sin = cos_sin[at, rotary_dim / 2 + i], at = pos_ids[row], or positions[row] where pos_ids is NULL. cos_sin
+ *     [max_seq_len, rotary_dim] contiguous, BSKV_FP32 or BSKV_BF16: long-context scaling is in its values.
+ *   q, q_out [nnz, num_qo_heads, head_dim], strides {row, head}; q_out may be q itself. Both NULL: no
+ *     queries. k, v [nnz, num_kv_heads, head_dim] and kv_cache (strides as for bskv_run_decode), all
+ *     NULL: queries only. dtype BSKV_BF16 or BSKV_FP16, head_dim 64 or 128.
+ *   Destination as for bskv_rope_quantize_fp8_append_paged (all int32 on the device). A row with
+ *   batch_indices -1 (any negative) has no token: nothing of it is written. A row whose destination is out of range
+ *   is not appended, one whose rotary position is has no output at all; both raise BSKV_ERR_DEVICE_INDEX
+ *   in the device status word. Rows that share a destination race.
+ */
+bskv_status bskv_norm_rope_append_paged(
+    const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides, const void* v,
+    const int64_t* v_strides, int32_t dtype, int64_t nnz, int32_t num_qo_heads, int32_t num_kv_heads,
+    int32_t head_dim, const void* q_weight, const void* k_weight, float eps, const void* cos_sin,
+    int32_t cos_sin_dtype, int64_t max_seq_len, int32_t rotary_dim, int32_t is_neox,
+    const int32_t* pos_ids, const int32_t* batch_indices, const int32_t* positions,
+    const int32_t* kv_indptr, const int32_t* kv_indices, int32_t batch, int32_t page_size,
+    int64_t num_pages, void* q_out, const int64_t* q_out_strides, void* kv_cache,
+    const int64_t* kv_strides, void* stream);
+
+/*
+ * Bounds of a paged cache's blocks, what bskv_run_select_blocks chooses by: for each page that holds one of
+ * the rows (batch_indices, positions; negative batch_indices: no token) and each kv head, the least and the
+ * greatest value of every key channel over the page's tokens (a NaN makes both NaN). A request's length is that of its
+ * kv_indptr / kv_indices / kv_last_page_len entry (device arrays). Run it after the rows were
+ * appended; a page without a row keeps its bounds.
+ *   kv_cache, kv_strides as for bskv_run_decode, 16-bit; only K is read.
+ *   bounds [num_pages, num_kv_heads, 2, head_dim] in the cache's type, strides {page, kv head} in multiples of 8
+ *     elements, the last two dims contiguous: least values, then greatest.
+ *   A row that is out of range is passed over and raises BSKV_ERR_DEVICE_INDEX in the device status word.
+ */
+bskv_status bskv_block_bounds_paged(
+    const void* kv_cache, const int64_t* kv_strides, int32_t dtype, int32_t num_kv_heads,
+    int32_t head_dim, int32_t page_size, int64_t num_pages, const int32_t* batch_indices,
+    const int32_t* positions, int64_t nnz, const int32_t* kv_indptr, const int32_t* kv_indices,
+    const int32_t* kv_last_page_len, int32_t batch, void* bounds, const int64_t* bounds_strides,
     void* stream);
 
 /*

@@ -23,4 +23,4 @@ balance bounds) rather than by a value printed on the pages, which give no
 partition rule.
 """
 
-from . import numerics, rope, attention, plan_ref, cache  # noqa: F401
+from . import numerics, rope, attention, plan_ref, cache, blocks  # noqa: F401
