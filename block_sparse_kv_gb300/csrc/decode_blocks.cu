@@ -37,7 +37,7 @@ struct BlocksParams {
   float* lse;
   const int32_t *blocks, *batch_indices, *positions, *kv_indptr, *kv_indices;
   float *ws_o, *ws_lse;
-  int* counters;
+  int* counters;   // per row: finished pieces
   int num_rows, top_k, per_worker, workers, places;  // places = num_rows * top_k
   int group, num_qo_heads, batch, num_pages;
   FastDiv heads, page_size, by_top, by_worker;
@@ -78,9 +78,8 @@ struct Walk {
   // the piece
   int row, at, stop;    // entries [at, stop) of the row's list are to come
   int start, pos;       // of the row's request
-  int piece;
+  int piece;            // its number among the row's
   bool fresh;           // no tile of the piece has been given out
-  bool skip;            // a row without a token
   // the window of up to 32 entries: lane i holds entry i's page and its attended tokens
   int page, count;
   uint32_t todo;        // entries that are not given out yet
@@ -96,16 +95,16 @@ struct Walk {
     row = -1;
     while (place < end) {
       int f0;
-      const int r = p.by_top.divmod(place, f0);
-      const int f1 = min(p.top_k, f0 + end - place);
-      const int first = place - f0;  // the row's first place
-      piece = p.by_worker.div(place) - p.by_worker.div(first);
+      const int r = p.by_top.divmod(place, f0), f1 = min(p.top_k, f0 + end - place);
+      piece = p.by_worker.div(place) - p.by_worker.div(place - f0);
       place += f1 - f0;
       int h;
       const int t = p.heads.divmod(r, h);
+      // the window of a full list is read along with the row's request
+      const int ahead = f0 + lane < p.top_k ? __ldg(p.blocks + int64_t(r) * p.top_k + f0 + lane) : -1;
       const int b = __ldg(p.batch_indices + t);
-      if (b < 0) continue;  // a row without a token: nothing is written
       pos = __ldg(p.positions + t);
+      if (b < 0) continue;  // a row without a token: nothing is written
       int n = 0;
       bool bad = b >= p.batch || pos < 0;
       if (!bad) {
@@ -118,19 +117,20 @@ struct Walk {
         n = 0;
       }
       n = min(n, p.top_k);
-      at = int(int64_t(f0) * n / p.top_k);
-      stop = int(int64_t(f1) * n / p.top_k);
+      at = n == p.top_k ? f0 : int(int64_t(f0) * n / p.top_k);
+      stop = n == p.top_k ? f1 : int(int64_t(f1) * n / p.top_k);
       row = r;
       fresh = true;
-      window();
+      window(at == f0, ahead);
       return;
     }
   }
-  __device__ __forceinline__ void window() {
+  // The next 32 entries; `ahead` holds them where `known`.
+  __device__ __forceinline__ void window(bool known = false, int ahead = -1) {
     page = -1;
     count = 0;
     if (at + lane < stop) {
-      const int block = __ldg(p.blocks + int64_t(row) * p.top_k + at + lane);
+      const int block = known ? ahead : __ldg(p.blocks + int64_t(row) * p.top_k + at + lane);
       if (block >= 0) {
         const int seen = p.page_size.div(pos) + 1;
         if (block < seen) {
@@ -418,7 +418,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     T* out = static_cast<T*>(p.out) + t * p.o_s0 + int64_t(h) * p.group * p.o_s1;
     float* lse = p.lse ? p.lse + int64_t(t) * p.num_qo_heads + h * p.group : nullptr;
     const Pieces pieces = pieces_of(p, info.row);
-    if (pieces.first == pieces.last) {
+    const int count = pieces.last - pieces.first + 1;
+    if (count == 1) {
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) {
         const int d = n * 8 + 2 * cq;
@@ -445,7 +446,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       if (r1 < p.group) p.ws_lse[base + r1] = z1;
     }
     __syncwarp();
-    const int count = pieces.last - pieces.first + 1;
     int old = 0;
     if (lane == 0) old = atomic_add_acq_rel(p.counters + info.row, 1);
     if (__shfl_sync(0xffffffffu, old, 0) == count - 1) {
@@ -477,14 +477,14 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 BlocksWorkspace blocks_workspace(const bskv_plan* plan) {
   BlocksWorkspace w{};
-  const size_t rows = size_t(plan->M) * size_t(plan->num_kv_heads), blocks = size_t(plan->max_blocks);
+  const size_t rows = size_t(plan->M) * size_t(plan->num_kv_heads), blocks = (size_t(plan->max_blocks) + 3) & ~size_t(3);
   const size_t group = size_t(plan->num_qo_heads / std::max(1, plan->num_kv_heads));
   const size_t slots = rows + size_t(plan->workers);
-  w.parts = plan->parts;
+  w.stride = int(blocks);
   size_t at = 0;
-  w.exact = at; at += align256(rows * blocks * 8);
-  w.scores = at; at += align256(rows * blocks * 4);
-  w.sums = at; at += align256(rows * size_t(plan->parts) * 4);
+  const size_t slice = std::min(rows, size_t(kSelectSlice) * size_t(plan->num_kv_heads));
+  w.exact = at; at += align256(slice * blocks * 8);
+  w.scores = at; at += align256(slice * blocks * 4);
   w.states = at; at += align256(slots * group * size_t(plan->head_dim) * 4);
   w.lse = at; at += align256(slots * group * 4);
   w.total = at;
@@ -548,7 +548,7 @@ extern "C" bskv_status bskv_run_decode_blocks(
   p.blocks = blocks; p.batch_indices = batch_indices; p.positions = positions; p.kv_indptr = kv_indptr; p.kv_indices = kv_indices;
   p.ws_o = reinterpret_cast<float*>(base + ws.states); p.ws_lse = reinterpret_cast<float*>(base + ws.lse);
   p.num_rows = plan->M * plan->num_kv_heads;
-  p.counters = plan->counters_dev + p.num_rows;  // the selection's come first
+  p.counters = plan->counters_dev + p.num_rows;  // behind the selection's
   p.top_k = plan->top_k; p.per_worker = plan->per_worker; p.workers = plan->workers; p.places = p.num_rows * plan->top_k;
   p.group = plan->num_qo_heads / plan->num_kv_heads; p.num_qo_heads = plan->num_qo_heads;
   p.batch = batch; p.num_pages = plan->num_pages;

@@ -162,14 +162,12 @@ inline bool fp4_page_size(int32_t page_size) {
   return page_size == 8 || (page_size >= 16 && page_size % 16 == 0);
 }
 
-// Block-sparse decode plans. A (query, kv head) row's blocks are scored by up to kSelectParts-many CTAs
-// (a part has at least kSelectMin blocks), all candidates of a row fit the shared memory of the CTA that
-// selects. The attention's workers are warps: the rows' lists of top_k blocks one after another, cut into
+// Block-sparse decode plans. The CTA that selects holds all candidates of a (query, kv head) row in shared
+// memory. The attention's workers are warps: the rows' lists of top_k blocks one after another, cut into
 // equal pieces of at least kBlocksMinTokens tokens.
-constexpr int kSelectThreads = 256;
 constexpr int kSelectMaxBlocks = 49152;
-constexpr int kSelectMin = 64;
-constexpr int kSelectCtasPerSm = 4;
+constexpr int kSelectSlice = 2048;  // queries that are selected for at a time (they share the workspace)
+constexpr int kSelectWide = 2048;   // more blocks than these are selected from by 1024 threads
 constexpr int kBlocksWarps = 8;
 constexpr int kBlocksMinTokens = 64;
 
@@ -229,9 +227,9 @@ struct bskv_plan {
   // request, the most tokens that one keeps, whether the kept rows stay in their pages
   int64_t kept_total = 0;
   int32_t sink = 0, recent = 0, longest = 0, most = 0, in_place = 0;
-  // blocks: M query tokens, top_k blocks of at most max_blocks, sink and recent of them by place; parts
-  // of a row when blocks are scored, list entries of a worker, workers of the attention
-  int32_t max_blocks = 0, parts = 0, per_worker = 0, workers = 0;
+  // blocks: M query tokens, top_k blocks of at most max_blocks, sink and recent of them by place; the
+  // attention's workers and the list places of each
+  int32_t max_blocks = 0, workers = 0, per_worker = 0;
   // set by bskv_plan_upload
   const int32_t* meta_dev = nullptr;
   int32_t* counters_dev = nullptr;  // one merge counter per merge item, zero between runs
@@ -239,11 +237,11 @@ struct bskv_plan {
 
 namespace bskv {
 
-// Where a block-sparse plan's parts of the float workspace begin (bytes): fp64 keys, fp32 scores and sums
+// Where a block-sparse plan's parts of the float workspace begin (bytes): fp64 keys and fp32 scores
 // of the selection, partial states of the attention.
 struct BlocksWorkspace {
-  size_t exact, scores, sums, states, lse, total;
-  int parts;
+  size_t exact, scores, states, lse, total;
+  int stride;  // blocks from one row's scores to the next's
 };
 BlocksWorkspace blocks_workspace(const bskv_plan* plan);
 

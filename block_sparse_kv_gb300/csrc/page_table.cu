@@ -24,7 +24,7 @@ using namespace dev;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxBatch = 8192;  // three sums per request in shared memory: 96 KB
+constexpr int kMaxBatch = 8192;  // five numbers per request in shared memory: 160 KB
 
 struct PageTableParams {
   const int32_t *lens, *news;
@@ -76,6 +76,8 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
   int* pages = sums;
   int* tokens = pages + p.batch + 1;
   int* fresh = tokens + p.batch + 1;
+  int* fresh_from = fresh + p.batch + 1;  // first fresh page, first new token
+  int* first_new = fresh_from + p.batch;
   __shared__ int3 warp_sums[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int free_n = 0;
@@ -93,6 +95,8 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
     pages[b] = r.pages;
     tokens[b] = r.len - r.first_new;
     fresh[b] = r.fresh;
+    fresh_from[b] = r.fresh_from;
+    first_new[b] = r.first_new;
   }
   __syncthreads();
   // each thread adds up a run of requests, the runs' sums are scanned over the CTA
@@ -139,10 +143,10 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
   const int num_entries = pages[p.batch], num_tokens = tokens[p.batch];
 
   // the id of page j of request b: a fresh one from the free list, else the table's; -1: none
-  auto page_id = [&](int b, int j, int fresh_from) {
+  auto page_id = [&](int b, int j) {
     int id;
-    if (j >= fresh_from) {
-      const int at = free_n - 1 - (fresh[b] + j - fresh_from);
+    if (j >= fresh_from[b]) {
+      const int at = free_n - 1 - (fresh[b] + j - fresh_from[b]);
       id = at >= 0 ? __ldg(p.free_pages + at) : -1;
     } else {
       id = p.table[b * p.t_s + j];
@@ -159,9 +163,8 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
       p.kv_indptr[b] = pages[b];
       p.qo_indptr[b] = tokens[b];
       if (b < p.batch) {
-        bool bad;
-        const Lens r = lens_of(p, b, bad);
-        p.kv_last_page_len[b] = r.pages > 0 ? r.len - (r.pages - 1) * int(p.page_size.d) : 0;
+        const int n = pages[b + 1] - pages[b], len = first_new[b] + tokens[b + 1] - tokens[b];
+        p.kv_last_page_len[b] = n > 0 ? len - (n - 1) * int(p.page_size.d) : 0;
       }
     }
     if (tid == 0) {
@@ -172,10 +175,8 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
   const int at = blockIdx.x * kThreads + tid, all = gridDim.x * kThreads;
   for (int e = at; e < num_entries; e += all) {
     const int b = owner(pages, p.batch, e), j = e - pages[b];
-    bool bad;
-    const Lens r = lens_of(p, b, bad);
-    const int id = page_id(b, j, r.fresh_from);
-    if (j >= r.fresh_from) p.table[b * p.t_s + j] = id;
+    const int id = page_id(b, j);
+    if (j >= fresh_from[b]) p.table[b * p.t_s + j] = id;
     p.kv_indices[e] = id;
   }
   // four token rows at a time; rows behind the last token get -1
@@ -183,7 +184,6 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
     int req[4], pos[4];
     int64_t slot[4];
     int b = -1, page = -1, id = -1;
-    Lens r{};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = int(r0) + i;
@@ -192,15 +192,13 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
       if (row >= num_tokens || row >= p.max_tokens) continue;
       if (b < 0 || row >= tokens[b + 1]) {
         b = owner(tokens, p.batch, row);
-        bool bad;
-        r = lens_of(p, b, bad);
         page = -1;
       }
       req[i] = b;
-      pos[i] = r.first_new + row - tokens[b];
+      pos[i] = first_new[b] + row - tokens[b];
       int in_page;
       const int j = p.page_size.divmod(pos[i], in_page);
-      if (j != page) id = page_id(b, page = j, r.fresh_from);
+      if (j != page) id = page_id(b, page = j);
       if (id >= 0) slot[i] = int64_t(id) * p.page_size.d + in_page;
     }
     if (r0 + 4 <= p.max_tokens) {
@@ -281,7 +279,7 @@ extern "C" bskv_status bskv_build_page_table(
   p.kv_indptr = kv_indptr; p.kv_indices = kv_indices; p.kv_last_page_len = kv_last_page_len; p.qo_indptr = qo_indptr;
   p.batch_indices = batch_indices; p.positions = positions; p.slots = slots; p.max_tokens = int(max_tokens);
   if (bskv_status s = status_args(&p.st)) return s;
-  const size_t smem = sizeof(int) * 3 * (size_t(batch) + 1);
+  const size_t smem = sizeof(int) * (5 * size_t(batch) + 3);
   static std::atomic<int> allowed[64];
   if (bskv_status s = allow_smem(reinterpret_cast<const void*>(page_table_kernel), smem, allowed, "build_page_table: cudaFuncSetAttribute"))
     return s;

@@ -412,7 +412,7 @@ void log_plan(const char* name, const bskv_plan* p) {
       kernel = "evict_select_kernel, evict_move_kernel";
       break;
     case KIND_BLOCKS:
-      kernel = "select_kernel, decode_blocks_kernel (one worker per warp)";
+      kernel = "score_kernel, select_kernel, decode_blocks_kernel (one worker per warp)";
       break;
     case KIND_MLA:
       kernel = p->mla_variant == MLA_PAGED ? "mla_kernel (rows from the page table)"
@@ -916,9 +916,6 @@ extern "C" bskv_status bskv_plan_decode_blocks(int32_t num_tokens, int32_t max_b
   p->num_qo_heads = num_qo_heads; p->num_kv_heads = num_kv_heads; p->head_dim = head_dim;
   p->dtype = dtype; p->num_sms = num_sms;
   p->max_blocks = max_blocks; p->top_k = top_k; p->sink = sink; p->recent = recent;
-  // rows are scored in parts while they alone do not fill the GPU
-  const int64_t want = (int64_t(num_sms) * kSelectCtasPerSm + rows - 1) / std::max<int64_t>(rows, 1);
-  p->parts = int32_t(std::max<int64_t>(1, std::min<int64_t>(want, (max_blocks + kSelectMin - 1) / kSelectMin)));
   // workers of the attention: a warp slot of the GPU each, unless their pieces would be too short
   const int64_t places = rows * top_k;
   const int64_t least = std::max<int64_t>(1, kBlocksMinTokens / page_size);

@@ -14,8 +14,8 @@
 //
 // Selection. The first `sink` and the last `recent` blocks that a query sees stay, and of the others the k of
 // highest score, as 64-bit arithmetic would choose them (the lowest index among equals). Scores are summed in
-// fp32 with an error of at most E = (group + 16) 2^-24 max_j sum_d |hi_d P_d| + |lo_d N_d|: coefficients
-// are sums of up to `group` terms, a lane's eight products one chain, five more additions join the lanes.
+// fp32 with an error of at most E = (group + 10) 2^-24 sum_d max_j |hi_jd| P_d + max_j |lo_jd| |N_d|: coefficients
+// are sums of up to `group` terms, a lane's eight products two chains of four, six more additions join them.
 // With s_k the k-th largest fp32 score, blocks above s_k + 2 E are chosen and those below s_k - 2 E are
 // not, whatever the rounding; only the blocks between are scored again, in fp64. Rows where nothing lies
 // between but as many blocks as are still wanted (nearly all) need no second look.
@@ -36,6 +36,7 @@ using namespace dev;
 // ---------------------------------------------------------------------------------------
 
 constexpr int kBoundsThreads = 256;
+constexpr int kBoundsCtas = 2;   // per SM
 constexpr int kBoundsRows = 32;  // most token rows that a CTA looks at
 
 struct BoundsParams {
@@ -65,6 +66,12 @@ struct Pair<__nv_bfloat16> {
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
   }
+  // the larger absolute values, with some sign; a number rather than NaN
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
   static __device__ __forceinline__ float2 values(uint32_t a) {
     return make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
   }
@@ -82,6 +89,11 @@ struct Pair<__half> {
     asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
   }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
   static __device__ __forceinline__ float2 values(uint32_t a) {
     return __half22float2(*reinterpret_cast<const __half2*>(&a));
   }
@@ -92,7 +104,7 @@ struct Pair<__half> {
 // is one of those, and a page that is done twice gets the same bytes. (Bound by reading the keys: rows
 // are D / 8 lanes of 16 bytes, eight of them in flight per lane.)
 template <typename T, int D>
-__global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_constant__ BoundsParams p) {
+__global__ void __launch_bounds__(kBoundsThreads, kBoundsCtas) bounds_kernel(const __grid_constant__ BoundsParams p) {
   constexpr int kLanes = D / 8, kSlots = 32 / kLanes, kAhead = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t first = int64_t(blockIdx.x) * p.rows;
@@ -172,10 +184,12 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_con
 // selection
 // ---------------------------------------------------------------------------------------
 
-constexpr int kThreads = kSelectThreads;
-constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 8;    // loads that a lane has in flight
-constexpr int kFew = 32;     // blocks between the bounds of certainty that are ranked by one warp
+constexpr int kScoreThreads = 256;
+constexpr int kScoreCtas = 2;  // per SM
+constexpr int kScoreStages = 3;
+constexpr int kAhead = 8;      // 16-byte loads of a lane at a time
+constexpr int kBins = 256;
+constexpr int kFew = 64;     // keys that are ranked one against the other
 
 struct SelectParams {
   const void* q;
@@ -184,13 +198,14 @@ struct SelectParams {
   int64_t b_s0, b_s1;  // bytes: page, kv head
   const int32_t *batch_indices, *positions, *kv_indptr, *kv_indices;
   int32_t* blocks;
-  float* scores;               // [rows][max_blocks]
-  float* sums;                 // [rows][parts]: largest sums of absolute products
-  unsigned long long* exact;   // [rows][max_blocks]: keys of fp64 scores
-  int* counters;               // [rows]
-  int group, batch, num_pages, max_blocks, parts, top_k, sink, recent;
-  FastDiv page_size, heads, by_parts;
-  float error;                 // E over the sum of absolute products
+  float* scores;               // [rows][stride]
+  unsigned* most;              // [rows]: bounds of the sums of absolute products, zero between runs
+  unsigned long long* exact;   // [rows][stride]: keys of fp64 scores
+  int group, batch, num_pages, max_blocks, stride, top_k, sink, recent;
+  int queries;
+  int set_heads, sets, head_groups;  // scoring: warps (kv heads) of a set, sets of a CTA, sets' worth of heads
+  FastDiv page_size, heads;
+  float error;                 // E over that bound
   StatusArgs st;
 };
 
@@ -209,126 +224,217 @@ __device__ __forceinline__ unsigned long long order_key(double x) {
   return u >> 63 ? ~u : u | (1ull << 63);
 }
 
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+
 // Sum over the CTA, for every thread; `buf` alternates between calls.
-__device__ __forceinline__ int block_sum(int v, int (&warp_sums)[2][kWarps], int& buf) {
+template <int WARPS>
+__device__ __forceinline__ int block_sum(int v, int (&warp_sums)[2][WARPS], int& buf) {
   v = __reduce_add_sync(0xffffffffu, v);
   int* mine = warp_sums[buf ^= 1];
   if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = v;
   __syncthreads();
-  int s = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) s += mine[w];
-  return s;
+  return __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < WARPS ? mine[threadIdx.x & 31] : 0);
 }
 
 // The coefficients of a lane's eight values of a block's bounds: sums over the group's heads of the
 // queries' negative parts (lo) or positive parts (hi).
-template <typename T, typename F>
-__device__ __forceinline__ void coefficients(const SelectParams& p, int t, int h, int d0, bool upper, F (&c)[8]) {
+template <typename T>
+__device__ __forceinline__ void coefficients(const SelectParams& p, int t, int h, int d0, bool upper, float (&c)[8]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) c[e] = F(0);
+  for (int e = 0; e < 8; ++e) c[e] = 0.f;
   const T* q = static_cast<const T*>(p.q) + t * p.q_s0 + int64_t(h) * p.group * p.q_s1 + d0;
-  for (int g = 0; g < p.group; ++g) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(q + g * p.q_s1));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  constexpr int kHeads = 4;  // loaded at a time
+  for (int g = 0; g < p.group; g += kHeads) {
+    uint4 a[kHeads];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = Pair<T>::values(w[e]);
-      // comparisons that let NaN through
-      c[2 * e] += F(upper ? (f.x < 0.f ? 0.f : f.x) : (f.x > 0.f ? 0.f : f.x));
-      c[2 * e + 1] += F(upper ? (f.y < 0.f ? 0.f : f.y) : (f.y > 0.f ? 0.f : f.y));
+    for (int i = 0; i < kHeads; ++i)
+      a[i] = g + i < p.group ? __ldg(reinterpret_cast<const uint4*>(q + (g + i) * p.q_s1)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const uint32_t w[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = Pair<T>::values(w[e]);
+        // comparisons that let NaN through
+        c[2 * e] += upper ? (f.x < 0.f ? 0.f : f.x) : (f.x > 0.f ? 0.f : f.x);
+        c[2 * e + 1] += upper ? (f.y < 0.f ? 0.f : f.y) : (f.y > 0.f ? 0.f : f.y);
+      }
     }
   }
 }
 
-// One part of a (query, kv head) row's blocks is scored by each of its CTAs; the last one to finish
-// selects.
+// What a query row sees: its blocks n (0: a row that is out of range), and the place of its request's pages.
+struct Row {
+  int n, start;
+};
+__device__ __forceinline__ Row row_of(const SelectParams& p, int b, int pos) {
+  Row r{0, 0};
+  if (b >= p.batch || pos < 0) return r;
+  r.start = __ldg(p.kv_indptr + b);
+  const int end = __ldg(p.kv_indptr + b + 1), n = p.page_size.div(pos) + 1;
+  if (n <= end - r.start && n <= p.max_blocks) r.n = n;
+  return r;
+}
+
+// Scores. A round is kTake candidates of a (query, kv head) row: kAhead 16-byte copies per lane, through a ring of the
+// warp's own. How many rounds a query has is known on the GPU only, so every CTA adds them up for all queries, and
+// each set of up to eight warps, one per kv head, takes an equal run of them: the heads' bounds of a page lie side by
+// side and are read at about the same time. (In parts of a fixed length, which short requests leave empty, the same
+// loop took 46 us for 64 requests of 2048 to 16384 tokens.)
+struct RoundInfo {
+  int row, at, end;  // (query, kv head); candidates [at, end) of it
+  uint32_t bits;     // candidates that have a page; kFirst, kLast: round of the row in this run
+};
+constexpr uint32_t kFirst = 1u << 30, kLast = 1u << 31;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const __grid_constant__ SelectParams p) {
   constexpr int kLanes = D / 4;       // lanes of 16 bytes that hold a block's bounds
-  constexpr int kPer = 32 / kLanes;   // blocks of one load instruction
-  extern __shared__ uint32_t keys[];  // of the row's candidates
-  __shared__ int warp_sums[2][kWarps], part_in[kWarps], part_tie[kWarps];
-  __shared__ float warp_most[kWarps];
-  __shared__ uint32_t warp_lo[kWarps], warp_hi[kWarps];
-  __shared__ int few_at[kFew], few_n, is_last;
-  __shared__ unsigned long long few_key[kFew];
+  constexpr int kPer = 32 / kLanes;   // blocks of one copy instruction
+  constexpr int kTake = kAhead * kPer;
+  constexpr int kWarps = kScoreThreads / 32;
+  extern __shared__ uint4 ring[];
+  __shared__ RoundInfo infos[kWarps][kScoreStages];
+  __shared__ int warp_sums[kWarps], before[kSelectSlice + 1];  // rounds of the queries before each
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int part;
-  const int row = p.by_parts.divmod(blockIdx.x, part);
-  int h;
-  const int t = p.heads.divmod(row, h);
-  const int b = __ldg(p.batch_indices + t);
-  if (b < 0) return;  // a row without a token
-  const int pos = __ldg(p.positions + t);
-  int32_t* out = p.blocks + int64_t(row) * p.top_k;
-  bool bad = b >= p.batch || pos < 0;
-  int start = 0, n = 0;
-  if (!bad) {
-    start = __ldg(p.kv_indptr + b);
-    n = p.page_size.div(pos) + 1;
-    bad = n > __ldg(p.kv_indptr + b + 1) - start || n > p.max_blocks;
-  }
-  if (bad) {
-    if (part == 0 && tid == 0) record_error(p.st, BSKV_ERR_DEVICE_INDEX);
-    n = 0;
-  }
-  const int k = p.top_k - p.sink - p.recent;
-  if (n <= p.top_k || k == 0) {
-    if (part == 0) {
-      for (int j = tid; j < p.top_k; j += kThreads)
-        out[j] = n <= p.top_k ? (j < n ? j : -1) : j < p.sink ? j : n - p.top_k + j;
+  launch_dependents();  // the selection's CTAs wait for all of this kernel
+  // rounds of each query, added up
+  {
+    const int per = (p.queries + kScoreThreads - 1) / kScoreThreads;
+    const int t0 = min(p.queries, tid * per), t1 = min(p.queries, t0 + per);
+    int own = 0;
+    for (int t = t0; t < t1; ++t) {
+      const int b = __ldg(p.batch_indices + t), pos = __ldg(p.positions + t);
+      const int n = b < 0 ? 0 : row_of(p, b, pos).n;
+      before[t] = n > p.top_k ? (n - p.sink - p.recent + kTake - 1) / kTake : 0;
+      own += before[t];
     }
-    return;
+    int v = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    v += __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0) - own;
+    for (int t = t0; t < t1; ++t) {
+      const int x = before[t];
+      before[t] = v;
+      v += x;
+    }
+    if (tid == kScoreThreads - 1) before[p.queries] = v;
+    __syncthreads();
   }
-  const int m = n - p.sink - p.recent;  // candidates, from block `sink` on
-  const int32_t* pages = p.kv_indices + start + p.sink;
-  // parts of whole rounds of the CTA's warps
-  constexpr int kRound = kWarps * kAhead * kPer;
-  const int share = ((m + p.parts - 1) / p.parts + kRound - 1) / kRound * kRound;
-  const int active = (m + share - 1) / share;
-  if (part >= active) return;
-  const int i0 = part * share, i1 = min(m, i0 + share);
-  float* scores = p.scores + int64_t(row) * p.max_blocks;
-  const uint8_t* head = p.bounds + h * p.b_s1;
+  const int per_head = before[p.queries];
+  // this warp's set and kv head; the set's run of the rounds of all groups of heads
+  const int set = blockIdx.x * p.sets + warp / p.set_heads, h_in = warp % p.set_heads;
+  if (warp / p.set_heads >= p.sets) return;
+  const int64_t total = int64_t(per_head) * p.head_groups, all = int64_t(gridDim.x) * p.sets;
+  int64_t todo = total * set / all;
+  const int64_t stop = total * (set + 1) / all;
   const int sub = lane % kLanes, which = lane / kLanes, d0 = 8 * (sub % (D / 8));
   const bool upper = sub >= D / 8;
+  uint4* mine = ring + warp * (kScoreStages * kAhead * 32) + lane;
+
+  // What is copied: candidates [at, end) of query t and head h are this run's, pages from `pages` on.
+  int t = 0, h = 0, at = 0, end = 0, row_end = 0, window = 0, pg = 0, next_pg = 0;
+  uint32_t first = 0;
+  const int32_t* pages = nullptr;
+  const uint8_t* head = nullptr;
+  // lane i: page of candidate at + i (of the last one past the end), page 0 with the top bit where it has none
+  auto page_at = [&](int i) {
+    int x = __ldg(pages + min(i + lane, row_end - 1));
+    if (x < 0 || x >= p.num_pages) {
+      record_error(p.st, BSKV_ERR_DEVICE_INDEX);
+      x = INT32_MIN;
+    }
+    return x;
+  };
+  auto open = [&]() {
+    at = end = 0;
+    while (todo < stop) {
+      const int group = int(todo / per_head), r = int(todo - int64_t(group) * per_head);
+      h = group * p.set_heads + h_in;
+      int lo = 0, hi = p.queries;  // the last query whose rounds begin at or before r
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (before[mid] <= r) lo = mid;
+        else hi = mid;
+      }
+      t = lo;
+      const int from = r - before[t], rounds = int(min(int64_t(before[t + 1] - r), stop - todo));
+      todo += rounds;
+      if (h >= int(p.heads.d)) continue;  // the last group may have fewer heads
+      const Row x = row_of(p, __ldg(p.batch_indices + t), __ldg(p.positions + t));
+      row_end = x.n - p.sink - p.recent;
+      at = from * kTake;
+      end = min(row_end, at + rounds * kTake);
+      pages = p.kv_indices + x.start + p.sink;
+      head = p.bounds + 16 * sub + h * p.b_s1;
+      first = kFirst;
+      window = at;
+      pg = page_at(at);
+      next_pg = page_at(at + 32);
+      return;
+    }
+  };
+  int issued = 0;
+  auto issue = [&]() {
+    if (at < end) {
+      const int stage = issued % kScoreStages;
+      if (at - window == 32) {
+        window = at;
+        pg = next_pg;
+        next_pg = page_at(at + 32);
+      }
+      const int base = at - window;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int from = __shfl_sync(0xffffffffu, pg & INT32_MAX, base + u * kPer + which);
+        cp_async_16(mine + (stage * kAhead + u) * 32, head + from * p.b_s0);
+      }
+      const uint32_t there = (__ballot_sync(0xffffffffu, pg >= 0) >> base) & ((1u << kTake) - 1u);
+      if (lane == 0) infos[warp][stage] = RoundInfo{t * int(p.heads.d) + h, at, min(end, at + kTake), there | first | (at + kTake >= end ? kLast : 0u)};
+      first = 0;
+      at += kTake;
+      ++issued;
+      if (at >= end) open();
+    }
+    cp_async_commit();
+  };
+  open();
+#pragma unroll
+  for (int i = 0; i < kScoreStages - 1; ++i) issue();
 
   float c[8];
-  coefficients<T, float>(p, t, h, d0, upper, c);
-  float most = 0.f;
-  for (int i = i0 + warp * kAhead * kPer; i < i1; i += kRound) {
-    // lane u: page of candidate i + u
-    int pg = -1;
-    if (lane < kAhead * kPer && i + lane < i1) {
-      pg = __ldg(pages + i + lane);
-      if (pg < 0 || pg >= p.num_pages) {
-        record_error(p.st, BSKV_ERR_DEVICE_INDEX);
-        pg = -1;
-      }
-    }
-    uint4 x[kAhead];
+  uint32_t largest[4];
+  for (int consumed = 0; consumed < issued; ++consumed) {
+    __syncwarp();  // the stage that is filled next has been read, and its round is described
+    const int stage = consumed % kScoreStages;
+    const RoundInfo info = infos[warp][stage];
+    issue();
+    if (info.bits & kFirst) {
+      int head_of;
+      const int query = p.heads.divmod(info.row, head_of);
+      coefficients<T>(p, query, head_of, d0, upper, c);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int from = __shfl_sync(0xffffffffu, pg, u * kPer + which);
-      x[u] = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(head + from * p.b_s0 + 16 * sub)) : make_uint4(0, 0, 0, 0);
+      for (int e = 0; e < 4; ++e) largest[e] = 0;
     }
+    cp_async_wait<kScoreStages - 1>();
     float s[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      float a = 0.f;
-      s[u] = 0.f;
+      const uint4 x = mine[(stage * kAhead + u) * 32];
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      float2 two = make_float2(0.f, 0.f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 f = Pair<T>::values(w[e]);
-        s[u] = fmaf(f.x, c[2 * e], s[u]);
-        a = fmaf(fabsf(f.x), fabsf(c[2 * e]), a);
-        s[u] = fmaf(f.y, c[2 * e + 1], s[u]);
-        a = fmaf(fabsf(f.y), fabsf(c[2 * e + 1]), a);
+        two = ffma2(Pair<T>::values(w[e]), make_float2(c[2 * e], c[2 * e + 1]), two);
+        largest[e] = Pair<T>::larger(largest[e], w[e]);
       }
-      // an infinite or NaN score has no rounding
-      most = a < INFINITY ? fmaxf(most, a) : most;
+      s[u] = two.x + two.y;
     }
     // sums over a block's lanes: halving the blocks a lane holds, then the lanes that hold the same
 #pragma unroll
@@ -343,82 +449,164 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
 #pragma unroll
     for (int o = kAhead; o < kLanes; o <<= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
     // lane bits 0, 1, 2 chose among 8, 4, 2 blocks: its block is their reversal
-    const int u = (lane & 1) * 4 + (lane & 2) + ((lane & 4) >> 2);
-    const int at = u * kPer + which;
-    const bool there = __shfl_sync(0xffffffffu, pg, at) >= 0;
-    if (sub < kAhead && i + at < i1) {
-      const float v = there ? s[0] : -INFINITY;
-      if (active == 1) keys[i + at] = order_key(v);
-      else scores[i + at] = v;
+    const int u = (lane & 1) * 4 + (lane & 2) + ((lane & 4) >> 2), i = u * kPer + which;
+    if (sub < kAhead && info.at + i < info.end)
+      p.scores[int64_t(info.row) * p.stride + info.at + i] = info.bits >> i & 1u ? s[0] : -INFINITY;
+    if (info.bits & kLast) {
+      // the bound of the sums of absolute products: infinite if any value is, and then every block is
+      // scored again in fp64
+      float most = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = Pair<T>::values(largest[e]);
+        most = fmaf(fabsf(f.x), fabsf(c[2 * e]), most);
+        most = fmaf(fabsf(f.y), fabsf(c[2 * e + 1]), most);
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) most += __shfl_xor_sync(0xffffffffu, most, o);
+      if (!(most >= 0.f)) most = INFINITY;  // an infinite value times a zero coefficient
+      if (kPer > 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
+      if (lane == 0) atomicMax(p.most + info.row, __float_as_uint(most));  // bits of numbers above zero are in their order
     }
   }
-  // sums of absolute products: over the lanes of the largest
-#pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) most += __shfl_xor_sync(0xffffffffu, most, o);
-  most = kPer == 1 ? most : fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
-  if (lane == 0) warp_most[warp] = most;
-  __syncthreads();
-  most = warp_most[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) most = fmaxf(most, warp_most[w]);
-  if (active > 1) {
-    float* sums = p.sums + int64_t(row) * p.parts;
-    if (tid == 0) {
-      sums[part] = most;
-      const int old = atomic_add_acq_rel(p.counters + row, 1);  // releases what the CTA wrote before the barrier
-      is_last = old == active - 1;
-    }
-    __syncthreads();
-    if (!is_last) return;
-    for (int i = tid; i < m; i += kThreads) keys[i] = order_key(__ldcg(scores + i));
-    for (int i = 0; i < active; ++i) most = fmaxf(most, __ldcg(sums + i));
-    if (tid == 0) p.counters[row] = 0;  // ready for the next run
-    __syncthreads();
-  }
+}
 
-  // kth: the k-th largest key, bit by bit below the bits that all keys share
-  uint32_t lo = 0xffffffffu, hi = 0;
-  for (int i = tid; i < m; i += kThreads) {
-    lo = min(lo, keys[i]);
-    hi = max(hi, keys[i]);
+// Selection: a CTA per (query, kv head) row.
+template <typename T, int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int kLanes = D / 4, kThreads = THREADS, kWarps = THREADS / 32;
+  extern __shared__ __align__(16) uint32_t keys[];  // of the row's candidates, zeros up to a multiple of four
+  __shared__ int warp_sums[2][kWarps], part_in[kWarps], part_tie[kWarps];
+  __shared__ uint32_t warp_lo[kWarps], warp_hi[kWarps];
+  __shared__ int few_at[kFew], few_n, bins[kBins], found_bin, found_n, found_wanted;
+  __shared__ uint32_t found_key;
+  __shared__ unsigned long long few_key[kFew];
+  __shared__ double cd[2 * D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row = blockIdx.x;
+  int h;
+  const int t = p.heads.divmod(row, h);
+  const int b = __ldg(p.batch_indices + t), pos = __ldg(p.positions + t);
+  const Row r = b < 0 ? Row{0, 0} : row_of(p, b, pos);
+  wait_for_prior_grid();
+  if (b < 0) return;  // a row without a token
+  int32_t* out = p.blocks + int64_t(row) * p.top_k;
+  const int n = r.n, k = p.top_k - p.sink - p.recent;
+  if (n == 0 && tid == 0) record_error(p.st, BSKV_ERR_DEVICE_INDEX);
+  if (n <= p.top_k || k == 0) {
+    for (int j = tid; j < p.top_k; j += kThreads)
+      out[j] = n <= p.top_k ? (j < n ? j : -1) : j < p.sink ? j : n - p.top_k + j;
+    return;
   }
+  const int m = n - p.sink - p.recent;  // candidates, from block `sink` on
+  const int32_t* pages = p.kv_indices + r.start + p.sink;
+  const float* scores = p.scores + int64_t(row) * p.stride;
+  const uint8_t* head = p.bounds + h * p.b_s1;
+  const int sub = lane % kLanes;
+  const int fours = (m + 3) >> 2;
+  const float most = __uint_as_float(__ldcg(p.most + row));
+  uint32_t lo = 0xffffffffu, hi = 0;
+  for (int i = tid; i < fours; i += kAhead * kThreads) {
+    float4 v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (i + u * kThreads < fours) v[u] = __ldcg(reinterpret_cast<const float4*>(scores) + i + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int at = 4 * (i + u * kThreads);
+      if (at >= m) continue;
+      const uint4 x = make_uint4(order_key(v[u].x), at + 1 < m ? order_key(v[u].y) : 0u, at + 2 < m ? order_key(v[u].z) : 0u,
+                                 at + 3 < m ? order_key(v[u].w) : 0u);
+      reinterpret_cast<uint4*>(keys)[i + u * kThreads] = x;
+      lo = min(min(lo, x.x - 1u), min(min(x.y - 1u, x.z - 1u), x.w - 1u));  // keys of scores are above zero
+      hi = max(max(hi, x.x), max(max(x.y, x.z), x.w));
+    }
+  }
+  const uint4* keys4 = reinterpret_cast<const uint4*>(keys);
+  // kth: the k-th largest key. Keys are counted in 256 bins over their range, then over the bin that holds
+  // the k-th, until that has few keys, which are ranked.
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) {
     warp_lo[warp] = lo;
     warp_hi[warp] = hi;
   }
+  if (tid < kBins) bins[tid] = 0;
   if (tid == 0) few_n = 0;
   __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, lane < kWarps ? warp_lo[lane] : 0xffffffffu) + 1u;
+  hi = __reduce_max_sync(0xffffffffu, lane < kWarps ? warp_hi[lane] : 0u);
+  if (tid == 0) p.most[row] = 0;  // every thread has read it; ready for the next run
+  int wanted = k;
+  uint32_t kth = hi, span = hi - lo;
+  for (int shift = max(0, 32 - __clz(hi - lo) - 8);; shift = max(0, shift - 8)) {
+    // keys from lo to lo + span by bins
+    auto count = [&](uint32_t x) {
+      if (x >= lo && x - lo <= span) atomicAdd(&bins[(x - lo) >> shift], 1);
+    };
+    for (int i = tid; i < fours; i += kThreads) {
+      const uint4 x = keys4[i];
+      count(x.x);
+      count(x.y);
+      count(x.z);
+      count(x.w);
+    }
+    __syncthreads();
+    // one warp, eight bins a lane: the bins of the lanes before are above
+    if (warp == 0) {
+      int mine[kBins / 32], sum = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    lo = min(lo, warp_lo[w]);
-    hi = max(hi, warp_hi[w]);
+      for (int u = 0; u < kBins / 32; ++u) {
+        const int at = kBins - 1 - (lane * (kBins / 32) + u);
+        sum += mine[u] = bins[at];
+        bins[at] = 0;
+      }
+      int v = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      int before = v - sum;
+      if (before < wanted && wanted <= v) {
+#pragma unroll
+        for (int u = 0; u < kBins / 32; ++u) {
+          if (before < wanted && wanted <= before + mine[u]) {
+            found_bin = kBins - 1 - (lane * (kBins / 32) + u);
+            found_n = mine[u];
+            found_wanted = wanted - before;
+          }
+          before += mine[u];
+        }
+      }
+    }
+    __syncthreads();
+    lo += uint32_t(found_bin) << shift;
+    span = (1u << shift) - 1;
+    wanted = found_wanted;
+    if (shift == 0) {
+      kth = lo;
+      break;
+    }
+    if (found_n <= kFew) {
+      for (int i = tid; i < m; i += kThreads)
+        if (keys[i] >= lo && keys[i] - lo <= span) few_at[atomicAdd(&few_n, 1)] = int(keys[i]);
+      __syncthreads();
+      if (tid < found_n) {
+        const uint32_t x = uint32_t(few_at[tid]);
+        int larger = 0, same = 0;
+        for (int j = 0; j < found_n; ++j) {
+          larger += uint32_t(few_at[j]) > x;
+          same += uint32_t(few_at[j]) == x;
+        }
+        if (larger < wanted && wanted <= larger + same) found_key = x;
+      }
+      __syncthreads();
+      kth = found_key;
+      break;
+    }
   }
   int buf = 0;
-  uint32_t kth = lo;
-  if (lo != hi) {
-    const int top = 31 - __clz(lo ^ hi);
-    kth = hi >> top >> 1 << top << 1;  // two shifts: `top` may be 31
-    for (int bit = top; bit >= 0; --bit) {
-      const uint32_t cand = kth | (1u << bit);
-      int cnt = 0;
-      for (int i = tid; i < m; i += kThreads) cnt += keys[i] >= cand;
-      cnt = block_sum(cnt, warp_sums, buf);
-      if (cnt >= k) kth = cand;
-      if (cnt == k) break;
-    }
-    // exactly k keys from here on: the k-th is the lowest of them
-    uint32_t least = 0xffffffffu;
-    for (int i = tid; i < m; i += kThreads)
-      if (keys[i] >= kth) least = min(least, keys[i]);
-    least = __reduce_min_sync(0xffffffffu, least);
-    if (lane == 0) warp_lo[warp] = least;
-    __syncthreads();
-    kth = warp_lo[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) kth = min(kth, warp_lo[w]);
-  }
   // certain above key_hi, out below key_lo
   uint32_t key_lo = kth, key_hi = kth;
   const float threshold = key_value(kth);
@@ -428,12 +616,14 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     key_lo = order_key(__fadd_rd(threshold, -2.f * err));
   }
   int above = 0, between = 0;
-  for (int i = tid; i < m; i += kThreads) {
-    above += keys[i] > key_hi;
-    between += keys[i] >= key_lo && keys[i] <= key_hi;
+  for (int i = tid; i < fours; i += kThreads) {
+    const uint4 x = keys4[i];
+    above += (x.x > key_hi) + (x.y > key_hi) + (x.z > key_hi) + (x.w > key_hi);
+    between += (x.x >= key_lo) + (x.y >= key_lo) + (x.z >= key_lo) + (x.w >= key_lo);
   }
   above = block_sum(above, warp_sums, buf);
-  between = block_sum(between, warp_sums, buf);
+  if (tid == 0) few_n = 0;
+  between = block_sum(between, warp_sums, buf) - above;
   const int want = k - above;  // of those between
   // Candidates stay whose key is above `sure`, and of those with the key `tie` the first `rest`.
   uint32_t sure = key_hi, tie = key_lo;
@@ -442,9 +632,19 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     sure = key_lo - 1;  // key_lo is above 0: it is the key of a number, or NaN's
     rest = 0;
   } else if (key_lo != key_hi) {
-    // fp64 scores of the blocks between
-    double cd[8];
-    coefficients<T, double>(p, t, h, d0, upper, cd);
+    // fp64 scores of the blocks between, with coefficients that the CTA adds up once: fp64 is slow here
+    for (int i = tid; i < 2 * D; i += kThreads) {
+      const T* q = static_cast<const T*>(p.q) + t * p.q_s0 + int64_t(h) * p.group * p.q_s1 + i % D;
+      double sum = 0.0;
+#pragma unroll 4
+      for (int g = 0; g < p.group; ++g) {
+        const float x = to_float(q[g * p.q_s1]);
+        sum += double(i >= D ? (x < 0.f ? 0.f : x) : (x > 0.f ? 0.f : x));
+      }
+      cd[i] = sum;
+    }
+    __syncthreads();
+    const double* mine = cd + 8 * sub;
     auto score64 = [&](int i) {
       const int pg = __ldg(pages + i);
       double s = -INFINITY;
@@ -455,8 +655,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f = Pair<T>::values(w[e]);
-          s = fma(double(f.x), cd[2 * e], s);
-          s = fma(double(f.y), cd[2 * e + 1], s);
+          s = fma(double(f.x), mine[2 * e], s);
+          s = fma(double(f.y), mine[2 * e + 1], s);
         }
       }
 #pragma unroll
@@ -483,7 +683,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
         keys[few_at[tid]] = rank < want ? 0xffffffffu : 0u;
       }
     } else {
-      unsigned long long* exact = p.exact + int64_t(row) * p.max_blocks;
+      unsigned long long* exact = p.exact + int64_t(row) * p.stride;
       for (int i = warp * 32; i < m; i += kThreads) {
         const uint32_t key = i + lane < m ? keys[i + lane] : 0u;
         for (uint32_t todo = __ballot_sync(0xffffffffu, key >= key_lo && key <= key_hi); todo; todo &= todo - 1) {
@@ -509,13 +709,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     __syncthreads();
   }
 
-  // each warp writes a contiguous run of the candidates: counts, then places
-  const int run = ((m + kWarps - 1) / kWarps + 31) & ~31;
-  const int r0 = min(m, warp * run), r1 = min(m, r0 + run);
+  // each warp writes a contiguous run of the candidates, four of them a lane: counts, then places
+  const int run = ((fours + kWarps - 1) / kWarps + 31) & ~31;
+  const int r0 = min(fours, warp * run), r1 = min(fours, r0 + run);
+  const bool has_ties = rest > 0;
   int in = 0, ties = 0;
   for (int i = r0 + lane; i < r1; i += 32) {
-    in += keys[i] > sure;
-    ties += rest > 0 && keys[i] == tie;
+    const uint4 x = keys4[i];
+    in += (x.x > sure) + (x.y > sure) + (x.z > sure) + (x.w > sure);
+    if (has_ties) ties += (x.x == tie) + (x.y == tie) + (x.z == tie) + (x.w == tie);
   }
   in = __reduce_add_sync(0xffffffffu, in);
   ties = __reduce_add_sync(0xffffffffu, ties);
@@ -532,14 +734,34 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   at += p.sink + min(eq, rest);
   const uint32_t below = (1u << lane) - 1;
   for (int i = r0 + lane; i - lane < r1; i += 32) {
-    const uint32_t key = i < r1 ? keys[i] : 0u;
-    const bool tied = i < r1 && rest > 0 && key == tie;
-    const uint32_t tied_lanes = __ballot_sync(0xffffffffu, tied);
-    const bool stay = (i < r1 && key > sure) || (tied && eq + __popc(tied_lanes & below) < rest);
-    eq += __popc(tied_lanes);
-    const uint32_t staying = __ballot_sync(0xffffffffu, stay);
-    if (stay) out[at + __popc(staying & below)] = p.sink + i;
-    at += __popc(staying);
+    const uint4 x4 = i < r1 ? keys4[i] : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
+    bool stay[4];
+    int rank = eq;  // ties before this lane's
+    if (has_ties) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t lanes = __ballot_sync(0xffffffffu, x[u] == tie);
+        rank += __popc(lanes & below);
+        eq += __popc(lanes);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      stay[u] = x[u] > sure || (has_ties && x[u] == tie && rank < rest);
+      rank += x[u] == tie;
+    }
+    if (!__any_sync(0xffffffffu, stay[0] || stay[1] || stay[2] || stay[3])) continue;
+    int to = at;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t lanes = __ballot_sync(0xffffffffu, stay[u]);
+      to += __popc(lanes & below);
+      at += __popc(lanes);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (stay[u]) out[to++] = p.sink + 4 * i + u;
   }
   for (int j = tid; j < p.sink; j += kThreads) out[j] = j;
   for (int j = tid; j < p.recent; j += kThreads) out[p.top_k - p.recent + j] = n - p.recent + j;
@@ -555,14 +777,56 @@ bskv_status check_bounds(const char* who, const void* bounds, const int64_t* str
   return BSKV_OK;
 }
 
-template <typename T, int D>
-bskv_status launch_select(const SelectParams& p, int64_t rows, cudaStream_t st) {
-  auto kern = select_kernel<T, D>;
+template <typename T, int D, int THREADS>
+bskv_status launch_select(const SelectParams& p, int64_t rows, bool scored, cudaStream_t st) {
+  auto kern = select_kernel<T, D, THREADS>;
   static std::atomic<int> allowed[64];
-  const size_t smem = sizeof(uint32_t) * size_t(p.max_blocks);
+  const size_t smem = sizeof(uint32_t) * size_t(p.stride);
   if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "run_select_blocks: cudaFuncSetAttribute")) return s;
-  kern<<<unsigned(rows * p.parts), kThreads, smem, st>>>(p);
-  return cuda_check(cudaGetLastError(), "run_select_blocks launch");
+  // it may begin while the scores are made, and waits for them
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(rows));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = scored ? 1 : 0;
+  return cuda_check(cudaLaunchKernelEx(&cfg, kern, p), "run_select_blocks launch");
+}
+
+// Slices of at most kSelectSlice queries, one after the other: the scores of all of them share the workspace.
+template <typename T, int D>
+bskv_status launch_both(SelectParams p, int64_t queries, int num_sms, cudaStream_t st) {
+  constexpr int kWarps = kScoreThreads / 32;
+  auto kern = score_kernel<T, D>;
+  static std::atomic<int> allowed[64];
+  constexpr size_t smem = size_t(kWarps) * kScoreStages * kAhead * 32 * sizeof(uint4);
+  if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "run_select_blocks: cudaFuncSetAttribute")) return s;
+  const int heads = int(p.heads.d);
+  p.set_heads = std::min(heads, kWarps);
+  p.sets = kWarps / p.set_heads;
+  p.head_groups = (heads + p.set_heads - 1) / p.set_heads;
+  for (int64_t t0 = 0; t0 < queries; t0 += kSelectSlice) {
+    p.queries = int(std::min<int64_t>(kSelectSlice, queries - t0));
+    const bool scored = p.max_blocks > p.top_k && p.top_k > p.sink + p.recent;  // else there is no choice
+    if (scored) {
+      // rounds that there may be: a set of warps has some of them
+      const int64_t rounds = (int64_t(p.max_blocks) + 7) / 8 * p.queries * p.head_groups;
+      const int grid = int(std::min<int64_t>((rounds + p.sets - 1) / p.sets, int64_t(kScoreCtas) * num_sms));
+      kern<<<unsigned(grid), kScoreThreads, smem, st>>>(p);
+      if (bskv_status s = cuda_check(cudaGetLastError(), "run_select_blocks score launch")) return s;
+    }
+    const int64_t rows = int64_t(p.queries) * heads;
+    if (bskv_status s = p.max_blocks > kSelectWide ? launch_select<T, D, 1024>(p, rows, scored, st) : launch_select<T, D, 256>(p, rows, scored, st)) return s;
+    p.q = static_cast<const T*>(p.q) + kSelectSlice * p.q_s0;
+    p.batch_indices += kSelectSlice;
+    p.positions += kSelectSlice;
+    p.blocks += int64_t(kSelectSlice) * heads * p.top_k;
+  }
+  return BSKV_OK;
 }
 
 }  // namespace
@@ -609,13 +873,9 @@ extern "C" bskv_status bskv_block_bounds_paged(
   if (bskv_status s = status_args(&p.st)) return s;
   const unsigned grid = unsigned((nnz + p.rows - 1) / p.rows);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (head_dim == 128) {
-    if (dtype == BSKV_BF16) bounds_kernel<__nv_bfloat16, 128><<<grid, kBoundsThreads, 0, st>>>(p);
-    else bounds_kernel<__half, 128><<<grid, kBoundsThreads, 0, st>>>(p);
-  } else {
-    if (dtype == BSKV_BF16) bounds_kernel<__nv_bfloat16, 64><<<grid, kBoundsThreads, 0, st>>>(p);
-    else bounds_kernel<__half, 64><<<grid, kBoundsThreads, 0, st>>>(p);
-  }
+  auto kern = head_dim == 128 ? (dtype == BSKV_BF16 ? bounds_kernel<__nv_bfloat16, 128> : bounds_kernel<__half, 128>)
+                              : (dtype == BSKV_BF16 ? bounds_kernel<__nv_bfloat16, 64> : bounds_kernel<__half, 64>);
+  kern<<<grid, kBoundsThreads, 0, st>>>(p);
   return cuda_check(cudaGetLastError(), "block_bounds_paged launch");
 }
 
@@ -632,7 +892,6 @@ extern "C" bskv_status bskv_run_select_blocks(
   for (int i = 0; i < 2; ++i)
     if (q_strides[i] < 0 || q_strides[i] % 8) { set_error("%s: q stride %d (%lld elements) must be a multiple of 16 bytes", who, i, (long long)q_strides[i]); return BSKV_ERR_INVALID_ARG; }
   if (bskv_status s = check_bounds(who, bounds, bounds_strides, plan->head_dim)) return s;
-  const int64_t rows = int64_t(plan->M) * plan->num_kv_heads;
   const BlocksWorkspace ws = blocks_workspace(plan);
   uint8_t* base = static_cast<uint8_t*>(float_ws);
   SelectParams p{};
@@ -642,16 +901,15 @@ extern "C" bskv_status bskv_run_select_blocks(
   p.blocks = blocks;
   p.exact = reinterpret_cast<unsigned long long*>(base + ws.exact);
   p.scores = reinterpret_cast<float*>(base + ws.scores);
-  p.sums = reinterpret_cast<float*>(base + ws.sums);
-  p.counters = plan->counters_dev;
+  p.most = reinterpret_cast<unsigned*>(plan->counters_dev);
   p.group = plan->num_qo_heads / plan->num_kv_heads;
-  p.batch = batch; p.num_pages = plan->num_pages; p.max_blocks = plan->max_blocks; p.parts = ws.parts;
+  p.batch = batch; p.num_pages = plan->num_pages; p.max_blocks = plan->max_blocks; p.stride = ws.stride;
   p.top_k = plan->top_k; p.sink = plan->sink; p.recent = plan->recent;
-  p.page_size = FastDiv(plan->page_size); p.heads = FastDiv(plan->num_kv_heads); p.by_parts = FastDiv(ws.parts);
-  p.error = float((p.group + 16) * 1.01 * std::ldexp(1.0, -24));
+  p.page_size = FastDiv(plan->page_size); p.heads = FastDiv(plan->num_kv_heads);
+  p.error = float((p.group + 10) * 1.01 * std::ldexp(1.0, -24));
   if (bskv_status s = status_args(&p.st)) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (plan->head_dim == 128)
-    return plan->dtype == BSKV_BF16 ? launch_select<__nv_bfloat16, 128>(p, rows, st) : launch_select<__half, 128>(p, rows, st);
-  return plan->dtype == BSKV_BF16 ? launch_select<__nv_bfloat16, 64>(p, rows, st) : launch_select<__half, 64>(p, rows, st);
+    return plan->dtype == BSKV_BF16 ? launch_both<__nv_bfloat16, 128>(p, plan->M, plan->num_sms, st) : launch_both<__half, 128>(p, plan->M, plan->num_sms, st);
+  return plan->dtype == BSKV_BF16 ? launch_both<__nv_bfloat16, 64>(p, plan->M, plan->num_sms, st) : launch_both<__half, 64>(p, plan->M, plan->num_sms, st);
 }
