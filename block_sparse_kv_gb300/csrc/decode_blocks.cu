@@ -5,15 +5,17 @@
 // in one pass with a running maximum and sum.
 //
 // Bound by reading K and V of the listed blocks: a block of one head is a piece of page_size * D 16-bit
-// values, wherever its page lies. One worker is one warp; eight to a CTA and one CTA per SM keep up to
-// 192 KB of copies in flight, each warp in a ring of its own, so that no warp waits for another. The up to 16
-// query heads of a group are the M = 16 rows of mma.sync m16n8k16 against 16 tokens at a time.
+// values, wherever its page lies. One CTA per SM, eight warps with a ring of copies each, up to 192 KB in flight.
+// The up to 16 query heads of a group are the M = 16 rows of mma.sync m16n8k16 against 16 tokens at a time.
 //
-// Split. The lists' lengths are known on the GPU only, so the cut is made in list places: the rows'
-// lists of top_k places follow one another and each worker takes an equal run of them; a worker's run
-// covers the same fraction of a row's actual list (place f of top_k stands for entry f n / top_k of n),
-// so that short lists are cut as evenly as full ones. A row in several pieces leaves partial states in the float
-// workspace, and the warp that finishes its last piece joins them in the same launch, in piece order.
+// Split. The lists' lengths are known on the GPU only, so the cut is made in places: the rows' lists follow
+// one another in steps of 16 tokens (or pages of 8), top_k lists' worth of them per row, and each CTA takes an equal
+// run; a run covers the same fraction of a row's actual list (place f of F stands for step f n / top_k of a list of
+// n blocks), so that short lists are cut as evenly as full ones. The warps of a CTA share each row of its run
+// in equal parts and join their states in shared memory; a row that lies in several CTAs leaves their states in the
+// float workspace, and the CTA that finishes its last piece joins them in the same launch, in piece order.
+// With runs for warps instead of CTAs, which leave eight times as many states there, 64 requests with 64 blocks of 16
+// tokens took 50 us at 4 query heads per kv head and 65 at 16; whole rows to a warp ran at 1.04 of the floor.
 #include <algorithm>
 
 #include "cache_common.cuh"
@@ -38,19 +40,19 @@ struct BlocksParams {
   const int32_t *blocks, *batch_indices, *positions, *kv_indptr, *kv_indices;
   float *ws_o, *ws_lse;
   int* counters;   // per row: finished pieces
-  int num_rows, top_k, per_worker, workers, places;  // places = num_rows * top_k
+  int num_rows, top_k, team, workers, per_worker;
+  int steps, row_places, places;  // steps of a block; places of a row: its steps and what a piece costs; of all rows
   int group, num_qo_heads, batch, num_pages;
-  FastDiv heads, page_size, by_top, by_worker;
+  FastDiv heads, page_size, by_row, by_worker, by_steps;
   float scale_log2;
   StatusArgs st;
 };
 
-template <int D>
+template <int D, int STAGES>
 struct Ring {
-  static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr int kTileBytes = (D / 64) * kPanel;
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kBytes = kStages * kStageBytes;
+  static constexpr int kBytes = STAGES * kStageBytes;
 };
 
 // What the copying side tells the computing side about a stage.
@@ -58,50 +60,51 @@ struct StageInfo {
   int row;      // (query, kv head)
   int valid;    // tokens of its two groups of eight that are attended to: low and high half word
   int flags;    // 1: first tile of a piece, 2: last
-  int piece;    // of the row
 };
 constexpr int kFirst = 1, kLast = 2;
 
-// Pieces of a row: those of the workers from `first` to `last`.
+// Pieces of a row: those of the teams from `first` to `last`.
 struct Pieces {
   int first, last;
 };
 __device__ __forceinline__ Pieces pieces_of(const BlocksParams& p, int row) {
-  return Pieces{p.by_worker.div(row * p.top_k), p.by_worker.div(row * p.top_k + p.top_k - 1)};
+  return Pieces{p.by_worker.div(row * p.row_places), p.by_worker.div(row * p.row_places + p.top_k * p.steps - 1)};
 }
 
-// A worker's way through its places: piece by piece, 32 list entries at a time, one lane each.
+// A warp's way through its share of its team's run: row by row, 32 list entries at a time, one lane each.
 struct Walk {
   const BlocksParams& p;
-  int place, end;       // places that are to come
-  int lane;
-  // the piece
-  int row, at, stop;    // entries [at, stop) of the row's list are to come
+  int place, end;       // the team's places that are to come
+  int member, lane;
+  // the piece: this warp's steps [from, to) of the row's list, entries from `at` on are to come
+  int row, from, to, at;
   int start, pos;       // of the row's request
-  int piece;            // its number among the row's
   bool fresh;           // no tile of the piece has been given out
-  // the window of up to 32 entries: lane i holds entry i's page and its attended tokens
-  int page, count;
+  // the window of up to 32 entries: lane i holds entry i's page and its attended slots [begin, end_slot)
+  int page, begin, end_slot;
   uint32_t todo;        // entries that are not given out yet
   int entry, slot;      // the one being given out, and its next slot
 
-  __device__ __forceinline__ Walk(const BlocksParams& p_, int w, int lane_)
-      : p(p_), place(w * p_.per_worker), end(min(p_.places, place + p_.per_worker)), lane(lane_), todo(0), entry(-1) {
+  __device__ __forceinline__ Walk(const BlocksParams& p_, int worker, int member_, int lane_)
+      : p(p_), place(worker * p_.per_worker), end(min(p_.places, place + p_.per_worker)), member(member_), lane(lane_), todo(0), entry(-1) {
     open();
   }
   __device__ __forceinline__ bool live() const { return row >= 0; }
   // The next piece, if there is one.
   __device__ __forceinline__ void open() {
+    const int full = p.top_k * p.steps;
     row = -1;
     while (place < end) {
       int f0;
-      const int r = p.by_top.divmod(place, f0), f1 = min(p.top_k, f0 + end - place);
-      piece = p.by_worker.div(place) - p.by_worker.div(place - f0);
-      place += f1 - f0;
+      const int r = p.by_row.divmod(place, f0), f1 = min(full, f0 + end - place);
+      place += p.row_places - f0;
+      if (f0 >= full) continue;
       int h;
       const int t = p.heads.divmod(r, h);
       // the window of a full list is read along with the row's request
-      const int ahead = f0 + lane < p.top_k ? __ldg(p.blocks + int64_t(r) * p.top_k + f0 + lane) : -1;
+      from = f0 + (f1 - f0) * member / p.team;
+      const int first = p.by_steps.div(from);
+      const int ahead = first + lane < p.top_k ? __ldg(p.blocks + int64_t(r) * p.top_k + first + lane) : -1;
       const int b = __ldg(p.batch_indices + t);
       pos = __ldg(p.positions + t);
       if (b < 0) continue;  // a row without a token: nothing is written
@@ -113,47 +116,54 @@ struct Walk {
         bad = n > __ldg(p.kv_indptr + b + 1) - start;
       }
       if (bad) {
-        if (lane == 0) record_error(p.st, BSKV_ERR_DEVICE_INDEX);
+        if (lane == 0 && member == 0) record_error(p.st, BSKV_ERR_DEVICE_INDEX);
         n = 0;
       }
-      n = min(n, p.top_k);
-      at = n == p.top_k ? f0 : int(int64_t(f0) * n / p.top_k);
-      stop = n == p.top_k ? f1 : int(int64_t(f1) * n / p.top_k);
+      to = f0 + (f1 - f0) * (member + 1) / p.team;
+      if (n < p.top_k) {
+        const int a = int(int64_t(f0) * n / p.top_k), b1 = int(int64_t(f1) * n / p.top_k);
+        from = a + (b1 - a) * member / p.team;
+        to = a + (b1 - a) * (member + 1) / p.team;
+      }
+      at = p.by_steps.div(from);
       row = r;
       fresh = true;
-      window(at == f0, ahead);
+      window(at == first, ahead);
       return;
     }
   }
   // The next 32 entries; `ahead` holds them where `known`.
   __device__ __forceinline__ void window(bool known = false, int ahead = -1) {
     page = -1;
-    count = 0;
-    if (at + lane < stop) {
-      const int block = known ? ahead : __ldg(p.blocks + int64_t(row) * p.top_k + at + lane);
+    begin = end_slot = 0;
+    const int e = at + lane;
+    if (e * p.steps < to) {
+      const int block = known ? ahead : __ldg(p.blocks + int64_t(row) * p.top_k + e);
       if (block >= 0) {
         const int seen = p.page_size.div(pos) + 1;
         if (block < seen) {
           page = __ldg(p.kv_indices + start + block);
-          count = block < seen - 1 ? int(p.page_size.d) : pos - block * int(p.page_size.d) + 1;
+          begin = max(0, from - e * p.steps) * kTile;
+          end_slot = min(block < seen - 1 ? int(p.page_size.d) : pos - block * int(p.page_size.d) + 1,
+                         p.steps > 1 ? (to - e * p.steps) * kTile : int(p.page_size.d));
         }
         if (page < 0 || page >= p.num_pages) {
           record_error(p.st, BSKV_ERR_DEVICE_INDEX);
-          count = 0;
+          end_slot = 0;
         }
       }
     }
-    at = min(stop, at + 32);
-    todo = __ballot_sync(0xffffffffu, count > 0);
+    at += 32;
+    todo = __ballot_sync(0xffffffffu, begin < end_slot);
   }
   // Moves to an entry that has tokens left; false: the piece has none.
   __device__ __forceinline__ bool seek() {
     if (entry >= 0) return true;
-    while (!todo && at < stop) window();
+    while (!todo && at * p.steps < to) window();
     if (!todo) return false;
     entry = __ffs(todo) - 1;
     todo &= todo - 1;
-    slot = 0;
+    slot = __shfl_sync(0xffffffffu, begin, entry);
     return true;
   }
 };
@@ -241,66 +251,29 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, int v0
   }
 }
 
-// Joins the `count` states of a row from slot `first` on and writes them: a lane covers four values
-// of every (128 / D)-th query head. States without a token (lse -inf) are passed over.
-template <typename T, int D>
-__device__ __forceinline__ void join(const BlocksParams& p, int lane, int first, int count, T* out, float* lse) {
-  constexpr int kHeads = 128 / D, kAhead = 4;
-  const int dl = (lane * 4) % D;
-  for (int g = (lane * 4) / D; g - (lane * 4) / D < p.group; g += kHeads) {
-    float m = -INFINITY, total = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = 0; c0 < count; c0 += kAhead) {
-      float z[kAhead];
-      float4 x[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        z[j] = -INFINITY;
-        if (c0 + j < count && g < p.group) {
-          const int64_t at = int64_t(first + c0 + j) * p.group + g;
-          z[j] = __ldcg(p.ws_lse + at);
-          x[j] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * D + dl));
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (z[j] == -INFINITY) continue;
-        const float mn = fmaxf(m, z[j]);
-        const float sc = m == -INFINITY ? 0.f : expf(m - mn), w = expf(z[j] - mn);
-        total = total * sc + w;
-        acc.x = acc.x * sc + w * x[j].x;
-        acc.y = acc.y * sc + w * x[j].y;
-        acc.z = acc.z * sc + w * x[j].z;
-        acc.w = acc.w * sc + w * x[j].w;
-        // a NaN state makes the sums NaN; the maximum passes over it
-        m = mn;
-      }
-    }
-    if (g < p.group) {
-      const float inv = total == 0.f ? 0.f : 1.f / total;
-      uint32_t* to = reinterpret_cast<uint32_t*>(out + g * p.o_s1 + dl);
-      to[0] = MmaOp<T>::pack(acc.x * inv, acc.y * inv);
-      to[1] = MmaOp<T>::pack(acc.z * inv, acc.w * inv);
-      if (lse && dl == 0) lse[g] = total == 0.f ? -INFINITY : m + logf(total);
-    }
-  }
-}
+// States in shared memory: query head g of warp w has D values at (w * group + g) * D, value d at d ^ 4 (g % 8), so
+// that neither the fragments' stores nor the joining threads' loads meet in a bank more than twice.
+__device__ __forceinline__ int state_at(int row, int g, int d, int D) { return row * D + (d ^ ((g & 7) << 2)); }
 
-template <typename T, int D>
+template <typename T, int D, int STAGES>
 __global__ void __launch_bounds__(kWarps * 32, 1)
     decode_blocks_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ BlocksParams p) {
-  using R = Ring<D>;
+  using R = Ring<D, STAGES>;
   using Mma = MmaOp<T>;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ float top[kWarps][16], sum[kWarps][16];  // of each warp's state
+  __shared__ int finished[kWarps];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* ring = smem + warp * R::kBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * R::kBytes) + warp * R::kStages;
-  StageInfo* infos = reinterpret_cast<StageInfo*>(smem + kWarps * R::kBytes + kWarps * R::kStages * 8) + warp * R::kStages;
-  const int w = warp * gridDim.x + blockIdx.x;  // every SM has one worker before any has two
-  if (w >= p.workers) return;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * R::kBytes) + warp * STAGES;
+  StageInfo* infos = reinterpret_cast<StageInfo*>(smem + kWarps * R::kBytes + kWarps * STAGES * 8) + warp * STAGES;
+  float* states = reinterpret_cast<float*>(smem + kWarps * R::kBytes + kWarps * STAGES * (8 + 16));
+  const int team = warp / p.team, member = warp - team * p.team, first_warp = warp - member, threads = p.team * 32;
+  const int worker = team * gridDim.x + blockIdx.x;  // every SM has one team before any has two
+  if (worker >= p.workers) return;
   if (lane == 0) {
-    for (int s = 0; s < R::kStages; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < STAGES; ++s) mbar_init(&bars[s], 1);
     fence_mbar_init();
     prefetch_tensormap(&kv_map);
   }
@@ -310,22 +283,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int ps = int(p.page_size.d);
 
   // Copies the next tile of the walk into a stage; a piece without tokens is a tile of none.
-  Walk walk(p, w, lane);
+  Walk walk(p, worker, member, lane);
   uint32_t issued = 0;
   auto issue = [&]() {
     if (!walk.live()) return;
-    const int stage = issued % R::kStages;
+    const int stage = issued % STAGES;
     uint8_t* k_to = ring + stage * R::kStageBytes;
     uint8_t* v_to = k_to + R::kTileBytes;
-    StageInfo info{walk.row, 0, walk.fresh ? kFirst : 0, walk.piece};
+    StageInfo info{walk.row, 0, walk.fresh ? kFirst : 0};
     walk.fresh = false;
     int h;
     p.heads.divmod(walk.row, h);
     if (!walk.seek()) {
       if (lane == 0) mbar_arrive(&bars[stage]);
     } else if (ps >= kTile) {
-      const int page = __shfl_sync(0xffffffffu, walk.page, walk.entry), count = __shfl_sync(0xffffffffu, walk.count, walk.entry);
-      const int slot = walk.slot, left = count - slot;
+      const int page = __shfl_sync(0xffffffffu, walk.page, walk.entry), end = __shfl_sync(0xffffffffu, walk.end_slot, walk.entry);
+      const int slot = walk.slot, left = end - slot;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bars[stage], uint32_t(R::kStageBytes));
 #pragma unroll
@@ -336,14 +309,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       }
       info.valid = min(left, 8) | max(0, min(left - 8, 8)) << 16;
       walk.slot += kTile;
-      if (walk.slot >= count) walk.entry = -1;
+      if (walk.slot >= end) walk.entry = -1;
     } else {  // two pages of eight
-      const int page0 = __shfl_sync(0xffffffffu, walk.page, walk.entry), c0 = __shfl_sync(0xffffffffu, walk.count, walk.entry);
+      const int page0 = __shfl_sync(0xffffffffu, walk.page, walk.entry), c0 = __shfl_sync(0xffffffffu, walk.end_slot, walk.entry);
       walk.entry = -1;
       int page1 = -1, c1 = 0;
       if (walk.seek()) {
         page1 = __shfl_sync(0xffffffffu, walk.page, walk.entry);
-        c1 = __shfl_sync(0xffffffffu, walk.count, walk.entry);
+        c1 = __shfl_sync(0xffffffffu, walk.end_slot, walk.entry);
         walk.entry = -1;
       }
       if (lane == 0) {
@@ -367,7 +340,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (lane == 0) infos[stage] = info;
     ++issued;
   };
-  for (int s = 0; s < R::kStages; ++s) issue();
+  for (int s = 0; s < STAGES; ++s) issue();
   __syncwarp();
 
   uint32_t qa[D / 16][4];
@@ -376,8 +349,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int r0 = lane >> 2, r1 = r0 + 8, cq = lane & 3;
   uint32_t consumed = 0;
   bool ok = true;
+  // Every warp of the team goes through the same rows, so they meet at the end of each.
   while (consumed < issued) {
-    const int stage = consumed % R::kStages;
+    const int stage = consumed % STAGES;
     const StageInfo info = infos[stage];
     int h;
     const int t = p.heads.divmod(info.row, h);
@@ -396,79 +370,148 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       m0 = m1 = -INFINITY;
       l0 = l1 = 0.f;
     }
-    if (!warp_wait(&bars[stage], (consumed / R::kStages) & 1u, p.st, forced)) {
-      ok = false;
-      break;
+    if (ok) ok = warp_wait(&bars[stage], (consumed / STAGES) & 1u, p.st, forced);
+    if (ok) {
+      const uint32_t at = smem_u32(ring + stage * R::kStageBytes);
+      if (info.valid) attend_tile<T, D>(at, at + R::kTileBytes, info.valid & 0xffff, info.valid >> 16, p.scale_log2, lane, qa, o, m0, m1, l0, l1);
+      ++consumed;
+      __syncwarp();
+      if (lane == 0) fence_proxy_async_smem();
+      issue();
+      __syncwarp();
     }
-    const uint32_t at = smem_u32(ring + stage * R::kStageBytes);
-    if (info.valid) attend_tile<T, D>(at, at + R::kTileBytes, info.valid & 0xffff, info.valid >> 16, p.scale_log2, lane, qa, o, m0, m1, l0, l1);
-    ++consumed;
-    __syncwarp();
-    if (lane == 0) fence_proxy_async_smem();
-    issue();
-    __syncwarp();
-    if (!(info.flags & kLast)) continue;
+    if (ok && !(info.flags & kLast)) continue;
 
+    // this warp's state, relative to its own maximum
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
-    const float z0 = l0 == 0.f ? -INFINITY : (m0 + __log2f(l0)) * kLn2, z1 = l1 == 0.f ? -INFINITY : (m1 + __log2f(l1)) * kLn2;
-    T* out = static_cast<T*>(p.out) + t * p.o_s0 + int64_t(h) * p.group * p.o_s1;
-    float* lse = p.lse ? p.lse + int64_t(t) * p.num_qo_heads + h * p.group : nullptr;
+    if (r0 < p.group) {
+      if (cq == 0) {
+        top[warp][r0] = m0;
+        sum[warp][r0] = l0;
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2*>(states + state_at(warp * p.group + r0, r0, n * 8 + 2 * cq, D)) = make_float2(o[n][0], o[n][1]);
+    }
+    if (r1 < p.group) {
+      if (cq == 0) {
+        top[warp][r1] = m1;
+        sum[warp][r1] = l1;
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2*>(states + state_at(warp * p.group + r1, r1, n * 8 + 2 * cq, D)) = make_float2(o[n][2], o[n][3]);
+    }
+    // a warp whose wait gave up comes here too, wherever it was, and all leave together
+    if (!bar_and(1 + team, threads, ok)) {
+      ok = false;
+      break;
+    }
     const Pieces pieces = pieces_of(p, info.row);
     const int count = pieces.last - pieces.first + 1;
-    if (count == 1) {
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        const int d = n * 8 + 2 * cq;
-        if (r0 < p.group) *reinterpret_cast<uint32_t*>(out + r0 * p.o_s1 + d) = Mma::pack(o[n][0] * inv0, o[n][1] * inv0);
-        if (r1 < p.group) *reinterpret_cast<uint32_t*>(out + r1 * p.o_s1 + d) = Mma::pack(o[n][2] * inv1, o[n][3] * inv1);
+    T* out = static_cast<T*>(p.out) + t * p.o_s0 + int64_t(h) * p.group * p.o_s1;
+    float* lse = p.lse ? p.lse + int64_t(t) * p.num_qo_heads + h * p.group : nullptr;
+    // a row's slots follow one another: teams before it and rows before it have had one each
+    const int64_t slot0 = pieces.first + info.row;
+    const int64_t base = (slot0 + (worker - pieces.first)) * p.group;
+    for (int i = tid - 32 * first_warp; i < p.group * (D / 4); i += threads) {
+      const int g = i / (D / 4), d = i % (D / 4) * 4;
+      float m = -INFINITY, total = 0.f;
+      for (int w = first_warp; w < first_warp + p.team; ++w) m = fmaxf(m, top[w][g]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int w = first_warp; w < first_warp + p.team; ++w) {
+        const float l = sum[w][g];
+        if (l == 0.f) continue;  // no token
+        const float f = fast_exp2(top[w][g] - m);
+        const float4 x = *reinterpret_cast<const float4*>(states + state_at(w * p.group + g, g, d, D));
+        total = fmaf(f, l, total);
+        acc.x = fmaf(f, x.x, acc.x);
+        acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z);
+        acc.w = fmaf(f, x.w, acc.w);
       }
-      if (lse && cq == 0) {
-        if (r0 < p.group) lse[r0] = z0;
-        if (r1 < p.group) lse[r1] = z1;
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      const float z = total == 0.f ? -INFINITY : (m + __log2f(total)) * kLn2;
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      if (count == 1) {
+        *reinterpret_cast<uint2*>(out + g * p.o_s1 + d) = make_uint2(Mma::pack(acc.x, acc.y), Mma::pack(acc.z, acc.w));
+        if (lse && d == 0) lse[g] = z;
+      } else {
+        *reinterpret_cast<float4*>(p.ws_o + (base + g) * D + d) = acc;
+        if (d == 0) p.ws_lse[base + g] = z;
       }
-      continue;
     }
-    // a row's slots follow one another: workers before it and rows before it have had one each
-    const int slot0 = pieces.first + info.row;
-    const int64_t base = int64_t(slot0 + info.piece) * p.group;
+    bar_and(1 + team, threads, true);  // the states are read, what was written is ordered before the count
+    if (count == 1) continue;
+    if (member == 0 && lane == 0) finished[team] = atomic_add_acq_rel(p.counters + info.row, 1);
+    bar_and(1 + team, threads, true);
+    if (finished[team] != count - 1) continue;
+    // the row's last piece: joins the states of all of them, in their order; those without a token (lse
+    // -inf) are passed over
+    for (int i = tid - 32 * first_warp; i < p.group * (D / 4); i += threads) {
+      const int g = i / (D / 4), d = i % (D / 4) * 4;
+      constexpr int kAhead = 4;
+      float m = -INFINITY, total = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c0 = 0; c0 < count; c0 += kAhead) {
+        float z[kAhead];
+        float4 x[kAhead];
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-      const int d = n * 8 + 2 * cq;
-      if (r0 < p.group) *reinterpret_cast<float2*>(p.ws_o + (base + r0) * D + d) = make_float2(o[n][0] * inv0, o[n][1] * inv0);
-      if (r1 < p.group) *reinterpret_cast<float2*>(p.ws_o + (base + r1) * D + d) = make_float2(o[n][2] * inv1, o[n][3] * inv1);
+        for (int j = 0; j < kAhead; ++j) {
+          z[j] = -INFINITY;
+          if (c0 + j < count) {
+            const int64_t from = (slot0 + c0 + j) * p.group + g;
+            z[j] = __ldcg(p.ws_lse + from);
+            x[j] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + from * D + d));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          if (z[j] == -INFINITY) continue;
+          const float mn = fmaxf(m, z[j]);
+          const float sc = m == -INFINITY ? 0.f : expf(m - mn), f = expf(z[j] - mn);
+          total = total * sc + f;
+          acc.x = acc.x * sc + f * x[j].x;
+          acc.y = acc.y * sc + f * x[j].y;
+          acc.z = acc.z * sc + f * x[j].z;
+          acc.w = acc.w * sc + f * x[j].w;
+          m = mn;
+        }
+      }
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      *reinterpret_cast<uint2*>(out + g * p.o_s1 + d) = make_uint2(Mma::pack(acc.x * inv, acc.y * inv), Mma::pack(acc.z * inv, acc.w * inv));
+      if (lse && d == 0) lse[g] = total == 0.f ? -INFINITY : m + logf(total);
     }
-    if (cq == 0) {
-      if (r0 < p.group) p.ws_lse[base + r0] = z0;
-      if (r1 < p.group) p.ws_lse[base + r1] = z1;
-    }
-    __syncwarp();
-    int old = 0;
-    if (lane == 0) old = atomic_add_acq_rel(p.counters + info.row, 1);
-    if (__shfl_sync(0xffffffffu, old, 0) == count - 1) {
-      join<T, D>(p, lane, slot0, count, out, lse);
-      if (lane == 0) p.counters[info.row] = 0;  // ready for the next run
-    }
-    __syncwarp();
+    if (member == 0 && lane == 0) p.counters[info.row] = 0;  // ready for the next run
   }
   if (!ok) {
     // the copies in flight land before the warp leaves (bounded, not forcible)
-    for (uint32_t s = consumed; s < issued; ++s) mbar_wait(&bars[s % R::kStages], (s / R::kStages) & 1u, p.st, false);
+    for (uint32_t s = consumed; s < issued; ++s) mbar_wait(&bars[s % STAGES], (s / STAGES) & 1u, p.st, false);
   }
 }
 
-template <typename T, int D>
-bskv_status launch(const CUtensorMap& map, const BlocksParams& p, int num_sms, cudaStream_t st) {
-  using R = Ring<D>;
-  auto kern = decode_blocks_kernel<T, D>;
-  constexpr size_t smem = 1024 + kWarps * (R::kBytes + R::kStages * (8 + sizeof(StageInfo)));
+template <typename T, int D, int STAGES>
+bskv_status launch(const CUtensorMap& map, const BlocksParams& p, int grid, cudaStream_t st) {
+  using R = Ring<D, STAGES>;
+  auto kern = decode_blocks_kernel<T, D, STAGES>;
+  static_assert(sizeof(StageInfo) <= 16, "stage infos");
+  const size_t smem = 1024 + kWarps * (R::kBytes + STAGES * (8 + 16)) + size_t(kWarps) * p.group * D * 4;
   static std::atomic<int> allowed[64];
   if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "run_decode_blocks: cudaFuncSetAttribute")) return s;
-  kern<<<unsigned(std::min(num_sms, p.workers)), kWarps * 32, smem, st>>>(map, p);
+  kern<<<unsigned(grid), kWarps * 32, smem, st>>>(map, p);
   return cuda_check(cudaGetLastError(), "run_decode_blocks launch");
+}
+
+// Stages by what shared memory holds beside the warps' states: with more than eight query heads of 128
+// dims these take 64 KB.
+template <typename T>
+bskv_status launch_any(const CUtensorMap& map, const BlocksParams& p, int D, int grid, cudaStream_t st) {
+  if (D == 64) return launch<T, 64, 5>(map, p, grid, st);
+  return p.group <= 8 ? launch<T, 128, 3>(map, p, grid, st) : launch<T, 128, 2>(map, p, grid, st);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -549,11 +592,12 @@ extern "C" bskv_status bskv_run_decode_blocks(
   p.ws_o = reinterpret_cast<float*>(base + ws.states); p.ws_lse = reinterpret_cast<float*>(base + ws.lse);
   p.num_rows = plan->M * plan->num_kv_heads;
   p.counters = plan->counters_dev + p.num_rows;  // behind the selection's
-  p.top_k = plan->top_k; p.per_worker = plan->per_worker; p.workers = plan->workers; p.places = p.num_rows * plan->top_k;
+  p.top_k = plan->top_k; p.team = plan->team; p.workers = plan->workers; p.per_worker = plan->per_worker;
+  p.steps = plan->steps; p.row_places = plan->row_places; p.places = p.num_rows * plan->row_places;
   p.group = plan->num_qo_heads / plan->num_kv_heads; p.num_qo_heads = plan->num_qo_heads;
   p.batch = batch; p.num_pages = plan->num_pages;
   p.heads = FastDiv(plan->num_kv_heads); p.page_size = FastDiv(plan->page_size);
-  p.by_top = FastDiv(plan->top_k); p.by_worker = FastDiv(plan->per_worker);
+  p.by_row = FastDiv(plan->row_places); p.by_worker = FastDiv(plan->per_worker); p.by_steps = FastDiv(plan->steps);
   p.scale_log2 = sm_scale_log2(sm_scale, plan->head_dim);
   if (bskv_status s = status_args(&p.st)) return s;
   const int ps = plan->page_size, D = plan->head_dim;
@@ -565,6 +609,6 @@ extern "C" bskv_status bskv_run_decode_blocks(
                                    5, kv_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (D == 128) return plan->dtype == BSKV_BF16 ? launch<__nv_bfloat16, 128>(map, p, plan->num_sms, st) : launch<__half, 128>(map, p, plan->num_sms, st);
-  return plan->dtype == BSKV_BF16 ? launch<__nv_bfloat16, 64>(map, p, plan->num_sms, st) : launch<__half, 64>(map, p, plan->num_sms, st);
+  const int grid = std::min(plan->num_sms, plan->workers);
+  return plan->dtype == BSKV_BF16 ? launch_any<__nv_bfloat16>(map, p, D, grid, st) : launch_any<__half>(map, p, D, grid, st);
 }

@@ -163,13 +163,21 @@ inline bool fp4_page_size(int32_t page_size) {
 }
 
 // Block-sparse decode plans. The CTA that selects holds all candidates of a (query, kv head) row in shared
-// memory. The attention's workers are warps: the rows' lists of top_k blocks one after another, cut into
-// equal pieces of at least kBlocksMinTokens tokens.
+// memory. The attention's workers are teams of warps: the rows' lists of top_k
+// blocks, in steps of 16 tokens, one after another, cut into equal runs.
 constexpr int kSelectMaxBlocks = 49152;
 constexpr int kSelectSlice = 2048;  // queries that are selected for at a time (they share the workspace)
 constexpr int kSelectWide = 2048;   // more blocks than these are selected from by 1024 threads
 constexpr int kBlocksWarps = 8;
-constexpr int kBlocksMinTokens = 64;
+constexpr int kBlocksMinSteps = 2;  // per warp of a worker
+constexpr int kBlocksRowSteps = 2;  // what another row costs a worker, per warp
+// Warps that share a row's list of `tiles` tiles of 16 tokens (1, 2, 4 or 8, a team): as many as leave no SM
+// without a row, and more while each of them has 32 tiles of 128 dims.
+inline int32_t blocks_team(int64_t rows, int64_t tiles, int32_t head_dim, int32_t num_sms) {
+  int32_t team = 1;
+  while (team < kBlocksWarps && (16 * rows * team < 15 * int64_t(num_sms) * kBlocksWarps || tiles * head_dim >= 32 * 128 * team)) team *= 2;
+  return team;
+}
 
 // Byte offset in the int workspace of the merge counters (after the metadata).
 inline size_t merge_counter_offset(size_t meta_words) { return ((meta_words * 4 + 255) / 256) * 256; }
@@ -228,8 +236,9 @@ struct bskv_plan {
   int64_t kept_total = 0;
   int32_t sink = 0, recent = 0, longest = 0, most = 0, in_place = 0;
   // blocks: M query tokens, top_k blocks of at most max_blocks, sink and recent of them by place; the
-  // attention's workers and the list places of each
-  int32_t max_blocks = 0, workers = 0, per_worker = 0;
+  // warps of one of the
+  // attention's workers, workers and the places of each, steps of a block, places of a row
+  int32_t max_blocks = 0, team = 0, workers = 0, per_worker = 0, steps = 0, row_places = 0;
   // set by bskv_plan_upload
   const int32_t* meta_dev = nullptr;
   int32_t* counters_dev = nullptr;  // one merge counter per merge item, zero between runs
