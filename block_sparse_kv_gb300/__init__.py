@@ -1121,16 +1121,40 @@ def bskv_run_evict_fp4(plan, scores, kv_codes, kv_scales, kept=None, compact_sco
 class PageTable:
     """The index arrays of a batch as bskv_build_page_table writes them: kv_indptr and qo_indptr [B + 1],
     kv_indices, kv_last_page_len [B] and, per new token, batch_indices, positions (int32) and slots
-    (int64); free_left [1] where pages were handed out of a free list, else None."""
+    (int64, or None); free_left [1] where pages are handed out of a free list, else None. The tensors are
+    checked here, once, and must not be resized."""
 
     __slots__ = ("kv_indptr", "kv_indices", "kv_last_page_len", "qo_indptr", "batch_indices", "positions",
-                 "slots", "free_left")
+                 "slots", "free_left", "_device", "_batch", "_entries", "_pointers")
 
-    def __init__(self, kv_indptr, kv_indices, kv_last_page_len, qo_indptr, batch_indices, positions, slots,
+    def __init__(self, kv_indptr, kv_indices, kv_last_page_len, qo_indptr, batch_indices, positions, slots=None,
                  free_left=None):
+        fn = "PageTable"
+        dev = _cuda_of(fn, "kv_indptr", kv_indptr)
+        _list_of(fn, "kv_indptr", kv_indptr, None, dev)
+        batch = kv_indptr.numel() - 1
+        if batch < 0:
+            raise ValueError("%s: kv_indptr is empty" % fn)
+        _list_of(fn, "batch_indices", batch_indices, None, dev)
+        rows = batch_indices.numel()
+        for name, t, n in (("kv_indices", kv_indices, None), ("kv_last_page_len", kv_last_page_len, batch),
+                           ("qo_indptr", qo_indptr, batch + 1), ("positions", positions, rows)):
+            _list_of(fn, name, t, n, dev)
+        if slots is not None:
+            _list_of(fn, "slots", slots, rows, dev, _I64T)
+        if free_left is not None:
+            _list_of(fn, "free_left", free_left, 1, dev)
+        self._device, self._batch, self._entries = dev, batch, kv_indices.numel()
+        self._pointers = (kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_indices.numel(), kv_last_page_len.data_ptr(),
+                          qo_indptr.data_ptr(), batch_indices.data_ptr(), positions.data_ptr(), _ptr(slots), rows)
         self.kv_indptr, self.kv_indices, self.kv_last_page_len = kv_indptr, kv_indices, kv_last_page_len
         self.qo_indptr, self.batch_indices, self.positions = qo_indptr, batch_indices, positions
         self.slots, self.free_left = slots, free_left
+
+    def __setattr__(self, name, value):
+        if hasattr(self, name):
+            raise AttributeError("PageTable: %s cannot be replaced; make another PageTable" % name)
+        object.__setattr__(self, name, value)
 
 
 _I64T = (torch.int64,)
@@ -1141,8 +1165,7 @@ def _list_of(fn, name, t, n, device, dtypes=_I32T):
     _dense(fn, (name, t))
 
 
-def _check_page_table(fn, _, seq_lens, block_table, new_lens, free_pages, free_count, kv_indptr,
-                      kv_indices, kv_last_page_len, qo_indptr, batch_indices, positions, slots, free_left):
+def _check_page_table(fn, _, seq_lens, block_table, new_lens, free_pages, free_count):
     dev = _cuda_of(fn, "seq_lens", seq_lens)
     _list_of(fn, "seq_lens", seq_lens, None, dev)
     batch = seq_lens.numel()
@@ -1155,21 +1178,8 @@ def _check_page_table(fn, _, seq_lens, block_table, new_lens, free_pages, free_c
     if free_pages is not None:
         _list_of(fn, "free_pages", free_pages, None, dev)
         _list_of(fn, "free_count", free_count, 1, dev)
-        if kv_indptr is not None:
-            _list_of(fn, "out.free_left", free_left, 1, dev)
-    if kv_indptr is not None:
-        most = batch * block_table.shape[1]
-        for name, t, n in (("kv_indptr", kv_indptr, batch + 1), ("kv_indices", kv_indices, None),
-                           ("kv_last_page_len", kv_last_page_len, batch), ("qo_indptr", qo_indptr, batch + 1),
-                           ("batch_indices", batch_indices, None)):
-            _list_of(fn, "out." + name, t, n, dev)
-        if kv_indices.numel() < most:
-            raise ValueError("%s: out.kv_indices has %d entries, %d requests may have %d pages"
-                             % (fn, kv_indices.numel(), batch, most))
-        _list_of(fn, "out.positions", positions, batch_indices.numel(), dev)
-        if slots is not None:
-            _list_of(fn, "out.slots", slots, batch_indices.numel(), dev, _I64T)
-    return dev, batch, block_table.shape[1], _strides_of(block_table, 1)[0]
+    return (dev, batch, block_table.shape[1], _strides_of(block_table, 1)[0],
+            0 if free_pages is None else free_pages.numel())
 
 
 def bskv_build_page_table(seq_lens, block_table, page_size, num_pages, new_lens=None, free_pages=None,
@@ -1180,13 +1190,9 @@ def bskv_build_page_table(seq_lens, block_table, page_size, num_pages, new_lens=
     block_table. The PageTable has room for max_tokens new tokens (None: B, and new_lens must be None);
     rows without one are -1. `out` is an earlier PageTable to write into (its room is what counts then)."""
     fn = "bskv_build_page_table"
+    dev, batch, max_pages, stride, most_free = _once(_call_layouts, _check_page_table, fn, None, seq_lens,
+                                                     block_table, new_lens, free_pages, free_count)
     o = out
-    if o is not None and not isinstance(o, PageTable):
-        raise TypeError("%s: out must be a PageTable" % fn)
-    arrays = (None,) * 8 if o is None else (o.kv_indptr, o.kv_indices, o.kv_last_page_len, o.qo_indptr,
-                                            o.batch_indices, o.positions, o.slots, o.free_left)
-    dev, batch, max_pages, stride = _once(_call_layouts, _check_page_table, fn, None, seq_lens, block_table,
-                                          new_lens, free_pages, free_count, *arrays)
     if o is None:
         if max_tokens is None:
             if new_lens is not None:
@@ -1201,11 +1207,17 @@ def bskv_build_page_table(seq_lens, block_table, page_size, num_pages, new_lens=
         o = PageTable(ints(batch + 1), ints(batch * max_pages), ints(batch), ints(batch + 1), ints(int(max_tokens)),
                       ints(int(max_tokens)), ints(int(max_tokens), torch.int64),
                       None if free_pages is None else ints(1))
+    elif not isinstance(o, PageTable):
+        raise TypeError("%s: out must be a PageTable" % fn)
+    elif o._device != dev or o._batch != batch or o._entries < batch * max_pages:
+        raise ValueError("%s: out is for %d requests and %d pages on %s; needed are %d, up to %d and %s"
+                         % (fn, o._batch, o._entries, o._device, batch, batch * max_pages, dev))
+    elif free_pages is not None and o.free_left is None:
+        raise ValueError("%s: free_pages need a PageTable with free_left" % fn)
+    free = (None, 0, None, None) if free_pages is None else (free_pages.data_ptr(), most_free, free_count.data_ptr(),
+                                                             o.free_left.data_ptr())
     _call(fn, dev, seq_lens.data_ptr(), _ptr(new_lens), batch, int(page_size), block_table.data_ptr(), stride,
-          max_pages, int(num_pages), _ptr(free_pages), 0 if free_pages is None else free_pages.numel(),
-          _ptr(free_count), None if free_pages is None else o.free_left.data_ptr(), o.kv_indptr.data_ptr(),
-          o.kv_indices.data_ptr(), o.kv_indices.numel(), o.kv_last_page_len.data_ptr(), o.qo_indptr.data_ptr(),
-          o.batch_indices.data_ptr(), o.positions.data_ptr(), _ptr(o.slots), o.batch_indices.numel())
+          max_pages, int(num_pages), *free, *o._pointers)
     return o
 
 

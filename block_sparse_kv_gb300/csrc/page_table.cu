@@ -172,21 +172,14 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
       if (num_tokens > p.max_tokens) record_error(p.st, BSKV_ERR_DEVICE_INDEX);
     }
   }
-  const int at = blockIdx.x * kThreads + tid, all = gridDim.x * kThreads;
-  for (int e = at; e < num_entries; e += all) {
-    const int b = owner(pages, p.batch, e), j = e - pages[b];
-    const int id = page_id(b, j);
-    if (j >= fresh_from[b]) p.table[b * p.t_s + j] = id;
-    p.kv_indices[e] = id;
-  }
-  // four token rows at a time; rows behind the last token get -1
-  for (int64_t r0 = int64_t(at) * 4; r0 < p.max_tokens; r0 += int64_t(all) * 4) {
+  // rows r0 .. r0 + 3 of the token map
+  auto write_rows = [&](int r0) {
     int req[4], pos[4];
     int64_t slot[4];
     int b = -1, page = -1, id = -1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = int(r0) + i;
+      const int row = r0 + i;
       req[i] = pos[i] = -1;
       slot[i] = -1;
       if (row >= num_tokens || row >= p.max_tokens) continue;
@@ -215,6 +208,19 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
         if (p.slots) p.slots[r0 + i] = i == 0 ? slot[0] : i == 1 ? slot[1] : slot[2];
       }
     }
+  };
+  // four token rows to a thread, or one page entry; rows behind the last token get -1
+  const int at = blockIdx.x * kThreads + tid, all = gridDim.x * kThreads, row_items = (p.max_tokens + 3) >> 2;
+  for (int64_t item = at; item < int64_t(row_items) + num_entries; item += all) {
+    if (item < row_items) {
+      write_rows(int(item) * 4);
+      continue;
+    }
+    const int e = int(item - row_items);
+    const int b = owner(pages, p.batch, e), j = e - pages[b];
+    const int id = page_id(b, j);
+    if (j >= fresh_from[b]) p.table[b * p.t_s + j] = id;
+    p.kv_indices[e] = id;
   }
 }
 
@@ -283,9 +289,8 @@ extern "C" bskv_status bskv_build_page_table(
   static std::atomic<int> allowed[64];
   if (bskv_status s = allow_smem(reinterpret_cast<const void*>(page_table_kernel), smem, allowed, "build_page_table: cudaFuncSetAttribute"))
     return s;
-  // A thread for every two page entries that there may be and for every four rows, on at most two CTAs
-  // per SM of the GPU.
-  const int64_t threads = std::max<int64_t>({int64_t(batch) * max_pages / 2, (max_tokens + 3) / 4, 1});
+  // A thread for every page entry that there may be and for every four rows, on at most two CTAs per SM.
+  const int64_t threads = std::max<int64_t>(int64_t(batch) * max_pages + (max_tokens + 3) / 4, 1);
   const unsigned grid = unsigned(std::min<int64_t>((threads + kThreads - 1) / kThreads, 304));
   page_table_kernel<<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
   return cuda_check(cudaGetLastError(), "build_page_table launch");

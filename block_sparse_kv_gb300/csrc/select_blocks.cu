@@ -36,8 +36,10 @@ using namespace dev;
 // ---------------------------------------------------------------------------------------
 
 constexpr int kBoundsThreads = 256;
-constexpr int kBoundsCtas = 2;   // per SM
-constexpr int kBoundsRows = 32;  // most token rows that a CTA looks at
+constexpr int kBoundsCtas = 3;   // per SM
+constexpr int kBoundsRows = 32;  // most token rows that a warp looks at
+constexpr int kBoundsStages = 2;
+constexpr int kBoundsAhead = 8;  // 16-byte copies of a lane at a time
 
 struct BoundsParams {
   const uint8_t* keys;
@@ -47,7 +49,8 @@ struct BoundsParams {
   const int32_t *batch_indices, *positions, *kv_indptr, *kv_indices, *kv_last_page_len;
   int64_t nnz;
   int heads, batch, num_pages, rows;
-  FastDiv page_size;
+  int units;  // groups of rows times kv heads
+  FastDiv page_size, by_head;
   StatusArgs st;
 };
 
@@ -99,84 +102,128 @@ struct Pair<__half> {
   }
 };
 
-// A CTA looks at `rows` token rows, a warp takes kv heads in turn. A page is done for each row that is
-// its first among consecutive rows: in whatever order the rows are, the lowest position of a page
-// is one of those, and a page that is done twice gets the same bytes. (Bound by reading the keys: rows
-// are D / 8 lanes of 16 bytes, eight of them in flight per lane.)
+// What the copying side tells the computing side about a stage.
+struct BoundsInfo {
+  int page, head;
+  int left;   // slots of the page from the stage's first on
+  int flags;  // 1: first round of the page, 2: last
+};
+
+// A warp looks at `rows` token rows for one kv head at a time. A page is done for each row that is its first
+// among consecutive rows: in whatever order the rows are, the lowest position of a page is one of those, and a
+// page that is done twice gets the same bytes. Bound by reading the keys: a row is D / 8 lanes of 16 bytes, and
+// the rows of up to 16 slots are copied while those before them are compared.
 template <typename T, int D>
 __global__ void __launch_bounds__(kBoundsThreads, kBoundsCtas) bounds_kernel(const __grid_constant__ BoundsParams p) {
-  constexpr int kLanes = D / 8, kSlots = 32 / kLanes, kAhead = 8;
+  constexpr int kLanes = D / 8, kSlots = 32 / kLanes, kRound = kSlots * kBoundsAhead, kWarps = kBoundsThreads / 32;
+  extern __shared__ uint4 ring[];
+  __shared__ BoundsInfo infos[kWarps][kBoundsStages];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t first = int64_t(blockIdx.x) * p.rows;
-  // lane i: row first + i
-  int page = -1, fill = 0;
-  if (lane < p.rows && first + lane < p.nnz) {
-    const int64_t i = first + lane;
-    const int b = __ldg(p.batch_indices + i), pos = __ldg(p.positions + i);
-    int slot = 0;
-    const int j = pos >= 0 ? p.page_size.divmod(pos, slot) : 0;
-    const bool before = i > 0 && __ldg(p.batch_indices + i - 1) == b && __ldg(p.positions + i - 1) == pos - 1;
-    if (b >= 0 && (slot == 0 || !before || pos < 0)) {
-      bool bad = b >= p.batch || pos < 0;
-      if (!bad) {
-        const int start = __ldg(p.kv_indptr + b), count = __ldg(p.kv_indptr + b + 1) - start;
-        bad = j >= count;
+  const int sub = lane % kLanes, slot0 = lane / kLanes;
+  uint4* mine = ring + warp * (kBoundsStages * kBoundsAhead * 32) + lane;
+  const int step = gridDim.x * kWarps;
+  int unit = blockIdx.x * kWarps + warp - step;
+  // the unit's pages that are to be done: lane i's row has page `page` with `fill` tokens
+  uint32_t todo = 0;
+  int page = -1, fill = 0, head = 0;
+  // the page that is being copied: slots [slot, n)
+  int pg = 0, slot = 0, n = 0;
+  auto look = [&]() {
+    const int64_t i = int64_t(p.by_head.divmod(unit, head)) * p.rows + lane;
+    page = -1;
+    if (lane < p.rows && i < p.nnz) {
+      const int b = __ldg(p.batch_indices + i), pos = __ldg(p.positions + i);
+      const int b0 = i > 0 ? __ldg(p.batch_indices + i - 1) : -1, pos0 = i > 0 ? __ldg(p.positions + i - 1) : 0;
+      int in_page = 0;
+      const int j = pos >= 0 ? p.page_size.divmod(pos, in_page) : 0;
+      const bool before = b0 == b && pos0 == pos - 1;
+      if (b >= 0 && (in_page == 0 || !before || pos < 0)) {
+        bool bad = b >= p.batch || pos < 0;
         if (!bad) {
-          page = __ldg(p.kv_indices + start + j);
-          fill = j == count - 1 ? __ldg(p.kv_last_page_len + b) : int(p.page_size.d);
-          bad = page < 0 || page >= p.num_pages || fill < 1 || fill > int(p.page_size.d);
+          const int start = __ldg(p.kv_indptr + b), count = __ldg(p.kv_indptr + b + 1) - start;
+          bad = j >= count;
+          if (!bad) {
+            page = __ldg(p.kv_indices + start + j);
+            fill = j == count - 1 ? __ldg(p.kv_last_page_len + b) : int(p.page_size.d);
+            bad = page < 0 || page >= p.num_pages || fill < 1 || fill > int(p.page_size.d);
+          }
+        }
+        if (bad) {
+          record_error(p.st, BSKV_ERR_DEVICE_INDEX);
+          page = -1;
         }
       }
-      if (bad) {
-        record_error(p.st, BSKV_ERR_DEVICE_INDEX);
-        page = -1;
-      }
     }
-  }
-  const uint32_t todo = __ballot_sync(0xffffffffu, page >= 0);
-  const int sub = lane % kLanes, slot0 = lane / kLanes;
-  for (uint32_t m = todo; m; m &= m - 1) {
-    const int src = __ffs(m) - 1;
-    const int pg = __shfl_sync(0xffffffffu, page, src), n = __shfl_sync(0xffffffffu, fill, src);
-    for (int h = warp; h < p.heads; h += kBoundsThreads / 32) {
-      const uint8_t* from = p.keys + pg * p.k_s0 + h * p.k_s2 + slot0 * p.k_s3 + 16 * sub;
-      uint32_t lo[4], hi[4];
+    todo = __ballot_sync(0xffffffffu, page >= 0);
+  };
+  int issued = 0;
+  auto issue = [&]() {
+    while (slot >= n && (todo || unit + step < p.units)) {
+      if (!todo) {
+        unit += step;
+        look();
+        continue;
+      }
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      pg = __shfl_sync(0xffffffffu, page, src);
+      n = __shfl_sync(0xffffffffu, fill, src);
+      slot = 0;
+    }
+    if (slot < n) {
+      const int stage = issued % kBoundsStages;
+      const uint8_t* from = p.keys + pg * p.k_s0 + head * p.k_s2 + (slot + slot0) * p.k_s3 + 16 * sub;
+#pragma unroll
+      for (int u = 0; u < kBoundsAhead; ++u) {
+        if (slot + slot0 + u * kSlots < n) cp_async_16(mine + (stage * kBoundsAhead + u) * 32, from);
+        from += kSlots * p.k_s3;
+      }
+      if (lane == 0) infos[warp][stage] = BoundsInfo{pg, head, n - slot, (slot == 0 ? 1 : 0) | (slot + kRound >= n ? 2 : 0)};
+      slot += kRound;
+      ++issued;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kBoundsStages - 1; ++i) issue();
+  uint32_t lo[4], hi[4];
+  for (int consumed = 0; consumed < issued; ++consumed) {
+    __syncwarp();  // the stage that is filled next has been read, and its round is described
+    const int stage = consumed % kBoundsStages;
+    const BoundsInfo info = infos[warp][stage];
+    issue();
+    cp_async_wait<kBoundsStages - 1>();
+    if (info.flags & 1) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         lo[c] = Pair<T>::kInf;
         hi[c] = Pair<T>::kNegInf;
       }
-      for (int s = 0; s < n; s += kSlots * kAhead) {
-        uint4 x[kAhead];
+    }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-          if (s + i * kSlots + slot0 < n) x[i] = __ldg(reinterpret_cast<const uint4*>(from + int64_t(s + i * kSlots) * p.k_s3));
+    for (int u = 0; u < kBoundsAhead; ++u) {
+      if (slot0 + u * kSlots >= info.left) continue;
+      const uint4 x = mine[(stage * kBoundsAhead + u) * 32];
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          if (s + i * kSlots + slot0 >= n) continue;
-          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            lo[c] = Pair<T>::low(lo[c], w[c]);
-            hi[c] = Pair<T>::high(hi[c], w[c]);
-          }
-        }
-      }
-#pragma unroll
-      for (int o = kLanes; o < 32; o <<= 1) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          lo[c] = Pair<T>::low(lo[c], __shfl_xor_sync(0xffffffffu, lo[c], o));
-          hi[c] = Pair<T>::high(hi[c], __shfl_xor_sync(0xffffffffu, hi[c], o));
-        }
-      }
-      // lo, then hi: 2 kLanes lanes write
-      if (lane < 2 * kLanes) {
-        const bool upper = lane >= kLanes;
-        *reinterpret_cast<uint4*>(p.bounds + pg * p.b_s0 + h * p.b_s1 + 16 * lane) =
-            upper ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      for (int c = 0; c < 4; ++c) {
+        lo[c] = Pair<T>::low(lo[c], w[c]);
+        hi[c] = Pair<T>::high(hi[c], w[c]);
       }
     }
+    if (!(info.flags & 2)) continue;
+#pragma unroll
+    for (int o = kLanes; o < 32; o <<= 1) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        lo[c] = Pair<T>::low(lo[c], __shfl_xor_sync(0xffffffffu, lo[c], o));
+        hi[c] = Pair<T>::high(hi[c], __shfl_xor_sync(0xffffffffu, hi[c], o));
+      }
+    }
+    // lo, then hi: 2 kLanes lanes write
+    if (lane < 2 * kLanes)
+      *reinterpret_cast<uint4*>(p.bounds + info.page * p.b_s0 + info.head * p.b_s1 + 16 * lane) =
+          lane >= kLanes ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
@@ -867,15 +914,24 @@ extern "C" bskv_status bskv_block_bounds_paged(
   p.kv_indptr = kv_indptr; p.kv_indices = kv_indices; p.kv_last_page_len = kv_last_page_len;
   p.nnz = nnz; p.heads = num_kv_heads; p.batch = batch; p.num_pages = int(num_pages);
   p.page_size = FastDiv(page_size);
-  // a row per CTA while there are fewer rows than keep the GPU busy, up to a warp's lanes of them
-  p.rows = int(std::min<int64_t>(kBoundsRows, (nnz + 1215) / 1216));
-  if ((nnz + p.rows - 1) / p.rows > INT32_MAX) { set_error("%s: too many rows", who); return BSKV_ERR_UNSUPPORTED; }
+  // a row at a time while the GPU has a warp for each row and head, up to a warp's lanes of them
+  constexpr int kWarps = kBoundsThreads / 32, kSms = 152;
+  const int64_t warps = int64_t(kSms) * kBoundsCtas * kWarps;
+  p.rows = int(std::min<int64_t>(kBoundsRows, (nnz * num_kv_heads + warps - 1) / warps));
+  const int64_t units = (nnz + p.rows - 1) / p.rows * num_kv_heads;
+  if (units > INT32_MAX / 2) { set_error("%s: too many rows", who); return BSKV_ERR_UNSUPPORTED; }
+  p.units = int(units);
+  p.by_head = FastDiv(num_kv_heads);
   if (bskv_status s = status_args(&p.st)) return s;
-  const unsigned grid = unsigned((nnz + p.rows - 1) / p.rows);
+  const unsigned grid = unsigned(std::min<int64_t>((units + kWarps - 1) / kWarps, int64_t(kSms) * kBoundsCtas));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto kern = head_dim == 128 ? (dtype == BSKV_BF16 ? bounds_kernel<__nv_bfloat16, 128> : bounds_kernel<__half, 128>)
                               : (dtype == BSKV_BF16 ? bounds_kernel<__nv_bfloat16, 64> : bounds_kernel<__half, 64>);
-  kern<<<grid, kBoundsThreads, 0, st>>>(p);
+  constexpr size_t smem = size_t(kWarps) * kBoundsStages * kBoundsAhead * 32 * sizeof(uint4);
+  static std::atomic<int> allowed[4][64];
+  if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed[(head_dim == 128) * 2 + (dtype == BSKV_BF16)], "block_bounds_paged: cudaFuncSetAttribute"))
+    return s;
+  kern<<<grid, kBoundsThreads, smem, st>>>(p);
   return cuda_check(cudaGetLastError(), "block_bounds_paged launch");
 }
 
