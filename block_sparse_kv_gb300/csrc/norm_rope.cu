@@ -316,8 +316,8 @@ extern "C" bskv_status bskv_norm_rope_append_paged(
     return BSKV_ERR_INVALID_ARG;
   }
   if (!has_q && !has_kv) { set_error("%s: neither queries nor keys and values", who); return BSKV_ERR_INVALID_ARG; }
-  if (num_pages > INT32_MAX || num_qo_heads > 65535 || num_kv_heads > 65535) {
-    set_error("%s: num_pages=%lld num_qo_heads=%d num_kv_heads=%d", who, (long long)num_pages, num_qo_heads, num_kv_heads);
+  if (nnz > INT32_MAX || num_pages > INT32_MAX || num_qo_heads > 65535 || num_kv_heads > 65535) {
+    set_error("%s: nnz=%lld num_pages=%lld num_qo_heads=%d num_kv_heads=%d", who, (long long)nnz, (long long)num_pages, num_qo_heads, num_kv_heads);
     return BSKV_ERR_UNSUPPORTED;
   }
   if (rotary_dim < 0 || rotary_dim > head_dim) { set_error("%s: rotary_dim %d outside [0, %d]", who, rotary_dim, head_dim); return BSKV_ERR_INVALID_ARG; }
