@@ -8,14 +8,16 @@
 // values, wherever its page lies. One CTA per SM, eight warps with a ring of copies each, up to 192 KB in flight.
 // The up to 16 query heads of a group are the M = 16 rows of mma.sync m16n8k16 against 16 tokens at a time.
 //
-// Split. The lists' lengths are known on the GPU only, so the cut is made in places: the rows' lists follow
-// one another in steps of 16 tokens (or pages of 8), top_k lists' worth of them per row, and each CTA takes an equal
-// run; a run covers the same fraction of a row's actual list (place f of F stands for step f n / top_k of a list of
-// n blocks), so that short lists are cut as evenly as full ones. The warps of a CTA share each row of its run
-// in equal parts and join their states in shared memory; a row that lies in several CTAs leaves their states in the
-// float workspace, and the CTA that finishes its last piece joins them in the same launch, in piece order.
-// With runs for warps instead of CTAs, which leave eight times as many states there, 64 requests with 64 blocks of 16
-// tokens took 50 us at 4 query heads per kv head and 65 at 16; whole rows to a warp ran at 1.04 of the floor.
+// Split. The lists' lengths are known on the GPU only, so the cut is made in places: the rows' lists of top_k blocks
+// follow one another in steps of 16 tokens (or pages of 8), and each team of 1, 2, 4 or 8 warps takes an equal run of
+// them; a run covers the same fraction of a row's actual list (place f stands for step f n / top_k of a list of
+// n blocks), so that short lists are cut as evenly as full ones. The warps of a team share each row of its run
+// in equal parts and join their states in shared memory; a row that lies in several runs leaves their states in the
+// float workspace, and the team that finishes its last piece joins them in the same launch, in piece order.
+// A piece costs a warp about 4 us beside its tiles, which is why the team's size matters (1, 2, 4, 8 warps; us): 64
+// requests, 8 kv heads, 64 blocks of 16 tokens 52.9, 48.6, 47.0, 49.6 (floor 40.3); 300 with 8 blocks 29.8, 33.0, 43.3,
+// 63.2 (24.3); 32 with 32 blocks of 64 and 8 query heads per kv head 64.9, 55.9, 49.6, 47.6 (40.3); one with 128
+// blocks 28.7, 18.1, 12.6, 13.0. The plan's rule is at blocks_team().
 #include <algorithm>
 
 #include "cache_common.cuh"

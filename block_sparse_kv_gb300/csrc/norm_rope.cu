@@ -11,8 +11,8 @@
 //   y_d = r (x_d A_d + x_partner B_d),  A_d = w_d cos, B_d = -+ w_partner sin.
 // Rows come by asynchronous copies through shared memory, a batch ahead, and a lane takes from there two groups of
 // four values whose partners it has too, so that only the mean needs other lanes. What is left to watch is the
-// number of instructions: one row per 165 of them and warp, with partners by shuffles and factors made per
-// batch, took 157 us on 32000 tokens of 48 heads (5.2 TB/s).
+// number of instructions: with partners by shuffles and factors made per batch, 165 for two rows of 128 dims, 32000
+// tokens of 48 heads took 157 us; so, with 130, they take 127 (6.4 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -28,7 +28,7 @@ using namespace dev;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSms = 152;
-constexpr int kCtasPerSm = 3;
+constexpr int kCtasPerSm = 3;  // 2: 131 us, and 39 instead of 33 for 64 dims; 4 CTAs spill: 208
 constexpr int kBatch = 4;  // rows of a lane per batch
 constexpr int kStages = 3;
 constexpr int kUnroll = 2;

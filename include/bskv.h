@@ -726,7 +726,7 @@ bskv_status bskv_build_page_table(
  * Queries and keys normalised per head and rotated, keys and values appended to the paged cache that
  * bskv_run_decode reads. In fp32, rounded once:
  *   y = x * w / sqrt(mean(x^2) + eps) over head_dim, with q_weight for q, k_weight for k ([head_dim] of
- *     dtype, NULL: x itself);
+ *     dtype, NULL: x itself); the squares, and x * w, have to stay within fp32's range;
  *   the first rotary_dim values (a multiple of 16, 0: none) rotate as in bskv_rope_quantize_fp8: is_neox != 0
  *     pairs i with i + rotary_dim / 2, 0 pairs 2i with 2i + 1; pair i uses cos = cos_sin[at, i] and
  *     sin = cos_sin[at, rotary_dim / 2 + i], at = pos_ids[row], or positions[row] where pos_ids is NULL. cos_sin
