@@ -81,14 +81,7 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
   int* first_new = fresh_from + p.batch;
   __shared__ int3 warp_sums[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int free_n = 0;
-  if (p.free_pages) {
-    free_n = __ldg(p.free_count);
-    if (free_n < 0 || free_n > p.max_free) {
-      if (blockIdx.x == 0 && tid == 0) record_error(p.st, BSKV_ERR_DEVICE_INDEX);
-      free_n = 0;
-    }
-  }
+  int free_n = p.free_pages ? __ldg(p.free_count) : 0;
   for (int b = tid; b < p.batch; b += kThreads) {
     bool bad;
     const Lens r = lens_of(p, b, bad);
@@ -98,6 +91,10 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
     fresh[b] = r.fresh;
     fresh_from[b] = r.fresh_from;
     first_new[b] = r.first_new;
+  }
+  if (free_n < 0 || (p.free_pages && free_n > p.max_free)) {
+    if (blockIdx.x == 0 && tid == 0) record_error(p.st, BSKV_ERR_DEVICE_INDEX);
+    free_n = 0;
   }
   __syncthreads();
   // each thread adds up a run of requests, the runs' sums are scanned over the CTA
@@ -144,19 +141,16 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
   const int num_entries = pages[p.batch], num_tokens = tokens[p.batch];
 
   // the id of page j of request b: a fresh one from the free list, else the table's; -1: none
-  auto page_id = [&](int b, int j) {
-    int id;
-    if (j >= fresh_from[b]) {
-      const int at = free_n - 1 - (fresh[b] + j - fresh_from[b]);
-      id = at >= 0 ? __ldg(p.free_pages + at) : -1;
-    } else {
-      id = p.table[b * p.t_s + j];
-    }
-    if (id < 0 || id >= p.num_pages) {
-      record_error(p.st, BSKV_ERR_DEVICE_INDEX);
-      id = -1;
-    }
-    return id;
+  auto read_id = [&](int b, int j) -> int {
+    const int nth = j - fresh_from[b];
+    if (nth < 0) return p.table[b * p.t_s + j];
+    const int at = free_n - 1 - (fresh[b] + nth);
+    return at >= 0 ? __ldg(p.free_pages + at) : -1;
+  };
+  auto checked = [&](int id) -> int {
+    if (id >= 0 && id < p.num_pages) return id;
+    record_error(p.st, BSKV_ERR_DEVICE_INDEX);
+    return -1;
   };
 
   if (blockIdx.x == 0) {
@@ -177,23 +171,24 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
   auto write_rows = [&](int r0) {
     int req[4], pos[4];
     int64_t slot[4];
-    int b = -1, page = -1, id = -1;
+    int id[4], in_page[4], b = -1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = r0 + i;
       req[i] = pos[i] = -1;
-      slot[i] = -1;
       if (row >= num_tokens || row >= p.max_tokens) continue;
-      if (b < 0 || row >= tokens[b + 1]) {
-        b = owner(tokens, p.batch, row);
-        page = -1;
-      }
+      if (b >= 0 && row >= tokens[b + 1]) b = b + 2 <= p.batch && row < tokens[b + 2] ? b + 1 : -1;  // often the next request's
+      if (b < 0) b = owner(tokens, p.batch, row);
       req[i] = b;
       pos[i] = first_new[b] + row - tokens[b];
-      int in_page;
-      const int j = p.page_size.divmod(pos[i], in_page);
-      if (j != page) id = page_id(b, page = j);
-      if (id >= 0) slot[i] = int64_t(id) * p.page_size.d + in_page;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (req[i] >= 0) id[i] = read_id(req[i], p.page_size.divmod(pos[i], in_page[i]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      slot[i] = -1;
+      if (req[i] >= 0 && (id[i] = checked(id[i])) >= 0) slot[i] = int64_t(id[i]) * p.page_size.d + in_page[i];
     }
     if (r0 + 4 <= p.max_tokens) {
       *reinterpret_cast<int4*>(p.batch_indices + r0) = make_int4(req[0], req[1], req[2], req[3]);
@@ -219,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const __grid_const
     }
     const int e = int(item - row_items);
     const int b = owner(pages, p.batch, e), j = e - pages[b];
-    const int id = page_id(b, j);
+    const int id = checked(read_id(b, j));
     if (j >= fresh_from[b]) p.table[b * p.t_s + j] = id;
     p.kv_indices[e] = id;
   }
