@@ -170,13 +170,17 @@ struct Walk {
   }
 };
 
-// Row r of 64-column half hf of a stage's K or V: rows of 128 bytes, 128-byte swizzle.
-__device__ __forceinline__ uint32_t tile_row(uint32_t base, int r, int hf) { return base + hf * kPanel + r * 128; }
+// A stage holds, for each 64-column half, what one copy brings of a page: its rows of K, then its rows of V, 128
+// bytes each with the 128-byte swizzle. So the second eight rows are `eight` bytes behind the first: 1024, or 2048
+// with pages of eight, of which a tile takes two.
+__device__ __forceinline__ uint32_t tile_row(uint32_t base, int r, int hf, uint32_t eight) {
+  return base + hf * (2 * kPanel) + (r >> 3) * eight + (r & 7) * 128;
+}
 
 // One tile of 16 tokens for the (up to 16) query heads of a row. v0 and v1 of the two groups of eight
 // tokens are attended to.
 template <typename T, int D>
-__device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, int v0, int v1, float scale_log2, int lane,
+__device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, uint32_t eight, int v0, int v1, float scale_log2, int lane,
                                             const uint32_t (&qa)[D / 16][4], float (&o)[D / 8][4], float& m0,
                                             float& m1, float& l0, float& l1) {
   using Mma = MmaOp<T>;
@@ -185,7 +189,7 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, int v0
     // slots that are not attended to may hold anything: 0 * NaN must not reach the output
     for (int i = lane; i < kTile * (D / 8); i += 32) {
       const int r = i / (D / 8), c = i % (D / 8);
-      if ((r & 7) >= (r < 8 ? v0 : v1)) sts128(tile_row(v_at, r, c >> 3) + (c & 7) * 16, make_uint4(0, 0, 0, 0));
+      if ((r & 7) >= (r < 8 ? v0 : v1)) sts128(tile_row(v_at, r, c >> 3, eight) + (c & 7) * 16, make_uint4(0, 0, 0, 0));
     }
     __syncwarp();
   }
@@ -196,7 +200,7 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, int v0
     for (int kk = 0; kk < D / 16; ++kk) {
       const int dim = kk * 16 + (mi & 1) * 8;
       uint32_t b0, b1, b2, b3;
-      ldsm_x4(tile_row(k_at, r, dim / 64) + ((((dim % 64) / 8) ^ (r & 7)) << 4), b0, b1, b2, b3);
+      ldsm_x4(tile_row(k_at, r, dim / 64, eight) + ((((dim % 64) / 8) ^ (r & 7)) << 4), b0, b1, b2, b3);
       Mma::run(s[0], qa[kk], b0, b1);
       Mma::run(s[1], qa[kk], b2, b3);
     }
@@ -246,7 +250,7 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, int v0
     for (int dd = 0; dd < D / 16; ++dd) {
       const int dim = dd * 16 + (mi >> 1) * 8;
       uint32_t b0, b1, b2, b3;
-      ldsm_x4_t(tile_row(v_at, r, dim / 64) + ((((dim % 64) / 8) ^ (r & 7)) << 4), b0, b1, b2, b3);
+      ldsm_x4_t(tile_row(v_at, r, dim / 64, eight) + ((((dim % 64) / 8) ^ (r & 7)) << 4), b0, b1, b2, b3);
       Mma::run(o[2 * dd], pa, b0, b1);
       Mma::run(o[2 * dd + 1], pa, b2, b3);
     }
@@ -283,6 +287,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const bool forced = forced_timeout(p.st);
   const uint64_t policy = l2_evict_first_policy();
   const int ps = int(p.page_size.d);
+  const uint32_t eight = ps < kTile ? kPanel : kPanel / 2, v_at = ps < kTile ? kPanel / 2 : kPanel;
 
   // Copies the next tile of the walk into a stage; a piece without tokens is a tile of none.
   Walk walk(p, worker, member, lane);
@@ -290,8 +295,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   auto issue = [&]() {
     if (!walk.live()) return;
     const int stage = issued % STAGES;
-    uint8_t* k_to = ring + stage * R::kStageBytes;
-    uint8_t* v_to = k_to + R::kTileBytes;
+    uint8_t* to = ring + stage * R::kStageBytes;
     StageInfo info{walk.row, 0, walk.fresh ? kFirst : 0};
     walk.fresh = false;
     int h;
@@ -304,10 +308,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       if (lane == 0) {
         mbar_arrive_expect_tx(&bars[stage], uint32_t(R::kStageBytes));
 #pragma unroll
-        for (int hf = 0; hf < D / 64; ++hf) {
-          tma_load_5d_hint(k_to + hf * kPanel, &kv_map, hf * 64, slot, h, 0, page, &bars[stage], policy);
-          tma_load_5d_hint(v_to + hf * kPanel, &kv_map, hf * 64, slot, h, 1, page, &bars[stage], policy);
-        }
+        for (int hf = 0; hf < D / 64; ++hf)
+          tma_load_5d_hint(to + hf * 2 * kPanel, &kv_map, hf * 64, slot, h, 0, page, &bars[stage], policy);
       }
       info.valid = min(left, 8) | max(0, min(left - 8, 8)) << 16;
       walk.slot += kTile;
@@ -325,12 +327,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         mbar_arrive_expect_tx(&bars[stage], uint32_t(c1 ? R::kStageBytes : R::kStageBytes / 2));
 #pragma unroll
         for (int hf = 0; hf < D / 64; ++hf) {
-          tma_load_5d_hint(k_to + hf * kPanel, &kv_map, hf * 64, 0, h, 0, page0, &bars[stage], policy);
-          tma_load_5d_hint(v_to + hf * kPanel, &kv_map, hf * 64, 0, h, 1, page0, &bars[stage], policy);
-          if (c1) {
-            tma_load_5d_hint(k_to + hf * kPanel + 1024, &kv_map, hf * 64, 0, h, 0, page1, &bars[stage], policy);
-            tma_load_5d_hint(v_to + hf * kPanel + 1024, &kv_map, hf * 64, 0, h, 1, page1, &bars[stage], policy);
-          }
+          tma_load_5d_hint(to + hf * 2 * kPanel, &kv_map, hf * 64, 0, h, 0, page0, &bars[stage], policy);
+          if (c1) tma_load_5d_hint(to + hf * 2 * kPanel + kPanel, &kv_map, hf * 64, 0, h, 0, page1, &bars[stage], policy);
         }
       }
       info.valid = c0 | c1 << 16;
@@ -375,7 +373,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (ok) ok = warp_wait(&bars[stage], (consumed / STAGES) & 1u, p.st, forced);
     if (ok) {
       const uint32_t at = smem_u32(ring + stage * R::kStageBytes);
-      if (info.valid) attend_tile<T, D>(at, at + R::kTileBytes, info.valid & 0xffff, info.valid >> 16, p.scale_log2, lane, qa, o, m0, m1, l0, l1);
+      if (info.valid) attend_tile<T, D>(at, at + v_at, eight, info.valid & 0xffff, info.valid >> 16, p.scale_log2, lane, qa, o, m0, m1, l0, l1);
       ++consumed;
       __syncwarp();
       if (lane == 0) fence_proxy_async_smem();
@@ -605,7 +603,7 @@ extern "C" bskv_status bskv_run_decode_blocks(
   const int ps = plan->page_size, D = plan->head_dim;
   const uint64_t dims[5] = {uint64_t(D), uint64_t(ps), uint64_t(plan->num_kv_heads), 2, uint64_t(plan->num_pages)};
   const uint64_t strides[4] = {uint64_t(kv_strides[3]) * 2, uint64_t(kv_strides[2]) * 2, uint64_t(kv_strides[1]) * 2, uint64_t(kv_strides[0]) * 2};
-  const uint32_t box[5] = {64, uint32_t(std::min(ps, kTile)), 1, 1, 1};
+  const uint32_t box[5] = {64, uint32_t(std::min(ps, kTile)), 1, 2, 1};  // K and V of a page
   CUtensorMap map;
   if (bskv_status s = encode_tiled(&map, plan->dtype == BSKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                                    5, kv_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
