@@ -928,6 +928,11 @@ extern "C" bskv_status bskv_plan_decode_blocks(int32_t num_tokens, int32_t max_b
   // us, cut 12.9)
   const int64_t whole = (rows + teams - 1) / teams;
   if (rows > 0 && 8 * whole * teams <= 9 * rows) p->per_worker = int32_t(whole * row_places);
+  // a run's tokens and a team's shares of it are counted in 31 bits, and so are the steps of a list's next 64 entries
+  if (p->per_worker > INT32_MAX / 64 || (int64_t(top_k) + 64) * p->steps > INT32_MAX) {
+    set_error("%s: lists of %d blocks of %d tokens on %d SMs are too long", who, top_k, page_size, num_sms);
+    return BSKV_ERR_UNSUPPORTED;
+  }
   p->workers = int32_t((places + p->per_worker - 1) / p->per_worker);
   std::vector<int32_t> none;
   std::vector<Chunk> no_chunks;

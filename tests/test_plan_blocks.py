@@ -41,6 +41,15 @@ def test_plan_refusals(lib, kw, status):
     assert e.value.status == status and "plan_decode_blocks" in str(e.value)
 
 
+@pytest.mark.parametrize("kw", [dict(top=1 << 27, sms=1), dict(top=1 << 25, ps=64, sms=1), dict(top=1, sink=0, recent=1, ps=1 << 30),
+                                dict(top=64, ps=1 << 28, sms=1)])
+def test_plan_of_lists_past_31_bits(lib, kw):
+    """Lists whose steps, or a team's share of which, the kernels' 31 bits would not hold."""
+    with pytest.raises(bskv.BskvError) as e:
+        _plan(tokens=1, hq=1, hkv=1, **kw)
+    assert e.value.status == "ERR_UNSUPPORTED" and "plan_decode_blocks" in str(e.value)
+
+
 def test_plan_of_a_type_without_a_code(lib):
     with pytest.raises(ValueError, match="dtype"):
         _plan(dtype=torch.float64)
