@@ -19,6 +19,7 @@
 // 63.2 (24.3); 32 with 32 blocks of 64 and 8 query heads per kv head 64.9, 55.9, 49.6, 47.6 (40.3); one with 128
 // blocks 28.7, 18.1, 12.6, 13.0. The plan's rule is at blocks_team().
 #include <algorithm>
+#include <cfloat>
 
 #include "cache_common.cuh"
 #include "internal.h"
@@ -205,7 +206,7 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, uint32
       Mma::run(s[1], qa[kk], b2, b3);
     }
   }
-  float mx0 = -INFINITY, mx1 = -INFINITY;
+  float mx0 = -FLT_MAX, mx1 = -FLT_MAX;  // finite: a logit of -inf has no weight, in a tile of only such ones too
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt) {
     const int valid = nt ? v1 : v0;

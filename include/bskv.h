@@ -499,7 +499,7 @@ bskv_status bskv_run_select_blocks(
  *   q, out [num_tokens, num_qo_heads, head_dim], strides {row, head} in multiples of 8 elements; kv_cache and kv_strides as
  *     for bskv_run_decode; lse [num_tokens, num_qo_heads] float32 contiguous, or NULL.
  *   Rows with a negative batch_indices have no token: their out and lse are left as they were. A row that is out of range
- *   (raised as above), or that lists no block, gets out = 0 and lse = -inf.
+ *   (raised as above), or that lists no block, gets out = 0 and lse = -inf, as do heads whose every logit is -inf.
  *   Deterministic: the same inputs give the same bits.
  */
 bskv_status bskv_run_decode_blocks(

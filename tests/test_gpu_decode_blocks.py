@@ -191,6 +191,28 @@ def test_sharp_and_large_logits(cuda):
         _check(out, lse, _expect(s, 1.0 / math.sqrt(d)), BF)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_infinite_keys(cuda, dtype):
+    """Logits of -inf have no weight: in whole blocks, wherever they stand in a list; heads that see nothing else get
+    what a row without a block gets."""
+    lens, new, ps, hq, hkv, d, top = [1024, 160, 40], [1, 1, 1], 16, 4, 2, 64, 64
+    s = _inputs(lens, new, ps, hq, hkv, d, top, dtype, 13)
+    p = bskv.bskv_plan_decode_blocks(3, 64, s["pages"], ps, hq, hkv, d, top, dtype=dtype)
+    s["q"][:, :, 5] = s["q"][:, :, 5].abs() + 0.5
+    for b, blocks in enumerate([(0, 1, 30, 31, 32, 63), (0, 9), (0, 1, 2)]):
+        for j in blocks:
+            s["kv"][pages_of(s, b)[j], 0, :, :min(ps, lens[b] - j * ps), 5] = -float("inf")
+    out, lse = bskv.bskv_run_decode_blocks(p, s["q"].to(cuda), s["kv"].to(cuda), s["blocks"].to(cuda), *lists(s, cuda),
+                                           return_lse=True)
+    assert bskv.bskv_get_device_status() == 0
+    assert (out[2] == 0).all() and (lse[2] == -float("inf")).all()
+    # without those blocks nothing else changes
+    for b, blocks in enumerate([(0, 1, 30, 31, 32, 63), (0, 9), (0, 1, 2)]):
+        for j in blocks:
+            s["blocks"][b][s["blocks"][b] == j] = -1
+    _check(out, lse, _expect(s, 1.0 / math.sqrt(d)), dtype)
+
+
 def test_forced_timeout(cuda):
     """Waits that give up are reported; after an upload the plan runs again."""
     lens, new, ps, hq, hkv, d, top, dtype = CASES[1]
