@@ -117,7 +117,7 @@ struct BoundsInfo {
 // among consecutive rows: in whatever order the rows are, the lowest position of a page is one of those, and a
 // page that is done twice gets the same bytes. Bound by reading the keys: a row is D / 8 lanes of 16 bytes, and
 // the rows of up to 16 slots are copied while those before them are compared (32000 tokens of 8 heads in pages of 16:
-// 16.4 us, 4.5 TB/s of keys and bounds; by CTAs of 32 rows with loads in registers 20.4).
+// 16.1 us, 4.6 TB/s of keys and bounds; by CTAs of 32 rows with loads in registers 20.4).
 template <typename T, int D>
 __global__ void __launch_bounds__(kBoundsThreads, kBoundsCtas) bounds_kernel(const __grid_constant__ BoundsParams p) {
   constexpr int kLanes = D / 8, kSlots = 32 / kLanes, kRound = kSlots * kBoundsAhead, kWarps = kBoundsThreads / 32;
