@@ -115,15 +115,15 @@ _SIGS = {
     "bskv_run_evict_fp4": ([_P, _P, _I64P, _I32, _P, _I64P, _P, _I64P, _P, _P], _I32),
     "bskv_build_page_table": ([_P, _P, _I32, _I32, _P, _I64, _I32, _I32, _P, _I32, _P, _P, _P, _P, _I64,
                                _P, _P, _P, _P, _P, _I64, _P], _I32),
-    "bskv_norm_rope_append_paged": ([_P, _I64P, _P, _I64P, _P, _I64P, _I32, _I64, _I32, _I32, _I32, _P,
+    "bskv_norm_rope_append_paged": ([_P, _P, _P, _P, _P, _P, _I32, _I64, _I32, _I32, _I32, _P,
                                      _P, _F, _P, _I32, _I64, _I32, _I32, _P, _P, _P, _P, _P, _I32, _I32,
-                                     _I64, _P, _I64P, _P, _I64P, _P], _I32),
-    "bskv_block_bounds_paged": ([_P, _I64P, _I32, _I32, _I32, _I32, _I64, _P, _P, _I64, _P, _P, _P,
-                                 _I32, _P, _I64P, _P], _I32),
+                                     _I64, _P, _P, _P, _P, _P], _I32),
+    "bskv_block_bounds_paged": ([_P, _P, _I32, _I32, _I32, _I32, _I64, _P, _P, _I64, _P, _P, _P,
+                                 _I32, _P, _P, _P], _I32),
     "bskv_plan_decode_blocks": ([_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
                                  ctypes.POINTER(_P)], _I32),
-    "bskv_run_select_blocks": ([_P, _P, _I64P, _P, _I64P, _P, _P, _P, _P, _I32, _P, _P, _SZ, _P], _I32),
-    "bskv_run_decode_blocks": ([_P, _P, _I64P, _P, _I64P, _P, _P, _P, _P, _P, _I32, _P, _I64P, _P, _F,
+    "bskv_run_select_blocks": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _SZ, _P], _I32),
+    "bskv_run_decode_blocks": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _P, _F,
                                 _P, _SZ, _P], _I32),
     "bskv_merge_states": ([_P, _P, _I64, _I32, _I32, _I32, _P, _I32, _P, _P], _I32),
     "bskv_get_device_status": ([_I32P, _I32], _I32),
@@ -180,6 +180,7 @@ def _stream(t=None):
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # of an initialised CUDA
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -732,7 +733,7 @@ def _strides_of(t, n):
 def _call(fn, dev, *args):
     """The C entry point `fn` on the current stream of the tensors' device."""
     entry = getattr(_lib or load_library(), fn)
-    if torch.cuda.current_device() == dev.index:
+    if _current_device() == dev.index:
         code = entry(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
@@ -772,7 +773,7 @@ def _once(memo, check, fn, owner, *tensors):
     """check(fn, owner, *tensors), which depends on nothing but the memo's owner and the tensors'
     shapes, strides, types and devices: the answer is kept for calls with the same ones."""
     try:
-        key = (fn,) + tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+        key = (fn,) + tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
                              for t in tensors])
     except AttributeError:  # not tensors; the check says which
         return check(fn, owner, *tensors)
@@ -1145,8 +1146,9 @@ class PageTable:
         if free_left is not None:
             _list_of(fn, "free_left", free_left, 1, dev)
         self._device, self._batch, self._entries = dev, batch, kv_indices.numel()
-        self._pointers = (kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_indices.numel(), kv_last_page_len.data_ptr(),
-                          qo_indptr.data_ptr(), batch_indices.data_ptr(), positions.data_ptr(), _ptr(slots), rows)
+        self._pointers = (_P(kv_indptr.data_ptr()), _P(kv_indices.data_ptr()), _I64(kv_indices.numel()),
+                          _P(kv_last_page_len.data_ptr()), _P(qo_indptr.data_ptr()), _P(batch_indices.data_ptr()),
+                          _P(positions.data_ptr()), _P(_ptr(slots)), _I64(rows))
         self.kv_indptr, self.kv_indices, self.kv_last_page_len = kv_indptr, kv_indices, kv_last_page_len
         self.qo_indptr, self.batch_indices, self.positions = qo_indptr, batch_indices, positions
         self.slots, self.free_left = slots, free_left
@@ -1158,6 +1160,15 @@ class PageTable:
 
 
 _I64T = (torch.int64,)
+
+
+def _at(strides):
+    """The address of an array of strides, which it keeps alive, as a call takes it without converting it again."""
+    if strides is None:
+        return None
+    p = _P(ctypes.addressof(strides))
+    p.strides = strides
+    return p
 
 
 def _list_of(fn, name, t, n, device, dtypes=_I32T):
@@ -1178,8 +1189,9 @@ def _check_page_table(fn, _, seq_lens, block_table, new_lens, free_pages, free_c
     if free_pages is not None:
         _list_of(fn, "free_pages", free_pages, None, dev)
         _list_of(fn, "free_count", free_count, 1, dev)
-    return (dev, batch, block_table.shape[1], _strides_of(block_table, 1)[0],
-            0 if free_pages is None else free_pages.numel())
+    most = block_table.shape[1]
+    return (dev, batch, batch * most, _I32(batch), (_I64(_strides_of(block_table, 1)[0]), _I32(most)),
+            _I32(0 if free_pages is None else free_pages.numel()))
 
 
 def bskv_build_page_table(seq_lens, block_table, page_size, num_pages, new_lens=None, free_pages=None,
@@ -1190,8 +1202,8 @@ def bskv_build_page_table(seq_lens, block_table, page_size, num_pages, new_lens=
     block_table. The PageTable has room for max_tokens new tokens (None: B, and new_lens must be None);
     rows without one are -1. `out` is an earlier PageTable to write into (its room is what counts then)."""
     fn = "bskv_build_page_table"
-    dev, batch, max_pages, stride, most_free = _once(_call_layouts, _check_page_table, fn, None, seq_lens,
-                                                     block_table, new_lens, free_pages, free_count)
+    dev, batch, entries, requests, shape, most_free = _once(
+        _call_layouts, _check_page_table, fn, None, seq_lens, block_table, new_lens, free_pages, free_count)
     o = out
     if o is None:
         if max_tokens is None:
@@ -1204,20 +1216,20 @@ def bskv_build_page_table(seq_lens, block_table, page_size, num_pages, new_lens=
         def ints(n, dtype=torch.int32):
             return torch.empty(n, dtype=dtype, device=dev)
 
-        o = PageTable(ints(batch + 1), ints(batch * max_pages), ints(batch), ints(batch + 1), ints(int(max_tokens)),
+        o = PageTable(ints(batch + 1), ints(entries), ints(batch), ints(batch + 1), ints(int(max_tokens)),
                       ints(int(max_tokens)), ints(int(max_tokens), torch.int64),
                       None if free_pages is None else ints(1))
     elif not isinstance(o, PageTable):
         raise TypeError("%s: out must be a PageTable" % fn)
-    elif o._device != dev or o._batch != batch or o._entries < batch * max_pages:
+    elif o._device != dev or o._batch != batch or o._entries < entries:
         raise ValueError("%s: out is for %d requests and %d pages on %s; needed are %d, up to %d and %s"
-                         % (fn, o._batch, o._entries, o._device, batch, batch * max_pages, dev))
+                         % (fn, o._batch, o._entries, o._device, batch, entries, dev))
     elif free_pages is not None and o.free_left is None:
         raise ValueError("%s: free_pages need a PageTable with free_left" % fn)
-    free = (None, 0, None, None) if free_pages is None else (free_pages.data_ptr(), most_free, free_count.data_ptr(),
-                                                             o.free_left.data_ptr())
-    _call(fn, dev, seq_lens.data_ptr(), _ptr(new_lens), batch, int(page_size), block_table.data_ptr(), stride,
-          max_pages, int(num_pages), *free, *o._pointers)
+    free = (None, most_free, None, None) if free_pages is None else (
+        free_pages.data_ptr(), most_free, free_count.data_ptr(), o.free_left.data_ptr())
+    _call(fn, dev, seq_lens.data_ptr(), _ptr(new_lens), requests, int(page_size), block_table.data_ptr(), *shape,
+          int(num_pages), *free, *o._pointers)
     return o
 
 
@@ -1280,8 +1292,9 @@ def _check_norm_rope(fn, _, q, k, v, cos_sin_cache, batch_indices, positions, kv
         batch = kv_indptr.numel() - 1
         if batch < 0:
             raise ValueError("%s: kv_indptr is empty" % fn)
-    return (dev, qs, qos, ks, vs, cs, (_DT[first.dtype], nnz, hq, hkv, dim), (table, limit, rot),
-            (batch, page_size, pages))
+    return (dev, _at(qs), _at(qos), _at(ks), _at(vs), _at(cs),
+            (_I32(_DT[first.dtype]), _I64(nnz), _I32(hq), _I32(hkv), _I32(dim)), (_I32(table), _I64(limit), _I32(rot)),
+            (_I32(batch), _I32(page_size), _I64(pages)))
 
 
 def bskv_norm_rope_append_paged(q, k, v, cos_sin_cache, batch_indices, positions, kv_indptr, kv_indices,
@@ -1327,7 +1340,8 @@ def _check_block_bounds(fn, _, kv_cache, bounds, batch_indices, positions, kv_in
     if batch < 0:
         raise ValueError("%s: kv_indptr is empty" % fn)
     _list_of(fn, "kv_last_page_len", kv_last_page_len, batch, dev)
-    return dev, _strides_of(kv_cache, 4), bs, (_DT[kv_cache.dtype], heads, dim, page_size, pages), nnz, batch
+    return (dev, _at(_strides_of(kv_cache, 4)), _at(bs),
+            (_I32(_DT[kv_cache.dtype]), _I32(heads), _I32(dim), _I32(page_size), _I64(pages)), _I64(nnz), _I32(batch))
 
 
 def bskv_block_bounds_paged(kv_cache, bounds, batch_indices, positions, kv_indptr, kv_indices, kv_last_page_len):
@@ -1375,14 +1389,14 @@ def _check_blocks(fn, plan, q, blocks, batch_indices, positions, kv_indptr, kv_i
     _list_of(fn, "kv_indices", kv_indices, None, dev)
     if kv_indptr.numel() < 1:
         raise ValueError("%s: kv_indptr is empty" % fn)
-    return dev, _strides_of(q, 2), kv_indptr.numel() - 1
+    return dev, _at(_strides_of(q, 2)), _I32(kv_indptr.numel() - 1)
 
 
 def _check_select_blocks(fn, plan, q, bounds, *lists):
     i = plan.info
     dev, qs, batch = _check_blocks(fn, plan, q, *lists)
     bs = _bounds_strides(fn, bounds, (i["num_pages"], i["num_kv_heads"], 2, i["head_dim"]), (i["dtype"],), dev)
-    return dev, qs, bs, batch, i["blocks_shape"]
+    return dev, qs, _at(bs), batch, i["blocks_shape"]
 
 
 def bskv_run_select_blocks(plan, q, bounds, batch_indices, positions, kv_indptr, kv_indices, blocks=None):
@@ -1417,7 +1431,7 @@ def _check_decode_blocks(fn, plan, q, kv_cache, out, lse, *lists):
         _want(fn, "lse", lse, shape[:2], _F32T, dev)
         _dense(fn, ("lse", lse))
     outs = _strides(shape[1] * shape[2], shape[2]) if out is None else _strides_of(out, 2)
-    return dev, qs, cache[0], outs, batch, shape
+    return dev, qs, _at(cache[0]), _at(outs), batch, shape
 
 
 def bskv_run_decode_blocks(plan, q, kv_cache, blocks, batch_indices, positions, kv_indptr, kv_indices,
