@@ -83,6 +83,39 @@ def test_rows_and_cache(cuda, case):
     assert bskv.bskv_get_device_status() == 0
 
 
+LONG = [
+    # enough tokens that a warp takes whole ones, several in turn
+    ([1500, 2200], [1500, 2100], 16, 5, 2, 64, 64, True, (1, 1), BF, torch.float32),
+    ([4100], [4100], 8, 3, 1, 128, 32, False, (1, 0), FP, BF),
+    ([2500], [2500], 16, 18, 9, 64, 16, False, (0, 1), BF, torch.float32),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_many_tokens(cuda, case):
+    lens, new, ps, hq, hkv, d, rot, neox, _, dtype, _ = LONG[case]
+    s = _make(LONG[case], 3)
+    s["req"][[0, 77, 2431, sum(new) - 1]] = -1  # rows without a token
+    cache, out = s["cache"].to(cuda), torch.full(s["q"].shape, 3.0, dtype=dtype, device=cuda)
+    bskv.bskv_norm_rope_append_paged(
+        s["q"].to(cuda), s["k"].to(cuda), s["v"].to(cuda), _dev(s["cos_sin"], cuda), *lists(s, cuda), cache,
+        q_weight=_dev(s["wq"], cuda), k_weight=_dev(s["wk"], cuda), eps=1e-5, is_neox=neox, q_out=out)
+    live = s["req"] >= 0
+    assert (out[(~live).to(cuda)] == 3.0).all()
+    at = s["pos"].tolist()
+    q, size = _expect(s, "q", s["wq"], rot, neox, at)
+    _close(to64(out)[live], q[live], size[live], dtype)
+    k, size = _expect(s, "k", s["wk"], rot, neox, at)
+    page = s["indices"].long()[s["indptr"].long()[s["req"][live].long()] + s["pos"][live].long() // ps]
+    slot = s["pos"][live].long() % ps
+    got = cache.cpu()
+    _close(to64(got[page, 0, :, slot]), k[live], size[live], dtype)
+    assert torch.equal(got[page, 1, :, slot], s["v"][live])
+    got[page, :, :, slot] = s["cache"][page, :, :, slot]
+    assert torch.equal(got.view(torch.int16), s["cache"].view(torch.int16))
+    assert bskv.bskv_get_device_status() == 0
+
+
 def test_strided_in_place_and_halves(cuda):
     """q, k and v as parts of one projection's output, q rotated in place, a cache in another order; and the
     same from two calls, of the queries and of the rest."""
