@@ -669,15 +669,16 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     key_hi = order_key(__fadd_ru(threshold, 2.f * err));
     key_lo = order_key(__fadd_rd(threshold, -2.f * err));
   }
-  int above = 0, between = 0;
+  int counts = 0;  // keys above key_hi, and in the upper half word those from key_lo on: both below 2^16
+  static_assert(kSelectMaxBlocks < 1 << 16, "two counts in a word");
   for (int i = tid; i < fours; i += kThreads) {
     const uint4 x = keys4[i];
-    above += (x.x > key_hi) + (x.y > key_hi) + (x.z > key_hi) + (x.w > key_hi);
-    between += (x.x >= key_lo) + (x.y >= key_lo) + (x.z >= key_lo) + (x.w >= key_lo);
+    counts += (x.x > key_hi) + (x.y > key_hi) + (x.z > key_hi) + (x.w > key_hi);
+    counts += ((x.x >= key_lo) + (x.y >= key_lo) + (x.z >= key_lo) + (x.w >= key_lo)) << 16;
   }
-  above = block_sum(above, warp_sums, buf);
   if (tid == 0) few_n = 0;
-  between = block_sum(between, warp_sums, buf) - above;
+  counts = block_sum(counts, warp_sums, buf);
+  const int above = counts & 0xffff, between = int(unsigned(counts) >> 16) - above;
   const int want = k - above;  // of those between
   // Candidates stay whose key is above `sure`, and of those with the key `tie` the first `rest`.
   uint32_t sure = key_hi, tie = key_lo;
@@ -780,11 +781,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     part_tie[warp] = ties;
   }
   __syncthreads();
-  int at = 0, eq = 0;
-  for (int w = 0; w < warp; ++w) {
-    at += part_in[w];
-    eq += part_tie[w];
-  }
+  int at = __reduce_add_sync(0xffffffffu, lane < warp ? part_in[lane] : 0), eq = __reduce_add_sync(0xffffffffu, lane < warp ? part_tie[lane] : 0);
   at += p.sink + min(eq, rest);
   const uint32_t below = (1u << lane) - 1;
   for (int i = r0 + lane; i - lane < r1; i += 32) {
