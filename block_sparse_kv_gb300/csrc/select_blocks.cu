@@ -349,7 +349,9 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const 
   constexpr int kWarps = kScoreThreads / 32;
   extern __shared__ uint4 ring[];
   __shared__ RoundInfo infos[kWarps][kScoreStages];
-  __shared__ int warp_sums[kWarps], before[kSelectSlice + 1];  // rounds of the queries before each
+  // rounds of the queries before each; the place of its request's pages, the blocks that it sees
+  __shared__ int warp_sums[kWarps], before[kSelectSlice + 1], starts[kSelectSlice];
+  __shared__ uint16_t seen[kSelectSlice];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   launch_dependents();  // the selection's CTAs wait for all of this kernel
   // rounds of each query, added up
@@ -359,8 +361,10 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const 
     int own = 0;
     for (int t = t0; t < t1; ++t) {
       const int b = __ldg(p.batch_indices + t), pos = __ldg(p.positions + t);
-      const int n = b < 0 ? 0 : row_of(p, b, pos).n;
-      before[t] = n > p.top_k ? (n - p.sink - p.recent + kTake - 1) / kTake : 0;
+      const Row x = b < 0 ? Row{0, 0} : row_of(p, b, pos);
+      before[t] = x.n > p.top_k ? (x.n - p.sink - p.recent + kTake - 1) / kTake : 0;
+      starts[t] = x.start;
+      seen[t] = uint16_t(x.n);
       own += before[t];
     }
     int v = own;
@@ -420,11 +424,10 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const 
       const int from = r - before[t], rounds = int(min(int64_t(before[t + 1] - r), stop - todo));
       todo += rounds;
       if (h >= int(p.heads.d)) continue;  // the last group may have fewer heads
-      const Row x = row_of(p, __ldg(p.batch_indices + t), __ldg(p.positions + t));
-      row_end = x.n - p.sink - p.recent;
+      row_end = seen[t] - p.sink - p.recent;
       at = from * kTake;
       end = min(row_end, at + rounds * kTake);
-      pages = p.kv_indices + x.start + p.sink;
+      pages = p.kv_indices + starts[t] + p.sink;
       head = p.bounds + 16 * sub + h * p.b_s1;
       first = kFirst;
       window = at;
