@@ -166,7 +166,7 @@ inline bool fp4_page_size(int32_t page_size) {
 // memory. The attention's workers are teams of warps: the rows' lists of top_k
 // blocks, in steps of 16 tokens, one after another, cut into equal runs.
 constexpr int kSelectMaxBlocks = 49152;
-constexpr int kSelectSlice = 1024;  // queries that are selected for at a time (they share the workspace)
+constexpr int kSelectSlice = 2048;  // queries that are selected for at a time (they share the workspace)
 constexpr int kSelectWide = 2048;   // more blocks than these are selected from by 1024 threads
 constexpr int kBlocksWarps = 8;
 constexpr int kBlocksMinSteps = 2;  // per warp of a worker
