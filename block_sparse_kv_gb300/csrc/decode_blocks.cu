@@ -6,7 +6,9 @@
 //
 // Bound by reading K and V of the listed blocks: a block of one head is a piece of page_size * D 16-bit
 // values, wherever its page lies. One CTA per SM, eight warps with a ring of copies each, up to 192 KB in flight.
-// The up to 16 query heads of a group are the M = 16 rows of mma.sync m16n8k16 against 16 tokens at a time.
+// The up to 16 query heads of a group are the M = 16 rows of mma.sync m16n8k16 against 16 tokens at a time. The
+// weights go into the product with V as sums of two 16-bit values: of up to eight heads both parts are rows of one
+// product, more heads take two.
 //
 // Split. The lists' lengths are known on the GPU only, so the cut is made in places: the rows' lists of top_k blocks
 // follow one another in steps of 16 tokens (or pages of 8), and each team of 1, 2, 4 or 8 warps takes an equal run of
@@ -20,6 +22,7 @@
 // blocks 28.7, 18.1, 12.6, 13.0. The plan's rule is at blocks_team().
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "cache_common.cuh"
 #include "internal.h"
@@ -178,9 +181,23 @@ __device__ __forceinline__ uint32_t tile_row(uint32_t base, int r, int hf, uint3
   return base + hf * (2 * kPanel) + (r >> 3) * eight + (r & 7) * 128;
 }
 
-// One tile of 16 tokens for the (up to 16) query heads of a row. v0 and v1 of the two groups of eight
-// tokens are attended to.
-template <typename T, int D>
+// Two weights as sums of two 16-bit values each: what the first leaves of them, half a step of theirs at most, is
+// held by the second to half a step of its own.
+template <typename T>
+__device__ __forceinline__ void two_parts(float a, float b, uint32_t& first, uint32_t& second) {
+  first = MmaOp<T>::pack(a, b);
+  float2 f;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    f = make_float2(__uint_as_float(first << 16), __uint_as_float(first & 0xffff0000u));
+  else
+    f = __half22float2(*reinterpret_cast<const __half2*>(&first));
+  second = MmaOp<T>::pack(a - f.x, b - f.y);
+}
+
+// One tile of 16 tokens for the query heads of a row: up to eight, or WIDE up to 16. v0 and v1 of the two groups of
+// eight tokens are attended to. With up to eight heads o[n][2] and o[n][3], the accumulators of rows 8 to 15, belong to
+// the weights' second parts.
+template <typename T, int D, bool WIDE>
 __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, uint32_t eight, int v0, int v1, float scale_log2, int lane,
                                             const uint32_t (&qa)[D / 16][4], float (&o)[D / 8][4], float& m0,
                                             float& m1, float& l0, float& l1) {
@@ -211,30 +228,36 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, uint32
   for (int nt = 0; nt < 2; ++nt) {
     const int valid = nt ? v1 : v0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[nt][e] = 2 * cq + (e & 1) < valid ? s[nt][e] * scale_log2 : -INFINITY;
+    for (int e = 0; e < (WIDE ? 4 : 2); ++e) s[nt][e] = 2 * cq + (e & 1) < valid ? s[nt][e] * scale_log2 : -INFINITY;
     mx0 = fmaxf(mx0, fmaxf(s[nt][0], s[nt][1]));
-    mx1 = fmaxf(mx1, fmaxf(s[nt][2], s[nt][3]));
+    if constexpr (WIDE) mx1 = fmaxf(mx1, fmaxf(s[nt][2], s[nt][3]));
   }
   mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
   mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-  mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-  mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-  const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-  const float a0 = fast_exp2(m0 - mn0), a1 = fast_exp2(m1 - mn1);
+  const float mn0 = fmaxf(m0, mx0), a0 = fast_exp2(m0 - mn0);
   m0 = mn0;
-  m1 = mn1;
+  float mn1 = 0.f, a1 = a0;
+  if constexpr (WIDE) {
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+    mn1 = fmaxf(m1, mx1);
+    a1 = fast_exp2(m1 - mn1);
+    m1 = mn1;
+  }
   float ps0 = 0.f, ps1 = 0.f;
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt) {
     s[nt][0] = fast_exp2(s[nt][0] - mn0);
     s[nt][1] = fast_exp2(s[nt][1] - mn0);
-    s[nt][2] = fast_exp2(s[nt][2] - mn1);
-    s[nt][3] = fast_exp2(s[nt][3] - mn1);
     ps0 += s[nt][0] + s[nt][1];
-    ps1 += s[nt][2] + s[nt][3];
+    if constexpr (WIDE) {
+      s[nt][2] = fast_exp2(s[nt][2] - mn1);
+      s[nt][3] = fast_exp2(s[nt][3] - mn1);
+      ps1 += s[nt][2] + s[nt][3];
+    }
   }
   l0 = l0 * a0 + ps0;
-  l1 = l1 * a1 + ps1;
+  if constexpr (WIDE) l1 = l1 * a1 + ps1;
 #pragma unroll
   for (int n = 0; n < D / 8; ++n) {
     o[n][0] *= a0;
@@ -242,9 +265,20 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, uint32
     o[n][2] *= a1;
     o[n][3] *= a1;
   }
-  // weights at most 1 round to 16 bits for the product with V
-  const uint32_t pa[4] = {Mma::pack(s[0][0], s[0][1]), Mma::pack(s[0][2], s[0][3]), Mma::pack(s[1][0], s[1][1]),
-                          Mma::pack(s[1][2], s[1][3])};
+  // The product with V takes weights of 16 bits. Rounded to those they made the output's error against 64 bits a quarter
+  // larger than its own rounding does (bf16: 2.1e-3 of its norm, so 1.65e-3); in two parts they add nothing to be seen.
+  // Times are the same for up to eight heads (64 requests of 8 x 4 heads 47.9 and 47.7 us), for 16 heads 49.5 and 50.4
+  // with 128 dims, 66.5 and 69.9 with 64.
+  uint32_t pa[4], pb[4];
+  two_parts<T>(s[0][0], s[0][1], pa[0], pb[0]);
+  two_parts<T>(s[1][0], s[1][1], pa[2], pb[2]);
+  if constexpr (WIDE) {
+    two_parts<T>(s[0][2], s[0][3], pa[1], pb[1]);
+    two_parts<T>(s[1][2], s[1][3], pa[3], pb[3]);
+  } else {
+    pa[1] = pb[0];
+    pa[3] = pb[2];
+  }
   {
     const int mi = lane >> 3, r = (mi & 1) * 8 + (lane & 7);
 #pragma unroll
@@ -254,6 +288,10 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, uint32
       ldsm_x4_t(tile_row(v_at, r, dim / 64, eight) + ((((dim % 64) / 8) ^ (r & 7)) << 4), b0, b1, b2, b3);
       Mma::run(o[2 * dd], pa, b0, b1);
       Mma::run(o[2 * dd + 1], pa, b2, b3);
+      if constexpr (WIDE) {
+        Mma::run(o[2 * dd], pb, b0, b1);
+        Mma::run(o[2 * dd + 1], pb, b2, b3);
+      }
     }
   }
 }
@@ -262,7 +300,7 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, uint32
 // that neither the fragments' stores nor the joining threads' loads meet in a bank more than twice.
 __device__ __forceinline__ int state_at(int row, int g, int d, int D) { return row * D + (d ^ ((g & 7) << 2)); }
 
-template <typename T, int D, int STAGES>
+template <typename T, int D, bool WIDE, int STAGES>
 __global__ void __launch_bounds__(kWarps * 32, 1)
     decode_blocks_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ BlocksParams p) {
   using R = Ring<D, STAGES>;
@@ -362,9 +400,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       for (int kk = 0; kk < D / 16; ++kk) {
         const int d = kk * 16 + 2 * cq;
         qa[kk][0] = r0 < p.group ? __ldg(reinterpret_cast<const uint32_t*>(q + r0 * p.q_s1 + d)) : 0u;
-        qa[kk][1] = r1 < p.group ? __ldg(reinterpret_cast<const uint32_t*>(q + r1 * p.q_s1 + d)) : 0u;
+        qa[kk][1] = WIDE && r1 < p.group ? __ldg(reinterpret_cast<const uint32_t*>(q + r1 * p.q_s1 + d)) : 0u;
         qa[kk][2] = r0 < p.group ? __ldg(reinterpret_cast<const uint32_t*>(q + r0 * p.q_s1 + d + 8)) : 0u;
-        qa[kk][3] = r1 < p.group ? __ldg(reinterpret_cast<const uint32_t*>(q + r1 * p.q_s1 + d + 8)) : 0u;
+        qa[kk][3] = WIDE && r1 < p.group ? __ldg(reinterpret_cast<const uint32_t*>(q + r1 * p.q_s1 + d + 8)) : 0u;
       }
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
@@ -374,7 +412,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (ok) ok = warp_wait(&bars[stage], (consumed / STAGES) & 1u, p.st, forced);
     if (ok) {
       const uint32_t at = smem_u32(ring + stage * R::kStageBytes);
-      if (info.valid) attend_tile<T, D>(at, at + v_at, eight, info.valid & 0xffff, info.valid >> 16, p.scale_log2, lane, qa, o, m0, m1, l0, l1);
+      if (info.valid) attend_tile<T, D, WIDE>(at, at + v_at, eight, info.valid & 0xffff, info.valid >> 16, p.scale_log2, lane, qa, o, m0, m1, l0, l1);
       ++consumed;
       __syncwarp();
       if (lane == 0) fence_proxy_async_smem();
@@ -386,8 +424,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     // this warp's state, relative to its own maximum
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if constexpr (WIDE) {
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    } else {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][0] += o[n][2];
+        o[n][1] += o[n][3];
+      }
+    }
     if (r0 < p.group) {
       if (cq == 0) {
         top[warp][r0] = m0;
@@ -397,7 +443,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       for (int n = 0; n < D / 8; ++n)
         *reinterpret_cast<float2*>(states + state_at(warp * p.group + r0, r0, n * 8 + 2 * cq, D)) = make_float2(o[n][0], o[n][1]);
     }
-    if (r1 < p.group) {
+    if (WIDE && r1 < p.group) {
       if (cq == 0) {
         top[warp][r1] = m1;
         sum[warp][r1] = l1;
@@ -495,10 +541,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
 }
 
-template <typename T, int D, int STAGES>
+template <typename T, int D, bool WIDE, int STAGES>
 bskv_status launch(const CUtensorMap& map, const BlocksParams& p, int grid, cudaStream_t st) {
   using R = Ring<D, STAGES>;
-  auto kern = decode_blocks_kernel<T, D, STAGES>;
+  auto kern = decode_blocks_kernel<T, D, WIDE, STAGES>;
   static_assert(sizeof(StageInfo) <= 16, "stage infos");
   const size_t smem = 1024 + kWarps * (R::kBytes + STAGES * (8 + 16)) + size_t(kWarps) * p.group * D * 4;
   static std::atomic<int> allowed[64];
@@ -511,8 +557,8 @@ bskv_status launch(const CUtensorMap& map, const BlocksParams& p, int grid, cuda
 // dims these take 64 KB.
 template <typename T>
 bskv_status launch_any(const CUtensorMap& map, const BlocksParams& p, int D, int grid, cudaStream_t st) {
-  if (D == 64) return launch<T, 64, 5>(map, p, grid, st);
-  return p.group <= 8 ? launch<T, 128, 3>(map, p, grid, st) : launch<T, 128, 2>(map, p, grid, st);
+  if (p.group <= 8) return D == 64 ? launch<T, 64, false, 5>(map, p, grid, st) : launch<T, 128, false, 3>(map, p, grid, st);
+  return D == 64 ? launch<T, 64, true, 5>(map, p, grid, st) : launch<T, 128, true, 2>(map, p, grid, st);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
