@@ -470,10 +470,12 @@ bskv_status bskv_run_evict_fp4(const bskv_plan* plan, float* scores, const int64
  * The blocks that each query and kv head attends to, for a plan of bskv_plan_decode_blocks. Query row t is
  * token positions[t] of request batch_indices[t] and sees the request's blocks 0 .. positions[t] /
  * page_size. Of a block, with bounds lo and hi, the score is the sum over the query heads r of the kv head's group of
- *   sum_d max(q[t, r, d] lo_d, q[t, r, d] hi_d),
- * which no sum of the group's logits with one of the block's keys exceeds (for lo <= hi). Besides the first `sink` and the last
+ *   sum_d max(q[t, r, d] lo_d, q[t, r, d] hi_d), for lo_d <= hi_d as the bounds are written,
+ * which no sum of the group's logits with one of the block's keys exceeds. (Each term is q hi_d where q is above zero, q lo_d
+ * where it is below, whatever the other bound is, and of q = 0 it is 0, or NaN beside an infinite bound; a bound that is NaN makes
+ * the score NaN.) Besides the first `sink` and the last
  * `recent` blocks those of highest score are chosen, as 64-bit arithmetic orders them (NaN as the highest, the lowest
- * block among equals). Scores have to stay within fp32's range; infinite ones are equal.
+ * block among equals). Scores have to stay within fp32's range unless a value is infinite; infinite scores are equal.
  *   q [num_tokens, num_qo_heads, head_dim], strides {row, head} in multiples of 8 elements; bounds as
  *     bskv_block_bounds_paged writes them; kv_indptr [batch + 1] and kv_indices on the device.
  *   blocks [num_tokens, num_kv_heads, top_k] int32 contiguous: the chosen blocks ascending, -1 behind

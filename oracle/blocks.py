@@ -55,10 +55,13 @@ def block_bounds(cache, page, fill):
 
 
 def block_scores(q, bounds):
-    """q [group, D] and bounds [blocks, 2, D] -> scores [blocks]."""
+    """q [group, D] and bounds [blocks, 2, D] -> scores [blocks]: each head's greatest possible logit, summed over the
+    heads, term by term max(q lo, q hi) of bounds in order. Out of order the sign of q says which is meant; zero times an
+    infinite bound is NaN, and a bound that is NaN stays NaN."""
+    q, lo, hi = np.asarray(q, dtype=np.float64)[:, None, :], bounds[None, :, 0], bounds[None, :, 1]
     with np.errstate(invalid="ignore"):
-        plus, minus = np.maximum(q, 0.0).sum(0), np.minimum(q, 0.0).sum(0)
-        return (bounds[:, 1] * plus).sum(-1) + (bounds[:, 0] * minus).sum(-1)
+        term = np.where(q > 0, q * hi, np.where(q < 0, q * lo, q * lo + q * hi))
+        return np.where(np.isnan(lo) | np.isnan(hi), np.nan, term).sum((0, 2))
 
 
 def select(scores, top_k, sink, recent):

@@ -52,3 +52,74 @@ def test_weights_keep_more_than_16_bits(cuda, group, d, ps, dtype):
             bad = ~(np.abs(to64(out[t, h * group:(h + 1) * group]) - want) <= tol)
             assert not bad.any(), (t, h, int(bad.sum()), float((np.abs(to64(out[t, h * group:(h + 1) * group]) - want) / tol).max()))
             assert (np.abs(to64(lse[t, h * group:(h + 1) * group]) - z) <= 4 * rel[:, 0] + 2.0 ** -22 * np.abs(z)).all()
+
+
+# ---- the choice -------------------------------------------------------------------------
+
+KINDS = ["masked", "lower", "upper", "one sign", "zero", "query", "near", "lost page"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("blocks,ps,hkv,group,d,dtype", [(60, 16, 2, 1, 128, BF), (300, 8, 1, 3, 64, FP), (2500, 8, 1, 2, 64, BF),
+                                                        (2100, 8, 1, 1, 128, FP)])
+def test_choice_by_infinite_bounds(cuda, kind, blocks, ps, hkv, group, d, dtype):
+    """Bounds of keys that are infinite, by which the choice is still that of the sum of max(q lo, q hi)."""
+    g = torch.Generator().manual_seed(len(kind))
+    lens, new, top, sink, recent = [blocks * ps - 3, 5 * ps], [2, 1], 20, 1, 2
+    s = batch(lens, new, ps, 3)
+    n, hq = sum(new), hkv * group
+    kv = torch.randn(s["pages"], 2, hkv, ps, d, generator=g).to(dtype)
+    q = torch.randn(n, hq, d, generator=g).to(dtype)
+    row = pages_of(s, 0)
+    pick = lambda m: torch.tensor(row[torch.randperm(blocks - 4, generator=g)[:m].numpy() + 1])  # noqa: E731
+    q[:, :, 7] = q[:, :, 7].abs() + 0.5
+    q[:, :, 9] = -q[:, :, 9].abs() - 0.5
+    inf = float("inf")
+    if kind == "near":  # most blocks differ in what fp32 sums lose
+        kv[:, 0] = kv[row[0], 0, :, :1].expand_as(kv[:, 0]).clone() * 64
+        kv[:, 0, :, 0, d // 2] = (torch.randint(0, 2, kv[:, 0, :, 0, 0].shape, generator=g) * 2.0 ** -12).to(dtype)
+        kv[:, 0, :, 1:, d // 2] = 0
+        q[:, :, d // 2] = 1.0
+    if kind == "masked":  # every key of a block, as a mask does; most blocks of the row, or a few
+        kv[pick(blocks - 4 - (top // 2 if d == 64 else 2 * top)), 0, :, :, 7] = -inf
+    if kind in ("lower", "near", "one sign", "lost page"):  # a key only: the block counts by its others
+        kv[pick(blocks // 3), 0, :, 2, 7] = -inf
+    if kind in ("upper", "one sign", "lost page"):
+        kv[pick(blocks // 3), 0, :, 2, 9] = inf
+    if kind == "one sign":  # some heads the other way: the score is infinite
+        q[1, ::2, 7] = -1.0
+        q[1, :, 9] = -1.0
+        kv[pick(5), 0, :, 1, 9] = -inf
+    if kind == "zero":  # a product with zero is not a number
+        q[0, 0, 7] = 0.0
+        q[1, :, 7] = -0.0
+        kv[pick(top // 2), 0, :, 3, 7] = -inf
+    if kind == "query":
+        q[0, 0, 11] = inf
+        q[1, 0, 11] = float("nan")
+    cache, bounds = kv.to(cuda), torch.zeros(s["pages"], hkv, 2, d, dtype=dtype, device=cuda)
+    whole = batch(lens, lens, ps, 3)
+    bskv.bskv_block_bounds_paged(cache, bounds, *lists(whole, cuda), s["last"].to(cuda))
+    assert bskv.bskv_get_device_status() == 0
+    b64, q64 = to64(bounds), to64(q)
+    req, pos, indptr, indices = lists(s, cuda)
+    lost = []
+    if kind == "lost page":
+        lost = [3, 4, blocks // 2]
+        indices[lost] = s["pages"]
+    p = bskv.bskv_plan_decode_blocks(n, blocks, s["pages"], ps, hq, hkv, d, top, sink, recent, dtype)
+    for _ in range(2):
+        got = bskv.bskv_run_select_blocks(p, q.to(cuda), bounds, req, pos, indptr, indices).cpu().numpy()
+        assert bskv.bskv_get_device_status() == (6 if lost else 0)
+        for t in range(n):
+            pages = pages_of(s, int(s["req"][t]))[:int(s["pos"][t]) // ps + 1]
+            for h in range(hkv):
+                x = q64[t, h * group:(h + 1) * group]
+                score = ob.block_scores(x, b64[pages, h])
+                with np.errstate(invalid="ignore"):
+                    direct = np.maximum(x[:, None] * b64[None, pages, h, 0], x[:, None] * b64[None, pages, h, 1]).sum((0, 2))
+                if kind != "query":  # there a product of infinity and zero may stand beside the greater one
+                    np.testing.assert_allclose(score, direct, rtol=1e-12, atol=1e-9)
+                if int(s["req"][t]) == 0:
+                    score[lost] = -np.inf
+                assert got[t, h].tolist() == ob.select(score, top, sink, recent), (t, h)

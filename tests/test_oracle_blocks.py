@@ -60,3 +60,19 @@ def test_attend_is_a_softmax():
     assert (size >= np.abs(out)).all()
     out, lse, _ = ob.attend(q, k[:0], v[:0], 0.5)
     assert (out == 0).all() and (lse == -np.inf).all()
+
+
+def test_scores_of_infinite_bounds_are_the_sums_of_greater_products():
+    """A channel whose bounds are infinite on either side or both, under queries of one sign, of both, and of zero."""
+    inf = np.inf
+    pairs = [(-inf, -inf), (-inf, 2.0), (-3.0, inf), (-inf, inf), (inf, inf), (1.0, 2.0)]
+    bounds = np.ones((len(pairs), 2, 3))
+    bounds[:, 0, 1], bounds[:, 1, 1] = [x[0] for x in pairs], [x[1] for x in pairs]
+    for q1 in ([0.5], [-0.5], [0.0], [0.5, 2.0], [-0.5, -1.0], [0.5, -1.0], [0.0, 3.0]):
+        q = np.full((len(q1), 3), 0.25)
+        q[:, 1] = q1
+        with np.errstate(invalid="ignore"):
+            direct = np.maximum(q[:, None] * bounds[None, :, 0], q[:, None] * bounds[None, :, 1]).sum((0, 2))
+        np.testing.assert_array_equal(ob.block_scores(q, bounds), direct)
+    assert ob.block_scores(np.full((1, 3), 0.25), bounds)[0] == -inf  # no key of it can have weight
+    assert ob.block_scores(np.full((1, 3), 0.25), bounds)[1] == 1.0
