@@ -646,6 +646,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const _
   const int t = p.heads.divmod(row, h);
   const int b = __ldg(p.batch_indices + t), pos = __ldg(p.positions + t);
   const Row r = b < 0 ? Row{0, 0} : row_of(p, b, pos);
+  if (h == 0) {  // the pages of blocks that are listed without a score, the same for all heads; the scores are still made
+    const int listed = r.n <= p.top_k ? r.n : p.sink + p.recent;
+    for (int j = tid; j < listed; j += kThreads) {
+      const int pg = __ldg(p.kv_indices + r.start + (r.n <= p.top_k || j < p.sink ? j : r.n - listed + j));
+      if (pg < 0 || pg >= p.num_pages) record_error(p.st, BSKV_ERR_DEVICE_INDEX);
+    }
+  }
   wait_for_prior_grid();
   if (b < 0) return;  // a row without a token
   int32_t* out = p.blocks + int64_t(row) * p.top_k;

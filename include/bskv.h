@@ -481,8 +481,9 @@ bskv_status bskv_run_evict_fp4(const bskv_plan* plan, float* scores, const int64
  *   blocks [num_tokens, num_kv_heads, top_k] int32 contiguous: the chosen blocks ascending, -1 behind
  *     the last where the query sees fewer.
  *   Rows with a negative batch_indices have no token: their part of blocks is left as it was. A row that is out of range,
- *   or sees more than max_blocks, gets -1 everywhere, a block whose page id is out of range the lowest score; both raise
- *   BSKV_ERR_DEVICE_INDEX in the device status word.
+ *   or sees more than max_blocks, gets -1 everywhere; a block whose page id is out of range has the lowest score, and is
+ *   listed where it is listed without one (the first, the last, and all of a row that sees at most top_k). Both raise
+ *   BSKV_ERR_DEVICE_INDEX in the device status word. A block that is neither listed nor scored is not looked at.
  *   float_ws as for bskv_run_decode. Runs of one plan share its workspaces and must not overlap on the GPU.
  */
 bskv_status bskv_run_select_blocks(

@@ -123,3 +123,35 @@ def test_choice_by_infinite_bounds(cuda, kind, blocks, ps, hkv, group, d, dtype)
                 if int(s["req"][t]) == 0:
                     score[lost] = -np.inf
                 assert got[t, h].tolist() == ob.select(score, top, sink, recent), (t, h)
+
+
+@pytest.mark.parametrize("bad", ["first", "last", "short row", "scored", "unseen", "no token"])
+@pytest.mark.parametrize("top,hkv", [(12, 2), (3, 3)])  # with 3 there is no choice: the first and the last are all
+def test_pages_out_of_range_are_reported(cuda, bad, top, hkv):
+    """Whether a block is listed by its place or competes by its score."""
+    g = torch.Generator().manual_seed(7)
+    ps, d, sink, recent = 16, 64, 1, 2
+    s = batch([640, 100, 640], [1, 2, 1], ps, 1)
+    s["pos"][3] = 299  # sees 19 of 40 blocks
+    req, pos, indptr, indices = lists(s, cuda)
+    at = {"first": 0, "last": 38, "short row": 40 + 5, "scored": 20, "unseen": 47 + 30, "no token": 41}[bad]
+    n = 4
+    if bad == "short row" and top == 3:
+        at = 40 + 6
+    if bad == "no token":
+        req[1:3] = -1
+    q = torch.randn(n, 2 * hkv, d, generator=g).to(BF)
+    bounds = torch.randn(s["pages"], hkv, 2, d, generator=g).sort(2).values.to(BF)
+    p = bskv.bskv_plan_decode_blocks(n, 40, s["pages"], ps, 2 * hkv, hkv, d, top, sink, recent, BF)
+    want = bskv.bskv_run_select_blocks(p, q.to(cuda), bounds.to(cuda), req, pos, indptr, indices)
+    assert bskv.bskv_get_device_status() == 0
+    for value in (s["pages"], -1):
+        indices[at] = value
+        got = bskv.bskv_run_select_blocks(p, q.to(cuda), bounds.to(cuda), req, pos, indptr, indices)
+        # a block that neither competes nor is listed is not looked at
+        assert bskv.bskv_get_device_status() == (0 if bad in ("unseen", "no token") or (bad == "scored" and top == 3) else 6)
+        live = (req >= 0).nonzero()[:, 0]
+        if bad != "scored":
+            assert torch.equal(got[live], want[live])
+        else:
+            assert top == 3 or not (got[0] == at).any()
