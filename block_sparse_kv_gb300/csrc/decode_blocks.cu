@@ -572,9 +572,9 @@ BlocksWorkspace blocks_workspace(const bskv_plan* plan) {
   const size_t slots = rows + size_t(plan->workers);
   w.stride = int(blocks);
   size_t at = 0;
-  const size_t slice = std::min(rows, size_t(kSelectSlice) * size_t(plan->num_kv_heads));
-  w.exact = at; at += align256(slice * blocks * 8);
-  w.scores = at; at += align256(slice * blocks * 4);
+  const size_t heads = size_t(std::max(1, plan->num_kv_heads)), query = heads * blocks * 4;
+  w.slice = int64_t(std::min(std::max<size_t>(1, kSelectBytes / query), size_t(kSelectSlice)));
+  w.scores = at; at += align256(std::min(rows, size_t(w.slice) * heads) * blocks * 4);
   w.states = at; at += align256(slots * group * size_t(plan->head_dim) * 4);
   w.lse = at; at += align256(slots * group * 4);
   w.total = at;

@@ -166,7 +166,11 @@ inline bool fp4_page_size(int32_t page_size) {
 // memory. The attention's workers are teams of warps: the rows' lists of top_k
 // blocks, in steps of 16 tokens, one after another, cut into equal runs.
 constexpr int kSelectMaxBlocks = 49152;
-constexpr int kSelectSlice = 2048;  // queries that are selected for at a time (they share the workspace)
+// Queries that are selected for at a time share the workspace's scores: as many as fit kSelectBytes, at least one, at
+// most kSelectSlice. (2048 queries of 131072 tokens and 8 kv heads take 9.2 ms with room for all, 512 MB, 9.4 with 64 MB,
+// 9.8 with 16; 1024 of 65536 tokens 2.52, 2.49 and 2.58.)
+constexpr int kSelectSlice = 2048;
+constexpr size_t kSelectBytes = size_t(64) << 20;
 constexpr int kSelectWide = 2048;   // more blocks than these are selected from by 1024 threads
 constexpr int kBlocksWarps = 8;
 constexpr int kBlocksMinSteps = 2;  // per warp of a worker
@@ -246,11 +250,12 @@ struct bskv_plan {
 
 namespace bskv {
 
-// Where a block-sparse plan's parts of the float workspace begin (bytes): fp64 keys and fp32 scores
-// of the selection, partial states of the attention.
+// Where a block-sparse plan's parts of the float workspace begin (bytes): scores of the selection,
+// partial states of the attention.
 struct BlocksWorkspace {
-  size_t exact, scores, states, lse, total;
-  int stride;  // blocks from one row's scores to the next's
+  size_t scores, states, lse, total;
+  int stride;     // blocks from one row's scores to the next's
+  int64_t slice;  // queries whose scores there is room for
 };
 BlocksWorkspace blocks_workspace(const bskv_plan* plan);
 

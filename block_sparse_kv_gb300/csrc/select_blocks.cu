@@ -260,9 +260,8 @@ struct SelectParams {
   int64_t b_s0, b_s1;  // bytes: page, kv head
   const int32_t *batch_indices, *positions, *kv_indptr, *kv_indices;
   int32_t* blocks;
-  float* scores;               // [rows][stride]
+  float* scores;               // [rows][stride]; then the upper halves of fp64 scores' keys
   unsigned* most;              // [rows]: bounds of the sums of absolute products, zero between runs
-  unsigned long long* exact;   // [rows][stride]: keys of fp64 scores
   int group, batch, num_pages, max_blocks, stride, top_k, sink, recent;
   int queries;
   int set_heads, sets, head_groups;  // scoring: warps (kv heads) of a set, sets of a CTA, sets' worth of heads
@@ -351,9 +350,9 @@ struct RoundInfo {
 };
 constexpr uint32_t kFirst = 1u << 30, kLast = 1u << 31;
 
-// KEPT: what each query sees is kept from the count of the rounds, for up to kKept queries (64 requests 43.3 against
-// 43.8 us, a step of long requests 42.5 against 43.2). Slices of more queries look it up again: 4096 queries of 4096 and
-// 16384 tokens took 101 and 1076 us, in slices of kKept 121 and 1106.
+// KEPT: what each query sees is kept from the count of the rounds, for up to kKept queries (64 requests 43.1 against
+// 43.7 us, one 18.6 against 19.1, a step of long requests 42.2 against 42.7, in turn and within 0.1). Slices of more
+// queries look it up again: 4096 queries of 4096 and 16384 tokens took 101 and 1076 us, in slices of kKept 121 and 1106.
 template <typename T, int D, bool KEPT>
 __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const __grid_constant__ SelectParams p) {
   constexpr int kLanes = D / 4;       // lanes of 16 bytes that hold a block's bounds
@@ -633,7 +632,7 @@ __device__ __noinline__ float score_again(const SelectParams& p, int t, int h, c
 template <typename T, int D, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const __grid_constant__ SelectParams p) {
   constexpr int kLanes = D / 4, kThreads = THREADS, kWarps = THREADS / 32;
-  extern __shared__ __align__(16) uint32_t keys[];  // of the row's candidates, zeros up to a multiple of four
+  extern __shared__ __align__(16) uint32_t keys[];  // of the row's candidates, zeros up to a multiple of four; marks
   __shared__ int warp_sums[2][kWarps], part_in[kWarps], part_tie[kWarps];
   __shared__ uint32_t warp_lo[kWarps], warp_hi[kWarps];
   __shared__ int few_at[kFew], few_n, bins[kBins], found_bin, found_n, found_wanted;
@@ -852,20 +851,27 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const _
         keys[few_at[tid]] = rank < want ? 0xffffffffu : 0u;
       }
     } else {
-      unsigned long long* exact = p.exact + int64_t(row) * p.stride;
+      // the fp64 keys' halves take the places of the fp32 scores and of their keys; a bit marks each
+      uint32_t *marks = keys + p.stride, *upper = reinterpret_cast<uint32_t*>(scores);
       for (int i = warp * 32; i < m; i += kThreads) {
         const uint32_t key = i + lane < m ? keys[i + lane] : 0u;
-        for (uint32_t todo = __ballot_sync(0xffffffffu, key >= key_lo && key <= key_hi); todo; todo &= todo - 1) {
+        const uint32_t mark = __ballot_sync(0xffffffffu, key >= key_lo && key <= key_hi);
+        if (lane == 0) marks[i >> 5] = mark;
+        for (uint32_t todo = mark; todo; todo &= todo - 1) {
           const int at = i + __ffs(todo) - 1;
           const unsigned long long k64 = score64(at);
-          if (lane == 0) exact[at] = k64;
+          if (lane == 0) {
+            upper[at] = uint32_t(k64 >> 32);
+            keys[at] = uint32_t(k64);
+          }
         }
       }
       __syncthreads();
+      auto marked = [&](int i) { return (marks[i >> 5] >> (i & 31) & 1u) != 0; };
+      auto exact = [&](int i) { return (unsigned long long)(upper[i]) << 32 | keys[i]; };
       auto count = [&](unsigned long long from) {
         int cnt = 0;
-        for (int i = tid; i < m; i += kThreads)
-          cnt += keys[i] >= key_lo && keys[i] <= key_hi && exact[i] >= from;
+        for (int i = tid; i < m; i += kThreads) cnt += marked(i) && exact(i) >= from;
         return block_sum(cnt, warp_sums, buf);
       };
       unsigned long long kth64 = 0;
@@ -873,7 +879,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const _
         if (count(kth64 | (1ull << bit)) >= want) kth64 |= 1ull << bit;
       rest = want - (kth64 == ~0ull ? 0 : count(kth64 + 1));
       for (int i = tid; i < m; i += kThreads)
-        if (keys[i] >= key_lo && keys[i] <= key_hi) keys[i] = exact[i] > kth64 ? 0xffffffffu : exact[i] == kth64 ? key_hi : 0u;
+        if (marked(i)) keys[i] = exact(i) > kth64 ? 0xffffffffu : exact(i) == kth64 ? key_hi : 0u;
     }
     __syncthreads();
   }
@@ -946,7 +952,7 @@ template <typename T, int D, int THREADS>
 bskv_status launch_select(const SelectParams& p, int64_t rows, bool scored, cudaStream_t st) {
   auto kern = select_kernel<T, D, THREADS>;
   static std::atomic<int> allowed[64];
-  const size_t smem = sizeof(uint32_t) * size_t(p.stride);
+  const size_t smem = sizeof(uint32_t) * (size_t(p.stride) + (size_t(p.stride) + 31) / 32);
   if (bskv_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed, "run_select_blocks: cudaFuncSetAttribute")) return s;
   // it may begin while the scores are made, and waits for them
   cudaLaunchAttribute attr{};
@@ -962,11 +968,11 @@ bskv_status launch_select(const SelectParams& p, int64_t rows, bool scored, cuda
   return cuda_check(cudaLaunchKernelEx(&cfg, kern, p), "run_select_blocks launch");
 }
 
-// Slices of at most kSelectSlice queries, one after the other: the scores of all of them share the workspace.
+// Slices of at most `slice` queries, one after the other: the scores of all of them share the workspace.
 template <typename T, int D>
-bskv_status launch_both(SelectParams p, int64_t queries, int num_sms, cudaStream_t st) {
+bskv_status launch_both(SelectParams p, int64_t queries, int64_t slice, int num_sms, cudaStream_t st) {
   constexpr int kWarps = kScoreThreads / 32;
-  const bool kept = queries <= kKept;
+  const bool kept = std::min(queries, slice) <= kKept;
   auto kern = kept ? score_kernel<T, D, true> : score_kernel<T, D, false>;
   static std::atomic<int> allowed[2][64];
   constexpr size_t smem = size_t(kWarps) * kScoreStages * kAhead * 32 * sizeof(uint4);
@@ -975,8 +981,8 @@ bskv_status launch_both(SelectParams p, int64_t queries, int num_sms, cudaStream
   p.set_heads = std::min(heads, kWarps);
   p.sets = kWarps / p.set_heads;
   p.head_groups = (heads + p.set_heads - 1) / p.set_heads;
-  for (int64_t t0 = 0; t0 < queries; t0 += kSelectSlice) {
-    p.queries = int(std::min<int64_t>(kSelectSlice, queries - t0));
+  for (int64_t t0 = 0; t0 < queries; t0 += slice) {
+    p.queries = int(std::min(slice, queries - t0));
     const bool scored = p.max_blocks > p.top_k && p.top_k > p.sink + p.recent;  // else there is no choice
     if (scored) {
       // rounds that there may be: a set of warps has some of them
@@ -987,10 +993,10 @@ bskv_status launch_both(SelectParams p, int64_t queries, int num_sms, cudaStream
     }
     const int64_t rows = int64_t(p.queries) * heads;
     if (bskv_status s = p.max_blocks > kSelectWide ? launch_select<T, D, 1024>(p, rows, scored, st) : launch_select<T, D, 256>(p, rows, scored, st)) return s;
-    p.q = static_cast<const T*>(p.q) + kSelectSlice * p.q_s0;
-    p.batch_indices += kSelectSlice;
-    p.positions += kSelectSlice;
-    p.blocks += int64_t(kSelectSlice) * heads * p.top_k;
+    p.q = static_cast<const T*>(p.q) + slice * p.q_s0;
+    p.batch_indices += slice;
+    p.positions += slice;
+    p.blocks += slice * heads * p.top_k;
   }
   return BSKV_OK;
 }
@@ -1075,7 +1081,6 @@ extern "C" bskv_status bskv_run_select_blocks(
   p.bounds = static_cast<const uint8_t*>(bounds); p.b_s0 = 2 * bounds_strides[0]; p.b_s1 = 2 * bounds_strides[1];
   p.batch_indices = batch_indices; p.positions = positions; p.kv_indptr = kv_indptr; p.kv_indices = kv_indices;
   p.blocks = blocks;
-  p.exact = reinterpret_cast<unsigned long long*>(base + ws.exact);
   p.scores = reinterpret_cast<float*>(base + ws.scores);
   p.most = reinterpret_cast<unsigned*>(plan->counters_dev);
   p.group = plan->num_qo_heads / plan->num_kv_heads;
@@ -1086,6 +1091,6 @@ extern "C" bskv_status bskv_run_select_blocks(
   if (bskv_status s = status_args(&p.st)) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (plan->head_dim == 128)
-    return plan->dtype == BSKV_BF16 ? launch_both<__nv_bfloat16, 128>(p, plan->M, plan->num_sms, st) : launch_both<__half, 128>(p, plan->M, plan->num_sms, st);
-  return plan->dtype == BSKV_BF16 ? launch_both<__nv_bfloat16, 64>(p, plan->M, plan->num_sms, st) : launch_both<__half, 64>(p, plan->M, plan->num_sms, st);
+    return plan->dtype == BSKV_BF16 ? launch_both<__nv_bfloat16, 128>(p, plan->M, ws.slice, plan->num_sms, st) : launch_both<__half, 128>(p, plan->M, ws.slice, plan->num_sms, st);
+  return plan->dtype == BSKV_BF16 ? launch_both<__nv_bfloat16, 64>(p, plan->M, ws.slice, plan->num_sms, st) : launch_both<__half, 64>(p, plan->M, ws.slice, plan->num_sms, st);
 }

@@ -289,6 +289,9 @@ bskv_status bskv_plan_evict(const int32_t* kv_indptr, const int32_t* kv_indices,
  *   score.
  *   Head counts, head_dim, page_size and dtype as for bskv_plan_decode_fp4 (up to 16 query heads per
  *   kv head).
+ *   The float workspace holds 4 bytes per block and kv head of as many queries as fit 64 MB (one at least, 2048 at
+ *   most; longer batches are selected for in slices of those), and 4 (head_dim + 1) bytes per query head for each
+ *   query and for the group of each of up to 8 num_sms workers.
  */
 bskv_status bskv_plan_decode_blocks(int32_t num_tokens, int32_t max_blocks, int32_t num_pages,
                                     int32_t page_size, int32_t num_qo_heads, int32_t num_kv_heads,

@@ -155,3 +155,36 @@ def test_pages_out_of_range_are_reported(cuda, bad, top, hkv):
             assert torch.equal(got[live], want[live])
         else:
             assert top == 3 or not (got[0] == at).any()
+
+
+@pytest.mark.parametrize("kind", ["normal", "near"])
+def test_choice_in_slices_by_memory(cuda, kind):
+    """A plan for long requests has room for the scores of 85 queries at a time; 301 of several requests, some without
+    a token, with scores that fp32 orders and with ones that it does not."""
+    g = torch.Generator().manual_seed(2)
+    ps, hkv, d, top, sink, recent = 8, 4, 64, 30, 1, 2
+    lens, new = [1600, 40, 900, 2, 1601], [100, 20, 81, 1, 99]
+    s = batch(lens, new, ps, 4)
+    n = sum(new)
+    kv = torch.randn(s["pages"], 2, hkv, ps, d, generator=g).to(BF)
+    q = torch.randn(n, hkv, d, generator=g).to(BF)
+    if kind == "near":
+        kv[:, 0] = kv[:1, 0, :, :1].expand_as(kv[:, 0]).clone() * 64
+        kv[:, 0, :, 0, d // 2] = (torch.randint(0, 2, kv[:, 0, :, 0, 0].shape, generator=g) * 2.0 ** -12).to(BF)
+        kv[:, 0, :, 1:, d // 2] = 0
+        q[:, :, d // 2] = 1.0
+    bounds = torch.zeros(s["pages"], hkv, 2, d, dtype=BF, device=cuda)
+    bskv.bskv_block_bounds_paged(kv.to(cuda), bounds, *lists(batch(lens, lens, ps, 4), cuda), s["last"].to(cuda))
+    req, pos, indptr, indices = lists(s, cuda)
+    gone = list(range(80, 95)) + [n - 1]
+    req[gone] = -1
+    blocks = torch.full((n, hkv, top), -9, dtype=torch.int32, device=cuda)
+    p = bskv.bskv_plan_decode_blocks(n, 49152, s["pages"], ps, hkv, hkv, d, top, sink, recent, BF)
+    bskv.bskv_run_select_blocks(p, q.to(cuda), bounds, req, pos, indptr, indices, blocks=blocks)
+    assert bskv.bskv_get_device_status() == 0
+    b64, q64, got = to64(bounds), to64(q), blocks.tolist()
+    for t in range(n):
+        pages = pages_of(s, int(s["req"][t]))[:int(s["pos"][t]) // ps + 1]
+        for h in range(hkv):
+            want = [-9] * top if t in gone else ob.select(ob.block_scores(q64[t, h:h + 1], b64[pages, h]), top, sink, recent)
+            assert got[t][h] == want, (t, h)

@@ -160,3 +160,16 @@ def test_binding_refuses_tensors_on_the_host(lib):
         bskv.bskv_run_select_blocks(None, q, bounds, i, i, i, i)
     with pytest.raises(ValueError, match="give k, v"):
         bskv.bskv_norm_rope_append_paged(q, q, None, None, i, i, i, i, kv)
+
+
+@pytest.mark.parametrize("tokens,blocks,hq,hkv", [(2048, 8192, 32, 8), (1 << 15, 8192, 8, 2), (512, 49152, 64, 64), (2048, 2048, 32, 8)])
+def test_workspace_of_long_chunks(lib, tokens, blocks, hq, hkv):
+    """Scores of long chunks share 64 MB; the rest are partial states, which grow with the queries alone."""
+    states = (tokens * hkv + 8 * 152) * (hq // hkv) * 129 * 4
+    assert _plan(tokens=tokens, blocks=blocks, hq=hq, hkv=hkv).workspace_sizes()[1] <= (64 << 20) + states + 4096
+
+
+def test_workspace_of_a_query_past_the_scores_share(lib):
+    """One query's scores always have room."""
+    one, two = (_plan(tokens=t, blocks=49152, hq=400, hkv=400).workspace_sizes()[1] for t in (1, 2))
+    assert one >= 400 * 49152 * 4 and two - one < 400 * 49152
