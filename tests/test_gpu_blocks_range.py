@@ -188,3 +188,37 @@ def test_choice_in_slices_by_memory(cuda, kind):
         for h in range(hkv):
             want = [-9] * top if t in gone else ob.select(ob.block_scores(q64[t, h:h + 1], b64[pages, h]), top, sink, recent)
             assert got[t][h] == want, (t, h)
+
+
+# ---- both -------------------------------------------------------------------------------
+
+def test_shared_pages_give_what_the_definition_gives(cuda):
+    """Requests that list the same pages and a row that comes twice: each is the definition's, and nothing is reported."""
+    ps, hq, hkv, d, top = 16, 4, 2, 64, 3
+    s = batch([100], [1], ps, 3)
+    pages = pages_of(s, 0)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda)  # noqa: E731
+    where = i32([0, 1, 0, 1]), i32([99, 99, 99, 63]), i32([0, 7, 14]), i32(pages.tolist() * 2)
+    g = torch.Generator().manual_seed(3)
+    kv = torch.randn(s["pages"], 2, hkv, ps, d, generator=g).to(BF)
+    q = torch.randn(2, hq, d, generator=g).to(BF)[[0, 0, 0, 1]]
+    bounds = torch.zeros(s["pages"], hkv, 2, d, dtype=BF, device=cuda)
+    bskv.bskv_block_bounds_paged(kv.to(cuda), bounds, *lists(batch([100], [100], ps, 3), cuda), s["last"].to(cuda))
+    p = bskv.bskv_plan_decode_blocks(4, 7, s["pages"], ps, hq, hkv, d, top, dtype=BF)
+    blocks = bskv.bskv_run_select_blocks(p, q.to(cuda), bounds, *where)
+    out, lse = bskv.bskv_run_decode_blocks(p, q.to(cuda), kv.to(cuda), blocks, *where, return_lse=True)
+    assert bskv.bskv_get_device_status() == 0
+    q64, kv64, b64 = to64(q), to64(kv), to64(bounds)
+    for t, pos in enumerate([99, 99, 99, 63]):
+        for h in range(hkv):
+            x = q64[t, 2 * h:2 * h + 2]
+            want = ob.select(ob.block_scores(x, b64[pages[:pos // ps + 1], h]), top, 0, 1)
+            assert blocks[t, h].tolist() == want
+            at = np.array([j for c in want for j in range(c * ps, min(pos + 1, (c + 1) * ps))])
+            k, v = kv64[pages[at // ps], 0, h, at % ps], kv64[pages[at // ps], 1, h, at % ps]
+            ref, z, size = ob.attend(x, k, v, d ** -0.5)
+            # a logit is off by 64 + 8 roundings of the sum of its terms' sizes, a weight by twice that
+            err = (np.abs(x) @ np.abs(k).T).max(-1) * d ** -0.5 * 72 * 2.0 ** -24
+            tol = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * (2 * err[:, None] + 2.0 ** -15) * size
+            assert (np.abs(to64(out[t, 2 * h:2 * h + 2]) - ref) <= tol).all()
+            assert (np.abs(to64(lse[t, 2 * h:2 * h + 2]) - z) <= err + 2.0 ** -18 + 2.0 ** -22 * np.abs(z)).all()
