@@ -76,3 +76,12 @@ def test_scores_of_infinite_bounds_are_the_sums_of_greater_products():
         np.testing.assert_array_equal(ob.block_scores(q, bounds), direct)
     assert ob.block_scores(np.full((1, 3), 0.25), bounds)[0] == -inf  # no key of it can have weight
     assert ob.block_scores(np.full((1, 3), 0.25), bounds)[1] == 1.0
+
+
+def test_rotation_agrees_with_the_prologue_s():
+    """The rotation of 64 dims is the one that the latent rows' prologue makes of its tail."""
+    rng = np.random.default_rng(3)
+    x, t = rng.standard_normal((5, 64)), rng.standard_normal(64)
+    for neox in (True, False):
+        y, _ = ob.norm_rope(x, None, 0.0, t, 64, neox)
+        np.testing.assert_allclose(y, rope.rotate(x, t[:32], t[32:], neox), rtol=1e-14, atol=1e-14)
