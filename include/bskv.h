@@ -709,6 +709,10 @@ bskv_status bskv_dequantize_fp4_paged(
  *     entries first, to the requests in order: page j of a request gets one if no older token lies in it,
  *     and its entry of block_table is written. *free_left (other memory) takes the number that remains.
  *     All three NULL: block_table holds every page already.
+ *     Nothing here gives pages back. Where a request gets shorter (drafted tokens that were rejected), the entries
+ *     of block_table from ceil(length / page_size) on are no longer its pages, and a request that grows over such an
+ *     entry has it overwritten by a fresh page: the caller puts the old ids behind the free list's last first, as it
+ *     does with all pages of a request that ends, or they are in no list any more.
  *   Written: kv_indptr and qo_indptr [batch + 1], kv_indices [max_entries >= batch * max_pages] and
  *     kv_last_page_len [batch], as host plans take them (qo_indptr delimits the new tokens); and for new token i in
  *     order of request and position batch_indices[i], positions[i] and, unless NULL, slots[i] (int64: page *

@@ -102,3 +102,32 @@ def test_what_does_not_fit(cuda, what):
     else:
         assert t.kv_indices.tolist()[:6] == [0, -1, 2, 3, -1, -1] and t.free_left.tolist() == [0]
         assert t.slots.tolist() == [-1] * 9
+
+
+def test_pages_of_rejected_drafts_go_back_to_the_free_list(cuda):
+    """Requests that grow by drafted tokens and lose some of them: with their pages put back before the next step, every
+    page of the pool is listed by one request or free, after every step."""
+    ps, pool, batch, most = 4, 40, 3, 10
+    rng = np.random.default_rng(0)
+    i32 = dict(dtype=torch.int32, device=cuda)
+    free_pages, free_count = torch.tensor(rng.permutation(pool), **i32), torch.full((1,), pool, **i32)
+    block_table, lens = torch.full((batch, most), -1, **i32), torch.zeros(batch, **i32)
+    for step in range(30):
+        new = torch.tensor(rng.integers(0, 7, batch), **i32)
+        new = torch.minimum(new, most * ps - lens)
+        lens += new
+        t = bskv.bskv_build_page_table(lens, block_table, ps, pool, new_lens=new, free_pages=free_pages, free_count=free_count,
+                                       max_tokens=24)
+        free_count.copy_(t.free_left)
+        assert bskv.bskv_get_device_status() == 0
+        n = int(t.kv_indptr[-1])
+        assert sorted(t.kv_indices[:n].tolist() + free_pages[:int(free_count)].tolist()) == list(range(pool))
+        drop = torch.minimum(torch.tensor(rng.integers(0, 9, batch), **i32), lens)
+        if step % 10 == 9:
+            drop = lens.clone()  # the requests end
+        for b in range(batch):
+            old = block_table[b, -(-int(lens[b] - drop[b]) // ps):-(-int(lens[b]) // ps)]
+            at = int(free_count)
+            free_pages[at:at + old.numel()] = old
+            free_count += old.numel()
+        lens -= drop
