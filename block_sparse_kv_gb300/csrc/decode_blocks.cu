@@ -412,7 +412,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (ok) ok = warp_wait(&bars[stage], (consumed / STAGES) & 1u, p.st, forced);
     if (ok) {
       const uint32_t at = smem_u32(ring + stage * R::kStageBytes);
-      if (info.valid) attend_tile<T, D, WIDE>(at, at + v_at, eight, info.valid & 0xffff, info.valid >> 16, p.scale_log2, lane, qa, o, m0, m1, l0, l1);
+      if (info.valid)
+        attend_tile<T, D, WIDE>(at, at + v_at, eight, info.valid & 0xffff, info.valid >> 16, p.scale_log2, lane, qa, o,
+                                m0, m1, l0, l1);
       ++consumed;
       __syncwarp();
       if (lane == 0) fence_proxy_async_smem();
@@ -649,7 +651,8 @@ extern "C" bskv_status bskv_run_decode_blocks(
   if (bskv_status s = status_args(&p.st)) return s;
   const int ps = plan->page_size, D = plan->head_dim;
   const uint64_t dims[5] = {uint64_t(D), uint64_t(ps), uint64_t(plan->num_kv_heads), 2, uint64_t(plan->num_pages)};
-  const uint64_t strides[4] = {uint64_t(kv_strides[3]) * 2, uint64_t(kv_strides[2]) * 2, uint64_t(kv_strides[1]) * 2, uint64_t(kv_strides[0]) * 2};
+  const uint64_t strides[4] = {uint64_t(kv_strides[3]) * 2, uint64_t(kv_strides[2]) * 2, uint64_t(kv_strides[1]) * 2,
+                               uint64_t(kv_strides[0]) * 2};
   const uint32_t box[5] = {64, uint32_t(std::min(ps, kTile)), 1, 2, 1};  // K and V of a page
   CUtensorMap map;
   if (bskv_status s = encode_tiled(&map, plan->dtype == BSKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,

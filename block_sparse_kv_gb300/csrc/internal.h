@@ -162,16 +162,19 @@ inline bool fp4_page_size(int32_t page_size) {
   return page_size == 8 || (page_size >= 16 && page_size % 16 == 0);
 }
 
-// Block-sparse decode plans. The CTA that selects holds all candidates of a (query, kv head) row in shared
-// memory. The attention's workers are teams of warps: the rows' lists of top_k
-// blocks, in steps of 16 tokens, one after another, cut into equal runs.
+// Block-sparse decode plans. The CTA that selects holds all candidates of a (query, kv head) row in
+// shared memory. The attention's workers are teams of warps: the rows' lists of top_k blocks, in steps
+// of 16 tokens, one after another, cut into equal runs.
 constexpr int kSelectMaxBlocks = 49152;
-// Queries that are selected for at a time share the workspace's scores: as many as fit kSelectBytes, at least one, at
-// most kSelectSlice. (2048 queries of 131072 tokens and 8 kv heads take 9.2 ms with room for all, 512 MB, 9.4 with 64 MB,
-// 9.8 with 16; 1024 of 65536 tokens 2.52, 2.49 and 2.58.)
+// Queries that are selected for at a time share the workspace's scores: as many as fit kSelectBytes,
+// at least one, at most kSelectSlice. (2048 queries of 131072 tokens and 8 kv heads take 9.2 ms with
+// room for all, 512 MB, 9.4 with 64 MB, 9.8 with 16; 1024 of 65536 tokens 2.52, 2.49 and 2.58.)
 constexpr int kSelectSlice = 2048;
 constexpr size_t kSelectBytes = size_t(64) << 20;
-constexpr int kSelectWide = 2048;   // more blocks than these are selected from by 1024 threads
+// More blocks than these are selected from by 1024 threads, not 256 (8 rows of 1536, 2048, 4096 and 16384
+// blocks of 128 dims take 10.6, 11.3, 14.7 and 29.7 us with 256 threads, 10.6, 11.0, 13.3 and 24.5 with 1024;
+// 128 rows of 2048 and 16384 39.7 and 233, 39.3 and 222; 512 of 2048 118 and 131).
+constexpr int kSelectWide = 2048;
 constexpr int kBlocksWarps = 8;
 constexpr int kBlocksMinSteps = 2;  // per warp of a worker
 constexpr int kBlocksRowSteps = 2;  // what another row costs a worker, per warp
@@ -240,8 +243,8 @@ struct bskv_plan {
   int64_t kept_total = 0;
   int32_t sink = 0, recent = 0, longest = 0, most = 0, in_place = 0;
   // blocks: M query tokens, top_k blocks of at most max_blocks, sink and recent of them by place; the
-  // warps of one of the
-  // attention's workers, workers and the places of each, steps of a block, places of a row
+  // warps of one of the attention's workers, workers and the places of each, steps of a block, places
+  // of a row
   int32_t max_blocks = 0, team = 0, workers = 0, per_worker = 0, steps = 0, row_places = 0;
   // set by bskv_plan_upload
   const int32_t* meta_dev = nullptr;

@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const _
       const int kind = c < p.q_batches ? 0 : c < p.q_batches + p.k_batches ? 1 : 2;
       const T* from = static_cast<const T*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v);
       const int64_t s0 = kind == 0 ? p.q_s0 : kind == 1 ? p.k_s0 : p.v_s0, s1 = kind == 0 ? p.q_s1 : kind == 1 ? p.k_s1 : p.v_s1;
-      const int heads = kind ? p.hkv : p.hq, g = (c - (kind == 0 ? 0 : kind == 1 ? p.q_batches : p.q_batches + p.k_batches)) * kBatch * kRows + row;
+      const int before = kind == 0 ? 0 : kind == 1 ? p.q_batches : p.q_batches + p.k_batches;
+      const int heads = kind ? p.hkv : p.hq, g = (c - before) * kBatch * kRows + row;
       from += c_token * s0 + g * s1 + 8 * sub;
 #pragma unroll
       for (int r = 0; r < kBatch; ++r) {
@@ -202,7 +203,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const _
       issue();
       cp_async_wait<kStages - 1>();
       __syncwarp();
-      const int heads = kind ? p.hkv : p.hq, g0 = (i - (kind == 0 ? 0 : kind == 1 ? p.q_batches : p.q_batches + p.k_batches)) * kBatch * kRows;
+      const int before = kind == 0 ? 0 : kind == 1 ? p.q_batches : p.q_batches + p.k_batches;
+      const int heads = kind ? p.hkv : p.hq, g0 = (i - before) * kBatch * kRows;
       T* out = kind ? cache : static_cast<T*>(p.q_out) + token * p.o_s0;
       if (live && out) {
         const int64_t s1 = kind ? p.c_s2 : p.o_s1;

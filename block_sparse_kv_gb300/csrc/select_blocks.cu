@@ -23,8 +23,8 @@
 // it). Rows where nothing lies between but as many blocks as are still wanted (nearly all) need no second look.
 //
 // Two launches, the second ready to go when the first ends: scoring keeps the memory busy only while all SMs score.
-// With the selection by the CTA that finished a row's last part the operator took 56 us for the 64 requests above and
-// 31 for one of 131072 tokens, in two launches 44 and 19.
+// With the selection by the CTA that finished a row's last part the operator took 56 us for 64 requests of 2048 to
+// 16384 tokens and 31 for one of 131072 (8 kv heads, blocks of 16), in two launches 43 and 19.
 #include <algorithm>
 #include <type_traits>
 
@@ -467,7 +467,8 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const 
         cp_async_16(mine + (stage * kAhead + u) * 32, head + from * p.b_s0);
       }
       const uint32_t there = (__ballot_sync(0xffffffffu, pg >= 0) >> base) & ((1u << kTake) - 1u);
-      if (lane == 0) infos[warp][stage] = RoundInfo{t * int(p.heads.d) + h, at, min(end, at + kTake), there | first | (at + kTake >= end ? kLast : 0u)};
+      const uint32_t bits = there | first | (at + kTake >= end ? kLast : 0u);
+      if (lane == 0) infos[warp][stage] = RoundInfo{t * int(p.heads.d) + h, at, min(end, at + kTake), bits};
       first = 0;
       at += kTake;
       ++issued;
@@ -542,11 +543,12 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const 
   }
 }
 
-// The scores of a row's m candidates again, where bounds or query values are not finite; every thread of the CTA calls it.
-// Of an infinite bound and a coefficient of zero nothing is added, unless a head's query value is zero there: that one's
-// product is NaN. Returns the bound of the sums of absolute products, of the finite bounds. (One request of 131072 tokens,
-// half of its blocks masked, takes 125 us where finite ones take 17.3, 64 requests of 16384 129 and 66. As
-// part of the scoring it was 27 and 110, but finite rows paid: a step took 43.6 instead of 42.1.)
+// The scores of a row's m candidates again, where bounds or query values are not finite; every thread of
+// the CTA calls it. Of an infinite bound and a coefficient of zero nothing is added, unless a head's query
+// value is zero there: that one's product is NaN. Returns the bound of the sums of absolute products, of the
+// finite bounds. (One request of 131072 tokens, half of its blocks masked, takes 125 us where finite ones take
+// 17.3, 64 requests of 16384 129 and 66. As part of the scoring it was 27 and 110, but finite rows paid: a step
+// took 43.6 instead of 42.1.)
 template <typename T, int D, int THREADS>
 __device__ __noinline__ float score_again(const SelectParams& p, int t, int h, const int32_t* pages, const uint8_t* head,
                                           float* scores, int m) {
@@ -645,7 +647,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const _
   const int t = p.heads.divmod(row, h);
   const int b = __ldg(p.batch_indices + t), pos = __ldg(p.positions + t);
   const Row r = b < 0 ? Row{0, 0} : row_of(p, b, pos);
-  if (h == 0) {  // the pages of blocks that are listed without a score, the same for all heads; the scores are still made
+  // the pages of blocks that are listed without a score, the same for all heads; the scores are still made
+  if (h == 0) {
     const int listed = r.n <= p.top_k ? r.n : p.sink + p.recent;
     for (int j = tid; j < listed; j += kThreads) {
       const int pg = __ldg(p.kv_indices + r.start + (r.n <= p.top_k || j < p.sink ? j : r.n - listed + j));
@@ -901,7 +904,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const _
     part_tie[warp] = ties;
   }
   __syncthreads();
-  int at = __reduce_add_sync(0xffffffffu, lane < warp ? part_in[lane] : 0), eq = __reduce_add_sync(0xffffffffu, lane < warp ? part_tie[lane] : 0);
+  int at = __reduce_add_sync(0xffffffffu, lane < warp ? part_in[lane] : 0);
+  int eq = __reduce_add_sync(0xffffffffu, lane < warp ? part_tie[lane] : 0);
   at += p.sink + min(eq, rest);
   const uint32_t below = (1u << lane) - 1;
   for (int i = r0 + lane; i - lane < r1; i += 32) {
@@ -992,7 +996,8 @@ bskv_status launch_both(SelectParams p, int64_t queries, int64_t slice, int num_
       if (bskv_status s = cuda_check(cudaGetLastError(), "run_select_blocks score launch")) return s;
     }
     const int64_t rows = int64_t(p.queries) * heads;
-    if (bskv_status s = p.max_blocks > kSelectWide ? launch_select<T, D, 1024>(p, rows, scored, st) : launch_select<T, D, 256>(p, rows, scored, st)) return s;
+    const auto launch = p.max_blocks > kSelectWide ? launch_select<T, D, 1024> : launch_select<T, D, 256>;
+    if (bskv_status s = launch(p, rows, scored, st)) return s;
     p.q = static_cast<const T*>(p.q) + slice * p.q_s0;
     p.batch_indices += slice;
     p.positions += slice;
@@ -1072,7 +1077,10 @@ extern "C" bskv_status bskv_run_select_blocks(
   if (!q || !q_strides || !aligned16(q)) { set_error("%s: q must be a 16-byte aligned tensor", who); return BSKV_ERR_INVALID_ARG; }
   if (plan->num_pages == 0) { set_error("%s: a cache without pages", who); return BSKV_ERR_INVALID_ARG; }
   for (int i = 0; i < 2; ++i)
-    if (q_strides[i] < 0 || q_strides[i] % 8) { set_error("%s: q stride %d (%lld elements) must be a multiple of 16 bytes", who, i, (long long)q_strides[i]); return BSKV_ERR_INVALID_ARG; }
+    if (q_strides[i] < 0 || q_strides[i] % 8) {
+      set_error("%s: q stride %d (%lld elements) must be a multiple of 16 bytes", who, i, (long long)q_strides[i]);
+      return BSKV_ERR_INVALID_ARG;
+    }
   if (bskv_status s = check_bounds(who, bounds, bounds_strides, plan->head_dim)) return s;
   const BlocksWorkspace ws = blocks_workspace(plan);
   uint8_t* base = static_cast<uint8_t*>(float_ws);
@@ -1090,7 +1098,8 @@ extern "C" bskv_status bskv_run_select_blocks(
   p.error = float((p.group + 10) * 1.01 * std::ldexp(1.0, -24));
   if (bskv_status s = status_args(&p.st)) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (plan->head_dim == 128)
-    return plan->dtype == BSKV_BF16 ? launch_both<__nv_bfloat16, 128>(p, plan->M, ws.slice, plan->num_sms, st) : launch_both<__half, 128>(p, plan->M, ws.slice, plan->num_sms, st);
-  return plan->dtype == BSKV_BF16 ? launch_both<__nv_bfloat16, 64>(p, plan->M, ws.slice, plan->num_sms, st) : launch_both<__half, 64>(p, plan->M, ws.slice, plan->num_sms, st);
+  const bool bf16 = plan->dtype == BSKV_BF16;
+  const auto launch = plan->head_dim == 128 ? (bf16 ? launch_both<__nv_bfloat16, 128> : launch_both<__half, 128>)
+                                            : (bf16 ? launch_both<__nv_bfloat16, 64> : launch_both<__half, 64>);
+  return launch(p, plan->M, ws.slice, plan->num_sms, st);
 }
