@@ -544,21 +544,24 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) score_kernel(const 
 }
 
 // The scores of a row's m candidates again, where bounds or query values are not finite; every thread of
-// the CTA calls it. Of an infinite bound and a coefficient of zero nothing is added, unless a head's query
-// value is zero there: that one's product is NaN. Returns the bound of the sums of absolute products, of the
-// finite bounds. (One request of 131072 tokens, half of its blocks masked, takes 125 us where finite ones take
-// 17.3, 64 requests of 16384 129 and 66. As part of the scoring it was 27 and 110, but finite rows paid: a step
-// took 43.6 instead of 42.1.)
+// the CTA calls it. Of an infinite bound and a coefficient of zero nothing is added; where a head's query
+// value is zero, whatever the others' are, its product with an infinite bound is NaN. Returns the bound of the
+// sums of absolute products, of the finite bounds. (One request of 131072 tokens, half of its blocks masked,
+// takes 133 us where finite ones take 17.3, 64 requests of 16384 133 and 66. As part of the scoring it was 27
+// and 110, but finite rows paid: a step took 43.6 instead of 42.1. As a function that is called, the selection
+// of 64 finite rows took 44.5 instead of 43.4.)
 template <typename T, int D, int THREADS>
-__device__ __noinline__ float score_again(const SelectParams& p, int t, int h, const int32_t* pages, const uint8_t* head,
-                                          float* scores, int m) {
+__device__ __forceinline__ float score_again(const SelectParams& p, int t, int h, const int32_t* pages,
+                                             const uint8_t* head, float* scores, int m) {
   constexpr int kLanes = D / 4, kPer = 32 / kLanes, kWarps = THREADS / 32, kDeep = 4, kStep = kWarps * kPer * kDeep;
   __shared__ float warp_most[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % kLanes, which = lane / kLanes, d0 = 8 * (sub % (D / 8));
   float c[8];
   coefficients<T>(p, t, h, d0, sub >= D / 8, c);
-  // pairs of channels where the coefficient is not zero, or a head's query value is: a mask of each half
-  uint32_t keep[4] = {0, 0, 0, 0}, largest[4] = {0, 0, 0, 0};
+  // masks of the halves of pairs of channels: where the coefficient is not zero; where a head's query value is
+  uint32_t keep[4], zero[4] = {0, 0, 0, 0}, largest[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) keep[e] = (c[2 * e] != 0.f ? 0xffffu : 0u) | (c[2 * e + 1] != 0.f ? 0xffff0000u : 0u);
   const T* q = static_cast<const T*>(p.q) + t * p.q_s0 + int64_t(h) * p.group * p.q_s1 + d0;
   for (int g = 0; g < p.group; ++g) {
     const uint4 a = __ldg(reinterpret_cast<const uint4*>(q + g * p.q_s1));
@@ -566,7 +569,7 @@ __device__ __noinline__ float score_again(const SelectParams& p, int t, int h, c
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 f = Pair<T>::values(w[e]);
-      keep[e] |= (f.x == 0.f || c[2 * e] != 0.f ? 0xffffu : 0u) | (f.y == 0.f || c[2 * e + 1] != 0.f ? 0xffff0000u : 0u);
+      zero[e] |= (f.x == 0.f ? 0xffffu : 0u) | (f.y == 0.f ? 0xffff0000u : 0u);
     }
   }
   int pg[kDeep];
@@ -592,8 +595,9 @@ __device__ __noinline__ float score_again(const SelectParams& p, int t, int h, c
       float2 two = make_float2(0.f, 0.f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t size = w[e] & 0x7fff7fffu;
-        two = ffma2(Pair<T>::values(w[e] & (keep[e] | Pair<T>::not_infinite(size))), make_float2(c[2 * e], c[2 * e + 1]), two);
+        const uint32_t size = w[e] & 0x7fff7fffu, other = Pair<T>::not_infinite(size);
+        const uint32_t v = (w[e] & (keep[e] | other)) | (zero[e] & ~other);  // all bits set are NaN
+        two = ffma2(Pair<T>::values(v), make_float2(c[2 * e], c[2 * e + 1]), two);
         largest[e] = Pair<T>::larger(largest[e], size & Pair<T>::finite(size));
       }
       s[u] = two.x + two.y;

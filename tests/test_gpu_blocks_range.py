@@ -125,6 +125,39 @@ def test_choice_by_infinite_bounds(cuda, kind, blocks, ps, hkv, group, d, dtype)
                 assert got[t, h].tolist() == ob.select(score, top, sink, recent), (t, h)
 
 
+@pytest.mark.parametrize("d,dtype", [(64, BF), (128, FP)])
+@pytest.mark.parametrize("group", [1, 2, 3, 8])
+def test_choice_by_bounds_that_are_infinite_anywhere(cuda, group, d, dtype):
+    """Infinite bounds of both signs in random places of rows of 40 and of 2300 blocks, under heads whose query values are
+    above, below and zero in the same channel."""
+    inf, ps, hkv, top = float("inf"), 8, 2, 12
+    for seed in range(6):
+        g = torch.Generator().manual_seed(seed)
+        s = batch([2300 * ps, 40 * ps, 700 * ps], [1, 2, 1], ps, seed)
+        n = sum(s["new"])
+        q = torch.randn(n, hkv * group, d, generator=g)
+        q[torch.rand(q.shape, generator=g) < (0.0, 0.02, 0.3)[seed % 3]] = 0.0
+        if seed % 2:
+            q = q.abs()
+        q = q.to(dtype)
+        bounds = torch.randn(s["pages"], hkv, 2, d, generator=g).sort(2).values.to(dtype)
+        lo, hi = bounds[:, :, 0], bounds[:, :, 1]
+        for x, value in ((lo, -inf), (hi, inf)):
+            x[torch.rand(x.shape, generator=g) < 0.002] = value
+        for value in (-inf, inf):
+            both = torch.rand(lo.shape, generator=g) < 0.002
+            lo[both], hi[both] = value, value
+        p = bskv.bskv_plan_decode_blocks(n, 2300, s["pages"], ps, hkv * group, hkv, d, top, 1, 2, dtype)
+        got = bskv.bskv_run_select_blocks(p, q.to(cuda), bounds.to(cuda), *lists(s, cuda)).cpu().numpy()
+        assert bskv.bskv_get_device_status() == 0
+        q64, b64 = to64(q), to64(bounds)
+        for t in range(n):
+            pages = pages_of(s, int(s["req"][t]))[:int(s["pos"][t]) // ps + 1]
+            for h in range(hkv):
+                score = ob.block_scores(q64[t, h * group:(h + 1) * group], b64[pages, h])
+                assert got[t, h].tolist() == ob.select(score, top, 1, 2), (seed, t, h)
+
+
 @pytest.mark.parametrize("bad", ["first", "last", "short row", "scored", "unseen", "no token"])
 @pytest.mark.parametrize("top,hkv", [(12, 2), (3, 3)])  # with 3 there is no choice: the first and the last are all
 def test_pages_out_of_range_are_reported(cuda, bad, top, hkv):
