@@ -17,9 +17,9 @@
 // in equal parts and join their states in shared memory; a row that lies in several runs leaves their states in the
 // float workspace, and the team that finishes its last piece joins them in the same launch, in piece order.
 // A piece costs a warp about 4 us beside its tiles, which is why the team's size matters (1, 2, 4, 8 warps; us): 64
-// requests, 8 kv heads, 64 blocks of 16 tokens 52.9, 48.6, 47.0, 49.6 (floor 40.3); 300 with 8 blocks 29.8, 33.0, 43.3,
-// 63.2 (24.3); 32 with 32 blocks of 64 and 8 query heads per kv head 64.9, 55.9, 49.6, 47.6 (40.3); one with 128
-// blocks 28.7, 18.1, 12.6, 13.0. The plan's rule is at blocks_team().
+// requests, 8 kv heads, 64 blocks of 16 tokens 56.3, 50.3, 47.9, 47.7 (floor 40.2); 300 with 8 blocks 29.2, 31.0, 36.9,
+// 56.8 (23.5); 32 with 32 blocks of 64 and 8 query heads per kv head 65.3, 55.0, 50.4, 48.3 (40.2); one with 128
+// blocks 51.3, 18.1, 9.8, 9.1. The plan's rule is at blocks_team().
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
