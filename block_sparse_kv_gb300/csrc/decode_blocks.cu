@@ -194,6 +194,17 @@ __device__ __forceinline__ void two_parts(float a, float b, uint32_t& first, uin
   second = MmaOp<T>::pack(a - f.x, b - f.y);
 }
 
+// A pair of values with the greatest number of their sign in place of infinities (and some number of NaN).
+template <typename T>
+__device__ __forceinline__ uint32_t finite_values(uint32_t x) {
+  uint32_t y;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x7f7f7f7fu));
+  else
+    asm("min.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x7bff7bffu));
+  return y;
+}
+
 // One tile of 16 tokens for the query heads of a row: up to eight, or WIDE up to 16. v0 and v1 of the two groups of
 // eight tokens are attended to. With up to eight heads o[n][2] and o[n][3], the accumulators of rows 8 to 15, belong to
 // the weights' second parts.
@@ -267,8 +278,8 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, uint32
   }
   // The product with V takes weights of 16 bits. Rounded to those they made the output's error against 64 bits a quarter
   // larger than its own rounding does (bf16: 2.1e-3 of its norm, so 1.65e-3); in two parts they add nothing to be seen.
-  // Times are the same for up to eight heads (64 requests of 8 x 4 heads 47.9 and 47.7 us), for 16 heads 49.5 and 50.4
-  // with 128 dims, 66.5 and 69.9 with 64.
+  // Times are the same for up to eight heads (64 requests of 8 x 4 heads 47.9 and 47.7 us), for 16 heads 49.5 and 50.9
+  // with 128 dims, 66.5 and 70.0 with 64.
   uint32_t pa[4], pb[4];
   two_parts<T>(s[0][0], s[0][1], pa[0], pb[0]);
   two_parts<T>(s[1][0], s[1][1], pa[2], pb[2]);
@@ -288,9 +299,10 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, uint32
       ldsm_x4_t(tile_row(v_at, r, dim / 64, eight) + ((((dim % 64) / 8) ^ (r & 7)) << 4), b0, b1, b2, b3);
       Mma::run(o[2 * dd], pa, b0, b1);
       Mma::run(o[2 * dd + 1], pa, b2, b3);
+      // a second part may be zero or negative: times infinity it must not meet the first's product
       if constexpr (WIDE) {
-        Mma::run(o[2 * dd], pb, b0, b1);
-        Mma::run(o[2 * dd + 1], pb, b2, b3);
+        Mma::run(o[2 * dd], pb, finite_values<T>(b0), finite_values<T>(b1));
+        Mma::run(o[2 * dd + 1], pb, finite_values<T>(b2), finite_values<T>(b3));
       }
     }
   }
@@ -430,10 +442,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
       l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
     } else {
+      // a second part may be zero or negative: an infinite value counts by the first alone
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) {
-        o[n][0] += o[n][2];
-        o[n][1] += o[n][3];
+        if (fabsf(o[n][0]) < INFINITY) o[n][0] += o[n][2];
+        if (fabsf(o[n][1]) < INFINITY) o[n][1] += o[n][3];
       }
     }
     if (r0 < p.group) {

@@ -54,6 +54,46 @@ def test_weights_keep_more_than_16_bits(cuda, group, d, ps, dtype):
             assert (np.abs(to64(lse[t, h * group:(h + 1) * group]) - z) <= 4 * rel[:, 0] + 2.0 ** -22 * np.abs(z)).all()
 
 
+@pytest.mark.parametrize("group", [1, 4, 8, 9, 16])
+@pytest.mark.parametrize("d,dtype", [(128, BF), (64, BF), (128, FP), (64, FP)])
+def test_infinite_values_stay_infinite(cuda, group, d, dtype):
+    """Values of either sign, of both and NaN among those that are attended to: the weighted sum is the same one as in 64
+    bits, whatever the weights are (one key alone has a weight of one)."""
+    lens, ps, hkv = [100, 1, 37, 300, 16], 16, 2
+    g = torch.Generator().manual_seed(group)
+    s = batch(lens, [1] * 5, ps, group)
+    q = torch.randint(-2, 3, (5, hkv * group, d), generator=g).to(dtype)
+    kv = torch.randn(s["pages"], 2, hkv, ps, d, generator=g).to(dtype)
+    kv[:, 0] = torch.randint(-2, 3, kv[:, 0].shape, generator=g).to(dtype)
+    inf = float("inf")
+    for b, n in enumerate(lens):
+        pages = pages_of(s, b)
+        for c, at in ((3, 0), (5, n - 1), (9, n // 2), (20, n // 3), (d - 1, 0)):
+            kv[pages[at // ps], 1, :, at % ps, c] = -inf if c == 9 else inf
+        kv[pages[(n - 1) // ps], 1, :, (n - 1) % ps, 20] = -inf
+        kv[pages[0], 1, :, 0, 40] = float("nan")
+    most = 19
+    blocks = torch.full((5, hkv, most), -1, dtype=torch.int32)
+    for t, n in enumerate(lens):
+        blocks[t, :, :-(-n // ps)] = torch.arange(-(-n // ps), dtype=torch.int32)
+    p = bskv.bskv_plan_decode_blocks(5, most, s["pages"], ps, hkv * group, hkv, d, most, dtype=dtype)
+    out = to64(bskv.bskv_run_decode_blocks(p, q.to(cuda), kv.to(cuda), blocks.to(cuda), *lists(s, cuda), sm_scale=1 / 32))
+    assert bskv.bskv_get_device_status() == 0
+    q64, kv64, half = to64(q), to64(kv), torch.finfo(dtype).eps / 2
+    for t, n in enumerate(lens):
+        tokens = np.arange(n)
+        for h in range(hkv):
+            r = slice(h * group, (h + 1) * group)
+            pages = pages_of(s, t)[tokens // ps]
+            with np.errstate(invalid="ignore"):
+                want, _, size = ob.attend(q64[t, r], kv64[pages, 0, h, tokens % ps], kv64[pages, 1, h, tokens % ps], 1 / 32)
+            fine = np.isfinite(want)
+            assert (~fine).any()
+            np.testing.assert_array_equal(out[t, r][~fine], want[~fine])
+            # finite channels: the output's rounding, and logits of a few units in fp32
+            assert (np.abs(out[t, r][fine] - want[fine]) <= (half * np.abs(want) + 2.0 ** -14 * size)[fine] + 2.0 ** -24).all()
+
+
 # ---- the choice -------------------------------------------------------------------------
 
 KINDS = ["masked", "lower", "upper", "one sign", "zero", "query", "near", "lost page"]
