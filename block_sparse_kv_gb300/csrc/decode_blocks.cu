@@ -234,6 +234,9 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, uint32
       Mma::run(s[1], qa[kk], b2, b3);
     }
   }
+  // m0 and m1 are the references that weights are relative to: the greatest logit, less 15 in fp16. So these weights go up
+  // to 2^15, and one is lost below 2^-39 of the greatest, not below 2^-24 (many of which can be much of the sum).
+  constexpr float kBelow = std::is_same<T, __half>::value ? 15.f : 0.f;
   float mx0 = -FLT_MAX, mx1 = -FLT_MAX;  // finite: a logit of -inf has no weight, in a tile of only such ones too
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt) {
@@ -245,13 +248,13 @@ __device__ __forceinline__ void attend_tile(uint32_t k_at, uint32_t v_at, uint32
   }
   mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
   mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-  const float mn0 = fmaxf(m0, mx0), a0 = fast_exp2(m0 - mn0);
+  const float mn0 = fmaxf(m0, mx0 - kBelow), a0 = fast_exp2(m0 - mn0);
   m0 = mn0;
   float mn1 = 0.f, a1 = a0;
   if constexpr (WIDE) {
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-    mn1 = fmaxf(m1, mx1);
+    mn1 = fmaxf(m1, mx1 - kBelow);
     a1 = fast_exp2(m1 - mn1);
     m1 = mn1;
   }
@@ -435,7 +438,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
     if (ok && !(info.flags & kLast)) continue;
 
-    // this warp's state, relative to its own maximum
+    // this warp's state, relative to its own reference
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     if constexpr (WIDE) {

@@ -54,6 +54,33 @@ def test_weights_keep_more_than_16_bits(cuda, group, d, ps, dtype):
             assert (np.abs(to64(lse[t, h * group:(h + 1) * group]) - z) <= 4 * rel[:, 0] + 2.0 ** -22 * np.abs(z)).all()
 
 
+@pytest.mark.parametrize("group", [1, 8, 12])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("below", [10, 16, 18, 24])
+@pytest.mark.parametrize("at", [0, 2000, 4999])
+def test_many_small_weights_in_fp16(cuda, group, d, below, at):
+    """One key takes nearly all weight, and 4999 others e^-below each, which 16 bits alone do not hold: they are all that
+    the output has."""
+    n, ps, dtype = 5000, 16, FP
+    s = batch([n], [1], ps, 1)
+    q = torch.zeros(1, group, d, dtype=dtype)
+    q[:, :, 0] = 1.0
+    kv = torch.zeros(s["pages"], 2, 1, ps, d, dtype=dtype)
+    kv[:, 1] = 1024.0
+    page = pages_of(s, 0)[at // ps]
+    kv[page, 0, 0, at % ps, 0], kv[page, 1, 0, at % ps] = float(below), 0.0
+    most = -(-n // ps)
+    p = bskv.bskv_plan_decode_blocks(1, most, s["pages"], ps, group, 1, d, most, dtype=dtype)
+    blocks = torch.arange(most, dtype=torch.int32).view(1, 1, most).to(cuda)
+    out, lse = bskv.bskv_run_decode_blocks(p, q.to(cuda), kv.to(cuda), blocks, *lists(s, cuda), return_lse=True, sm_scale=1.0)
+    w = np.exp(-float(below))
+    want, z = 1024.0 * (n - 1) * w / (1 + (n - 1) * w), below + np.log1p((n - 1) * w)
+    # the output's rounding; the logit with its factor of log2 e, the exponentials and sums of 313 tiles; what a
+    # weight loses, half of 2^-39, for each of them
+    assert (np.abs(to64(out) - want) <= (2.0 ** -11 + (4 * below + 4 * 313 + 40) * 2.0 ** -23) * want + 1024 * n * 2.0 ** -40 + 2.0 ** -25).all()
+    assert (np.abs(to64(lse) - z) <= (4 * below + 4 * 313 + 40) * 2.0 ** -23 + 2.0 ** -22 * z).all()
+
+
 @pytest.mark.parametrize("group", [1, 4, 8, 9, 16])
 @pytest.mark.parametrize("d,dtype", [(128, BF), (64, BF), (128, FP), (64, FP)])
 def test_infinite_values_stay_infinite(cuda, group, d, dtype):
